@@ -469,6 +469,128 @@ kvo_status sparse_decode_attn_static(const void* q, const void* k_buf, const voi
                                      int fuse_window_merge, kvo_stream_t stream);
 
 /*
+ * Around the decode step: rotary positions, and a paged cache held on the GPU
+ * (bf16, or 8 bits with a scale for each page and KV head) with the attention
+ * that reads it.  Like sparse_decode_attn_static these calls need no context;
+ * every pointer is memory of the current device unless stated, nothing is
+ * allocated, kept or synchronized, and all of them can be captured into a CUDA
+ * graph.  `stream` NULL is the legacy default stream.  Arguments are checked on
+ * the host; offsets, lengths and page ids that the GPU finds out of range are
+ * skipped and recorded in the caller's optional device word `status` (KVO_DEV_*
+ * bits are OR-ed in; NULL drops them).  Calls share no scratch: two calls may
+ * overlap on the GPU unless one writes what the other reads or writes.
+ *
+ * kvo_rope -- rotary positions.
+ *   x: bf16 [tokens][heads][head_dim] with any token and head stride (elements,
+ *   multiples of 8; the last dimension contiguous; 16-byte aligned), e.g. the q
+ *   and k heads of a fused projection.  out: the same shape with its own
+ *   strides; out == x with equal strides rotates in place; other overlaps are
+ *   not allowed.  pos: device int32 [tokens], any value (a negative position
+ *   turns backwards).  freq: device uint64 [rot_dim / 2], each pair's frequency
+ *   in turns per position, in units of 2^-64: the phase pos * freq is exact
+ *   modulo a turn at every position.  Scalings for long contexts are other
+ *   frequencies, and `amplitude` multiplies the rotated values.
+ *   interleaved 0: pairs (i, i + rot_dim / 2); 1: pairs (2i, 2i + 1).  Values
+ *   from rot_dim on pass through unchanged.  fp32, rounded once to bf16.
+ *   Errors: KVO_ERR_INVALID for head_dim not a multiple of 16 in 16..4096,
+ *   rot_dim not a multiple of 16 in 16..head_dim, bad counts, strides or
+ *   alignment, or null pointers (tokens == 0 launches nothing); KVO_ERR_CUDA.
+ */
+kvo_status kvo_rope(const void* x, int64_t x_token_stride, int64_t x_head_stride, void* out,
+                    int64_t out_token_stride, int64_t out_head_stride, const int32_t* pos, const uint64_t* freq,
+                    int64_t tokens, int heads, int head_dim, int rot_dim, int interleaved, float amplitude,
+                    kvo_stream_t stream);
+
+#define KVO_PAGES_BF16 0
+#define KVO_PAGES_E4M3 1
+
+/* A paged cache of one layer; every buffer is the caller's. */
+typedef struct {
+    void* k_pages;         /* [n_pages][n_kv_heads][page_size][head_dim], bf16 or e4m3, 16-byte aligned */
+    void* v_pages;
+    float* k_scale;        /* e4m3: [n_pages][n_kv_heads], value = code * scale, scale > 0; bf16: unused */
+    float* v_scale;
+    const int32_t* table;  /* [batch][max_pages]: token t of request b is row t % page_size of page table[b][t / page_size] */
+    int32_t batch, n_kv_heads;
+    int32_t head_dim;      /* 64 or 128 */
+    int32_t page_size;     /* 16, 32, 64 or 128 */
+    int32_t n_pages, max_pages;
+    int32_t format;        /* KVO_PAGES_BF16 or KVO_PAGES_E4M3 */
+} kvo_paged_cache;
+
+/*
+ * kvo_paged_append -- append keys and values, keys rotated on the way.
+ *   k, v: bf16 [tokens][n_kv_heads][head_dim], heads contiguous, any token
+ *   stride (elements, a multiple of 8).  cu: device int32 [batch + 1]: tokens
+ *   cu[b] .. cu[b + 1] - 1 are request b's (ascending, none may be there);
+ *   NULL: one token each (tokens == batch).  start: device int32 [batch]: the
+ *   tokens the request has already; its i-th new token gets position and cache
+ *   row start[b] + i.  freq (NULL: no rotation), rot_dim, interleaved and
+ *   amplitude: as kvo_rope.  A key is rotated in fp32 and rounded once to bf16;
+ *   that value goes to k_out (bf16 [tokens][n_kv_heads][head_dim], optional)
+ *   and to the cache.  q (optional): bf16 [tokens][n_q_heads][head_dim], heads
+ *   contiguous, any token stride, rotated into the contiguous q_out by the same
+ *   launch.  k_out may be k and q_out q where those are contiguous.
+ *   e4m3 pages: a page's scale is the smallest power of two s >= 2^-100 with
+ *   |x| <= 448 s for the finite values written to it.  A page whose first row
+ *   is written starts afresh; otherwise its scale never shrinks, and when it
+ *   grows the rows before start[b] are moved to the new scale (exact but for
+ *   codes that become subnormal).  Codes are x * (1 / s) rounded to nearest
+ *   even; an infinity or a NaN is stored as NaN.
+ *   Rows of the pages that no new token takes keep their bytes (but for that
+ *   move), and so do rows of q_out and k_out outside every request.  A page may
+ *   be written by one request of a call only; pages shared by requests may be
+ *   read by kvo_paged_attn.
+ *   Status bits: KVO_DEV_BAD_COUNT (cu outside 0..tokens or descending, start
+ *   < 0, a token past max_pages * page_size), KVO_DEV_BAD_BLOCK_ID (a page id
+ *   outside 0..n_pages - 1); such requests or pages are not written, nor are
+ *   their rows of k_out.
+ *   Errors: KVO_ERR_INVALID, KVO_ERR_CUDA.
+ */
+kvo_status kvo_paged_append(const kvo_paged_cache* cache, const void* k, int64_t k_token_stride, const void* v,
+                            int64_t v_token_stride, int64_t tokens, const int32_t* cu, const int32_t* start,
+                            const uint64_t* freq, int rot_dim, int interleaved, float amplitude, const void* q,
+                            int64_t q_token_stride, int n_q_heads, void* q_out, void* k_out, int32_t* status,
+                            kvo_stream_t stream);
+
+/*
+ * kvo_paged_attn -- GQA decode attention over a paged cache, one query token
+ * per request.
+ *   q: bf16 [batch][n_q_heads][head_dim], contiguous; n_q_heads / n_kv_heads
+ *   <= 16.  lens: device int32 [batch], the tokens of each request (0 allowed).
+ *   max_len: the caller's upper bound of lens (0: the table's capacity); it
+ *   only sizes the launch and the workspace, longer requests are still attended
+ *   to in full.  blocks (optional): device int32 [batch][n_kv_heads][n_blocks],
+ *   the logical blocks (pages) each KV head attends to instead of the whole
+ *   request -- what select_topk returns for block_size == page_size -- of which
+ *   the first counts[b][h] count (counts NULL: all).  A listed block is cut at
+ *   the request's length, one past it adds nothing, one listed twice counts
+ *   twice.
+ *   o: bf16 [batch][n_q_heads][head_dim]; lse: fp32 [batch][n_q_heads], natural
+ *   log.  Softmax scale 1/sqrt(head_dim), fp32 accumulation.  A request with
+ *   nothing to attend to gets o = 0, lse = -inf.  What lies in a page behind
+ *   the last token is never used, NaN included.
+ *   o is rounded once to bf16, as the projection that follows takes it: the
+ *   weights are rounded to 11 bits (8 with bf16 pages) on the tensor cores, so
+ *   fp32 would carry no more.  Two calls give the same bits.
+ *   workspace: kvo_paged_attn_workspace bytes, 256-byte aligned, contents
+ *   undefined before and after; one call at a time may use it (two captured
+ *   graphs that may overlap need one each).
+ *   Status bits: KVO_DEV_BAD_BLOCK_ID (a page or block id out of range: adds
+ *   nothing), KVO_DEV_BAD_COUNT (a length or count out of range: clamped),
+ *   KVO_DEV_TIMEOUT (a bounded wait of 2 s gave up: outputs are invalid).
+ *   Errors: KVO_ERR_INVALID, KVO_ERR_CUDA.
+ */
+kvo_status kvo_paged_attn(const kvo_paged_cache* cache, const void* q, int n_q_heads, const int32_t* lens,
+                          int64_t max_len, const int32_t* blocks, const int32_t* counts, int n_blocks, void* o,
+                          float* lse, void* workspace, size_t workspace_bytes, int32_t* status, kvo_stream_t stream);
+
+/* kvo_paged_attn_workspace -- bytes kvo_paged_attn needs for these arguments
+ * (n_blocks 0: no block list).  Host only; reads the descriptor's sizes. */
+kvo_status kvo_paged_attn_workspace(const kvo_paged_cache* cache, int n_q_heads, int n_blocks, int64_t max_len,
+                                    size_t* bytes_out);
+
+/*
  * kvo_set_gather_shape -- launch shape of the host -> HBM gather kernel:
  * ctas (0: the default, 2 per SM), threads per CTA (32..256, multiple of 32)
  * and 16-byte loads of K and of V in flight per lane (1, 2 or 4).  The gather

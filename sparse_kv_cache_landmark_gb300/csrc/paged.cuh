@@ -1,0 +1,79 @@
+// The paged device cache: layout, checks and small device helpers shared by the
+// append and the attention that reads it.
+//
+// Page p of KV head h holds page_size rows of head_dim values, contiguous:
+// [n_pages][Hkv][page_size][head_dim], bf16 or e4m3.  In e4m3 a value is
+// code * scale[p][h].  Token t of request b lives in row t % page_size of page
+// table[b][t / page_size].
+#pragma once
+#include <cuda_fp16.h>
+#include <stdint.h>
+
+#include "kvo_internal.cuh"
+
+namespace kvo {
+
+constexpr float E4M3_MAX = 448.f;
+
+// Two floats -> two e4m3 codes (lo in the low byte), to nearest even, +-448 beyond; NaN stays NaN.
+__device__ __forceinline__ uint16_t f32x2_to_e4m3x2(float lo, float hi) {
+    uint16_t r;
+    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+// Two e4m3 codes -> f16x2 (exact: every e4m3 value is an f16 value).
+__device__ __forceinline__ uint32_t e4m3x2_to_f16x2(uint16_t v) {
+    uint32_t r;
+    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"(v));
+    return r;
+}
+
+// Smallest power of two s >= 2^-100 with amax <= 448 s, amax finite: with
+// amax = m 2^e, m in [1, 2), that is 2^(e - 8) up to m = 1.75 and 2^(e - 7) above.
+// A power of two makes code * s, and a page's move to a larger scale, exact
+// above the subnormal codes; it costs no precision, since a float format's
+// relative step is the same at every binade.
+__device__ __forceinline__ float e4m3_scale(float amax) {
+    const uint32_t u = __float_as_uint(amax);
+    const int e = (int)(u >> 23) - 127 - ((u & 0x7FFFFFu) <= 0x600000u ? 8 : 7);
+    return __uint_as_float((uint32_t)(max(e, -100) + 127) << 23);
+}
+
+// The last i in [0, n) with first(i) <= key, for a non-decreasing `first` with
+// first(0) <= key; called by a whole warp, 32 probes a round.  Terminates (with
+// some index in range) whatever `first` returns.
+template <typename F>
+__device__ __forceinline__ int warp_find(int n, int64_t key, F first) {
+    const int lane = threadIdx.x & 31;
+    int lo = 0;
+    while (n > 1) {
+        const int step = (n + 31) / 32;
+        const int at = lane * step;
+        const bool le = at < n && first(lo + at) <= key;
+        const int k = max(0, 31 - __clz((int)__ballot_sync(0xffffffffu, le)));
+        lo += k * step;
+        n = max(1, min(step, n - k * step));
+    }
+    return lo;
+}
+
+// Host: a message for a cache descriptor that no call may use, or NULL.
+inline const char* paged_cache_error(const kvo_paged_cache* c) {
+    if (!c) return "null cache";
+    if (c->batch < 0 || c->n_kv_heads < 1) return "need batch >= 0 and n_kv_heads >= 1";
+    if (c->head_dim != 64 && c->head_dim != 128) return "head_dim must be 64 or 128";
+    if (c->page_size != 16 && c->page_size != 32 && c->page_size != 64 && c->page_size != 128)
+        return "page_size must be 16, 32, 64 or 128";
+    if (c->n_pages < 1 || c->max_pages < 1) return "need n_pages >= 1 and max_pages >= 1";
+    if ((int64_t)c->max_pages * c->page_size > INT32_MAX) return "max_pages * page_size must fit in 31 bits";
+    if ((int64_t)c->n_pages * c->n_kv_heads * c->page_size > INT32_MAX)
+        return "n_pages * n_kv_heads * page_size must fit in 31 bits";
+    if ((int64_t)c->batch * c->n_kv_heads > (1 << 20)) return "batch * n_kv_heads must be <= 2^20";
+    if (c->format != KVO_PAGES_BF16 && c->format != KVO_PAGES_E4M3) return "format must be KVO_PAGES_BF16 or KVO_PAGES_E4M3";
+    if (!c->k_pages || !c->v_pages || !c->table) return "null pages or table";
+    if ((uintptr_t)c->k_pages % 16 || (uintptr_t)c->v_pages % 16) return "pages must be 16-byte aligned";
+    if (c->format == KVO_PAGES_E4M3 && (!c->k_scale || !c->v_scale)) return "e4m3 pages need k_scale and v_scale";
+    return nullptr;
+}
+
+}  // namespace kvo

@@ -1,0 +1,72 @@
+// kvo_rope: rotary positions of packed heads (the mathematics is in rope.cuh).
+//
+// Bound by HBM: every value is read and written once (4 bytes per value), and
+// the angle of a (token, pair) is shared by all heads.  A thread owns 16 values
+// (8 pairs) of one token, computes their 8 cosines and sines once and walks the
+// token's heads with four heads' loads in flight.
+#include <stdio.h>
+
+#include <algorithm>
+
+#include "kvo_internal.cuh"
+#include "rope.cuh"
+
+namespace kvo {
+
+constexpr int ROPE_THREADS = 256;
+
+// grid.x: (token, unit) pairs; grid.y: runs of `heads_per` heads.
+__global__ void __launch_bounds__(ROPE_THREADS)
+rope_kernel(const uint16_t* x, int64_t x_tok, int64_t x_head, uint16_t* out, int64_t out_tok,
+            int64_t out_head, const int32_t* __restrict__ pos, RopeArgs R, int64_t n, int units, int heads,
+            int heads_per) {
+    const int64_t i = (int64_t)blockIdx.x * ROPE_THREADS + threadIdx.x;
+    if (i >= n) return;
+    const int64_t t = i / units;
+    const int u = (int)(i - t * units);
+    const int h0 = blockIdx.y * heads_per, h1 = min(heads, h0 + heads_per);
+    rope_heads(R, x + t * x_tok, x_head, out + t * out_tok, out_head, u, __ldg(pos + t), h0, h1);
+}
+
+int rope_heads_per_thread(int64_t n, int heads) {
+    // The 8 sincos of a thread cost about as much as 5 heads' rotation, so a
+    // thread takes as many heads as leave about 1024 threads for each of the
+    // 152 SMs; short inputs are spread to one head a thread.
+    const int64_t want = 152 * 1024;
+    const int64_t splits = std::min<int64_t>(heads, std::max<int64_t>(1, (want + n - 1) / n));
+    return (int)((heads + splits - 1) / splits);
+}
+
+}  // namespace kvo
+
+extern "C" kvo_status kvo_rope(const void* x, int64_t x_token_stride, int64_t x_head_stride, void* out,
+                               int64_t out_token_stride, int64_t out_head_stride, const int32_t* pos,
+                               const uint64_t* freq, int64_t tokens, int heads, int head_dim, int rot_dim,
+                               int interleaved, float amplitude, kvo_stream_t stream) {
+    using namespace kvo;
+    auto bad = [](const char* m) { set_last_error(m); return KVO_ERR_INVALID; };
+    if (tokens < 0 || heads < 1) return bad("need tokens >= 0 and heads >= 1");
+    if (heads > 65535) return bad("heads must be <= 65535");
+    if (head_dim < 16 || head_dim % 16 || head_dim > 4096) return bad("head_dim must be a multiple of 16 in 16..4096");
+    if (rot_dim < 16 || rot_dim % 16 || rot_dim > head_dim)
+        return bad("rot_dim must be a multiple of 16 in 16..head_dim");
+    if (tokens == 0) return KVO_OK;
+    if (!x || !out || !pos || !freq) return bad("null pointer argument");
+    if ((uintptr_t)x % 16 || (uintptr_t)out % 16) return bad("x and out must be 16-byte aligned");
+    if (x_token_stride % 8 || x_head_stride % 8 || out_token_stride % 8 || out_head_stride % 8)
+        return bad("strides must be multiples of 8 elements");
+    if (x == out && (x_token_stride != out_token_stride || x_head_stride != out_head_stride))
+        return bad("in place needs equal strides");
+    const int units = head_dim / 16;
+    if (tokens > (int64_t)INT32_MAX * ROPE_THREADS / units) return bad("too many tokens");
+    const int64_t n = tokens * units;
+    const int per = rope_heads_per_thread(n, heads);
+    const RopeArgs R{(const unsigned long long*)freq, rot_dim, interleaved ? 1 : 0, amplitude};
+    const dim3 grid((unsigned)((n + ROPE_THREADS - 1) / ROPE_THREADS), (unsigned)((heads + per - 1) / per));
+    rope_kernel<<<grid, ROPE_THREADS, 0, (cudaStream_t)stream>>>((const uint16_t*)x, x_token_stride, x_head_stride,
+                                                                (uint16_t*)out, out_token_stride, out_head_stride, pos,
+                                                                R, n, units, heads, per);
+    const cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess) { set_last_error(cudaGetErrorString(e)); return KVO_ERR_CUDA; }
+    return KVO_OK;
+}

@@ -8,6 +8,7 @@ library or a CUDA device every call fails.
 from __future__ import annotations
 
 import ctypes
+import math
 import os
 from typing import List, Optional, Sequence
 
@@ -26,7 +27,8 @@ EXPORTS = ["kv_offload_init", "kv_offload_destroy", "select_topk", "index_diff",
            "kvo_decode_step_dual", "kvo_set_gather_reserve", "kvo_set_graphs", "kvo_append",
            "kvo_set_attn_impl", "kvo_set_select_impl", "kvo_resident_slots", "kvo_resident_fetched",
            "kvo_set_prefetch_budget", "kvo_set_lowrank_keys", "kvo_plan_attention", "kvo_plan_select", "kvo_set_wait_test",
-           "kvo_set_spec_policy", "kvo_spec_stats"]
+           "kvo_set_spec_policy", "kvo_spec_stats", "kvo_rope", "kvo_paged_append", "kvo_paged_attn",
+           "kvo_paged_attn_workspace"]
 PROFILE_KINDS = ["select", "diff", "coalesce", "gather_prefetch", "gather_urgent", "attention", "recon"]
 
 
@@ -42,6 +44,13 @@ class _Config(ctypes.Structure):
                 ("window", ctypes.c_int32), ("n_layers", ctypes.c_int32),
                 ("seq_lens", ctypes.POINTER(ctypes.c_int32)), ("max_append", ctypes.c_int32),
                 ("resident", ctypes.c_int32)]
+
+
+class _PagedCache(ctypes.Structure):
+    _fields_ = [("k_pages", ctypes.c_void_p), ("v_pages", ctypes.c_void_p), ("k_scale", ctypes.c_void_p),
+                ("v_scale", ctypes.c_void_p), ("table", ctypes.c_void_p), ("batch", ctypes.c_int32),
+                ("n_kv_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32), ("page_size", ctypes.c_int32),
+                ("n_pages", ctypes.c_int32), ("max_pages", ctypes.c_int32), ("format", ctypes.c_int32)]
 
 
 _LIB: Optional[ctypes.CDLL] = None
@@ -90,6 +99,11 @@ def lib() -> ctypes.CDLL:
         L.kvo_spec_stats.argtypes = [P, ctypes.POINTER(ctypes.c_int64)]
         DP, IP = ctypes.POINTER(ctypes.c_double), ctypes.POINTER(ctypes.c_int32)
         L.kvo_profile_trace.argtypes = [P, DP, DP, IP, IP, I, ctypes.POINTER(ctypes.c_int)]
+        I64, F, PC = ctypes.c_int64, ctypes.c_float, ctypes.POINTER(_PagedCache)
+        L.kvo_rope.argtypes = [VP, I64, I64, VP, I64, I64, VP, VP, I64, I, I, I, I, F, VP]
+        L.kvo_paged_append.argtypes = [PC, VP, I64, VP, I64, I64, VP, VP, VP, I, I, F, VP, I64, I, VP, VP, VP, VP]
+        L.kvo_paged_attn.argtypes = [PC, VP, I, VP, I64, VP, VP, I, VP, VP, VP, ctypes.c_size_t, VP, VP]
+        L.kvo_paged_attn_workspace.argtypes = [PC, I, I, I64, ctypes.POINTER(ctypes.c_size_t)]
         L.kvo_last_error.argtypes = [P]
         L.kvo_last_error.restype = ctypes.c_char_p
         for name in EXPORTS:
@@ -218,6 +232,224 @@ def sparse_decode_attn_static(q, k_buf, v_buf, slot_of_true, k_win, v_win, *, ba
                                            _ptr(v_win), _ptr(o), _ptr(lse), _ptr(status), batch, n_q_heads,
                                            n_kv_heads, head_dim, block_size, top_k, window,
                                            int(bool(fuse_window_merge)), _stream(stream)))
+    return o, lse
+
+
+def _need(dev, name, t, dtype, shape=None, contiguous=True):
+    """Check one buffer of a context-free call; raises ``KvoError`` before anything is launched."""
+    if t is None:
+        raise KvoError(KVO_ERR_INVALID, f"{name} is required")
+    if t.dtype != dtype:
+        raise KvoError(KVO_ERR_INVALID, f"{name} must be {dtype}, got {t.dtype}")
+    if shape is not None and t.shape != shape:
+        raise KvoError(KVO_ERR_INVALID, f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    if contiguous and not t.is_contiguous():
+        raise KvoError(KVO_ERR_INVALID, f"{name} must be contiguous")
+    if t.device != dev or dev.type != "cuda":
+        raise KvoError(KVO_ERR_INVALID, f"all buffers must be on one CUDA device, {name} is on {t.device}")
+    return t
+
+
+def _rows(dev, name, t, heads_contiguous=True):
+    """Check a bf16 [tokens][heads][d] buffer with free token (and head) strides; returns its strides."""
+    _need(dev, name, t, torch.bfloat16, contiguous=False)
+    if t.dim() != 3:
+        raise KvoError(KVO_ERR_INVALID, f"{name} must be [tokens][heads][head_dim]")
+    st, sh, sd = t.stride()
+    if t.shape[2] > 1 and sd != 1 or heads_contiguous and t.shape[1] > 1 and sh != t.shape[2]:
+        raise KvoError(KVO_ERR_INVALID, f"{name}: the last dimension{'s' if heads_contiguous else ''} must be contiguous")
+    # a dimension of one has no stride of its own
+    return (st if t.shape[0] > 1 else t.shape[1] * t.shape[2]), (sh if t.shape[1] > 1 else t.shape[2])
+
+
+class _on:
+    """Make ``device`` current around a library call (nothing when it is already)."""
+
+    def __init__(self, device):
+        self.want = device.index
+
+    def __enter__(self):
+        self.had = torch.cuda.current_device()
+        if self.want is not None and self.want != self.had:
+            torch.cuda.set_device(self.want)
+
+    def __exit__(self, *exc):
+        if self.want is not None and self.want != self.had:
+            torch.cuda.set_device(self.had)
+
+
+def rope_frequencies(rot_dim: int, base: float = 10000.0, scaling: Optional[str] = None, factor: float = 1.0,
+                     original_len: int = 8192, low: float = 1.0, high: float = 4.0, device="cuda"):
+    """Frequencies and amplitude for ``rope`` and ``paged_append`` (host only, made once per model).
+
+    Pair i turns by base^(-2i / rot_dim) radians a position.  ``scaling`` for
+    contexts ``factor`` times longer than ``original_len``: None; "linear" divides
+    every frequency by the factor; "banded" divides those that turn fewer than
+    ``low`` times within ``original_len``, keeps those that turn more than ``high``
+    times and blends between; "ramp" blends over the pair index instead, from the
+    pair that turns ``high`` times (kept) to the one that turns ``low`` times
+    (divided), and scales the rotated values by 0.1 ln(factor) + 1.
+    Returns (int64 tensor [rot_dim / 2] of turns per position in units of 2^-64,
+    amplitude).
+    """
+    if rot_dim < 16 or rot_dim % 16:
+        raise KvoError(KVO_ERR_INVALID, "rot_dim must be a positive multiple of 16")
+    if scaling not in (None, "linear", "banded", "ramp"):
+        raise KvoError(KVO_ERR_INVALID, f"scaling must be None, 'linear', 'banded' or 'ramp', got {scaling!r}")
+    if not (factor > 0 and base > 1 and original_len > 0 and high > low > 0):
+        raise KvoError(KVO_ERR_INVALID, "need factor > 0, base > 1, original_len > 0 and high > low > 0")
+    freq, amplitude = [], 1.0
+    index = lambda turns: rot_dim * math.log(original_len / (turns * 2 * math.pi)) / (2 * math.log(base))
+    for i in range(rot_dim // 2):
+        f = base ** (-2.0 * i / rot_dim)
+        if scaling == "linear":
+            keep = 0.0
+        elif scaling == "banded":
+            keep = (original_len * f / (2 * math.pi) - low) / (high - low)
+        elif scaling == "ramp":
+            first, last = max(math.floor(index(high)), 0), min(math.ceil(index(low)), rot_dim - 1)
+            keep = 1.0 - (i - first) / max(last - first, 1e-3)
+            amplitude = 0.1 * math.log(factor) + 1.0 if factor > 1 else 1.0
+        else:
+            keep = 1.0
+        keep = min(1.0, max(0.0, keep))
+        u = int(round((keep * f + (1.0 - keep) * f / factor) / (2 * math.pi) * 2.0 ** 64)) % 2 ** 64
+        freq.append(u - 2 ** 64 if u >= 2 ** 63 else u)
+    return torch.tensor(freq, dtype=torch.int64, device=device), amplitude
+
+
+def rope(x, pos, freq, interleaved: bool = False, amplitude: float = 1.0, out=None, stream=None):
+    """Rotary positions (C: kvo_rope).  x: CUDA bf16 [tokens][heads][d], last dimension contiguous, any token and
+    head stride; pos: int32 [tokens]; freq: ``rope_frequencies``.  ``out=x`` rotates in place."""
+    dev = x.device
+    st, sh = _rows(dev, "x", x, heads_contiguous=False)
+    T, H, d = x.shape
+    _need(dev, "pos", pos, torch.int32, (T,))
+    _need(dev, "freq", freq, torch.int64)
+    if out is None:
+        out = torch.empty((T, H, d), dtype=torch.bfloat16, device=dev)
+    elif out.shape != x.shape:
+        raise KvoError(KVO_ERR_INVALID, f"out must have shape {tuple(x.shape)}, got {tuple(out.shape)}")
+    ot, oh = _rows(dev, "out", out, heads_contiguous=False)
+    with _on(dev):
+        _check(lib().kvo_rope(x.data_ptr(), st, sh, out.data_ptr(), ot, oh, pos.data_ptr(), freq.data_ptr(), T, H, d,
+                              2 * freq.numel(), int(bool(interleaved)), amplitude, _stream(stream)))
+    return out
+
+
+def _paged(k_pages, v_pages, k_scale, v_scale, table) -> _PagedCache:
+    """Checked descriptor of a paged cache ([n_pages][Hkv][page_size][d] pools, int32 [batch][max_pages] table)."""
+    if k_pages is None or k_pages.dim() != 4 or table is None or table.dim() != 2:
+        raise KvoError(KVO_ERR_INVALID, "pages must be [n_pages][n_kv_heads][page_size][head_dim], table [batch][max_pages]")
+    dev, dt = k_pages.device, k_pages.dtype
+    if dt not in (torch.bfloat16, torch.float8_e4m3fn):
+        raise KvoError(KVO_ERR_INVALID, f"pages must be bfloat16 or float8_e4m3fn, got {dt}")
+    _need(dev, "k_pages", k_pages, dt)
+    _need(dev, "v_pages", v_pages, dt, k_pages.shape)
+    _need(dev, "table", table, torch.int32)
+    n, h, p, d = k_pages.shape
+    ks = vs = None
+    if dt == torch.float8_e4m3fn:
+        ks = _need(dev, "k_scale", k_scale, torch.float32, (n, h)).data_ptr()
+        vs = _need(dev, "v_scale", v_scale, torch.float32, (n, h)).data_ptr()
+    return _PagedCache(k_pages.data_ptr(), v_pages.data_ptr(), ks, vs, table.data_ptr(), table.shape[0], h, d, p, n,
+                       table.shape[1], 0 if ks is None else 1)
+
+
+def paged_append(k, v, k_pages, v_pages, table, start, *, cu=None, k_scale=None, v_scale=None, freq=None,
+                 interleaved: bool = False, amplitude: float = 1.0, q=None, q_out=None, k_out=None, status=None,
+                 stream=None):
+    """Append keys and values to a paged cache, keys (and q) rotated on the way (C: kvo_paged_append).
+
+    k, v: CUDA bf16 [tokens][Hkv][d]; k_pages, v_pages: [n_pages][Hkv][page_size][d], bfloat16 or
+    float8_e4m3fn with k_scale, v_scale fp32 [n_pages][Hkv]; table: int32 [batch][max_pages]; start: int32
+    [batch], the tokens each request has already; cu: int32 [batch + 1] token offsets (None: one token
+    each).  Returns q_out, the rotated q (None without q).
+    """
+    c = _paged(k_pages, v_pages, k_scale, v_scale, table)
+    dev = k_pages.device
+    kt, _ = _rows(dev, "k", k)
+    vt, _ = _rows(dev, "v", v)
+    T = k.shape[0]
+    shape = (T, c.n_kv_heads, c.head_dim)
+    if k.shape != shape or v.shape != shape:
+        raise KvoError(KVO_ERR_INVALID, f"k and v must have shape {shape}, got {tuple(k.shape)} and {tuple(v.shape)}")
+    _need(dev, "start", start, torch.int32, (c.batch,))
+    if cu is not None:
+        _need(dev, "cu", cu, torch.int32, (c.batch + 1,))
+    if freq is not None:
+        _need(dev, "freq", freq, torch.int64)
+    if k_out is not None:
+        _need(dev, "k_out", k_out, torch.bfloat16, shape)
+    if status is not None:
+        _need(dev, "status", status, torch.int32)
+    qt = hq = 0
+    if q is not None:
+        qt, _ = _rows(dev, "q", q)
+        hq = q.shape[1]
+        if q.shape != (T, hq, c.head_dim):
+            raise KvoError(KVO_ERR_INVALID, f"q must have shape {(T, hq, c.head_dim)}, got {tuple(q.shape)}")
+        if q_out is None:
+            q_out = torch.empty((T, hq, c.head_dim), dtype=torch.bfloat16, device=dev)
+        else:
+            _need(dev, "q_out", q_out, torch.bfloat16, (T, hq, c.head_dim))
+    with _on(dev):
+        _check(lib().kvo_paged_append(c, k.data_ptr(), kt, v.data_ptr(), vt, T, _ptr(cu), start.data_ptr(),
+                                      _ptr(freq), 0 if freq is None else 2 * freq.numel(), int(bool(interleaved)),
+                                      amplitude, _ptr(q), qt, hq, _ptr(q_out) if q is not None else None, _ptr(k_out),
+                                      _ptr(status), _stream(stream)))
+    return q_out if q is not None else None
+
+
+def paged_attn(q, k_pages, v_pages, table, lens, *, k_scale=None, v_scale=None, blocks=None, counts=None,
+               max_len: int = 0, o=None, lse=None, workspace=None, status=None, stream=None):
+    """Decode attention over a paged cache (C: kvo_paged_attn) -> (o bf16 [batch][Hq][d], lse fp32 [batch][Hq]).
+
+    q: CUDA bf16 [batch][Hq][d]; pools, scales and table as in ``paged_append``; lens: int32 [batch];
+    blocks: int32 [batch][Hkv][n], the logical pages each KV head attends to (e.g. ``select_topk``'s),
+    counts: int32 [batch][Hkv].  The workspace comes from torch's allocator when none is given; it must
+    then stay on the stream that is current (give one for another ``stream``).
+    """
+    c = _paged(k_pages, v_pages, k_scale, v_scale, table)
+    dev = k_pages.device
+    if q.dim() != 3:
+        raise KvoError(KVO_ERR_INVALID, "q must be [batch][n_q_heads][head_dim]")
+    hq = q.shape[1]
+    _need(dev, "q", q, torch.bfloat16, (c.batch, hq, c.head_dim))
+    _need(dev, "lens", lens, torch.int32, (c.batch,))
+    n_blocks = 0
+    if blocks is not None:
+        n_blocks = blocks.shape[-1]
+        if blocks.numel() != c.batch * c.n_kv_heads * n_blocks or n_blocks == 0:
+            raise KvoError(KVO_ERR_INVALID, f"blocks must be [batch][n_kv_heads][n], got {tuple(blocks.shape)}")
+        _need(dev, "blocks", blocks, torch.int32)
+    if counts is not None:
+        if blocks is None:
+            raise KvoError(KVO_ERR_INVALID, "counts needs blocks")
+        _need(dev, "counts", counts, torch.int32)
+        if counts.numel() != c.batch * c.n_kv_heads:
+            raise KvoError(KVO_ERR_INVALID, f"counts must be [batch][n_kv_heads], got {tuple(counts.shape)}")
+    if status is not None:
+        _need(dev, "status", status, torch.int32)
+    if o is None:
+        o = torch.empty((c.batch, hq, c.head_dim), dtype=torch.bfloat16, device=dev)
+    else:
+        _need(dev, "o", o, torch.bfloat16, (c.batch, hq, c.head_dim))
+    if lse is None:
+        lse = torch.empty((c.batch, hq), dtype=torch.float32, device=dev)
+    else:
+        _need(dev, "lse", lse, torch.float32, (c.batch, hq))
+    L = lib()
+    n = ctypes.c_size_t(0)
+    _check(L.kvo_paged_attn_workspace(c, hq, n_blocks, max_len, ctypes.byref(n)))
+    if workspace is None:
+        workspace = torch.empty(n.value, dtype=torch.uint8, device=dev)
+    else:
+        _need(dev, "workspace", workspace, torch.uint8)
+    with _on(dev):
+        _check(L.kvo_paged_attn(c, q.data_ptr(), hq, lens.data_ptr(), max_len, _ptr(blocks), _ptr(counts), n_blocks,
+                                o.data_ptr(), lse.data_ptr(), workspace.data_ptr(), workspace.numel(), _ptr(status),
+                                _stream(stream)))
     return o, lse
 
 

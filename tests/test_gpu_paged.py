@@ -1,0 +1,398 @@
+"""Rotary positions, the paged cache (bf16 and e4m3) and the attention over it, against plain 64-bit references."""
+import math
+
+import pytest
+import torch
+
+from sparse_kv_cache_landmark_gb300 import kvo
+from tests import paged_ref as ref
+
+pytestmark = pytest.mark.gpu
+E4M3 = torch.float8_e4m3fn
+
+
+def gen(seed):
+    return torch.Generator().manual_seed(seed)
+
+
+def normal(g, *shape, scale=1.0):
+    return (torch.randn(*shape, generator=g) * scale).bfloat16().cuda()
+
+
+def i32(x):
+    return torch.tensor(x, dtype=torch.int32, device="cuda")
+
+
+# ------------------------------------------------------------------ rotary positions
+@pytest.mark.parametrize("tokens,heads,d,rot,interleaved,scaling", [
+    (1, 1, 64, 64, False, None), (1, 40, 128, 128, True, "banded"), (5, 3, 128, 64, False, "linear"),
+    (37, 10, 128, 128, False, "ramp"), (33, 5, 64, 16, True, None), (6, 2, 48, 32, False, None),
+    (4, 1, 256, 256, True, "banded"), (300, 48, 128, 96, False, None)])
+def test_rope_matches_reference(tokens, heads, d, rot, interleaved, scaling):
+    g = gen(tokens * 1000 + heads)
+    freq, amp = kvo.rope_frequencies(rot, 500000.0, scaling, factor=8.0)
+    x = normal(g, tokens, heads, d)
+    pos = torch.randint(0, 1 << 20, (tokens,), generator=g, dtype=torch.int32)
+    pos[0] = 2 ** 31 - 1 if tokens > 1 else 131071
+    if tokens > 2:
+        pos[1], pos[2] = 0, -77777
+    y = kvo.rope(x, pos.cuda(), freq, interleaved, amp)
+    n = min(tokens, 40)
+    want, mag = ref.rope(x[:n], pos[:n], freq, interleaved, amp)
+    ref.check(y[:n], want, ref.rope_bound(want, mag), "rope")
+    assert torch.equal(y[..., rot:], x[..., rot:])
+
+
+def test_rope_strides_and_in_place():
+    """q and k heads of a fused projection, a head-major buffer, in place, and a single token of odd strides."""
+    g = gen(5)
+    freq, amp = kvo.rope_frequencies(128)
+    pos = i32([3, 70000, 12, 9, 9])
+    qkv = normal(g, 5, 12, 128)
+    want = kvo.rope(qkv[:, 2:9].contiguous(), pos, freq)
+    assert torch.equal(kvo.rope(qkv[:, 2:9], pos, freq), want)
+    head_major = qkv[:, 2:9].transpose(0, 1).contiguous().transpose(0, 1)
+    assert torch.equal(kvo.rope(head_major, pos, freq), want)
+    before = qkv.clone()
+    assert kvo.rope(qkv[:, 2:9], pos, freq, out=qkv[:, 2:9]).data_ptr() == qkv[:, 2:9].data_ptr()
+    assert torch.equal(qkv[:, 2:9], want)
+    assert torch.equal(qkv[:, :2], before[:, :2]) and torch.equal(qkv[:, 9:], before[:, 9:])
+    assert kvo.rope(qkv[:0], pos[:0], freq).shape == (0, 12, 128)
+    # turning by p, then by -p, comes back to within the two roundings
+    x = before[:, 2:9].float()
+    back = kvo.rope(want, -pos, freq).float()
+    pair = x.abs() + x.roll(64, -1).abs()
+    assert ((back - x).abs() <= 2 * 2.0 ** -8 * pair + 2.0 ** -19 * pair).all()
+
+
+# ------------------------------------------------------------------ append
+def pools(g, n_pages, hkv, page, d, e4m3):
+    """Pools full of stale bytes (NaN codes among them), scales full of NaN."""
+    if not e4m3:
+        k, v = normal(g, n_pages, hkv, page, d), normal(g, n_pages, hkv, page, d)
+        k[0] = math.nan
+        return k, v, None, None
+    raw = [torch.randint(0, 256, (n_pages, hkv, page, d), generator=g, dtype=torch.uint8).cuda().view(E4M3)
+           for _ in range(2)]
+    scale = [torch.full((n_pages, hkv), math.nan, device="cuda") for _ in range(2)]
+    return raw[0], raw[1], scale[0], scale[1]
+
+
+def bytes_of(t):
+    return t.view(torch.uint8 if t.element_size() == 1 else torch.int16).cpu().clone()
+
+
+def pow2_scale(amax):
+    s = 2.0 ** -100
+    while s * 448.0 < amax:
+        s *= 2
+    return s
+
+
+def expect_append(raw, scale, x, table, start, cu, page):
+    """The pool's bytes (and scales) after appending the bf16 rows x, by the definition."""
+    for b in range(len(start)):
+        at, end = start[b], start[b] + cu[b + 1] - cu[b]
+        while at < end:
+            p, lo, n = table[b][at // page], at % page, min(page - at % page, end - at)
+            rows = x[cu[b] + at - start[b]:cu[b] + at - start[b] + n]
+            for h in range(x.shape[1]):
+                if scale is None:
+                    raw[p, h, lo:lo + n] = rows[:, h].view(torch.int16)
+                    continue
+                r = rows[:, h].float()
+                fin = r[torch.isfinite(r)]
+                s = pow2_scale(float(fin.abs().max()) if fin.numel() else 0.0)
+                if lo:
+                    old = float(scale[p, h])
+                    s = max(s, old)
+                    raw[p, h, :lo] = (raw[p, h, :lo].view(E4M3).float() * (old / s)).to(E4M3).view(torch.uint8)
+                scale[p, h] = s
+                r = torch.where(torch.isfinite(r), r, torch.full_like(r, math.nan))
+                raw[p, h, lo:lo + n] = (r * (1.0 / s)).to(E4M3).view(torch.uint8)
+            at += n
+
+
+def same_bytes(got, want, what):
+    """Equal bytes, any NaN code of e4m3 equal to any other."""
+    nan = lambda t: (t & 0x7F) == 0x7F if t.dtype == torch.uint8 else torch.zeros_like(t, dtype=torch.bool)
+    bad = (got != want) & ~(nan(got) & nan(want))
+    assert not bad.any(), f"{what}: {int(bad.sum())} of {bad.numel()} differ, first at {bad.nonzero()[0].tolist()}"
+
+
+@pytest.mark.parametrize("e4m3", [True, False])
+@pytest.mark.parametrize("d,hkv,hq,page,counts,starts,rot,interleaved", [
+    (128, 2, 8, 16, [1, 1, 1], [0, 15, 16], 128, False),          # decode: a page begun, filled, begun again
+    (64, 1, 1, 32, [1], [31], 32, True),
+    (128, 1, 3, 64, [70, 0, 1, 200], [3, 5, 63, 0], 64, False),    # ragged prompts, one request without tokens
+    (64, 3, 6, 128, [129, 257], [127, 1], 64, True),
+    (128, 2, 2, 128, [300], [0], 0, False),                       # no rotation
+    (64, 8, 16, 16, [17] * 40, list(range(40)), 48, False)])
+def test_append_matches_definition(e4m3, d, hkv, hq, page, counts, starts, rot, interleaved):
+    g = gen(page + d + len(counts))
+    b, tokens = len(counts), sum(counts)
+    cu = [0]
+    for n in counts:
+        cu.append(cu[-1] + n)
+    per = [(s + n + page - 1) // page for s, n in zip(starts, counts)]
+    n_pages = sum(per) + 2
+    order = torch.randperm(n_pages, generator=g).tolist()
+    table = [[order.pop() for _ in range(p)] + [0] * (max(per) - p) for p in per]
+    kp, vp, ks, vs = pools(g, n_pages, hkv, page, d, e4m3)
+    if e4m3:      # pages that the requests have begun hold values of a known scale, some too small for what comes
+        for i, s in enumerate(starts):
+            if s % page:
+                p = table[i][s // page]
+                for sc, pool in ((ks, kp), (vs, vp)):
+                    sc[p] = torch.tensor([2.0 ** (-20 + 9 * ((i + h) % 3)) for h in range(hkv)]).cuda()
+                    pool[p].copy_((torch.randn(hkv, page, d, generator=g) * 90).clamp(-448, 448).to(E4M3).cuda())
+    wide = normal(g, tokens + 3, hq + 2 * hkv, d)                  # a fused projection with padding rows behind
+    q, k, v = wide[:tokens, :hq], wide[:tokens, hq:hq + hkv], wide[:tokens, hq + hkv:]
+    freq = kvo.rope_frequencies(rot, 10000.0)[0] if rot else None
+    k_out = torch.full((tokens, hkv, d), 7.0, dtype=torch.bfloat16, device="cuda")
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    want_k, want_v = bytes_of(kp), bytes_of(vp)
+    want_ks, want_vs = (ks.cpu(), vs.cpu()) if e4m3 else (None, None)
+    one = all(n == 1 for n in counts)
+    for again in range(2):        # the same rows again: nothing changes
+        q_out = kvo.paged_append(k, v, kp, vp, i32(table), i32(starts), cu=None if one else i32(cu), k_scale=ks,
+                                 v_scale=vs, freq=freq, interleaved=interleaved, q=q, k_out=k_out, status=status)
+        assert int(status.item()) == 0
+        if again:
+            assert torch.equal(bytes_of(kp), first[0]) and torch.equal(bytes_of(vp), first[1])
+            break
+        first = bytes_of(kp), bytes_of(vp)
+        pos = torch.cat([torch.arange(n) + s for n, s in zip(counts, starts)])
+        if rot:
+            want, mag = ref.rope(k, pos, freq, interleaved, 1.0)
+            ref.check(k_out, want, ref.rope_bound(want, mag), "k_out")
+            assert torch.equal(q_out, kvo.rope(q, pos.int().cuda(), freq, interleaved))
+        else:
+            assert torch.equal(k_out, k) and torch.equal(q_out, q)
+        expect_append(want_k, want_ks, k_out.cpu(), table, starts, cu, page)
+        expect_append(want_v, want_vs, v.cpu(), table, starts, cu, page)
+        same_bytes(bytes_of(kp), want_k, "k pages")
+        same_bytes(bytes_of(vp), want_v, "v pages")
+        if e4m3:
+            assert torch.equal(torch.nan_to_num(ks.cpu(), -1.0), torch.nan_to_num(want_ks, -1.0))
+            assert torch.equal(torch.nan_to_num(vs.cpu(), -1.0), torch.nan_to_num(want_vs, -1.0))
+
+
+def test_append_extreme_values():
+    """Zeros, the largest bf16, subnormals, infinities and NaN: scales from the finite values, NaN codes for the rest."""
+    rows = torch.zeros(6, 1, 64)
+    rows[1, 0, 0] = 3.3e38
+    rows[2, 0, :3] = torch.tensor([math.inf, -math.inf, math.nan])
+    rows[2, 0, 3] = 448.0
+    rows[3, 0, 5] = 1e-39
+    rows[4, 0, 7] = 449.0 * 2 ** -9
+    rows[5, 0, :2] = torch.tensor([448.0, 2.0 ** -9])
+    x = rows.bfloat16().cuda()
+    kp, vp, ks, vs = pools(gen(1), 6, 1, 16, 64, True)
+    kvo.paged_append(x, x, kp, vp, i32([[i] for i in range(6)]), i32([0] * 6), k_scale=ks, v_scale=vs)
+    want, want_s = bytes_of(kp), torch.full((6, 1), math.nan)
+    expect_append(want, want_s, x.cpu(), [[i] for i in range(6)], [0] * 6, list(range(7)), 16)
+    same_bytes(bytes_of(kp), want, "k pages")
+    same_bytes(bytes_of(vp)[:, :, :1], bytes_of(kp)[:, :, :1], "v pages")
+    assert torch.equal(ks.cpu(), want_s) and torch.equal(vs.cpu(), want_s)
+    assert float(ks[0]) == 2.0 ** -100 and float(ks[2]) == 1.0
+
+
+def test_append_skips_what_is_out_of_range():
+    """Bad page ids, tokens past the table and bad offsets: a status bit, the rest of the call unharmed."""
+    g = gen(3)
+    k = normal(g, 4, 1, 64)
+    for table, start, cu, bit in [([[0], [9], [1], [-1]], [0, 0, 0, 0], None, kvo.DEV_BAD_BLOCK_ID),
+                                  ([[0], [2], [1], [3]], [0, 16, 0, -5], None, kvo.DEV_BAD_COUNT),
+                                  ([[0], [1]], [0, 0], [0, 2, 9], kvo.DEV_BAD_COUNT),
+                                  ([[0], [1]], [0, 0], [0, 3, 1], kvo.DEV_BAD_COUNT)]:
+        kp, vp, ks, vs = pools(g, 4, 1, 16, 64, True)
+        before = bytes_of(kp)
+        status = torch.zeros(1, dtype=torch.int32, device="cuda")
+        q_out = torch.full((4, 1, 64), 5.0, dtype=torch.bfloat16, device="cuda")
+        kvo.paged_append(k, k, kp, vp, i32(table), i32(start), cu=None if cu is None else i32(cu), k_scale=ks,
+                         v_scale=vs, q=k, q_out=q_out, status=status)
+        assert int(status.item()) == bit
+        after = bytes_of(kp)
+        good = [0, 1] if cu is None and bit == kvo.DEV_BAD_BLOCK_ID else [0, 1] if cu is None else [0]
+        assert (after[0, 0, 0] != before[0, 0, 0]).any()
+        for p in set(range(4)) - set(good):
+            assert torch.equal(after[p], before[p])
+
+
+# ------------------------------------------------------------------ attention
+def cache_of(g, lens, hkv, page, d, e4m3, spare=1):
+    """Pools whose rows behind each request's last token are NaN, scales of several binades, and the 64-bit rows."""
+    need = [max(1, (n + page - 1) // page) for n in lens]
+    n_pages = sum(need) + spare
+    order = torch.randperm(n_pages, generator=g).tolist()
+    table = [[order.pop() for _ in range(p)] + [order[0]] * (max(need) - p) for p in need]
+    scale = [None, None]
+    if e4m3:
+        pool = [(torch.randn(n_pages, hkv, page, d, generator=g) * 100).clamp(-448, 448).to(E4M3) for _ in range(2)]
+        scale = [torch.exp2(torch.randint(-9, -5, (n_pages, hkv), generator=g).float()) for _ in range(2)]
+        scale[1][0] *= 1.37                                        # a scale that is no power of two is allowed
+        full = [p.double() * s.double()[..., None, None] for p, s in zip(pool, scale)]
+    else:
+        pool = [torch.randn(n_pages, hkv, page, d, generator=g).bfloat16() for _ in range(2)]
+        full = [p.double() for p in pool]
+    rows = []
+    for i, n in enumerate(lens):
+        at = torch.tensor(table[i][:(n + page - 1) // page], dtype=torch.long)
+        rows.append([f[at].transpose(0, 1).flatten(1, 2)[:, :n] for f in full])
+        last = table[i][(n - 1) // page] if n else None
+        if n and n % page:
+            for p in pool:
+                p.view(torch.uint8 if e4m3 else torch.int16)[last, :, n % page:] = 0x7F if e4m3 else 0x7FC0
+    to = lambda t: None if t is None else t.cuda()
+    return [to(p) for p in pool], [to(s) for s in scale], i32(table), rows
+
+
+def check_attention(q, got, rows, hkv, weight, pick=None):
+    o, lse = got
+    r = q.shape[1] // hkv
+    for b, (k, v) in enumerate(rows):
+        for h in range(q.shape[1]):
+            kk, vv = k[h // r], v[h // r]
+            if pick is not None:
+                kk, vv = kk[pick[b][h // r]], vv[pick[b][h // r]]
+            want, wl, tol, tl = ref.attention(q[b, h].double().cpu(), kk, vv, weight)
+            ref.check(o[b, h], want, tol, f"o[{b}][{h}]")
+            assert float(lse[b, h]) == wl or abs(float(lse[b, h]) - wl) <= tl, (b, h, float(lse[b, h]), wl)
+
+
+@pytest.mark.parametrize("e4m3", [True, False])
+@pytest.mark.parametrize("d,hkv,r,page,lens", [
+    (128, 1, 1, 16, [1]), (64, 1, 1, 16, [1]), (128, 2, 4, 32, [0, 33, 16, 100]), (64, 2, 4, 16, [4096]),
+    (128, 1, 16, 64, [2500, 7]), (64, 3, 9, 128, [129, 0, 640, 1]), (128, 8, 4, 64, [700, 1, 513]),
+    (64, 1, 5, 32, [15, 16, 17, 31, 32, 33, 63, 64, 65] * 3), (128, 1, 2, 16, [0, 0]), (128, 1, 8, 128, [9000])])
+def test_paged_attention_matches_reference(e4m3, d, hkv, r, page, lens):
+    g = gen(d + r + len(lens))
+    (kp, vp), (ks, vs), table, rows = cache_of(g, lens, hkv, page, d, e4m3)
+    q = normal(g, len(lens), hkv * r, d, scale=1.5)
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    first = None
+    for max_len in (0, max(max(lens), 1)):
+        got = kvo.paged_attn(q, kp, vp, table, i32(lens), k_scale=ks, v_scale=vs, max_len=max_len, status=status)
+        check_attention(q, got, rows, hkv, ref.F16 if e4m3 else ref.BF16)
+    again = kvo.paged_attn(q, kp, vp, table, i32(lens), k_scale=ks, v_scale=vs, max_len=max_len, status=status)
+    assert torch.equal(again[0], got[0]) and torch.equal(again[1], got[1])
+    assert int(status.item()) == 0
+
+
+@pytest.mark.parametrize("e4m3", [True, False])
+@pytest.mark.parametrize("d,hkv,r,page,n_blocks,lens", [
+    (128, 2, 4, 32, 3, [300, 70]), (64, 1, 8, 16, 40, [700, 3, 0]), (128, 4, 1, 64, 12, [1500])])
+def test_paged_attention_over_listed_blocks(e4m3, d, hkv, r, page, n_blocks, lens):
+    """Each KV head its own blocks, a cut last one, one past the end, one twice, and counts of every size."""
+    g = gen(n_blocks)
+    (kp, vp), (ks, vs), table, rows = cache_of(g, lens, hkv, page, d, e4m3)
+    have = table.shape[1]
+    blocks = torch.randint(0, have, (len(lens), hkv, n_blocks), generator=g, dtype=torch.int32)
+    blocks[0, 0, 0] = (lens[0] - 1) // page
+    blocks[0, 0, -1] = blocks[0, 0, 0]
+    counts = torch.randint(0, n_blocks + 1, (len(lens), hkv), generator=g, dtype=torch.int32)
+    counts[0, 0] = n_blocks
+    counts[-1, -1] = 0
+    for cnt in (None, counts):
+        pick = []
+        for b, n in enumerate(lens):
+            pick.append([])
+            for h in range(hkv):
+                use = blocks[b, h, :n_blocks if cnt is None else int(cnt[b, h])].tolist()
+                pick[-1].append(torch.tensor([t for x in use for t in range(x * page, min(n, (x + 1) * page))],
+                                             dtype=torch.long))
+        q = normal(g, len(lens), hkv * r, d)
+        got = kvo.paged_attn(q, kp, vp, table, i32(lens), k_scale=ks, v_scale=vs, blocks=blocks.cuda(),
+                             counts=None if cnt is None else cnt.cuda())
+        check_attention(q, got, rows, hkv, ref.F16 if e4m3 else ref.BF16, pick)
+
+
+def test_paged_attention_extreme_scores():
+    """Scores far apart (the maximum rises late), a q row of zeros, large and tiny q, NaN in an attended key."""
+    g = gen(11)
+    lens, d, page = [400, 400, 400, 400, 64], 64, 16
+    (kp, vp), (ks, vs), table, rows = cache_of(g, lens, 1, page, d, True)
+    q = normal(g, 5, 2, d)
+    q[0] *= 60.0
+    q[1] = 0.0
+    q[2] *= 1e-20
+    q[3, 0], q[3, 1] = rows[3][0][0][399].bfloat16().cuda() * 30, -rows[3][0][0][0].bfloat16().cuda() * 30
+    got = kvo.paged_attn(q, kp, vp, table, i32(lens), k_scale=ks, v_scale=vs)
+    check_attention(q, got, rows, 1, ref.F16)
+    kp.view(torch.uint8)[int(table[4, 1]), 0, 3, 5] = 0x7F
+    o, lse = kvo.paged_attn(q, kp, vp, table, i32(lens), k_scale=ks, v_scale=vs)
+    assert o[4].isnan().all() and lse[4].isnan().all()
+    assert torch.equal(o[:4], got[0][:4])
+
+
+def test_paged_attention_reports_what_is_out_of_range():
+    g = gen(2)
+    (kp, vp), (ks, vs), table, rows = cache_of(g, [64, 64], 1, 16, 64, True)
+    q = normal(g, 2, 4, 64)
+    run = lambda tb, ln, **kw: kvo.paged_attn(q, kp, vp, tb, ln, k_scale=ks, v_scale=vs, status=status, **kw)
+    good = kvo.paged_attn(q, kp, vp, table, i32([64, 64]), k_scale=ks, v_scale=vs)
+    for bad_id in (-1, kp.shape[0], 2 ** 31 - 1):
+        status = torch.zeros(1, dtype=torch.int32, device="cuda")
+        tb = table.clone()
+        tb[1, 2] = bad_id
+        o, _ = run(tb, i32([64, 64]))
+        assert int(status.item()) == kvo.DEV_BAD_BLOCK_ID
+        assert torch.equal(o[0], good[0][0])
+        keep = torch.tensor([t for t in range(64) if t // 16 != 2])
+        check_attention(q[1:], (o[1:], _[1:]), [[rows[1][0][:, keep], rows[1][1][:, keep]]], 1, ref.F16)
+    for lens in ([64, -3], [64, 10 ** 6]):
+        status = torch.zeros(1, dtype=torch.int32, device="cuda")
+        o, _ = run(table, i32(lens))
+        assert int(status.item()) == kvo.DEV_BAD_COUNT and torch.equal(o[0], good[0][0])
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    run(table, i32([64, 64]), blocks=i32([[[0, 1, -1, 99]], [[0, 1, 2, 3]]]))
+    assert int(status.item()) == kvo.DEV_BAD_BLOCK_ID
+
+
+def test_append_then_attend_step_by_step():
+    """Prompts, then tokens one by one, through the 8-bit cache: what a decode loop does, replayed from a graph and
+    on a stream of its own."""
+    g = gen(21)
+    d, hkv, r, page, prompt, steps = 128, 2, 4, 16, [37, 5, 16], 20
+    b = len(prompt)
+    cap = (max(prompt) + steps + page - 1) // page
+    table = torch.randperm(b * cap, generator=g).int().view(b, cap).cuda()
+    kp = torch.zeros(b * cap, hkv, page, d, dtype=E4M3, device="cuda")
+    vp, ks = torch.zeros_like(kp), torch.ones(b * cap, hkv, device="cuda")
+    vs = torch.ones_like(ks)
+    freq, amp = kvo.rope_frequencies(d, 500000.0, "banded", 8.0)
+    cu = [0]
+    for n in prompt:
+        cu.append(cu[-1] + n)
+    k, v = normal(g, cu[-1], hkv, d), normal(g, cu[-1], hkv, d)
+    kvo.paged_append(k, v, kp, vp, table, i32([0] * b), cu=i32(cu), k_scale=ks, v_scale=vs, freq=freq, amplitude=amp)
+    lens, start = i32([n + 1 for n in prompt]), i32(prompt)
+    q, kn, vn = normal(g, b, hkv * r, d), normal(g, b, hkv, d), normal(g, b, hkv, d)
+
+    def step():
+        qr = kvo.paged_append(kn, vn, kp, vp, table, start, k_scale=ks, v_scale=vs, freq=freq, amplitude=amp, q=q)
+        out = kvo.paged_attn(qr, kp, vp, table, lens, k_scale=ks, v_scale=vs)
+        start.add_(1)
+        lens.add_(1)
+        return qr, out
+
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        step()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=side):
+            qr, got = step()
+        for i in range(steps - 1):
+            for t in (q, kn, vn):
+                t.copy_(normal(g, *t.shape, scale=1.0 + i))
+            graph.replay()
+            if i % 6 == 5:
+                side.synchronize()
+                n = [p + 2 + i for p in prompt]
+                codes = [(p.double() * s.double()[..., None, None]).cpu() for p, s in ((kp, ks), (vp, vs))]
+                rows = [[c[table[j].cpu().long()].transpose(0, 1).flatten(1, 2)[:, :n[j]] for c in codes]
+                        for j in range(b)]
+                check_attention(qr, got, rows, hkv, ref.F16)
+    torch.cuda.current_stream().wait_stream(side)

@@ -1,0 +1,140 @@
+"""What the rotary and paged-cache calls refuse, on the host, before anything is launched (CPU only)."""
+import ctypes
+
+import pytest
+import torch
+
+from sparse_kv_cache_landmark_gb300 import kvo
+
+
+@pytest.fixture(scope="module")
+def lib():
+    from sparse_kv_cache_landmark_gb300 import build
+    build.build()
+    return kvo.lib()
+
+
+P = 4096          # an aligned address that is never read
+
+
+def refused(lib, st, frag):
+    assert st == kvo.KVO_ERR_INVALID
+    assert frag in lib.kvo_last_error(None).decode()
+
+
+@pytest.mark.parametrize("kw,frag", [
+    (dict(tokens=-1), "tokens"), (dict(heads=0), "heads"), (dict(head_dim=24), "head_dim"), (dict(rot=8), "rot_dim"),
+    (dict(rot=144), "rot_dim"), (dict(x=None), "null"), (dict(out=None), "null"), (dict(pos=None), "null"),
+    (dict(freq=None), "null"), (dict(x=P + 8), "aligned"), (dict(xs=132), "strides"), (dict(out=P, os=256), "in place")])
+def test_rope_refuses(lib, kw, frag):
+    a = dict(x=P, xs=128, xh=128, out=2 * P, os=128, oh=128, pos=P, freq=P, tokens=4, heads=1, head_dim=128, rot=128)
+    a.update(kw)
+    refused(lib, lib.kvo_rope(a["x"], a["xs"], a["xh"], a["out"], a["os"], a["oh"], a["pos"], a["freq"], a["tokens"],
+                              a["heads"], a["head_dim"], a["rot"], 0, 1.0, None), frag)
+
+
+def test_nothing_to_do_launches_nothing(lib):
+    assert lib.kvo_rope(None, 0, 0, None, 0, 0, None, None, 0, 1, 128, 128, 0, 1.0, None) == kvo.KVO_OK
+    c = cache()
+    assert lib.kvo_paged_append(c, None, 0, None, 0, 0, None, None, None, 0, 0, 1.0, None, 0, 0, None, None, None,
+                                None) == kvo.KVO_OK
+    c.batch = 0
+    assert lib.kvo_paged_attn(c, None, 8, None, 0, None, None, 0, None, None, None, 0, None, None) == kvo.KVO_OK
+
+
+def cache(**kw):
+    a = dict(k=P, v=P, ks=P, vs=P, table=P, batch=2, hkv=2, d=128, page=32, n_pages=8, max_pages=4, fmt=1)
+    a.update(kw)
+    return kvo._PagedCache(a["k"], a["v"], a["ks"], a["vs"], a["table"], a["batch"], a["hkv"], a["d"], a["page"],
+                           a["n_pages"], a["max_pages"], a["fmt"])
+
+
+BAD_CACHES = [(dict(batch=-1), "batch"), (dict(hkv=0), "n_kv_heads"), (dict(d=96), "head_dim"), (dict(page=48), "page_size"),
+              (dict(n_pages=0), "n_pages"), (dict(max_pages=0), "max_pages"), (dict(fmt=2), "format"),
+              (dict(k=None), "null"), (dict(table=None), "null"), (dict(v=P + 4), "aligned"), (dict(ks=None), "k_scale"),
+              (dict(max_pages=2 ** 27), "31 bits"), (dict(n_pages=2 ** 27), "31 bits")]
+
+
+@pytest.mark.parametrize("kw,frag", BAD_CACHES)
+def test_both_calls_refuse_bad_caches(lib, kw, frag):
+    c = cache(**kw)
+    refused(lib, lib.kvo_paged_append(c, P, 256, P, 256, 2, None, P, None, 0, 0, 1.0, None, 0, 0, None, None, None, None), frag)
+    refused(lib, lib.kvo_paged_attn(c, P, 8, P, 0, None, None, 0, P, P, P, 1 << 30, None, None), frag)
+    n = ctypes.c_size_t(7)
+    refused(lib, lib.kvo_paged_attn_workspace(c, 8, 0, 0, ctypes.byref(n)), frag)
+    assert n.value == 0
+
+
+@pytest.mark.parametrize("kw,frag", [
+    (dict(tokens=-1), "tokens"), (dict(tokens=3), "appends one token"), (dict(k=None), "null"), (dict(start=None), "null"),
+    (dict(freq=P, rot=8), "rot_dim"), (dict(freq=P, rot=256), "rot_dim"), (dict(q=P, q_out=None), "q_out"),
+    (dict(q=P, q_out=P, hq=0), "n_q_heads"), (dict(v=P + 2), "aligned"), (dict(kt=250), "strides")])
+def test_append_refuses(lib, kw, frag):
+    a = dict(k=P, kt=256, v=P, tokens=2, start=P, freq=None, rot=0, q=None, hq=8, q_out=None)
+    a.update(kw)
+    refused(lib, lib.kvo_paged_append(cache(), a["k"], a["kt"], a["v"], 256, a["tokens"], None, a["start"], a["freq"],
+                                      a["rot"], 0, 1.0, a["q"], 1024, a["hq"], a["q_out"], None, None, None), frag)
+    refused(lib, lib.kvo_paged_append(None, P, 256, P, 256, 2, None, P, None, 0, 0, 1.0, None, 0, 0, None, None, None,
+                                      None), "null cache")
+
+
+@pytest.mark.parametrize("kw,frag", [
+    (dict(hq=7), "multiple"), (dict(hq=34), "<= 16"), (dict(q=None), "null"), (dict(lens=None), "null"),
+    (dict(o=None), "null"), (dict(ws=None), "null"), (dict(max_len=-1), "max_len"), (dict(blocks=P, n=0), "n_blocks"),
+    (dict(counts=P), "counts"), (dict(q=P + 2), "aligned"), (dict(ws=P + 16), "aligned"), (dict(size=64), "too small"),
+    (dict(blocks=P, n=2 ** 28), "31 bits")])
+def test_attention_refuses(lib, kw, frag):
+    a = dict(q=P, hq=8, lens=P, max_len=0, blocks=None, counts=None, n=0, o=P, ws=P, size=1 << 30)
+    a.update(kw)
+    refused(lib, lib.kvo_paged_attn(cache(), a["q"], a["hq"], a["lens"], a["max_len"], a["blocks"], a["counts"], a["n"],
+                                    a["o"], P, a["ws"], a["size"], None, None), frag)
+
+
+def test_workspace_grows_with_the_work(lib):
+    n = ctypes.c_size_t(0)
+    sizes = []
+    for max_len in (1, 128, 0):
+        assert lib.kvo_paged_attn_workspace(cache(max_pages=1024), 8, 0, max_len, ctypes.byref(n)) == kvo.KVO_OK
+        sizes.append(n.value)
+    assert 0 < sizes[0] < sizes[2] and sizes == sorted(sizes)
+
+
+def test_wrappers_check_buffers():
+    bf = lambda *s: torch.zeros(*s, dtype=torch.bfloat16)
+    i = lambda *s: torch.zeros(*s, dtype=torch.int32)
+    freq, amp = kvo.rope_frequencies(64, device="cpu")
+    assert amp == 1.0 and freq.shape == (32,)
+    with pytest.raises(kvo.KvoError, match="bfloat16"):
+        kvo.rope(torch.zeros(2, 1, 64), i(2), freq)
+    with pytest.raises(kvo.KvoError, match="CUDA device"):
+        kvo.rope(bf(2, 1, 64), i(2), freq)
+    with pytest.raises(kvo.KvoError, match="CUDA device"):
+        kvo.paged_append(bf(2, 1, 64), bf(2, 1, 64), bf(4, 1, 16, 64), bf(4, 1, 16, 64), i(2, 2), i(2))
+    with pytest.raises(kvo.KvoError, match="pages must be"):
+        kvo.paged_attn(bf(2, 4, 64), bf(4, 16, 64), bf(4, 16, 64), i(2, 2), i(2))
+    with pytest.raises(kvo.KvoError, match="bfloat16 or float8"):
+        kvo.paged_attn(bf(2, 4, 64), i(4, 1, 16, 64), i(4, 1, 16, 64), i(2, 2), i(2))
+    for bad in (dict(scaling="cubic"), dict(factor=0.0), dict(rot_dim=20), dict(base=1.0), dict(low=4.0, high=1.0)):
+        with pytest.raises(kvo.KvoError):
+            kvo.rope_frequencies(**{**dict(rot_dim=64, device="cpu"), **bad})
+
+
+def test_rope_frequencies():
+    """Turns per position in units of 2^-64: base^(-2i/rot) radians, and what each scaling leaves alone or divides."""
+    import math
+    turns = lambda t: [(x % 2 ** 64) / 2.0 ** 64 for x in t.tolist()]
+    plain = turns(kvo.rope_frequencies(128, 500000.0, device="cpu")[0])
+    for i, f in enumerate(plain):
+        assert math.isclose(f, 500000.0 ** (-2 * i / 128) / (2 * math.pi), rel_tol=1e-12)
+    lin = turns(kvo.rope_frequencies(128, 500000.0, "linear", 4.0, device="cpu")[0])
+    assert all(math.isclose(4 * a, b, rel_tol=1e-12) for a, b in zip(lin, plain))
+    for kind in ("banded", "ramp"):
+        f, amp = kvo.rope_frequencies(128, 500000.0, kind, 8.0, original_len=8192, low=1.0, high=4.0, device="cpu")
+        f = turns(f)
+        fast = [i for i, p in enumerate(plain) if p * 8192 > 8.0]
+        slow = [i for i, p in enumerate(plain) if p * 8192 < 0.5]
+        assert fast and slow
+        assert all(math.isclose(f[i], plain[i], rel_tol=1e-12) for i in fast)
+        assert all(math.isclose(8 * f[i], plain[i], rel_tol=1e-12) for i in slow)
+        assert all(f[i] <= plain[i] * (1 + 1e-12) and 8 * f[i] >= plain[i] * (1 - 1e-12) for i in range(64))
+        assert math.isclose(amp, 1.0 if kind == "banded" else 0.1 * math.log(8.0) + 1.0)
