@@ -469,9 +469,9 @@ kvo_status sparse_decode_attn_static(const void* q, const void* k_buf, const voi
                                      int fuse_window_merge, kvo_stream_t stream);
 
 /*
- * Around the decode step: rotary positions, and a paged cache held on the GPU
+ * Around the decode step: rotary positions, a paged cache held on the GPU
  * (bf16, or 8 bits with a scale for each page and KV head) with the attention
- * that reads it.  Like sparse_decode_attn_static these calls need no context;
+ * that reads it, and the attention over whole prompts.  Like sparse_decode_attn_static these calls need no context;
  * every pointer is memory of the current device unless stated, nothing is
  * allocated, kept or synchronized, and all of them can be captured into a CUDA
  * graph.  `stream` NULL is the legacy default stream.  Arguments are checked on
@@ -589,6 +589,31 @@ kvo_status kvo_paged_attn(const kvo_paged_cache* cache, const void* q, int n_q_h
  * (n_blocks 0: no block list).  Host only; reads the descriptor's sizes. */
 kvo_status kvo_paged_attn_workspace(const kvo_paged_cache* cache, int n_q_heads, int n_blocks, int64_t max_len,
                                     size_t* bytes_out);
+
+/*
+ * kvo_prompt_attn -- GQA attention over packed prompts.
+ *   q: bf16 [total_q][n_q_heads][head_dim], k, v: bf16 [total_k][n_kv_heads]
+ *   [head_dim]; heads contiguous, any token stride (elements, a multiple of 8
+ *   that covers the heads), 16-byte aligned.  head_dim 64 or 128, n_q_heads /
+ *   n_kv_heads <= 16.  cu_q, cu_k: device int32 [batch + 1], ascending: request
+ *   b's query tokens are rows cu_q[b] .. cu_q[b + 1] - 1, its keys rows cu_k[b]
+ *   .. cu_k[b + 1] - 1; either may be empty.  causal: query token i sees the
+ *   keys t <= i + (keys - queries), i.e. the last token sees them all (a chunk
+ *   of a prompt behind cached keys has more keys than queries); 0: every key.
+ *   o: bf16 [total_q][n_q_heads][head_dim], contiguous; lse (optional): fp32
+ *   [total_q][n_q_heads], natural log.  Softmax scale 1/sqrt(head_dim), fp32
+ *   accumulation, weights rounded to bf16, o rounded once to bf16.  A row that
+ *   sees no key gets o = 0, lse = -inf; rows outside every request keep their
+ *   bytes.  One request's values never reach another's rows; within a request a
+ *   NaN or an infinity in v may reach rows before it in the same 128-key tile.
+ *   Status bits: KVO_DEV_BAD_COUNT (offsets descending or outside 0..total: that
+ *   request is not written), KVO_DEV_TIMEOUT (a bounded wait of 2 s gave up:
+ *   outputs are invalid).  Errors: KVO_ERR_INVALID, KVO_ERR_CUDA.
+ */
+kvo_status kvo_prompt_attn(const void* q, int64_t q_token_stride, const void* k, int64_t k_token_stride,
+                           const void* v, int64_t v_token_stride, const int32_t* cu_q, const int32_t* cu_k, int batch,
+                           int64_t total_q, int64_t total_k, int n_q_heads, int n_kv_heads, int head_dim, int causal,
+                           void* o, float* lse, int32_t* status, kvo_stream_t stream);
 
 /*
  * kvo_set_gather_shape -- launch shape of the host -> HBM gather kernel:

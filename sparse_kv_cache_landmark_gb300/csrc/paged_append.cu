@@ -63,6 +63,12 @@ __device__ __forceinline__ void append_page(const AppendArgs& A) {
     const int u = blockIdx.x / A.hkv, h = blockIdx.x - u * A.hkv;
     __shared__ float red[2][APP_THREADS / 32];
 
+    if (blockIdx.x == 0 && A.status)                    // bad offsets of any request, also of one that no unit reaches
+        for (int i = tid; i < A.batch; i += APP_THREADS) {
+            int64_t t0, n;
+            int start;
+            if (!request_range(A, i, t0, n, start)) set_status(A.status, KVO_DEV_BAD_COUNT);
+        }
     // Request b has at most floor(n / page) + 2 touched pages, so its units start
     // at floor(cu[b] / page) + 2 b: every request finds its own without a scan.
     int b = u, j = 0;
@@ -73,10 +79,7 @@ __device__ __forceinline__ void append_page(const AppendArgs& A) {
     }
     int64_t t0, n;
     int start;
-    if (!request_range(A, b, t0, n, start)) {
-        if (tid == 0 && j == 0 && h == 0) set_status(A.status, KVO_DEV_BAD_COUNT);
-        return;
-    }
+    if (!request_range(A, b, t0, n, start)) return;
     const int64_t at = start / A.page + (int64_t)j;       // logical page
     const int64_t pos0 = max((int64_t)start, at * A.page), pos1 = min(start + n, (at + 1) * A.page);
     if (pos0 >= pos1) return;

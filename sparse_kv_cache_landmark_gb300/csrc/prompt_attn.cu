@@ -1,0 +1,451 @@
+// kvo_prompt_attn: causal (or full) GQA attention over packed prompts.
+//
+//   o_i = sum_t softmax_t(q_i . k_t / sqrt(d)) v_t,  t <= i + (nk - nq) where causal.
+//
+// Bound by the tensor cores: 4 d multiply-adds' worth of FLOPs for every
+// (query head, visible pair) against 4 bytes of K and V per pair tile.
+//
+// A work item is 256 query rows of one KV head: two tiles of 128 rows, each
+// floor(128 / r) tokens x the r query heads of the group, so that every K and V
+// tile is fetched once for the whole group and short prompts fill their tiles.
+// One CTA per item and SM, heaviest items first:
+//   warp 9   loads Q once and K, V tiles of 128 keys through a ring (TMA),
+//   warp 8   one thread issues tcgen05.mma: S_t = Q_t K^T (shared x shared) and
+//            O_t += P_t V (tensor memory x shared), in the order
+//            S_0(j), O_1(j-1), S_1(j), O_0(j): each tile's softmax runs beside
+//            the other tile's two products,
+//   warps 0-3, 4-7  the softmax of tile 0 and 1, one thread per row: S from
+//            tensor memory, online maximum and sum in fp32, P (bf16) back over S.
+// Tensor memory (512 columns): S_0, S_1 (128 each, P over their first half),
+// O_0, O_1 (d each, fp32).  O is rescaled, by the softmax threads, only when a
+// row's maximum rises by more than 2^8 (P then stays below 2^8 and the sum is
+// kept in the same units), which after the first tiles is rare.
+//
+// The weights P are rounded to bf16 as the matrix instruction takes them (V is
+// bf16, both operands have one type); their sum is taken in fp32 before that.
+#include <stdio.h>
+
+#include <algorithm>
+
+#include "kvo_internal.cuh"
+#include "paged.cuh"
+#include "tcgen05.cuh"
+#include "tensor_map.cuh"
+
+namespace kvo {
+
+constexpr int PR_THREADS = 384;
+constexpr int PR_ROWS = 128;               // query rows of a tile
+constexpr int PR_KEYS = 128;               // keys of a tile
+constexpr int PR_BLOCK = PR_ROWS * 128;    // bytes of 128 rows x 64 values
+constexpr float PR_RAISE = 8.f;            // log2
+
+template <int D>
+struct PrShape {
+    static constexpr int TILE = (D / 64) * PR_BLOCK;            // bytes of 128 rows x D values
+    static constexpr int STAGES = (192 * 1024 - 2 * TILE) / TILE;
+    static constexpr int SMEM = (2 + STAGES) * TILE + 1024;     // > half an SM's: one CTA per SM
+};
+
+struct PromptArgs {
+    const int32_t* cu_q;
+    const int32_t* cu_k;
+    uint16_t* o;
+    float* lse;                    // or NULL
+    int32_t* status;
+    long long total_q, total_k;
+    int batch, hq, hkv, r, tq, causal, units;
+    float scale_log2;
+    long long wait_ns;
+};
+
+__device__ __forceinline__ float pr_ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+struct PrShared {
+    uint64_t q_full, kv_full[12], kv_empty[12], s_full[2], p_full[2], o_done[2], v_tail, drain;
+    uint32_t tmem;
+    int abort;
+};
+
+// A wait that gives up after the limit, or once another warp has; every caller then leaves its loop.
+__device__ __forceinline__ bool pr_wait(PrShared& sh, const PromptArgs& A, uint64_t& bar, uint32_t parity) {
+    const uint32_t b = smem_u32(&bar);
+    for (int i = 0; i < 32; ++i)
+        if (mbar_try_wait(b, parity)) return true;
+    const uint64_t t0 = global_ns();
+    while (!mbar_try_wait(b, parity)) {
+        if (*(volatile int*)&sh.abort) return false;
+        if ((long long)(global_ns() - t0) > A.wait_ns) {
+            *(volatile int*)&sh.abort = 1;
+            if (A.status) atomicOr(A.status, KVO_DEV_TIMEOUT);
+            return false;
+        }
+    }
+    return true;
+}
+
+// The softmax of one tile: a thread owns row `row` of it; the row sees its request's keys [0, limit).
+template <int D>
+__device__ __forceinline__ void pr_softmax(PrShared& sh, const PromptArgs& A, int t, int n_tiles, int limit, bool real,
+                                           int64_t out_row) {
+    const uint32_t lanes = (uint32_t)(threadIdx.x & 96) << 16;          // this warp's quarter of the lanes
+    const uint32_t S = sh.tmem + 128 * t + lanes, O = sh.tmem + 256 + D * t + lanes;
+    float m = -INFINITY, l = 0.f;                                       // log2 units; l in units of 2^m
+    bool ok = true;
+    for (int j = 0; j < n_tiles; ++j) {
+        ok = pr_wait(sh, A, sh.s_full[t], j & 1);
+        if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
+        tc_fence_after();
+        uint32_t s[PR_KEYS];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) tmem_ld32(S + 32 * i, s + 32 * i);
+        tmem_wait_ld();
+        const int rem = limit - j * PR_KEYS;
+        if (rem < PR_KEYS) {
+#pragma unroll
+            for (int i = 0; i < PR_KEYS; ++i)
+                if (i >= rem) s[i] = 0xFF800000u;                       // -inf
+        }
+        float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+        for (int i = 0; i < PR_KEYS; i += 4)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) mx[e] = fmaxf(mx[e], __uint_as_float(s[i + e]));
+        const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * A.scale_log2;
+        if (__any_sync(0xffffffffu, top > m + PR_RAISE)) {
+            const float to = fmaxf(m, top);
+            const float f = m == -INFINITY ? 0.f : pr_ex2(m - to);
+            m = to;
+            l *= f;
+            if (j > 0) {
+                ok = pr_wait(sh, A, sh.o_done[t], (j - 1) & 1);
+                if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
+                tc_fence_after();
+#pragma unroll 1
+                for (int c = 0; c < D; c += 32) {
+                    uint32_t o[32];
+                    tmem_ld32(O + c, o);
+                    tmem_wait_ld();
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
+                    tmem_st32(O + c, o);
+                }
+            }
+        }
+        const float b = m == -INFINITY ? 0.f : -m;
+        float sum[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            uint32_t p[32];
+#pragma unroll
+            for (int i = 0; i < 32; ++i) {
+                const float x = pr_ex2(fmaf(__uint_as_float(s[64 * h + 2 * i]), A.scale_log2, b));
+                const float y = pr_ex2(fmaf(__uint_as_float(s[64 * h + 2 * i + 1]), A.scale_log2, b));
+                sum[(2 * i) & 3] += x;
+                sum[(2 * i + 1) & 3] += y;
+                const __nv_bfloat162 v = __floats2bfloat162_rn(x, y);
+                p[i] = *reinterpret_cast<const uint32_t*>(&v);
+            }
+            tmem_st32(S + 32 * h, p);
+        }
+        l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+        tmem_wait_st();
+        tc_fence_before();
+        mbar_arrive(smem_u32(&sh.p_full[t]));
+    }
+    if (ok && n_tiles > 0) {
+        ok = pr_wait(sh, A, sh.o_done[t], (n_tiles - 1) & 1);
+        ok = __all_sync(0xffffffffu, ok);
+        tc_fence_after();
+    }
+    if (!ok) return;
+    const float inv = l != 0.f ? 1.f / l : 0.f;
+#pragma unroll 1
+    for (int c = 0; c < D; c += 32) {
+        uint32_t o[32];
+        if (n_tiles > 0) {
+            tmem_ld32(O + c, o);
+            tmem_wait_ld();
+        } else {
+#pragma unroll
+            for (int i = 0; i < 32; ++i) o[i] = 0u;
+        }
+        if (real) {
+#pragma unroll
+            for (int i = 0; i < 32; i += 8) {
+                uint32_t w[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    // a row that saw nothing is zero, whatever its lane of tensor memory holds
+                    const float x = l != 0.f ? __uint_as_float(o[i + 2 * e]) * inv : 0.f;
+                    const float y = l != 0.f ? __uint_as_float(o[i + 2 * e + 1]) * inv : 0.f;
+                    const __nv_bfloat162 v = __floats2bfloat162_rn(x, y);
+                    w[e] = *reinterpret_cast<const uint32_t*>(&v);
+                }
+                *reinterpret_cast<uint4*>(A.o + out_row * D + c + i) = make_uint4(w[0], w[1], w[2], w[3]);
+            }
+        }
+    }
+    if (real && A.lse) A.lse[out_row] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
+}
+
+template <int D>
+__global__ void __launch_bounds__(PR_THREADS, 1)
+prompt_attn_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_k,
+                   const __grid_constant__ CUtensorMap map_v, const __grid_constant__ PromptArgs A) {
+    using P = PrShape<D>;
+    extern __shared__ uint8_t smem_raw[];
+    __shared__ PrShared sh;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int TU = 2 * A.tq;
+
+    if (blockIdx.x == 0 && A.status)           // bad offsets of any request, also of one that no item reaches
+        for (int i = tid; i < A.batch; i += PR_THREADS) {
+            const int64_t a = A.cu_q[i], e = A.cu_q[i + 1], c = A.cu_k[i], f = A.cu_k[i + 1];
+            if (a < 0 || e < a || e > A.total_q || c < 0 || f < c || f > A.total_k) atomicOr(A.status, KVO_DEV_BAD_COUNT);
+        }
+
+    // Request b has ceil(nq / TU) items; its slots start at floor(cu_q[b] / TU) + b, which leaves room for them.
+    const int g = blockIdx.x % A.hkv, u = A.units - 1 - (int)(blockIdx.x / A.hkv);
+    auto first = [&](int i) { return (int64_t)max(__ldg(A.cu_q + i), 0) / TU + i; };
+    const int b = warp_find(A.batch, u, first);
+    const int64_t j0 = u - first(b);
+    const int64_t qs = A.cu_q[b], qe = A.cu_q[b + 1], ks = A.cu_k[b], ke = A.cu_k[b + 1];
+    if (qs < 0 || qe < qs || qe > A.total_q || ks < 0 || ke < ks || ke > A.total_k) return;
+    const int nq = (int)(qe - qs), nk = (int)(ke - ks);
+    if (j0 < 0 || j0 * TU >= nq) return;
+    const int tok0 = (int)j0 * TU;
+    int n_t[2];
+#pragma unroll
+    for (int t = 0; t < 2; ++t) {
+        const int have = min(max(nq - tok0 - t * A.tq, 0), A.tq);
+        const int64_t see = A.causal ? min(max((int64_t)tok0 + t * A.tq + have + (nk - nq), (int64_t)0), (int64_t)nk) : nk;
+        n_t[t] = have ? (int)((see + PR_KEYS - 1) / PR_KEYS) : 0;
+    }
+    const int n = max(n_t[0], n_t[1]);
+
+    const uint32_t base = (smem_u32(smem_raw) + 1023u) & ~1023u;
+    const uint32_t ring = base + 2 * P::TILE;
+    if (tid == 0) {
+        mbar_init(smem_u32(&sh.q_full), 1);
+        for (int i = 0; i < P::STAGES; ++i) {
+            mbar_init(smem_u32(&sh.kv_full[i]), 1);
+            mbar_init(smem_u32(&sh.kv_empty[i]), 1);
+        }
+        for (int t = 0; t < 2; ++t) {
+            mbar_init(smem_u32(&sh.s_full[t]), 1);
+            mbar_init(smem_u32(&sh.p_full[t]), 128);
+            mbar_init(smem_u32(&sh.o_done[t]), 1);
+        }
+        mbar_init(smem_u32(&sh.v_tail), 1);
+        mbar_init(smem_u32(&sh.drain), 1);
+        sh.abort = 0;
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    if (warp == 8) tmem_alloc(smem_u32(&sh.tmem), 512);
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+
+    if (warp >= 8) {
+        regs_dec<88>();
+        if (warp == 9 && n > 0) {
+            // ------------------------------------------------ loads
+            int issued = 0;
+            bool ok = true;
+            if (lane == 0) {
+                const int tiles = n_t[1] > 0 ? 2 : 1;
+                mbar_expect_tx(smem_u32(&sh.q_full), (uint32_t)(tiles * (D / 64) * 128 * A.r * A.tq));
+                for (int t = 0; t < tiles; ++t)
+                    for (int x = 0; x < D / 64; ++x)
+                        tma_load_3d(base + t * P::TILE + x * PR_BLOCK, &map_q, 64 * x, g * A.r,
+                                    (int)qs + tok0 + t * A.tq, smem_u32(&sh.q_full));
+            }
+            for (int i = 0; i < 2 * n; ++i) {
+                const int st = i % P::STAGES, use = i / P::STAGES, key0 = (i >> 1) * PR_KEYS;
+                const bool is_v = i & 1;
+                if (use > 0) {
+                    ok = pr_wait(sh, A, sh.kv_empty[st], (use - 1) & 1);
+                    if (!__all_sync(0xffffffffu, ok)) break;
+                }
+                const uint32_t dst = ring + st * P::TILE;
+                // The last tile of a request runs into what lies behind it.  Its keys are masked as scores, but
+                // a weight of zero does not silence a NaN or an infinity in V: those rows are cleared here.
+                const bool tail = is_v && key0 + PR_KEYS > nk;
+                const uint32_t bar = smem_u32(tail ? &sh.v_tail : &sh.kv_full[st]);
+                if (lane == 0) {
+                    mbar_expect_tx(bar, P::TILE);
+                    for (int x = 0; x < D / 64; ++x)
+                        tma_load_3d(dst + x * PR_BLOCK, is_v ? &map_v : &map_k, 64 * x, g, (int)ks + key0, bar);
+                }
+                if (tail) {
+                    ok = pr_wait(sh, A, sh.v_tail, 0);
+                    if (!__all_sync(0xffffffffu, ok)) break;
+                    for (int x = 0; x < D / 64; ++x)
+                        for (uint32_t a = (nk - key0) * 128 + lane * 16; a < PR_BLOCK; a += 512)
+                            asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(dst + x * PR_BLOCK + a), "r"(0) : "memory");
+                    fence_async_smem();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(smem_u32(&sh.kv_full[st]));
+                }
+                issued = i + 1;
+            }
+            // After a wait that ran out: let every copy in flight land before the CTA may leave.
+            if (*(volatile int*)&sh.abort && lane == 0) {
+                mbar_wait_bounded(smem_u32(&sh.q_full), 0, A.wait_ns);
+                for (int i = max(0, issued - P::STAGES); i < issued; ++i)
+                    mbar_wait_bounded(smem_u32(&sh.kv_full[i % P::STAGES]), (i / P::STAGES) & 1, A.wait_ns);
+                if (issued < 2 * n && (issued & 1)) mbar_wait_bounded(smem_u32(&sh.v_tail), 0, A.wait_ns / 4);
+            }
+        } else if (warp == 8 && lane == 0 && n > 0) {
+            // ------------------------------------------------ matrix products
+            constexpr uint32_t ID_S = mma_desc(PR_ROWS, PR_KEYS, false), ID_O = mma_desc(PR_ROWS, D, true);
+            const uint32_t tm = sh.tmem;
+            auto full = [&](int i) { return pr_wait(sh, A, sh.kv_full[i % P::STAGES], (i / P::STAGES) & 1); };
+            auto empty = [&](int i) {      // only where a later load waits for it
+                if (i + P::STAGES < 2 * n) tc_commit(smem_u32(&sh.kv_empty[i % P::STAGES]));
+            };
+            auto scores = [&](int t, int j) {
+                const uint32_t k = ring + ((2 * j) % P::STAGES) * P::TILE, q = base + t * P::TILE;
+#pragma unroll
+                for (int e = 0; e < D / 16; ++e) {
+                    const uint32_t off = (e >> 2) * PR_BLOCK + (e & 3) * 32;
+                    mma_ss(tm + 128 * t, smem_desc(q + off, 16), smem_desc(k + off, 16), ID_S, e > 0);
+                }
+                tc_commit(smem_u32(&sh.s_full[t]));
+            };
+            auto values = [&](int t, int j) {
+                const uint32_t v = ring + ((2 * j + 1) % P::STAGES) * P::TILE;
+#pragma unroll
+                for (int e = 0; e < PR_KEYS / 16; ++e)
+                    mma_ts(tm + 256 + D * t, tm + 128 * t + 8 * e, smem_desc(v + e * 2048, PR_BLOCK), ID_O, j > 0 || e > 0);
+                tc_commit(smem_u32(&sh.o_done[t]));
+            };
+            bool ok = pr_wait(sh, A, sh.q_full, 0);
+            for (int j = 0; ok && j <= n; ++j) {
+                if (j < n) {
+                    if (!(ok = full(2 * j))) break;
+                    if (j < n_t[0]) scores(0, j);
+                }
+                if (j > 0) {
+                    if (j - 1 < n_t[1]) {
+                        if (!(ok = pr_wait(sh, A, sh.p_full[1], (j - 1) & 1))) break;
+                        tc_fence_after();
+                        values(1, j - 1);
+                    }
+                    empty(2 * j - 1);
+                }
+                if (j < n) {
+                    if (j < n_t[1]) scores(1, j);
+                    empty(2 * j);
+                    if (!(ok = full(2 * j + 1))) break;
+                    if (j < n_t[0]) {
+                        if (!(ok = pr_wait(sh, A, sh.p_full[0], j & 1))) break;
+                        tc_fence_after();
+                        values(0, j);
+                    }
+                }
+            }
+            // nothing of this CTA may be in flight when it leaves
+            tc_commit(smem_u32(&sh.drain));
+            mbar_wait_bounded(smem_u32(&sh.drain), 0, A.wait_ns);
+        }
+        __syncwarp();
+    } else {
+        regs_inc<208>();
+        const int t = warp >> 2, row = tid & 127;
+        const int tl = row / A.r, head = row - tl * A.r;
+        const int tok = tok0 + t * A.tq + tl;
+        const bool real = tl < A.tq && tok < nq;
+        int limit = 0;
+        if (real) limit = A.causal ? (int)min(max((int64_t)tok + 1 + (nk - nq), (int64_t)0), (int64_t)nk) : nk;
+        pr_softmax<D>(sh, A, t, n_t[t], limit, real, (qs + tok) * A.hq + g * A.r + head);
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (warp == 8) tmem_free(sh.tmem, 512);
+}
+
+template <int D>
+cudaError_t prompt_attn_launch(const CUtensorMap& q, const CUtensorMap& k, const CUtensorMap& v, const PromptArgs& A,
+                               unsigned ctas, cudaStream_t s) {
+    static std::atomic<uint64_t> done{0};
+    if (first_on_device(done)) {
+        const cudaError_t e =
+            cudaFuncSetAttribute(prompt_attn_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, PrShape<D>::SMEM);
+        if (e != cudaSuccess) return e;
+        mark_on_device(done);
+    }
+    prompt_attn_kernel<D><<<ctas, PR_THREADS, PrShape<D>::SMEM, s>>>(q, k, v, A);
+    return cudaGetLastError();
+}
+
+}  // namespace kvo
+
+extern "C" kvo_status kvo_prompt_attn(const void* q, int64_t q_token_stride, const void* k, int64_t k_token_stride,
+                                      const void* v, int64_t v_token_stride, const int32_t* cu_q, const int32_t* cu_k,
+                                      int batch, int64_t total_q, int64_t total_k, int n_q_heads, int n_kv_heads,
+                                      int head_dim, int causal, void* o, float* lse, int32_t* status,
+                                      kvo_stream_t stream) {
+    using namespace kvo;
+    auto bad = [](const char* m) { set_last_error(m); return KVO_ERR_INVALID; };
+    if (batch < 0 || total_q < 0 || total_k < 0 || total_q > INT32_MAX || total_k > INT32_MAX)
+        return bad("batch, total_q and total_k must be in 0..2^31 - 1");
+    if (n_kv_heads < 1 || n_q_heads < n_kv_heads || n_q_heads % n_kv_heads)
+        return bad("n_q_heads must be a multiple of n_kv_heads");
+    const int r = n_q_heads / n_kv_heads;
+    if (r > 16) return bad("n_q_heads / n_kv_heads must be <= 16");
+    if (head_dim != 64 && head_dim != 128) return bad("head_dim must be 64 or 128");
+    if (batch == 0 || total_q == 0) return KVO_OK;
+    if (!q || !o || !cu_q || !cu_k || (total_k > 0 && (!k || !v))) return bad("null pointer argument");
+    for (const void* p : {q, k, v, (const void*)o})
+        if ((uintptr_t)p % 16) return bad("q, k, v and o must be 16-byte aligned");
+    if (q_token_stride % 8 || k_token_stride % 8 || v_token_stride % 8) return bad("strides must be multiples of 8 elements");
+    if (q_token_stride < (int64_t)n_q_heads * head_dim || k_token_stride < (int64_t)n_kv_heads * head_dim ||
+        v_token_stride < (int64_t)n_kv_heads * head_dim)
+        return bad("token strides must cover the heads");
+    if (q_token_stride > (1ll << 38) || k_token_stride > (1ll << 38) || v_token_stride > (1ll << 38))
+        return bad("token strides must be below 2^38 elements");
+    PromptArgs A{};
+    A.cu_q = cu_q;
+    A.cu_k = cu_k;
+    A.o = (uint16_t*)o;
+    A.lse = lse;
+    A.status = status;
+    A.total_q = total_q;
+    A.total_k = total_k;
+    A.batch = batch;
+    A.hq = n_q_heads;
+    A.hkv = n_kv_heads;
+    A.r = r;
+    A.tq = PR_ROWS / r;
+    A.causal = causal ? 1 : 0;
+    A.scale_log2 = (float)(1.4426950408889634 / sqrt((double)head_dim));
+    A.wait_ns = 2000000000LL;
+    const int64_t units = total_q / (2 * A.tq) + batch, ctas = units * n_kv_heads;
+    if (ctas > INT32_MAX) return bad("too many tokens");
+    A.units = (int)units;
+    CUtensorMap mq, mk, mv;
+    const uint64_t sq[3] = {(uint64_t)head_dim, (uint64_t)n_q_heads, (uint64_t)total_q};
+    const uint64_t sk[3] = {(uint64_t)head_dim, (uint64_t)n_kv_heads, (uint64_t)std::max<int64_t>(total_k, 1)};
+    const uint64_t tq[2] = {(uint64_t)head_dim * 2, (uint64_t)q_token_stride * 2};
+    const uint64_t tk[2] = {(uint64_t)head_dim * 2, (uint64_t)k_token_stride * 2};
+    const uint64_t tv[2] = {(uint64_t)head_dim * 2, (uint64_t)v_token_stride * 2};
+    const uint32_t bq[3] = {64, (uint32_t)r, (uint32_t)A.tq}, bk[3] = {64, 1, PR_KEYS};
+    // without keys the maps of k and v are never used: q stands in for a null pointer
+    if (!tensor_map(&mq, q, 2, 3, sq, tq, bq) || !tensor_map(&mk, total_k ? k : q, 2, 3, sk, tk, bk) ||
+        !tensor_map(&mv, total_k ? v : q, 2, 3, sk, tv, bk)) {
+        set_last_error("cuTensorMapEncodeTiled failed for q, k or v");
+        return KVO_ERR_CUDA;
+    }
+    cudaStream_t s = (cudaStream_t)stream;
+    const cudaError_t e = head_dim == 128 ? prompt_attn_launch<128>(mq, mk, mv, A, (unsigned)ctas, s)
+                                          : prompt_attn_launch<64>(mq, mk, mv, A, (unsigned)ctas, s);
+    if (e != cudaSuccess) { set_last_error(cudaGetErrorString(e)); return KVO_ERR_CUDA; }
+    return KVO_OK;
+}

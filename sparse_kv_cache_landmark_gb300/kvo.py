@@ -28,7 +28,7 @@ EXPORTS = ["kv_offload_init", "kv_offload_destroy", "select_topk", "index_diff",
            "kvo_set_attn_impl", "kvo_set_select_impl", "kvo_resident_slots", "kvo_resident_fetched",
            "kvo_set_prefetch_budget", "kvo_set_lowrank_keys", "kvo_plan_attention", "kvo_plan_select", "kvo_set_wait_test",
            "kvo_set_spec_policy", "kvo_spec_stats", "kvo_rope", "kvo_paged_append", "kvo_paged_attn",
-           "kvo_paged_attn_workspace"]
+           "kvo_paged_attn_workspace", "kvo_prompt_attn"]
 PROFILE_KINDS = ["select", "diff", "coalesce", "gather_prefetch", "gather_urgent", "attention", "recon"]
 
 
@@ -104,6 +104,7 @@ def lib() -> ctypes.CDLL:
         L.kvo_paged_append.argtypes = [PC, VP, I64, VP, I64, I64, VP, VP, VP, I, I, F, VP, I64, I, VP, VP, VP, VP]
         L.kvo_paged_attn.argtypes = [PC, VP, I, VP, I64, VP, VP, I, VP, VP, VP, ctypes.c_size_t, VP, VP]
         L.kvo_paged_attn_workspace.argtypes = [PC, I, I, I64, ctypes.POINTER(ctypes.c_size_t)]
+        L.kvo_prompt_attn.argtypes = [VP, I64, VP, I64, VP, I64, VP, VP, I, I64, I64, I, I, I, I, VP, VP, VP, VP]
         L.kvo_last_error.argtypes = [P]
         L.kvo_last_error.restype = ctypes.c_char_p
         for name in EXPORTS:
@@ -450,6 +451,42 @@ def paged_attn(q, k_pages, v_pages, table, lens, *, k_scale=None, v_scale=None, 
         _check(L.kvo_paged_attn(c, q.data_ptr(), hq, lens.data_ptr(), max_len, _ptr(blocks), _ptr(counts), n_blocks,
                                 o.data_ptr(), lse.data_ptr(), workspace.data_ptr(), workspace.numel(), _ptr(status),
                                 _stream(stream)))
+    return o, lse
+
+
+def prompt_attn(q, k, v, cu_q, cu_k=None, causal: bool = True, o=None, lse=None, status=None, stream=None):
+    """Attention over packed prompts (C: kvo_prompt_attn) -> (o bf16 [total_q][Hq][d], lse fp32 [total_q][Hq]).
+
+    q: CUDA bf16 [total_q][Hq][d]; k, v: [total_k][Hkv][d], heads contiguous, any token stride; cu_q, cu_k:
+    int32 [batch + 1] offsets (cu_k None: cu_q).
+    """
+    dev = q.device
+    qt, _ = _rows(dev, "q", q)
+    kt, _ = _rows(dev, "k", k)
+    vt, _ = _rows(dev, "v", v)
+    T, hq, d = q.shape
+    n, hkv, _ = k.shape
+    if k.shape != (n, hkv, d) or v.shape != (n, hkv, d):
+        raise KvoError(KVO_ERR_INVALID, f"k and v must have shape {(n, hkv, d)}, got {tuple(k.shape)} and {tuple(v.shape)}")
+    cu_k = cu_q if cu_k is None else cu_k
+    _need(dev, "cu_q", cu_q, torch.int32)
+    _need(dev, "cu_k", cu_k, torch.int32, cu_q.shape)
+    if cu_q.dim() != 1 or cu_q.numel() < 1:
+        raise KvoError(KVO_ERR_INVALID, f"cu_q must be [batch + 1], got {tuple(cu_q.shape)}")
+    if o is None:
+        o = torch.empty((T, hq, d), dtype=torch.bfloat16, device=dev)
+    else:
+        _need(dev, "o", o, torch.bfloat16, (T, hq, d))
+    if lse is None:
+        lse = torch.empty((T, hq), dtype=torch.float32, device=dev)
+    else:
+        _need(dev, "lse", lse, torch.float32, (T, hq))
+    if status is not None:
+        _need(dev, "status", status, torch.int32)
+    with _on(dev):
+        _check(lib().kvo_prompt_attn(q.data_ptr(), qt, k.data_ptr(), kt, v.data_ptr(), vt, cu_q.data_ptr(),
+                                     cu_k.data_ptr(), cu_q.numel() - 1, T, n, hq, hkv, d, int(bool(causal)),
+                                     o.data_ptr(), lse.data_ptr(), _ptr(status), _stream(stream)))
     return o, lse
 
 

@@ -138,3 +138,26 @@ def test_rope_frequencies():
         assert all(math.isclose(8 * f[i], plain[i], rel_tol=1e-12) for i in slow)
         assert all(f[i] <= plain[i] * (1 + 1e-12) and 8 * f[i] >= plain[i] * (1 - 1e-12) for i in range(64))
         assert math.isclose(amp, 1.0 if kind == "banded" else 0.1 * math.log(8.0) + 1.0)
+
+
+@pytest.mark.parametrize("kw,frag", [
+    (dict(batch=-1), "batch"), (dict(tq=-1), "total_q"), (dict(hq=7), "multiple"), (dict(hkv=0), "multiple"),
+    (dict(hq=34), "<= 16"), (dict(d=96), "head_dim"), (dict(q=None), "null"), (dict(k=None), "null"),
+    (dict(cu_q=None), "null"), (dict(o=None), "null"), (dict(v=P + 8), "aligned"), (dict(qs=1028), "strides"),
+    (dict(ks=128), "cover"), (dict(qs=1 << 40), "2^38")])
+def test_prompt_attention_refuses(lib, kw, frag):
+    a = dict(q=P, qs=1024, k=P, ks=256, v=P, cu_q=P, batch=2, tq=10, hq=8, hkv=2, d=128, o=P)
+    a.update(kw)
+    refused(lib, lib.kvo_prompt_attn(a["q"], a["qs"], a["k"], a["ks"], a["v"], 256, a["cu_q"], P, a["batch"], a["tq"],
+                                     10, a["hq"], a["hkv"], a["d"], 1, a["o"], P, None, None), frag)
+
+
+def test_prompt_attention_without_tokens(lib):
+    assert lib.kvo_prompt_attn(None, 0, None, 0, None, 0, None, None, 0, 5, 5, 8, 2, 128, 1, None, None, None,
+                               None) == kvo.KVO_OK
+    assert lib.kvo_prompt_attn(None, 0, None, 0, None, 0, None, None, 3, 0, 5, 8, 2, 128, 1, None, None, None,
+                               None) == kvo.KVO_OK
+    bf = lambda *s: torch.zeros(*s, dtype=torch.bfloat16)
+    cu = torch.zeros(2, dtype=torch.int32)
+    with pytest.raises(kvo.KvoError, match="CUDA device"):
+        kvo.prompt_attn(bf(4, 2, 64), bf(4, 1, 64), bf(4, 1, 64), cu)
