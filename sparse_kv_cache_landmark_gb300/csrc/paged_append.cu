@@ -17,6 +17,7 @@
 
 #include <algorithm>
 
+#include "launch.cuh"
 #include "paged.cuh"
 #include "rope.cuh"
 
@@ -101,7 +102,7 @@ __device__ __forceinline__ void append_page(const AppendArgs& A) {
         const int w = tid + i * APP_THREADS, r = w / UNITS, un = w % UNITS;
         if (r < rows) {
             int ca, cb;
-            rope_chunks(A.R, un, ca, cb);
+            rope_chunks(A.R, D, un, ca, cb);
             const uint16_t* k = A.x[0] + (tok0 + r) * A.x_tok[0] + (int64_t)h * D;
             const uint16_t* v = A.x[1] + (tok0 + r) * A.x_tok[1] + (int64_t)h * D;
             xa[0][i] = *reinterpret_cast<const uint4*>(k + ca);
@@ -119,7 +120,7 @@ __device__ __forceinline__ void append_page(const AppendArgs& A) {
         if (rope_unit(A.R, un, (int)(pos0 + r), c, s)) rope_rotate(A.R.interleaved, c, s, xa[0][i], xb[0][i]);
         if (A.k_out) {
             int ca, cb;
-            rope_chunks(A.R, un, ca, cb);
+            rope_chunks(A.R, D, un, ca, cb);
             uint16_t* o = A.k_out + ((tok0 + r) * A.hkv + h) * D;
             *reinterpret_cast<uint4*>(o + ca) = xa[0][i];
             *reinterpret_cast<uint4*>(o + cb) = xb[0][i];
@@ -189,7 +190,7 @@ __device__ __forceinline__ void append_page(const AppendArgs& A) {
 #pragma unroll
         for (int x = 0; x < 2; ++x) {
             int ca, cb;
-            rope_chunks(A.R, un, ca, cb);
+            rope_chunks(A.R, D, un, ca, cb);
             const int64_t base = (((int64_t)p * A.hkv + h) * A.page + row0 + r) * D;
             if (!FP8) {
                 uint16_t* o = reinterpret_cast<uint16_t*>(A.pages[x]) + base;
@@ -219,6 +220,7 @@ __device__ __forceinline__ void append_page(const AppendArgs& A) {
 // Blocks [0, units * Hkv): pages.  The rest: q.
 template <int D, bool FP8, int MAXU>
 __global__ void __launch_bounds__(APP_THREADS) append_pages_kernel(const __grid_constant__ AppendArgs A) {
+    grid_wait();
     const int kv_blocks = A.units * A.hkv;
     if ((int)blockIdx.x < kv_blocks) {
         append_page<D, FP8, MAXU>(A);
@@ -244,7 +246,7 @@ __global__ void __launch_bounds__(APP_THREADS) append_pages_kernel(const __grid_
     int start;
     if (!request_range(A, b, t0, n, start) || t < t0 || t >= t0 + n) return;
     const int h0 = (int)split * A.q_per, h1 = min(A.hq, h0 + A.q_per);
-    rope_heads(A.R, A.q + t * A.q_tok, D, A.q_out + t * A.hq * D, D, u, (int)(start + (t - t0)), h0, h1);
+    rope_heads(A.R, D, A.q + t * A.q_tok, D, A.q_out + t * A.hq * D, D, u, (int)(start + (t - t0)), h0, h1);
 }
 
 int rope_heads_per_thread(int64_t n, int heads);
@@ -309,7 +311,8 @@ extern "C" kvo_status kvo_paged_append(const kvo_paged_cache* cache, const void*
     const int per_page = (cu ? cache->page_size : 1) * (D / 16);
     const int maxu = per_page <= APP_THREADS ? 1 : per_page <= 2 * APP_THREADS ? 2 : 4;
     cudaStream_t s = (cudaStream_t)stream;
-#define KVO_APPEND(D_, F_, U_) append_pages_kernel<D_, F_, U_><<<(unsigned)blocks, APP_THREADS, 0, s>>>(A)
+    cudaError_t e;
+#define KVO_APPEND(D_, F_, U_) e = launch_dependent(append_pages_kernel<D_, F_, U_>, dim3((unsigned)blocks), APP_THREADS, 0, s, 0, A)
 #define KVO_APPEND_U(D_, F_)                                                                  \
     do {                                                                                      \
         if (maxu == 1) KVO_APPEND(D_, F_, 1); else if (maxu == 2) KVO_APPEND(D_, F_, 2);      \
@@ -319,7 +322,6 @@ extern "C" kvo_status kvo_paged_append(const kvo_paged_cache* cache, const void*
     else { if (fp8) KVO_APPEND_U(64, true); else KVO_APPEND_U(64, false); }
 #undef KVO_APPEND_U
 #undef KVO_APPEND
-    const cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) { set_last_error(cudaGetErrorString(e)); return KVO_ERR_CUDA; }
     return KVO_OK;
 }

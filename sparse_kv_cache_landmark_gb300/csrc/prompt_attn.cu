@@ -28,6 +28,7 @@
 #include <algorithm>
 
 #include "kvo_internal.cuh"
+#include "launch.cuh"
 #include "paged.cuh"
 #include "tcgen05.cuh"
 #include "tensor_map.cuh"
@@ -203,6 +204,7 @@ prompt_attn_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int TU = 2 * A.tq;
 
+    grid_wait();
     if (blockIdx.x == 0 && A.status)           // bad offsets of any request, also of one that no item reaches
         for (int i = tid; i < A.batch; i += PR_THREADS) {
             const int64_t a = A.cu_q[i], e = A.cu_q[i + 1], c = A.cu_k[i], f = A.cu_k[i + 1];
@@ -381,8 +383,7 @@ cudaError_t prompt_attn_launch(const CUtensorMap& q, const CUtensorMap& k, const
         if (e != cudaSuccess) return e;
         mark_on_device(done);
     }
-    prompt_attn_kernel<D><<<ctas, PR_THREADS, PrShape<D>::SMEM, s>>>(q, k, v, A);
-    return cudaGetLastError();
+    return launch_dependent(prompt_attn_kernel<D>, dim3(ctas), PR_THREADS, PrShape<D>::SMEM, s, 0, q, k, v, A);
 }
 
 }  // namespace kvo

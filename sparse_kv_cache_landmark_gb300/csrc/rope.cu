@@ -9,6 +9,7 @@
 #include <algorithm>
 
 #include "kvo_internal.cuh"
+#include "launch.cuh"
 #include "rope.cuh"
 
 namespace kvo {
@@ -18,23 +19,24 @@ constexpr int ROPE_THREADS = 256;
 // grid.x: (token, unit) pairs; grid.y: runs of `heads_per` heads.
 __global__ void __launch_bounds__(ROPE_THREADS)
 rope_kernel(const uint16_t* x, int64_t x_tok, int64_t x_head, uint16_t* out, int64_t out_tok,
-            int64_t out_head, const int32_t* __restrict__ pos, RopeArgs R, int64_t n, int units, int heads,
+            int64_t out_head, const int32_t* __restrict__ pos, RopeArgs R, int d, int64_t n, int heads,
             int heads_per) {
+    const int units = d / 16;
     const int64_t i = (int64_t)blockIdx.x * ROPE_THREADS + threadIdx.x;
     if (i >= n) return;
     const int64_t t = i / units;
     const int u = (int)(i - t * units);
     const int h0 = blockIdx.y * heads_per, h1 = min(heads, h0 + heads_per);
-    rope_heads(R, x + t * x_tok, x_head, out + t * out_tok, out_head, u, __ldg(pos + t), h0, h1);
+    grid_wait();
+    rope_heads(R, d, x + t * x_tok, x_head, out + t * out_tok, out_head, u, __ldg(pos + t), h0, h1);
 }
 
+// Heads a thread takes: 8 sincos (about 300 instructions) are spread over them, which on long inputs hides under
+// the loads from 4 heads on; more CTAs even out the last wave, and short inputs go down to one head a thread.
 int rope_heads_per_thread(int64_t n, int heads) {
-    // The 8 sincos of a thread cost about as much as 5 heads' rotation, so a
-    // thread takes as many heads as leave about 1024 threads for each of the
-    // 152 SMs; short inputs are spread to one head a thread.
-    const int64_t want = 152 * 1024;
-    const int64_t splits = std::min<int64_t>(heads, std::max<int64_t>(1, (want + n - 1) / n));
-    return (int)((heads + splits - 1) / splits);
+    const int64_t want = 152 * 2048;
+    const int64_t splits = (want + n - 1) / n;
+    return (int)std::max<int64_t>(1, std::min<int64_t>(8, heads / std::max<int64_t>(1, splits)));
 }
 
 }  // namespace kvo
@@ -63,10 +65,9 @@ extern "C" kvo_status kvo_rope(const void* x, int64_t x_token_stride, int64_t x_
     const int per = rope_heads_per_thread(n, heads);
     const RopeArgs R{(const unsigned long long*)freq, rot_dim, interleaved ? 1 : 0, amplitude};
     const dim3 grid((unsigned)((n + ROPE_THREADS - 1) / ROPE_THREADS), (unsigned)((heads + per - 1) / per));
-    rope_kernel<<<grid, ROPE_THREADS, 0, (cudaStream_t)stream>>>((const uint16_t*)x, x_token_stride, x_head_stride,
-                                                                (uint16_t*)out, out_token_stride, out_head_stride, pos,
-                                                                R, n, units, heads, per);
-    const cudaError_t e = cudaGetLastError();
+    const cudaError_t e = launch_dependent(rope_kernel, grid, ROPE_THREADS, 0, (cudaStream_t)stream, 0, (const uint16_t*)x,
+                                           x_token_stride, x_head_stride, (uint16_t*)out, out_token_stride,
+                                           out_head_stride, pos, R, head_dim, n, heads, per);
     if (e != cudaSuccess) { set_last_error(cudaGetErrorString(e)); return KVO_ERR_CUDA; }
     return KVO_OK;
 }

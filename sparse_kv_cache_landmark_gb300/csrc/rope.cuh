@@ -14,40 +14,54 @@
 
 namespace kvo {
 
-// Pairs of a head: the first n_half units of 16 values rotate, the rest pass
-// through.  A unit is two chunks of 8 values (16 bytes): chunk a and chunk b
-// hold the two halves of 8 pairs (interleaved == 0), or 4 pairs each.
+// A head is cut into units of 16 values, two chunks of 8 (16 bytes) half a part
+// apart: unit u < rot_dim / 16 takes chunks 8 u and rot_dim / 2 + 8 u of the rotated
+// part, the units after it the same of the rest.  Neighbouring lanes then touch
+// neighbouring chunks in both pair layouts.
 struct RopeArgs {
     const unsigned long long* freq;   // [rot_dim / 2]; NULL: nothing rotates
-    int rot_dim;                      // a multiple of 16, <= head_dim
+    int rot_dim;                      // a multiple of 16, <= head_dim (0 without freq)
     int interleaved;                  // 0: pairs (i, i + rot_dim / 2); 1: pairs (2i, 2i + 1)
     float amp;                        // factor on the rotated values
 };
 
 __device__ __forceinline__ void rope_sincos(int pos, unsigned long long f, float amp, float& c, float& s) {
     const unsigned long long ph = (unsigned long long)(long long)pos * f;
-    const float half_turns = (float)(int)(ph >> 32) * 4.656612873077393e-10f;    // 2^-31
-    sincospif(half_turns, &s, &c);
+    // The nearest quarter turn is taken off as an integer, so the rest, at most an eighth of a turn, loses no more
+    // than 2^-27 half turns as a float; then the angle is turned back by q quarters.
+    const uint32_t top = (uint32_t)(ph >> 32);
+    const uint32_t q = (top + 0x20000000u) >> 30;
+    const float half_turns = (float)(int)(top - (q << 30)) * 4.656612873077393e-10f;    // 2^-31
+    float s0, c0;
+    sincospif(half_turns, &s0, &c0);
+    const float sq = (q & 1) ? c0 : s0, cq = (q & 1) ? s0 : c0;
+    s = (q & 2) ? -sq : sq;
+    c = ((q + 1) & 2) ? -cq : cq;
     c *= amp;
     s *= amp;
 }
 
-// First value of the two chunks of unit u (16 values) of a head.
-__device__ __forceinline__ void rope_chunks(const RopeArgs& R, int u, int& a, int& b) {
-    if (R.freq && !R.interleaved && 16 * u < R.rot_dim) {
+// First value of the two chunks of unit u of a head of d values.
+__device__ __forceinline__ void rope_chunks(const RopeArgs& R, int d, int u, int& a, int& b) {
+    const int n = R.rot_dim / 16;
+    if (u < n) {
         a = 8 * u;
         b = a + R.rot_dim / 2;
     } else {
-        a = 16 * u;
-        b = a + 8;
+        a = R.rot_dim + 8 * (u - n);
+        b = a + (d - R.rot_dim) / 2;
     }
 }
 
 // cos and sin of the 8 pairs of unit u; returns false for a unit that passes through.
 __device__ __forceinline__ bool rope_unit(const RopeArgs& R, int u, int pos, float (&c)[8], float (&s)[8]) {
-    if (!R.freq || 16 * u >= R.rot_dim) return false;
+    if (16 * u >= R.rot_dim) return false;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) rope_sincos(pos, __ldg(R.freq + 8 * u + i), R.amp, c[i], s[i]);
+    for (int i = 0; i < 8; ++i) {
+        // pairs 8u.. of the halves; interleaved: pairs 4u.. in chunk a, 4u.. of the second half of them in chunk b
+        const int pair = !R.interleaved ? 8 * u + i : i < 4 ? 4 * u + i : R.rot_dim / 4 + 4 * u + i - 4;
+        rope_sincos(pos, __ldg(R.freq + pair), R.amp, c[i], s[i]);
+    }
     return true;
 }
 
@@ -78,12 +92,12 @@ __device__ __forceinline__ void rope_rotate(bool interleaved, const float (&c)[8
 // One thread's part of rotating packed heads: unit u of one token, heads h0, h0 + 1, .. h1 - 1.
 // x and out point at the token.  In place (out == x with equal strides) is allowed: each
 // unit is read whole before it is written, by the thread that owns it.
-__device__ __forceinline__ void rope_heads(const RopeArgs& R, const uint16_t* x, int64_t x_head, uint16_t* out,
-                                           int64_t out_head, int u, int pos, int h0, int h1) {
+__device__ __forceinline__ void rope_heads(const RopeArgs& R, int d, const uint16_t* x, int64_t x_head,
+                                           uint16_t* out, int64_t out_head, int u, int pos, int h0, int h1) {
     float c[8], s[8];
     const bool rot = rope_unit(R, u, pos, c, s);
     int ca, cb;
-    rope_chunks(R, u, ca, cb);
+    rope_chunks(R, d, u, ca, cb);
     constexpr int IN_FLIGHT = 4;
     for (int h = h0; h < h1; h += IN_FLIGHT) {
         uint4 a[IN_FLIGHT], b[IN_FLIGHT];

@@ -73,15 +73,4 @@ __device__ __forceinline__ bool mbar_wait_bounded(uint32_t mbar, uint32_t parity
     return true;
 }
 
-// Host: true once per device for each `done` mask (function attributes are set per device).
-inline bool first_on_device(std::atomic<uint64_t>& done) {
-    int dev = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev > 63) return true;
-    return !(done.load(std::memory_order_relaxed) >> dev & 1);
-}
-inline void mark_on_device(std::atomic<uint64_t>& done) {
-    int dev = 0;
-    if (cudaGetDevice(&dev) == cudaSuccess && dev >= 0 && dev <= 63) done.fetch_or(1ull << dev, std::memory_order_relaxed);
-}
-
 }  // namespace kvo

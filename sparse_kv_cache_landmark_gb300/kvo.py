@@ -236,47 +236,58 @@ def sparse_decode_attn_static(q, k_buf, v_buf, slot_of_true, k_win, v_win, *, ba
     return o, lse
 
 
-def _need(dev, name, t, dtype, shape=None, contiguous=True):
-    """Check one buffer of a context-free call; raises ``KvoError`` before anything is launched."""
+def _need(dev, name, t, dtype, shape=None):
+    """Check one contiguous buffer of a context-free call; returns its address, or raises ``KvoError``."""
+    if t is not None and t.dtype is dtype and t.device == dev and t.is_contiguous() and (shape is None or t.shape == shape):
+        return t.data_ptr()
     if t is None:
         raise KvoError(KVO_ERR_INVALID, f"{name} is required")
     if t.dtype != dtype:
         raise KvoError(KVO_ERR_INVALID, f"{name} must be {dtype}, got {t.dtype}")
     if shape is not None and t.shape != shape:
         raise KvoError(KVO_ERR_INVALID, f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
-    if contiguous and not t.is_contiguous():
+    if not t.is_contiguous():
         raise KvoError(KVO_ERR_INVALID, f"{name} must be contiguous")
-    if t.device != dev or dev.type != "cuda":
-        raise KvoError(KVO_ERR_INVALID, f"all buffers must be on one CUDA device, {name} is on {t.device}")
-    return t
+    raise KvoError(KVO_ERR_INVALID, f"all buffers must be on one CUDA device: {name} is on {t.device}, not {dev}")
 
 
-def _rows(dev, name, t, heads_contiguous=True):
-    """Check a bf16 [tokens][heads][d] buffer with free token (and head) strides; returns its strides."""
-    _need(dev, name, t, torch.bfloat16, contiguous=False)
+def _rows(dev, name, t, free_heads=False):
+    """Check a bf16 [tokens][heads][d] buffer with a free token stride (and head stride); returns both."""
+    if t.dtype != torch.bfloat16:
+        raise KvoError(KVO_ERR_INVALID, f"{name} must be torch.bfloat16, got {t.dtype}")
     if t.dim() != 3:
-        raise KvoError(KVO_ERR_INVALID, f"{name} must be [tokens][heads][head_dim]")
+        raise KvoError(KVO_ERR_INVALID, f"{name} must be [tokens][heads][head_dim], got {tuple(t.shape)}")
+    if t.device != dev:
+        raise KvoError(KVO_ERR_INVALID, f"all buffers must be on one CUDA device: {name} is on {t.device}, not {dev}")
+    T, H, d = t.shape
     st, sh, sd = t.stride()
-    if t.shape[2] > 1 and sd != 1 or heads_contiguous and t.shape[1] > 1 and sh != t.shape[2]:
-        raise KvoError(KVO_ERR_INVALID, f"{name}: the last dimension{'s' if heads_contiguous else ''} must be contiguous")
-    # a dimension of one has no stride of its own
-    return (st if t.shape[0] > 1 else t.shape[1] * t.shape[2]), (sh if t.shape[1] > 1 else t.shape[2])
+    if H <= 1:                    # a dimension of one has no stride of its own
+        sh = d
+    if T <= 1:
+        st = max(H * sh, d)
+    if (sd != 1 and d > 1) or (sh != d and not free_heads):
+        raise KvoError(KVO_ERR_INVALID, f"{name}: heads must be contiguous" if sd == 1 else f"{name}: the last dimension must be contiguous")
+    return st, sh
 
 
-class _on:
-    """Make ``device`` current around a library call (nothing when it is already)."""
+def _cuda(dev, stream) -> int:
+    """Stream handle for a context-free call on ``dev`` (default: torch's current stream of that device)."""
+    if dev.type != "cuda":
+        raise KvoError(KVO_ERR_INVALID, f"all buffers must be on one CUDA device, got {dev}")
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(dev.index) or CUDA_STREAM_LEGACY
+    return (stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)) or CUDA_STREAM_LEGACY
 
-    def __init__(self, device):
-        self.want = device.index
 
-    def __enter__(self):
-        self.had = torch.cuda.current_device()
-        if self.want is not None and self.want != self.had:
-            torch.cuda.set_device(self.want)
-
-    def __exit__(self, *exc):
-        if self.want is not None and self.want != self.had:
-            torch.cuda.set_device(self.had)
+def _launch(dev, fn, *args):
+    """Call a library function with ``dev`` current; raises ``KvoError`` unless it returns KVO_OK."""
+    if dev.index == torch.cuda.current_device():
+        st = fn(*args)
+    else:
+        with torch.cuda.device(dev):
+            st = fn(*args)
+    if st != KVO_OK:
+        _check(st)
 
 
 def rope_frequencies(rot_dim: int, base: float = 10000.0, scaling: Optional[str] = None, factor: float = 1.0,
@@ -323,18 +334,17 @@ def rope(x, pos, freq, interleaved: bool = False, amplitude: float = 1.0, out=No
     """Rotary positions (C: kvo_rope).  x: CUDA bf16 [tokens][heads][d], last dimension contiguous, any token and
     head stride; pos: int32 [tokens]; freq: ``rope_frequencies``.  ``out=x`` rotates in place."""
     dev = x.device
-    st, sh = _rows(dev, "x", x, heads_contiguous=False)
+    st, sh = _rows(dev, "x", x, True)
     T, H, d = x.shape
-    _need(dev, "pos", pos, torch.int32, (T,))
-    _need(dev, "freq", freq, torch.int64)
+    pp, pf = _need(dev, "pos", pos, torch.int32, (T,)), _need(dev, "freq", freq, torch.int64)
     if out is None:
-        out = torch.empty((T, H, d), dtype=torch.bfloat16, device=dev)
-    elif out.shape != x.shape:
-        raise KvoError(KVO_ERR_INVALID, f"out must have shape {tuple(x.shape)}, got {tuple(out.shape)}")
-    ot, oh = _rows(dev, "out", out, heads_contiguous=False)
-    with _on(dev):
-        _check(lib().kvo_rope(x.data_ptr(), st, sh, out.data_ptr(), ot, oh, pos.data_ptr(), freq.data_ptr(), T, H, d,
-                              2 * freq.numel(), int(bool(interleaved)), amplitude, _stream(stream)))
+        out, ot, oh = x.new_empty((T, H, d)), H * d, d
+    else:
+        if out.shape != x.shape:
+            raise KvoError(KVO_ERR_INVALID, f"out must have shape {tuple(x.shape)}, got {tuple(out.shape)}")
+        ot, oh = _rows(dev, "out", out, True)
+    _launch(dev, lib().kvo_rope, x.data_ptr(), st, sh, out.data_ptr(), ot, oh, pp, pf, T, H, d, 2 * freq.numel(),
+            1 if interleaved else 0, amplitude, _cuda(dev, stream))
     return out
 
 
@@ -343,18 +353,17 @@ def _paged(k_pages, v_pages, k_scale, v_scale, table) -> _PagedCache:
     if k_pages is None or k_pages.dim() != 4 or table is None or table.dim() != 2:
         raise KvoError(KVO_ERR_INVALID, "pages must be [n_pages][n_kv_heads][page_size][head_dim], table [batch][max_pages]")
     dev, dt = k_pages.device, k_pages.dtype
-    if dt not in (torch.bfloat16, torch.float8_e4m3fn):
-        raise KvoError(KVO_ERR_INVALID, f"pages must be bfloat16 or float8_e4m3fn, got {dt}")
-    _need(dev, "k_pages", k_pages, dt)
-    _need(dev, "v_pages", v_pages, dt, k_pages.shape)
-    _need(dev, "table", table, torch.int32)
     n, h, p, d = k_pages.shape
-    ks = vs = None
-    if dt == torch.float8_e4m3fn:
-        ks = _need(dev, "k_scale", k_scale, torch.float32, (n, h)).data_ptr()
-        vs = _need(dev, "v_scale", v_scale, torch.float32, (n, h)).data_ptr()
-    return _PagedCache(k_pages.data_ptr(), v_pages.data_ptr(), ks, vs, table.data_ptr(), table.shape[0], h, d, p, n,
-                       table.shape[1], 0 if ks is None else 1)
+    if dt is torch.bfloat16:
+        ks = vs = None
+    elif dt is torch.float8_e4m3fn:
+        ks = _need(dev, "k_scale", k_scale, torch.float32, (n, h))
+        vs = _need(dev, "v_scale", v_scale, torch.float32, (n, h))
+    else:
+        raise KvoError(KVO_ERR_INVALID, f"pages must be bfloat16 or float8_e4m3fn, got {dt}")
+    return _PagedCache(_need(dev, "k_pages", k_pages, dt), _need(dev, "v_pages", v_pages, dt, k_pages.shape), ks, vs,
+                       _need(dev, "table", table, torch.int32), table.shape[0], h, d, p, n, table.shape[1],
+                       0 if ks is None else 1)
 
 
 def paged_append(k, v, k_pages, v_pages, table, start, *, cu=None, k_scale=None, v_scale=None, freq=None,
@@ -367,38 +376,30 @@ def paged_append(k, v, k_pages, v_pages, table, start, *, cu=None, k_scale=None,
     [batch], the tokens each request has already; cu: int32 [batch + 1] token offsets (None: one token
     each).  Returns q_out, the rotated q (None without q).
     """
-    c = _paged(k_pages, v_pages, k_scale, v_scale, table)
     dev = k_pages.device
-    kt, _ = _rows(dev, "k", k)
-    vt, _ = _rows(dev, "v", v)
+    c = _paged(k_pages, v_pages, k_scale, v_scale, table)
+    batch, hkv, d = table.shape[0], k_pages.shape[1], k_pages.shape[3]
+    kt, vt = _rows(dev, "k", k)[0], _rows(dev, "v", v)[0]
     T = k.shape[0]
-    shape = (T, c.n_kv_heads, c.head_dim)
+    shape = (T, hkv, d)
     if k.shape != shape or v.shape != shape:
         raise KvoError(KVO_ERR_INVALID, f"k and v must have shape {shape}, got {tuple(k.shape)} and {tuple(v.shape)}")
-    _need(dev, "start", start, torch.int32, (c.batch,))
-    if cu is not None:
-        _need(dev, "cu", cu, torch.int32, (c.batch + 1,))
-    if freq is not None:
-        _need(dev, "freq", freq, torch.int64)
-    if k_out is not None:
-        _need(dev, "k_out", k_out, torch.bfloat16, shape)
-    if status is not None:
-        _need(dev, "status", status, torch.int32)
+    ps = _need(dev, "start", start, torch.int32, (batch,))
+    pc = None if cu is None else _need(dev, "cu", cu, torch.int32, (batch + 1,))
+    pf = None if freq is None else _need(dev, "freq", freq, torch.int64)
+    pk = None if k_out is None else _need(dev, "k_out", k_out, torch.bfloat16, shape)
+    pst = None if status is None else _need(dev, "status", status, torch.int32)
+    pq = pqo = None
     qt = hq = 0
     if q is not None:
-        qt, _ = _rows(dev, "q", q)
-        hq = q.shape[1]
-        if q.shape != (T, hq, c.head_dim):
-            raise KvoError(KVO_ERR_INVALID, f"q must have shape {(T, hq, c.head_dim)}, got {tuple(q.shape)}")
+        qt, hq = _rows(dev, "q", q)[0], q.shape[1]
+        if q.shape != (T, hq, d):
+            raise KvoError(KVO_ERR_INVALID, f"q must have shape {(T, hq, d)}, got {tuple(q.shape)}")
         if q_out is None:
-            q_out = torch.empty((T, hq, c.head_dim), dtype=torch.bfloat16, device=dev)
-        else:
-            _need(dev, "q_out", q_out, torch.bfloat16, (T, hq, c.head_dim))
-    with _on(dev):
-        _check(lib().kvo_paged_append(c, k.data_ptr(), kt, v.data_ptr(), vt, T, _ptr(cu), start.data_ptr(),
-                                      _ptr(freq), 0 if freq is None else 2 * freq.numel(), int(bool(interleaved)),
-                                      amplitude, _ptr(q), qt, hq, _ptr(q_out) if q is not None else None, _ptr(k_out),
-                                      _ptr(status), _stream(stream)))
+            q_out = q.new_empty((T, hq, d))
+        pq, pqo = q.data_ptr(), _need(dev, "q_out", q_out, torch.bfloat16, (T, hq, d))
+    _launch(dev, lib().kvo_paged_append, c, k.data_ptr(), kt, v.data_ptr(), vt, T, pc, ps, pf,
+            0 if freq is None else 2 * freq.numel(), 1 if interleaved else 0, amplitude, pq, qt, hq, pqo, pk, pst, _cuda(dev, stream))
     return q_out if q is not None else None
 
 
@@ -411,46 +412,41 @@ def paged_attn(q, k_pages, v_pages, table, lens, *, k_scale=None, v_scale=None, 
     counts: int32 [batch][Hkv].  The workspace comes from torch's allocator when none is given; it must
     then stay on the stream that is current (give one for another ``stream``).
     """
-    c = _paged(k_pages, v_pages, k_scale, v_scale, table)
     dev = k_pages.device
+    c = _paged(k_pages, v_pages, k_scale, v_scale, table)
+    batch, hkv, d = table.shape[0], k_pages.shape[1], k_pages.shape[3]
     if q.dim() != 3:
-        raise KvoError(KVO_ERR_INVALID, "q must be [batch][n_q_heads][head_dim]")
+        raise KvoError(KVO_ERR_INVALID, f"q must be [batch][n_q_heads][head_dim], got {tuple(q.shape)}")
     hq = q.shape[1]
-    _need(dev, "q", q, torch.bfloat16, (c.batch, hq, c.head_dim))
-    _need(dev, "lens", lens, torch.int32, (c.batch,))
+    rows = (batch, hq, d)
+    pq, pl = _need(dev, "q", q, torch.bfloat16, rows), _need(dev, "lens", lens, torch.int32, (batch,))
+    pb = pc = None
     n_blocks = 0
     if blocks is not None:
         n_blocks = blocks.shape[-1]
-        if blocks.numel() != c.batch * c.n_kv_heads * n_blocks or n_blocks == 0:
+        if n_blocks == 0 or blocks.numel() != batch * hkv * n_blocks:
             raise KvoError(KVO_ERR_INVALID, f"blocks must be [batch][n_kv_heads][n], got {tuple(blocks.shape)}")
-        _need(dev, "blocks", blocks, torch.int32)
+        pb = _need(dev, "blocks", blocks, torch.int32)
     if counts is not None:
         if blocks is None:
             raise KvoError(KVO_ERR_INVALID, "counts needs blocks")
-        _need(dev, "counts", counts, torch.int32)
-        if counts.numel() != c.batch * c.n_kv_heads:
+        if counts.numel() != batch * hkv:
             raise KvoError(KVO_ERR_INVALID, f"counts must be [batch][n_kv_heads], got {tuple(counts.shape)}")
-    if status is not None:
-        _need(dev, "status", status, torch.int32)
+        pc = _need(dev, "counts", counts, torch.int32)
+    pst = None if status is None else _need(dev, "status", status, torch.int32)
     if o is None:
-        o = torch.empty((c.batch, hq, c.head_dim), dtype=torch.bfloat16, device=dev)
-    else:
-        _need(dev, "o", o, torch.bfloat16, (c.batch, hq, c.head_dim))
+        o = torch.empty_like(q)
+    po = _need(dev, "o", o, torch.bfloat16, rows)
     if lse is None:
-        lse = torch.empty((c.batch, hq), dtype=torch.float32, device=dev)
-    else:
-        _need(dev, "lse", lse, torch.float32, (c.batch, hq))
+        lse = q.new_empty((batch, hq), dtype=torch.float32)
+    pls = _need(dev, "lse", lse, torch.float32, (batch, hq))
     L = lib()
-    n = ctypes.c_size_t(0)
-    _check(L.kvo_paged_attn_workspace(c, hq, n_blocks, max_len, ctypes.byref(n)))
     if workspace is None:
-        workspace = torch.empty(n.value, dtype=torch.uint8, device=dev)
-    else:
-        _need(dev, "workspace", workspace, torch.uint8)
-    with _on(dev):
-        _check(L.kvo_paged_attn(c, q.data_ptr(), hq, lens.data_ptr(), max_len, _ptr(blocks), _ptr(counts), n_blocks,
-                                o.data_ptr(), lse.data_ptr(), workspace.data_ptr(), workspace.numel(), _ptr(status),
-                                _stream(stream)))
+        n = ctypes.c_size_t(0)
+        _check(L.kvo_paged_attn_workspace(c, hq, n_blocks, max_len, n))
+        workspace = q.new_empty(n.value, dtype=torch.uint8)
+    _launch(dev, L.kvo_paged_attn, c, pq, hq, pl, max_len, pb, pc, n_blocks, po, pls,
+            _need(dev, "workspace", workspace, torch.uint8), workspace.numel(), pst, _cuda(dev, stream))
     return o, lse
 
 
@@ -461,32 +457,23 @@ def prompt_attn(q, k, v, cu_q, cu_k=None, causal: bool = True, o=None, lse=None,
     int32 [batch + 1] offsets (cu_k None: cu_q).
     """
     dev = q.device
-    qt, _ = _rows(dev, "q", q)
-    kt, _ = _rows(dev, "k", k)
-    vt, _ = _rows(dev, "v", v)
+    qt, kt, vt = _rows(dev, "q", q)[0], _rows(dev, "k", k)[0], _rows(dev, "v", v)[0]
     T, hq, d = q.shape
-    n, hkv, _ = k.shape
+    n, hkv = k.shape[0], k.shape[1]
     if k.shape != (n, hkv, d) or v.shape != (n, hkv, d):
         raise KvoError(KVO_ERR_INVALID, f"k and v must have shape {(n, hkv, d)}, got {tuple(k.shape)} and {tuple(v.shape)}")
-    cu_k = cu_q if cu_k is None else cu_k
-    _need(dev, "cu_q", cu_q, torch.int32)
-    _need(dev, "cu_k", cu_k, torch.int32, cu_q.shape)
     if cu_q.dim() != 1 or cu_q.numel() < 1:
         raise KvoError(KVO_ERR_INVALID, f"cu_q must be [batch + 1], got {tuple(cu_q.shape)}")
+    pcq = _need(dev, "cu_q", cu_q, torch.int32)
+    pck = pcq if cu_k is None else _need(dev, "cu_k", cu_k, torch.int32, cu_q.shape)
+    pst = None if status is None else _need(dev, "status", status, torch.int32)
     if o is None:
-        o = torch.empty((T, hq, d), dtype=torch.bfloat16, device=dev)
-    else:
-        _need(dev, "o", o, torch.bfloat16, (T, hq, d))
+        o = q.new_empty((T, hq, d))
     if lse is None:
-        lse = torch.empty((T, hq), dtype=torch.float32, device=dev)
-    else:
-        _need(dev, "lse", lse, torch.float32, (T, hq))
-    if status is not None:
-        _need(dev, "status", status, torch.int32)
-    with _on(dev):
-        _check(lib().kvo_prompt_attn(q.data_ptr(), qt, k.data_ptr(), kt, v.data_ptr(), vt, cu_q.data_ptr(),
-                                     cu_k.data_ptr(), cu_q.numel() - 1, T, n, hq, hkv, d, int(bool(causal)),
-                                     o.data_ptr(), lse.data_ptr(), _ptr(status), _stream(stream)))
+        lse = q.new_empty((T, hq), dtype=torch.float32)
+    _launch(dev, lib().kvo_prompt_attn, q.data_ptr(), qt, k.data_ptr(), kt, v.data_ptr(), vt, pcq, pck,
+            cu_q.numel() - 1, T, n, hq, hkv, d, 1 if causal else 0, _need(dev, "o", o, torch.bfloat16, (T, hq, d)),
+            _need(dev, "lse", lse, torch.float32, (T, hq)), pst, _cuda(dev, stream))
     return o, lse
 
 
