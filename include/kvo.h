@@ -573,8 +573,8 @@ kvo_status kvo_paged_append(const kvo_paged_cache* cache, const void* k, int64_t
  *   o is rounded once to bf16, as the projection that follows takes it: the
  *   weights are rounded to 11 bits (8 with bf16 pages) on the tensor cores, so
  *   fp32 would carry no more.  Two calls give the same bits.
- *   workspace: kvo_paged_attn_workspace bytes, 256-byte aligned, contents
- *   undefined before and after; one call at a time may use it (two captured
+ *   workspace: kvo_paged_attn_workspace bytes (0 for small calls: NULL will do),
+ *   256-byte aligned, contents undefined before and after; one call at a time may use it (two captured
  *   graphs that may overlap need one each).
  *   Status bits: KVO_DEV_BAD_BLOCK_ID (a page or block id out of range: adds
  *   nothing), KVO_DEV_BAD_COUNT (a length or count out of range: clamped),
@@ -586,7 +586,7 @@ kvo_status kvo_paged_attn(const kvo_paged_cache* cache, const void* q, int n_q_h
                           float* lse, void* workspace, size_t workspace_bytes, int32_t* status, kvo_stream_t stream);
 
 /* kvo_paged_attn_workspace -- bytes kvo_paged_attn needs for these arguments
- * (n_blocks 0: no block list).  Host only; reads the descriptor's sizes. */
+ * (n_blocks 0: no block list; with one, counts or not).  Host only; reads the descriptor's sizes. */
 kvo_status kvo_paged_attn_workspace(const kvo_paged_cache* cache, int n_q_heads, int n_blocks, int64_t max_len,
                                     size_t* bytes_out);
 

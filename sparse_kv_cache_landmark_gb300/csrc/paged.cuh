@@ -65,7 +65,7 @@ inline const char* paged_cache_error(const kvo_paged_cache* c) {
     if (c->page_size != 16 && c->page_size != 32 && c->page_size != 64 && c->page_size != 128)
         return "page_size must be 16, 32, 64 or 128";
     if (c->n_pages < 1 || c->max_pages < 1) return "need n_pages >= 1 and max_pages >= 1";
-    if ((int64_t)c->max_pages * c->page_size > INT32_MAX) return "max_pages * page_size must fit in 31 bits";
+    if ((int64_t)c->max_pages * c->page_size >= (1 << 30)) return "max_pages * page_size must fit in 30 bits";
     if ((int64_t)c->n_pages * c->n_kv_heads * c->page_size > INT32_MAX)
         return "n_pages * n_kv_heads * page_size must fit in 31 bits";
     if ((int64_t)c->batch * c->n_kv_heads > (1 << 20)) return "batch * n_kv_heads must be <= 2^20";

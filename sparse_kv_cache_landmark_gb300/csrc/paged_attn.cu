@@ -47,8 +47,8 @@ namespace kvo {
 constexpr int PA_WARPS = 4;
 constexpr int PA_THREADS = PA_WARPS * 32;
 constexpr int PA_SUB = 16;                    // tokens of a subtile (one k step of the value product, and of a TMA box)
-constexpr int PA_RING = 64 * 1024;            // bytes of stages per CTA
-constexpr int PA_PER_SM = 3;                  // CTAs per SM: 64 KB of stages and 168 registers a thread each
+constexpr int PA_RING = 96 * 1024;            // bytes of stages per CTA
+constexpr int PA_PER_SM = 2;                  // CTAs per SM: 96 KB of stages each
 constexpr float PA_RAISE = 8.f;               // log2: how far a score may pass the running maximum
 constexpr float PA_BIAS = 6.f;                // log2: weights are held times 2^6 (f16's small end is 2^-24)
 
@@ -80,7 +80,7 @@ struct PagedAttnArgs {
     float4* part_ml;              // [2 ctas][r]: maximum, sum, sum of the rounded weights
     int2* info;                   // [G]: first and last CTA of a group cut by range borders; x < 0: not cut
     int32_t* status;
-    int batch, hkv, r, page, n_pages, max_pages, n_blocks, G;
+    int batch, hkv, r, page, shift, n_pages, max_pages, n_blocks, G;
     float scale_log2;
     long long wait_ns;
 };
@@ -106,16 +106,6 @@ __device__ __forceinline__ float ex2(float x) {
     float y;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
-}
-__device__ __forceinline__ uint4 lds128(uint32_t a) {
-    uint4 v;
-    asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a));
-    return v;
-}
-__device__ __forceinline__ uint2 lds64(uint32_t a) {
-    uint2 v;
-    asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(a));
-    return v;
 }
 template <bool FP8>
 __device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
@@ -158,7 +148,7 @@ struct PaState {
 // Scores and values of one tile; nv[s] of subtile s's 16 tokens are real (all: nv_all).
 template <int D, bool FP8, int NH>
 __device__ __forceinline__ void pa_tile(PaState<D, FP8, NH>& T, const uint32_t (&qf)[PaShape<D, FP8>::STEPS][NH][2],
-                                        const float (&qs)[NH][2], uint32_t ksm, uint32_t vsm,
+                                        const float (&qs)[NH][2], const uint8_t* ksm, const uint8_t* vsm,
                                         const float (&kscale)[PaShape<D, FP8>::SUBS],
                                         const float (&vscale)[PaShape<D, FP8>::SUBS],
                                         const int (&nv)[PaShape<D, FP8>::SUBS], bool all) {
@@ -180,10 +170,10 @@ __device__ __forceinline__ void pa_tile(PaState<D, FP8, NH>& T, const uint32_t (
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
                 const int row = 16 * u + 8 * i + g;
-                uint32_t a;
+                const uint8_t* a;
                 if (S::BOX == 128) a = ksm + (m >> 1) * BOXROWS + row * 128 + (((2 * c + (m & 1)) ^ (row & 7)) << 4);
                 else a = ksm + row * 64 + ((c ^ ((row >> 1) & 3)) << 4);
-                const uint4 v = lds128(a);
+                const uint4 v = *reinterpret_cast<const uint4*>(a);
                 w[i][0] = v.x; w[i][1] = v.y; w[i][2] = v.z; w[i][3] = v.w;
             }
             constexpr int PER = FP8 ? 4 : 2;                 // k steps of a chunk
@@ -290,10 +280,10 @@ __device__ __forceinline__ void pa_tile(PaState<D, FP8, NH>& T, const uint32_t (
             for (int k = 0; k < 4; ++k) {
                 const int tr = 16 * u + 2 * c + (k & 1) + 8 * (k >> 1);
                 if (S::BOX == 128) {
-                    const uint4 v = lds128(vsm + b * BOXROWS + tr * 128 + ((g ^ (tr & 7)) << 4));
+                    const uint4 v = *reinterpret_cast<const uint4*>(vsm + b * BOXROWS + tr * 128 + ((g ^ (tr & 7)) << 4));
                     w[k][0] = v.x; w[k][1] = v.y; w[k][VW - 2] = v.z; w[k][VW - 1] = v.w;
                 } else {
-                    const uint2 v = lds64(vsm + tr * 64 + ((((g >> 1) ^ ((tr >> 1) & 3)) << 4) | ((g & 1) << 3)));
+                    const uint2 v = *reinterpret_cast<const uint2*>(vsm + tr * 64 + ((((g >> 1) ^ ((tr >> 1) & 3)) << 4) | ((g & 1) << 3)));
                     w[k][0] = v.x; w[k][1] = v.y;
                 }
                 if (!all && tr - 16 * u >= nv[u])            // what lies behind the end may be NaN: 0 * NaN must not reach o
@@ -398,6 +388,7 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_consta
     float* cl = reinterpret_cast<float*>(ring_p + 48 * 1024);
     constexpr int MS = D + 4;
     const uint32_t wring = ring + warp * S::STAGES * S::STAGE;
+    const uint8_t* wring_p = ring_p + warp * S::STAGES * S::STAGE;
     const uint32_t wbar = smem_u32(bars) + warp * S::STAGES * 8;
     if (lane == 0)
         for (int i = 0; i < S::STAGES; ++i) mbar_init(wbar + 8 * i, 1);
@@ -476,30 +467,33 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_consta
         if (!CLU && cur >= gpre + n) { gpre += n; ++g; continue; }
         const int t0 = (int)(cur - gpre), t1 = CLU ? (int)hi : (int)min((long long)n, hi - gpre);
         const int len = pa_len(A, g / A.hkv);
-        const int n_logical = (pa_span(A, g) + A.page - 1) / A.page;
+        const int n_logical = (pa_span(A, g) + A.page - 1) >> A.shift;
         // this warp's tiles
         const int w0 = t0 + (int)((long long)(t1 - t0) * warp / PA_WARPS);
         const int w1 = t0 + (int)((long long)(t1 - t0) * (warp + 1) / PA_WARPS);
 
         // tiles w0..w1: pages come in batches of 32, one per lane; the next batch is loaded while this one is used
-        int base = (int)((long long)w0 * S::TILE / A.page);
+        int base = (w0 * S::TILE) >> A.shift;
         PaPage cur_p = pa_page(A, g, base + lane, len, n_logical), nxt_p = pa_page(A, g, base + 32 + lane, len, n_logical);
         int issued = w0;
-        // first row in the pool of the subtile at token t of the span, and its real tokens (issue side: up to a batch ahead)
+        // first row in the pool of the subtile at token t of the span, and its real tokens (up to a batch ahead)
         auto find = [&](int t, int& row, int& tok) {
-            const int pg = t / A.page, k = pg - base;
-            const int r0 = __shfl_sync(0xffffffffu, cur_p.row, k & 31), r1 = __shfl_sync(0xffffffffu, nxt_p.row, k & 31);
-            const int n0 = __shfl_sync(0xffffffffu, cur_p.tokens, k & 31), n1 = __shfl_sync(0xffffffffu, nxt_p.tokens, k & 31);
-            const int off = t - pg * A.page;
-            row = (k < 32 ? r0 : r1) + off;
-            tok = (k < 32 ? n0 : n1) - off;
+            const int pg = t >> A.shift, k = pg - base, off = t - (pg << A.shift);
+            row = __shfl_sync(0xffffffffu, k < 32 ? cur_p.row : nxt_p.row, k & 31) + off;
+            tok = __shfl_sync(0xffffffffu, k < 32 ? cur_p.tokens : nxt_p.tokens, k & 31) - off;
         };
+        const bool wide = A.page >= S::TILE;                 // a tile lies within one page
+        int st_in = 0, st_out = 0; // stages of the next tile to issue and to use
         auto issue = [&](int t) {  // copies of tile t into its stage: each subtile that has tokens
-            const int st = (t - w0) % S::STAGES;
-            const uint32_t bar = wbar + 8 * st, dst = wring + st * S::STAGE;
+            const uint32_t bar = wbar + 8 * st_in, dst = wring + st_in * S::STAGE;
+            if (++st_in == S::STAGES) st_in = 0;
             int row[S::SUBS], tok[S::SUBS];
-#pragma unroll
-            for (int u = 0; u < S::SUBS; ++u) find(t * S::TILE + u * PA_SUB, row[u], tok[u]);
+            find(t * S::TILE, row[0], tok[0]);
+            if (S::SUBS > 1) {
+                row[S::SUBS - 1] = row[0] + PA_SUB;
+                tok[S::SUBS - 1] = tok[0] - PA_SUB;
+                if (!wide) find(t * S::TILE + PA_SUB, row[S::SUBS - 1], tok[S::SUBS - 1]);
+            }
             if (lane == 0) {
                 int n_sub = 0;
 #pragma unroll
@@ -576,31 +570,38 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_consta
 
         // Every copy issued is waited for, also after a wait that ran out: none may land once the CTA has left.
         for (int t = w0; t < issued; ++t) {
-            if (t * S::TILE / A.page - base >= 32) {
+            const int pg = (t * S::TILE) >> A.shift;
+            if (pg - base >= 32) {
                 base += 32;
                 cur_p = nxt_p;
                 nxt_p = pa_page(A, g, base + 32 + lane, len, n_logical);
             }
             float ks[S::SUBS], vs[S::SUBS];
             int nv[S::SUBS];
-            bool some = false, all = true;
-#pragma unroll
-            for (int u = 0; u < S::SUBS; ++u) {
-                const int at = t * S::TILE + u * PA_SUB, pg = at / A.page, k = pg - base;
-                // the second subtile may open the next batch (pages of 16 tokens)
-                const bool next = k >= 32;
-                nv[u] = min(PA_SUB, __shfl_sync(0xffffffffu, next ? nxt_p.tokens : cur_p.tokens, k & 31) - (at - pg * A.page));
-                ks[u] = __shfl_sync(0xffffffffu, next ? nxt_p.ks : cur_p.ks, k & 31);
-                vs[u] = __shfl_sync(0xffffffffu, next ? nxt_p.vs : cur_p.vs, k & 31);
-                some |= nv[u] > 0;
-                all &= nv[u] == PA_SUB;
+            const int k = pg - base, off = t * S::TILE - (pg << A.shift);
+            const int tok = __shfl_sync(0xffffffffu, cur_p.tokens, k) - off;
+            nv[0] = min(PA_SUB, tok);
+            ks[0] = __shfl_sync(0xffffffffu, cur_p.ks, k);
+            vs[0] = __shfl_sync(0xffffffffu, cur_p.vs, k);
+            if (S::SUBS > 1) {
+                constexpr int U = S::SUBS - 1;
+                nv[U] = min(PA_SUB, tok - PA_SUB);
+                ks[U] = ks[0];
+                vs[U] = vs[0];
+                if (!wide) {       // pages of 16 tokens: the next page, of the same batch (tiles start at even pages)
+                    nv[U] = __shfl_sync(0xffffffffu, cur_p.tokens, (k + 1) & 31);
+                    ks[U] = __shfl_sync(0xffffffffu, cur_p.ks, (k + 1) & 31);
+                    vs[U] = __shfl_sync(0xffffffffu, cur_p.vs, (k + 1) & 31);
+                }
             }
-            const int st = (t - w0) % S::STAGES;
+            const bool some = nv[0] > 0 || nv[S::SUBS - 1] > 0, all = nv[0] == PA_SUB && nv[S::SUBS - 1] == PA_SUB;
+            const int st = st_out;
+            if (++st_out == S::STAGES) st_out = 0;
             if (some) {
                 if (!mbar_wait_bounded(wbar + 8 * st, (phase >> st) & 1, A.wait_ns)) dead = true;
                 phase ^= 1u << st;
                 if (!dead)
-                    pa_tile<D, FP8, NH>(T, qf, qs, wring + st * S::STAGE, wring + st * S::STAGE + S::TILE_BYTES, ks, vs, nv, all);
+                    pa_tile<D, FP8, NH>(T, qf, qs, wring_p + st * S::STAGE, wring_p + st * S::STAGE + S::TILE_BYTES, ks, vs, nv, all);
             }
             dead = __any_sync(0xffffffffu, dead);
             if (issued < w1 && !dead) issue(issued++);
@@ -717,60 +718,62 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_consta
     }
 }
 
-// Joins the parts of groups cut by range borders: grid (G, r), one thread per value column.
+// Joins the parts of groups cut by range borders: grid (G, r); thread (slice, value column), the slices take every
+// PA_JOIN-th part and are added in order.
+constexpr int PA_JOIN = 4;
 template <int D>
-__global__ void __launch_bounds__(D) paged_join_kernel(const __grid_constant__ PagedAttnArgs A) {
-    constexpr int BATCH = 64;                                 // parts whose factors are shared at a time
-    __shared__ float s_f[BATCH];
-    __shared__ float s_red[D / 32];
-    const int g = blockIdx.x, row = blockIdx.y, col = threadIdx.x;
+__global__ void __launch_bounds__(D * PA_JOIN) paged_join_kernel(const __grid_constant__ PagedAttnArgs A) {
+    __shared__ float s_red[D * PA_JOIN / 32];
+    __shared__ float s_acc[PA_JOIN][D + 2];
+    const int g = blockIdx.x, row = blockIdx.y, col = threadIdx.x % D, slice = threadIdx.x / D;
     grid_wait();
     const int2 info = A.info[g];
     if (info.x < 0) return;
     const int n = info.y - info.x / 2 + 1;                    // parts: the first CTA's slot, then slot 0 of each CTA after it
     auto part = [&](int i) { return (i == 0 ? (int64_t)info.x : 2 * ((int64_t)(info.x / 2) + i)) * A.r + row; };
     float m = -INFINITY;
-    for (int i = col; i < n; i += D) m = fmaxf(m, A.part_ml[part(i)].x);
+    for (int i = threadIdx.x; i < n; i += D * PA_JOIN) m = fmaxf(m, A.part_ml[part(i)].x);
 #pragma unroll
     for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-    if ((col & 31) == 0) s_red[col >> 5] = m;
+    if ((threadIdx.x & 31) == 0) s_red[threadIdx.x >> 5] = m;
     __syncthreads();
-    for (int i = 0; i < D / 32; ++i) m = fmaxf(m, s_red[i]);
+    for (int i = 0; i < D * PA_JOIN / 32; ++i) m = fmaxf(m, s_red[i]);
     float acc = 0.f, l = 0.f, lw = 0.f;
-    for (int i0 = 0; i0 < n; i0 += BATCH) {
-        const int k = min(BATCH, n - i0);
-        if (col < BATCH && col < k) {
-            const float4 ml = A.part_ml[part(i0 + col)];
-            s_f[col] = ml.y == 0.f ? 0.f : ex2(ml.x - m);
-        }
-        __syncthreads();
 #pragma unroll 8
-        for (int i = 0; i < k; ++i) {
-            const float f = s_f[i];
-            const int64_t at = part(i0 + i);
-            const float4 ml = A.part_ml[at];
-            const float o = A.part_o[at * D + col];
-            // an empty part adds nothing, whatever its maximum
-            if (ml.y != 0.f) { l += f * ml.y; lw += f * ml.z; acc += f * o; }
-        }
-        __syncthreads();
+    for (int i = slice; i < n; i += PA_JOIN) {
+        const int64_t at = part(i);
+        const float4 ml = A.part_ml[at];
+        const float o = A.part_o[at * D + col];
+        const float f = ex2(ml.x - m);
+        // an empty part adds nothing, whatever its maximum
+        if (ml.y != 0.f) { l += f * ml.y; lw += f * ml.z; acc += f * o; }
     }
+    s_acc[slice][col] = acc;
+    if (col == 0) { s_acc[slice][D] = l; s_acc[slice][D + 1] = lw; }
+    __syncthreads();
+    if (slice) return;
+    for (int k = 1; k < PA_JOIN; ++k) acc += s_acc[k][col];
+    l = lw = 0.f;
+    for (int k = 0; k < PA_JOIN; ++k) { l += s_acc[k][D]; lw += s_acc[k][D + 1]; }
     pa_store(A, (int64_t)g * A.r + row, D, col, acc, m, l, lw);
 }
 
-// How a call is cut.  `cluster` > 0: that many CTAs per group in a cluster, one launch: where that leaves at most
-// 1024 tokens a CTA (at least 128) and the groups' clusters fit the device at once, or one CTA a group does, i.e.
-// where latency counts.  0: ranges over
-// `ctas` CTAs, enough to fill the device, at least 8 subtiles each at the lengths the caller bounds.
+// How a call is cut.
+// cluster > 0: that many CTAs per group in a cluster and no second launch.  Taken where a CTA then has at most 2048
+// tokens, i.e. where latency counts (1 x 4096 bf16: 6.6 us against 10.9 in two launches), and for lists of blocks,
+// whose groups all have the same work (8 x 72 blocks of 64, e4m3: 20.6 us against 26.6).
+// cluster 0: equal ranges over `ctas` CTAs, enough to fill the device, at least 8 subtiles each at the lengths the
+// caller bounds.  Taken for long contexts, whose lengths the host does not know: where they differ by two a cluster
+// per group waits for the longest (16 x 64K-128K e4m3: 455 us against 555).
 struct PaPlan {
     int cluster, ctas;
 };
 constexpr int PA_SLOTS = PA_PER_SM * 152;
-PaPlan paged_attn_plan(int64_t groups, int64_t max_tokens) {
+PaPlan paged_attn_plan(int64_t groups, int64_t max_tokens, bool equal) {
     const int64_t want = std::max<int64_t>(1, (max_tokens + 127) / 128);
     const int64_t fit = std::min<int64_t>(16, PA_SLOTS / groups);
     const int64_t s = std::max<int64_t>(1, std::min(want, fit));
-    if (max_tokens <= 1024 * s) return {(int)s, (int)(s * groups)};
+    if (max_tokens <= 2048 * s || (equal && s * groups >= PA_SLOTS / 2)) return {(int)s, (int)(s * groups)};
     const int64_t subs = groups * ((max_tokens + PA_SUB - 1) / PA_SUB);
     return {0, (int)std::min<int64_t>(PA_SLOTS, std::max<int64_t>(1, (subs + 7) / 8))};
 }
@@ -778,7 +781,7 @@ PaPlan paged_attn_plan(int64_t groups, int64_t max_tokens) {
 size_t round256(size_t x) { return (x + 255) / 256 * 256; }
 
 size_t paged_attn_workspace(const PaPlan& plan, int G, int r, int d) {
-    if (plan.cluster) return 256;
+    if (plan.cluster) return 0;
     const int ctas = plan.ctas;
     return round256((size_t)G * sizeof(int2)) + round256((size_t)2 * ctas * r * sizeof(float4)) +
            (size_t)2 * ctas * r * d * sizeof(float);
@@ -800,7 +803,7 @@ const char* paged_attn_error(const kvo_paged_cache* c, int n_q_heads, int n_bloc
     if (n_q_heads < c->n_kv_heads || n_q_heads % c->n_kv_heads) return "n_q_heads must be a multiple of n_kv_heads";
     if (n_q_heads / c->n_kv_heads > 16) return "n_q_heads / n_kv_heads must be <= 16";
     if (max_len < 0) return "max_len must be >= 0";
-    if (n_blocks < 0 || (int64_t)n_blocks * c->page_size > INT32_MAX) return "n_blocks * page_size must fit in 31 bits";
+    if (n_blocks < 0 || (int64_t)n_blocks * c->page_size >= (1 << 30)) return "n_blocks * page_size must fit in 30 bits";
     return nullptr;
 }
 
@@ -824,7 +827,7 @@ cudaError_t paged_attn_launch(const CUtensorMap& mk, const CUtensorMap& mv, cons
         return launch_dependent(paged_attn_kernel<D, FP8, NH, true>, plan.ctas, PA_THREADS, smem, s, plan.cluster, mk, mv, A);
     e = launch_dependent(paged_attn_kernel<D, FP8, NH, false>, plan.ctas, PA_THREADS, smem, s, 0, mk, mv, A);
     if (e != cudaSuccess) return e;
-    return launch_dependent(paged_join_kernel<D>, dim3(A.G, A.r), D, 0, s, 0, A);
+    return launch_dependent(paged_join_kernel<D>, dim3(A.G, A.r), D * PA_JOIN, 0, s, 0, A);
 }
 
 }  // namespace
@@ -837,7 +840,7 @@ extern "C" kvo_status kvo_paged_attn_workspace(const kvo_paged_cache* cache, int
     *bytes_out = 0;
     if (const char* m = paged_attn_error(cache, n_q_heads, n_blocks, max_len)) return bad(m);
     const int G = cache->batch * cache->n_kv_heads;
-    *bytes_out = paged_attn_workspace(paged_attn_plan(std::max(G, 1), paged_attn_bound(cache, n_blocks, max_len)), G,
+    *bytes_out = paged_attn_workspace(paged_attn_plan(std::max(G, 1), paged_attn_bound(cache, n_blocks, max_len), n_blocks > 0), G,
                                       n_q_heads / cache->n_kv_heads, cache->head_dim);
     return KVO_OK;
 }
@@ -850,14 +853,15 @@ extern "C" kvo_status kvo_paged_attn(const kvo_paged_cache* cache, const void* q
     auto bad = [](const char* m) { set_last_error(m); return KVO_ERR_INVALID; };
     if (const char* m = paged_attn_error(cache, n_q_heads, blocks ? n_blocks : 0, max_len)) return bad(m);
     if (cache->batch == 0) return KVO_OK;
-    if (!q || !lens || !o || !lse || !workspace) return bad("null pointer argument");
+    if (!q || !lens || !o || !lse) return bad("null pointer argument");
     if (blocks && n_blocks < 1) return bad("blocks needs n_blocks >= 1");
     if (counts && !blocks) return bad("counts needs blocks");
     if ((uintptr_t)q % 16 || (uintptr_t)o % 16 || (uintptr_t)workspace % 256)
         return bad("q and o must be 16-byte aligned, the workspace 256-byte aligned");
     const int G = cache->batch * cache->n_kv_heads, r = n_q_heads / cache->n_kv_heads, D = cache->head_dim;
-    const PaPlan plan = paged_attn_plan(G, paged_attn_bound(cache, blocks ? n_blocks : 0, max_len));
-    if (workspace_bytes < paged_attn_workspace(plan, G, r, D)) return bad("the workspace is too small (kvo_paged_attn_workspace)");
+    const PaPlan plan = paged_attn_plan(G, paged_attn_bound(cache, blocks ? n_blocks : 0, max_len), blocks != nullptr);
+    const size_t need = paged_attn_workspace(plan, G, r, D);
+    if (need && (!workspace || workspace_bytes < need)) return bad("the workspace is too small (kvo_paged_attn_workspace)");
     const bool fp8 = cache->format == KVO_PAGES_E4M3;
     const int rb = fp8 ? D : 2 * D;
     CUtensorMap mk, mv;
@@ -886,6 +890,7 @@ extern "C" kvo_status kvo_paged_attn(const kvo_paged_cache* cache, const void* q
     A.hkv = cache->n_kv_heads;
     A.r = r;
     A.page = cache->page_size;
+    A.shift = cache->page_size == 16 ? 4 : cache->page_size == 32 ? 5 : cache->page_size == 64 ? 6 : 7;
     A.n_pages = cache->n_pages;
     A.max_pages = cache->max_pages;
     A.n_blocks = n_blocks;

@@ -8,6 +8,7 @@ library or a CUDA device every call fails.
 from __future__ import annotations
 
 import ctypes
+import functools
 import math
 import os
 from typing import List, Optional, Sequence
@@ -236,9 +237,14 @@ def sparse_decode_attn_static(q, k_buf, v_buf, slot_of_true, k_win, v_win, *, ba
     return o, lse
 
 
+# The checks of the context-free calls below are written to cost little where nothing is wrong: decode loops make
+# these calls once per layer and token.
+_BF16, _I32, _I64, _F32, _E4M3 = torch.bfloat16, torch.int32, torch.int64, torch.float32, torch.float8_e4m3fn
+
+
 def _need(dev, name, t, dtype, shape=None):
-    """Check one contiguous buffer of a context-free call; returns its address, or raises ``KvoError``."""
-    if t is not None and t.dtype is dtype and t.device == dev and t.is_contiguous() and (shape is None or t.shape == shape):
+    """Address of one contiguous buffer on CUDA device ``dev`` (ordinal), or a ``KvoError`` that says what is wrong."""
+    if t is not None and t.dtype is dtype and t.get_device() == dev and t.is_contiguous() and (shape is None or t.shape == shape):
         return t.data_ptr()
     if t is None:
         raise KvoError(KVO_ERR_INVALID, f"{name} is required")
@@ -248,17 +254,17 @@ def _need(dev, name, t, dtype, shape=None):
         raise KvoError(KVO_ERR_INVALID, f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
     if not t.is_contiguous():
         raise KvoError(KVO_ERR_INVALID, f"{name} must be contiguous")
-    raise KvoError(KVO_ERR_INVALID, f"all buffers must be on one CUDA device: {name} is on {t.device}, not {dev}")
+    raise KvoError(KVO_ERR_INVALID, f"all buffers must be on one CUDA device: {name} is on {t.device}")
 
 
 def _rows(dev, name, t, free_heads=False):
-    """Check a bf16 [tokens][heads][d] buffer with a free token stride (and head stride); returns both."""
-    if t.dtype != torch.bfloat16:
-        raise KvoError(KVO_ERR_INVALID, f"{name} must be torch.bfloat16, got {t.dtype}")
-    if t.dim() != 3:
-        raise KvoError(KVO_ERR_INVALID, f"{name} must be [tokens][heads][head_dim], got {tuple(t.shape)}")
-    if t.device != dev:
-        raise KvoError(KVO_ERR_INVALID, f"all buffers must be on one CUDA device: {name} is on {t.device}, not {dev}")
+    """Strides (token, head) of a bf16 [tokens][heads][d] buffer whose token stride (and head stride) is free."""
+    if t.dtype is not _BF16 or t.dim() != 3 or t.get_device() != dev:
+        if t.dtype is not _BF16:
+            raise KvoError(KVO_ERR_INVALID, f"{name} must be torch.bfloat16, got {t.dtype}")
+        if t.dim() != 3:
+            raise KvoError(KVO_ERR_INVALID, f"{name} must be [tokens][heads][head_dim], got {tuple(t.shape)}")
+        raise KvoError(KVO_ERR_INVALID, f"all buffers must be on one CUDA device: {name} is on {t.device}")
     T, H, d = t.shape
     st, sh, sd = t.stride()
     if H <= 1:                    # a dimension of one has no stride of its own
@@ -270,23 +276,20 @@ def _rows(dev, name, t, free_heads=False):
     return st, sh
 
 
-def _cuda(dev, stream) -> int:
-    """Stream handle for a context-free call on ``dev`` (default: torch's current stream of that device)."""
-    if dev.type != "cuda":
-        raise KvoError(KVO_ERR_INVALID, f"all buffers must be on one CUDA device, got {dev}")
+def _launch(dev, stream, fn, *args):
+    """Call a library function with ``dev`` current on ``stream`` (default: torch's current stream of that device)."""
+    if dev < 0:
+        raise KvoError(KVO_ERR_INVALID, "all buffers must be on one CUDA device, got cpu")
     if stream is None:
-        return torch._C._cuda_getCurrentRawStream(dev.index) or CUDA_STREAM_LEGACY
-    return (stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)) or CUDA_STREAM_LEGACY
-
-
-def _launch(dev, fn, *args):
-    """Call a library function with ``dev`` current; raises ``KvoError`` unless it returns KVO_OK."""
-    if dev.index == torch.cuda.current_device():
-        st = fn(*args)
+        h = torch._C._cuda_getCurrentRawStream(dev) or CUDA_STREAM_LEGACY
+    else:
+        h = (stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)) or CUDA_STREAM_LEGACY
+    if dev == torch._C._cuda_getDevice():
+        st = fn(*args, h)
     else:
         with torch.cuda.device(dev):
-            st = fn(*args)
-    if st != KVO_OK:
+            st = fn(*args, h)
+    if st:
         _check(st)
 
 
@@ -333,37 +336,37 @@ def rope_frequencies(rot_dim: int, base: float = 10000.0, scaling: Optional[str]
 def rope(x, pos, freq, interleaved: bool = False, amplitude: float = 1.0, out=None, stream=None):
     """Rotary positions (C: kvo_rope).  x: CUDA bf16 [tokens][heads][d], last dimension contiguous, any token and
     head stride; pos: int32 [tokens]; freq: ``rope_frequencies``.  ``out=x`` rotates in place."""
-    dev = x.device
+    dev = x.get_device()
     st, sh = _rows(dev, "x", x, True)
     T, H, d = x.shape
-    pp, pf = _need(dev, "pos", pos, torch.int32, (T,)), _need(dev, "freq", freq, torch.int64)
+    pp, pf = _need(dev, "pos", pos, _I32, (T,)), _need(dev, "freq", freq, _I64)
     if out is None:
         out, ot, oh = x.new_empty((T, H, d)), H * d, d
     else:
         if out.shape != x.shape:
             raise KvoError(KVO_ERR_INVALID, f"out must have shape {tuple(x.shape)}, got {tuple(out.shape)}")
         ot, oh = _rows(dev, "out", out, True)
-    _launch(dev, lib().kvo_rope, x.data_ptr(), st, sh, out.data_ptr(), ot, oh, pp, pf, T, H, d, 2 * freq.numel(),
-            1 if interleaved else 0, amplitude, _cuda(dev, stream))
+    _launch(dev, stream, lib().kvo_rope, x.data_ptr(), st, sh, out.data_ptr(), ot, oh, pp, pf, T, H, d,
+            2 * freq.numel(), 1 if interleaved else 0, amplitude)
     return out
 
 
-def _paged(k_pages, v_pages, k_scale, v_scale, table) -> _PagedCache:
-    """Checked descriptor of a paged cache ([n_pages][Hkv][page_size][d] pools, int32 [batch][max_pages] table)."""
-    if k_pages is None or k_pages.dim() != 4 or table is None or table.dim() != 2:
+def _paged(dev, k_pages, v_pages, k_scale, v_scale, table):
+    """Checked descriptor of a paged cache ([n_pages][Hkv][page_size][d] pools, int32 [batch][max_pages] table), and
+    (batch, Hkv, d)."""
+    if k_pages.dim() != 4 or table is None or table.dim() != 2:
         raise KvoError(KVO_ERR_INVALID, "pages must be [n_pages][n_kv_heads][page_size][head_dim], table [batch][max_pages]")
-    dev, dt = k_pages.device, k_pages.dtype
-    n, h, p, d = k_pages.shape
-    if dt is torch.bfloat16:
+    dt, shape, ts = k_pages.dtype, k_pages.shape, table.shape
+    n, h, p, d = shape
+    if dt is _BF16:
         ks = vs = None
-    elif dt is torch.float8_e4m3fn:
-        ks = _need(dev, "k_scale", k_scale, torch.float32, (n, h))
-        vs = _need(dev, "v_scale", v_scale, torch.float32, (n, h))
+    elif dt is _E4M3:
+        ks = _need(dev, "k_scale", k_scale, _F32, (n, h))
+        vs = _need(dev, "v_scale", v_scale, _F32, (n, h))
     else:
         raise KvoError(KVO_ERR_INVALID, f"pages must be bfloat16 or float8_e4m3fn, got {dt}")
-    return _PagedCache(_need(dev, "k_pages", k_pages, dt), _need(dev, "v_pages", v_pages, dt, k_pages.shape), ks, vs,
-                       _need(dev, "table", table, torch.int32), table.shape[0], h, d, p, n, table.shape[1],
-                       0 if ks is None else 1)
+    return _PagedCache(_need(dev, "k_pages", k_pages, dt), _need(dev, "v_pages", v_pages, dt, shape), ks, vs,
+                       _need(dev, "table", table, _I32), ts[0], h, d, p, n, ts[1], 0 if ks is None else 1), ts[0], h, d
 
 
 def paged_append(k, v, k_pages, v_pages, table, start, *, cu=None, k_scale=None, v_scale=None, freq=None,
@@ -376,19 +379,18 @@ def paged_append(k, v, k_pages, v_pages, table, start, *, cu=None, k_scale=None,
     [batch], the tokens each request has already; cu: int32 [batch + 1] token offsets (None: one token
     each).  Returns q_out, the rotated q (None without q).
     """
-    dev = k_pages.device
-    c = _paged(k_pages, v_pages, k_scale, v_scale, table)
-    batch, hkv, d = table.shape[0], k_pages.shape[1], k_pages.shape[3]
+    dev = k_pages.get_device()
+    c, batch, hkv, d = _paged(dev, k_pages, v_pages, k_scale, v_scale, table)
     kt, vt = _rows(dev, "k", k)[0], _rows(dev, "v", v)[0]
     T = k.shape[0]
     shape = (T, hkv, d)
     if k.shape != shape or v.shape != shape:
         raise KvoError(KVO_ERR_INVALID, f"k and v must have shape {shape}, got {tuple(k.shape)} and {tuple(v.shape)}")
-    ps = _need(dev, "start", start, torch.int32, (batch,))
-    pc = None if cu is None else _need(dev, "cu", cu, torch.int32, (batch + 1,))
-    pf = None if freq is None else _need(dev, "freq", freq, torch.int64)
-    pk = None if k_out is None else _need(dev, "k_out", k_out, torch.bfloat16, shape)
-    pst = None if status is None else _need(dev, "status", status, torch.int32)
+    ps = _need(dev, "start", start, _I32, (batch,))
+    pc = None if cu is None else _need(dev, "cu", cu, _I32, (batch + 1,))
+    pf, rot = (None, 0) if freq is None else (_need(dev, "freq", freq, _I64), 2 * freq.numel())
+    pk = None if k_out is None else _need(dev, "k_out", k_out, _BF16, shape)
+    pst = None if status is None else _need(dev, "status", status, _I32)
     pq = pqo = None
     qt = hq = 0
     if q is not None:
@@ -397,10 +399,23 @@ def paged_append(k, v, k_pages, v_pages, table, start, *, cu=None, k_scale=None,
             raise KvoError(KVO_ERR_INVALID, f"q must have shape {(T, hq, d)}, got {tuple(q.shape)}")
         if q_out is None:
             q_out = q.new_empty((T, hq, d))
-        pq, pqo = q.data_ptr(), _need(dev, "q_out", q_out, torch.bfloat16, (T, hq, d))
-    _launch(dev, lib().kvo_paged_append, c, k.data_ptr(), kt, v.data_ptr(), vt, T, pc, ps, pf,
-            0 if freq is None else 2 * freq.numel(), 1 if interleaved else 0, amplitude, pq, qt, hq, pqo, pk, pst, _cuda(dev, stream))
+            pqo = q_out.data_ptr()
+        else:
+            pqo = _need(dev, "q_out", q_out, _BF16, (T, hq, d))
+        pq = q.data_ptr()
+    _launch(dev, stream, lib().kvo_paged_append, c, k.data_ptr(), kt, v.data_ptr(), vt, T, pc, ps, pf, rot,
+            1 if interleaved else 0, amplitude, pq, qt, hq, pqo, pk, pst)
     return q_out if q is not None else None
+
+
+@functools.lru_cache(maxsize=4096)
+def _paged_attn_workspace(batch, hkv, d, page, n_pages, max_pages, fmt, hq, n_blocks, max_len) -> int:
+    """kvo_paged_attn_workspace's bytes: a function of the sizes alone (any non-null pointers will do)."""
+    n = ctypes.c_size_t(0)
+    p = 4096
+    c = _PagedCache(p, p, p, p, p, batch, hkv, d, page, n_pages, max_pages, fmt)
+    _check(lib().kvo_paged_attn_workspace(c, hq, n_blocks, max_len, ctypes.byref(n)))
+    return n.value
 
 
 def paged_attn(q, k_pages, v_pages, table, lens, *, k_scale=None, v_scale=None, blocks=None, counts=None,
@@ -412,41 +427,45 @@ def paged_attn(q, k_pages, v_pages, table, lens, *, k_scale=None, v_scale=None, 
     counts: int32 [batch][Hkv].  The workspace comes from torch's allocator when none is given; it must
     then stay on the stream that is current (give one for another ``stream``).
     """
-    dev = k_pages.device
-    c = _paged(k_pages, v_pages, k_scale, v_scale, table)
-    batch, hkv, d = table.shape[0], k_pages.shape[1], k_pages.shape[3]
+    dev = k_pages.get_device()
+    c, batch, hkv, d = _paged(dev, k_pages, v_pages, k_scale, v_scale, table)
     if q.dim() != 3:
         raise KvoError(KVO_ERR_INVALID, f"q must be [batch][n_q_heads][head_dim], got {tuple(q.shape)}")
     hq = q.shape[1]
     rows = (batch, hq, d)
-    pq, pl = _need(dev, "q", q, torch.bfloat16, rows), _need(dev, "lens", lens, torch.int32, (batch,))
+    pq, pl = _need(dev, "q", q, _BF16, rows), _need(dev, "lens", lens, _I32, (batch,))
     pb = pc = None
     n_blocks = 0
     if blocks is not None:
         n_blocks = blocks.shape[-1]
         if n_blocks == 0 or blocks.numel() != batch * hkv * n_blocks:
             raise KvoError(KVO_ERR_INVALID, f"blocks must be [batch][n_kv_heads][n], got {tuple(blocks.shape)}")
-        pb = _need(dev, "blocks", blocks, torch.int32)
+        pb = _need(dev, "blocks", blocks, _I32)
     if counts is not None:
         if blocks is None:
             raise KvoError(KVO_ERR_INVALID, "counts needs blocks")
         if counts.numel() != batch * hkv:
             raise KvoError(KVO_ERR_INVALID, f"counts must be [batch][n_kv_heads], got {tuple(counts.shape)}")
-        pc = _need(dev, "counts", counts, torch.int32)
-    pst = None if status is None else _need(dev, "status", status, torch.int32)
+        pc = _need(dev, "counts", counts, _I32)
+    pst = None if status is None else _need(dev, "status", status, _I32)
     if o is None:
         o = torch.empty_like(q)
-    po = _need(dev, "o", o, torch.bfloat16, rows)
+        po = o.data_ptr()
+    else:
+        po = _need(dev, "o", o, _BF16, rows)
     if lse is None:
-        lse = q.new_empty((batch, hq), dtype=torch.float32)
-    pls = _need(dev, "lse", lse, torch.float32, (batch, hq))
-    L = lib()
+        lse = q.new_empty((batch, hq), dtype=_F32)
+        pls = lse.data_ptr()
+    else:
+        pls = _need(dev, "lse", lse, _F32, (batch, hq))
     if workspace is None:
-        n = ctypes.c_size_t(0)
-        _check(L.kvo_paged_attn_workspace(c, hq, n_blocks, max_len, n))
-        workspace = q.new_empty(n.value, dtype=torch.uint8)
-    _launch(dev, L.kvo_paged_attn, c, pq, hq, pl, max_len, pb, pc, n_blocks, po, pls,
-            _need(dev, "workspace", workspace, torch.uint8), workspace.numel(), pst, _cuda(dev, stream))
+        size = _paged_attn_workspace(batch, hkv, d, c.page_size, c.n_pages, c.max_pages, c.format, hq, n_blocks, max_len)
+        if size:
+            workspace = q.new_empty(size, dtype=torch.uint8)
+        pw = workspace.data_ptr() if size else None
+    else:
+        pw, size = _need(dev, "workspace", workspace, torch.uint8), workspace.numel()
+    _launch(dev, stream, lib().kvo_paged_attn, c, pq, hq, pl, max_len, pb, pc, n_blocks, po, pls, pw, size, pst)
     return o, lse
 
 
@@ -456,24 +475,29 @@ def prompt_attn(q, k, v, cu_q, cu_k=None, causal: bool = True, o=None, lse=None,
     q: CUDA bf16 [total_q][Hq][d]; k, v: [total_k][Hkv][d], heads contiguous, any token stride; cu_q, cu_k:
     int32 [batch + 1] offsets (cu_k None: cu_q).
     """
-    dev = q.device
+    dev = q.get_device()
     qt, kt, vt = _rows(dev, "q", q)[0], _rows(dev, "k", k)[0], _rows(dev, "v", v)[0]
     T, hq, d = q.shape
-    n, hkv = k.shape[0], k.shape[1]
-    if k.shape != (n, hkv, d) or v.shape != (n, hkv, d):
+    n, hkv, dk = k.shape
+    if dk != d or v.shape != k.shape:
         raise KvoError(KVO_ERR_INVALID, f"k and v must have shape {(n, hkv, d)}, got {tuple(k.shape)} and {tuple(v.shape)}")
     if cu_q.dim() != 1 or cu_q.numel() < 1:
         raise KvoError(KVO_ERR_INVALID, f"cu_q must be [batch + 1], got {tuple(cu_q.shape)}")
-    pcq = _need(dev, "cu_q", cu_q, torch.int32)
-    pck = pcq if cu_k is None else _need(dev, "cu_k", cu_k, torch.int32, cu_q.shape)
-    pst = None if status is None else _need(dev, "status", status, torch.int32)
+    pcq = _need(dev, "cu_q", cu_q, _I32)
+    pck = pcq if cu_k is None else _need(dev, "cu_k", cu_k, _I32, cu_q.shape)
+    pst = None if status is None else _need(dev, "status", status, _I32)
     if o is None:
         o = q.new_empty((T, hq, d))
+        po = o.data_ptr()
+    else:
+        po = _need(dev, "o", o, _BF16, (T, hq, d))
     if lse is None:
-        lse = q.new_empty((T, hq), dtype=torch.float32)
-    _launch(dev, lib().kvo_prompt_attn, q.data_ptr(), qt, k.data_ptr(), kt, v.data_ptr(), vt, pcq, pck,
-            cu_q.numel() - 1, T, n, hq, hkv, d, 1 if causal else 0, _need(dev, "o", o, torch.bfloat16, (T, hq, d)),
-            _need(dev, "lse", lse, torch.float32, (T, hq)), pst, _cuda(dev, stream))
+        lse = q.new_empty((T, hq), dtype=_F32)
+        pl = lse.data_ptr()
+    else:
+        pl = _need(dev, "lse", lse, _F32, (T, hq))
+    _launch(dev, stream, lib().kvo_prompt_attn, q.data_ptr(), qt, k.data_ptr(), kt, v.data_ptr(), vt, pcq, pck,
+            cu_q.numel() - 1, T, n, hq, hkv, d, 1 if causal else 0, po, pl, pst)
     return o, lse
 
 

@@ -52,7 +52,7 @@ def cache(**kw):
 BAD_CACHES = [(dict(batch=-1), "batch"), (dict(hkv=0), "n_kv_heads"), (dict(d=96), "head_dim"), (dict(page=48), "page_size"),
               (dict(n_pages=0), "n_pages"), (dict(max_pages=0), "max_pages"), (dict(fmt=2), "format"),
               (dict(k=None), "null"), (dict(table=None), "null"), (dict(v=P + 4), "aligned"), (dict(ks=None), "k_scale"),
-              (dict(max_pages=2 ** 27), "31 bits"), (dict(n_pages=2 ** 27), "31 bits")]
+              (dict(max_pages=2 ** 27), "30 bits"), (dict(n_pages=2 ** 27), "31 bits")]
 
 
 @pytest.mark.parametrize("kw,frag", BAD_CACHES)
@@ -80,23 +80,24 @@ def test_append_refuses(lib, kw, frag):
 
 @pytest.mark.parametrize("kw,frag", [
     (dict(hq=7), "multiple"), (dict(hq=34), "<= 16"), (dict(q=None), "null"), (dict(lens=None), "null"),
-    (dict(o=None), "null"), (dict(ws=None), "null"), (dict(max_len=-1), "max_len"), (dict(blocks=P, n=0), "n_blocks"),
-    (dict(counts=P), "counts"), (dict(q=P + 2), "aligned"), (dict(ws=P + 16), "aligned"), (dict(size=64), "too small"),
-    (dict(blocks=P, n=2 ** 28), "31 bits")])
+    (dict(o=None), "null"), (dict(ws=None, mp=8192), "too small"), (dict(max_len=-1), "max_len"),
+    (dict(blocks=P, n=0), "n_blocks"), (dict(counts=P), "counts"), (dict(q=P + 2), "aligned"),
+    (dict(ws=P + 16), "aligned"), (dict(size=64, mp=8192), "too small"),
+    (dict(blocks=P, n=2 ** 28), "30 bits")])
 def test_attention_refuses(lib, kw, frag):
-    a = dict(q=P, hq=8, lens=P, max_len=0, blocks=None, counts=None, n=0, o=P, ws=P, size=1 << 30)
+    a = dict(q=P, hq=8, lens=P, max_len=0, blocks=None, counts=None, n=0, o=P, ws=P, size=1 << 30, mp=4)
     a.update(kw)
-    refused(lib, lib.kvo_paged_attn(cache(), a["q"], a["hq"], a["lens"], a["max_len"], a["blocks"], a["counts"], a["n"],
+    refused(lib, lib.kvo_paged_attn(cache(max_pages=a["mp"]), a["q"], a["hq"], a["lens"], a["max_len"], a["blocks"], a["counts"], a["n"],
                                     a["o"], P, a["ws"], a["size"], None, None), frag)
 
 
 def test_workspace_grows_with_the_work(lib):
     n = ctypes.c_size_t(0)
     sizes = []
-    for max_len in (1, 128, 0):
-        assert lib.kvo_paged_attn_workspace(cache(max_pages=1024), 8, 0, max_len, ctypes.byref(n)) == kvo.KVO_OK
+    for max_len in (1, 128, 100000, 0):
+        assert lib.kvo_paged_attn_workspace(cache(max_pages=8192), 8, 0, max_len, ctypes.byref(n)) == kvo.KVO_OK
         sizes.append(n.value)
-    assert 0 < sizes[0] < sizes[2] and sizes == sorted(sizes)
+    assert sizes[0] == sizes[1] == 0 < sizes[2] <= sizes[3]
 
 
 def test_wrappers_check_buffers():
