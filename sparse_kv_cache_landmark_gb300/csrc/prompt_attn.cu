@@ -10,10 +10,10 @@
 // tile is fetched once for the whole group and short prompts fill their tiles.
 // One CTA per item and SM, heaviest items first:
 //   warp 9   loads Q once and K, V tiles of 128 keys through a ring (TMA),
-//   warp 8   one thread issues tcgen05.mma: S_t = Q_t K^T (shared x shared) and
-//            O_t += P_t V (tensor memory x shared), in the order
-//            S_0(j), O_1(j-1), S_1(j), O_0(j): each tile's softmax runs beside
-//            the other tile's two products,
+//   warps 8, 10  one thread each issues the tcgen05.mma of tile 0 and 1: S_t =
+//            Q_t K^T (shared x shared) and O_t += P_t V (tensor memory x
+//            shared), in the order O_t(j), S_t(j+1): a tile's softmax runs
+//            beside the other tile's two products,
 //   warps 0-3, 4-7  the softmax of tile 0 and 1, one thread per row: S from
 //            tensor memory, online maximum and sum in fp32, P (bf16) back over S.
 // Tensor memory (512 columns): S_0, S_1 (128 each, P over their first half),
@@ -45,6 +45,7 @@ template <int D>
 struct PrShape {
     static constexpr int TILE = (D / 64) * PR_BLOCK;            // bytes of 128 rows x D values
     static constexpr int STAGES = (192 * 1024 - 2 * TILE) / TILE;
+    static constexpr int DEPTH = STAGES / 2;                    // tiles of keys that fit the ring, K and V
     static constexpr int SMEM = (2 + STAGES) * TILE + 1024;     // > half an SM's: one CTA per SM
 };
 
@@ -66,27 +67,52 @@ __device__ __forceinline__ float pr_ex2(float x) {
     return y;
 }
 
+// Two fp32 lanes in one instruction.
+__device__ __forceinline__ uint64_t pack2(float lo, float hi) {
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+    return r;
+}
+__device__ __forceinline__ void unpack2(uint64_t v, float& lo, float& hi) { asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v)); }
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+    float r;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+    return r;
+}
+
 struct PrShared {
-    uint64_t q_full, kv_full[12], kv_empty[12], s_full[2], p_full[2], o_done[2], v_tail, drain;
+    uint64_t q_full, kv_full[12], s_full[2][6], p_full[2][2], o_done[2], turn[2], drain[2], v_tail;
     uint32_t tmem;
     int abort;
 };
 
 // A wait that gives up after the limit, or once another warp has; every caller then leaves its loop.
-__device__ __forceinline__ bool pr_wait(PrShared& sh, const PromptArgs& A, uint64_t& bar, uint32_t parity) {
-    const uint32_t b = smem_u32(&bar);
-    for (int i = 0; i < 32; ++i)
-        if (mbar_try_wait(b, parity)) return true;
+__device__ __forceinline__ bool pr_wait_long(int* abort, int32_t* status, uint32_t bar, uint32_t parity, long long limit) {
     const uint64_t t0 = global_ns();
-    while (!mbar_try_wait(b, parity)) {
-        if (*(volatile int*)&sh.abort) return false;
-        if ((long long)(global_ns() - t0) > A.wait_ns) {
-            *(volatile int*)&sh.abort = 1;
-            if (A.status) atomicOr(A.status, KVO_DEV_TIMEOUT);
+    while (!mbar_try_wait(bar, parity)) {
+        if (*(volatile int*)abort) return false;
+        if ((long long)(global_ns() - t0) > limit) {
+            *(volatile int*)abort = 1;
+            if (status) atomicOr(status, KVO_DEV_TIMEOUT);
             return false;
         }
     }
     return true;
+}
+__device__ __forceinline__ bool pr_wait(PrShared& sh, const PromptArgs& A, uint64_t& bar, uint32_t parity) {
+    const uint32_t b = smem_u32(&bar);
+    if (mbar_try_wait(b, parity)) return true;
+    return pr_wait_long(&sh.abort, A.status, b, parity, A.wait_ns);
 }
 
 // The softmax of one tile: a thread owns row `row` of it; the row sees its request's keys [0, limit).
@@ -97,8 +123,11 @@ __device__ __forceinline__ void pr_softmax(PrShared& sh, const PromptArgs& A, in
     const uint32_t S = sh.tmem + 128 * t + lanes, O = sh.tmem + 256 + D * t + lanes;
     float m = -INFINITY, l = 0.f;                                       // log2 units; l in units of 2^m
     bool ok = true;
+    int slot = 0;                  // of S(j)'s barrier, and its parity
+    uint32_t parity = 0;
     for (int j = 0; j < n_tiles; ++j) {
-        ok = pr_wait(sh, A, sh.s_full[t], j & 1);
+        ok = pr_wait(sh, A, sh.s_full[t][slot], parity);
+        if (++slot == PrShape<D>::DEPTH) { slot = 0; parity ^= 1; }
         if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
         tc_fence_after();
         uint32_t s[PR_KEYS];
@@ -111,21 +140,22 @@ __device__ __forceinline__ void pr_softmax(PrShared& sh, const PromptArgs& A, in
             for (int i = 0; i < PR_KEYS; ++i)
                 if (i >= rem) s[i] = 0xFF800000u;                       // -inf
         }
-        float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+        float mx[4];
 #pragma unroll
-        for (int i = 0; i < PR_KEYS; i += 4)
+        for (int e = 0; e < 4; ++e) mx[e] = __uint_as_float(s[e]);
 #pragma unroll
-            for (int e = 0; e < 4; ++e) mx[e] = fmaxf(mx[e], __uint_as_float(s[i + e]));
-        const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * A.scale_log2;
+        for (int i = 4; i + 8 <= PR_KEYS; i += 8)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) mx[e] = max3(mx[e], __uint_as_float(s[i + e]), __uint_as_float(s[i + 4 + e]));
+#pragma unroll
+        for (int e = 0; e < 4; ++e) mx[e] = fmaxf(mx[e], __uint_as_float(s[PR_KEYS - 4 + e]));
+        const float top = fmaxf(max3(mx[0], mx[1], mx[2]), mx[3]) * A.scale_log2;
         if (__any_sync(0xffffffffu, top > m + PR_RAISE)) {
             const float to = fmaxf(m, top);
             const float f = m == -INFINITY ? 0.f : pr_ex2(m - to);
             m = to;
             l *= f;
-            if (j > 0) {
-                ok = pr_wait(sh, A, sh.o_done[t], (j - 1) & 1);
-                if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
-                tc_fence_after();
+            if (j > 0) {           // S(j) complete: so is O += P(j - 1) V, which was issued before it
 #pragma unroll 1
                 for (int c = 0; c < D; c += 32) {
                     uint32_t o[32];
@@ -138,28 +168,34 @@ __device__ __forceinline__ void pr_softmax(PrShared& sh, const PromptArgs& A, in
             }
         }
         const float b = m == -INFINITY ? 0.f : -m;
-        float sum[4] = {0.f, 0.f, 0.f, 0.f};
+        const uint64_t scale2 = pack2(A.scale_log2, A.scale_log2), b2 = pack2(b, b);
+        uint64_t sum[2] = {0ull, 0ull};
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            uint32_t p[32];
+        for (int h = 0; h < 4; ++h) {
+            uint32_t p[16];
 #pragma unroll
-            for (int i = 0; i < 32; ++i) {
-                const float x = pr_ex2(fmaf(__uint_as_float(s[64 * h + 2 * i]), A.scale_log2, b));
-                const float y = pr_ex2(fmaf(__uint_as_float(s[64 * h + 2 * i + 1]), A.scale_log2, b));
-                sum[(2 * i) & 3] += x;
-                sum[(2 * i + 1) & 3] += y;
+            for (int i = 0; i < 16; ++i) {
+                float x, y;
+                unpack2(fma2(pack2(__uint_as_float(s[32 * h + 2 * i]), __uint_as_float(s[32 * h + 2 * i + 1])), scale2, b2), x, y);
+                x = pr_ex2(x);
+                y = pr_ex2(y);
+                sum[i & 1] = add2(sum[i & 1], pack2(x, y));
                 const __nv_bfloat162 v = __floats2bfloat162_rn(x, y);
                 p[i] = *reinterpret_cast<const uint32_t*>(&v);
             }
-            tmem_st32(S + 32 * h, p);
+            tmem_st16(S + 16 * h, p);
+            if (h & 1) {           // half of the weights are there: the value product may begin on them
+                tmem_wait_st();
+                tc_fence_before();
+                mbar_arrive(smem_u32(&sh.p_full[t][h >> 1]));
+            }
         }
-        l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
-        tmem_wait_st();
-        tc_fence_before();
-        mbar_arrive(smem_u32(&sh.p_full[t]));
+        float s0, s1;
+        unpack2(add2(sum[0], sum[1]), s0, s1);
+        l += s0 + s1;
     }
     if (ok && n_tiles > 0) {
-        ok = pr_wait(sh, A, sh.o_done[t], (n_tiles - 1) & 1);
+        ok = pr_wait(sh, A, sh.o_done[t], 0);
         ok = __all_sync(0xffffffffu, ok);
         tc_fence_after();
     }
@@ -234,17 +270,16 @@ prompt_attn_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
     const uint32_t ring = base + 2 * P::TILE;
     if (tid == 0) {
         mbar_init(smem_u32(&sh.q_full), 1);
-        for (int i = 0; i < P::STAGES; ++i) {
-            mbar_init(smem_u32(&sh.kv_full[i]), 1);
-            mbar_init(smem_u32(&sh.kv_empty[i]), 1);
-        }
+        for (int i = 0; i < P::STAGES; ++i) mbar_init(smem_u32(&sh.kv_full[i]), 1);
         for (int t = 0; t < 2; ++t) {
-            mbar_init(smem_u32(&sh.s_full[t]), 1);
-            mbar_init(smem_u32(&sh.p_full[t]), 128);
+            for (int i = 0; i < P::DEPTH; ++i) mbar_init(smem_u32(&sh.s_full[t][i]), 1);
+            mbar_init(smem_u32(&sh.p_full[t][0]), 128);
+            mbar_init(smem_u32(&sh.p_full[t][1]), 128);
             mbar_init(smem_u32(&sh.o_done[t]), 1);
+            mbar_init(smem_u32(&sh.turn[t]), 1);
+            mbar_init(smem_u32(&sh.drain[t]), 1);
         }
         mbar_init(smem_u32(&sh.v_tail), 1);
-        mbar_init(smem_u32(&sh.drain), 1);
         sh.abort = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
@@ -268,10 +303,17 @@ prompt_attn_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
                                     (int)qs + tok0 + t * A.tq, smem_u32(&sh.q_full));
             }
             for (int i = 0; i < 2 * n; ++i) {
-                const int st = i % P::STAGES, use = i / P::STAGES, key0 = (i >> 1) * PR_KEYS;
+                const int st = i % P::STAGES, jj = i >> 1, key0 = jj * PR_KEYS;
                 const bool is_v = i & 1;
-                if (use > 0) {
-                    ok = pr_wait(sh, A, sh.kv_empty[st], (use - 1) & 1);
+                if (i >= P::STAGES) {
+                    // K(jj - DEPTH)'s stage is free once both tiles' scores with it are there, V(jj - DEPTH)'s once the
+                    // scores after it are, which were issued after its value product (n_t differ by one at most, so
+                    // those exist).  Each of these barriers completes next with a tile that this loop loads later, so
+                    // a parity says which phase is meant.
+                    const int x = jj - P::DEPTH + is_v;
+#pragma unroll
+                    for (int t = 0; t < 2; ++t)
+                        if (x < n_t[t] && ok) ok = pr_wait(sh, A, sh.s_full[t][x % P::DEPTH], (x / P::DEPTH) & 1);
                     if (!__all_sync(0xffffffffu, ok)) break;
                 }
                 const uint32_t dst = ring + st * P::TILE;
@@ -303,58 +345,62 @@ prompt_attn_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
                     mbar_wait_bounded(smem_u32(&sh.kv_full[i % P::STAGES]), (i / P::STAGES) & 1, A.wait_ns);
                 if (issued < 2 * n && (issued & 1)) mbar_wait_bounded(smem_u32(&sh.v_tail), 0, A.wait_ns / 4);
             }
-        } else if (warp == 8 && lane == 0 && n > 0) {
-            // ------------------------------------------------ matrix products
+        } else if ((warp & 1) == 0 && lane == 0 && n_t[(warp - 8) >> 1] > 0) {
+            // ------------------------------------------------ matrix products of one tile
+            // The tensor cores queue a few instructions only; with a thread of its own for each tile, one tile's
+            // waits and commits (about 100 and 55 cycles) pass while the other's products run.  They take turns, so
+            // that the tiles stay half a period apart: left alone both fall into step, and then the tensor cores
+            // idle while both do their softmax.
             constexpr uint32_t ID_S = mma_desc(PR_ROWS, PR_KEYS, false), ID_O = mma_desc(PR_ROWS, D, true);
-            const uint32_t tm = sh.tmem;
-            auto full = [&](int i) { return pr_wait(sh, A, sh.kv_full[i % P::STAGES], (i / P::STAGES) & 1); };
-            auto empty = [&](int i) {      // only where a later load waits for it
-                if (i + P::STAGES < 2 * n) tc_commit(smem_u32(&sh.kv_empty[i % P::STAGES]));
-            };
-            auto scores = [&](int t, int j) {
-                const uint32_t k = ring + ((2 * j) % P::STAGES) * P::TILE, q = base + t * P::TILE;
+            const int t = (warp - 8) >> 1, n_mine = n_t[t], n_other = n_t[t ^ 1];
+            const uint32_t S = sh.tmem + 128 * t, O = sh.tmem + 256 + D * t;
+            const uint64_t q = smem_desc(base + t * P::TILE, 16), k0 = smem_desc(ring, 16), v0 = smem_desc(ring, PR_BLOCK);
+            auto scores = [&](int stage, bool pass) {            // stage 2 (j % DEPTH) holds K(j)
+                const uint64_t k = k0 + stage * (P::TILE >> 4);
 #pragma unroll
                 for (int e = 0; e < D / 16; ++e) {
-                    const uint32_t off = (e >> 2) * PR_BLOCK + (e & 3) * 32;
-                    mma_ss(tm + 128 * t, smem_desc(q + off, 16), smem_desc(k + off, 16), ID_S, e > 0);
+                    if (e == D / 32 && pass) mbar_arrive(smem_u32(&sh.turn[t ^ 1]));     // queued work covers the hand-over
+                    const int off = (e >> 2) * (PR_BLOCK >> 4) + (e & 3) * 2;
+                    mma_ss(S, q + off, k + off, ID_S, e > 0);
                 }
-                tc_commit(smem_u32(&sh.s_full[t]));
+                tc_commit(smem_u32(&sh.s_full[t][stage >> 1]));
             };
-            auto values = [&](int t, int j) {
-                const uint32_t v = ring + ((2 * j + 1) % P::STAGES) * P::TILE;
+            int ks = 0, vs = 1;                      // stages of K and V, and the parities of their next fill
+            uint32_t kp = 0, vp = 0;
+            bool ok = pr_wait(sh, A, sh.q_full, 0) && pr_wait(sh, A, sh.kv_full[0], 0);
+            if (ok) scores(0, false);
+            for (int j = 0; ok && j < n_mine; ++j) {
+                ks += 2;
+                if (ks >= P::STAGES) { ks -= P::STAGES; kp ^= 1; }
+                if (!(ok = pr_wait(sh, A, sh.kv_full[vs], vp))) break;
+                if (j + 1 < n_mine && !(ok = pr_wait(sh, A, sh.kv_full[ks], kp))) break;
+                const uint64_t v = v0 + vs * (P::TILE >> 4);
 #pragma unroll
-                for (int e = 0; e < PR_KEYS / 16; ++e)
-                    mma_ts(tm + 256 + D * t, tm + 128 * t + 8 * e, smem_desc(v + e * 2048, PR_BLOCK), ID_O, j > 0 || e > 0);
-                tc_commit(smem_u32(&sh.o_done[t]));
-            };
-            bool ok = pr_wait(sh, A, sh.q_full, 0);
-            for (int j = 0; ok && j <= n; ++j) {
-                if (j < n) {
-                    if (!(ok = full(2 * j))) break;
-                    if (j < n_t[0]) scores(0, j);
-                }
-                if (j > 0) {
-                    if (j - 1 < n_t[1]) {
-                        if (!(ok = pr_wait(sh, A, sh.p_full[1], (j - 1) & 1))) break;
-                        tc_fence_after();
-                        values(1, j - 1);
+                for (int h = 0; h < 2; ++h) {        // in two halves of the keys, each as its weights come
+                    if (!ok || !(ok = pr_wait(sh, A, sh.p_full[t][h], j & 1))) break;
+                    if (h == 0) {
+                        const int k = t ? j : j - 1;             // the other tile's round before this one
+                        if (k >= 0 && k < n_other && !(ok = pr_wait(sh, A, sh.turn[t], k & 1))) break;
                     }
-                    empty(2 * j - 1);
+                    tc_fence_after();
+#pragma unroll
+                    for (int e = 4 * h; e < 4 * h + 4; ++e)
+                        mma_ts(O, S + 8 * e, v + e * (2048 >> 4), ID_O, j > 0 || e > 0);
                 }
-                if (j < n) {
-                    if (j < n_t[1]) scores(1, j);
-                    empty(2 * j);
-                    if (!(ok = full(2 * j + 1))) break;
-                    if (j < n_t[0]) {
-                        if (!(ok = pr_wait(sh, A, sh.p_full[0], j & 1))) break;
-                        tc_fence_after();
-                        values(0, j);
-                    }
+                if (!ok) break;
+                // One commit for the scores stands for the value product before them as well.
+                if (j + 1 < n_mine) {
+                    scores(ks, true);
+                } else {
+                    tc_commit(smem_u32(&sh.o_done[t]));
+                    mbar_arrive(smem_u32(&sh.turn[t ^ 1]));
                 }
+                vs += 2;
+                if (vs >= P::STAGES) { vs -= P::STAGES; vp ^= 1; }
             }
             // nothing of this CTA may be in flight when it leaves
-            tc_commit(smem_u32(&sh.drain));
-            mbar_wait_bounded(smem_u32(&sh.drain), 0, A.wait_ns);
+            tc_commit(smem_u32(&sh.drain[t]));
+            mbar_wait_bounded(smem_u32(&sh.drain[t]), 0, A.wait_ns);
         }
         __syncwarp();
     } else {

@@ -66,6 +66,12 @@ __device__ __forceinline__ void tmem_st32(uint32_t addr, const uint32_t* r) {
         KVO_W8(r, 8), KVO_W8(r, 16), KVO_W8(r, 24), "r"(addr)
         : "memory");
 }
+__device__ __forceinline__ void tmem_st16(uint32_t addr, const uint32_t* r) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%16], {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15};" ::KVO_W8(r, 0),
+        KVO_W8(r, 8), "r"(addr)
+        : "memory");
+}
 #undef KVO_R8
 #undef KVO_W8
 __device__ __forceinline__ void tmem_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
