@@ -3,12 +3,14 @@
 Every step of the decode path runs in the library's CUDA kernels; this module
 turns torch tensors into pointers, allocates outputs with torch, and raises
 ``KvoError`` on any non-OK status.  There is no fallback: without the built
-library or a CUDA device every call fails.
+library or a CUDA device every call fails.  The serving calls (rope, paged_append,
+paged_attn, prompt_attn), which a decode loop makes once per layer and token, go
+through a native binding (csrc/binding.cpp) instead of ctypes.
 """
 from __future__ import annotations
 
 import ctypes
-import functools
+import importlib.util
 import math
 import os
 from typing import List, Optional, Sequence
@@ -237,60 +239,23 @@ def sparse_decode_attn_static(q, k_buf, v_buf, slot_of_true, k_win, v_win, *, ba
     return o, lse
 
 
-# The checks of the context-free calls below are written to cost little where nothing is wrong: decode loops make
-# these calls once per layer and token.
-_BF16, _I32, _I64, _F32, _E4M3 = torch.bfloat16, torch.int32, torch.int64, torch.float32, torch.float8_e4m3fn
+_BINDING = None
 
 
-def _need(dev, name, t, dtype, shape=None):
-    """Address of one contiguous buffer on CUDA device ``dev`` (ordinal), or a ``KvoError`` that says what is wrong."""
-    if t is not None and t.dtype is dtype and t.get_device() == dev and t.is_contiguous() and (shape is None or t.shape == shape):
-        return t.data_ptr()
-    if t is None:
-        raise KvoError(KVO_ERR_INVALID, f"{name} is required")
-    if t.dtype != dtype:
-        raise KvoError(KVO_ERR_INVALID, f"{name} must be {dtype}, got {t.dtype}")
-    if shape is not None and t.shape != shape:
-        raise KvoError(KVO_ERR_INVALID, f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
-    if not t.is_contiguous():
-        raise KvoError(KVO_ERR_INVALID, f"{name} must be contiguous")
-    raise KvoError(KVO_ERR_INVALID, f"all buffers must be on one CUDA device: {name} is on {t.device}")
-
-
-def _rows(dev, name, t, free_heads=False):
-    """Strides (token, head) of a bf16 [tokens][heads][d] buffer whose token stride (and head stride) is free."""
-    if t.dtype is not _BF16 or t.dim() != 3 or t.get_device() != dev:
-        if t.dtype is not _BF16:
-            raise KvoError(KVO_ERR_INVALID, f"{name} must be torch.bfloat16, got {t.dtype}")
-        if t.dim() != 3:
-            raise KvoError(KVO_ERR_INVALID, f"{name} must be [tokens][heads][head_dim], got {tuple(t.shape)}")
-        raise KvoError(KVO_ERR_INVALID, f"all buffers must be on one CUDA device: {name} is on {t.device}")
-    T, H, d = t.shape
-    st, sh, sd = t.stride()
-    if H <= 1:                    # a dimension of one has no stride of its own
-        sh = d
-    if T <= 1:
-        st = max(H * sh, d)
-    if (sd != 1 and d > 1) or (sh != d and not free_heads):
-        raise KvoError(KVO_ERR_INVALID, f"{name}: heads must be contiguous" if sd == 1 else f"{name}: the last dimension must be contiguous")
-    return st, sh
-
-
-def _launch(dev, stream, fn, *args):
-    """Call a library function with ``dev`` current on ``stream`` (default: torch's current stream of that device)."""
-    if dev < 0:
-        raise KvoError(KVO_ERR_INVALID, "all buffers must be on one CUDA device, got cpu")
-    if stream is None:
-        h = torch._C._cuda_getCurrentRawStream(dev) or CUDA_STREAM_LEGACY
-    else:
-        h = (stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)) or CUDA_STREAM_LEGACY
-    if dev == torch._C._cuda_getDevice():
-        st = fn(*args, h)
-    else:
-        with torch.cuda.device(dev):
-            st = fn(*args, h)
-    if st:
-        _check(st)
+def _native():
+    """The native binding of the serving calls (built beside libkvo.so); raises if it is missing."""
+    global _BINDING
+    if _BINDING is None:
+        lib()
+        path = os.path.join(_HERE, "_kvo_binding.so")
+        if not os.path.exists(path):
+            raise RuntimeError(f"_kvo_binding.so not built ({path}); run __graft_entry__.build()")
+        spec = importlib.util.spec_from_file_location("_kvo_binding", path)
+        m = importlib.util.module_from_spec(spec)
+        spec.loader.exec_module(m)
+        m.raise_with(KvoError)
+        _BINDING = m
+    return _BINDING
 
 
 def rope_frequencies(rot_dim: int, base: float = 10000.0, scaling: Optional[str] = None, factor: float = 1.0,
@@ -336,37 +301,7 @@ def rope_frequencies(rot_dim: int, base: float = 10000.0, scaling: Optional[str]
 def rope(x, pos, freq, interleaved: bool = False, amplitude: float = 1.0, out=None, stream=None):
     """Rotary positions (C: kvo_rope).  x: CUDA bf16 [tokens][heads][d], last dimension contiguous, any token and
     head stride; pos: int32 [tokens]; freq: ``rope_frequencies``.  ``out=x`` rotates in place."""
-    dev = x.get_device()
-    st, sh = _rows(dev, "x", x, True)
-    T, H, d = x.shape
-    pp, pf = _need(dev, "pos", pos, _I32, (T,)), _need(dev, "freq", freq, _I64)
-    if out is None:
-        out, ot, oh = x.new_empty((T, H, d)), H * d, d
-    else:
-        if out.shape != x.shape:
-            raise KvoError(KVO_ERR_INVALID, f"out must have shape {tuple(x.shape)}, got {tuple(out.shape)}")
-        ot, oh = _rows(dev, "out", out, True)
-    _launch(dev, stream, lib().kvo_rope, x.data_ptr(), st, sh, out.data_ptr(), ot, oh, pp, pf, T, H, d,
-            2 * freq.numel(), 1 if interleaved else 0, amplitude)
-    return out
-
-
-def _paged(dev, k_pages, v_pages, k_scale, v_scale, table):
-    """Checked descriptor of a paged cache ([n_pages][Hkv][page_size][d] pools, int32 [batch][max_pages] table), and
-    (batch, Hkv, d)."""
-    if k_pages.dim() != 4 or table is None or table.dim() != 2:
-        raise KvoError(KVO_ERR_INVALID, "pages must be [n_pages][n_kv_heads][page_size][head_dim], table [batch][max_pages]")
-    dt, shape, ts = k_pages.dtype, k_pages.shape, table.shape
-    n, h, p, d = shape
-    if dt is _BF16:
-        ks = vs = None
-    elif dt is _E4M3:
-        ks = _need(dev, "k_scale", k_scale, _F32, (n, h))
-        vs = _need(dev, "v_scale", v_scale, _F32, (n, h))
-    else:
-        raise KvoError(KVO_ERR_INVALID, f"pages must be bfloat16 or float8_e4m3fn, got {dt}")
-    return _PagedCache(_need(dev, "k_pages", k_pages, dt), _need(dev, "v_pages", v_pages, dt, shape), ks, vs,
-                       _need(dev, "table", table, _I32), ts[0], h, d, p, n, ts[1], 0 if ks is None else 1), ts[0], h, d
+    return (_BINDING or _native()).rope(x, pos, freq, interleaved, amplitude, out, stream)
 
 
 def paged_append(k, v, k_pages, v_pages, table, start, *, cu=None, k_scale=None, v_scale=None, freq=None,
@@ -379,43 +314,8 @@ def paged_append(k, v, k_pages, v_pages, table, start, *, cu=None, k_scale=None,
     [batch], the tokens each request has already; cu: int32 [batch + 1] token offsets (None: one token
     each).  Returns q_out, the rotated q (None without q).
     """
-    dev = k_pages.get_device()
-    c, batch, hkv, d = _paged(dev, k_pages, v_pages, k_scale, v_scale, table)
-    kt, vt = _rows(dev, "k", k)[0], _rows(dev, "v", v)[0]
-    T = k.shape[0]
-    shape = (T, hkv, d)
-    if k.shape != shape or v.shape != shape:
-        raise KvoError(KVO_ERR_INVALID, f"k and v must have shape {shape}, got {tuple(k.shape)} and {tuple(v.shape)}")
-    ps = _need(dev, "start", start, _I32, (batch,))
-    pc = None if cu is None else _need(dev, "cu", cu, _I32, (batch + 1,))
-    pf, rot = (None, 0) if freq is None else (_need(dev, "freq", freq, _I64), 2 * freq.numel())
-    pk = None if k_out is None else _need(dev, "k_out", k_out, _BF16, shape)
-    pst = None if status is None else _need(dev, "status", status, _I32)
-    pq = pqo = None
-    qt = hq = 0
-    if q is not None:
-        qt, hq = _rows(dev, "q", q)[0], q.shape[1]
-        if q.shape != (T, hq, d):
-            raise KvoError(KVO_ERR_INVALID, f"q must have shape {(T, hq, d)}, got {tuple(q.shape)}")
-        if q_out is None:
-            q_out = q.new_empty((T, hq, d))
-            pqo = q_out.data_ptr()
-        else:
-            pqo = _need(dev, "q_out", q_out, _BF16, (T, hq, d))
-        pq = q.data_ptr()
-    _launch(dev, stream, lib().kvo_paged_append, c, k.data_ptr(), kt, v.data_ptr(), vt, T, pc, ps, pf, rot,
-            1 if interleaved else 0, amplitude, pq, qt, hq, pqo, pk, pst)
-    return q_out if q is not None else None
-
-
-@functools.lru_cache(maxsize=4096)
-def _paged_attn_workspace(batch, hkv, d, page, n_pages, max_pages, fmt, hq, n_blocks, max_len) -> int:
-    """kvo_paged_attn_workspace's bytes: a function of the sizes alone (any non-null pointers will do)."""
-    n = ctypes.c_size_t(0)
-    p = 4096
-    c = _PagedCache(p, p, p, p, p, batch, hkv, d, page, n_pages, max_pages, fmt)
-    _check(lib().kvo_paged_attn_workspace(c, hq, n_blocks, max_len, ctypes.byref(n)))
-    return n.value
+    return (_BINDING or _native()).paged_append(k, v, k_pages, v_pages, table, start, cu, k_scale, v_scale, freq,
+                                                interleaved, amplitude, q, q_out, k_out, status, stream)
 
 
 def paged_attn(q, k_pages, v_pages, table, lens, *, k_scale=None, v_scale=None, blocks=None, counts=None,
@@ -427,46 +327,8 @@ def paged_attn(q, k_pages, v_pages, table, lens, *, k_scale=None, v_scale=None, 
     counts: int32 [batch][Hkv].  The workspace comes from torch's allocator when none is given; it must
     then stay on the stream that is current (give one for another ``stream``).
     """
-    dev = k_pages.get_device()
-    c, batch, hkv, d = _paged(dev, k_pages, v_pages, k_scale, v_scale, table)
-    if q.dim() != 3:
-        raise KvoError(KVO_ERR_INVALID, f"q must be [batch][n_q_heads][head_dim], got {tuple(q.shape)}")
-    hq = q.shape[1]
-    rows = (batch, hq, d)
-    pq, pl = _need(dev, "q", q, _BF16, rows), _need(dev, "lens", lens, _I32, (batch,))
-    pb = pc = None
-    n_blocks = 0
-    if blocks is not None:
-        n_blocks = blocks.shape[-1]
-        if n_blocks == 0 or blocks.numel() != batch * hkv * n_blocks:
-            raise KvoError(KVO_ERR_INVALID, f"blocks must be [batch][n_kv_heads][n], got {tuple(blocks.shape)}")
-        pb = _need(dev, "blocks", blocks, _I32)
-    if counts is not None:
-        if blocks is None:
-            raise KvoError(KVO_ERR_INVALID, "counts needs blocks")
-        if counts.numel() != batch * hkv:
-            raise KvoError(KVO_ERR_INVALID, f"counts must be [batch][n_kv_heads], got {tuple(counts.shape)}")
-        pc = _need(dev, "counts", counts, _I32)
-    pst = None if status is None else _need(dev, "status", status, _I32)
-    if o is None:
-        o = torch.empty_like(q)
-        po = o.data_ptr()
-    else:
-        po = _need(dev, "o", o, _BF16, rows)
-    if lse is None:
-        lse = q.new_empty((batch, hq), dtype=_F32)
-        pls = lse.data_ptr()
-    else:
-        pls = _need(dev, "lse", lse, _F32, (batch, hq))
-    if workspace is None:
-        size = _paged_attn_workspace(batch, hkv, d, c.page_size, c.n_pages, c.max_pages, c.format, hq, n_blocks, max_len)
-        if size:
-            workspace = q.new_empty(size, dtype=torch.uint8)
-        pw = workspace.data_ptr() if size else None
-    else:
-        pw, size = _need(dev, "workspace", workspace, torch.uint8), workspace.numel()
-    _launch(dev, stream, lib().kvo_paged_attn, c, pq, hq, pl, max_len, pb, pc, n_blocks, po, pls, pw, size, pst)
-    return o, lse
+    return (_BINDING or _native()).paged_attn(q, k_pages, v_pages, table, lens, k_scale, v_scale, blocks, counts, max_len,
+                                              o, lse, workspace, status, stream)
 
 
 def prompt_attn(q, k, v, cu_q, cu_k=None, causal: bool = True, o=None, lse=None, status=None, stream=None):
@@ -475,30 +337,7 @@ def prompt_attn(q, k, v, cu_q, cu_k=None, causal: bool = True, o=None, lse=None,
     q: CUDA bf16 [total_q][Hq][d]; k, v: [total_k][Hkv][d], heads contiguous, any token stride; cu_q, cu_k:
     int32 [batch + 1] offsets (cu_k None: cu_q).
     """
-    dev = q.get_device()
-    qt, kt, vt = _rows(dev, "q", q)[0], _rows(dev, "k", k)[0], _rows(dev, "v", v)[0]
-    T, hq, d = q.shape
-    n, hkv, dk = k.shape
-    if dk != d or v.shape != k.shape:
-        raise KvoError(KVO_ERR_INVALID, f"k and v must have shape {(n, hkv, d)}, got {tuple(k.shape)} and {tuple(v.shape)}")
-    if cu_q.dim() != 1 or cu_q.numel() < 1:
-        raise KvoError(KVO_ERR_INVALID, f"cu_q must be [batch + 1], got {tuple(cu_q.shape)}")
-    pcq = _need(dev, "cu_q", cu_q, _I32)
-    pck = pcq if cu_k is None else _need(dev, "cu_k", cu_k, _I32, cu_q.shape)
-    pst = None if status is None else _need(dev, "status", status, _I32)
-    if o is None:
-        o = q.new_empty((T, hq, d))
-        po = o.data_ptr()
-    else:
-        po = _need(dev, "o", o, _BF16, (T, hq, d))
-    if lse is None:
-        lse = q.new_empty((T, hq), dtype=_F32)
-        pl = lse.data_ptr()
-    else:
-        pl = _need(dev, "lse", lse, _F32, (T, hq))
-    _launch(dev, stream, lib().kvo_prompt_attn, q.data_ptr(), qt, k.data_ptr(), kt, v.data_ptr(), vt, pcq, pck,
-            cu_q.numel() - 1, T, n, hq, hkv, d, 1 if causal else 0, po, pl, pst)
-    return o, lse
+    return (_BINDING or _native()).prompt_attn(q, k, v, cu_q, cu_k, causal, o, lse, status, stream)
 
 
 class Context:
