@@ -6,13 +6,17 @@
 // step before the quantisation (2^-9 relative against e4m3's 2^-4) makes the
 // prompt's own attention and the cache agree on what the key is.
 //
-// One CTA owns one (page, KV head) that the call touches, so the page's scale
-// needs no atomics: it holds the page's new rows in registers, takes their
+// Prompts: one CTA owns one (page, KV head) that the call touches, so the page's
+// scale needs no atomics: it holds the page's new rows in registers, takes their
 // largest magnitude, settles the scale, moves rows of earlier calls to it when
-// it grew, and writes codes.  Further CTAs of the same launch rotate q.
+// it grew, and writes codes.  CTAs that rotate q are interleaved with them in one
+// launch: the first are bound by latency (offsets, then rows, then codes), the
+// second by HBM, and side by side they fill it.
 //
-// Bound by HBM on prompts (k and v read once, pages and k_out written once)
-// and by one chain of dependent loads on a decode step.
+// One token per request: a warp owns one (token, head), of K and V or of q; each
+// lane turns D / 64 pairs, so the angles take one or two sincos in a row.  Bound by a
+// chain of dependent loads (start, page, old scale), about 1 us each.
+//
 #include <stdio.h>
 
 #include <algorithm>
@@ -23,7 +27,7 @@
 
 namespace kvo {
 
-constexpr int APP_THREADS = 256;
+constexpr int APP_THREADS = 256;              // at most; small pages take smaller CTAs
 
 struct AppendArgs {
     uint8_t* pages[2];            // K, V
@@ -40,6 +44,7 @@ struct AppendArgs {
     int64_t tokens, q_tok;
     int batch, hkv, hq, page, n_pages, max_pages;
     int units;                    // upper bound of the pages touched
+    int64_t kv_blocks, blocks;    // CTAs of pages, and of the launch
     int q_per;                    // query heads per thread
     RopeArgs R;
 };
@@ -51,55 +56,93 @@ __device__ __forceinline__ void set_status(int32_t* status, int bits) {
 // Request b's token range; false (with a status bit) when the caller's offsets
 // leave [0, tokens] or the start is negative.
 __device__ __forceinline__ bool request_range(const AppendArgs& A, int b, int64_t& t0, int64_t& n, int& start) {
-    t0 = A.cu ? A.cu[b] : b;
-    n = A.cu ? (int64_t)A.cu[b + 1] - t0 : 1;
+    t0 = A.cu[b];
+    n = (int64_t)A.cu[b + 1] - t0;
     start = A.start[b];
     return t0 >= 0 && n >= 0 && t0 + n <= A.tokens && start >= 0;
 }
 
+// Moves `words` 16-byte words of codes to another scale: thread i of n.
+__device__ __forceinline__ void rescale_rows(uint8_t* codes, int words, float ratio, int i, int n) {
+    uint4* row = reinterpret_cast<uint4*>(codes);
+    for (int w = i; w < words; w += n) {
+        uint4 v = row[w];
+        uint16_t* cv = reinterpret_cast<uint16_t*>(&v);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            const uint32_t hh = e4m3x2_to_f16x2(cv[e]);
+            const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&hh));
+            cv[e] = f32x2_to_e4m3x2(f.x * ratio, f.y * ratio);
+        }
+        row[w] = v;
+    }
+}
+
+// Which request and which of its touched pages unit u is.  Request b has at most floor(n / page) + 2 of them, so its
+// units start at floor(cu[b] / page) + 2 b: every request finds its own without a scan.  By a whole warp.
+struct AppendUnit {
+    int b, j, start;
+    int64_t t0, n;
+    bool ok;
+};
+__device__ __forceinline__ AppendUnit append_unit(const AppendArgs& A, int u) {
+    AppendUnit U;
+    if (A.batch <= 32) {           // all offsets and starts in one round of loads
+        const int lane = threadIdx.x & 31;
+        const bool have = lane < A.batch;
+        const int c0 = have ? __ldg(A.cu + lane) : 0, c1 = have ? __ldg(A.cu + lane + 1) : 0;
+        const int st = have ? __ldg(A.start + lane) : 0;
+        const int64_t first = (int64_t)max(c0, 0) / A.page + 2 * (int64_t)lane;
+        U.b = max(0, 31 - __clz((int)__ballot_sync(0xffffffffu, have && first <= u)));
+        U.j = u - (int)__shfl_sync(0xffffffffu, first, U.b);
+        U.t0 = __shfl_sync(0xffffffffu, c0, U.b);
+        U.n = (int64_t)__shfl_sync(0xffffffffu, c1, U.b) - U.t0;
+        U.start = __shfl_sync(0xffffffffu, st, U.b);
+        U.ok = U.t0 >= 0 && U.n >= 0 && U.t0 + U.n <= A.tokens && U.start >= 0;
+    } else {
+        auto first = [&](int i) { return (int64_t)max(__ldg(A.cu + i), 0) / A.page + 2 * (int64_t)i; };
+        U.b = warp_find(A.batch, u, first);
+        U.j = u - (int)first(U.b);
+        U.ok = request_range(A, U.b, U.t0, U.n, U.start);
+    }
+    return U;
+}
+
+// Bad offsets of any request, also of one that no unit reaches; by one CTA of the launch.
+__device__ __forceinline__ void append_check(const AppendArgs& A) {
+    for (int i = threadIdx.x; i < A.batch; i += blockDim.x) {
+        int64_t t0, n;
+        int start;
+        if (!request_range(A, i, t0, n, start)) set_status(A.status, KVO_DEV_BAD_COUNT);
+    }
+}
+
 template <int D, bool FP8, int MAXU>
-__device__ __forceinline__ void append_page(const AppendArgs& A) {
+__device__ __forceinline__ void append_page(const AppendArgs& A, int block) {
     constexpr int UNITS = D / 16;                       // 16-value units of a row
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int u = blockIdx.x / A.hkv, h = blockIdx.x - u * A.hkv;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, NT = blockDim.x;
+    const int u = block / A.hkv, h = block - u * A.hkv;
     __shared__ float red[2][APP_THREADS / 32];
 
-    if (blockIdx.x == 0 && A.status)                    // bad offsets of any request, also of one that no unit reaches
-        for (int i = tid; i < A.batch; i += APP_THREADS) {
-            int64_t t0, n;
-            int start;
-            if (!request_range(A, i, t0, n, start)) set_status(A.status, KVO_DEV_BAD_COUNT);
-        }
-    // Request b has at most floor(n / page) + 2 touched pages, so its units start
-    // at floor(cu[b] / page) + 2 b: every request finds its own without a scan.
-    int b = u, j = 0;
-    if (A.cu) {
-        auto first = [&](int i) { return (int64_t)max(__ldg(A.cu + i), 0) / A.page + 2 * (int64_t)i; };
-        b = warp_find(A.batch, u, first);
-        j = u - (int)first(b);
-    }
-    int64_t t0, n;
-    int start;
-    if (!request_range(A, b, t0, n, start)) return;
-    const int64_t at = start / A.page + (int64_t)j;       // logical page
-    const int64_t pos0 = max((int64_t)start, at * A.page), pos1 = min(start + n, (at + 1) * A.page);
+    if (block == 0 && A.status) append_check(A);
+    const AppendUnit U = append_unit(A, u);
+    if (!U.ok) return;
+    const int start = U.start;
+    const int64_t at = start / A.page + (int64_t)U.j;       // logical page
+    const int64_t pos0 = max((int64_t)start, at * A.page), pos1 = min(start + U.n, (at + 1) * A.page);
     if (pos0 >= pos1) return;
     if (at >= A.max_pages) {
         if (tid == 0 && h == 0) set_status(A.status, KVO_DEV_BAD_COUNT);
         return;
     }
-    const int p = A.table[(int64_t)b * A.max_pages + at];
-    if (p < 0 || p >= A.n_pages) {
-        if (tid == 0 && h == 0) set_status(A.status, KVO_DEV_BAD_BLOCK_ID);
-        return;
-    }
+    const int p = A.table[(int64_t)U.b * A.max_pages + at];
     const int row0 = (int)(pos0 - at * A.page), rows = (int)(pos1 - pos0);
-    const int64_t tok0 = t0 + (pos0 - start);
+    const int64_t tok0 = U.t0 + (pos0 - start);
 
     uint4 xa[2][MAXU], xb[2][MAXU];
 #pragma unroll
     for (int i = 0; i < MAXU; ++i) {
-        const int w = tid + i * APP_THREADS, r = w / UNITS, un = w % UNITS;
+        const int w = tid + i * NT, r = w / UNITS, un = w % UNITS;
         if (r < rows) {
             int ca, cb;
             rope_chunks(A.R, D, un, ca, cb);
@@ -111,10 +154,14 @@ __device__ __forceinline__ void append_page(const AppendArgs& A) {
             xb[1][i] = *reinterpret_cast<const uint4*>(v + cb);
         }
     }
+    if (p < 0 || p >= A.n_pages) {                          // checked while the rows are on their way
+        if (tid == 0 && h == 0) set_status(A.status, KVO_DEV_BAD_BLOCK_ID);
+        return;
+    }
     float top[2] = {0.f, 0.f};
 #pragma unroll
     for (int i = 0; i < MAXU; ++i) {
-        const int w = tid + i * APP_THREADS, r = w / UNITS, un = w % UNITS;
+        const int w = tid + i * NT, r = w / UNITS, un = w % UNITS;
         if (r >= rows) continue;
         float c[8], s[8];
         if (rope_unit(A.R, un, (int)(pos0 + r), c, s)) rope_rotate(A.R.interleaved, c, s, xa[0][i], xb[0][i]);
@@ -153,27 +200,15 @@ __device__ __forceinline__ void append_page(const AppendArgs& A) {
         for (int x = 0; x < 2; ++x) {
             float m = 0.f;
 #pragma unroll
-            for (int i = 0; i < APP_THREADS / 32; ++i) m = fmaxf(m, red[x][i]);
+            for (int i = 0; i < APP_THREADS / 32; ++i)
+                if (i < NT / 32) m = fmaxf(m, red[x][i]);
             float s = e4m3_scale(m);
             float* slot = A.scale[x] + (int64_t)p * A.hkv + h;
             if (row0 > 0) {                                // rows of earlier calls: the scale never shrinks
                 const float old = *slot;
                 s = fmaxf(s, old);
-                if (s != old) {
-                    const float ratio = old / s;
-                    uint4* row = reinterpret_cast<uint4*>(A.pages[x] + ((int64_t)p * A.hkv + h) * A.page * D);
-                    for (int w = tid; w < row0 * UNITS; w += APP_THREADS) {
-                        uint4 v = row[w];
-                        uint16_t* cv = reinterpret_cast<uint16_t*>(&v);
-#pragma unroll
-                        for (int e = 0; e < 8; ++e) {
-                            const uint32_t hh = e4m3x2_to_f16x2(cv[e]);
-                            const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&hh));
-                            cv[e] = f32x2_to_e4m3x2(f.x * ratio, f.y * ratio);
-                        }
-                        row[w] = v;
-                    }
-                }
+                if (s != old)
+                    rescale_rows(A.pages[x] + ((int64_t)p * A.hkv + h) * A.page * D, row0 * UNITS, old / s, tid, NT);
             }
             inv[x] = 1.f / s;
             top[x] = s;
@@ -185,7 +220,7 @@ __device__ __forceinline__ void append_page(const AppendArgs& A) {
     }
 #pragma unroll
     for (int i = 0; i < MAXU; ++i) {
-        const int w = tid + i * APP_THREADS, r = w / UNITS, un = w % UNITS;
+        const int w = tid + i * NT, r = w / UNITS, un = w % UNITS;
         if (r >= rows) continue;
 #pragma unroll
         for (int x = 0; x < 2; ++x) {
@@ -217,36 +252,171 @@ __device__ __forceinline__ void append_page(const AppendArgs& A) {
     }
 }
 
-// Blocks [0, units * Hkv): pages.  The rest: q.
+// Pages and runs of q, spread evenly over the grid.
 template <int D, bool FP8, int MAXU>
 __global__ void __launch_bounds__(APP_THREADS) append_pages_kernel(const __grid_constant__ AppendArgs A) {
     grid_wait();
-    const int kv_blocks = A.units * A.hkv;
-    if ((int)blockIdx.x < kv_blocks) {
-        append_page<D, FP8, MAXU>(A);
+    // the pages among blocks 0 .. i - 1: floor(i * kv_blocks / blocks)
+    const int64_t kv = (int64_t)blockIdx.x * A.kv_blocks / A.blocks, kv1 = ((int64_t)blockIdx.x + 1) * A.kv_blocks / A.blocks;
+    if (kv1 > kv) {
+        append_page<D, FP8, MAXU>(A, (int)kv);
         return;
     }
     constexpr int UNITS = D / 16;
-    const int64_t i = (int64_t)(blockIdx.x - kv_blocks) * APP_THREADS + threadIdx.x;
-    const int64_t per_split = (A.tokens * UNITS + APP_THREADS - 1) / APP_THREADS * APP_THREADS;
+    const int64_t i = ((int64_t)blockIdx.x - kv) * blockDim.x + threadIdx.x;
+    const int64_t per_split = (A.tokens * UNITS + blockDim.x - 1) / blockDim.x * blockDim.x;
     const int64_t split = i / per_split, k = i - split * per_split;
     if (k >= A.tokens * UNITS) return;
     const int64_t t = k / UNITS;
     const int u = (int)(k - t * UNITS);
-    int b = (int)t;
-    if (A.cu) {
-        int lo = 0, hi = A.batch;                          // the last b with cu[b] <= t
-        while (hi - lo > 1) {
-            const int mid = (lo + hi) / 2;
-            if (__ldg(A.cu + mid) <= t) lo = mid; else hi = mid;
-        }
-        b = lo;
+    int lo = 0, hi = A.batch;                              // the last b with cu[b] <= t
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) / 2;
+        if (__ldg(A.cu + mid) <= t) lo = mid; else hi = mid;
     }
     int64_t t0, n;
     int start;
-    if (!request_range(A, b, t0, n, start) || t < t0 || t >= t0 + n) return;
+    if (!request_range(A, lo, t0, n, start) || t < t0 || t >= t0 + n) return;
     const int h0 = (int)split * A.q_per, h1 = min(A.hq, h0 + A.q_per);
     rope_heads(A.R, D, A.q + t * A.q_tok, D, A.q_out + t * A.hq * D, D, u, (int)(start + (t - t0)), h0, h1);
+}
+
+constexpr int STEP_WARPS = 4;
+
+// One token per request: warp (b, h) appends K and V of KV head h, or rotates query head h - Hkv.
+// Lane i holds slots i * N .. i * N + N - 1 of the head's D / 2: slot s is pair s of the rotated part, or values
+// 2 s, 2 s + 1 of the rest.
+template <int D, bool FP8>
+__global__ void __launch_bounds__(STEP_WARPS * 32) append_step_kernel(const __grid_constant__ AppendArgs A) {
+    constexpr int N = D / 64;
+    const int lane = threadIdx.x & 31, heads = A.hkv + (A.q ? A.hq : 0);
+    const int64_t w = (int64_t)blockIdx.x * STEP_WARPS + (threadIdx.x >> 5);
+    grid_wait();
+    if (w >= (int64_t)A.batch * heads) return;
+    const int b = (int)(w / heads), h = (int)(w - (int64_t)b * heads);
+    const bool is_q = h >= A.hkv;
+    const uint16_t* x = is_q ? A.q + b * A.q_tok + (h - A.hkv) * D : A.x[0] + b * A.x_tok[0] + h * D;
+    const int start = __ldg(A.start + b);
+    const int s0 = lane * N;
+    const bool rot = 2 * s0 < A.R.rot_dim, split = rot && !A.R.interleaved;
+    const int ca = split ? s0 : 2 * s0, cb = split ? s0 + A.R.rot_dim / 2 : 2 * s0 + N;   // the two groups of N values
+    uint16_t xa[N], xb[N];
+    uint16_t v[2 * N];
+    if constexpr (N == 2) {
+        const uint32_t a = *reinterpret_cast<const uint32_t*>(x + ca), c = *reinterpret_cast<const uint32_t*>(x + cb);
+        xa[0] = (uint16_t)a; xa[1] = (uint16_t)(a >> 16); xb[0] = (uint16_t)c; xb[1] = (uint16_t)(c >> 16);
+    } else {
+        xa[0] = x[ca]; xb[0] = x[cb];
+    }
+    if (!is_q) {
+        const uint16_t* y = A.x[1] + b * A.x_tok[1] + h * D + 2 * s0;
+        if constexpr (N == 2) {
+            const uint2 a = *reinterpret_cast<const uint2*>(y);
+            v[0] = (uint16_t)a.x; v[1] = (uint16_t)(a.x >> 16); v[2] = (uint16_t)a.y; v[3] = (uint16_t)(a.y >> 16);
+        } else {
+            const uint32_t a = *reinterpret_cast<const uint32_t*>(y);
+            v[0] = (uint16_t)a; v[1] = (uint16_t)(a >> 16);
+        }
+    }
+    unsigned long long freq[N];
+#pragma unroll
+    for (int i = 0; i < N; ++i) freq[i] = rot ? __ldg(A.R.freq + s0 + i) : 0ull;
+    // The page (and its scale) are fetched before the angles are computed.
+    const int at = start / A.page, row0 = start - at * A.page;
+    int p = -1;
+    bool bad = start < 0;
+    if (!is_q && !bad) {
+        if (at >= A.max_pages) bad = true; else p = __ldg(A.table + (int64_t)b * A.max_pages + at);
+    }
+    const bool good = !is_q && p >= 0 && p < A.n_pages;
+    float old[2] = {0.f, 0.f};
+    if (FP8 && good && row0 > 0) {
+        old[0] = A.scale[0][(int64_t)p * A.hkv + h];
+        old[1] = A.scale[1][(int64_t)p * A.hkv + h];
+    }
+    if (rot) {
+        float f[2 * N];            // xa, xb as they come: pair i is (xa[i], xb[i]), or neighbours where interleaved
+#pragma unroll
+        for (int i = 0; i < N; ++i) { f[i] = __uint_as_float((uint32_t)xa[i] << 16); f[N + i] = __uint_as_float((uint32_t)xb[i] << 16); }
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            float c, s;
+            rope_sincos(start, freq[i], A.R.amp, c, s);
+            const float u0 = A.R.interleaved ? f[2 * i] : f[i], v0 = A.R.interleaved ? f[2 * i + 1] : f[N + i];
+            const float nu = u0 * c - v0 * s, nv = u0 * s + v0 * c;
+            if (A.R.interleaved) { f[2 * i] = nu; f[2 * i + 1] = nv; } else { f[i] = nu; f[N + i] = nv; }
+        }
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            xa[i] = __bfloat16_as_ushort(__float2bfloat16_rn(f[i]));
+            xb[i] = __bfloat16_as_ushort(__float2bfloat16_rn(f[N + i]));
+        }
+    }
+    auto store = [&](uint16_t* o) {      // the rotated row of D values
+        if constexpr (N == 2) {
+            *reinterpret_cast<uint32_t*>(o + ca) = (uint32_t)xa[0] | (uint32_t)xa[1] << 16;
+            *reinterpret_cast<uint32_t*>(o + cb) = (uint32_t)xb[0] | (uint32_t)xb[1] << 16;
+        } else {
+            o[ca] = xa[0]; o[cb] = xb[0];
+        }
+    };
+    if (is_q) {
+        if (!bad) store(A.q_out + ((int64_t)b * A.hq + h - A.hkv) * D);
+        return;
+    }
+    if (!good) {
+        if (lane == 0 && h == 0) set_status(A.status, bad ? KVO_DEV_BAD_COUNT : KVO_DEV_BAD_BLOCK_ID);
+        return;
+    }
+    if (A.k_out) store(A.k_out + ((int64_t)b * A.hkv + h) * D);
+    const int64_t base = (((int64_t)p * A.hkv + h) * A.page + row0) * D;
+    if constexpr (!FP8) {
+        store(reinterpret_cast<uint16_t*>(A.pages[0]) + base);
+        uint16_t* o = reinterpret_cast<uint16_t*>(A.pages[1]) + base + 2 * s0;
+        if constexpr (N == 2)
+            *reinterpret_cast<uint2*>(o) = make_uint2((uint32_t)v[0] | (uint32_t)v[1] << 16, (uint32_t)v[2] | (uint32_t)v[3] << 16);
+        else
+            *reinterpret_cast<uint32_t*>(o) = (uint32_t)v[0] | (uint32_t)v[1] << 16;
+    } else {
+        float f[2][2 * N], top[2] = {0.f, 0.f}, inv[2];
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            f[0][i] = __uint_as_float((uint32_t)xa[i] << 16);
+            f[0][N + i] = __uint_as_float((uint32_t)xb[i] << 16);
+            f[1][2 * i] = __uint_as_float((uint32_t)v[2 * i] << 16);
+            f[1][2 * i + 1] = __uint_as_float((uint32_t)v[2 * i + 1] << 16);
+        }
+#pragma unroll
+        for (int y = 0; y < 2; ++y) {
+#pragma unroll
+            for (int i = 0; i < 2 * N; ++i)
+                if (fabsf(f[y][i]) < INFINITY) top[y] = fmaxf(top[y], fabsf(f[y][i]));
+#pragma unroll
+            for (int o = 16; o; o >>= 1) top[y] = fmaxf(top[y], __shfl_xor_sync(0xffffffffu, top[y], o));
+            float s = e4m3_scale(top[y]);
+            if (row0 > 0) {
+                s = fmaxf(s, old[y]);
+                if (s != old[y])
+                    rescale_rows(A.pages[y] + ((int64_t)p * A.hkv + h) * A.page * D, row0 * (D / 16), old[y] / s, lane, 32);
+            }
+            if (lane == 0) A.scale[y][(int64_t)p * A.hkv + h] = s;
+            inv[y] = 1.f / s;
+#pragma unroll
+            for (int i = 0; i < 2 * N; ++i) f[y][i] = fabsf(f[y][i]) < INFINITY ? f[y][i] * inv[y] : NAN;
+        }
+        uint8_t* o = A.pages[0] + base;
+        uint8_t* ov = A.pages[1] + base + 2 * s0;
+        if constexpr (N == 2) {
+            *reinterpret_cast<uint16_t*>(o + ca) = f32x2_to_e4m3x2(f[0][0], f[0][1]);
+            *reinterpret_cast<uint16_t*>(o + cb) = f32x2_to_e4m3x2(f[0][2], f[0][3]);
+            *reinterpret_cast<uint32_t*>(ov) = (uint32_t)f32x2_to_e4m3x2(f[1][0], f[1][1]) | (uint32_t)f32x2_to_e4m3x2(f[1][2], f[1][3]) << 16;
+        } else {
+            const uint16_t two = f32x2_to_e4m3x2(f[0][0], f[0][1]);
+            o[ca] = (uint8_t)two;
+            o[cb] = (uint8_t)(two >> 8);
+            *reinterpret_cast<uint16_t*>(ov) = f32x2_to_e4m3x2(f[1][0], f[1][1]);
+        }
+    }
 }
 
 int rope_heads_per_thread(int64_t n, int heads);
@@ -297,31 +467,43 @@ extern "C" kvo_status kvo_paged_append(const kvo_paged_cache* cache, const void*
     A.n_pages = cache->n_pages;
     A.max_pages = cache->max_pages;
     A.R = RopeArgs{(const unsigned long long*)freq, freq ? rot_dim : 0, interleaved ? 1 : 0, amplitude};
-    const int64_t units = cu ? tokens / cache->page_size + 2 * (int64_t)cache->batch : cache->batch;
-    A.units = (int)units;
-    int64_t blocks = units * hkv;
-    if (q) {
-        const int64_t n = tokens * (D / 16);
-        A.q_per = rope_heads_per_thread(n, n_q_heads);
-        blocks += (n + APP_THREADS - 1) / APP_THREADS * ((n_q_heads + A.q_per - 1) / A.q_per);
-    }
-    if (blocks > INT32_MAX) return bad("too many tokens");
     const bool fp8 = cache->format == KVO_PAGES_E4M3;
-    // rows x 16-value units of a page over 256 threads; without cu a page takes one row
-    const int per_page = (cu ? cache->page_size : 1) * (D / 16);
-    const int maxu = per_page <= APP_THREADS ? 1 : per_page <= 2 * APP_THREADS ? 2 : 4;
     cudaStream_t s = (cudaStream_t)stream;
     cudaError_t e;
-#define KVO_APPEND(D_, F_, U_) e = launch_dependent(append_pages_kernel<D_, F_, U_>, dim3((unsigned)blocks), APP_THREADS, 0, s, 0, A)
-#define KVO_APPEND_U(D_, F_)                                                                  \
-    do {                                                                                      \
-        if (maxu == 1) KVO_APPEND(D_, F_, 1); else if (maxu == 2) KVO_APPEND(D_, F_, 2);      \
-        else KVO_APPEND(D_, F_, 4);                                                           \
-    } while (0)
-    if (D == 128) { if (fp8) KVO_APPEND_U(128, true); else KVO_APPEND_U(128, false); }
-    else { if (fp8) KVO_APPEND_U(64, true); else KVO_APPEND_U(64, false); }
-#undef KVO_APPEND_U
+    if (!cu) {
+        const int64_t warps = (int64_t)cache->batch * (hkv + (q ? n_q_heads : 0)), blocks = (warps + STEP_WARPS - 1) / STEP_WARPS;
+        if (blocks > INT32_MAX) return bad("too many tokens");
+        const dim3 grid((unsigned)blocks);
+        const int nt = STEP_WARPS * 32;
+        if (D == 128) e = fp8 ? launch_dependent(append_step_kernel<128, true>, grid, nt, 0, s, 0, A) : launch_dependent(append_step_kernel<128, false>, grid, nt, 0, s, 0, A);
+        else e = fp8 ? launch_dependent(append_step_kernel<64, true>, grid, nt, 0, s, 0, A) : launch_dependent(append_step_kernel<64, false>, grid, nt, 0, s, 0, A);
+    } else {
+        const int64_t units = tokens / cache->page_size + 2 * (int64_t)cache->batch;
+        if (units * hkv > INT32_MAX / 2) return bad("too many tokens");
+        A.units = (int)units;
+        A.kv_blocks = A.blocks = units * hkv;
+        // 16-value units of a page over 64 to 256 threads, 1, 2 or 4 to a thread
+        const int per_page = cache->page_size * (D / 16);
+        const int nt = std::min(APP_THREADS, per_page);
+        const int maxu = (per_page + nt - 1) / nt;
+        if (q) {
+            const int64_t n = tokens * (D / 16);
+            A.q_per = rope_heads_per_thread(n, n_q_heads);
+            A.blocks += (n + nt - 1) / nt * ((n_q_heads + A.q_per - 1) / A.q_per);
+        }
+        if (A.blocks > INT32_MAX) return bad("too many tokens");
+        const dim3 grid((unsigned)A.blocks);
+#define KVO_APPEND(D_, F_, U_) e = launch_dependent(append_pages_kernel<D_, F_, U_>, grid, nt, 0, s, 0, A)
+        if (D == 128) {
+            if (maxu == 1) { if (fp8) KVO_APPEND(128, true, 1); else KVO_APPEND(128, false, 1); }
+            else if (maxu == 2) { if (fp8) KVO_APPEND(128, true, 2); else KVO_APPEND(128, false, 2); }
+            else { if (fp8) KVO_APPEND(128, true, 4); else KVO_APPEND(128, false, 4); }
+        } else {
+            if (maxu == 1) { if (fp8) KVO_APPEND(64, true, 1); else KVO_APPEND(64, false, 1); }
+            else { if (fp8) KVO_APPEND(64, true, 2); else KVO_APPEND(64, false, 2); }
+        }
 #undef KVO_APPEND
+    }
     if (e != cudaSuccess) { set_last_error(cudaGetErrorString(e)); return KVO_ERR_CUDA; }
     return KVO_OK;
 }
