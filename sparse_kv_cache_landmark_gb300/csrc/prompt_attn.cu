@@ -90,6 +90,12 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
     return r;
 }
 
+__device__ __forceinline__ void st_global_32(void* p, const uint32_t (&w)[8]) {
+    asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(p), "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3]),
+                 "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+                 : "memory");
+}
+
 struct PrShared {
     uint64_t q_full, kv_full[12], s_full[2][6], p_full[2][2], o_done[2], turn[2], drain[2], v_tail;
     uint32_t tmem;
@@ -213,17 +219,17 @@ __device__ __forceinline__ void pr_softmax(PrShared& sh, const PromptArgs& A, in
         }
         if (real) {
 #pragma unroll
-            for (int i = 0; i < 32; i += 8) {
-                uint32_t w[4];
+            for (int i = 0; i < 32; i += 16) {
+                uint32_t w[8];
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
+                for (int e = 0; e < 8; ++e) {
                     // a row that saw nothing is zero, whatever its lane of tensor memory holds
                     const float x = l != 0.f ? __uint_as_float(o[i + 2 * e]) * inv : 0.f;
                     const float y = l != 0.f ? __uint_as_float(o[i + 2 * e + 1]) * inv : 0.f;
                     const __nv_bfloat162 v = __floats2bfloat162_rn(x, y);
                     w[e] = *reinterpret_cast<const uint32_t*>(&v);
                 }
-                *reinterpret_cast<uint4*>(A.o + out_row * D + c + i) = make_uint4(w[0], w[1], w[2], w[3]);
+                st_global_32(A.o + out_row * D + c + i, w);      // whole sectors: a thread's row is its own
             }
         }
     }
@@ -240,35 +246,12 @@ prompt_attn_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int TU = 2 * A.tq;
 
-    grid_wait();
-    if (blockIdx.x == 0 && A.status)           // bad offsets of any request, also of one that no item reaches
-        for (int i = tid; i < A.batch; i += PR_THREADS) {
-            const int64_t a = A.cu_q[i], e = A.cu_q[i + 1], c = A.cu_k[i], f = A.cu_k[i + 1];
-            if (a < 0 || e < a || e > A.total_q || c < 0 || f < c || f > A.total_k) atomicOr(A.status, KVO_DEV_BAD_COUNT);
-        }
-
-    // Request b has ceil(nq / TU) items; its slots start at floor(cu_q[b] / TU) + b, which leaves room for them.
-    const int g = blockIdx.x % A.hkv, u = A.units - 1 - (int)(blockIdx.x / A.hkv);
-    auto first = [&](int i) { return (int64_t)max(__ldg(A.cu_q + i), 0) / TU + i; };
-    const int b = warp_find(A.batch, u, first);
-    const int64_t j0 = u - first(b);
-    const int64_t qs = A.cu_q[b], qe = A.cu_q[b + 1], ks = A.cu_k[b], ke = A.cu_k[b + 1];
-    if (qs < 0 || qe < qs || qe > A.total_q || ks < 0 || ke < ks || ke > A.total_k) return;
-    const int nq = (int)(qe - qs), nk = (int)(ke - ks);
-    if (j0 < 0 || j0 * TU >= nq) return;
-    const int tok0 = (int)j0 * TU;
-    int n_t[2];
-#pragma unroll
-    for (int t = 0; t < 2; ++t) {
-        const int have = min(max(nq - tok0 - t * A.tq, 0), A.tq);
-        const int64_t see = A.causal ? min(max((int64_t)tok0 + t * A.tq + have + (nk - nq), (int64_t)0), (int64_t)nk) : nk;
-        n_t[t] = have ? (int)((see + PR_KEYS - 1) / PR_KEYS) : 0;
-    }
-    const int n = max(n_t[0], n_t[1]);
-
     const uint32_t base = (smem_u32(smem_raw) + 1023u) & ~1023u;
     const uint32_t ring = base + 2 * P::TILE;
-    if (tid == 0) {
+    if (warp == 9 && lane == 0) {                 // the loading thread sets up the barriers: its first loads need no other
+        tensor_map_prefetch(&map_q);
+        tensor_map_prefetch(&map_k);
+        tensor_map_prefetch(&map_v);
         mbar_init(smem_u32(&sh.q_full), 1);
         for (int i = 0; i < P::STAGES; ++i) mbar_init(smem_u32(&sh.kv_full[i]), 1);
         for (int t = 0; t < 2; ++t) {
@@ -283,6 +266,61 @@ prompt_attn_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
         sh.abort = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
+    grid_wait();
+    if (blockIdx.x == 0 && A.status)           // bad offsets of any request, also of one that no item reaches
+        for (int i = tid; i < A.batch; i += PR_THREADS) {
+            const int64_t a = A.cu_q[i], e = A.cu_q[i + 1], c = A.cu_k[i], f = A.cu_k[i + 1];
+            if (a < 0 || e < a || e > A.total_q || c < 0 || f < c || f > A.total_k) atomicOr(A.status, KVO_DEV_BAD_COUNT);
+        }
+
+    // Request b has ceil(nq / TU) items; its slots start at floor(cu_q[b] / TU) + b, which leaves room for them.
+    const int g = blockIdx.x % A.hkv, u = A.units - 1 - (int)(blockIdx.x / A.hkv);
+    int64_t j0, qs, qe, ks, ke;
+    if (A.batch <= 32) {                       // all offsets in one round of loads
+        const bool have = lane < A.batch;
+        const int a = have ? __ldg(A.cu_q + lane) : 0, e = have ? __ldg(A.cu_q + lane + 1) : 0;
+        const int c = have ? __ldg(A.cu_k + lane) : 0, f = have ? __ldg(A.cu_k + lane + 1) : 0;
+        const int64_t first = (int64_t)max(a, 0) / TU + lane;
+        const int b = max(0, 31 - __clz((int)__ballot_sync(0xffffffffu, have && first <= u)));
+        j0 = u - __shfl_sync(0xffffffffu, first, b);
+        qs = __shfl_sync(0xffffffffu, a, b);
+        qe = __shfl_sync(0xffffffffu, e, b);
+        ks = __shfl_sync(0xffffffffu, c, b);
+        ke = __shfl_sync(0xffffffffu, f, b);
+    } else {
+        auto first = [&](int i) { return (int64_t)max(__ldg(A.cu_q + i), 0) / TU + i; };
+        const int b = warp_find(A.batch, u, first);
+        j0 = u - first(b);
+        qs = A.cu_q[b];
+        qe = A.cu_q[b + 1];
+        ks = A.cu_k[b];
+        ke = A.cu_k[b + 1];
+    }
+    if (qs < 0 || qe < qs || qe > A.total_q || ks < 0 || ke < ks || ke > A.total_k) return;
+    const int nq = (int)(qe - qs), nk = (int)(ke - ks);
+    if (j0 < 0 || j0 * TU >= nq) return;
+    const int tok0 = (int)j0 * TU;
+    int n_t[2];
+#pragma unroll
+    for (int t = 0; t < 2; ++t) {
+        const int have = min(max(nq - tok0 - t * A.tq, 0), A.tq);
+        const int64_t see = A.causal ? min(max((int64_t)tok0 + t * A.tq + have + (nk - nq), (int64_t)0), (int64_t)nk) : nk;
+        n_t[t] = have ? (int)((see + PR_KEYS - 1) / PR_KEYS) : 0;
+    }
+    const int n = max(n_t[0], n_t[1]);
+
+    if (warp == 9 && lane == 0 && n > 0) {     // Q and the first keys
+        const int tiles = n_t[1] > 0 ? 2 : 1;
+        mbar_expect_tx(smem_u32(&sh.kv_full[0]), P::TILE);
+        for (int x = 0; x < D / 64; ++x)
+            tma_load_3d(ring + x * PR_BLOCK, &map_k, 64 * x, g, (int)ks, smem_u32(&sh.kv_full[0]));
+        mbar_expect_tx(smem_u32(&sh.q_full), (uint32_t)(tiles * (D / 64) * 128 * A.r * A.tq));
+        for (int t = 0; t < tiles; ++t)
+            for (int x = 0; x < D / 64; ++x)
+                tma_load_3d(base + t * P::TILE + x * PR_BLOCK, &map_q, 64 * x, g * A.r, (int)qs + tok0 + t * A.tq,
+                            smem_u32(&sh.q_full));
+    }
+    __syncwarp();
     if (warp == 8) tmem_alloc(smem_u32(&sh.tmem), 512);
     tc_fence_before();
     __syncthreads();
@@ -292,17 +330,9 @@ prompt_attn_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
         regs_dec<88>();
         if (warp == 9 && n > 0) {
             // ------------------------------------------------ loads
-            int issued = 0;
+            int issued = 1;
             bool ok = true;
-            if (lane == 0) {
-                const int tiles = n_t[1] > 0 ? 2 : 1;
-                mbar_expect_tx(smem_u32(&sh.q_full), (uint32_t)(tiles * (D / 64) * 128 * A.r * A.tq));
-                for (int t = 0; t < tiles; ++t)
-                    for (int x = 0; x < D / 64; ++x)
-                        tma_load_3d(base + t * P::TILE + x * PR_BLOCK, &map_q, 64 * x, g * A.r,
-                                    (int)qs + tok0 + t * A.tq, smem_u32(&sh.q_full));
-            }
-            for (int i = 0; i < 2 * n; ++i) {
+            for (int i = 1; i < 2 * n; ++i) {
                 const int st = i % P::STAGES, jj = i >> 1, key0 = jj * PR_KEYS;
                 const bool is_v = i & 1;
                 if (i >= P::STAGES) {
@@ -451,7 +481,8 @@ extern "C" kvo_status kvo_prompt_attn(const void* q, int64_t q_token_stride, con
     if (batch == 0 || total_q == 0) return KVO_OK;
     if (!q || !o || !cu_q || !cu_k || (total_k > 0 && (!k || !v))) return bad("null pointer argument");
     for (const void* p : {q, k, v, (const void*)o})
-        if ((uintptr_t)p % 16) return bad("q, k, v and o must be 16-byte aligned");
+        if ((uintptr_t)p % 16) return bad("q, k, v and o must be 16-byte aligned (o: 32)");
+    if ((uintptr_t)o % 32) return bad("o must be 32-byte aligned");
     if (q_token_stride % 8 || k_token_stride % 8 || v_token_stride % 8) return bad("strides must be multiples of 8 elements");
     if (q_token_stride < (int64_t)n_q_heads * head_dim || k_token_stride < (int64_t)n_kv_heads * head_dim ||
         v_token_stride < (int64_t)n_kv_heads * head_dim)

@@ -48,6 +48,9 @@ inline bool tensor_map_rows(CUtensorMap* m, const void* base, int elem, int d, u
     return tensor_map(m, base, elem, 2, sizes, strides, box);
 }
 
+__device__ __forceinline__ void tensor_map_prefetch(const CUtensorMap* map) {
+    asm volatile("prefetch.tensormap [%0];" ::"l"(map) : "memory");
+}
 __device__ __forceinline__ void tma_load_2d(uint32_t dst, const CUtensorMap* map, int x, int y, uint32_t mbar) {
     asm volatile(
         "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::"r"(
