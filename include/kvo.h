@@ -600,8 +600,8 @@ kvo_status kvo_paged_attn_workspace(const kvo_paged_cache* cache, int n_q_heads,
  *   .. cu_k[b + 1] - 1; either may be empty.  causal: query token i sees the
  *   keys t <= i + (keys - queries), i.e. the last token sees them all (a chunk
  *   of a prompt behind cached keys has more keys than queries); 0: every key.
- *   o: bf16 [total_q][n_q_heads][head_dim], contiguous, 32-byte aligned; lse
- *   (optional): fp32 [total_q][n_q_heads], natural log.  Softmax scale 1/sqrt(head_dim), fp32
+ *   o: bf16 [total_q][n_q_heads][head_dim], contiguous; lse (optional): fp32
+ *   [total_q][n_q_heads], natural log.  Softmax scale 1/sqrt(head_dim), fp32
  *   accumulation, weights rounded to bf16, o rounded once to bf16.  A row that
  *   sees no key gets o = 0, lse = -inf; rows outside every request keep their
  *   bytes.  One request's values never reach another's rows; within a request a

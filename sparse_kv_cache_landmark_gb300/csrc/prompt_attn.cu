@@ -90,14 +90,8 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
     return r;
 }
 
-__device__ __forceinline__ void st_global_32(void* p, const uint32_t (&w)[8]) {
-    asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(p), "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3]),
-                 "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
-                 : "memory");
-}
-
 struct PrShared {
-    uint64_t q_full, kv_full[12], s_full[2][6], p_full[2][2], o_done[2], turn[2], drain[2], v_tail;
+    uint64_t q_full[2], kv_full[12], s_full[2][6], p_full[2][2], o_done[2], turn[2], drain[2], v_tail;
     uint32_t tmem;
     int abort;
 };
@@ -124,7 +118,7 @@ __device__ __forceinline__ bool pr_wait(PrShared& sh, const PromptArgs& A, uint6
 // The softmax of one tile: a thread owns row `row` of it; the row sees its request's keys [0, limit).
 template <int D>
 __device__ __forceinline__ void pr_softmax(PrShared& sh, const PromptArgs& A, int t, int n_tiles, int limit, bool real,
-                                           int64_t out_row) {
+                                           int64_t out_row, uint8_t* q_smem) {
     const uint32_t lanes = (uint32_t)(threadIdx.x & 96) << 16;          // this warp's quarter of the lanes
     const uint32_t S = sh.tmem + 128 * t + lanes, O = sh.tmem + 256 + D * t + lanes;
     float m = -INFINITY, l = 0.f;                                       // log2 units; l in units of 2^m
@@ -206,7 +200,13 @@ __device__ __forceinline__ void pr_softmax(PrShared& sh, const PromptArgs& A, in
         tc_fence_after();
     }
     if (!ok) return;
+    // The row goes through this warp's part of Q's memory (its tile's products are done), so that the warp writes
+    // whole rows: 32 threads with a row each would touch 32 lines a store.  16-byte chunks, turned by the row against
+    // bank conflicts.
     const float inv = l != 0.f ? 1.f / l : 0.f;
+    const int lane = threadIdx.x & 31;
+    constexpr int CH = D / 8;                                           // chunks of a row
+    uint8_t* rows = q_smem + (threadIdx.x & 96) * (2 * D);
 #pragma unroll 1
     for (int c = 0; c < D; c += 32) {
         uint32_t o[32];
@@ -217,21 +217,28 @@ __device__ __forceinline__ void pr_softmax(PrShared& sh, const PromptArgs& A, in
 #pragma unroll
             for (int i = 0; i < 32; ++i) o[i] = 0u;
         }
-        if (real) {
 #pragma unroll
-            for (int i = 0; i < 32; i += 16) {
-                uint32_t w[8];
+        for (int i = 0; i < 32; i += 8) {
+            uint32_t w[4];
 #pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    // a row that saw nothing is zero, whatever its lane of tensor memory holds
-                    const float x = l != 0.f ? __uint_as_float(o[i + 2 * e]) * inv : 0.f;
-                    const float y = l != 0.f ? __uint_as_float(o[i + 2 * e + 1]) * inv : 0.f;
-                    const __nv_bfloat162 v = __floats2bfloat162_rn(x, y);
-                    w[e] = *reinterpret_cast<const uint32_t*>(&v);
-                }
-                st_global_32(A.o + out_row * D + c + i, w);      // whole sectors: a thread's row is its own
+            for (int e = 0; e < 4; ++e) {
+                // a row that saw nothing is zero, whatever its lane of tensor memory holds
+                const float x = l != 0.f ? __uint_as_float(o[i + 2 * e]) * inv : 0.f;
+                const float y = l != 0.f ? __uint_as_float(o[i + 2 * e + 1]) * inv : 0.f;
+                const __nv_bfloat162 v = __floats2bfloat162_rn(x, y);
+                w[e] = *reinterpret_cast<const uint32_t*>(&v);
             }
+            const int ch = ((c + i) / 8) ^ (lane & 7);
+            *reinterpret_cast<uint4*>(rows + lane * (2 * D) + ch * 16) = make_uint4(w[0], w[1], w[2], w[3]);
         }
+    }
+    __syncwarp();
+#pragma unroll
+    for (int i = 0; i < CH; ++i) {                                      // 32 / CH rows at a time
+        const int row = i * (32 / CH) + lane / CH, ch = lane % CH;
+        const long long to = __shfl_sync(0xffffffffu, real ? (long long)out_row : -1ll, row);
+        const uint4 v = *reinterpret_cast<const uint4*>(rows + row * (2 * D) + (ch ^ (row & 7)) * 16);
+        if (to >= 0) *reinterpret_cast<uint4*>(A.o + to * D + ch * 8) = v;
     }
     if (real && A.lse) A.lse[out_row] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
 }
@@ -252,9 +259,9 @@ prompt_attn_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
         tensor_map_prefetch(&map_q);
         tensor_map_prefetch(&map_k);
         tensor_map_prefetch(&map_v);
-        mbar_init(smem_u32(&sh.q_full), 1);
         for (int i = 0; i < P::STAGES; ++i) mbar_init(smem_u32(&sh.kv_full[i]), 1);
         for (int t = 0; t < 2; ++t) {
+            mbar_init(smem_u32(&sh.q_full[t]), 1);
             for (int i = 0; i < P::DEPTH; ++i) mbar_init(smem_u32(&sh.s_full[t][i]), 1);
             mbar_init(smem_u32(&sh.p_full[t][0]), 128);
             mbar_init(smem_u32(&sh.p_full[t][1]), 128);
@@ -310,15 +317,16 @@ prompt_attn_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
     const int n = max(n_t[0], n_t[1]);
 
     if (warp == 9 && lane == 0 && n > 0) {     // Q and the first keys
-        const int tiles = n_t[1] > 0 ? 2 : 1;
         mbar_expect_tx(smem_u32(&sh.kv_full[0]), P::TILE);
         for (int x = 0; x < D / 64; ++x)
             tma_load_3d(ring + x * PR_BLOCK, &map_k, 64 * x, g, (int)ks, smem_u32(&sh.kv_full[0]));
-        mbar_expect_tx(smem_u32(&sh.q_full), (uint32_t)(tiles * (D / 64) * 128 * A.r * A.tq));
-        for (int t = 0; t < tiles; ++t)
+        for (int t = 0; t < 2; ++t) {
+            if (n_t[t] == 0) continue;         // a tile that sees no key: nothing reads its Q
+            mbar_expect_tx(smem_u32(&sh.q_full[t]), (uint32_t)((D / 64) * 128 * A.r * A.tq));
             for (int x = 0; x < D / 64; ++x)
                 tma_load_3d(base + t * P::TILE + x * PR_BLOCK, &map_q, 64 * x, g * A.r, (int)qs + tok0 + t * A.tq,
-                            smem_u32(&sh.q_full));
+                            smem_u32(&sh.q_full[t]));
+        }
     }
     __syncwarp();
     if (warp == 8) tmem_alloc(smem_u32(&sh.tmem), 512);
@@ -370,7 +378,8 @@ prompt_attn_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
             }
             // After a wait that ran out: let every copy in flight land before the CTA may leave.
             if (*(volatile int*)&sh.abort && lane == 0) {
-                mbar_wait_bounded(smem_u32(&sh.q_full), 0, A.wait_ns);
+                for (int t = 0; t < 2; ++t)
+                    if (n_t[t] > 0) mbar_wait_bounded(smem_u32(&sh.q_full[t]), 0, A.wait_ns);
                 for (int i = max(0, issued - P::STAGES); i < issued; ++i)
                     mbar_wait_bounded(smem_u32(&sh.kv_full[i % P::STAGES]), (i / P::STAGES) & 1, A.wait_ns);
                 if (issued < 2 * n && (issued & 1)) mbar_wait_bounded(smem_u32(&sh.v_tail), 0, A.wait_ns / 4);
@@ -397,7 +406,7 @@ prompt_attn_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
             };
             int ks = 0, vs = 1;                      // stages of K and V, and the parities of their next fill
             uint32_t kp = 0, vp = 0;
-            bool ok = pr_wait(sh, A, sh.q_full, 0) && pr_wait(sh, A, sh.kv_full[0], 0);
+            bool ok = pr_wait(sh, A, sh.q_full[t], 0) && pr_wait(sh, A, sh.kv_full[0], 0);
             if (ok) scores(0, false);
             for (int j = 0; ok && j < n_mine; ++j) {
                 ks += 2;
@@ -441,7 +450,8 @@ prompt_attn_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
         const bool real = tl < A.tq && tok < nq;
         int limit = 0;
         if (real) limit = A.causal ? (int)min(max((int64_t)tok + 1 + (nk - nq), (int64_t)0), (int64_t)nk) : nk;
-        pr_softmax<D>(sh, A, t, n_t[t], limit, real, (qs + tok) * A.hq + g * A.r + head);
+        pr_softmax<D>(sh, A, t, n_t[t], limit, real, (qs + tok) * A.hq + g * A.r + head,
+                      smem_raw + (base - smem_u32(smem_raw)) + t * P::TILE);
     }
     tc_fence_before();
     __syncthreads();
@@ -481,8 +491,7 @@ extern "C" kvo_status kvo_prompt_attn(const void* q, int64_t q_token_stride, con
     if (batch == 0 || total_q == 0) return KVO_OK;
     if (!q || !o || !cu_q || !cu_k || (total_k > 0 && (!k || !v))) return bad("null pointer argument");
     for (const void* p : {q, k, v, (const void*)o})
-        if ((uintptr_t)p % 16) return bad("q, k, v and o must be 16-byte aligned (o: 32)");
-    if ((uintptr_t)o % 32) return bad("o must be 32-byte aligned");
+        if ((uintptr_t)p % 16) return bad("q, k, v and o must be 16-byte aligned");
     if (q_token_stride % 8 || k_token_stride % 8 || v_token_stride % 8) return bad("strides must be multiples of 8 elements");
     if (q_token_stride < (int64_t)n_q_heads * head_dim || k_token_stride < (int64_t)n_kv_heads * head_dim ||
         v_token_stride < (int64_t)n_kv_heads * head_dim)
