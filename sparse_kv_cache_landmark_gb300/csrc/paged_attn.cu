@@ -47,8 +47,7 @@ namespace kvo {
 constexpr int PA_WARPS = 4;
 constexpr int PA_THREADS = PA_WARPS * 32;
 constexpr int PA_SUB = 16;                    // tokens of a subtile (one k step of the value product, and of a TMA box)
-constexpr int PA_RING = 96 * 1024;            // bytes of stages per CTA
-constexpr int PA_PER_SM = 2;                  // CTAs per SM: 96 KB of stages each
+constexpr int PA_RING = 64 * 1024;            // bytes of stages per CTA
 constexpr float PA_RAISE = 8.f;               // log2: how far a score may pass the running maximum
 constexpr float PA_BIAS = 6.f;                // log2: weights are held times 2^6 (f16's small end is 2^-24)
 
@@ -57,7 +56,7 @@ struct PaShape {
     static constexpr int RB = FP8 ? D : 2 * D;               // bytes of a row
     static constexpr int BOX = RB > 128 ? 128 : RB;          // bytes of a box row
     static constexpr int NBOX = RB / BOX;
-    static constexpr int SUBS = RB > 128 ? 1 : 2;            // subtiles of a tile (8 KB a stage at most)
+    static constexpr int SUBS = 256 / RB;                    // subtiles of a tile: 8 KB a stage
     static constexpr int TILE = SUBS * PA_SUB;               // tokens of a tile
     static constexpr int TILE_BYTES = TILE * RB;             // K or V of one tile
     static constexpr int STAGE = 2 * TILE_BYTES;
@@ -65,6 +64,7 @@ struct PaShape {
     static constexpr int KCH = RB / 64;                      // 16-byte chunks of a key row per lane
     static constexpr int STEPS = D / 16;                     // k steps of k . q
     static constexpr int MT = D / 16;                        // m tiles of v^T p
+    static constexpr int CHAINS = SUBS > 2 ? 1 : 2;          // accumulators a subtile's scores alternate between
 };
 
 struct PagedAttnArgs {
@@ -76,9 +76,9 @@ struct PagedAttnArgs {
     const int32_t* counts;        // [G] or NULL: n_blocks each
     uint16_t* o;
     float* lse;
-    float* part_o;                // [2 ctas][r][D]
-    float4* part_ml;              // [2 ctas][r]: maximum, sum, sum of the rounded weights
-    int2* info;                   // [G]: first and last CTA of a group cut by range borders; x < 0: not cut
+    float* part_o;                // [2 warps][r][D]
+    float4* part_ml;              // [2 warps][r]: maximum, sum, sum of the rounded weights
+    int2* info;                   // [G]: first slot and last warp of a group cut by range borders; x < 0: not cut
     int32_t* status;
     int batch, hkv, r, page, shift, n_pages, max_pages, n_blocks, G;
     float scale_log2;
@@ -145,23 +145,25 @@ struct PaState {
     float vs;                              // the value scale that o is held in
 };
 
-// Scores and values of one tile; nv[s] of subtile s's 16 tokens are real (all: nv_all).
-template <int D, bool FP8, int NH>
+// Scores and values of one tile; nv[s] of subtile s's 16 tokens are real (FULL: all of them).
+template <int D, bool FP8, int NH, bool FULL>
 __device__ __forceinline__ void pa_tile(PaState<D, FP8, NH>& T, const uint32_t (&qf)[PaShape<D, FP8>::STEPS][NH][2],
                                         const float (&qs)[NH][2], const uint8_t* ksm, const uint8_t* vsm,
                                         const float (&kscale)[PaShape<D, FP8>::SUBS],
                                         const float (&vscale)[PaShape<D, FP8>::SUBS],
-                                        const int (&nv)[PaShape<D, FP8>::SUBS], bool all) {
+                                        const int (&nv)[PaShape<D, FP8>::SUBS]) {
     using S = PaShape<D, FP8>;
     constexpr int BOXROWS = S::TILE * 128;
     const int lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
-    float sc[S::SUBS][NH][2][4];                             // two chains each, so that products follow closer
+    float sc[S::SUBS][NH][S::CHAINS][4];
 #pragma unroll
     for (int u = 0; u < S::SUBS; ++u)
 #pragma unroll
         for (int x = 0; x < NH; ++x)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) sc[u][x][0][e] = sc[u][x][1][e] = 0.f;
+            for (int e = 0; e < 4; ++e)
+#pragma unroll
+                for (int k = 0; k < S::CHAINS; ++k) sc[u][x][k][e] = 0.f;
 #pragma unroll
     for (int m = 0; m < S::KCH; ++m)
 #pragma unroll
@@ -187,7 +189,7 @@ __device__ __forceinline__ void pa_tile(PaState<D, FP8, NH>& T, const uint32_t (
                 }
 #pragma unroll
                 for (int x = 0; x < NH; ++x)
-                    mma16816<FP8>(sc[u][x][s & 1], a, qf[PER * m + s][x][0], qf[PER * m + s][x][1]);
+                    mma16816<FP8>(sc[u][x][s & (S::CHAINS - 1)], a, qf[PER * m + s][x][0], qf[PER * m + s][x][1]);
             }
         }
     float mx[NH][2];
@@ -199,9 +201,10 @@ __device__ __forceinline__ void pa_tile(PaState<D, FP8, NH>& T, const uint32_t (
 #pragma unroll
             for (int u = 0; u < S::SUBS; ++u) {
                 const float f = qs[x][e] * kscale[u];
-                sc[u][x][0][e] = (sc[u][x][0][e] + sc[u][x][1][e]) * f;
-                sc[u][x][0][e + 2] = (sc[u][x][0][e + 2] + sc[u][x][1][e + 2]) * f;
-                if (!all) {
+                constexpr int L = S::CHAINS - 1;
+                sc[u][x][0][e] = (L ? sc[u][x][0][e] + sc[u][x][L][e] : sc[u][x][0][e]) * f;
+                sc[u][x][0][e + 2] = (L ? sc[u][x][0][e + 2] + sc[u][x][L][e + 2] : sc[u][x][0][e + 2]) * f;
+                if (!FULL) {
                     if (g >= nv[u]) sc[u][x][0][e] = -INFINITY;
                     if (g + 8 >= nv[u]) sc[u][x][0][e + 2] = -INFINITY;
                 }
@@ -230,7 +233,8 @@ __device__ __forceinline__ void pa_tile(PaState<D, FP8, NH>& T, const uint32_t (
     float fold[S::SUBS];           // what a weight is multiplied by so that o stays in units of T.vs
     if (FP8) {
         float top = vscale[0];
-        if (S::SUBS > 1) top = fmaxf(top, vscale[S::SUBS - 1]);
+#pragma unroll
+        for (int u = 1; u < S::SUBS; ++u) top = fmaxf(top, vscale[u]);
         if (top > T.vs) {          // uniform over the warp
             const float f = T.vs / top;
             T.vs = top;
@@ -286,7 +290,7 @@ __device__ __forceinline__ void pa_tile(PaState<D, FP8, NH>& T, const uint32_t (
                     const uint2 v = *reinterpret_cast<const uint2*>(vsm + tr * 64 + ((((g >> 1) ^ ((tr >> 1) & 3)) << 4) | ((g & 1) << 3)));
                     w[k][0] = v.x; w[k][1] = v.y;
                 }
-                if (!all && tr - 16 * u >= nv[u])            // what lies behind the end may be NaN: 0 * NaN must not reach o
+                if (!FULL && tr - 16 * u >= nv[u])            // what lies behind the end may be NaN: 0 * NaN must not reach o
 #pragma unroll
                     for (int i = 0; i < VW; ++i) w[k][i] = 0u;
             }
@@ -324,17 +328,16 @@ __device__ __forceinline__ int pa_col(int q, int g) {
     return (q >> 3) * 64 + g * 8 + (q & 7);
 }
 
-// What one lane knows of a batch of 32 pages of the segment: page, scales, tokens.
+// What one lane knows of a page of its group: its entry of the table, which is not looked at before the page is
+// needed (so that the load of a batch ahead holds nobody up), and its real tokens (0: nothing to read).
 struct PaPage {
-    int row;          // first row of the page in the pool seen as [n_pages * Hkv * page] rows; < 0: skip
-    int tokens;       // real tokens of the page
-    float ks, vs;
+    int entry, tokens;
 };
 
-__device__ __forceinline__ PaPage pa_page(const PagedAttnArgs& A, int g, int i, int len, int n_logical) {
-    PaPage P{-1, 0, 0.f, 0.f};
-    if (i >= n_logical) return P;
-    const int b = g / A.hkv, h = g - b * A.hkv;
+__device__ __forceinline__ PaPage pa_page(const PagedAttnArgs& A, int g, int i) {
+    PaPage P{0, 0};
+    if (g >= A.G || i >= (pa_span(A, g) + A.page - 1) >> A.shift) return P;
+    const int b = g / A.hkv;
     int logical = i;
     if (A.blocks) {
         logical = __ldg(A.blocks + (int64_t)g * A.n_blocks + i);
@@ -343,25 +346,26 @@ __device__ __forceinline__ PaPage pa_page(const PagedAttnArgs& A, int g, int i, 
             return P;
         }
     }
-    P.tokens = min(A.page, len - logical * A.page);
-    if (P.tokens <= 0) return P;
-    const int page = __ldg(A.table + (int64_t)b * A.max_pages + logical);
-    if (page < 0 || page >= A.n_pages) {
-        if (A.status) atomicOr(A.status, KVO_DEV_BAD_BLOCK_ID);
-        P.tokens = 0;
-        return P;
-    }
-    P.row = (page * A.hkv + h) * A.page;
-    if (A.scale[0]) {
-        P.ks = __ldg(A.scale[0] + (int64_t)page * A.hkv + h);
-        P.vs = __ldg(A.scale[1] + (int64_t)page * A.hkv + h);
-    } else {
-        P.ks = P.vs = 1.f;
-    }
+    P.tokens = max(min(A.page, pa_len(A, b) - logical * A.page), 0);
+    if (P.tokens > 0) P.entry = __ldg(A.table + (int64_t)b * A.max_pages + logical);
     return P;
 }
 
-__device__ __forceinline__ void fence_async() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
+// Kept beside a stage: the group of the tile in it and that group's tiles, and its subtiles' scales and real tokens.
+template <int SUBS>
+struct PaInfo {
+    float ks[SUBS], vs[SUBS];
+    int nv[SUBS], g, n;
+};
+
+// Copies 4 bytes to shared memory; mbar gets the thread's arrival once its copies before have landed.
+__device__ __forceinline__ void copy4(void* dst, const float* src) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
+}
+__device__ __forceinline__ void arrive_copied(uint32_t mbar) {
+    asm volatile("cp.async.mbarrier.arrive.noinc.shared.b64 [%0];" ::"r"(mbar) : "memory");
+}
+__device__ __forceinline__ void prefetch_l1(const void* p) { asm volatile("prefetch.global.L1 [%0];" ::"l"(p)); }
 
 __device__ __forceinline__ void pa_store(const PagedAttnArgs& A, int64_t row, int d, int col, float acc, float m, float l,
                                          float lw) {
@@ -369,55 +373,366 @@ __device__ __forceinline__ void pa_store(const PagedAttnArgs& A, int64_t row, in
     if (col == 0) A.lse[row] = l == 0.f ? -INFINITY : (m + log2f(l) - PA_BIAS) * 0.6931471805599453f;
 }
 
-// CLU: one thread-block cluster per group splits the group's tiles and joins its CTAs' states through distributed
-// shared memory.  Else: equal ranges of all groups' tiles, parts joined by the second kernel.
-template <int D, bool FP8, int NH, bool CLU>
-__global__ void __launch_bounds__(PA_THREADS, PA_PER_SM)
-paged_attn_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v,
-                  const __grid_constant__ PagedAttnArgs A) {
+// Query fragments of group g: heads 8 x + lane / 4 as columns (heads beyond r: zero), and the scores' factors of the
+// lane's heads 8 x + 2c, 8 x + 2c + 1.
+template <int D, bool FP8, int NH>
+__device__ __forceinline__ void pa_query(const PagedAttnArgs& A, int g, uint32_t (&qf)[PaShape<D, FP8>::STEPS][NH][2],
+                                         float (&qs)[NH][2]) {
+    using S = PaShape<D, FP8>;
+    const int lane = threadIdx.x & 31, gr = lane >> 2, c = lane & 3;
+    const uint16_t* qg = A.q + (int64_t)g * A.r * D;
+#pragma unroll
+    for (int x = 0; x < NH; ++x) {
+        const int head = gr + 8 * x;
+        float amax = 0.f;
+#pragma unroll
+        for (int m = 0; m < S::KCH; ++m) {
+            constexpr int ES = FP8 ? 1 : 2, PER = FP8 ? 4 : 2;
+            const int box = S::BOX == 128 ? m >> 1 : 0, ch = S::BOX == 128 ? 2 * c + (m & 1) : c;
+            const int e0 = box * (128 / ES) + ch * (16 / ES);
+#pragma unroll
+            for (int s = 0; s < PER; ++s)
+#pragma unroll
+                for (int k = 0; k < 2; ++k) {
+                    const uint32_t v = head < A.r ? *reinterpret_cast<const uint32_t*>(qg + head * D + e0 + 4 * s + 2 * k) : 0u;
+                    qf[PER * m + s][x][k] = v;
+                    amax = fmaxf(amax, fmaxf(fabsf(bf16lo_to_f32(v)), fabsf(bf16hi_to_f32(v))));
+                }
+        }
+        float scale = A.scale_log2;
+        if (FP8) {
+            amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
+            amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
+            // row / 2^(e - 8): the largest value is in [2^8, 2^9)
+            const int e = min(max((int)(__float_as_uint(amax) >> 23) - 127, -110), 126);
+            const float f = __uint_as_float((uint32_t)(8 - e + 127) << 23);
+            scale = A.scale_log2 * __uint_as_float((uint32_t)(e - 8 + 127) << 23);
+#pragma unroll
+            for (int s = 0; s < S::STEPS; ++s)
+#pragma unroll
+                for (int k = 0; k < 2; ++k) {
+                    const uint32_t v = qf[s][x][k];
+                    qf[s][x][k] = pack_f16(bf16lo_to_f32(v) * f, bf16hi_to_f32(v) * f);
+                }
+        }
+        // head 8 x + h's scale sits in lanes 4 h ..
+        qs[x][0] = __shfl_sync(0xffffffffu, scale, 8 * c);
+        qs[x][1] = __shfl_sync(0xffffffffu, scale, 8 * c + 4);
+    }
+}
+
+// One warp attends to `count` tiles in a row, from tile t0 of group g0 on and, unless ONE, through the groups after it.
+// The copies run STAGES tiles ahead, across groups.  finish(T, g, its tiles, first, count) takes each group's state.
+// Returns whether every wait was met; every copy issued has landed in any case.
+template <int D, bool FP8, int NH, bool ONE, typename F>
+__device__ __forceinline__ bool pa_run(const PagedAttnArgs& A, const CUtensorMap* map_k, const CUtensorMap* map_v,
+                                       uint32_t ring, const uint8_t* ring_p, uint32_t bar,
+                                       PaInfo<PaShape<D, FP8>::SUBS>* info, int g0, int t0, long long count, F&& finish) {
+    using S = PaShape<D, FP8>;
+    const int lane = threadIdx.x & 31;
+    // Pages come in batches of 32, one per lane; the next batch, of this group or of the one after, is fetched while
+    // this one is used.
+    int bg = g0, base = (t0 * S::TILE) >> A.shift, ng = bg, nbase = base;
+    auto next_batch = [&]() {
+        nbase += 32;
+        if ((nbase << A.shift) < pa_span(A, ng)) return pa_page(A, ng, nbase + lane);
+        if constexpr (ONE) {
+            return PaPage{0, 0};
+        } else {
+            do ++ng; while (ng < A.G && pa_span(A, ng) <= 0);
+            nbase = 0;
+            return pa_page(A, ng, lane);
+        }
+    };
+    int page, tokens;              // of this lane's page of the batch in use; -1: the table's entry is out of range
+    auto use = [&](const PaPage& P) {
+        const bool bad = P.tokens > 0 && (P.entry < 0 || P.entry >= A.n_pages);
+        page = bad ? -1 : P.entry;
+        tokens = bad ? 0 : P.tokens;
+        if (bad && A.status) atomicOr(A.status, KVO_DEV_BAD_BLOCK_ID);
+    };
+    use(pa_page(A, bg, base + lane));
+    PaPage nxt{0, 0};
+    bool fetched = false;          // nxt is the batch at (ng, nbase)
+    // the next tile to issue: its group, that group's KV head and tiles
+    int ig = g0, ih = g0 % A.hkv, it = t0, in = (pa_span(A, g0) + S::TILE - 1) / S::TILE;
+    int st_in = 0;
+    long long issued = 0;
+    auto issue = [&]() {
+        if (!ONE && it >= in) {
+            do in = (pa_span(A, ++ig) + S::TILE - 1) / S::TILE; while (in <= 0);   // the count ends before the groups do
+            it = 0;
+            ih = ig % A.hkv;
+            // its queries are wanted in a moment
+            for (int i = lane * 64; i < A.r * D; i += 32 * 64) prefetch_l1(A.q + (int64_t)ig * A.r * D + i);
+        }
+        const int tok = it * S::TILE, pg = tok >> A.shift;
+        if (ig != bg || pg - base >= 32) {
+            if (!fetched) nxt = next_batch();
+            bg = ng;
+            base = nbase;
+            use(nxt);
+            nxt = next_batch();
+            fetched = true;
+        }
+        // lane u takes subtile u
+        const int mine = tok + (lane & (S::SUBS - 1)) * PA_SUB, my_pg = mine >> A.shift, k = (my_pg - base) & 31;
+        const int off = mine - (my_pg << A.shift);
+        const int my_page = __shfl_sync(0xffffffffu, page, k);
+        const int nv = min(max(__shfl_sync(0xffffffffu, tokens, k) - off, 0), PA_SUB);
+        const uint32_t b = bar + 8 * st_in, dst = ring + st_in * S::STAGE;
+        const uint32_t have = __ballot_sync(0xffffffffu, lane < S::SUBS && nv > 0);
+        if (lane < S::SUBS) info[st_in].nv[lane] = nv;
+        if (lane == 0) {
+            info[st_in].g = ig;
+            info[st_in].n = in;
+            if (have) mbar_expect_tx(b, __popc(have) * (S::STAGE / S::SUBS));
+        }
+        __syncwarp();
+        if (have >> lane & 1) {
+            const int slot = my_page * A.hkv + ih, row = slot * A.page + off;
+#pragma unroll
+            for (int x = 0; x < S::NBOX; ++x) {
+                const uint32_t at = dst + x * (S::TILE * 128) + lane * (PA_SUB * S::BOX);
+                tma_load_2d(at, map_k, x * (128 / (FP8 ? 1 : 2)), row, b);
+                tma_load_2d(at + S::TILE_BYTES, map_v, x * (128 / (FP8 ? 1 : 2)), row, b);
+            }
+            if (FP8) {
+                copy4(&info[st_in].ks[lane], A.scale[0] + slot);
+                copy4(&info[st_in].vs[lane], A.scale[1] + slot);
+            }
+        } else if (lane < S::SUBS) {
+            info[st_in].ks[lane] = info[st_in].vs[lane] = 0.f;
+        }
+        if (FP8 && have && lane < S::SUBS) arrive_copied(b);
+        if (++st_in == S::STAGES) st_in = 0;
+        ++it;
+        ++issued;
+    };
+    while (issued < min(count, (long long)S::STAGES)) issue();
+    if (!fetched) {
+        nxt = next_batch();
+        fetched = true;
+    }
+
+    uint32_t qf[S::STEPS][NH][2];
+    float qs[NH][2];
+    PaState<D, FP8, NH> T;
+    auto begin = [&](int g) {
+        pa_query<D, FP8, NH>(A, g, qf, qs);
+#pragma unroll
+        for (int x = 0; x < NH; ++x) {
+#pragma unroll
+            for (int j = 0; j < S::MT; ++j) T.o[j][x][0] = T.o[j][x][1] = T.o[j][x][2] = T.o[j][x][3] = 0.f;
+            T.m[x][0] = T.m[x][1] = -INFINITY;
+            T.l[x][0] = T.l[x][1] = T.lw[x][0] = T.lw[x][1] = 0.f;
+        }
+        T.vs = 0.f;
+    };
+    int cg = g0, cn = 0, first = t0, done = 0, st = 0;
+    uint32_t phase = 0;            // bit i: parity of stage i's next wait
+    bool dead = false;
+    begin(cg);
+    // Every copy issued is waited for, also after a wait that ran out: none may land once the CTA has left.
+    for (long long c = 0; c < issued; ++c) {
+        const PaInfo<S::SUBS>& I = info[st];
+        if (!ONE && I.g != cg) {
+            finish(T, cg, cn, first, done);
+            cg = I.g;
+            first = done = 0;
+            begin(cg);
+        }
+        cn = I.n;
+        int nv[S::SUBS];
+        bool some = false, all = true;
+#pragma unroll
+        for (int u = 0; u < S::SUBS; ++u) {
+            nv[u] = I.nv[u];
+            some |= nv[u] > 0;
+            all &= nv[u] == PA_SUB;
+        }
+        if (some) {
+            if (!mbar_wait_bounded(bar + 8 * st, (phase >> st) & 1, A.wait_ns)) dead = true;
+            phase ^= 1u << st;
+            float ks[S::SUBS], vs[S::SUBS];
+#pragma unroll
+            for (int u = 0; u < S::SUBS; ++u) {
+                ks[u] = FP8 ? I.ks[u] : 1.f;
+                vs[u] = FP8 ? I.vs[u] : 1.f;
+            }
+            const uint8_t* tile = ring_p + st * S::STAGE;
+            if (dead) {
+            } else if (all) {
+                pa_tile<D, FP8, NH, true>(T, qf, qs, tile, tile + S::TILE_BYTES, ks, vs, nv);
+            } else {
+                pa_tile<D, FP8, NH, false>(T, qf, qs, tile, tile + S::TILE_BYTES, ks, vs, nv);
+            }
+        }
+        if (++st == S::STAGES) st = 0;
+        ++done;
+        dead = __any_sync(0xffffffffu, dead);
+        if (issued < count && !dead) issue();
+    }
+    if (dead && lane == 0 && A.status) atomicOr(A.status, KVO_DEV_TIMEOUT);
+    finish(T, cg, cn, first, done);
+    return !dead;
+}
+
+// The sums of a state over the warp's token lanes.
+template <int D, bool FP8, int NH>
+__device__ __forceinline__ void pa_sum(const PaState<D, FP8, NH>& T, int x, int e, float& l, float& lw) {
+    l = T.l[x][e];
+    lw = FP8 ? 0.f : T.lw[x][e];
+#pragma unroll
+    for (int o = 4; o < 32; o <<= 1) {
+        l += __shfl_xor_sync(0xffffffffu, l, o);
+        if (!FP8) lw += __shfl_xor_sync(0xffffffffu, lw, o);
+    }
+    if (FP8) lw = l;
+}
+
+// The shared memory of both kernels: stages, what is kept beside them, and their barriers.
+template <int D, bool FP8>
+struct PaShared {
+    uint64_t bars[PA_WARPS][PaShape<D, FP8>::STAGES];
+    PaInfo<PaShape<D, FP8>::SUBS> info[PA_WARPS][PaShape<D, FP8>::STAGES];
+};
+template <int D, bool FP8>
+__device__ __forceinline__ void pa_init(PaShared<D, FP8>& sh) {
+    const int warp = threadIdx.x >> 5;
+    // a stage is full with its tiles and, in e4m3, each subtile's scales
+    if ((threadIdx.x & 31) == 0)
+        for (int i = 0; i < PaShape<D, FP8>::STAGES; ++i)
+            mbar_init(smem_u32(&sh.bars[warp][i]), FP8 ? 1 + PaShape<D, FP8>::SUBS : 1);
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    __syncwarp();
+}
+
+// One thread-block cluster per group: its warps split the group's tiles, and the states are joined through shared
+// memory, then through distributed shared memory.
+template <int D, bool FP8, int NH>
+__global__ void __launch_bounds__(PA_THREADS, NH == 1 ? 3 : 2)
+paged_cluster_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v,
+                     const __grid_constant__ PagedAttnArgs A) {
     using S = PaShape<D, FP8>;
     extern __shared__ uint8_t smem_raw[];
-    __shared__ __align__(8) uint64_t bars[PA_WARPS * S::STAGES];
-    __shared__ long long s_pre, s_scan[PA_WARPS];
-    __shared__ int s_g, s_dead;
+    __shared__ PaShared<D, FP8> sh;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const uint32_t ring = (smem_u32(smem_raw) + 1023u) & ~1023u;
     uint8_t* ring_p = smem_raw + (ring - smem_u32(smem_raw));
-    // Outside a segment's copies the ring's memory also holds the warps' states, [4][r][D + 4], and the CTA's, [r][D + 4].
+    // After the copies the ring's memory holds the warps' states, [4][r][D + 4], and the CTA's, [r][D + 4].
     float* mrg = reinterpret_cast<float*>(ring_p);
     float* cl = reinterpret_cast<float*>(ring_p + 48 * 1024);
     constexpr int MS = D + 4;
-    const uint32_t wring = ring + warp * S::STAGES * S::STAGE;
-    const uint8_t* wring_p = ring_p + warp * S::STAGES * S::STAGE;
-    const uint32_t wbar = smem_u32(bars) + warp * S::STAGES * 8;
-    if (lane == 0)
-        for (int i = 0; i < S::STAGES; ++i) mbar_init(wbar + 8 * i, 1);
-    if (tid == 0) s_dead = 0;
-    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
-    auto tiles_of = [&](int g) { return (pa_span(A, g) + S::TILE - 1) / S::TILE; };
-
+    pa_init(sh);
     grid_wait();
-    long long total = 0, n_cta = 1, lo = 0, hi = 0, gpre = 0;
-    int g = 0;
-    if constexpr (CLU) {
-        const uint32_t rank = cluster_rank(), size = cluster_size();
-        g = blockIdx.x / size;
-        const int n = tiles_of(g);
-        lo = (long long)n * rank / size;
-        hi = (long long)n * (rank + 1) / size;
-        if (tid == 0 && rank == 0) pa_check_counts(A, g);
-        __syncthreads();
-    } else {
-    // this CTA's range of the tiles of all groups
-    const int per = (A.G + PA_THREADS - 1) / PA_THREADS;
-    long long sum = 0;
-    for (int i = 0; i < per; ++i) {
-        const int g = tid * per + i;
-        if (g >= A.G) break;
-        sum += tiles_of(g);
-        if (blockIdx.x == 0) pa_check_counts(A, g);
+    const uint32_t rank = cluster_rank(), size = cluster_size();
+    const int g = blockIdx.x / size, n = (pa_span(A, g) + S::TILE - 1) / S::TILE;
+    if (tid == 0 && rank == 0) pa_check_counts(A, g);
+    const long long parts = (long long)PA_WARPS * size, me = (long long)rank * PA_WARPS + warp;
+    const int t0 = (int)(n * me / parts), t1 = (int)(n * (me + 1) / parts);
+    const int ws = warp * S::STAGES * S::STAGE;
+    pa_run<D, FP8, NH, true>(A, &map_k, &map_v, ring + ws, ring_p + ws, smem_u32(sh.bars[warp]), sh.info[warp], g, t0, t1 - t0,
+                             [&](PaState<D, FP8, NH>& T, int, int, int, int) {
+        __syncthreads();           // the ring is free
+        const int gr = lane >> 2, c = lane & 3;
+#pragma unroll
+        for (int x = 0; x < NH; ++x)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                float l, lw;
+                pa_sum(T, x, e, l, lw);
+                const int head = 8 * x + 2 * c + e;
+                if (head < A.r) {
+                    float* dst = mrg + (warp * A.r + head) * MS;
+                    if (gr == 0) { dst[D] = T.m[x][e]; dst[D + 1] = l; dst[D + 2] = lw; dst[D + 3] = FP8 ? T.vs : 1.f; }
+#pragma unroll
+                    for (int j = 0; j < S::MT; ++j) {
+                        dst[pa_col<D, FP8>(2 * j, gr)] = T.o[j][x][e];
+                        dst[pa_col<D, FP8>(2 * j + 1, gr)] = T.o[j][x][e + 2];
+                    }
+                }
+            }
+    });
+    __syncthreads();
+    for (int i = tid; i < A.r * D; i += PA_THREADS) {
+        const int row = i / D, col = i - row * D;
+        float m = -INFINITY;
+#pragma unroll
+        for (int w = 0; w < PA_WARPS; ++w) m = fmaxf(m, mrg[(w * A.r + row) * MS + D]);
+        float acc = 0.f, l = 0.f, lw = 0.f;
+#pragma unroll
+        for (int w = 0; w < PA_WARPS; ++w) {
+            const float* src = mrg + (w * A.r + row) * MS;
+            if (src[D + 1] == 0.f) continue;
+            const float f = ex2(src[D] - m);
+            l += f * src[D + 1];
+            lw += f * src[D + 2];
+            acc += f * src[D + 3] * src[col];
+        }
+        float* dst = cl + row * MS;
+        dst[col] = acc;
+        if (col == 0) { dst[D] = m; dst[D + 1] = l; dst[D + 2] = lw; }
     }
-    // inclusive prefix over the CTA: shuffles within a warp, the warps' totals through shared memory
+    cluster_barrier();
+    for (int i = tid + rank * PA_THREADS; i < A.r * D; i += PA_THREADS * size) {
+        const int row = i / D, col = i - row * D;
+        const float* src = cl + row * MS;
+        float m = -INFINITY, acc = 0.f, l = 0.f, lw = 0.f;
+        for (uint32_t k0 = 0; k0 < size; k0 += 8) {          // eight CTAs' loads in flight
+            float mk[8], lk[8], wk[8], ok[8];
+#pragma unroll
+            for (int i8 = 0; i8 < 8; ++i8) {
+                const uint32_t k = min(k0 + i8, size - 1);
+                mk[i8] = ld_cluster_f32(src + D, k);
+                lk[i8] = ld_cluster_f32(src + D + 1, k);
+                wk[i8] = ld_cluster_f32(src + D + 2, k);
+                ok[i8] = ld_cluster_f32(src + col, k);
+            }
+            float to = m;
+#pragma unroll
+            for (int i8 = 0; i8 < 8; ++i8) to = fmaxf(to, mk[i8]);
+            const float f0 = l == 0.f ? 0.f : ex2(m - to);
+            m = to;
+            l *= f0; lw *= f0; acc *= f0;
+#pragma unroll
+            for (int i8 = 0; i8 < 8; ++i8)
+                if (k0 + i8 < size && lk[i8] != 0.f) {
+                    const float f = ex2(mk[i8] - m);
+                    l += f * lk[i8]; lw += f * wk[i8]; acc += f * ok[i8];
+                }
+        }
+        pa_store(A, (int64_t)g * A.r + row, D, col, acc, m, l, lw);
+    }
+    cluster_barrier();             // nobody leaves while its states are read
+}
+
+// Equal ranges of all groups' tiles, one per warp.
+template <int D, bool FP8, int NH>
+__global__ void __launch_bounds__(PA_THREADS, 2)
+paged_range_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v,
+                   const __grid_constant__ PagedAttnArgs A) {
+    using S = PaShape<D, FP8>;
+    extern __shared__ uint8_t smem_raw[];
+    __shared__ PaShared<D, FP8> sh;
+    __shared__ long long s_scan[PA_WARPS], s_pre[PA_WARPS];
+    __shared__ int s_g[PA_WARPS];
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const uint32_t ring = (smem_u32(smem_raw) + 1023u) & ~1023u;
+    const uint8_t* ring_p = smem_raw + (ring - smem_u32(smem_raw));
+    auto tiles_of = [&](int g) { return (pa_span(A, g) + S::TILE - 1) / S::TILE; };
+    pa_init(sh);
+    grid_wait();
+    // Prefix of the tiles over the CTA, by requests, or by groups where each has a list of its own: each thread's
+    // share, then shuffles within a warp, then the warps' totals through shared memory.
+    const int heads = A.blocks ? 1 : A.hkv, units = A.G / heads, per = (units + PA_THREADS - 1) / PA_THREADS;
+    long long sum = 0, total = 0;
+    for (int i = 0; i < per; ++i) {
+        const int u = tid * per + i;
+        if (u >= units) break;
+        sum += (long long)heads * tiles_of(u * heads);
+        if (blockIdx.x == 0) pa_check_counts(A, u * heads);
+    }
     long long inc = sum;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -432,348 +747,181 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_consta
         total += s_scan[w];
     }
     const long long pre = inc - sum;
-    n_cta = max(1ll, min((long long)gridDim.x, total));                      // a tile for each, so every range holds work
-    lo = blockIdx.x < n_cta ? total * blockIdx.x / n_cta : total;
-    hi = blockIdx.x < n_cta ? total * (blockIdx.x + 1) / n_cta : total;
-    if (lo >= pre && lo < pre + sum) {
-        long long at = pre;
-        for (int i = 0; i < per; ++i) {
-            const int k = tid * per + i;
-            const int n = k < A.G ? tiles_of(k) : 0;
-            if (lo < at + n) { s_g = k; s_pre = at; break; }
-            at += n;
+    // two tiles at least to a warp, at most 512 parts to join for a group, and warps spread over the CTAs before they
+    // fill them
+    const long long n_warp = max(1ll, min(min((long long)gridDim.x * PA_WARPS, 512ll * A.G), total / 2));
+    auto start = [&](long long w) { return w < n_warp ? total * w / n_warp : total; };
+#pragma unroll
+    for (int w = 0; w < PA_WARPS; ++w) {
+        const long long lo = start((long long)w * gridDim.x + blockIdx.x);
+        if (lo >= pre && lo < pre + sum) {
+            long long at = pre;
+            for (int i = 0; i < per; ++i) {
+                const int u = tid * per + i, n = u < units ? tiles_of(u * heads) : 0;
+                if (lo < at + (long long)n * heads) {
+                    const int h = (int)((lo - at) / n);
+                    s_g[w] = u * heads + h;
+                    s_pre[w] = at + (long long)h * n;
+                    break;
+                }
+                at += (long long)n * heads;
+            }
         }
     }
     __syncthreads();
-    // groups with nothing to attend to
-    for (int k = blockIdx.x; k < A.G; k += gridDim.x)
-        if (tiles_of(k) == 0) {
-            for (int i = tid; i < A.r * D; i += PA_THREADS) A.o[(int64_t)k * A.r * D + i] = 0;
-            for (int i = tid; i < A.r; i += PA_THREADS) A.lse[(int64_t)k * A.r + i] = -INFINITY;
-            if (tid == 0) A.info[k] = make_int2(-1, -1);
-        }
     grid_launch_next();            // the join's CTAs may take their places; they wait for this grid's end
+    // groups with nothing to attend to
+    for (int g = blockIdx.x; g < A.G; g += gridDim.x)
+        if (tiles_of(g) == 0) {
+            for (int i = tid; i < A.r * D; i += PA_THREADS) A.o[(int64_t)g * A.r * D + i] = 0;
+            for (int i = tid; i < A.r; i += PA_THREADS) A.lse[(int64_t)g * A.r + i] = -INFINITY;
+            if (tid == 0) A.info[g] = make_int2(-1, -1);
+        }
+    const long long me = (long long)warp * gridDim.x + blockIdx.x, lo = start(me), hi = start(me + 1);
     if (lo >= hi) return;
-    g = s_g;
-    gpre = s_pre;
-    }
-
-    uint32_t phase = 0;            // bit i: parity of stage i's next wait
-    long long cur = lo;
+    long long before = s_pre[warp];    // tiles of the groups before the one being finished
     int seg = 0;
-    bool dead = false;
-    while (CLU || cur < hi) {      // a cluster's CTA has one segment, empty or not
-        const int n = tiles_of(g);
-        if (!CLU && cur >= gpre + n) { gpre += n; ++g; continue; }
-        const int t0 = (int)(cur - gpre), t1 = CLU ? (int)hi : (int)min((long long)n, hi - gpre);
-        const int len = pa_len(A, g / A.hkv);
-        const int n_logical = (pa_span(A, g) + A.page - 1) >> A.shift;
-        // this warp's tiles
-        const int w0 = t0 + (int)((long long)(t1 - t0) * warp / PA_WARPS);
-        const int w1 = t0 + (int)((long long)(t1 - t0) * (warp + 1) / PA_WARPS);
-
-        // tiles w0..w1: pages come in batches of 32, one per lane; the next batch is loaded while this one is used
-        int base = (w0 * S::TILE) >> A.shift;
-        PaPage cur_p = pa_page(A, g, base + lane, len, n_logical), nxt_p = pa_page(A, g, base + 32 + lane, len, n_logical);
-        int issued = w0;
-        // first row in the pool of the subtile at token t of the span, and its real tokens (up to a batch ahead)
-        auto find = [&](int t, int& row, int& tok) {
-            const int pg = t >> A.shift, k = pg - base, off = t - (pg << A.shift);
-            row = __shfl_sync(0xffffffffu, k < 32 ? cur_p.row : nxt_p.row, k & 31) + off;
-            tok = __shfl_sync(0xffffffffu, k < 32 ? cur_p.tokens : nxt_p.tokens, k & 31) - off;
-        };
-        const bool wide = A.page >= S::TILE;                 // a tile lies within one page
-        int st_in = 0, st_out = 0; // stages of the next tile to issue and to use
-        auto issue = [&](int t) {  // copies of tile t into its stage: each subtile that has tokens
-            const uint32_t bar = wbar + 8 * st_in, dst = wring + st_in * S::STAGE;
-            if (++st_in == S::STAGES) st_in = 0;
-            int row[S::SUBS], tok[S::SUBS];
-            find(t * S::TILE, row[0], tok[0]);
-            if (S::SUBS > 1) {
-                row[S::SUBS - 1] = row[0] + PA_SUB;
-                tok[S::SUBS - 1] = tok[0] - PA_SUB;
-                if (!wide) find(t * S::TILE + PA_SUB, row[S::SUBS - 1], tok[S::SUBS - 1]);
-            }
-            if (lane == 0) {
-                int n_sub = 0;
+    const int ws = warp * S::STAGES * S::STAGE;
+    pa_run<D, FP8, NH, false>(A, &map_k, &map_v, ring + ws, ring_p + ws, smem_u32(sh.bars[warp]), sh.info[warp], s_g[warp],
+                              (int)(lo - before), hi - lo, [&](PaState<D, FP8, NH>& T, int g, int n, int first, int done) {
+        const bool whole = done == n;
+        const long long slot = 2 * me + (seg ? 1 : 0);
+        const int gr = lane >> 2, c = lane & 3;
 #pragma unroll
-                for (int u = 0; u < S::SUBS; ++u) n_sub += tok[u] > 0;
-                if (n_sub) mbar_expect_tx(bar, n_sub * (S::STAGE / S::SUBS));
+        for (int x = 0; x < NH; ++x)
 #pragma unroll
-                for (int u = 0; u < S::SUBS; ++u)
-                    if (tok[u] > 0) {
+            for (int e = 0; e < 2; ++e) {
+                float l, lw;
+                pa_sum(T, x, e, l, lw);
+                const int head = 8 * x + 2 * c + e;
+                if (head >= A.r) continue;
+                const float m = T.m[x][e];
+                const int64_t row = whole ? (int64_t)g * A.r + head : slot * A.r + head;
+                // the lane's columns are runs of 8 places of the order of pa_tile
+                const float f = whole ? (lw != 0.f ? (FP8 ? T.vs : 1.f) / lw : 0.f) : FP8 ? T.vs : 1.f;
 #pragma unroll
-                        for (int x = 0; x < S::NBOX; ++x) {
-                            const uint32_t at = dst + x * (S::TILE * 128) + u * (PA_SUB * S::BOX);
-                            tma_load_2d(at, &map_k, x * (128 / (FP8 ? 1 : 2)), row[u], bar);
-                            tma_load_2d(at + S::TILE_BYTES, &map_v, x * (128 / (FP8 ? 1 : 2)), row[u], bar);
-                        }
-                    }
-            }
-        };
-        for (; issued < min(w1, w0 + S::STAGES);) issue(issued++);
-
-        // query fragments: heads 8 x + lane / 4 of the group as columns (heads beyond r: zero)
-        uint32_t qf[S::STEPS][NH][2];
-        float qs[NH][2];
-        {
-            const int gr = lane >> 2, c = lane & 3;
-            const uint16_t* qg = A.q + (int64_t)g * A.r * D;
+                for (int q = 0; q < 2 * S::MT; q += 8) {
+                    float v[8];
 #pragma unroll
-            for (int x = 0; x < NH; ++x) {
-                const int head = gr + 8 * x;
-                float amax = 0.f;
+                    for (int i = 0; i < 4; ++i) { v[2 * i] = T.o[q / 2 + i][x][e] * f; v[2 * i + 1] = T.o[q / 2 + i][x][e + 2] * f; }
+                    const int64_t at = row * D + pa_col<D, FP8>(q, gr);
+                    if (whole) {
+                        uint32_t w[4];
 #pragma unroll
-                for (int m = 0; m < S::KCH; ++m) {
-                    constexpr int ES = FP8 ? 1 : 2, PER = FP8 ? 4 : 2;
-                    const int box = S::BOX == 128 ? m >> 1 : 0, ch = S::BOX == 128 ? 2 * c + (m & 1) : c;
-                    const int e0 = box * (128 / ES) + ch * (16 / ES);
-#pragma unroll
-                    for (int s = 0; s < PER; ++s)
-#pragma unroll
-                        for (int k = 0; k < 2; ++k) {
-                            const uint32_t v = head < A.r ? *reinterpret_cast<const uint32_t*>(qg + head * D + e0 + 4 * s + 2 * k) : 0u;
-                            qf[PER * m + s][x][k] = v;
-                            amax = fmaxf(amax, fmaxf(fabsf(bf16lo_to_f32(v)), fabsf(bf16hi_to_f32(v))));
-                        }
-                }
-                float scale = A.scale_log2;
-                if (FP8) {
-                    amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
-                    amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
-                    // row / 2^(e - 8): the largest value is in [2^8, 2^9)
-                    const int e = min(max((int)(__float_as_uint(amax) >> 23) - 127, -110), 126);
-                    const float f = __uint_as_float((uint32_t)(8 - e + 127) << 23);
-                    scale = A.scale_log2 * __uint_as_float((uint32_t)(e - 8 + 127) << 23);
-#pragma unroll
-                    for (int s = 0; s < S::STEPS; ++s)
-#pragma unroll
-                        for (int k = 0; k < 2; ++k) {
-                            const uint32_t v = qf[s][x][k];
-                            qf[s][x][k] = pack_f16(bf16lo_to_f32(v) * f, bf16hi_to_f32(v) * f);
-                        }
-                }
-                // head 8 x + h's scale sits in lanes 4 h ..: this lane needs heads 2c and 2c + 1
-                qs[x][0] = __shfl_sync(0xffffffffu, scale, 8 * c);
-                qs[x][1] = __shfl_sync(0xffffffffu, scale, 8 * c + 4);
-            }
-        }
-        PaState<D, FP8, NH> T;
-#pragma unroll
-        for (int x = 0; x < NH; ++x) {
-#pragma unroll
-            for (int j = 0; j < S::MT; ++j) T.o[j][x][0] = T.o[j][x][1] = T.o[j][x][2] = T.o[j][x][3] = 0.f;
-            T.m[x][0] = T.m[x][1] = -INFINITY;
-            T.l[x][0] = T.l[x][1] = T.lw[x][0] = T.lw[x][1] = 0.f;
-        }
-        T.vs = 0.f;
-
-        // Every copy issued is waited for, also after a wait that ran out: none may land once the CTA has left.
-        for (int t = w0; t < issued; ++t) {
-            const int pg = (t * S::TILE) >> A.shift;
-            if (pg - base >= 32) {
-                base += 32;
-                cur_p = nxt_p;
-                nxt_p = pa_page(A, g, base + 32 + lane, len, n_logical);
-            }
-            float ks[S::SUBS], vs[S::SUBS];
-            int nv[S::SUBS];
-            const int k = pg - base, off = t * S::TILE - (pg << A.shift);
-            const int tok = __shfl_sync(0xffffffffu, cur_p.tokens, k) - off;
-            nv[0] = min(PA_SUB, tok);
-            ks[0] = __shfl_sync(0xffffffffu, cur_p.ks, k);
-            vs[0] = __shfl_sync(0xffffffffu, cur_p.vs, k);
-            if (S::SUBS > 1) {
-                constexpr int U = S::SUBS - 1;
-                nv[U] = min(PA_SUB, tok - PA_SUB);
-                ks[U] = ks[0];
-                vs[U] = vs[0];
-                if (!wide) {       // pages of 16 tokens: the next page, of the same batch (tiles start at even pages)
-                    nv[U] = __shfl_sync(0xffffffffu, cur_p.tokens, (k + 1) & 31);
-                    ks[U] = __shfl_sync(0xffffffffu, cur_p.ks, (k + 1) & 31);
-                    vs[U] = __shfl_sync(0xffffffffu, cur_p.vs, (k + 1) & 31);
-                }
-            }
-            const bool some = nv[0] > 0 || nv[S::SUBS - 1] > 0, all = nv[0] == PA_SUB && nv[S::SUBS - 1] == PA_SUB;
-            const int st = st_out;
-            if (++st_out == S::STAGES) st_out = 0;
-            if (some) {
-                if (!mbar_wait_bounded(wbar + 8 * st, (phase >> st) & 1, A.wait_ns)) dead = true;
-                phase ^= 1u << st;
-                if (!dead)
-                    pa_tile<D, FP8, NH>(T, qf, qs, wring_p + st * S::STAGE, wring_p + st * S::STAGE + S::TILE_BYTES, ks, vs, nv, all);
-            }
-            dead = __any_sync(0xffffffffu, dead);
-            if (issued < w1 && !dead) issue(issued++);
-        }
-        if (dead && lane == 0) {   // a copy never came: say so, and leave once every thread knows
-            if (A.status) atomicOr(A.status, KVO_DEV_TIMEOUT);
-            s_dead = 1;
-        }
-        __syncthreads();           // the ring is free
-        if (!CLU && s_dead) return;
-        // the warps' states
-        {
-            const int gr = lane >> 2, c = lane & 3;
-#pragma unroll
-            for (int x = 0; x < NH; ++x)
-#pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    float l = T.l[x][e], lw = FP8 ? l : T.lw[x][e];
-#pragma unroll
-                    for (int o = 4; o < 32; o <<= 1) {
-                        l += __shfl_xor_sync(0xffffffffu, l, o);
-                        if (!FP8) lw += __shfl_xor_sync(0xffffffffu, lw, o);
-                    }
-                    if (FP8) lw = l;
-                    const int head = 8 * x + 2 * c + e;
-                    if (head < A.r) {
-                        float* dst = mrg + (warp * A.r + head) * MS;
-                        if (gr == 0) { dst[D] = T.m[x][e]; dst[D + 1] = l; dst[D + 2] = lw; dst[D + 3] = FP8 ? T.vs : 1.f; }
-#pragma unroll
-                        for (int j = 0; j < S::MT; ++j) {
-                            dst[pa_col<D, FP8>(2 * j, gr)] = T.o[j][x][e];
-                            dst[pa_col<D, FP8>(2 * j + 1, gr)] = T.o[j][x][e + 2];
-                        }
+                        for (int i = 0; i < 4; ++i) w[i] = lw != 0.f ? pack_bf(v[2 * i], v[2 * i + 1]) : 0u;
+                        *reinterpret_cast<uint4*>(A.o + at) = make_uint4(w[0], w[1], w[2], w[3]);
+                    } else {
+                        *reinterpret_cast<float4*>(A.part_o + at) = make_float4(v[0], v[1], v[2], v[3]);
+                        *reinterpret_cast<float4*>(A.part_o + at + 4) = make_float4(v[4], v[5], v[6], v[7]);
                     }
                 }
-        }
-        __syncthreads();
-        const bool whole = t0 == 0 && t1 == n;
-        const int slot = 2 * blockIdx.x + (seg ? 1 : 0);
-        for (int i = tid; i < A.r * D; i += PA_THREADS) {
-            const int row = i / D, col = i - row * D;
-            float m = -INFINITY;
-#pragma unroll
-            for (int w = 0; w < PA_WARPS; ++w) m = fmaxf(m, mrg[(w * A.r + row) * MS + D]);
-            float acc = 0.f, l = 0.f, lw = 0.f;
-#pragma unroll
-            for (int w = 0; w < PA_WARPS; ++w) {
-                const float* src = mrg + (w * A.r + row) * MS;
-                if (src[D + 1] == 0.f) continue;
-                const float f = ex2(src[D] - m);
-                l += f * src[D + 1];
-                lw += f * src[D + 2];
-                acc += f * src[D + 3] * src[col];
-            }
-            if constexpr (CLU) {
-                float* dst = cl + row * MS;
-                dst[col] = acc;
-                if (col == 0) { dst[D] = m; dst[D + 1] = l; dst[D + 2] = lw; }
-            } else if (whole) {
-                pa_store(A, (int64_t)g * A.r + row, D, col, acc, m, l, lw);
-            } else {
-                const int64_t at = (int64_t)slot * A.r + row;
-                A.part_o[at * D + col] = acc;
-                if (col == 0) A.part_ml[at] = make_float4(m, l, lw, 0.f);
-            }
-        }
-        if constexpr (CLU) {
-            cluster_barrier();
-            const uint32_t rank = cluster_rank(), size = cluster_size();
-            for (int i = tid + rank * PA_THREADS; i < A.r * D; i += PA_THREADS * size) {
-                const int row = i / D, col = i - row * D;
-                const float* src = cl + row * MS;
-                float m = -INFINITY, acc = 0.f, l = 0.f, lw = 0.f;
-                for (uint32_t k0 = 0; k0 < size; k0 += 8) {      // eight CTAs' loads in flight
-                    float mk[8], lk[8], wk[8], ok[8];
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        const uint32_t k = min(k0 + i, size - 1);
-                        mk[i] = ld_cluster_f32(src + D, k);
-                        lk[i] = ld_cluster_f32(src + D + 1, k);
-                        wk[i] = ld_cluster_f32(src + D + 2, k);
-                        ok[i] = ld_cluster_f32(src + col, k);
-                    }
-                    float to = m;
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) to = fmaxf(to, mk[i]);
-                    const float f0 = l == 0.f ? 0.f : ex2(m - to);
-                    m = to;
-                    l *= f0; lw *= f0; acc *= f0;
-#pragma unroll
-                    for (int i = 0; i < 8; ++i)
-                        if (k0 + i < size && lk[i] != 0.f) {
-                            const float f = ex2(mk[i] - m);
-                            l += f * lk[i]; lw += f * wk[i]; acc += f * ok[i];
-                        }
+                if (gr == 0) {
+                    if (whole) A.lse[row] = l == 0.f ? -INFINITY : (m + log2f(l) - PA_BIAS) * 0.6931471805599453f;
+                    else A.part_ml[row] = make_float4(m, l, lw, 0.f);
                 }
-                pa_store(A, (int64_t)g * A.r + row, D, col, acc, m, l, lw);
             }
-            cluster_barrier();     // nobody leaves while its states are read
-            return;
+        if (lane == 0 && whole) A.info[g] = make_int2(-1, -1);
+        if (lane == 0 && !whole && first == 0) {
+            // the warp that holds the group's last tile: the largest w with total * w / n_warp <= that tile
+            const long long last = before + n - 1;
+            long long w = last * n_warp / total;
+            while (w + 1 < n_warp && total * (w + 1) / n_warp <= last) ++w;
+            while (w > 0 && total * w / n_warp > last) --w;
+            A.info[g] = make_int2((int)slot, (int)w);
         }
-        if (tid == 0 && t0 == 0) {
-            // the CTA that holds the group's last tile: the largest c with total * c / n_cta <= that tile
-            const long long last = gpre + n - 1;
-            long long cl = last * n_cta / total;
-            while (cl + 1 < n_cta && total * (cl + 1) / n_cta <= last) ++cl;
-            while (cl > 0 && total * cl / n_cta > last) --cl;
-            A.info[g] = whole ? make_int2(-1, -1) : make_int2(slot, (int)cl);
-        }
-        fence_async();             // the next segment's copies overwrite the states
-        __syncthreads();
-        cur = gpre + t1;
+        before += n;
         ++seg;
-    }
+    });
 }
 
-// Joins the parts of groups cut by range borders: grid (G, r); thread (slice, value column), the slices take every
-// PA_JOIN-th part and are added in order.
-constexpr int PA_JOIN = 4;
+// Joins the parts of groups cut by range borders.  `slices` warps (1, 2, 4 or 8) take a (group, head): warp s adds
+// parts s, s + slices, .. of 4 or 2 value columns a lane, and the slices are added in order.
+constexpr int PA_JOIN = 8;         // warps of a CTA
 template <int D>
-__global__ void __launch_bounds__(D * PA_JOIN) paged_join_kernel(const __grid_constant__ PagedAttnArgs A) {
-    __shared__ float s_red[D * PA_JOIN / 32];
-    __shared__ float s_acc[PA_JOIN][D + 2];
-    const int g = blockIdx.x, row = blockIdx.y, col = threadIdx.x % D, slice = threadIdx.x / D;
+__global__ void __launch_bounds__(PA_JOIN * 32) paged_join_kernel(const __grid_constant__ PagedAttnArgs A, int slices) {
+    constexpr int N = D / 32;
+    __shared__ float s_acc[PA_JOIN][D], s_m[PA_JOIN], s_l[PA_JOIN][2];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, slice = warp % slices;
+    const int64_t pair = ((int64_t)blockIdx.x * PA_JOIN + warp) / slices;
     grid_wait();
+    const bool have = pair < (int64_t)A.G * A.r;
+    const int g = have ? (int)(pair / A.r) : 0, row = have ? (int)(pair - (int64_t)g * A.r) : 0;
     const int2 info = A.info[g];
-    if (info.x < 0) return;
-    const int n = info.y - info.x / 2 + 1;                    // parts: the first CTA's slot, then slot 0 of each CTA after it
+    const bool cut = have && info.x >= 0;
+    const int n = cut ? info.y - info.x / 2 + 1 : 0;          // parts: the first warp's slot, then slot 0 of each warp after it
     auto part = [&](int i) { return (i == 0 ? (int64_t)info.x : 2 * ((int64_t)(info.x / 2) + i)) * A.r + row; };
     float m = -INFINITY;
-    for (int i = threadIdx.x; i < n; i += D * PA_JOIN) m = fmaxf(m, A.part_ml[part(i)].x);
+    for (int i = slice * 32 + lane; i < n; i += slices * 32) m = fmaxf(m, A.part_ml[part(i)].x);
 #pragma unroll
     for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-    if ((threadIdx.x & 31) == 0) s_red[threadIdx.x >> 5] = m;
-    __syncthreads();
-    for (int i = 0; i < D * PA_JOIN / 32; ++i) m = fmaxf(m, s_red[i]);
-    float acc = 0.f, l = 0.f, lw = 0.f;
+    if (slices > 1) {
+        if (lane == 0) s_m[warp] = m;
+        __syncthreads();
+        for (int i = 0; i < slices; ++i) m = fmaxf(m, s_m[warp - slice + i]);
+    }
+    float acc[N], l = 0.f, lw = 0.f;
+#pragma unroll
+    for (int e = 0; e < N; ++e) acc[e] = 0.f;
 #pragma unroll 8
-    for (int i = slice; i < n; i += PA_JOIN) {
+    for (int i = slice; i < n; i += slices) {
         const int64_t at = part(i);
         const float4 ml = A.part_ml[at];
-        const float o = A.part_o[at * D + col];
+        float o[N];
+        if constexpr (N == 4) {
+            const float4 v = *reinterpret_cast<const float4*>(A.part_o + at * D + 4 * lane);
+            o[0] = v.x; o[1] = v.y; o[2] = v.z; o[3] = v.w;
+        } else {
+            const float2 v = *reinterpret_cast<const float2*>(A.part_o + at * D + 2 * lane);
+            o[0] = v.x; o[1] = v.y;
+        }
         const float f = ex2(ml.x - m);
-        // an empty part adds nothing, whatever its maximum
-        if (ml.y != 0.f) { l += f * ml.y; lw += f * ml.z; acc += f * o; }
+        if (ml.y != 0.f) {         // an empty part adds nothing, whatever its maximum
+            l += f * ml.y;
+            lw += f * ml.z;
+#pragma unroll
+            for (int e = 0; e < N; ++e) acc[e] += f * o[e];
+        }
     }
-    s_acc[slice][col] = acc;
-    if (col == 0) { s_acc[slice][D] = l; s_acc[slice][D + 1] = lw; }
-    __syncthreads();
-    if (slice) return;
-    for (int k = 1; k < PA_JOIN; ++k) acc += s_acc[k][col];
-    l = lw = 0.f;
-    for (int k = 0; k < PA_JOIN; ++k) { l += s_acc[k][D]; lw += s_acc[k][D + 1]; }
-    pa_store(A, (int64_t)g * A.r + row, D, col, acc, m, l, lw);
+    if (slices > 1) {
+#pragma unroll
+        for (int e = 0; e < N; ++e) s_acc[warp][N * lane + e] = acc[e];
+        if (lane == 0) { s_l[warp][0] = l; s_l[warp][1] = lw; }
+        __syncthreads();
+        if (slice) return;
+        for (int i = 1; i < slices; ++i) {
+            l += s_l[warp + i][0];
+            lw += s_l[warp + i][1];
+#pragma unroll
+            for (int e = 0; e < N; ++e) acc[e] += s_acc[warp + i][N * lane + e];
+        }
+    }
+    if (!cut) return;
+    const int64_t to = (int64_t)g * A.r + row;
+#pragma unroll
+    for (int e = 0; e < N; e += 2)
+        *reinterpret_cast<uint32_t*>(A.o + to * D + N * lane + e) = lw != 0.f ? pack_bf(acc[e] / lw, acc[e + 1] / lw) : 0u;
+    if (lane == 0) A.lse[to] = l == 0.f ? -INFINITY : (m + log2f(l) - PA_BIAS) * 0.6931471805599453f;
 }
 
 // How a call is cut.
-// cluster > 0: that many CTAs per group in a cluster and no second launch.  Taken where a CTA then has at most 2048
-// tokens, i.e. where latency counts (1 x 4096 bf16: 6.6 us against 10.9 in two launches), and for lists of blocks,
-// whose groups all have the same work (8 x 72 blocks of 64, e4m3: 20.6 us against 26.6).
-// cluster 0: equal ranges over `ctas` CTAs, enough to fill the device, at least 8 subtiles each at the lengths the
-// caller bounds.  Taken for long contexts, whose lengths the host does not know: where they differ by two a cluster
-// per group waits for the longest (16 x 64K-128K e4m3: 455 us against 555).
+// cluster > 0: that many CTAs per group in a cluster and no second launch.  Taken where the groups' clusters fit the
+// device at once with at most 1536 tokens a CTA, i.e. where latency counts: e4m3, 8 KV heads of 128, one request of
+// 4096 tokens 10.4 us against 13.8 as ranges, 4 of 8192 17.8 against 21.7, 16 of 4096 29.7 against 37.7; but one of
+// 32768 (2048 tokens a CTA) 27.8 against 25.0, one of 131072 86 against 57.
+// cluster 0: equal ranges over `ctas` CTAs, two to an SM (three are slower: 16 x 64K-128K 457 us against 430), with at
+// least 8 subtiles each at the lengths the caller bounds.  The host does not know the lengths: where they differ a
+// cluster per group waits for the longest.
 struct PaPlan {
     int cluster, ctas;
 };
-constexpr int PA_SLOTS = PA_PER_SM * 152;
-PaPlan paged_attn_plan(int64_t groups, int64_t max_tokens, bool equal) {
+constexpr int PA_SLOTS = 2 * 152;             // CTAs of the range kernel
+constexpr int PA_FIT = 400;                   // CTAs in clusters that start at once, three to an SM; 448 in sevens do not
+PaPlan paged_attn_plan(int64_t groups, int64_t max_tokens) {
     const int64_t want = std::max<int64_t>(1, (max_tokens + 127) / 128);
-    const int64_t fit = std::min<int64_t>(16, PA_SLOTS / groups);
-    const int64_t s = std::max<int64_t>(1, std::min(want, fit));
-    if (max_tokens <= 2048 * s || (equal && s * groups >= PA_SLOTS / 2)) return {(int)s, (int)(s * groups)};
+    int64_t s = 0;
+    for (int c : {1, 2, 3, 4, 6, 8, 12, 16})
+        if (c * groups <= PA_FIT && (c <= want || c == 1)) s = c;
+    if (s && max_tokens <= 1536 * s) return {(int)s, (int)(s * groups)};
     const int64_t subs = groups * ((max_tokens + PA_SUB - 1) / PA_SUB);
     return {0, (int)std::min<int64_t>(PA_SLOTS, std::max<int64_t>(1, (subs + 7) / 8))};
 }
@@ -782,9 +930,9 @@ size_t round256(size_t x) { return (x + 255) / 256 * 256; }
 
 size_t paged_attn_workspace(const PaPlan& plan, int G, int r, int d) {
     if (plan.cluster) return 0;
-    const int ctas = plan.ctas;
-    return round256((size_t)G * sizeof(int2)) + round256((size_t)2 * ctas * r * sizeof(float4)) +
-           (size_t)2 * ctas * r * d * sizeof(float);
+    const int warps = plan.ctas * PA_WARPS;
+    return round256((size_t)G * sizeof(int2)) + round256((size_t)2 * warps * r * sizeof(float4)) +
+           (size_t)2 * warps * r * d * sizeof(float);
 }
 
 }  // namespace kvo
@@ -815,19 +963,24 @@ cudaError_t paged_attn_launch(const CUtensorMap& mk, const CUtensorMap& mv, cons
     static std::atomic<uint64_t> done{0};
     cudaError_t e = cudaSuccess;
     if (first_on_device(done)) {
-        e = cudaFuncSetAttribute(paged_attn_kernel<D, FP8, NH, true>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+        e = cudaFuncSetAttribute(paged_cluster_kernel<D, FP8, NH>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
         if (e == cudaSuccess)
-            e = cudaFuncSetAttribute(paged_attn_kernel<D, FP8, NH, true>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+            e = cudaFuncSetAttribute(paged_cluster_kernel<D, FP8, NH>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
         if (e == cudaSuccess)
-            e = cudaFuncSetAttribute(paged_attn_kernel<D, FP8, NH, false>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+            e = cudaFuncSetAttribute(paged_range_kernel<D, FP8, NH>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
         if (e != cudaSuccess) return e;
         mark_on_device(done);
     }
     if (plan.cluster)
-        return launch_dependent(paged_attn_kernel<D, FP8, NH, true>, plan.ctas, PA_THREADS, smem, s, plan.cluster, mk, mv, A);
-    e = launch_dependent(paged_attn_kernel<D, FP8, NH, false>, plan.ctas, PA_THREADS, smem, s, 0, mk, mv, A);
+        return launch_dependent(paged_cluster_kernel<D, FP8, NH>, plan.ctas, PA_THREADS, smem, s, plan.cluster, mk, mv, A);
+    e = launch_dependent(paged_range_kernel<D, FP8, NH>, plan.ctas, PA_THREADS, smem, s, 0, mk, mv, A);
     if (e != cudaSuccess) return e;
-    return launch_dependent(paged_join_kernel<D>, dim3(A.G, A.r), D * PA_JOIN, 0, s, 0, A);
+    // as many warps to a pair as keep the device's about 9000 warps (8 CTAs of 8 to an SM) in one wave
+    const int64_t pairs = (int64_t)A.G * A.r;
+    int slices = PA_JOIN;
+    while (slices > 1 && pairs * slices > 152 * 64) slices /= 2;
+    const dim3 grid((unsigned)((pairs * slices + PA_JOIN - 1) / PA_JOIN));
+    return launch_dependent(paged_join_kernel<D>, grid, PA_JOIN * 32, 0, s, 0, A, slices);
 }
 
 }  // namespace
@@ -840,7 +993,7 @@ extern "C" kvo_status kvo_paged_attn_workspace(const kvo_paged_cache* cache, int
     *bytes_out = 0;
     if (const char* m = paged_attn_error(cache, n_q_heads, n_blocks, max_len)) return bad(m);
     const int G = cache->batch * cache->n_kv_heads;
-    *bytes_out = paged_attn_workspace(paged_attn_plan(std::max(G, 1), paged_attn_bound(cache, n_blocks, max_len), n_blocks > 0), G,
+    *bytes_out = paged_attn_workspace(paged_attn_plan(std::max(G, 1), paged_attn_bound(cache, n_blocks, max_len)), G,
                                       n_q_heads / cache->n_kv_heads, cache->head_dim);
     return KVO_OK;
 }
@@ -859,7 +1012,7 @@ extern "C" kvo_status kvo_paged_attn(const kvo_paged_cache* cache, const void* q
     if ((uintptr_t)q % 16 || (uintptr_t)o % 16 || (uintptr_t)workspace % 256)
         return bad("q and o must be 16-byte aligned, the workspace 256-byte aligned");
     const int G = cache->batch * cache->n_kv_heads, r = n_q_heads / cache->n_kv_heads, D = cache->head_dim;
-    const PaPlan plan = paged_attn_plan(G, paged_attn_bound(cache, blocks ? n_blocks : 0, max_len), blocks != nullptr);
+    const PaPlan plan = paged_attn_plan(G, paged_attn_bound(cache, blocks ? n_blocks : 0, max_len));
     const size_t need = paged_attn_workspace(plan, G, r, D);
     if (need && (!workspace || workspace_bytes < need)) return bad("the workspace is too small (kvo_paged_attn_workspace)");
     const bool fp8 = cache->format == KVO_PAGES_E4M3;
@@ -884,7 +1037,7 @@ extern "C" kvo_status kvo_paged_attn(const kvo_paged_cache* cache, const void* q
     uint8_t* ws = (uint8_t*)workspace;
     A.info = (int2*)ws;
     A.part_ml = (float4*)(ws + round256((size_t)G * sizeof(int2)));
-    A.part_o = (float*)((uint8_t*)A.part_ml + round256((size_t)2 * plan.ctas * r * sizeof(float4)));
+    A.part_o = (float*)((uint8_t*)A.part_ml + round256((size_t)2 * plan.ctas * PA_WARPS * r * sizeof(float4)));
     A.status = status;
     A.batch = cache->batch;
     A.hkv = cache->n_kv_heads;
