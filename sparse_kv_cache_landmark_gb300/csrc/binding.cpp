@@ -113,30 +113,39 @@ int int32_size(int64_t v, const char* name) {
     return (int)v;
 }
 
-// The stream handle for the C ABI: torch's current stream of the device, a torch stream or a raw handle.  The ABI
-// gets the legacy default stream by its name, cudaStreamLegacy.
-kvo_stream_t stream_of(PyObject* o, const at::Device& dev) {
-    uintptr_t h = 0;
-    if (o == Py_None) {
-        h = (uintptr_t)c10::cuda::getCurrentCUDAStream(dev.index()).stream();
-    } else {
-        PyObject* a = PyObject_GetAttrString(o, "cuda_stream");
-        if (!a) {
-            PyErr_Clear();
-            a = o;
-            Py_INCREF(a);
+// The stream of a call: torch's current stream of the device, or the torch stream or raw handle that was given.  A
+// given stream is made current for the call, so that outputs and workspace come from its own memory pool: a block of
+// another stream's pool could still be in use there, or be handed out again while this call runs.
+struct Stream {
+    kvo_stream_t handle;                         // the legacy default stream by its name, cudaStreamLegacy
+    c10::cuda::OptionalCUDAStreamGuard guard;
+
+    Stream(PyObject* o, const at::Device& dev) {
+        if (!dev.is_cuda()) refuse("all buffers must be on one CUDA device, got " + dev.str());
+        uintptr_t h = 0;
+        if (o == Py_None) {
+            h = (uintptr_t)c10::cuda::getCurrentCUDAStream(dev.index()).stream();
+        } else {
+            PyObject* a = PyObject_GetAttrString(o, "cuda_stream");
+            if (!a) {
+                PyErr_Clear();
+                a = o;
+                Py_INCREF(a);
+            }
+            h = (uintptr_t)PyLong_AsUnsignedLongLong(a);
+            Py_DECREF(a);
+            if (PyErr_Occurred()) throw PythonError{};
+            const bool legacy = h <= 1;
+            guard.reset_stream(legacy ? c10::cuda::getDefaultCUDAStream(dev.index())
+                                      : c10::cuda::getStreamFromExternal((cudaStream_t)h, dev.index()));
         }
-        h = (uintptr_t)PyLong_AsUnsignedLongLong(a);
-        Py_DECREF(a);
-        if (PyErr_Occurred()) throw PythonError{};
+        handle = (kvo_stream_t)(h ? h : 1);
     }
-    return (kvo_stream_t)(h ? h : 1);
-}
+};
 
 // Runs a C call with the device current; raises on any status but KVO_OK.
 template <typename F>
 void launch(const at::Device& dev, F&& call) {
-    if (!dev.is_cuda()) refuse("all buffers must be on one CUDA device, got " + dev.str());
     const c10::cuda::CUDAGuard guard(dev);
     const kvo_status st = call();
     if (st != KVO_OK) throw Refused{st, kvo_last_error(nullptr)};
@@ -187,6 +196,7 @@ PyObject* py_rope(PyObject*, PyObject* const* a, Py_ssize_t n) {
         const at::Tensor& freq = need(a[2], "freq", dev, at::kLong);
         const bool inter = truth(a[3]);
         const float amp = number(a[4]);
+        const Stream stream(a[6], dev);
         at::Tensor out;
         int64_t tok = H * d, head = d;
         if (a[5] == Py_None) {
@@ -202,7 +212,7 @@ PyObject* py_rope(PyObject*, PyObject* const* a, Py_ssize_t n) {
         launch(dev, [&] {
             return kvo_rope(x.t.data_ptr(), x.tok, x.head, out.data_ptr(), tok, head, (const int32_t*)pos.data_ptr(),
                             (const uint64_t*)freq.data_ptr(), T, int32_size(H, "heads"), int32_size(d, "head_dim"),
-                            int32_size(2 * freq.numel(), "freq"), inter, amp, stream_of(a[6], dev));
+                            int32_size(2 * freq.numel(), "freq"), inter, amp, stream.handle);
         });
         return THPVariable_Wrap(out);
     });
@@ -266,6 +276,7 @@ PyObject* py_paged_append(PyObject*, PyObject* const* a, Py_ssize_t n) {
         }
         const bool inter = truth(a[10]);
         const float amp = number(a[11]);
+        const Stream stream(a[16], dev);
         const void* qp = nullptr;
         int64_t qt = 0, hq = 0;
         at::Tensor q_out;
@@ -285,7 +296,7 @@ PyObject* py_paged_append(PyObject*, PyObject* const* a, Py_ssize_t n) {
         launch(dev, [&] {
             return kvo_paged_append(&c, k.t.data_ptr(), k.tok, v.t.data_ptr(), v.tok, T, cu, start, freq, rot, inter, amp,
                                     qp, qt, int32_size(hq, "n_q_heads"), qp ? q_out.data_ptr() : nullptr, k_out, status,
-                                    stream_of(a[16], dev));
+                                    stream.handle);
         });
         if (!qp) Py_RETURN_NONE;
         return THPVariable_Wrap(q_out);
@@ -320,10 +331,11 @@ PyObject* py_paged_attn(PyObject*, PyObject* const* a, Py_ssize_t n) {
             counts = (const int32_t*)t.data_ptr();
         }
         const int64_t max_len = integer(a[9]);
+        const Stream stream(a[14], dev);
         at::Tensor o = a[10] == Py_None ? empty(shape, at::kBFloat16, dev) : need(a[10], "o", dev, at::kBFloat16, at::IntArrayRef(shape));
         at::Tensor lse = a[11] == Py_None ? empty(lshape, at::kFloat, dev) : need(a[11], "lse", dev, at::kFloat, at::IntArrayRef(lshape));
         int32_t* status = status_of(a[13], dev);
-        at::Tensor ws;                 // from torch's allocator: it belongs to the current stream, as the outputs do
+        at::Tensor ws;                 // from torch's allocator, like the outputs
         size_t bytes = 0;
         if (a[12] == Py_None) {
             const kvo_status st = kvo_paged_attn_workspace(&c, int32_size(hq, "n_q_heads"), int32_size(n_blocks, "n_blocks"), max_len, &bytes);
@@ -336,7 +348,7 @@ PyObject* py_paged_attn(PyObject*, PyObject* const* a, Py_ssize_t n) {
         launch(dev, [&] {
             return kvo_paged_attn(&c, q.data_ptr(), (int)hq, lens, max_len, blocks, counts, int32_size(n_blocks, "n_blocks"),
                                   o.data_ptr(), (float*)lse.data_ptr(), ws.defined() ? ws.data_ptr() : nullptr, bytes, status,
-                                  stream_of(a[14], dev));
+                                  stream.handle);
         });
         return pair(o, lse);
     });
@@ -356,6 +368,7 @@ PyObject* py_prompt_attn(PyObject*, PyObject* const* a, Py_ssize_t n) {
         if (cq.dim() != 1 || cq.numel() < 1) refuse("cu_q must be [batch + 1], got " + shape_text(cq.sizes()));
         const at::Tensor& ck = a[4] == Py_None ? cq : need(a[4], "cu_k", dev, at::kInt, cq.sizes());
         const bool causal = truth(a[5]);
+        const Stream stream(a[9], dev);
         at::Tensor o = a[6] == Py_None ? empty(shape, at::kBFloat16, dev) : need(a[6], "o", dev, at::kBFloat16, at::IntArrayRef(shape));
         at::Tensor lse = a[7] == Py_None ? empty(lshape, at::kFloat, dev) : need(a[7], "lse", dev, at::kFloat, at::IntArrayRef(lshape));
         int32_t* status = status_of(a[8], dev);
@@ -364,7 +377,7 @@ PyObject* py_prompt_attn(PyObject*, PyObject* const* a, Py_ssize_t n) {
                                    (const int32_t*)cq.data_ptr(), (const int32_t*)ck.data_ptr(),
                                    int32_size(cq.numel() - 1, "batch"), T, m, int32_size(hq, "n_q_heads"),
                                    int32_size(hkv, "n_kv_heads"), int32_size(d, "head_dim"), causal, o.data_ptr(),
-                                   (float*)lse.data_ptr(), status, stream_of(a[9], dev));
+                                   (float*)lse.data_ptr(), status, stream.handle);
         });
         return pair(o, lse);
     });

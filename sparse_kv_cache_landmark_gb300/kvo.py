@@ -243,7 +243,11 @@ _BINDING = None
 
 
 def _native():
-    """The native binding of the serving calls (built beside libkvo.so); raises if it is missing."""
+    """The native binding of the serving calls (built beside libkvo.so); raises if it is missing.
+
+    These calls run on torch's current stream of their buffers' device, or on ``stream``, whose memory pool the outputs
+    and workspaces then come from.  They are for inference: nothing is recorded for a backward pass.
+    """
     global _BINDING
     if _BINDING is None:
         lib()
@@ -324,8 +328,7 @@ def paged_attn(q, k_pages, v_pages, table, lens, *, k_scale=None, v_scale=None, 
 
     q: CUDA bf16 [batch][Hq][d]; pools, scales and table as in ``paged_append``; lens: int32 [batch];
     blocks: int32 [batch][Hkv][n], the logical pages each KV head attends to (e.g. ``select_topk``'s),
-    counts: int32 [batch][Hkv].  The workspace comes from torch's allocator when none is given; it must
-    then stay on the stream that is current (give one for another ``stream``).
+    counts: int32 [batch][Hkv].
     """
     return (_BINDING or _native()).paged_attn(q, k_pages, v_pages, table, lens, k_scale, v_scale, blocks, counts, max_len,
                                               o, lse, workspace, status, stream)

@@ -400,3 +400,65 @@ def test_append_then_attend_step_by_step():
                         for j in range(b)]
                 check_attention(qr, got, rows, hkv, ref.F16)
     torch.cuda.current_stream().wait_stream(side)
+
+
+# ------------------------------------------------------------------ where memory lies, and on which stream
+def test_rows_behind_the_last_request_keep_their_bytes():
+    g = gen(8)
+    kp, vp, ks, vs = pools(g, 4, 1, 16, 64, True)
+    k = normal(g, 9, 1, 64)
+    q_out, k_out = (torch.full((9, n, 64), 5.0, dtype=torch.bfloat16, device="cuda") for n in (3, 1))
+    kvo.paged_append(k, k, kp, vp, i32([[0], [1]]), i32([0, 2]), cu=i32([1, 4, 7]), k_scale=ks, v_scale=vs,
+                     freq=kvo.rope_frequencies(64)[0], q=normal(g, 9, 3, 64), q_out=q_out, k_out=k_out)
+    for t in (q_out, k_out):
+        assert (t[0] == 5.0).all() and (t[7:] == 5.0).all() and (t[1:7] != 5.0).any()
+
+
+def test_pools_past_four_gigabytes():
+    """Pages whose first byte lies past 2^32, rows past 2^31 values: append and attention reach them."""
+    g = gen(12)
+    hkv, page, d = 2, 128, 128
+    n_pages = 2 ** 32 // (hkv * page * d) + 40
+    kp, vp = (torch.empty(n_pages, hkv, page, d, dtype=E4M3, device="cuda") for _ in range(2))
+    ks, vs = (torch.ones(n_pages, hkv, device="cuda") for _ in range(2))
+    table = (n_pages - 1 - torch.arange(6, dtype=torch.int32)).view(2, 3).cuda()
+    counts, cu = [300, 129], [0, 300, 429]
+    k, v = normal(g, 429, hkv, d), normal(g, 429, hkv, d)
+    kvo.paged_append(k, v, kp, vp, table, i32([0, 0]), cu=i32(cu), k_scale=ks, v_scale=vs)
+    q = normal(g, 2, 4 * hkv, d)
+    got = kvo.paged_attn(q, kp, vp, table, i32(counts), k_scale=ks, v_scale=vs)
+    rows = []
+    for b, n in enumerate(counts):
+        at = table[b].long()
+        rows.append([(p[at].float().double() * s[at].double()[..., None, None]).transpose(0, 1).flatten(1, 2)[:, :n].cpu()
+                     for p, s in ((kp, ks), (vp, vs))])
+    for (a, b), (x, y) in zip(((0, 300), (300, 429)), rows):         # the codes are those of the rows appended
+        assert ((x.transpose(0, 1) - k[a:b].double().cpu()).abs() <= 2.0 ** -4 * k[a:b].double().cpu().abs() + 2.0 ** -9).all()
+    check_attention(q, got, rows, hkv, ref.F16)
+
+
+def test_calls_on_a_stream_of_their_own():
+    """Given a stream, outputs and workspace come from its pool: memory that the current stream frees and takes again
+    meanwhile is not touched."""
+    g = gen(17)
+    lens = [30000, 20000]
+    (kp, vp), (ks, vs), table, _ = cache_of(g, lens, 1, 64, 128, True)
+    wide = torch.zeros(2, 8192, dtype=torch.int32, device="cuda")          # cut into ranges: a workspace is needed
+    wide[:, :table.shape[1]] = table
+    q, ln = normal(g, 2, 8, 128), i32(lens)
+    want = kvo.paged_attn(q, kp, vp, wide, ln, k_scale=ks, v_scale=vs)
+    x = normal(g, 4000, 8, 128)
+    pos, (freq, amp) = torch.arange(4000, dtype=torch.int32, device="cuda"), kvo.rope_frequencies(128)
+    want_x = kvo.rope(x, pos, freq, amplitude=amp)
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for handle in (side, side.cuda_stream):
+        outs = []
+        for _ in range(20):
+            outs.append((kvo.paged_attn(q, kp, vp, wide, ln, k_scale=ks, v_scale=vs, stream=handle),
+                         kvo.rope(x, pos, freq, amplitude=amp, stream=handle)))
+            for n in (1 << 12, 1 << 20, 8 << 20):
+                torch.full((n,), 255, dtype=torch.uint8, device="cuda")    # freed at once
+        torch.cuda.synchronize()
+        for (o, lse), y in outs:
+            assert torch.equal(o, want[0]) and torch.equal(lse, want[1]) and torch.equal(y, want_x)

@@ -169,3 +169,67 @@ def test_from_prompt_to_decode(e4m3):
         assert (lse3.view(-1) - want_lse.view(-1)).abs().max() <= 1e-3
     finally:
         ctx.close()
+
+
+def test_prompt_attention_past_four_gigabytes():
+    """A request whose rows lie past 2^31 values of q, k, v and o."""
+    g = gen(41)
+    hq, hkv, d, n = 32, 32, 128, 150
+    T = 2 ** 32 // (2 * hq * d) + 5000
+    q, k, v = (torch.empty(T, hq, d, dtype=torch.bfloat16, device="cuda") for _ in range(3))
+    o = torch.empty(T, hq, d, dtype=torch.bfloat16, device="cuda")
+    lse = torch.full((T, hq), 2.0, device="cuda")
+    for t in (q, k, v):
+        t[T - n:] = normal(g, n, hq, d)
+    o[T - n - 64:T - n] = 7.0
+    cu = [T - n, T]
+    kvo.prompt_attn(q, k, v, i32(cu), o=o, lse=lse)
+    check_rows(q[T - n:], k[T - n:], v[T - n:], o[T - n:], lse[T - n:], [0, n], [0, n], True, rows=[0, 77, n - 1])
+    assert (o[T - n - 64:T - n] == 7.0).all() and (lse[:T - n] == 2.0).all()
+
+
+def test_many_requests_in_one_call():
+    """More requests than one round of offsets holds, empty ones among them."""
+    g = gen(43)
+    nq = [(7 * i) % 5 for i in range(90)]
+    cq = cuts(nq)
+    q, k, v = normal(g, cq[-1], 4, 64), normal(g, cq[-1], 2, 64), normal(g, cq[-1], 2, 64)
+    o, lse = kvo.prompt_attn(q, k, v, i32(cq))
+    check_rows(q, k, v, o, lse, cq, cq, True)
+
+
+def test_calls_in_two_graphs_and_streams():
+    """Prompt attention, append and decode captured twice and replayed side by side, each with its own outputs."""
+    g = gen(47)
+    n, hq, hkv, d = 200, 8, 2, 64
+    sets = []
+    for _ in range(2):
+        s = dict(q=normal(g, n, hq, d), k=normal(g, n, hkv, d), v=normal(g, n, hkv, d), cu=i32([0, 77, n]),
+                 kp=torch.zeros(64, hkv, 16, d, dtype=torch.bfloat16, device="cuda"), table=torch.arange(32, dtype=torch.int32, device="cuda").view(2, 16))
+        s["vp"] = torch.zeros_like(s["kp"])
+        sets.append(s)
+
+    def run(s):
+        kvo.paged_append(s["k"], s["v"], s["kp"], s["vp"], s["table"], i32_zero, cu=s["cu"])
+        a = kvo.prompt_attn(s["q"], s["k"], s["v"], s["cu"])
+        return a + kvo.paged_attn(s["q"][:2].contiguous(), s["kp"], s["vp"], s["table"], lens)
+
+    i32_zero, lens = i32([0, 0]), i32([77, 123])
+    want = [[t.clone() for t in run(s)] for s in sets]
+    graphs = []
+    for s in sets:
+        st = torch.cuda.Stream()
+        st.wait_stream(torch.cuda.current_stream())
+        gr = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(gr, stream=st):
+            out = run(s)
+        graphs.append((gr, st, out))
+    torch.cuda.synchronize()
+    for _ in range(30):
+        for gr, st, _o in graphs:
+            with torch.cuda.stream(st):
+                gr.replay()
+    torch.cuda.synchronize()
+    for w, (_g, _s, out) in zip(want, graphs):
+        for a, b in zip(w, out):
+            assert torch.equal(a, b)
