@@ -625,6 +625,7 @@ paged_cluster_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_con
     float* cl = reinterpret_cast<float*>(ring_p + 48 * 1024);
     constexpr int MS = D + 4;
     pa_init(sh);
+    if (tid == 0) { tensor_map_prefetch(&map_k); tensor_map_prefetch(&map_v); }
     grid_wait();
     const uint32_t rank = cluster_rank(), size = cluster_size();
     const int g = blockIdx.x / size, n = (pa_span(A, g) + S::TILE - 1) / S::TILE;
@@ -722,6 +723,7 @@ paged_range_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_const
     const uint8_t* ring_p = smem_raw + (ring - smem_u32(smem_raw));
     auto tiles_of = [&](int g) { return (pa_span(A, g) + S::TILE - 1) / S::TILE; };
     pa_init(sh);
+    if (tid == 0) { tensor_map_prefetch(&map_k); tensor_map_prefetch(&map_v); }
     grid_wait();
     // Prefix of the tiles over the CTA, by requests, or by groups where each has a list of its own: each thread's
     // share, then shuffles within a warp, then the warps' totals through shared memory.
@@ -750,7 +752,8 @@ paged_range_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_const
     // two tiles at least to a warp, at most 512 parts to join for a group, and warps spread over the CTAs before they
     // fill them
     const long long n_warp = max(1ll, min(min((long long)gridDim.x * PA_WARPS, 512ll * A.G), total / 2));
-    auto start = [&](long long w) { return w < n_warp ? total * w / n_warp : total; };
+    const long long each = total / n_warp, extra = total - each * n_warp;       // the first `extra` warps take one more
+    auto start = [&](long long w) { return w < n_warp ? each * w + min(w, extra) : total; };
 #pragma unroll
     for (int w = 0; w < PA_WARPS; ++w) {
         const long long lo = start((long long)w * gridDim.x + blockIdx.x);
@@ -822,11 +825,9 @@ paged_range_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_const
             }
         if (lane == 0 && whole) A.info[g] = make_int2(-1, -1);
         if (lane == 0 && !whole && first == 0) {
-            // the warp that holds the group's last tile: the largest w with total * w / n_warp <= that tile
-            const long long last = before + n - 1;
-            long long w = last * n_warp / total;
-            while (w + 1 < n_warp && total * (w + 1) / n_warp <= last) ++w;
-            while (w > 0 && total * w / n_warp > last) --w;
+            // the warp that holds the group's last tile
+            const long long last = before + n - 1, wide = extra * (each + 1);
+            const long long w = last < wide ? last / (each + 1) : extra + (last - wide) / each;
             A.info[g] = make_int2((int)slot, (int)w);
         }
         before += n;
@@ -850,6 +851,22 @@ __global__ void __launch_bounds__(PA_JOIN * 32) paged_join_kernel(const __grid_c
     const bool cut = have && info.x >= 0;
     const int n = cut ? info.y - info.x / 2 + 1 : 0;          // parts: the first warp's slot, then slot 0 of each warp after it
     auto part = [&](int i) { return (i == 0 ? (int64_t)info.x : 2 * ((int64_t)(info.x / 2) + i)) * A.r + row; };
+    auto values = [&](int i, float (&o)[N]) {
+        const float* at = A.part_o + part(i) * D + N * lane;
+        if constexpr (N == 4) {
+            const float4 v = *reinterpret_cast<const float4*>(at);
+            o[0] = v.x; o[1] = v.y; o[2] = v.z; o[3] = v.w;
+        } else {
+            const float2 v = *reinterpret_cast<const float2*>(at);
+            o[0] = v.x; o[1] = v.y;
+        }
+    };
+    // the first parts' values are on their way while the maxima are compared
+    constexpr int AHEAD = 4;
+    float o0[AHEAD][N];
+#pragma unroll
+    for (int k = 0; k < AHEAD; ++k)
+        if (slice + k * slices < n) values(slice + k * slices, o0[k]);
     float m = -INFINITY;
     for (int i = slice * 32 + lane; i < n; i += slices * 32) m = fmaxf(m, A.part_ml[part(i)].x);
 #pragma unroll
@@ -862,18 +879,8 @@ __global__ void __launch_bounds__(PA_JOIN * 32) paged_join_kernel(const __grid_c
     float acc[N], l = 0.f, lw = 0.f;
 #pragma unroll
     for (int e = 0; e < N; ++e) acc[e] = 0.f;
-#pragma unroll 8
-    for (int i = slice; i < n; i += slices) {
-        const int64_t at = part(i);
-        const float4 ml = A.part_ml[at];
-        float o[N];
-        if constexpr (N == 4) {
-            const float4 v = *reinterpret_cast<const float4*>(A.part_o + at * D + 4 * lane);
-            o[0] = v.x; o[1] = v.y; o[2] = v.z; o[3] = v.w;
-        } else {
-            const float2 v = *reinterpret_cast<const float2*>(A.part_o + at * D + 2 * lane);
-            o[0] = v.x; o[1] = v.y;
-        }
+    auto add = [&](int i, const float (&o)[N]) {
+        const float4 ml = A.part_ml[part(i)];
         const float f = ex2(ml.x - m);
         if (ml.y != 0.f) {         // an empty part adds nothing, whatever its maximum
             l += f * ml.y;
@@ -881,6 +888,15 @@ __global__ void __launch_bounds__(PA_JOIN * 32) paged_join_kernel(const __grid_c
 #pragma unroll
             for (int e = 0; e < N; ++e) acc[e] += f * o[e];
         }
+    };
+#pragma unroll
+    for (int k = 0; k < AHEAD; ++k)
+        if (slice + k * slices < n) add(slice + k * slices, o0[k]);
+#pragma unroll 8
+    for (int i = slice + AHEAD * slices; i < n; i += slices) {
+        float o[N];
+        values(i, o);
+        add(i, o);
     }
     if (slices > 1) {
 #pragma unroll
