@@ -484,8 +484,8 @@ kvo_status sparse_decode_attn_static(const void* q, const void* k_buf, const voi
  *   x: bf16 [tokens][heads][head_dim] with any token and head stride (elements,
  *   multiples of 8; the last dimension contiguous; 16-byte aligned), e.g. the q
  *   and k heads of a fused projection.  out: the same shape with its own
- *   strides; out == x with equal strides rotates in place; other overlaps are
- *   not allowed.  pos: device int32 [tokens], any value (a negative position
+ *   strides (no row of it twice); out == x with equal strides rotates in place;
+ *   other overlaps are not allowed.  pos: device int32 [tokens], any value (a negative position
  *   turns backwards).  freq: device uint64 [rot_dim / 2], each pair's frequency
  *   in turns per position, in units of 2^-64: the phase pos * freq is exact
  *   modulo a turn at every position.  Scalings for long contexts are other
@@ -530,7 +530,8 @@ typedef struct {
  *   that value goes to k_out (bf16 [tokens][n_kv_heads][head_dim], optional)
  *   and to the cache.  q (optional): bf16 [tokens][n_q_heads][head_dim], heads
  *   contiguous, any token stride, rotated into the contiguous q_out by the same
- *   launch.  k_out may be k and q_out q where those are contiguous.
+ *   launch.  k_out may be k and q_out q where those are contiguous; other
+ *   overlaps are refused.
  *   e4m3 pages: a page's scale is the smallest power of two s >= 2^-100 with
  *   |x| <= 448 s for the finite values written to it.  A page whose first row
  *   is written starts afresh; otherwise its scale never shrinks, and when it
@@ -566,13 +567,15 @@ kvo_status kvo_paged_append(const kvo_paged_cache* cache, const void* k, int64_t
  *   the first counts[b][h] count (counts NULL: all).  A listed block is cut at
  *   the request's length, one past it adds nothing, one listed twice counts
  *   twice.
- *   o: bf16 [batch][n_q_heads][head_dim]; lse: fp32 [batch][n_q_heads], natural
- *   log.  Softmax scale 1/sqrt(head_dim), fp32 accumulation.  A request with
+ *   o: bf16 [batch][n_q_heads][head_dim], apart from q; lse: fp32
+ *   [batch][n_q_heads], natural log.  Softmax scale 1/sqrt(head_dim), fp32 accumulation.  A request with
  *   nothing to attend to gets o = 0, lse = -inf.  What lies in a page behind
  *   the last token is never used, NaN included.
  *   o is rounded once to bf16, as the projection that follows takes it: the
  *   weights are rounded to 11 bits (8 with bf16 pages) on the tensor cores, so
- *   fp32 would carry no more.  Two calls give the same bits.
+ *   fp32 would carry no more.  With e4m3 pages the weights are rounded next to
+ *   the group's largest v_scale: a page keeps the 11 bits as long as its v_scale
+ *   is no more than 2^20 times smaller.  Two calls give the same bits.
  *   workspace: kvo_paged_attn_workspace bytes (0 for small calls: NULL will do),
  *   256-byte aligned, contents undefined before and after; one call at a time may use it (two captured
  *   graphs that may overlap need one each).
@@ -600,8 +603,8 @@ kvo_status kvo_paged_attn_workspace(const kvo_paged_cache* cache, int n_q_heads,
  *   .. cu_k[b + 1] - 1; either may be empty.  causal: query token i sees the
  *   keys t <= i + (keys - queries), i.e. the last token sees them all (a chunk
  *   of a prompt behind cached keys has more keys than queries); 0: every key.
- *   o: bf16 [total_q][n_q_heads][head_dim], contiguous; lse (optional): fp32
- *   [total_q][n_q_heads], natural log.  Softmax scale 1/sqrt(head_dim), fp32
+ *   o: bf16 [total_q][n_q_heads][head_dim], contiguous, apart from q, k and v;
+ *   lse (optional): fp32 [total_q][n_q_heads], natural log.  Softmax scale 1/sqrt(head_dim), fp32
  *   accumulation, weights rounded to bf16, o rounded once to bf16.  A row that
  *   sees no key gets o = 0, lse = -inf; rows outside every request keep their
  *   bytes.  One request's values never reach another's rows; within a request a

@@ -295,10 +295,10 @@ PyObject* py_paged_append(PyObject*, PyObject* const* a, Py_ssize_t n) {
         int32_t* status = status_of(a[15], dev);
         launch(dev, [&] {
             return kvo_paged_append(&c, k.t.data_ptr(), k.tok, v.t.data_ptr(), v.tok, T, cu, start, freq, rot, inter, amp,
-                                    qp, qt, int32_size(hq, "n_q_heads"), qp ? q_out.data_ptr() : nullptr, k_out, status,
+                                    qp, qt, int32_size(hq, "n_q_heads"), q_out.defined() ? q_out.data_ptr() : nullptr, k_out, status,
                                     stream.handle);
         });
-        if (!qp) Py_RETURN_NONE;
+        if (!q_out.defined()) Py_RETURN_NONE;          // (an empty q has no address)
         return THPVariable_Wrap(q_out);
     });
 }

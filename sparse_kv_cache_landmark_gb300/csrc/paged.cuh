@@ -57,6 +57,14 @@ __device__ __forceinline__ int warp_find(int n, int64_t key, F first) {
     return lo;
 }
 
+// Host: whether two byte ranges share a byte.
+inline bool ranges_meet(const void* a, int64_t na, const void* b, int64_t nb) {
+    const uintptr_t x = (uintptr_t)a, y = (uintptr_t)b;
+    return na > 0 && nb > 0 && x < y + (uintptr_t)nb && y < x + (uintptr_t)na;
+}
+// Host: bytes from the first to the last of `n` bf16 rows of `len` values, `stride` apart.
+inline int64_t rows_bytes(int64_t n, int64_t stride, int64_t len) { return n > 0 ? 2 * ((n - 1) * stride + len) : 0; }
+
 // Host: a message for a cache descriptor that no call may use, or NULL.
 inline const char* paged_cache_error(const kvo_paged_cache* c) {
     if (!c) return "null cache";
@@ -70,7 +78,7 @@ inline const char* paged_cache_error(const kvo_paged_cache* c) {
         return "n_pages * n_kv_heads * page_size must fit in 31 bits";
     if ((int64_t)c->batch * c->n_kv_heads > (1 << 20)) return "batch * n_kv_heads must be <= 2^20";
     if (c->format != KVO_PAGES_BF16 && c->format != KVO_PAGES_E4M3) return "format must be KVO_PAGES_BF16 or KVO_PAGES_E4M3";
-    if (!c->k_pages || !c->v_pages || !c->table) return "null pages or table";
+    if (!c->k_pages || !c->v_pages || (!c->table && c->batch > 0)) return "null pages or table";
     if ((uintptr_t)c->k_pages % 16 || (uintptr_t)c->v_pages % 16) return "pages must be 16-byte aligned";
     if (c->format == KVO_PAGES_E4M3 && (!c->k_scale || !c->v_scale)) return "e4m3 pages need k_scale and v_scale";
     return nullptr;

@@ -472,15 +472,28 @@ extern "C" kvo_status kvo_paged_append(const kvo_paged_cache* cache, const void*
     auto bad = [](const char* m) { set_last_error(m); return KVO_ERR_INVALID; };
     if (const char* m = paged_cache_error(cache)) return bad(m);
     if (tokens < 0 || tokens > INT32_MAX) return bad("tokens must be in 0..2^31 - 1");
-    if (tokens == 0 || cache->batch == 0) return KVO_OK;
-    if (!k || !v || !start) return bad("null k, v or start");
+    if (tokens == 0 || (cache->batch == 0 && cu)) return KVO_OK;
     if (!cu && tokens != cache->batch) return bad("without cu every request appends one token: tokens must equal batch");
+    if (!k || !v || !start) return bad("null k, v or start");
     const int D = cache->head_dim, hkv = cache->n_kv_heads;
     if (freq && (rot_dim < 16 || rot_dim % 16 || rot_dim > D)) return bad("rot_dim must be a multiple of 16 in 16..head_dim");
     if (q && (!q_out || n_q_heads < 1 || n_q_heads > 4096)) return bad("q needs q_out and n_q_heads in 1..4096");
     for (const void* p : {k, v, q, (const void*)q_out, (const void*)k_out})
         if ((uintptr_t)p % 16) return bad("k, v, q, q_out and k_out must be 16-byte aligned");
     if (k_token_stride % 8 || v_token_stride % 8 || q_token_stride % 8) return bad("strides must be multiples of 8 elements");
+    // an output is its input in place, row for row, or apart from everything that the call reads
+    struct Rows { const void* at; int64_t stride, len; } in[3] = {{k, k_token_stride, (int64_t)hkv * D},
+                                                                  {v, v_token_stride, (int64_t)hkv * D},
+                                                                  {q, q_token_stride, (int64_t)n_q_heads * D}};
+    struct Out { void* at; int64_t len; int own; } out[2] = {{k_out, (int64_t)hkv * D, 0}, {q ? q_out : nullptr, (int64_t)n_q_heads * D, 2}};
+    for (const Out& o : out)
+        for (int i = 0; o.at && i < 3; ++i) {
+            if (!in[i].at || !ranges_meet(o.at, 2 * tokens * o.len, in[i].at, rows_bytes(tokens, in[i].stride, in[i].len))) continue;
+            if (i != o.own || o.at != in[i].at || (tokens > 1 && in[i].stride != o.len))
+                return bad("k_out and q_out must be apart from the inputs, or k and q themselves where those are contiguous");
+        }
+    if (k_out && q && ranges_meet(k_out, 2 * tokens * out[0].len, q_out, 2 * tokens * out[1].len))
+        return bad("k_out and q_out must not overlap");
 
     AppendArgs A{};
     A.pages[0] = (uint8_t*)cache->k_pages;

@@ -1037,6 +1037,8 @@ extern "C" kvo_status kvo_paged_attn(const kvo_paged_cache* cache, const void* q
     const PaPlan plan = paged_attn_plan(G, paged_attn_bound(cache, blocks ? n_blocks : 0, max_len));
     const size_t need = paged_attn_workspace(plan, G, r, D);
     if (need && (!workspace || workspace_bytes < need)) return bad("the workspace is too small (kvo_paged_attn_workspace)");
+    const int64_t bytes = 2ll * cache->batch * n_q_heads * D;
+    if (ranges_meet(o, bytes, q, bytes)) return bad("o must not overlap q");
     const bool fp8 = cache->format == KVO_PAGES_E4M3;
     const int rb = fp8 ? D : 2 * D;
     CUtensorMap mk, mv;

@@ -510,6 +510,11 @@ extern "C" kvo_status kvo_prompt_attn(const void* q, int64_t q_token_stride, con
         return bad("token strides must cover the heads");
     if (q_token_stride > (1ll << 38) || k_token_stride > (1ll << 38) || v_token_stride > (1ll << 38))
         return bad("token strides must be below 2^38 elements");
+    const int64_t o_bytes = rows_bytes(total_q, (int64_t)n_q_heads * head_dim, (int64_t)n_q_heads * head_dim);
+    if (ranges_meet(o, o_bytes, q, rows_bytes(total_q, q_token_stride, (int64_t)n_q_heads * head_dim)) ||
+        ranges_meet(o, o_bytes, k, rows_bytes(total_k, k_token_stride, (int64_t)n_kv_heads * head_dim)) ||
+        ranges_meet(o, o_bytes, v, rows_bytes(total_k, v_token_stride, (int64_t)n_kv_heads * head_dim)))
+        return bad("o must not overlap q, k or v");
     PromptArgs A{};
     A.cu_q = cu_q;
     A.cu_k = cu_k;

@@ -58,6 +58,8 @@ extern "C" kvo_status kvo_rope(const void* x, int64_t x_token_stride, int64_t x_
     if ((uintptr_t)x % 16 || (uintptr_t)out % 16) return bad("x and out must be 16-byte aligned");
     if (x_token_stride % 8 || x_head_stride % 8 || out_token_stride % 8 || out_head_stride % 8)
         return bad("strides must be multiples of 8 elements");
+    if ((tokens > 1 && out_token_stride == 0) || (heads > 1 && out_head_stride == 0))
+        return bad("rows of out must not share memory");
     if (x == out && (x_token_stride != out_token_stride || x_head_stride != out_head_stride))
         return bad("in place needs equal strides");
     const int units = head_dim / 16;

@@ -462,3 +462,38 @@ def test_calls_on_a_stream_of_their_own():
         torch.cuda.synchronize()
         for (o, lse), y in outs:
             assert torch.equal(o, want[0]) and torch.equal(lse, want[1]) and torch.equal(y, want_x)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, E4M3])
+def test_no_requests(dtype):
+    """An empty batch: empty results, the pools as they were."""
+    fp8 = dtype == E4M3
+    kp, vp = (torch.zeros(3, 2, 16, 64, device="cuda").to(dtype) for _ in range(2))
+    sc = torch.full((3, 2), 0.5, device="cuda") if fp8 else None
+    none = torch.empty(0, 2, 64, dtype=torch.bfloat16, device="cuda")
+    table, start = torch.empty(0, 4, dtype=torch.int32, device="cuda"), torch.empty(0, dtype=torch.int32, device="cuda")
+    q = torch.empty(0, 8, 64, dtype=torch.bfloat16, device="cuda")
+    status = i32([0])
+    q_out = kvo.paged_append(none, none, kp, vp, table, start, k_scale=sc, v_scale=sc, q=q, status=status)
+    o, lse = kvo.paged_attn(q, kp, vp, table, start, k_scale=sc, v_scale=sc, status=status)
+    assert q_out.shape == o.shape == (0, 8, 64) and lse.shape == (0, 8) and int(status) == 0
+    assert not kp.view(torch.uint8).any() and not vp.view(torch.uint8).any()
+    o, lse = kvo.prompt_attn(q, none, none, i32([0]), status=status)
+    assert o.shape == (0, 8, 64) and lse.shape == (0, 8) and int(status) == 0
+
+
+def test_append_in_place_on_both_paths():
+    """k_out is k and q_out is q, contiguous, for one token each and for packed prompts."""
+    g = gen(77)
+    freq, amp = kvo.rope_frequencies(128)
+    for cu, start in ((None, [3, 20, 0]), ([0, 1, 1, 3], [3, 20, 0])):
+        k, v, q = normal(g, 3, 2, 128), normal(g, 3, 2, 128), normal(g, 3, 8, 128)
+        kw = dict(freq=freq, amplitude=amp, cu=None if cu is None else i32(cu))
+        table = i32([[0, 1], [2, 3], [4, 5]])
+        pools = [torch.zeros(6, 2, 16, 128, dtype=torch.bfloat16, device="cuda") for _ in range(4)]
+        k_out = torch.empty_like(k)
+        q_out = kvo.paged_append(k, v, pools[0], pools[1], table, i32(start), q=q, k_out=k_out, **kw)
+        k2, q2 = k.clone(), q.clone()
+        assert kvo.paged_append(k2, v, pools[2], pools[3], table, i32(start), q=q2, q_out=q2, k_out=k2, **kw) is q2
+        assert torch.equal(k2, k_out) and torch.equal(q2, q_out)
+        assert torch.equal(pools[0], pools[2]) and torch.equal(pools[1], pools[3])

@@ -162,3 +162,42 @@ def test_prompt_attention_without_tokens(lib):
     cu = torch.zeros(2, dtype=torch.int32)
     with pytest.raises(kvo.KvoError, match="CUDA device"):
         kvo.prompt_attn(bf(4, 2, 64), bf(4, 1, 64), bf(4, 1, 64), cu)
+
+
+@pytest.mark.parametrize("kw", [dict(ot=0), dict(oh=0), dict(ot=0, oh=0)])
+def test_rope_refuses_outputs_that_share_rows(lib, kw):
+    a = dict(ot=256, oh=128)
+    a.update(kw)
+    refused(lib, lib.kvo_rope(P, 256, 128, 2 * P, a["ot"], a["oh"], P, P, 4, 2, 128, 128, 0, 1.0, None), "share memory")
+
+
+@pytest.mark.parametrize("kw,frag", [
+    (dict(k_out=P + 128), "apart"), (dict(k_out=P, kt=512), "apart"), (dict(k_out=2 * P), "apart"),
+    (dict(q_out=3 * P + 1024), "apart"), (dict(q_out=3 * P, qt=2048), "apart"), (dict(q_out=P), "apart"),
+    (dict(k_out=3 * P), "apart"), (dict(q_out=5 * P, k_out=5 * P + 1024), "must not overlap")])
+def test_append_refuses_overlapping_outputs(lib, kw, frag):
+    """Two tokens of 2 and 8 heads of 128: rows of 512 and 2048 bytes; k, v and q at P, 2 P and 3 P."""
+    a = dict(kt=256, qt=1024, q_out=4 * P, k_out=6 * P)
+    a.update(kw)
+    refused(lib, lib.kvo_paged_append(cache(), P, a["kt"], 2 * P, 256, 2, None, P, None, 0, 0, 1.0, 3 * P, a["qt"], 8,
+                                      a["q_out"], a["k_out"], None, None), frag)
+
+
+def test_attention_refuses_outputs_over_inputs(lib):
+    for o in (P, P + 1024, P - 2048):                   # q: 2 x 8 x 128 values, 4096 bytes
+        refused(lib, lib.kvo_paged_attn(cache(), P, 8, P, 0, None, None, 0, o, P, None, 0, None, None), "overlap q")
+    for o in (16 * P, 32 * P, 48 * P, 48 * P - 256):
+        refused(lib, lib.kvo_prompt_attn(16 * P, 1024, 32 * P, 256, 48 * P, 256, P, P, 2, 10, 10, 8, 2, 128, 1, o, P, None,
+                                         None), "overlap")
+
+
+def test_calls_for_no_requests(lib):
+    """A table without rows has no address."""
+    c = cache(batch=0, table=None)
+    assert lib.kvo_paged_attn(c, None, 8, None, 0, None, None, 0, None, None, None, 0, None, None) == kvo.KVO_OK
+    assert lib.kvo_paged_append(c, None, 256, None, 256, 0, None, None, None, 0, 0, 1.0, None, 0, 0, None, None, None,
+                                None) == kvo.KVO_OK
+    assert lib.kvo_paged_append(c, P, 256, P, 256, 3, P, P, None, 0, 0, 1.0, None, 0, 0, None, None, None,
+                                None) == kvo.KVO_OK
+    refused(lib, lib.kvo_paged_append(c, P, 256, P, 256, 3, None, P, None, 0, 0, 1.0, None, 0, 0, None, None, None, None),
+            "tokens must equal batch")
