@@ -7,7 +7,9 @@
 // A work item is 256 query rows of one KV head: two tiles of 128 rows, each
 // floor(128 / r) tokens x the r query heads of the group, so that every K and V
 // tile is fetched once for the whole group and short prompts fill their tiles.
-// One CTA per item and SM, heaviest items first:
+// One CTA per item and SM, heaviest items first (or, where few items would leave
+// SMs idle, a cluster of 2, 4 or 8 CTAs that split the item's keys and join their
+// parts through distributed shared memory, in a fixed order):
 //   warp 9   loads Q once and K, V tiles of 128 keys through a ring (TMA),
 //   warps 8, 10  one thread each issues the tcgen05.mma of tile 0 and 1: S_t =
 //            Q_t K^T (shared x shared) and O_t += P_t V (tensor memory x
@@ -26,7 +28,9 @@
 // commits, against 2048 at full rate; the kernel runs one in 2790.  P in shared
 // memory would take 2120, but then products, P and the tiles that arrive ask for
 // 3070 cycles of shared-memory bandwidth.  An item's start and end (its first
-// loads, its last softmax and rows) add about 5 us.
+// loads, its last softmax and rows) add about 5 us, the join of split items 5 more:
+// 64 KB of fp32 rows come from the other CTAs' shared memory at about 10 bytes a
+// cycle and SM, 3.5 us.
 //
 // Measured (32 query and 8 KV heads of 128): 16384 tokens 1400 us (1570 TFLOP/s, 0.83
 // of cuBLAS's bf16 rate here), 8192 356 us (1540), 3 chunks of 4099 tokens in all
@@ -127,10 +131,35 @@ __device__ __forceinline__ bool pr_wait(PrShared& sh, const PromptArgs& A, uint6
     return pr_wait_long(&sh.abort, A.status, b, parity, A.wait_ns);
 }
 
-// The softmax of one tile: a thread owns row `row` of it; the row sees its request's keys [0, limit).
+// One part of an item: 256 rows of fp32 values in shared memory, each with its maximum and sum.  16-byte chunks, turned
+// by the row against bank conflicts.
 template <int D>
+__device__ __forceinline__ float4* pr_part_row(uint8_t* part, int i, int chunk) {
+    return reinterpret_cast<float4*>(part) + i * (D / 4) + (chunk ^ (i & 7));
+}
+template <int D>
+__device__ __forceinline__ float2* pr_part_ml(uint8_t* part, int i) {
+    return reinterpret_cast<float2*>(part + 2 * PR_ROWS * D * 4) + i;
+}
+__device__ __forceinline__ float2 ld_cluster_f32x2(const void* local, uint32_t rank) {
+    uint32_t remote;
+    float2 v;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(remote) : "r"(smem_u32(local)), "r"(rank));
+    asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(remote) : "memory");
+    return v;
+}
+__device__ __forceinline__ float4 ld_cluster_f32x4(const void* local, uint32_t rank) {
+    uint32_t remote;
+    float4 v;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(remote) : "r"(smem_u32(local)), "r"(rank));
+    asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(remote) : "memory");
+    return v;
+}
+
+// The softmax of one tile: a thread owns row `row` of it; the row sees its request's keys [0, limit).
+template <int D, bool SPLIT>
 __device__ __forceinline__ void pr_softmax(PrShared& sh, const PromptArgs& A, int t, int n_tiles, int limit, bool real,
-                                           int64_t out_row, uint8_t* q_smem) {
+                                           int64_t out_row, uint8_t* smem) {
     const uint32_t lanes = (uint32_t)(threadIdx.x & 96) << 16;          // this warp's quarter of the lanes
     const uint32_t S = sh.tmem + 128 * t + lanes, O = sh.tmem + 256 + D * t + lanes;
     float m = -INFINITY, l = 0.f;                                       // log2 units; l in units of 2^m
@@ -211,7 +240,28 @@ __device__ __forceinline__ void pr_softmax(PrShared& sh, const PromptArgs& A, in
         ok = __all_sync(0xffffffffu, ok);
         tc_fence_after();
     }
+    if constexpr (SPLIT) {
+        // Both tiles' products are done: what they read may be overwritten.  After a wait that ran out too: nothing
+        // else reads it any more.
+        bar_named(1, 256);
+        const int i = threadIdx.x;
+        if (n_tiles > 0) {
+#pragma unroll 1
+            for (int c = 0; c < D; c += 32) {
+                uint32_t o[32];
+                tmem_ld32(O + c, o);
+                tmem_wait_ld();
+#pragma unroll
+                for (int e = 0; e < 32; e += 4)
+                    *pr_part_row<D>(smem, i, (c + e) / 4) = make_float4(__uint_as_float(o[e]), __uint_as_float(o[e + 1]),
+                                                                        __uint_as_float(o[e + 2]), __uint_as_float(o[e + 3]));
+            }
+        }
+        *pr_part_ml<D>(smem, i) = make_float2(m, l);
+        return;
+    }
     if (!ok) return;
+    uint8_t* q_smem = smem + t * PrShape<D>::TILE;
     // The row goes through this warp's part of Q's memory (its tile's products are done), so that the warp writes
     // whole rows: 32 threads with a row each would touch 32 lines a store.  16-byte chunks, turned by the row against
     // bank conflicts.
@@ -255,7 +305,65 @@ __device__ __forceinline__ void pr_softmax(PrShared& sh, const PromptArgs& A, in
     if (real && A.lse) A.lse[out_row] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
 }
 
-template <int D>
+// Joins the parts of an item: this CTA takes every PARTS-th row.  A warp's lanes hold AT_ONCE rows; BATCH of those are
+// fetched together, since each takes the way to the other CTAs' shared memory and back.
+template <int D, int PARTS>
+__device__ __forceinline__ void pr_join(const PromptArgs& A, uint8_t* smem, int part, int g, int64_t qs, int nq, int tok0) {
+    constexpr int CH = D / 4, AT_ONCE = 32 / CH, ROWS = 2 * PR_ROWS / PARTS / 8, TURNS = ROWS / AT_ONCE;
+    constexpr int BATCH = TURNS < 16 / PARTS ? TURNS : 16 / PARTS;
+    static_assert(ROWS * PARTS == 32, "a lane for every maximum and sum of the warp's rows");
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, ch = lane % CH;
+    // Row w (0 .. ROWS - 1) of the warp is row (w * 8 + warp) * PARTS + part of the item.  Its lanes w * PARTS + k fetch part
+    // k's maximum and sum: a load of one address by the whole warp is as dear as 32 there.
+    const float2 ml = ld_cluster_f32x2(pr_part_ml<D>(smem, ((lane / PARTS) * 8 + warp) * PARTS + part), lane % PARTS);
+    float to = ml.x;
+#pragma unroll
+    for (int k = 1; k < PARTS; k <<= 1) to = fmaxf(to, __shfl_xor_sync(0xffffffffu, to, k));
+    const float f = ml.y == 0.f ? 0.f : pr_ex2(ml.x - to);     // a part that saw nothing has weight 0
+    float sum = f * ml.y;
+#pragma unroll
+    for (int k = 1; k < PARTS; k <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, k);
+    const float w_part = sum != 0.f ? f / sum : 0.f;
+    const float lse = sum == 0.f ? -INFINITY : (to + log2f(sum)) * 0.6931471805599453f;
+#pragma unroll 1
+    for (int x0 = 0; x0 < TURNS; x0 += BATCH) {
+        float4 o[BATCH][PARTS];
+        int64_t out[BATCH];        // the row in o, or none
+#pragma unroll
+        for (int y = 0; y < BATCH; ++y) {
+            const int i = (((x0 + y) * AT_ONCE + lane / CH) * 8 + warp) * PARTS + part;
+            const int t = i / PR_ROWS, row = i % PR_ROWS, tl = row / A.r, tok = tok0 + t * A.tq + tl;
+            out[y] = tl < A.tq && tok < nq ? (qs + tok) * A.hq + g * A.r + row - tl * A.r : -1;
+            if (out[y] < 0) continue;
+#pragma unroll
+            for (int k = 0; k < PARTS; ++k)
+                o[y][k] = k == part ? *pr_part_row<D>(smem, i, ch) : ld_cluster_f32x4(pr_part_row<D>(smem, i, ch), k);
+        }
+#pragma unroll
+        for (int y = 0; y < BATCH; ++y) {
+            const int w = (x0 + y) * AT_ONCE + lane / CH;
+            float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+            for (int k = 0; k < PARTS; ++k) {
+                const float c = __shfl_sync(0xffffffffu, w_part, w * PARTS + k);
+                if (c == 0.f) continue;        // its memory may hold anything
+                acc.x += c * o[y][k].x;
+                acc.y += c * o[y][k].y;
+                acc.z += c * o[y][k].z;
+                acc.w += c * o[y][k].w;
+            }
+            const float row_lse = __shfl_sync(0xffffffffu, lse, w * PARTS);
+            if (out[y] < 0) continue;
+            const __nv_bfloat162 a = __floats2bfloat162_rn(acc.x, acc.y), b = __floats2bfloat162_rn(acc.z, acc.w);
+            *reinterpret_cast<uint2*>(A.o + out[y] * D + 4 * ch) =
+                make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b));
+            if (ch == 0 && A.lse) A.lse[out[y]] = row_lse;
+        }
+    }
+}
+
+// SPLIT: a cluster of CTAs shares an item's keys and joins its parts.
+template <int D, bool SPLIT>
 __global__ void __launch_bounds__(PR_THREADS, 1)
 prompt_attn_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_k,
                    const __grid_constant__ CUtensorMap map_v, const __grid_constant__ PromptArgs A) {
@@ -293,7 +401,8 @@ prompt_attn_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
         }
 
     // Request b has ceil(nq / TU) items; its slots start at floor(cu_q[b] / TU) + b, which leaves room for them.
-    const int g = blockIdx.x % A.hkv, u = A.units - 1 - (int)(blockIdx.x / A.hkv);
+    const int parts = SPLIT ? (int)cluster_size() : 1, part = SPLIT ? (int)cluster_rank() : 0, item = blockIdx.x / parts;
+    const int g = item % A.hkv, u = A.units - 1 - item / A.hkv;
     int64_t j0, qs, qe, ks, ke;
     if (A.batch <= 32) {                       // all offsets in one round of loads
         const bool have = lane < A.batch;
@@ -326,7 +435,16 @@ prompt_attn_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
         const int64_t see = A.causal ? min(max((int64_t)tok0 + t * A.tq + have + (nk - nq), (int64_t)0), (int64_t)nk) : nk;
         n_t[t] = have ? (int)((see + PR_KEYS - 1) / PR_KEYS) : 0;
     }
-    const int n = max(n_t[0], n_t[1]);
+    int n = max(n_t[0], n_t[1]), first = 0;        // tiles of keys of this CTA, and the first of them
+    if (SPLIT) {
+        first = (int)((int64_t)n * part / parts);
+        const int mine = (int)((int64_t)n * (part + 1) / parts) - first;
+        n_t[0] = min(max(n_t[0] - first, 0), mine);
+        n_t[1] = min(max(n_t[1] - first, 0), mine);
+        n = max(n_t[0], n_t[1]);
+    }
+    const int key_first = first * PR_KEYS, nk_here = nk - key_first;
+    ks += key_first;
 
     if (warp == 9 && lane == 0 && n > 0) {     // Q and the first keys
         mbar_expect_tx(smem_u32(&sh.kv_full[0]), P::TILE);
@@ -369,7 +487,7 @@ prompt_attn_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
                 const uint32_t dst = ring + st * P::TILE;
                 // The last tile of a request runs into what lies behind it.  Its keys are masked as scores, but
                 // a weight of zero does not silence a NaN or an infinity in V: those rows are cleared here.
-                const bool tail = is_v && key0 + PR_KEYS > nk;
+                const bool tail = is_v && key0 + PR_KEYS > nk_here;
                 const uint32_t bar = smem_u32(tail ? &sh.v_tail : &sh.kv_full[st]);
                 if (lane == 0) {
                     mbar_expect_tx(bar, P::TILE);
@@ -380,7 +498,7 @@ prompt_attn_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
                     ok = pr_wait(sh, A, sh.v_tail, 0);
                     if (!__all_sync(0xffffffffu, ok)) break;
                     for (int x = 0; x < D / 64; ++x)
-                        for (uint32_t a = (nk - key0) * 128 + lane * 16; a < PR_BLOCK; a += 512)
+                        for (uint32_t a = (nk_here - key0) * 128 + lane * 16; a < PR_BLOCK; a += 512)
                             asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(dst + x * PR_BLOCK + a), "r"(0) : "memory");
                     fence_async_smem();
                     __syncwarp();
@@ -454,6 +572,7 @@ prompt_attn_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
             mbar_wait_bounded(smem_u32(&sh.drain[t]), 0, A.wait_ns);
         }
         __syncwarp();
+        if constexpr (SPLIT) { cluster_barrier(); cluster_barrier(); }     // as below
     } else {
         regs_inc<208>();
         const int t = warp >> 2, row = tid & 127;
@@ -462,8 +581,16 @@ prompt_attn_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
         const bool real = tl < A.tq && tok < nq;
         int limit = 0;
         if (real) limit = A.causal ? (int)min(max((int64_t)tok + 1 + (nk - nq), (int64_t)0), (int64_t)nk) : nk;
-        pr_softmax<D>(sh, A, t, n_t[t], limit, real, (qs + tok) * A.hq + g * A.r + head,
-                      smem_raw + (base - smem_u32(smem_raw)) + t * P::TILE);
+        uint8_t* smem = smem_raw + (base - smem_u32(smem_raw));
+        if (SPLIT) limit = max(limit - key_first, 0);
+        pr_softmax<D, SPLIT>(sh, A, t, n_t[t], limit, real, (qs + tok) * A.hq + g * A.r + head, smem);
+        if constexpr (SPLIT) {
+            cluster_barrier();
+            if (parts == 2) pr_join<D, 2>(A, smem, part, g, qs, nq, tok0);
+            else if (parts == 4) pr_join<D, 4>(A, smem, part, g, qs, nq, tok0);
+            else pr_join<D, 8>(A, smem, part, g, qs, nq, tok0);
+            cluster_barrier();         // nobody leaves while its part is read
+        }
     }
     tc_fence_before();
     __syncthreads();
@@ -471,17 +598,40 @@ prompt_attn_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
     if (warp == 8) tmem_free(sh.tmem, 512);
 }
 
-template <int D>
+template <int D, bool SPLIT>
 cudaError_t prompt_attn_launch(const CUtensorMap& q, const CUtensorMap& k, const CUtensorMap& v, const PromptArgs& A,
-                               unsigned ctas, cudaStream_t s) {
+                               int parts, unsigned items, cudaStream_t s) {
     static std::atomic<uint64_t> done{0};
     if (first_on_device(done)) {
         const cudaError_t e =
-            cudaFuncSetAttribute(prompt_attn_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, PrShape<D>::SMEM);
+            cudaFuncSetAttribute(prompt_attn_kernel<D, SPLIT>, cudaFuncAttributeMaxDynamicSharedMemorySize, PrShape<D>::SMEM);
         if (e != cudaSuccess) return e;
         mark_on_device(done);
     }
-    return launch_dependent(prompt_attn_kernel<D>, dim3(ctas), PR_THREADS, PrShape<D>::SMEM, s, 0, q, k, v, A);
+    return launch_dependent(prompt_attn_kernel<D, SPLIT>, dim3(items * parts), PR_THREADS, PrShape<D>::SMEM, s,
+                            SPLIT ? parts : 0, q, k, v, A);
+}
+
+// How many CTAs share an item's keys: the number whose items end first by estimate.  The host knows means only: `items`
+// items of `least` to `most` tiles of keys.  An item takes 1.36 us per tile and 6 us besides, 11 where parts are joined;
+// 152 items run at once, or 76, 36 and 14 clusters of 2, 4 and 8 (as measured: larger clusters leave SMs idle).  The
+// end is that of the longest item, or the mean time of the items in each place, the last round with the shortest.
+// Measured in us, unsplit / split in 2 / 4 / 8, 32 and 8 heads of 128, tokens behind cached keys: 1 behind 8000 101 / 57
+// / 32 / 19, 64 behind 2000 31 / 24 / 18 / 16, 512 behind 1500 29 / 23 / 34 / 65, 256 behind 32000 363 / 194 / 104 / 174,
+// 1400 behind 32000 736 / 588 / 533 / 703; but 512 alone 12.3 / 14.3 / 25 / 58, 1024 behind 32000 374 / 389 / 417 / 523,
+// 8192 alone 360 / 478 / 648 / 1143.  The estimate is within a fifth of these.
+int prompt_attn_parts(int64_t items, int64_t least, int64_t most) {
+    struct { int parts, fit; double us; } const choice[] = {{1, 152, 6.}, {2, 76, 11.}, {4, 36, 11.}, {8, 14, 11.}};
+    const double lo = 1.36 * (double)least, hi = 1.36 * (double)most;
+    int best = 1;
+    double first = INFINITY;
+    for (const auto& c : choice) {
+        const double rounds = (double)items / c.fit;
+        const double t = std::max(hi / c.parts + c.us, rounds * ((lo + hi) / 2 / c.parts + c.us) +
+                                                           (ceil(rounds) - rounds) * (lo / c.parts + c.us));
+        if (t < first) { first = t; best = c.parts; }
+    }
+    return best;
 }
 
 }  // namespace kvo
@@ -548,8 +698,14 @@ extern "C" kvo_status kvo_prompt_attn(const void* q, int64_t q_token_stride, con
         return KVO_ERR_CUDA;
     }
     cudaStream_t s = (cudaStream_t)stream;
-    const cudaError_t e = head_dim == 128 ? prompt_attn_launch<128>(mq, mk, mv, A, (unsigned)ctas, s)
-                                          : prompt_attn_launch<64>(mq, mk, mv, A, (unsigned)ctas, s);
+    const int64_t tu = 2 * A.tq, items = std::max((total_q + tu - 1) / tu, std::min<int64_t>(batch, total_q)) * n_kv_heads;
+    const int64_t keys = total_k / batch, unseen = causal ? std::min(total_q / batch, keys) : 0;    // by the first token
+    const int parts = prompt_attn_parts(items, (keys - unseen + PR_KEYS - 1) / PR_KEYS, (keys + PR_KEYS - 1) / PR_KEYS);
+    if (ctas * parts > INT32_MAX) return bad("too many tokens");
+    cudaError_t e;
+#define KVO_PROMPT(D_) (parts > 1 ? prompt_attn_launch<D_, true>(mq, mk, mv, A, parts, (unsigned)ctas, s) : prompt_attn_launch<D_, false>(mq, mk, mv, A, 1, (unsigned)ctas, s))
+    e = head_dim == 128 ? KVO_PROMPT(128) : KVO_PROMPT(64);
+#undef KVO_PROMPT
     if (e != cudaSuccess) { set_last_error(cudaGetErrorString(e)); return KVO_ERR_CUDA; }
     return KVO_OK;
 }

@@ -73,6 +73,50 @@ def test_prompt_attention_long(d, r, n, scale):
     check_rows(q, k, v, o, lse, [0, n], [0, n], True, rows=[0, 1, 127, 128, 129, 255, 256, 640, n // 2, n - 2, n - 1])
 
 
+@pytest.mark.parametrize("d,hkv,r", [(128, 8, 4), (64, 16, 2)])
+def test_prompt_attention_fills_the_device(d, hkv, r):
+    """Enough items that each has a CTA of its own."""
+    g = gen(d)
+    n = 1300
+    q, k, v = normal(g, n, hkv * r, d, scale=3.0), normal(g, n, hkv, d), normal(g, n, hkv, d)
+    o, lse = kvo.prompt_attn(q, k, v, i32([0, n]))
+    check_rows(q, k, v, o, lse, [0, n], [0, n], True, rows=[0, 127, 128, 700, n - 1])
+
+
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("d,hkv,r,nq,nk", [
+    (128, 1, 4, [5], [1500]), (64, 1, 1, [1], [2000]), (128, 2, 3, [50], [1153]), (64, 1, 16, [3], [1024]),
+    (128, 1, 2, [5, 0, 40], [3000, 700, 17]), (64, 2, 5, [1, 9, 300], [4000, 1, 260]), (128, 8, 4, [200], [1500]),
+    (64, 8, 4, [130, 60], [2500, 900]), (128, 8, 4, [500], [2000]), (64, 4, 8, [300], [2100])])
+def test_prompt_attention_splits_long_keys(causal, d, hkv, r, nq, nk):
+    """Few query rows and many keys: a cluster shares each item's keys.  Parts without a tile, requests that end within
+    the first part, rows that see nothing, and NaN behind the last key."""
+    g = gen(sum(nk) + r)
+    cq, ck = cuts(nq), cuts(nk)
+    q, k, v = (normal(g, n, h, d, scale=s) for n, h, s in ((cq[-1], hkv * r, 2.0), (ck[-1] + 40, hkv, 1.0), (ck[-1] + 40, hkv, 1.0)))
+    k[ck[-1]:], v[ck[-1]:] = math.nan, math.nan
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    o, lse = kvo.prompt_attn(q, k, v, i32(cq), i32(ck), causal, status=status)
+    assert int(status.item()) == 0
+    check_rows(q, k, v, o, lse, cq, ck, causal, rows=[0, 1, 4, 30, 39, 63, 64, 129, 199, 299, 499])
+    again = kvo.prompt_attn(q, k, v, i32(cq), i32(ck), causal)
+    assert torch.equal(again[0], o) and torch.equal(again[1], lse)
+
+
+def test_prompt_attention_split_ignores_other_requests():
+    """A request of NaN keys and values and one with bad offsets beside one whose keys are split."""
+    g = gen(61)
+    q, k, v = normal(g, 30, 4, 128), normal(g, 5000, 1, 128), normal(g, 5000, 1, 128)
+    k[2300:], v[2300:] = math.nan, math.nan
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    o = torch.full((30, 4, 128), 7.0, dtype=torch.bfloat16, device="cuda")
+    lse = torch.full((30, 4), 7.0, device="cuda")
+    kvo.prompt_attn(q, k, v, i32([0, 10, 15, 20]), i32([0, 2300, 4000, 5001]), o=o, lse=lse, status=status)
+    assert int(status.item()) == kvo.DEV_BAD_COUNT
+    check_rows(q, k, v, o, lse, [0, 10], [0, 2300], True)
+    assert bool(o[10:15].isnan().all()) and bool((o[15:] == 7.0).all()) and bool((lse[15:] == 7.0).all())
+
+
 def test_prompt_attention_keeps_requests_apart():
     """Views of a fused projection with NaN in the padding and in a neighbour: other requests' rows stay clean, and
     rows behind the last request keep their bytes."""
