@@ -42,6 +42,7 @@
 #include <stdio.h>
 
 #include <algorithm>
+#include <type_traits>
 
 #include "launch.cuh"
 #include "paged.cuh"
@@ -373,12 +374,6 @@ __device__ __forceinline__ void arrive_copied(uint32_t mbar) {
 }
 __device__ __forceinline__ void prefetch_l1(const void* p) { asm volatile("prefetch.global.L1 [%0];" ::"l"(p)); }
 
-__device__ __forceinline__ void pa_store(const PagedAttnArgs& A, int64_t row, int d, int col, float acc, float m, float l,
-                                         float lw) {
-    A.o[row * d + col] = __bfloat16_as_ushort(__float2bfloat16_rn(lw != 0.f ? acc / lw : 0.f));
-    if (col == 0) A.lse[row] = l == 0.f ? -INFINITY : (m + log2f(l) - PA_BIAS) * 0.6931471805599453f;
-}
-
 // Query fragments of group g: heads 8 x + lane / 4 as columns (heads beyond r: zero), and the scores' factors of the
 // lane's heads 8 x + 2c, 8 x + 2c + 1.
 template <int D, bool FP8, int NH>
@@ -682,35 +677,53 @@ paged_cluster_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_con
         if (col == 0) { dst[D] = m; dst[D + 1] = l; dst[D + 2] = lw; }
     }
     cluster_barrier();
-    for (int i = tid + rank * PA_THREADS; i < A.r * D; i += PA_THREADS * size) {
-        const int row = i / D, col = i - row * D;
-        const float* src = cl + row * MS;
-        float m = -INFINITY, acc = 0.f, l = 0.f, lw = 0.f;
-        for (uint32_t k0 = 0; k0 < size; k0 += 8) {          // eight CTAs' loads in flight
-            float mk[8], lk[8], wk[8], ok[8];
+    // W lanes hold 4 columns each of a row; the warp's 32 / W groups of lanes take every (32 / W)-th CTA's part.  Lane k of
+    // 16 fetches CTA k's maximum and sums: a load of one address by the whole warp is as dear there as 32.
+    auto join = [&](auto width) {
+        constexpr int W = decltype(width)::value, N = 32 / W, RUNS = D / (4 * W), MOST = 16;    // CTAs of a cluster at most
+        for (int u = rank * PA_WARPS + warp; u < A.r * RUNS; u += size * PA_WARPS) {
+            const int row = u / RUNS, col = ((u - row * RUNS) * W + lane % W) * 4;
+            const float* src = cl + row * MS;
+            const float4 ml = lane % MOST < size ? ld_cluster_f32x4(src + D, lane % MOST) : make_float4(-INFINITY, 0.f, 0.f, 0.f);
+            float4 acc = make_float4(0.f, 0.f, 0.f, 0.f), o[MOST / N];
 #pragma unroll
-            for (int i8 = 0; i8 < 8; ++i8) {
-                const uint32_t k = min(k0 + i8, size - 1);
-                mk[i8] = ld_cluster_f32(src + D, k);
-                lk[i8] = ld_cluster_f32(src + D + 1, k);
-                wk[i8] = ld_cluster_f32(src + D + 2, k);
-                ok[i8] = ld_cluster_f32(src + col, k);
+            for (int i = 0; i < MOST / N; ++i)
+                if (N * i + lane / W < size) o[i] = ld_cluster_f32x4(src + col, N * i + lane / W);
+            float m = ml.x;
+#pragma unroll
+            for (int i = 1; i < MOST; i <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, i));
+            const float f = ml.y == 0.f ? 0.f : ex2(ml.x - m);
+            float l = f * ml.y, lw = f * ml.z;
+#pragma unroll
+            for (int i = 1; i < MOST; i <<= 1) {
+                l += __shfl_xor_sync(0xffffffffu, l, i);
+                if (!FP8) lw += __shfl_xor_sync(0xffffffffu, lw, i);
             }
-            float to = m;
+            if (FP8) lw = l;
 #pragma unroll
-            for (int i8 = 0; i8 < 8; ++i8) to = fmaxf(to, mk[i8]);
-            const float f0 = l == 0.f ? 0.f : ex2(m - to);
-            m = to;
-            l *= f0; lw *= f0; acc *= f0;
+            for (int i = 0; i < MOST / N; ++i) {
+                const float c = __shfl_sync(0xffffffffu, f, N * i + lane / W, MOST);
+                if (N * i + lane / W < size) { acc.x += c * o[i].x; acc.y += c * o[i].y; acc.z += c * o[i].z; acc.w += c * o[i].w; }
+            }
 #pragma unroll
-            for (int i8 = 0; i8 < 8; ++i8)
-                if (k0 + i8 < size && lk[i8] != 0.f) {
-                    const float f = ex2(mk[i8] - m);
-                    l += f * lk[i8]; lw += f * wk[i8]; acc += f * ok[i8];
-                }
+            for (int i = W; i < 32; i <<= 1) {
+                acc.x += __shfl_xor_sync(0xffffffffu, acc.x, i);
+                acc.y += __shfl_xor_sync(0xffffffffu, acc.y, i);
+                acc.z += __shfl_xor_sync(0xffffffffu, acc.z, i);
+                acc.w += __shfl_xor_sync(0xffffffffu, acc.w, i);
+            }
+            const int64_t to = (int64_t)g * A.r + row;
+            const bool some = lw != 0.f;
+            if (lane < W)
+                *reinterpret_cast<uint2*>(A.o + to * D + col) =
+                    make_uint2(some ? pack_bf(acc.x / lw, acc.y / lw) : 0u, some ? pack_bf(acc.z / lw, acc.w / lw) : 0u);
+            if (lane < W && col == 0) A.lse[to] = l == 0.f ? -INFINITY : (m + log2f(l) - PA_BIAS) * 0.6931471805599453f;
         }
-        pa_store(A, (int64_t)g * A.r + row, D, col, acc, m, l, lw);
-    }
+    };
+    // Large clusters have more warps than rows: they take runs of 32 columns (1 x 4096, 16 CTAs: 10.3 us, 10.9 with whole
+    // rows; but 32 x 512, one CTA: 13.8, and 12.5 with whole rows).
+    if (size > 8) join(std::integral_constant<int, 8>());
+    else join(std::integral_constant<int, D / 4>());
     cluster_barrier();             // nobody leaves while its states are read
 }
 

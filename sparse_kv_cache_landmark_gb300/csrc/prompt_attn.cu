@@ -141,21 +141,6 @@ template <int D>
 __device__ __forceinline__ float2* pr_part_ml(uint8_t* part, int i) {
     return reinterpret_cast<float2*>(part + 2 * PR_ROWS * D * 4) + i;
 }
-__device__ __forceinline__ float2 ld_cluster_f32x2(const void* local, uint32_t rank) {
-    uint32_t remote;
-    float2 v;
-    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(remote) : "r"(smem_u32(local)), "r"(rank));
-    asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(remote) : "memory");
-    return v;
-}
-__device__ __forceinline__ float4 ld_cluster_f32x4(const void* local, uint32_t rank) {
-    uint32_t remote;
-    float4 v;
-    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(remote) : "r"(smem_u32(local)), "r"(rank));
-    asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(remote) : "memory");
-    return v;
-}
-
 // The softmax of one tile: a thread owns row `row` of it; the row sees its request's keys [0, limit).
 template <int D, bool SPLIT>
 __device__ __forceinline__ void pr_softmax(PrShared& sh, const PromptArgs& A, int t, int n_tiles, int limit, bool real,
