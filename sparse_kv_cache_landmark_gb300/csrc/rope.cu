@@ -32,10 +32,11 @@ rope_kernel(const uint16_t* x, int64_t x_tok, int64_t x_head, uint16_t* out, int
     rope_heads(R, d, x + t * x_tok, x_head, out + t * out_tok, out_head, u, __ldg(pos + t), h0, h1);
 }
 
-// Heads a thread takes: 8 sincos (about 300 instructions) are spread over them, which on long inputs hides under
-// the loads from 4 heads on; more CTAs even out the last wave, and short inputs go down to one head a thread.
+// Heads a thread takes: 8 sincos (about 300 instructions) are spread over them, so as many as leave each SM 128 threads,
+// up to 8 (two batches of loads).  With 2048 threads an SM instead 500 tokens of 40 heads took 6.5 us for 4.7, 2000 10.8
+// for 8.0; with 32, 128 tokens 4.5 for 3.2.
 int rope_heads_per_thread(int64_t n, int heads) {
-    const int64_t want = 152 * 2048;
+    const int64_t want = 152 * 128;
     const int64_t splits = (want + n - 1) / n;
     return (int)std::max<int64_t>(1, std::min<int64_t>(8, heads / std::max<int64_t>(1, splits)));
 }
