@@ -11,7 +11,9 @@
 // takes their largest magnitude, settles the scale, moves rows of earlier calls
 // to it when it grew, and writes codes.  q is rotated by a second kernel that
 // starts beside the last pages: with its own register count it keeps half as many
-// loads again in flight as in one kernel with the pages (75.3 -> 68.5 us).
+// loads again in flight as in one kernel with the pages (75.3 -> 68.5 us before the
+// pages' rows were fetched a head ahead).  16391 tokens, 32 and 8 heads of 128 with
+// k_out, e4m3 pages of 64: 65.5 us, 6.1 TB/s (0.91 of a measured copy).
 //
 // One token per request: a warp owns one (token, head), of K and V or of q; each
 // lane turns D / 64 pairs, so the angles take one or two sincos in a row.  Bound by a
@@ -28,7 +30,7 @@
 
 namespace kvo {
 
-constexpr int APP_THREADS = 256;              // at most; small pages take smaller CTAs
+constexpr int APP_THREADS = 256;              // of the kernel of q, and of pages unless they are small or very large
 
 struct AppendArgs {
     uint8_t* pages[2];            // K, V
@@ -154,13 +156,19 @@ __device__ __forceinline__ uint2 quantise8(const uint4& v, float inv) {
     return make_uint2(codes[0], codes[1]);
 }
 
-template <int D, bool FP8, int MAXU>
-__device__ __forceinline__ void append_page(const AppendArgs& A, int block) {
+// A page's heads, by at most MAXT threads with MAXU units each.  AHEAD: the next head's rows are fetched while this
+// one's are worked on, and the angles make room for them in shared memory, [4 MAXU][MAXT] (dynamic).
+template <int D, bool FP8, int MAXU, int MAXT, bool AHEAD>
+__global__ void __launch_bounds__(MAXT) append_pages_kernel(const __grid_constant__ AppendArgs A) {
     constexpr int UNITS = D / 16;                       // 16-value units of a row
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, NT = blockDim.x;
+    const int block = blockIdx.x, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, NT = blockDim.x;
     const int u = block / A.runs, h0 = (block - u * A.runs) * A.run, h1 = min(A.hkv, h0 + A.run);
-    __shared__ uint32_t red[2][2][APP_THREADS / 32];    // by the head's parity: one barrier a head
+    __shared__ uint32_t red[2][2][MAXT / 32];           // by the head's parity: one barrier a head
+    extern __shared__ float4 angles[];
+    auto angle = [&](int i) -> float4& { return angles[i * MAXT + tid]; };
 
+    grid_wait();
+    grid_launch_next();            // the rotation of q may begin beside the last pages
     if (block == 0 && A.status) append_check(A);
     const AppendUnit U = append_unit(A, u);
     if (!U.ok) return;
@@ -180,8 +188,8 @@ __device__ __forceinline__ void append_page(const AppendArgs& A, int block) {
     int row[MAXU], ca[MAXU], cb[MAXU];
     float c[MAXU][8], s[MAXU][8];
     bool rot[MAXU];
-    uint4 xa[2][MAXU], xb[2][MAXU];
-    auto load = [&](int h) {
+    uint4 xa[2][MAXU], xb[2][MAXU], na[2][MAXU], nb[2][MAXU];
+    auto load = [&](int h, uint4 (&xa)[2][MAXU], uint4 (&xb)[2][MAXU]) {
 #pragma unroll
         for (int i = 0; i < MAXU; ++i)
             if (row[i] < rows) {
@@ -199,7 +207,7 @@ __device__ __forceinline__ void append_page(const AppendArgs& A, int block) {
         row[i] = w / UNITS;
         rope_chunks(A.R, D, w % UNITS, ca[i], cb[i]);
     }
-    load(h0);
+    load(h0, xa, xb);
     if (p < 0 || p >= A.n_pages) {                          // checked while the rows are on their way
         if (tid == 0 && h0 == 0) set_status(A.status, KVO_DEV_BAD_BLOCK_ID);
         return;
@@ -208,8 +216,28 @@ __device__ __forceinline__ void append_page(const AppendArgs& A, int block) {
     for (int i = 0; i < MAXU; ++i)
         rot[i] = row[i] < rows && rope_unit(A.R, (tid + i * NT) % UNITS, (int)(pos0 + row[i]), c[i], s[i]);
 
+    if (AHEAD) {
+#pragma unroll
+        for (int i = 0; i < MAXU; ++i)
+            if (rot[i]) {
+                angle(4 * i) = make_float4(c[i][0], c[i][1], c[i][2], c[i][3]);
+                angle(4 * i + 1) = make_float4(c[i][4], c[i][5], c[i][6], c[i][7]);
+                angle(4 * i + 2) = make_float4(s[i][0], s[i][1], s[i][2], s[i][3]);
+                angle(4 * i + 3) = make_float4(s[i][4], s[i][5], s[i][6], s[i][7]);
+            }
+    }
     for (int h = h0; h < h1; ++h) {
-        if (h > h0) load(h);
+        if (AHEAD) {
+            if (h > h0) {
+#pragma unroll
+                for (int i = 0; i < MAXU; ++i)
+#pragma unroll
+                    for (int x = 0; x < 2; ++x) { xa[x][i] = na[x][i]; xb[x][i] = nb[x][i]; }
+            }
+            if (h + 1 < h1) load(h + 1, na, nb);
+        } else if (h > h0) {
+            load(h, xa, xb);
+        }
         const int64_t slot = (int64_t)p * A.hkv + h;
         float old[2] = {0.f, 0.f};
         if (FP8 && row0 > 0) { old[0] = A.scale[0][slot]; old[1] = A.scale[1][slot]; }
@@ -217,7 +245,17 @@ __device__ __forceinline__ void append_page(const AppendArgs& A, int block) {
 #pragma unroll
         for (int i = 0; i < MAXU; ++i) {
             if (row[i] >= rows) continue;
-            if (rot[i]) rope_rotate(A.R.interleaved, c[i], s[i], xa[0][i], xb[0][i]);
+            if (rot[i]) {
+                if (AHEAD) {       // the thread's own words
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        const float4 vc = angle(4 * i + e), vs = angle(4 * i + 2 + e);
+                        c[i][4 * e] = vc.x; c[i][4 * e + 1] = vc.y; c[i][4 * e + 2] = vc.z; c[i][4 * e + 3] = vc.w;
+                        s[i][4 * e] = vs.x; s[i][4 * e + 1] = vs.y; s[i][4 * e + 2] = vs.z; s[i][4 * e + 3] = vs.w;
+                    }
+                }
+                rope_rotate(A.R.interleaved, c[i], s[i], xa[0][i], xb[0][i]);
+            }
             if (A.k_out) {
                 uint16_t* o = A.k_out + ((tok0 + row[i]) * A.hkv + h) * D;
                 *reinterpret_cast<uint4*>(o + ca[i]) = xa[0][i];
@@ -242,7 +280,7 @@ __device__ __forceinline__ void append_page(const AppendArgs& A, int block) {
         auto read_max = [&](int x) {
             uint32_t m = 0;
 #pragma unroll
-            for (int i = 0; i < APP_THREADS / 32; ++i)
+            for (int i = 0; i < MAXT / 32; ++i)
                 if (i < NT / 32) m = max(m, red[h & 1][x][i]);
             return m;
         };
@@ -287,13 +325,6 @@ __device__ __forceinline__ void append_page(const AppendArgs& A, int block) {
             }
         }
     }
-}
-
-template <int D, bool FP8, int MAXU>
-__global__ void __launch_bounds__(APP_THREADS) append_pages_kernel(const __grid_constant__ AppendArgs A) {
-    grid_wait();
-    grid_launch_next();            // the rotation of q may begin beside the last pages
-    append_page<D, FP8, MAXU>(A, blockIdx.x);
 }
 
 // Rotates packed q: (token, unit) pairs along x, runs of heads along y.  It depends on nothing that the pages' kernel
@@ -459,6 +490,37 @@ __global__ void __launch_bounds__(STEP_WARPS * 32) append_step_kernel(const __gr
     }
 }
 
+template <int D, bool FP8, int MAXU, int MAXT, bool AHEAD>
+cudaError_t append_pages_launch(const AppendArgs& A, unsigned ctas, int threads, cudaStream_t s) {
+    constexpr int smem = AHEAD ? 4 * MAXU * MAXT * (int)sizeof(float4) : 0;
+    if (smem > 48 * 1024) {
+        static std::atomic<uint64_t> done{0};
+        if (first_on_device(done)) {
+            const cudaError_t e = cudaFuncSetAttribute(append_pages_kernel<D, FP8, MAXU, MAXT, AHEAD>,
+                                                       cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+            if (e != cudaSuccess) return e;
+            mark_on_device(done);
+        }
+    }
+    return launch_dependent(append_pages_kernel<D, FP8, MAXU, MAXT, AHEAD>, dim3(ctas), threads, smem, s, 0, A);
+}
+
+// 16-value units of a page over 64 to 512 threads, 1 or 2 to a thread.  Rows of e4m3 pages are fetched a head ahead
+// where a CTA has several heads (16391 tokens x 8 heads with q, pages of 16 / 32 / 64: 75.5 -> 69.3, 77.8 -> 70.8, 69.5 ->
+// 65.5 us; with one head 2000 tokens took 13.4 for 12.4); bf16 pages, which wait for no scale, gain nothing by it (70.3
+// -> 71.4, 70.3 -> 72.9, 70.4 -> 69.0).  Pages of 128 rows in 256 threads of 4 units would take 206 registers.
+template <int D, bool FP8>
+cudaError_t append_pages(const AppendArgs& A, unsigned ctas, cudaStream_t s) {
+    const int units = A.page * (D / 16), nt = units > 512 ? 512 : std::min(APP_THREADS, units);
+    const bool ahead = FP8 && A.run > 1;
+    if constexpr (D == 128)
+        if (nt == 512)
+            return ahead ? append_pages_launch<D, FP8, 2, 512, FP8>(A, ctas, nt, s) : append_pages_launch<D, FP8, 2, 512, false>(A, ctas, nt, s);
+    if (units > nt)
+        return ahead ? append_pages_launch<D, FP8, 2, APP_THREADS, FP8>(A, ctas, nt, s) : append_pages_launch<D, FP8, 2, APP_THREADS, false>(A, ctas, nt, s);
+    return ahead ? append_pages_launch<D, FP8, 1, APP_THREADS, FP8>(A, ctas, nt, s) : append_pages_launch<D, FP8, 1, APP_THREADS, false>(A, ctas, nt, s);
+}
+
 int rope_heads_per_thread(int64_t n, int heads);
 
 }  // namespace kvo
@@ -536,24 +598,12 @@ extern "C" kvo_status kvo_paged_append(const kvo_paged_cache* cache, const void*
         A.units = (int)units;
         // The offsets and the angles of a page's rows cost about as much as one head's rest: where there are pages
         // enough to fill the device, a CTA takes up to 8 heads with them (16391 tokens x 8 heads, e4m3, with q: 80.5 us
-        // at 1 head, 73.2 at 2, 70.4 at 4, 68.5 at 8).
+        // at 1 head, 73.2 at 2, 70.4 at 4, 68.5 at 8, before rows were fetched ahead).
         A.run = (int)std::max<int64_t>(1, std::min<int64_t>(std::min(hkv, 8), units * hkv / 228));
         A.runs = (hkv + A.run - 1) / A.run;
-        // 16-value units of a page over 64 to 256 threads, 1, 2 or 4 to a thread
-        const int per_page = cache->page_size * (D / 16);
-        const int nt = std::min(APP_THREADS, per_page);
-        const int maxu = (per_page + nt - 1) / nt;
-        const dim3 grid((unsigned)(units * A.runs));
-#define KVO_APPEND(D_, F_, U_) e = launch_dependent(append_pages_kernel<D_, F_, U_>, grid, nt, 0, s, 0, A)
-        if (D == 128) {
-            if (maxu == 1) { if (fp8) KVO_APPEND(128, true, 1); else KVO_APPEND(128, false, 1); }
-            else if (maxu == 2) { if (fp8) KVO_APPEND(128, true, 2); else KVO_APPEND(128, false, 2); }
-            else { if (fp8) KVO_APPEND(128, true, 4); else KVO_APPEND(128, false, 4); }
-        } else {
-            if (maxu == 1) { if (fp8) KVO_APPEND(64, true, 1); else KVO_APPEND(64, false, 1); }
-            else { if (fp8) KVO_APPEND(64, true, 2); else KVO_APPEND(64, false, 2); }
-        }
-#undef KVO_APPEND
+        const unsigned ctas = (unsigned)(units * A.runs);
+        if (D == 128) e = fp8 ? append_pages<128, true>(A, ctas, s) : append_pages<128, false>(A, ctas, s);
+        else e = fp8 ? append_pages<64, true>(A, ctas, s) : append_pages<64, false>(A, ctas, s);
         if (q && e == cudaSuccess) {
             const int64_t n = tokens * (D / 16);
             A.q_per = rope_heads_per_thread(n, n_q_heads);
