@@ -1010,10 +1010,10 @@ cudaError_t paged_attn_launch(const CUtensorMap& mk, const CUtensorMap& mv, cons
         return launch_dependent(paged_cluster_kernel<D, FP8, NH>, plan.ctas, PA_THREADS, smem, s, plan.cluster, mk, mv, A);
     e = launch_dependent(paged_range_kernel<D, FP8, NH>, plan.ctas, PA_THREADS, smem, s, 0, mk, mv, A);
     if (e != cudaSuccess) return e;
-    // as many warps to a pair as keep the device's about 9000 warps (8 CTAs of 8 to an SM) in one wave
+    // as many warps to a pair as keep them in one wave: 5 CTAs of 8 to an SM (50 registers a thread)
     const int64_t pairs = (int64_t)A.G * A.r;
     int slices = PA_JOIN;
-    while (slices > 1 && pairs * slices > 152 * 64) slices /= 2;
+    while (slices > 1 && pairs * slices > 152 * 40) slices /= 2;
     const dim3 grid((unsigned)((pairs * slices + PA_JOIN - 1) / PA_JOIN));
     return launch_dependent(paged_join_kernel<D>, grid, PA_JOIN * 32, 0, s, 0, A, slices);
 }
