@@ -7,9 +7,9 @@
 //
 // Bound by HBM: each KV head's bytes are read once for all r query heads of its
 // group.  Work: the tiles (8 KB of K and V: 32 tokens of 128 e4m3 values) of every
-// (request, KV head), laid out group after group, are cut into equal contiguous
-// ranges, one per warp, so ragged batches end together; the lengths are device
-// data, so each CTA finds its warps' ranges by a prefix sum.  A warp keeps its
+// (request, KV head), laid out group after group, are cut into contiguous ranges
+// of equal cost, one per warp, so ragged batches end together; the lengths are
+// device data, so each CTA finds its warps' ranges by a prefix sum.  A warp keeps its
 // next tiles in flight in its own ring of shared-memory stages, across the borders
 // of groups, and waits for no other warp.  TMA fills the stages (128-byte-swizzled
 // boxes of 16 rows, so that key and value fragments are read without bank
@@ -17,9 +17,9 @@
 // flight on an SM is enough: with 192 KB 16 x 64K-128K took 450 us instead of 433.
 // One pass: running maximum and sum in fp32 registers.
 //
-// Measured (e4m3, 32 query and 8 KV heads of 128): 16 x 32768 tokens 168 us (6.4 TB/s,
-// 0.94 of a measured copy), 16 x 65536-131072 433 us (6.8 TB/s, 1.0), 64 x 256-4096
-// 61 us (0.65: about 8 us until the first tile, 7 us for the join), 1 x 131072 57 us.
+// Measured (e4m3, 32 query and 8 KV heads of 128): 16 x 32768 tokens 166 us (6.5 TB/s,
+// 0.95 of a measured copy), 16 x 65536-131072 433 us (6.8 TB/s, 1.0), 64 x 256-4096
+// 55 us (0.72: about 7 us until the first tile, 5 us for the join), 1 x 131072 56 us.
 //
 // Tensor cores: mma.sync m16n8k16 on transposed products, S^T = K Q^T and O^T =
 // V^T P^T: tokens and value columns are the 16 matrix rows, query heads the 8
@@ -53,6 +53,9 @@ namespace kvo {
 
 constexpr int PA_WARPS = 4;
 constexpr int PA_THREADS = PA_WARPS * 32;
+// Tiles that a warp could take in the time it needs to take up a group (64 x 16-8192 tokens: 102 us with 0, 92.4 with 1, 89.4
+// with 2, 89.1 with 4; 128 x 500-1000: 46.7, 45.1, 44.9, 46.1).
+constexpr int PA_SWITCH = 2;
 constexpr int PA_SUB = 16;                    // tokens of a subtile (one k step of the value product, and of a TMA box)
 constexpr int PA_RING = 64 * 1024;            // bytes of stages per CTA
 constexpr float PA_RAISE = 8.f;               // log2: how far a score may pass the running maximum
@@ -727,7 +730,12 @@ paged_cluster_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_con
     cluster_barrier();             // nobody leaves while its states are read
 }
 
-// Equal ranges of all groups' tiles, one per warp.
+// 64-bit divisions are long; most numbers here are short.
+__device__ __forceinline__ long long pa_div(long long a, long long b) {
+    return (a | b) >> 31 ? a / b : (long long)((unsigned)a / (unsigned)b);
+}
+
+// Ranges of all groups' tiles, of equal cost, one per warp.
 template <int D, bool FP8, int NH>
 __global__ void __launch_bounds__(PA_THREADS, 2)
 paged_range_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v,
@@ -735,8 +743,7 @@ paged_range_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_const
     using S = PaShape<D, FP8>;
     extern __shared__ uint8_t smem_raw[];
     __shared__ PaShared<D, FP8> sh;
-    __shared__ long long s_scan[PA_WARPS], s_pre[PA_WARPS];
-    __shared__ int s_g[PA_WARPS];
+    __shared__ long long s_scan[2][PA_WARPS], s_to[2][PA_THREADS];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const uint32_t ring = (smem_u32(smem_raw) + 1023u) & ~1023u;
     const uint8_t* ring_p = smem_raw + (ring - smem_u32(smem_raw));
@@ -744,54 +751,69 @@ paged_range_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_const
     pa_init(sh);
     if (tid == 0) { tensor_map_prefetch(&map_k); tensor_map_prefetch(&map_v); }
     grid_wait();
-    // Prefix of the tiles over the CTA, by requests, or by groups where each has a list of its own: each thread's
-    // share, then shuffles within a warp, then the warps' totals through shared memory.
+    // Ranges are equal in cost: a group's tiles and PA_SWITCH for taking it up.  Prefixes of both over the CTA, by
+    // requests, or by groups where each has a list of its own: each thread's share, then shuffles within a warp, then the
+    // warps' totals through shared memory.
     const int heads = A.blocks ? 1 : A.hkv, units = A.G / heads, per = (units + PA_THREADS - 1) / PA_THREADS;
-    long long sum = 0, total = 0;
+    auto cost_of = [](int n) { return n > 0 ? n + PA_SWITCH : 0; };
+    long long cost = 0, tiles = 0, total = 0;
     for (int i = 0; i < per; ++i) {
         const int u = tid * per + i;
         if (u >= units) break;
-        sum += (long long)heads * tiles_of(u * heads);
+        const int n = tiles_of(u * heads);
+        tiles += (long long)heads * n;
+        cost += (long long)heads * cost_of(n);
         if (blockIdx.x == 0) pa_check_counts(A, u * heads);
     }
-    long long inc = sum;
+    long long cost_to = cost, tiles_to = tiles;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-        const long long x = __shfl_up_sync(0xffffffffu, inc, o);
-        if (lane >= o) inc += x;
+        const long long x = __shfl_up_sync(0xffffffffu, cost_to, o), y = __shfl_up_sync(0xffffffffu, tiles_to, o);
+        if (lane >= o) { cost_to += x; tiles_to += y; }
     }
-    if (lane == 31) s_scan[warp] = inc;
+    if (lane == 31) { s_scan[0][warp] = cost_to; s_scan[1][warp] = tiles_to; }
     __syncthreads();
+    long long all_tiles = 0;
 #pragma unroll
     for (int w = 0; w < PA_WARPS; ++w) {
-        if (w < warp) inc += s_scan[w];
-        total += s_scan[w];
+        if (w < warp) { cost_to += s_scan[0][w]; tiles_to += s_scan[1][w]; }
+        total += s_scan[0][w];
+        all_tiles += s_scan[1][w];
     }
-    const long long pre = inc - sum;
-    // two tiles at least to a warp, at most 512 parts to join for a group, and warps spread over the CTAs before they
-    // fill them
-    const long long n_warp = max(1ll, min(min((long long)gridDim.x * PA_WARPS, 512ll * A.G), total / 2));
-    const long long each = total / n_warp, extra = total - each * n_warp;       // the first `extra` warps take one more
-    auto start = [&](long long w) { return w < n_warp ? each * w + min(w, extra) : total; };
-#pragma unroll
-    for (int w = 0; w < PA_WARPS; ++w) {
-        const long long lo = start((long long)w * gridDim.x + blockIdx.x);
-        if (lo >= pre && lo < pre + sum) {
-            long long at = pre;
-            for (int i = 0; i < per; ++i) {
-                const int u = tid * per + i, n = u < units ? tiles_of(u * heads) : 0;
-                if (lo < at + (long long)n * heads) {
-                    const int h = (int)((lo - at) / n);
-                    s_g[w] = u * heads + h;
-                    s_pre[w] = at + (long long)h * n;
-                    break;
-                }
-                at += (long long)n * heads;
-            }
-        }
-    }
+    s_to[0][tid] = cost_to - cost;
+    s_to[1][tid] = tiles_to - tiles;
     __syncthreads();
     grid_launch_next();            // the join's CTAs may take their places; they wait for this grid's end
+    // a cost of two at least to a warp, at most 512 parts to join for a group, and warps spread over the CTAs before they
+    // fill them
+    const long long n_warp = max(1ll, min(min((long long)gridDim.x * PA_WARPS, 512ll * A.G), total / 2));
+    const long long each = pa_div(total, n_warp), extra = total - each * n_warp;    // the first `extra` warps take one more
+    auto start = [&](long long w) { return w < n_warp ? each * w + min(w, extra) : total; };
+    // The border at cost x, by the warp: the group it falls in, that group's cost prefix, and the tile it lies before, x less
+    // the prefix and PA_SWITCH, or the first.  Returns that tile's number among all.
+    auto border = [&](long long x, int& g, int& in, long long& before) {
+        if (x >= total) return all_tiles;
+        int seg = -1;
+#pragma unroll
+        for (int i = 0; i < PA_THREADS; i += 32) seg += __popc(__ballot_sync(0xffffffffu, s_to[0][i + lane] <= x));
+        long long c = s_to[0][seg], t = s_to[1][seg];
+        for (int u = seg * per;; ++u) {
+            const int n = u < units ? tiles_of(u * heads) : 0, k = cost_of(n);
+            if (u == seg * per + per - 1 || x < c + (long long)k * heads) {
+                const int h = (int)pa_div(x - c, max(k, 1));
+                before = c + (long long)h * k;
+                g = u * heads + h;
+                in = max((int)(x - before) - PA_SWITCH, 0);
+                return t + (long long)h * n + in;
+            }
+            c += (long long)k * heads;
+            t += (long long)n * heads;
+        }
+    };
+    const long long me = (long long)warp * gridDim.x + blockIdx.x;
+    int g0 = 0, t0 = 0, g1, t1;
+    long long before = 0, before1;     // cost of the groups before the one being finished
+    const long long at = border(start(me), g0, t0, before), count = border(start(me + 1), g1, t1, before1) - at;
     // groups with nothing to attend to
     for (int g = blockIdx.x; g < A.G; g += gridDim.x)
         if (tiles_of(g) == 0) {
@@ -799,13 +821,10 @@ paged_range_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_const
             for (int i = tid; i < A.r; i += PA_THREADS) A.lse[(int64_t)g * A.r + i] = -INFINITY;
             if (tid == 0) A.info[g] = make_int2(-1, -1);
         }
-    const long long me = (long long)warp * gridDim.x + blockIdx.x, lo = start(me), hi = start(me + 1);
-    if (lo >= hi) return;
-    long long before = s_pre[warp];    // tiles of the groups before the one being finished
+    if (count <= 0) return;
     int seg = 0;
     const int ws = warp * S::STAGES * S::STAGE;
-    pa_run<D, FP8, NH, false>(A, &map_k, &map_v, ring + ws, ring_p + ws, smem_u32(sh.bars[warp]), sh.info[warp], s_g[warp],
-                              (int)(lo - before), hi - lo, [&](PaState<D, FP8, NH>& T, int g, int n, int first, int done) {
+    pa_run<D, FP8, NH, false>(A, &map_k, &map_v, ring + ws, ring_p + ws, smem_u32(sh.bars[warp]), sh.info[warp], g0, t0, count, [&](PaState<D, FP8, NH>& T, int g, int n, int first, int done) {
         const bool whole = done == n;
         const long long slot = 2 * me + (seg ? 1 : 0);
         const int gr = lane >> 2, c = lane & 3;
@@ -845,11 +864,11 @@ paged_range_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_const
         if (lane == 0 && whole) A.info[g] = make_int2(-1, -1);
         if (lane == 0 && !whole && first == 0) {
             // the warp that holds the group's last tile
-            const long long last = before + n - 1, wide = extra * (each + 1);
+            const long long last = before + PA_SWITCH + n - 1, wide = extra * (each + 1);
             const long long w = last < wide ? last / (each + 1) : extra + (last - wide) / each;
             A.info[g] = make_int2((int)slot, (int)w);
         }
-        before += n;
+        before += n + PA_SWITCH;
         ++seg;
     });
 }
