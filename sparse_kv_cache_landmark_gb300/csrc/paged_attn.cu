@@ -960,21 +960,23 @@ __global__ void __launch_bounds__(PA_JOIN * 32) paged_join_kernel(const __grid_c
 // How a call is cut.
 // cluster > 0: that many CTAs per group in a cluster and no second launch.  Taken where the groups' clusters fit the
 // device at once with at most 1536 tokens a CTA, i.e. where latency counts: e4m3, 8 KV heads of 128, one request of
-// 4096 tokens 10.4 us against 13.8 as ranges, 4 of 8192 17.8 against 21.7, 16 of 4096 29.7 against 37.7; but one of
-// 32768 (2048 tokens a CTA) 27.8 against 25.0, one of 131072 86 against 57.
-// cluster 0: equal ranges over `ctas` CTAs, two to an SM (three are slower: 16 x 64K-128K 457 us against 430), with at
-// least 8 subtiles each at the lengths the caller bounds.  The host does not know the lengths: where they differ a
-// cluster per group waits for the longest.
+// 4096 tokens 10.4 us against 13.5 as ranges, 4 of 8192 17.4 against 20.2, 16 of 4096 29.9 against 33.3; but one of
+// 24576 and more (2048 tokens a CTA at 32768) 22.8 against 20.7.
+// cluster 0: ranges of equal cost over `ctas` CTAs, two to an SM (three are slower: 16 x 64K-128K 457 us against 430), with
+// at least 8 subtiles each at the lengths the caller bounds.  The host does not know the lengths: where they differ a
+// cluster per group waits for the longest (16 x 512-4096: 20.9 us against 20.0 as ranges).
 struct PaPlan {
     int cluster, ctas;
 };
 constexpr int PA_SLOTS = 2 * 152;             // CTAs of the range kernel
-constexpr int PA_FIT = 400;                   // CTAs in clusters that start at once, three to an SM; 448 in sevens do not
-PaPlan paged_attn_plan(int64_t groups, int64_t max_tokens) {
+// CTAs in clusters that start at once: three to an SM (448 in sevens do not), two with 16 heads' registers; clusters of
+// 16 fill a GPC less well (384, or 256 of 16 heads, do not start at once: 3 x 4096 tokens 19.9 us, 15.2 as ranges).
+int paged_attn_fit(int r, int cluster) { return cluster < 16 ? (r <= 8 ? 400 : 280) : (r <= 8 ? 300 : 200); }
+PaPlan paged_attn_plan(int64_t groups, int r, int64_t max_tokens) {
     const int64_t want = std::max<int64_t>(1, (max_tokens + 127) / 128);
     int64_t s = 0;
     for (int c : {1, 2, 3, 4, 6, 8, 12, 16})
-        if (c * groups <= PA_FIT && (c <= want || c == 1)) s = c;
+        if (c * groups <= paged_attn_fit(r, c) && (c <= want || c == 1)) s = c;
     if (s && max_tokens <= 1536 * s) return {(int)s, (int)(s * groups)};
     const int64_t subs = groups * ((max_tokens + PA_SUB - 1) / PA_SUB);
     return {0, (int)std::min<int64_t>(PA_SLOTS, std::max<int64_t>(1, (subs + 7) / 8))};
@@ -1047,7 +1049,7 @@ extern "C" kvo_status kvo_paged_attn_workspace(const kvo_paged_cache* cache, int
     *bytes_out = 0;
     if (const char* m = paged_attn_error(cache, n_q_heads, n_blocks, max_len)) return bad(m);
     const int G = cache->batch * cache->n_kv_heads;
-    *bytes_out = paged_attn_workspace(paged_attn_plan(std::max(G, 1), paged_attn_bound(cache, n_blocks, max_len)), G,
+    *bytes_out = paged_attn_workspace(paged_attn_plan(std::max(G, 1), n_q_heads / cache->n_kv_heads, paged_attn_bound(cache, n_blocks, max_len)), G,
                                       n_q_heads / cache->n_kv_heads, cache->head_dim);
     return KVO_OK;
 }
@@ -1066,7 +1068,7 @@ extern "C" kvo_status kvo_paged_attn(const kvo_paged_cache* cache, const void* q
     if ((uintptr_t)q % 16 || (uintptr_t)o % 16 || (uintptr_t)workspace % 256)
         return bad("q and o must be 16-byte aligned, the workspace 256-byte aligned");
     const int G = cache->batch * cache->n_kv_heads, r = n_q_heads / cache->n_kv_heads, D = cache->head_dim;
-    const PaPlan plan = paged_attn_plan(G, paged_attn_bound(cache, blocks ? n_blocks : 0, max_len));
+    const PaPlan plan = paged_attn_plan(G, r, paged_attn_bound(cache, blocks ? n_blocks : 0, max_len));
     const size_t need = paged_attn_workspace(plan, G, r, D);
     if (need && (!workspace || workspace_bytes < need)) return bad("the workspace is too small (kvo_paged_attn_workspace)");
     const int64_t bytes = 2ll * cache->batch * n_q_heads * D;
