@@ -9,11 +9,11 @@
 // Prompts: one CTA owns one page that the call touches, of one to eight KV heads,
 // so a page's scale needs no atomics: it holds the page's new rows in registers,
 // takes their largest magnitude, settles the scale, moves rows of earlier calls
-// to it when it grew, and writes codes.  q is rotated by a second kernel that
-// starts beside the last pages: with its own register count it keeps half as many
-// loads again in flight as in one kernel with the pages (75.3 -> 68.5 us before the
-// pages' rows were fetched a head ahead).  16391 tokens, 32 and 8 heads of 128 with
-// k_out, e4m3 pages of 64: 65.5 us, 6.1 TB/s (0.91 of a measured copy).
+// to it when it grew, and writes codes.  q is rotated by further CTAs of the same
+// launch, behind those of the pages (a second kernel that starts beside the last
+// pages took 70.3 us for 64.1 with pages of 16 rows, 65.4 for 66.0 with 64, 6.1 for
+// 5.1 at 500 tokens, and 4 us more of the host).  16391 tokens, 32 and 8 heads of 128
+// with k_out, e4m3 pages of 64: 66.0 us, 6.1 TB/s (0.90 of a measured copy).
 //
 // One token per request: a warp owns one (token, head), of K and V or of q; each
 // lane turns D / 64 pairs, so the angles take one or two sincos in a row.  Bound by a
@@ -30,7 +30,7 @@
 
 namespace kvo {
 
-constexpr int APP_THREADS = 256;              // of the kernel of q, and of pages unless they are small or very large
+constexpr int APP_THREADS = 256;              // of a CTA, unless pages are small or very large
 
 struct AppendArgs {
     uint8_t* pages[2];            // K, V
@@ -48,7 +48,8 @@ struct AppendArgs {
     int batch, hkv, hq, page, n_pages, max_pages;
     int units;                    // upper bound of the pages touched
     int runs, run;                // a CTA of pages takes `run` KV heads, `runs` CTAs a page
-    int q_per;                    // query heads per thread
+    int q_per, q_blocks;          // query heads per thread; CTAs for a run of so many
+    int page_ctas;                // CTAs of pages; those after them rotate q
     RopeArgs R;
 };
 
@@ -156,6 +157,28 @@ __device__ __forceinline__ uint2 quantise8(const uint4& v, float inv) {
     return make_uint2(codes[0], codes[1]);
 }
 
+// Rotates packed q: CTA `block` of them takes (token, unit) pairs of a run of q_per heads.
+template <int D>
+__device__ __forceinline__ void append_q(const AppendArgs& A, int block) {
+    constexpr int UNITS = D / 16;
+    const int run = block / A.q_blocks;
+    const int64_t k = (int64_t)(block - run * A.q_blocks) * blockDim.x + threadIdx.x;
+    if (k >= A.tokens * UNITS) return;
+    const int64_t t = k / UNITS;
+    const int u = (int)(k - t * UNITS);
+    int lo = 0, hi = A.batch;                                  // the last b with cu[b] <= t
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) / 2;
+        if (__ldg(A.cu + mid) <= t) lo = mid; else hi = mid;
+    }
+    int64_t t0, n;
+    int start;
+    if (request_range(A, lo, t0, n, start) && t >= t0 && t < t0 + n) {
+        const int h0 = run * A.q_per, h1 = min(A.hq, h0 + A.q_per);
+        rope_heads(A.R, D, A.q + t * A.q_tok, D, A.q_out + t * A.hq * D, D, u, (int)(start + (t - t0)), h0, h1);
+    }
+}
+
 // A page's heads, by at most MAXT threads with MAXU units each.  AHEAD: the next head's rows are fetched while this
 // one's are worked on, and the angles make room for them in shared memory, [4 MAXU][MAXT] (dynamic).
 template <int D, bool FP8, int MAXU, int MAXT, bool AHEAD>
@@ -168,8 +191,11 @@ __global__ void __launch_bounds__(MAXT) append_pages_kernel(const __grid_constan
     auto angle = [&](int i) -> float4& { return angles[i * MAXT + tid]; };
 
     grid_wait();
-    grid_launch_next();            // the rotation of q may begin beside the last pages
     if (block == 0 && A.status) append_check(A);
+    if (block >= A.page_ctas) {
+        append_q<D>(A, block - A.page_ctas);
+        return;
+    }
     const AppendUnit U = append_unit(A, u);
     if (!U.ok) return;
     const int start = U.start;
@@ -327,31 +353,6 @@ __global__ void __launch_bounds__(MAXT) append_pages_kernel(const __grid_constan
     }
 }
 
-// Rotates packed q: (token, unit) pairs along x, runs of heads along y.  It depends on nothing that the pages' kernel
-// writes, and starts after that kernel has waited for what came before; it waits for that kernel's end itself, as
-// what follows waits for this one's only.
-template <int D>
-__global__ void __launch_bounds__(APP_THREADS) append_q_kernel(const __grid_constant__ AppendArgs A) {
-    constexpr int UNITS = D / 16;
-    const int64_t k = (int64_t)blockIdx.x * APP_THREADS + threadIdx.x;
-    if (k < A.tokens * UNITS) {
-        const int64_t t = k / UNITS;
-        const int u = (int)(k - t * UNITS);
-        int lo = 0, hi = A.batch;                              // the last b with cu[b] <= t
-        while (hi - lo > 1) {
-            const int mid = (lo + hi) / 2;
-            if (__ldg(A.cu + mid) <= t) lo = mid; else hi = mid;
-        }
-        int64_t t0, n;
-        int start;
-        if (request_range(A, lo, t0, n, start) && t >= t0 && t < t0 + n) {
-            const int h0 = blockIdx.y * A.q_per, h1 = min(A.hq, h0 + A.q_per);
-            rope_heads(A.R, D, A.q + t * A.q_tok, D, A.q_out + t * A.hq * D, D, u, (int)(start + (t - t0)), h0, h1);
-        }
-    }
-    grid_wait();
-}
-
 constexpr int STEP_WARPS = 4;
 
 // One token per request: warp (b, h) appends K and V of KV head h, or rotates query head h - Hkv.
@@ -491,7 +492,7 @@ __global__ void __launch_bounds__(STEP_WARPS * 32) append_step_kernel(const __gr
 }
 
 template <int D, bool FP8, int MAXU, int MAXT, bool AHEAD>
-cudaError_t append_pages_launch(const AppendArgs& A, unsigned ctas, int threads, cudaStream_t s) {
+cudaError_t append_pages_launch(const AppendArgs& A, int64_t ctas, int threads, cudaStream_t s) {
     constexpr int smem = AHEAD ? 4 * MAXU * MAXT * (int)sizeof(float4) : 0;
     if (smem > 48 * 1024) {
         static std::atomic<uint64_t> done{0};
@@ -502,16 +503,20 @@ cudaError_t append_pages_launch(const AppendArgs& A, unsigned ctas, int threads,
             mark_on_device(done);
         }
     }
-    return launch_dependent(append_pages_kernel<D, FP8, MAXU, MAXT, AHEAD>, dim3(ctas), threads, smem, s, 0, A);
+    return launch_dependent(append_pages_kernel<D, FP8, MAXU, MAXT, AHEAD>, dim3((unsigned)ctas), threads, smem, s, 0, A);
 }
 
 // 16-value units of a page over 64 to 512 threads, 1 or 2 to a thread.  Rows of e4m3 pages are fetched a head ahead
 // where a CTA has several heads (16391 tokens x 8 heads with q, pages of 16 / 32 / 64: 75.5 -> 69.3, 77.8 -> 70.8, 69.5 ->
 // 65.5 us; with one head 2000 tokens took 13.4 for 12.4); bf16 pages, which wait for no scale, gain nothing by it (70.3
 // -> 71.4, 70.3 -> 72.9, 70.4 -> 69.0).  Pages of 128 rows in 256 threads of 4 units would take 206 registers.
+int append_threads(int page, int d) {
+    const int units = page * (d / 16);
+    return units > 512 ? 512 : std::min(APP_THREADS, units);
+}
 template <int D, bool FP8>
-cudaError_t append_pages(const AppendArgs& A, unsigned ctas, cudaStream_t s) {
-    const int units = A.page * (D / 16), nt = units > 512 ? 512 : std::min(APP_THREADS, units);
+cudaError_t append_pages(const AppendArgs& A, int64_t ctas, cudaStream_t s) {
+    const int units = A.page * (D / 16), nt = append_threads(A.page, D);
     const bool ahead = FP8 && A.run > 1;
     if constexpr (D == 128)
         if (nt == 512)
@@ -598,19 +603,21 @@ extern "C" kvo_status kvo_paged_append(const kvo_paged_cache* cache, const void*
         A.units = (int)units;
         // The offsets and the angles of a page's rows cost about as much as one head's rest: where there are pages
         // enough to fill the device, a CTA takes up to 8 heads with them (16391 tokens x 8 heads, e4m3, with q: 80.5 us
-        // at 1 head, 73.2 at 2, 70.4 at 4, 68.5 at 8, before rows were fetched ahead).
-        A.run = (int)std::max<int64_t>(1, std::min<int64_t>(std::min(hkv, 8), units * hkv / 228));
+        // at 1 head, 73.2 at 2, 70.4 at 4, 68.5 at 8, before rows were fetched ahead), and likewise where many requests touch
+        // many pages (100 requests of 7 tokens 17.9 us at 1 head, 13.4 at 3, 16.6 at 7).
+        A.run = (int)std::max<int64_t>(1, std::min<int64_t>(std::min(hkv, 8), std::max(tokens / cache->page_size * hkv / 228, units * hkv / 456)));
         A.runs = (hkv + A.run - 1) / A.run;
-        const unsigned ctas = (unsigned)(units * A.runs);
+        A.page_ctas = (int)(units * A.runs);
+        int64_t ctas = A.page_ctas;
+        if (q) {
+            const int64_t n = tokens * (D / 16), threads = append_threads(A.page, D);
+            A.q_per = rope_heads_per_thread(n, n_q_heads);
+            A.q_blocks = (int)((n + threads - 1) / threads);
+            ctas += (int64_t)A.q_blocks * ((n_q_heads + A.q_per - 1) / A.q_per);
+            if (ctas > INT32_MAX) return bad("too many tokens");
+        }
         if (D == 128) e = fp8 ? append_pages<128, true>(A, ctas, s) : append_pages<128, false>(A, ctas, s);
         else e = fp8 ? append_pages<64, true>(A, ctas, s) : append_pages<64, false>(A, ctas, s);
-        if (q && e == cudaSuccess) {
-            const int64_t n = tokens * (D / 16);
-            A.q_per = rope_heads_per_thread(n, n_q_heads);
-            const dim3 qgrid((unsigned)((n + APP_THREADS - 1) / APP_THREADS), (unsigned)((n_q_heads + A.q_per - 1) / A.q_per));
-            e = D == 128 ? launch_dependent(append_q_kernel<128>, qgrid, APP_THREADS, 0, s, 0, A)
-                         : launch_dependent(append_q_kernel<64>, qgrid, APP_THREADS, 0, s, 0, A);
-        }
     }
     if (e != cudaSuccess) { set_last_error(cudaGetErrorString(e)); return KVO_ERR_CUDA; }
     return KVO_OK;
