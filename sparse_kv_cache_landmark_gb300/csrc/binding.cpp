@@ -6,7 +6,7 @@
 #include <Python.h>
 
 #include <ATen/core/Tensor.h>
-#include <ATen/ops/empty.h>
+#include <ATen/cuda/EmptyTensor.h>
 #include <c10/cuda/CUDAFunctions.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
@@ -151,8 +151,9 @@ void launch(const at::Device& dev, F&& call) {
     if (st != KVO_OK) throw Refused{st, kvo_last_error(nullptr)};
 }
 
+// From torch's allocator, past the dispatcher (0.4 us less a tensor on the Grace host).
 at::Tensor empty(at::IntArrayRef shape, at::ScalarType dt, const at::Device& dev) {
-    return at::empty(shape, at::TensorOptions().dtype(dt).device(dev));
+    return at::TensorBase(at::detail::empty_cuda(shape, dt, dev, std::nullopt));
 }
 
 template <typename F>
