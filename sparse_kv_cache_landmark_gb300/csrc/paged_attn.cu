@@ -37,7 +37,9 @@
 // A group cut by range borders leaves partial (m, l, o) in the workspace, in
 // fp32, joined by a second kernel.  Small calls, where latency counts, take one
 // cluster per group instead, whose CTAs join through distributed shared memory
-// in the same launch.  Both join in a fixed order: results do not depend on timing.
+// in the same launch: each CTA leaves its part of a row in the memory of the CTA
+// that joins it (one barrier; reading the others' parts takes two, and 1 us more).
+// Both join in a fixed order: results do not depend on timing.
 #include <cuda.h>
 #include <stdio.h>
 
@@ -58,6 +60,9 @@ constexpr int PA_THREADS = PA_WARPS * 32;
 constexpr int PA_SWITCH = 2;
 constexpr int PA_SUB = 16;                    // tokens of a subtile (one k step of the value product, and of a TMA box)
 constexpr int PA_RING = 64 * 1024;            // bytes of stages per CTA
+// Bytes of the parts that a CTA of a cluster joins: ceil(units / CTAs) slots of as many parts as CTAs, 16 bytes for a lane
+// and 16 more each; the most is 8 rows over 6 CTAs (2 x 6 x 528), or 16 rows in runs of 8 lanes over 12 (6 x 12 x 144).
+constexpr int pa_parts_bytes(int nh) { return nh == 1 ? 6400 : 10496; }
 constexpr float PA_RAISE = 8.f;               // log2: how far a score may pass the running maximum
 constexpr float PA_BIAS = 6.f;                // log2: weights are held times 2^6 (f16's small end is 2^-24)
 
@@ -612,6 +617,11 @@ __device__ __forceinline__ void pa_init(PaShared<D, FP8>& sh) {
     __syncwarp();
 }
 
+// 64-bit divisions are long; most numbers here are short.
+__device__ __forceinline__ long long pa_div(long long a, long long b) {
+    return (a | b) >> 31 ? a / b : (long long)((unsigned)a / (unsigned)b);
+}
+
 // One thread-block cluster per group: its warps split the group's tiles, and the states are joined through shared
 // memory, then through distributed shared memory.
 template <int D, bool FP8, int NH>
@@ -624,18 +634,21 @@ paged_cluster_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_con
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const uint32_t ring = (smem_u32(smem_raw) + 1023u) & ~1023u;
     uint8_t* ring_p = smem_raw + (ring - smem_u32(smem_raw));
-    // After the copies the ring's memory holds the warps' states, [4][r][D + 4], and the CTA's, [r][D + 4].
+    // After the copies the ring's memory holds the warps' states, [4][r][D + 4]; behind it is what the cluster's CTAs leave
+    // to this one to join.
     float* mrg = reinterpret_cast<float*>(ring_p);
-    float* cl = reinterpret_cast<float*>(ring_p + 48 * 1024);
+    float* parts = reinterpret_cast<float*>(ring_p + PA_RING);
     constexpr int MS = D + 4;
+    cluster_arrive();              // this CTA has started: others may write to its memory
     pa_init(sh);
     if (tid == 0) { tensor_map_prefetch(&map_k); tensor_map_prefetch(&map_v); }
     grid_wait();
     const uint32_t rank = cluster_rank(), size = cluster_size();
     const int g = blockIdx.x / size, n = (pa_span(A, g) + S::TILE - 1) / S::TILE;
     if (tid == 0 && rank == 0) pa_check_counts(A, g);
-    const long long parts = (long long)PA_WARPS * size, me = (long long)rank * PA_WARPS + warp;
-    const int t0 = (int)(n * me / parts), t1 = (int)(n * (me + 1) / parts);
+    const int warps = PA_WARPS * size, me = rank * PA_WARPS + warp;
+    const int t0 = (int)pa_div((long long)n * me, warps), t1 = (int)pa_div((long long)n * (me + 1), warps);
+    for (int i = lane * 64; i < A.r * D; i += 32 * 64) prefetch_l1(A.q + (int64_t)g * A.r * D + i);
     const int ws = warp * S::STAGES * S::STAGE;
     pa_run<D, FP8, NH, true>(A, &map_k, &map_v, ring + ws, ring_p + ws, smem_u32(sh.bars[warp]), sh.info[warp], g, t0, t1 - t0,
                              [&](PaState<D, FP8, NH>& T, int, int, int, int) {
@@ -660,38 +673,45 @@ paged_cluster_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_con
             }
     });
     __syncthreads();
-    for (int i = tid; i < A.r * D; i += PA_THREADS) {
-        const int row = i / D, col = i - row * D;
-        float m = -INFINITY;
-#pragma unroll
-        for (int w = 0; w < PA_WARPS; ++w) m = fmaxf(m, mrg[(w * A.r + row) * MS + D]);
-        float acc = 0.f, l = 0.f, lw = 0.f;
-#pragma unroll
-        for (int w = 0; w < PA_WARPS; ++w) {
-            const float* src = mrg + (w * A.r + row) * MS;
-            if (src[D + 1] == 0.f) continue;
-            const float f = ex2(src[D] - m);
-            l += f * src[D + 1];
-            lw += f * src[D + 2];
-            acc += f * src[D + 3] * src[col];
-        }
-        float* dst = cl + row * MS;
-        dst[col] = acc;
-        if (col == 0) { dst[D] = m; dst[D + 1] = l; dst[D + 2] = lw; }
-    }
-    cluster_barrier();
-    // W lanes hold 4 columns each of a row; the warp's 32 / W groups of lanes take every (32 / W)-th CTA's part.  Lane k of
-    // 16 fetches CTA k's maximum and sums: a load of one address by the whole warp is as dear there as 32.
+    cluster_wait();                // all have started
+    // A row is cut into runs of W lanes with 4 columns each, which are joined by the CTAs in turn: unit u (row and run) by CTA
+    // u % size, as its slot u / size.  Every CTA leaves its part of a unit, its columns and (maximum, sum, sum of the rounded
+    // weights), in the joining CTA's memory.  There a warp's 32 / W groups of lanes take every (32 / W)-th part, and lane k of
+    // 16 part k's maximum and sums.
     auto join = [&](auto width) {
         constexpr int W = decltype(width)::value, N = 32 / W, RUNS = D / (4 * W), MOST = 16;    // CTAs of a cluster at most
-        for (int u = rank * PA_WARPS + warp; u < A.r * RUNS; u += size * PA_WARPS) {
-            const int row = u / RUNS, col = ((u - row * RUNS) * W + lane % W) * 4;
-            const float* src = cl + row * MS;
-            const float4 ml = lane % MOST < size ? ld_cluster_f32x4(src + D, lane % MOST) : make_float4(-INFINITY, 0.f, 0.f, 0.f);
-            float4 acc = make_float4(0.f, 0.f, 0.f, 0.f), o[MOST / N];
+        constexpr int STRIDE = 4 * W + 4;                           // floats of a part
+        for (int i = tid; i < A.r * (D / 4); i += PA_THREADS) {
+            const int row = i / (D / 4), col = (i - row * (D / 4)) * 4;
+            float m = -INFINITY;
 #pragma unroll
-            for (int i = 0; i < MOST / N; ++i)
-                if (N * i + lane / W < size) o[i] = ld_cluster_f32x4(src + col, N * i + lane / W);
+            for (int w = 0; w < PA_WARPS; ++w) m = fmaxf(m, mrg[(w * A.r + row) * MS + D]);
+            float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+            float l = 0.f, lw = 0.f;
+#pragma unroll
+            for (int w = 0; w < PA_WARPS; ++w) {
+                const float* src = mrg + (w * A.r + row) * MS;
+                const float4 ml = *reinterpret_cast<const float4*>(src + D), o = *reinterpret_cast<const float4*>(src + col);
+                if (ml.y == 0.f) continue;
+                const float f = ex2(ml.x - m), fo = f * ml.w;
+                l += f * ml.y;
+                lw += f * ml.z;
+                acc.x += fo * o.x;
+                acc.y += fo * o.y;
+                acc.z += fo * o.z;
+                acc.w += fo * o.w;
+            }
+            const int u = row * RUNS + col / (4 * W), slot = u / (int)size, to = u - slot * (int)size;
+            float* dst = parts + (slot * size + rank) * STRIDE;
+            st_cluster_f32x4(dst + col % (4 * W), to, acc);
+            if (col % (4 * W) == 0) st_cluster_f32x4(dst + 4 * W, to, make_float4(m, l, lw, 0.f));
+        }
+        cluster_barrier();
+        for (int slot = warp; slot * (int)size + (int)rank < A.r * RUNS; slot += PA_WARPS) {
+            const int u = slot * size + rank, row = u / RUNS, col = ((u - row * RUNS) * W + lane % W) * 4;
+            const float* src = parts + slot * size * STRIDE;
+            float4 ml = make_float4(-INFINITY, 0.f, 0.f, 0.f), acc = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (lane % MOST < size) ml = *reinterpret_cast<const float4*>(src + (lane % MOST) * STRIDE + 4 * W);
             float m = ml.x;
 #pragma unroll
             for (int i = 1; i < MOST; i <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, i));
@@ -705,8 +725,12 @@ paged_cluster_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_con
             if (FP8) lw = l;
 #pragma unroll
             for (int i = 0; i < MOST / N; ++i) {
-                const float c = __shfl_sync(0xffffffffu, f, N * i + lane / W, MOST);
-                if (N * i + lane / W < size) { acc.x += c * o[i].x; acc.y += c * o[i].y; acc.z += c * o[i].z; acc.w += c * o[i].w; }
+                const int k = N * i + lane / W;
+                const float c = __shfl_sync(0xffffffffu, f, k, MOST);
+                if (k < size) {
+                    const float4 o = *reinterpret_cast<const float4*>(src + k * STRIDE + (lane % W) * 4);
+                    acc.x += c * o.x; acc.y += c * o.y; acc.z += c * o.z; acc.w += c * o.w;
+                }
             }
 #pragma unroll
             for (int i = W; i < 32; i <<= 1) {
@@ -723,16 +747,10 @@ paged_cluster_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_con
             if (lane < W && col == 0) A.lse[to] = l == 0.f ? -INFINITY : (m + log2f(l) - PA_BIAS) * 0.6931471805599453f;
         }
     };
-    // Large clusters have more warps than rows: they take runs of 32 columns (1 x 4096, 16 CTAs: 10.3 us, 10.9 with whole
-    // rows; but 32 x 512, one CTA: 13.8, and 12.5 with whole rows).
+    // Large clusters have more warps than rows: they take runs of 32 columns (before the parts were left to the joining CTA,
+    // 1 x 4096, 16 CTAs: 10.3 us, 10.9 with whole rows; but 32 x 512, one CTA: 13.8, and 12.5 with whole rows).
     if (size > 8) join(std::integral_constant<int, 8>());
     else join(std::integral_constant<int, D / 4>());
-    cluster_barrier();             // nobody leaves while its states are read
-}
-
-// 64-bit divisions are long; most numbers here are short.
-__device__ __forceinline__ long long pa_div(long long a, long long b) {
-    return (a | b) >> 31 ? a / b : (long long)((unsigned)a / (unsigned)b);
 }
 
 // Ranges of all groups' tiles, of equal cost, one per warp.
@@ -960,11 +978,11 @@ __global__ void __launch_bounds__(PA_JOIN * 32) paged_join_kernel(const __grid_c
 // How a call is cut.
 // cluster > 0: that many CTAs per group in a cluster and no second launch.  Taken where the groups' clusters fit the
 // device at once with at most 1536 tokens a CTA, i.e. where latency counts: e4m3, 8 KV heads of 128, one request of
-// 4096 tokens 10.4 us against 13.5 as ranges, 4 of 8192 17.4 against 20.2, 16 of 4096 29.9 against 33.3; but one of
-// 24576 and more (2048 tokens a CTA at 32768) 22.8 against 20.7.
+// 4096 tokens 9.1 us against 13.5 as ranges, 4 of 8192 16.3 against 20.2, 16 of 4096 28.6 against 33.3; from 24576 on
+// (1536 tokens a CTA) ranges are as fast or faster (20.7).
 // cluster 0: ranges of equal cost over `ctas` CTAs, two to an SM (three are slower: 16 x 64K-128K 457 us against 430), with
 // at least 8 subtiles each at the lengths the caller bounds.  The host does not know the lengths: where they differ a
-// cluster per group waits for the longest (16 x 512-4096: 20.9 us against 20.0 as ranges).
+// cluster per group waits for the longest (16 x 512-4096: 19.8 us against 20.0 as ranges).
 struct PaPlan {
     int cluster, ctas;
 };
@@ -1015,11 +1033,11 @@ template <int D, bool FP8, int NH>
 cudaError_t paged_attn_launch(const CUtensorMap& mk, const CUtensorMap& mv, const kvo::PagedAttnArgs& A,
                               const kvo::PaPlan& plan, cudaStream_t s) {
     using namespace kvo;
-    const int smem = PA_RING + 1024;
+    const int smem = PA_RING + 1024, smem_cluster = smem + pa_parts_bytes(NH);
     static std::atomic<uint64_t> done{0};
     cudaError_t e = cudaSuccess;
     if (first_on_device(done)) {
-        e = cudaFuncSetAttribute(paged_cluster_kernel<D, FP8, NH>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+        e = cudaFuncSetAttribute(paged_cluster_kernel<D, FP8, NH>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem_cluster);
         if (e == cudaSuccess)
             e = cudaFuncSetAttribute(paged_cluster_kernel<D, FP8, NH>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
         if (e == cudaSuccess)
@@ -1028,7 +1046,7 @@ cudaError_t paged_attn_launch(const CUtensorMap& mk, const CUtensorMap& mv, cons
         mark_on_device(done);
     }
     if (plan.cluster)
-        return launch_dependent(paged_cluster_kernel<D, FP8, NH>, plan.ctas, PA_THREADS, smem, s, plan.cluster, mk, mv, A);
+        return launch_dependent(paged_cluster_kernel<D, FP8, NH>, plan.ctas, PA_THREADS, smem_cluster, s, plan.cluster, mk, mv, A);
     e = launch_dependent(paged_range_kernel<D, FP8, NH>, plan.ctas, PA_THREADS, smem, s, 0, mk, mv, A);
     if (e != cudaSuccess) return e;
     // as many warps to a pair as keep them in one wave: 5 CTAs of 8 to an SM (50 registers a thread)
