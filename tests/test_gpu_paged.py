@@ -178,6 +178,14 @@ def test_append_matches_definition(e4m3, d, hkv, hq, page, counts, starts, rot, 
             assert torch.equal(torch.nan_to_num(vs.cpu(), -1.0), torch.nan_to_num(want_vs, -1.0))
 
 
+@pytest.mark.parametrize("e4m3", [True, False])
+@pytest.mark.parametrize("d,page", [(128, 16), (128, 32), (128, 64), (128, 128), (64, 32), (64, 64), (64, 128)])
+def test_append_of_many_short_requests(e4m3, d, page):
+    """Several heads to a CTA, each kind of page: rows begun, a page's border passed, heads left over for the last CTA."""
+    counts, starts = [(5 * i) % 9 + 1 for i in range(70)], [(29 * i) % (2 * page) for i in range(70)]
+    test_append_matches_definition(e4m3, d, 7, 14, page, counts, starts, d // 2, d == 64)
+
+
 def test_append_extreme_values():
     """Zeros, the largest bf16, subnormals, infinities and NaN: scales from the finite values, NaN codes for the rest."""
     rows = torch.zeros(6, 1, 64)
@@ -282,6 +290,31 @@ def test_paged_attention_matches_reference(e4m3, d, hkv, r, page, lens):
             first = got
         check_attention(q, got, rows, hkv, ref.F16 if e4m3 else ref.BF16)
     assert int(status.item()) == 0
+
+
+@pytest.mark.parametrize("d,e4m3", [(128, True), (64, False), (64, True), (128, False)])
+@pytest.mark.parametrize("groups,r", [(390, 8), (200, 5), (133, 8), (100, 1), (66, 8), (50, 3), (33, 8), (18, 7), (280, 9), (140, 16),
+                                      (93, 11), (70, 16), (46, 16), (35, 13), (23, 16), (12, 16)])
+def test_paged_attention_in_clusters_of_every_size(groups, r, d, e4m3):
+    """1 to 16 CTAs a group (as many as fit for so many groups), most of whose warps have no tile."""
+    g = gen(groups + r)
+    lens = [(37 * i) % 71 for i in range(groups)]
+    lens[groups // 2], lens[-1] = 900, 300
+    (kp, vp), (ks, vs), table, rows = cache_of(g, lens, 1, 16, d, e4m3)
+    bound = 1500 if groups > 200 else 2100        # more than 15 x 128 tokens may take 16 CTAs, more than 1536 need two
+    wide = torch.zeros(groups, 140, dtype=torch.int32, device="cuda")
+    wide[:, :table.shape[1]] = table
+    q = normal(g, groups, r, d, scale=1.5)
+    got = kvo.paged_attn(q, kp, vp, wide, i32(lens), k_scale=ks, v_scale=vs, max_len=bound)
+    keep = sorted({0, 1, 2, 5, groups // 3, groups // 2, groups - 2, groups - 1})
+    check_attention(q[keep], (got[0][keep], got[1][keep]), [rows[i] for i in keep], 1, ref.F16 if e4m3 else ref.BF16)
+    again = kvo.paged_attn(q, kp, vp, wide, i32(lens), k_scale=ks, v_scale=vs, max_len=bound)
+    assert torch.equal(again[0], got[0]) and torch.equal(again[1], got[1])
+    # as ranges
+    long = torch.zeros(groups, 120000 // 16, dtype=torch.int32, device="cuda")
+    long[:, :table.shape[1]] = table
+    other = kvo.paged_attn(q, kp, vp, long, i32(lens), k_scale=ks, v_scale=vs)
+    check_attention(q[keep], (other[0][keep], other[1][keep]), [rows[i] for i in keep], 1, ref.F16 if e4m3 else ref.BF16)
 
 
 @pytest.mark.parametrize("e4m3", [True, False])
