@@ -782,6 +782,15 @@ kvo_status kvo_profile_trace(kvo_ctx* ctx, double* start_ms, double* end_ms, int
  */
 kvo_status kvo_set_wait_test(kvo_ctx* ctx, int64_t limit_ns, int skip_tile);
 
+/*
+ * kvo_set_call_wait_test -- the same for the context-free kvo_paged_attn, in
+ * the calls that this thread makes (and captures) from now on.  skip >= 0 makes
+ * every warp announce its tile number skip without copying it.  Errors:
+ * KVO_ERR_INVALID for limit_ns outside 1 ms .. 10 s or skip < -1.  Not for
+ * production use.
+ */
+kvo_status kvo_set_call_wait_test(int64_t limit_ns, int skip);
+
 /* Human-readable description of the last error of ctx (or of the last
  * context-free call when ctx is NULL).  Never NULL. */
 const char* kvo_last_error(const kvo_ctx* ctx);

@@ -297,5 +297,11 @@ cudaError_t prepare_attention(Ctx& c);
 
 // Sets the message kvo_last_error(NULL) returns (context-free calls).
 void set_last_error(const char* msg);
+// What kvo_set_call_wait_test set for the context-free attention calls of this thread.
+struct CallWait {
+    long long limit_ns = 2000000000LL;
+    int skip = -1;
+};
+extern thread_local CallWait call_wait;
 
 }  // namespace kvo

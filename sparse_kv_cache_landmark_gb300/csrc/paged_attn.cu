@@ -96,8 +96,9 @@ struct PagedAttnArgs {
     int2* info;                   // [G]: first slot and last warp of a group cut by range borders; x < 0: not cut
     int32_t* status;
     int batch, hkv, r, page, shift, n_pages, max_pages, n_blocks, G;
+    int warps;                    // of the range kernel
     float scale_log2;
-    long long wait_ns;
+    long long wait_ns, skip;      // skip: the tile that every warp announces without copying it (tests; -1: none)
 };
 
 __device__ __forceinline__ int pa_len(const PagedAttnArgs& A, int b) {
@@ -498,7 +499,7 @@ __device__ __forceinline__ bool pa_run(const PagedAttnArgs& A, const CUtensorMap
             if (have) mbar_expect_tx(b, __popc(have) * (S::STAGE / S::SUBS));
         }
         __syncwarp();
-        if (have >> lane & 1) {
+        if ((have >> lane & 1) && issued != A.skip) {
             const int slot = my_page * A.hkv + ih, row = slot * A.page + off;
 #pragma unroll
             for (int x = 0; x < S::NBOX; ++x) {
@@ -904,7 +905,9 @@ __global__ void __launch_bounds__(PA_JOIN * 32) paged_join_kernel(const __grid_c
     const bool have = pair < (int64_t)A.G * A.r;
     const int g = have ? (int)(pair / A.r) : 0, row = have ? (int)(pair - (int64_t)g * A.r) : 0;
     const int2 info = A.info[g];
-    const bool cut = have && info.x >= 0;
+    // A warp whose wait ran out leaves the words of the groups after it as they were in the workspace, whatever that is:
+    // only a range of this launch's warps is read, so that nothing past the workspace is, and no more parts than warps.
+    const bool cut = have && info.x >= 0 && info.x / 2 <= info.y && info.y < A.warps;
     const int n = cut ? info.y - info.x / 2 + 1 : 0;          // parts: the first warp's slot, then slot 0 of each warp after it
     auto part = [&](int i) { return (i == 0 ? (int64_t)info.x : 2 * ((int64_t)(info.x / 2) + i)) * A.r + row; };
     auto values = [&](int i, float (&o)[N]) {
@@ -1125,7 +1128,9 @@ extern "C" kvo_status kvo_paged_attn(const kvo_paged_cache* cache, const void* q
     A.n_blocks = n_blocks;
     A.G = G;
     A.scale_log2 = (float)(1.4426950408889634 / sqrt((double)D));
-    A.wait_ns = 2000000000LL;
+    A.warps = plan.ctas * PA_WARPS;
+    A.wait_ns = call_wait.limit_ns;
+    A.skip = call_wait.skip;
     cudaStream_t s = (cudaStream_t)stream;
     cudaError_t e;
 #define KVO_PAGED(D_, F_) (r <= 8 ? paged_attn_launch<D_, F_, 1>(mk, mv, A, plan, s) : paged_attn_launch<D_, F_, 2>(mk, mv, A, plan, s))

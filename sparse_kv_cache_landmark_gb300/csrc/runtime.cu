@@ -557,6 +557,7 @@ bool buf_ok(const kvo::Ctx& c, int buf) { return buf == 0 || buf == 1 || (c.resi
 
 }  // namespace
 
+thread_local kvo::CallWait kvo::call_wait;
 void kvo::set_last_error(const char* msg) { g_err = msg ? msg : ""; }
 
 extern "C" {
@@ -1415,6 +1416,16 @@ kvo_status kvo_set_wait_test(kvo_ctx* ctx, int64_t limit_ns, int skip_tile) {
     drop_graphs(c);
     c.att_wait_ns = limit_ns;
     c.att_skip_tile = skip_tile;
+    return KVO_OK;
+}
+
+kvo_status kvo_set_call_wait_test(int64_t limit_ns, int skip) {
+    if (limit_ns < 1000000 || limit_ns > 10000000000LL || skip < -1) {
+        kvo::set_last_error("need 1 ms <= limit_ns <= 10 s and skip >= -1");
+        return KVO_ERR_INVALID;
+    }
+    kvo::call_wait.limit_ns = limit_ns;
+    kvo::call_wait.skip = skip;
     return KVO_OK;
 }
 

@@ -30,6 +30,7 @@ EXPORTS = ["kv_offload_init", "kv_offload_destroy", "select_topk", "index_diff",
            "kvo_decode_step_dual", "kvo_set_gather_reserve", "kvo_set_graphs", "kvo_append",
            "kvo_set_attn_impl", "kvo_set_select_impl", "kvo_resident_slots", "kvo_resident_fetched",
            "kvo_set_prefetch_budget", "kvo_set_lowrank_keys", "kvo_plan_attention", "kvo_plan_select", "kvo_set_wait_test",
+           "kvo_set_call_wait_test",
            "kvo_set_spec_policy", "kvo_spec_stats", "kvo_rope", "kvo_paged_append", "kvo_paged_attn",
            "kvo_paged_attn_workspace", "kvo_prompt_attn"]
 PROFILE_KINDS = ["select", "diff", "coalesce", "gather_prefetch", "gather_urgent", "attention", "recon"]
@@ -98,6 +99,7 @@ def lib() -> ctypes.CDLL:
         L.kvo_set_lowrank_keys.argtypes = [P, I, I, VP, VP]
         L.kvo_append.argtypes = [P, VP, VP, VP]
         L.kvo_set_wait_test.argtypes = [P, ctypes.c_int64, I]
+        L.kvo_set_call_wait_test.argtypes = [ctypes.c_int64, I]
         L.kvo_set_spec_policy.argtypes = [P, I]
         L.kvo_spec_stats.argtypes = [P, ctypes.POINTER(ctypes.c_int64)]
         DP, IP = ctypes.POINTER(ctypes.c_double), ctypes.POINTER(ctypes.c_int32)
@@ -341,6 +343,11 @@ def prompt_attn(q, k, v, cu_q, cu_k=None, causal: bool = True, o=None, lse=None,
     int32 [batch + 1] offsets (cu_k None: cu_q).
     """
     return (_BINDING or _native()).prompt_attn(q, k, v, cu_q, cu_k, causal, o, lse, status, stream)
+
+
+def set_call_wait_test(limit_ns: int = 2_000_000_000, skip: int = -1):
+    """Bounded-wait test switch of this thread's context-free attention calls (C: kvo_set_call_wait_test)."""
+    _check(lib().kvo_set_call_wait_test(int(limit_ns), int(skip)))
 
 
 class Context:

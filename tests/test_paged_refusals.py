@@ -201,3 +201,10 @@ def test_calls_for_no_requests(lib):
                                 None) == kvo.KVO_OK
     refused(lib, lib.kvo_paged_append(c, P, 256, P, 256, 3, None, P, None, 0, 0, 1.0, None, 0, 0, None, None, None, None),
             "tokens must equal batch")
+
+
+@pytest.mark.parametrize("limit,skip", [(999999, -1), (10 ** 10 + 1, -1), (10 ** 9, -2)])
+def test_wait_switch_refuses_bad_limits(limit, skip):
+    with pytest.raises(kvo.KvoError, match="limit_ns"):
+        kvo.set_call_wait_test(limit, skip)
+    kvo.set_call_wait_test()
