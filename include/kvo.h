@@ -783,9 +783,11 @@ kvo_status kvo_profile_trace(kvo_ctx* ctx, double* start_ms, double* end_ms, int
 kvo_status kvo_set_wait_test(kvo_ctx* ctx, int64_t limit_ns, int skip_tile);
 
 /*
- * kvo_set_call_wait_test -- the same for the context-free kvo_paged_attn, in
- * the calls that this thread makes (and captures) from now on.  skip >= 0 makes
- * every warp announce its tile number skip without copying it.  Errors:
+ * kvo_set_call_wait_test -- the same for the context-free kvo_paged_attn and
+ * kvo_prompt_attn, in the calls that this thread makes (and captures) from now
+ * on.  skip >= 0 makes every warp of the former announce its tile number skip
+ * without copying it, and every CTA of the latter its load number skip (K and V
+ * of the first tile of keys are 0 and 1, of the next 2 and 3).  Errors:
  * KVO_ERR_INVALID for limit_ns outside 1 ms .. 10 s or skip < -1.  Not for
  * production use.
  */

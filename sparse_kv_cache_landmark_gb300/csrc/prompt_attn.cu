@@ -74,6 +74,7 @@ struct PromptArgs {
     long long total_q, total_k;
     int batch, hq, hkv, r, tq, causal, units;
     float scale_log2;
+    int skip;                      // the load (K(0), V(0), K(1), ..) that every CTA announces without copying it (tests; -1: none)
     long long wait_ns;
 };
 
@@ -110,6 +111,7 @@ struct PrShared {
     uint64_t q_full[2], kv_full[12], s_full[2][6], p_full[2][2], o_done[2], turn[2], drain[2], v_tail;
     uint32_t tmem;
     int abort;
+    int issued, tail_open;         // what the loading warp leaves: its loads, and whether one more is on its way into v_tail
 };
 
 // A wait that gives up after the limit, or once another warp has; every caller then leaves its loop.
@@ -226,8 +228,8 @@ __device__ __forceinline__ void pr_softmax(PrShared& sh, const PromptArgs& A, in
         tc_fence_after();
     }
     if constexpr (SPLIT) {
-        // Both tiles' products are done: what they read may be overwritten.  After a wait that ran out too: nothing
-        // else reads it any more.
+        // Both tiles' products are done: what they read may be overwritten.  After a wait that ran out loads may still land
+        // over the parts: the outputs are invalid then, and the loading warp waits for its loads before the CTA leaves.
         bar_named(1, 256);
         const int i = threadIdx.x;
         if (n_tiles > 0) {
@@ -375,7 +377,7 @@ prompt_attn_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
             mbar_init(smem_u32(&sh.drain[t]), 1);
         }
         mbar_init(smem_u32(&sh.v_tail), 1);
-        sh.abort = 0;
+        sh.abort = sh.issued = sh.tail_open = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
     grid_wait();
@@ -433,7 +435,7 @@ prompt_attn_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
 
     if (warp == 9 && lane == 0 && n > 0) {     // Q and the first keys
         mbar_expect_tx(smem_u32(&sh.kv_full[0]), P::TILE);
-        for (int x = 0; x < D / 64; ++x)
+        for (int x = 0; x < D / 64 && A.skip != 0; ++x)
             tma_load_3d(ring + x * PR_BLOCK, &map_k, 64 * x, g, (int)ks, smem_u32(&sh.kv_full[0]));
         for (int t = 0; t < 2; ++t) {
             if (n_t[t] == 0) continue;         // a tile that sees no key: nothing reads its Q
@@ -454,7 +456,7 @@ prompt_attn_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
         if (warp == 9 && n > 0) {
             // ------------------------------------------------ loads
             int issued = 1;
-            bool ok = true;
+            bool ok = true, tail_open = false;
             for (int i = 1; i < 2 * n; ++i) {
                 const int st = i % P::STAGES, jj = i >> 1, key0 = jj * PR_KEYS;
                 const bool is_v = i & 1;
@@ -476,12 +478,14 @@ prompt_attn_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
                 const uint32_t bar = smem_u32(tail ? &sh.v_tail : &sh.kv_full[st]);
                 if (lane == 0) {
                     mbar_expect_tx(bar, P::TILE);
-                    for (int x = 0; x < D / 64; ++x)
+                    for (int x = 0; x < D / 64 && i != A.skip; ++x)
                         tma_load_3d(dst + x * PR_BLOCK, is_v ? &map_v : &map_k, 64 * x, g, (int)ks + key0, bar);
                 }
                 if (tail) {
+                    tail_open = true;
                     ok = pr_wait(sh, A, sh.v_tail, 0);
                     if (!__all_sync(0xffffffffu, ok)) break;
+                    tail_open = false;
                     for (int x = 0; x < D / 64; ++x)
                         for (uint32_t a = (nk_here - key0) * 128 + lane * 16; a < PR_BLOCK; a += 512)
                             asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(dst + x * PR_BLOCK + a), "r"(0) : "memory");
@@ -491,14 +495,7 @@ prompt_attn_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
                 }
                 issued = i + 1;
             }
-            // After a wait that ran out: let every copy in flight land before the CTA may leave.
-            if (*(volatile int*)&sh.abort && lane == 0) {
-                for (int t = 0; t < 2; ++t)
-                    if (n_t[t] > 0) mbar_wait_bounded(smem_u32(&sh.q_full[t]), 0, A.wait_ns);
-                for (int i = max(0, issued - P::STAGES); i < issued; ++i)
-                    mbar_wait_bounded(smem_u32(&sh.kv_full[i % P::STAGES]), (i / P::STAGES) & 1, A.wait_ns);
-                if (issued < 2 * n && (issued & 1)) mbar_wait_bounded(smem_u32(&sh.v_tail), 0, A.wait_ns / 4);
-            }
+            if (lane == 0) { sh.issued = issued; sh.tail_open = tail_open; }
         } else if ((warp & 1) == 0 && lane == 0 && n_t[(warp - 8) >> 1] > 0) {
             // ------------------------------------------------ matrix products of one tile
             // The tensor cores queue a few instructions only; with a thread of its own for each tile, one tile's
@@ -554,7 +551,10 @@ prompt_attn_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
             }
             // nothing of this CTA may be in flight when it leaves
             tc_commit(smem_u32(&sh.drain[t]));
-            mbar_wait_bounded(smem_u32(&sh.drain[t]), 0, A.wait_ns);
+            if (!mbar_wait_bounded(smem_u32(&sh.drain[t]), 0, A.wait_ns)) {
+                *(volatile int*)&sh.abort = 1;
+                if (A.status) atomicOr(A.status, KVO_DEV_TIMEOUT);
+            }
         }
         __syncwarp();
         if constexpr (SPLIT) { cluster_barrier(); cluster_barrier(); }     // as below
@@ -581,6 +581,16 @@ prompt_attn_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
     __syncthreads();
     tc_fence_after();
     if (warp == 8) tmem_free(sh.tmem, 512);
+    // Every warp has left its waits, so `abort` is final.  Where it is set somebody stopped before all loads had landed:
+    // the thread that issued them stays until they have, and with it the CTA and its shared memory.
+    if (warp == 9 && lane == 0 && sh.abort) {
+        const int issued = sh.issued;
+        for (int t = 0; t < 2; ++t)
+            if (issued && n_t[t] > 0) mbar_wait_bounded(smem_u32(&sh.q_full[t]), 0, A.wait_ns);
+        for (int i = max(0, issued - P::STAGES); i < issued; ++i)
+            mbar_wait_bounded(smem_u32(&sh.kv_full[i % P::STAGES]), (i / P::STAGES) & 1, A.wait_ns);
+        if (sh.tail_open) mbar_wait_bounded(smem_u32(&sh.v_tail), 0, A.wait_ns);
+    }
 }
 
 template <int D, bool SPLIT>
@@ -665,7 +675,8 @@ extern "C" kvo_status kvo_prompt_attn(const void* q, int64_t q_token_stride, con
     A.tq = PR_ROWS / r;
     A.causal = causal ? 1 : 0;
     A.scale_log2 = (float)(1.4426950408889634 / sqrt((double)head_dim));
-    A.wait_ns = 2000000000LL;
+    A.skip = call_wait.skip;
+    A.wait_ns = call_wait.limit_ns;
     const int64_t units = total_q / (2 * A.tq) + batch, ctas = units * n_kv_heads;
     if (ctas > INT32_MAX) return bad("too many tokens");
     A.units = (int)units;

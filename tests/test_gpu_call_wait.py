@@ -86,3 +86,25 @@ def test_paged_attention_wait_runs_out(e4m3, lens, cap, tile):
     runs_out(lambda status: kvo.paged_attn(*a, status=status, **kw), tile)
     got = kvo.paged_attn(*a, **kw)
     assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+
+
+# n tiles of 128 keys: loads 0 .. 2n - 1; the last V goes through a barrier of its own where it is cut
+@pytest.mark.parametrize("d,hkv,r,nq,nk,loads", [
+    (128, 1, 4, [130], None, [0, 1, 2, 3]),                      # two tiles, the last one cut: nothing but the first loads
+    (64, 2, 4, [3, 0, 129, 1, 256], None, [0, 1, 3]),            # short prompts in one call, whole and cut tiles
+    (128, 8, 4, [1300], None, [0, 7, 16, 21]),                   # loads that wait for a stage of the ring
+    (128, 1, 4, [5], [1500], [0, 1, 2, 3]),                      # split over clusters: parts of one to a few tiles
+    (64, 1, 2, [40, 3], [3000, 17], [0, 1, 4]),
+    (128, 8, 4, [200], [6000], [0, 5, 14])])
+def test_prompt_attention_wait_runs_out(d, hkv, r, nq, nk, loads):
+    g = gen(d + r)
+    cuts = lambda counts: [sum(counts[:i]) for i in range(len(counts) + 1)]
+    cq, ck = cuts(nq), cuts(nk or nq)
+    q, k, v = normal(g, cq[-1], hkv * r, d), normal(g, ck[-1], hkv, d), normal(g, ck[-1], hkv, d)
+    call = lambda status=None: kvo.prompt_attn(q, k, v, i32(cq), i32(ck), status=status)
+    want = call()
+    for load in loads:
+        runs_out(call, load)
+        status = i32([0])
+        got = call(status)
+        assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1]) and int(status.item()) == 0
