@@ -57,6 +57,29 @@ __device__ __forceinline__ int warp_find(int n, int64_t key, F first) {
     return lo;
 }
 
+// Packed requests: request i's rows are cu[i] .. cu[i + 1] - 1 of `total`.  It is served where its offsets ascend within
+// 0..total and it begins at or behind the end of every earlier request of which that is true, so no row belongs to two.
+// Request i's work starts at slot cu[i] / rows + extra * i and has n / rows + extra slots: those of served requests do not
+// meet, and where all offsets ascend the last request that starts at or before a slot holds it.  A warp sees at a glance
+// whether they do for up to 32 requests (a lane each); calls of more take them as they are: for each CTA to look at all
+// of them cost 4 % of a call of 33 requests and 28 % of one of 4000.
+__device__ __forceinline__ bool offsets_ascend(int a, int e, int64_t total) { return a >= 0 && e >= a && e <= total; }
+
+// Whole warp, up to 32 requests, lane i with offsets a and e of request i: the served request that holds a slot, or -1,
+// whatever the offsets are.
+static __device__ __noinline__ int find_served(int a, int e, int batch, int64_t total, int slot, int rows, int extra) {
+    const int lane = threadIdx.x & 31;
+    const bool own = lane < batch && offsets_ascend(a, e, total);
+    int end = own ? e : 0;         // the end of the requests up to this one
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int x = __shfl_up_sync(0xffffffffu, end, o);
+        if (lane >= o) end = max(end, x);
+    }
+    const int before = __shfl_up_sync(0xffffffffu, end, 1), first = max(a, 0) / rows + extra * lane;
+    return __ffs((int)__ballot_sync(0xffffffffu, own && (lane == 0 || a >= before) && slot >= first && slot < first + (e - a) / rows + extra)) - 1;
+}
+
 // Host: whether two byte ranges share a byte.
 inline bool ranges_meet(const void* a, int64_t na, const void* b, int64_t nb) {
     const uintptr_t x = (uintptr_t)a, y = (uintptr_t)b;

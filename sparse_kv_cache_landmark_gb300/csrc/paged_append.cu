@@ -103,6 +103,11 @@ __device__ __forceinline__ AppendUnit append_unit(const AppendArgs& A, int u) {
         U.n = (int64_t)__shfl_sync(0xffffffffu, c1, U.b) - U.t0;
         U.start = __shfl_sync(0xffffffffu, st, U.b);
         U.ok = U.t0 >= 0 && U.n >= 0 && U.t0 + U.n <= A.tokens && U.start >= 0;
+        if (__any_sync(0xffffffffu, !offsets_ascend(c0, c1, A.tokens))) {
+            U.b = find_served(c0, c1, A.batch, A.tokens, u, A.page, 2);
+            U.ok = U.b >= 0 && request_range(A, U.b, U.t0, U.n, U.start);
+            if (U.ok) U.j = u - ((int)U.t0 / A.page + 2 * U.b);
+        }
     } else {
         auto first = [&](int i) { return (int64_t)max(__ldg(A.cu + i), 0) / A.page + 2 * (int64_t)i; };
         U.b = warp_find(A.batch, u, first);
@@ -157,14 +162,27 @@ __device__ __forceinline__ uint2 quantise8(const uint4& v, float inv) {
     return make_uint2(codes[0], codes[1]);
 }
 
+// One thread, up to 32 requests: the served one that holds a row, or -1, whatever the offsets are.
+static __device__ __noinline__ int find_served_row(const int32_t* cu, int batch, int64_t total, int64_t row) {
+    int before = 0;
+    for (int i = 0; i < batch; ++i) {
+        const int a = __ldg(cu + i), e = __ldg(cu + i + 1);
+        if (!offsets_ascend(a, e, total)) continue;
+        if (a >= before && row >= a && row < e) return i;
+        before = max(before, e);
+    }
+    return -1;
+}
+
 // Rotates packed q: CTA `block` of them takes (token, unit) pairs of a run of q_per heads.
 template <int D>
 __device__ __forceinline__ void append_q(const AppendArgs& A, int block) {
     constexpr int UNITS = D / 16;
     const int run = block / A.q_blocks;
-    const int64_t k = (int64_t)(block - run * A.q_blocks) * blockDim.x + threadIdx.x;
-    if (k >= A.tokens * UNITS) return;
-    const int64_t t = k / UNITS;
+    const int64_t k = (int64_t)(block - run * A.q_blocks) * blockDim.x + threadIdx.x, t = k / UNITS;
+    const int mine = threadIdx.x & 31;
+    const bool look = A.batch <= 32 && mine < A.batch;
+    const int c0 = look ? __ldg(A.cu + mine) : 0, c1 = look ? __ldg(A.cu + mine + 1) : 0;
     const int u = (int)(k - t * UNITS);
     int lo = 0, hi = A.batch;                                  // the last b with cu[b] <= t
     while (hi - lo > 1) {
@@ -173,7 +191,12 @@ __device__ __forceinline__ void append_q(const AppendArgs& A, int block) {
     }
     int64_t t0, n;
     int start;
-    if (request_range(A, lo, t0, n, start) && t >= t0 && t < t0 + n) {
+    bool ok = request_range(A, lo, t0, n, start);
+    if (__any_sync(0xffffffffu, !offsets_ascend(c0, c1, A.tokens))) {
+        lo = find_served_row(A.cu, A.batch, A.tokens, t);
+        ok = lo >= 0 && request_range(A, lo, t0, n, start);
+    }
+    if (k < A.tokens * UNITS && ok && t >= t0 && t < t0 + n) {
         const int h0 = run * A.q_per, h1 = min(A.hq, h0 + A.q_per);
         rope_heads(A.R, D, A.q + t * A.q_tok, D, A.q_out + t * A.hq * D, D, u, (int)(start + (t - t0)), h0, h1);
     }

@@ -402,6 +402,15 @@ prompt_attn_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
         qe = __shfl_sync(0xffffffffu, e, b);
         ks = __shfl_sync(0xffffffffu, c, b);
         ke = __shfl_sync(0xffffffffu, f, b);
+        if (__any_sync(0xffffffffu, !offsets_ascend(a, e, A.total_q))) {
+            const int at = find_served(a, e, A.batch, A.total_q, u, TU, 1);
+            if (at < 0) return;
+            qs = A.cu_q[at];
+            qe = A.cu_q[at + 1];
+            ks = A.cu_k[at];
+            ke = A.cu_k[at + 1];
+            j0 = u - ((int)qs / TU + at);
+        }
     } else {
         auto first = [&](int i) { return (int64_t)max(__ldg(A.cu_q + i), 0) / TU + i; };
         const int b = warp_find(A.batch, u, first);
