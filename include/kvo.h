@@ -547,7 +547,7 @@ typedef struct {
  *   outside 0..n_pages - 1); such requests or pages are not written, nor are
  *   their rows of k_out.  A request whose offsets ascend but which begins before
  *   the end of an earlier such one is not served either; all others are, unless
- *   the call has more than 32 requests: then any of its rows may be missing.
+ *   the call has more than 32 requests: then all of its rows are undefined.
  *   Errors: KVO_ERR_INVALID, KVO_ERR_CUDA.
  */
 kvo_status kvo_paged_append(const kvo_paged_cache* cache, const void* k, int64_t k_token_stride, const void* v,
@@ -614,7 +614,7 @@ kvo_status kvo_paged_attn_workspace(const kvo_paged_cache* cache, int n_q_heads,
  *   Status bits: KVO_DEV_BAD_COUNT (offsets descending or outside 0..total: that
  *   request is not written, nor one whose queries begin before the end of an
  *   earlier one's; all others are, unless the call has more than 32 requests:
- *   then any of its rows may be missing), KVO_DEV_TIMEOUT (a bounded wait of 2 s
+ *   then all of its rows are undefined), KVO_DEV_TIMEOUT (a bounded wait of 2 s
  *   gave up: outputs are invalid).  Errors: KVO_ERR_INVALID, KVO_ERR_CUDA.
  */
 kvo_status kvo_prompt_attn(const void* q, int64_t q_token_stride, const void* k, int64_t k_token_stride,
