@@ -265,7 +265,7 @@ def _native():
 
 
 def rope_frequencies(rot_dim: int, base: float = 10000.0, scaling: Optional[str] = None, factor: float = 1.0,
-                     original_len: int = 8192, low: float = 1.0, high: float = 4.0, device="cuda"):
+                     original_len: int = 8192, low: float = 1.0, high: Optional[float] = None, device="cuda"):
     """Frequencies and amplitude for ``rope`` and ``paged_append`` (host only, made once per model).
 
     Pair i turns by base^(-2i / rot_dim) radians a position.  ``scaling`` for
@@ -274,7 +274,8 @@ def rope_frequencies(rot_dim: int, base: float = 10000.0, scaling: Optional[str]
     ``low`` times within ``original_len``, keeps those that turn more than ``high``
     times and blends between; "ramp" blends over the pair index instead, from the
     pair that turns ``high`` times (kept) to the one that turns ``low`` times
-    (divided), and scales the rotated values by 0.1 ln(factor) + 1.
+    (divided), and scales the rotated values by 0.1 ln(factor) + 1.  ``high`` None is
+    the scaling's usual bound, 4 turns for "banded" and 32 for "ramp".
     Returns (int64 tensor [rot_dim / 2] of turns per position in units of 2^-64,
     amplitude).
     """
@@ -282,6 +283,8 @@ def rope_frequencies(rot_dim: int, base: float = 10000.0, scaling: Optional[str]
         raise KvoError(KVO_ERR_INVALID, "rot_dim must be a positive multiple of 16")
     if scaling not in (None, "linear", "banded", "ramp"):
         raise KvoError(KVO_ERR_INVALID, f"scaling must be None, 'linear', 'banded' or 'ramp', got {scaling!r}")
+    if high is None:
+        high = 32.0 if scaling == "ramp" else 4.0
     if not (factor > 0 and base > 1 and original_len > 0 and high > low > 0):
         raise KvoError(KVO_ERR_INVALID, "need factor > 0, base > 1, original_len > 0 and high > low > 0")
     freq, amplitude = [], 1.0
