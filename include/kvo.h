@@ -484,17 +484,21 @@ kvo_status sparse_decode_attn_static(const void* q, const void* k_buf, const voi
  *   x: bf16 [tokens][heads][head_dim] with any token and head stride (elements,
  *   multiples of 8; the last dimension contiguous; 16-byte aligned), e.g. the q
  *   and k heads of a fused projection.  out: the same shape with its own
- *   strides (no row of it twice); out == x with equal strides rotates in place;
- *   other overlaps are not allowed.  pos: device int32 [tokens], any value (a negative position
- *   turns backwards).  freq: device uint64 [rot_dim / 2], each pair's frequency
- *   in turns per position, in units of 2^-64: the phase pos * freq is exact
- *   modulo a turn at every position.  Scalings for long contexts are other
- *   frequencies, and `amplitude` multiplies the rotated values.
+ *   strides (rows that share no memory); out == x with equal strides rotates in
+ *   place; other overlaps are refused.  Views of one buffer are apart where no row
+ *   of one meets a row of the other: with equal strides; with equal token strides
+ *   and other head strides, where a token's heads from first to last lie apart;
+ *   with other token strides, where their whole ranges do.  pos: device int32
+ *   [tokens], any value (a negative position turns backwards).  freq: device
+ *   uint64 [rot_dim / 2], each pair's frequency in turns per position, in units of
+ *   2^-64: the phase pos * freq is exact modulo a turn at every position.  Scalings
+ *   for long contexts are other frequencies, and `amplitude` multiplies the rotated
+ *   values.
  *   interleaved 0: pairs (i, i + rot_dim / 2); 1: pairs (2i, 2i + 1).  Values
  *   from rot_dim on pass through unchanged.  fp32, rounded once to bf16.
  *   Errors: KVO_ERR_INVALID for head_dim not a multiple of 16 in 16..4096,
- *   rot_dim not a multiple of 16 in 16..head_dim, bad counts, strides or
- *   alignment, or null pointers (tokens == 0 launches nothing); KVO_ERR_CUDA.
+ *   rot_dim not a multiple of 16 in 16..head_dim, bad counts, strides, alignment
+ *   or overlaps, or null pointers (tokens == 0 launches nothing); KVO_ERR_CUDA.
  */
 kvo_status kvo_rope(const void* x, int64_t x_token_stride, int64_t x_head_stride, void* out,
                     int64_t out_token_stride, int64_t out_head_stride, const int32_t* pos, const uint64_t* freq,

@@ -41,6 +41,45 @@ int rope_heads_per_thread(int64_t n, int heads) {
     return (int)std::max<int64_t>(1, std::min<int64_t>(8, heads / std::max<int64_t>(1, splits)));
 }
 
+// Which memory rows share.  A view has rows of d values at t * tok + h * head, t < T, h < H; strides of any size.
+typedef __int128 wide;
+struct RopeView {
+    const void* at;
+    int64_t tok, head;
+};
+// Whether m * step lies between lo and hi, both excluded, for some |m| < n.
+bool multiple_between(wide lo, wide hi, int64_t step, int64_t n) {
+    const wide s = step < 0 ? -(wide)step : (wide)step;
+    if (s == 0 || n == 1) return lo < 0 && 0 < hi;
+    const wide below = lo >= 0 ? lo / s : -((-lo + s - 1) / s);          // floor
+    const wide m = std::max<wide>(below + 1, 1 - (wide)n);
+    return m < n && m * s < hi;
+}
+// Whether two rows of the view share a value.
+bool rope_rows_share(const RopeView& v, int64_t T, int H, int d) {
+    if ((H == 1 || v.head >= d) && (T == 1 || v.tok >= (wide)(H - 1) * v.head + d)) return false;    // token after token
+    if ((T == 1 || v.tok >= d) && (H == 1 || v.head >= (wide)(T - 1) * v.tok + d)) return false;     // head after head
+    if (T > 1 && v.tok > -d && v.tok < d) return true;
+    for (int h = 1; h < H; ++h)
+        if (multiple_between(-d - (wide)h * v.head, d - (wide)h * v.head, v.tok, T)) return true;
+    return false;
+}
+// Whether a row of x shares a value with a row of out.  Exact for equal strides; with equal token strides a token's heads
+// are taken as one run, and with others all rows.
+bool rope_views_meet(const RopeView& x, const RopeView& out, int64_t T, int H, int d) {
+    const wide apart = ((wide)(intptr_t)out.at - (wide)(intptr_t)x.at) / 2;      // both are 16-byte aligned
+    auto low = [](wide n, int64_t stride) { return stride < 0 ? n * stride : (wide)0; };
+    auto high = [](wide n, int64_t stride) { return stride > 0 ? n * stride : (wide)0; };
+    const wide x0 = low(H - 1, x.head), x1 = high(H - 1, x.head) + d;            // a token's heads
+    const wide o0 = apart + low(H - 1, out.head), o1 = apart + high(H - 1, out.head) + d;
+    if (o0 + low(T - 1, out.tok) >= x1 + high(T - 1, x.tok) || x0 + low(T - 1, x.tok) >= o1 + high(T - 1, out.tok)) return false;
+    if (T > 1 && x.tok != out.tok) return true;
+    if (H > 1 && x.head != out.head) return multiple_between(x0 - o1, x1 - o0, x.tok, T);
+    for (int h = 1 - H; h < H; ++h)
+        if (multiple_between(-d - apart - (wide)h * x.head, d - apart - (wide)h * x.head, x.tok, T)) return true;
+    return false;
+}
+
 }  // namespace kvo
 
 extern "C" kvo_status kvo_rope(const void* x, int64_t x_token_stride, int64_t x_head_stride, void* out,
@@ -63,6 +102,10 @@ extern "C" kvo_status kvo_rope(const void* x, int64_t x_token_stride, int64_t x_
         return bad("rows of out must not share memory");
     if (x == out && (x_token_stride != out_token_stride || x_head_stride != out_head_stride))
         return bad("in place needs equal strides");
+    const RopeView in{x, x_token_stride, x_head_stride}, to{out, out_token_stride, out_head_stride};
+    if (rope_rows_share(to, tokens, heads, head_dim)) return bad("rows of out must not share memory");
+    if (x != out && rope_views_meet(in, to, tokens, heads, head_dim))
+        return bad("out must be apart from x, or x itself with equal strides");
     const int units = head_dim / 16;
     if (tokens > (int64_t)INT32_MAX * ROPE_THREADS / units) return bad("too many tokens");
     const int64_t n = tokens * units;

@@ -309,7 +309,8 @@ def rope_frequencies(rot_dim: int, base: float = 10000.0, scaling: Optional[str]
 
 def rope(x, pos, freq, interleaved: bool = False, amplitude: float = 1.0, out=None, stream=None):
     """Rotary positions (C: kvo_rope).  x: CUDA bf16 [tokens][heads][d], last dimension contiguous, any token and
-    head stride; pos: int32 [tokens]; freq: ``rope_frequencies``.  ``out=x`` rotates in place."""
+    head stride; pos: int32 [tokens]; freq: ``rope_frequencies``.  ``out=x`` rotates in place; any other ``out`` shares
+    no memory with x."""
     return (_BINDING or _native()).rope(x, pos, freq, interleaved, amplitude, out, stream)
 
 

@@ -530,3 +530,38 @@ def test_append_in_place_on_both_paths():
         assert kvo.paged_append(k2, v, pools[2], pools[3], table, i32(start), q=q2, q_out=q2, k_out=k2, **kw) is q2
         assert torch.equal(k2, k_out) and torch.equal(q2, q_out)
         assert torch.equal(pools[0], pools[2]) and torch.equal(pools[1], pools[3])
+
+
+def test_rope_into_views():
+    """out apart from x: other heads of the same projection, heads side by side with x's, with other head strides, head
+    after head, with padding between tokens."""
+    g = gen(6)
+    T, H, d = 9, 3, 64
+    freq, amp = kvo.rope_frequencies(d)
+    pos = i32([5 * i for i in range(T)])
+    x = normal(g, T, H, d)
+    want = kvo.rope(x, pos, freq)
+
+    def views():
+        wide = normal(g, T, 20, d)
+        yield wide, wide[:, :H], wide[:, H:2 * H]                              # the next heads
+        yield wide, wide[:, 7:7 + H], wide[:, 2:2 + H]                         # heads before
+        pairs = wide.view(T, 10, 2, d)
+        yield wide, pairs[:, :H, 0], pairs[:, :H, 1]                           # every other head
+        yield wide, wide[:, :H], wide[:, 10:10 + 2 * H:2]                      # another head stride
+        yield wide, wide[:, 10:10 + 2 * H:2], wide[:, :H]
+        planes = normal(g, 2, H, T, d)
+        yield planes, planes[0].transpose(0, 1), planes[1].transpose(0, 1)     # head after head
+        mixed = normal(g, H, 2, T, d)
+        yield mixed, mixed[:, 0].transpose(0, 1), mixed[:, 1].transpose(0, 1)
+        rows = normal(g, 2 * T, H, d)
+        yield rows, rows[::2], rows[1::2]                                      # every other row
+        yield rows, rows[:T], rows[T:]
+
+    for whole, a, b in views():
+        a.copy_(x)
+        expect = whole.clone()
+        at = b.storage_offset(), b.stride()
+        expect.as_strided(b.shape, at[1], at[0]).copy_(want)
+        kvo.rope(a, pos, freq, out=b)
+        assert torch.equal(whole, expect)

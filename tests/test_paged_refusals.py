@@ -208,3 +208,17 @@ def test_wait_switch_refuses_bad_limits(limit, skip):
     with pytest.raises(kvo.KvoError, match="limit_ns"):
         kvo.set_call_wait_test(limit, skip)
     kvo.set_call_wait_test()
+
+
+# x: 8 heads of 128 of a projection of 22, 4 tokens, at 16 P
+@pytest.mark.parametrize("out,ot,oh,frag", [
+    (16 * P + 4 * 256, 2816, 128, "apart"),                             # heads 4 .. 11 of the same projection
+    (16 * P - 256, 2816, 128, "apart"),                                # one head before
+    (16 * P + 16, 2816, 128, "apart"),                                 # 8 values further
+    (16 * P + 2816 * 2, 2816, 128, "apart"),                           # one token further
+    (16 * P + 7 * 256, 2816, 256, "apart"),                            # every other head from the last one on
+    (16 * P + 8 * 256, 1024, 128, "apart"),                            # contiguous, across the rows of x
+    (64 * P, 1024, 64, "share memory"), (64 * P, 896, 128, "share memory"), (64 * P, 64, 4 * 128, "share memory"),
+    (64 * P, 128, 256, "share memory"), (64 * P, -120, 1024, "share memory"), (64 * P, 1024, -120, "share memory")])
+def test_rope_refuses_overlaps(lib, out, ot, oh, frag):
+    refused(lib, lib.kvo_rope(16 * P, 2816, 128, out, ot, oh, P, P, 4, 8, 128, 128, 0, 1.0, None), frag)
