@@ -51,8 +51,9 @@ def _link_binding(obj: str) -> None:
     if not _newer(BINDING, [obj, LIB]):
         return
     torch = os.path.join(os.path.dirname(importlib.util.find_spec("torch").origin), "lib")
-    r = subprocess.run(["g++", "-shared", "-o", BINDING, obj, LIB, "-Wl,-rpath,$ORIGIN", f"-L{torch}", "-ltorch_python",
-                        "-ltorch_cpu", "-ltorch_cuda", "-lc10_cuda", "-lc10"], capture_output=True, text=True)
+    # libkvo.so has no soname, so that a C program linked with its path starts without an rpath; the binding finds it beside itself
+    r = subprocess.run(["g++", "-shared", "-o", BINDING, obj, f"-L{PKG}", "-l:libkvo.so", "-Wl,-rpath,$ORIGIN", f"-L{torch}",
+                        "-ltorch_python", "-ltorch_cpu", "-ltorch_cuda", "-lc10_cuda", "-lc10"], capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"linking the binding failed:\n{r.stderr}")
 
@@ -84,7 +85,7 @@ def build(verbose: bool = False, ptxas_info: bool = False) -> str:
             if lg:
                 sys.stderr.write(lg)
     if _newer(LIB, objs):
-        cmd = [NVCC, *ARCH, "-shared", "-cudart", "shared", "-Xlinker", "-soname,libkvo.so", "-o", LIB, *objs,
+        cmd = [NVCC, *ARCH, "-shared", "-cudart", "shared", "-o", LIB, *objs,
                "-Xlinker", "-rpath,/usr/local/cuda/lib64"]
         r = subprocess.run(cmd, capture_output=True, text=True)
         if r.returncode != 0:
