@@ -535,7 +535,9 @@ typedef struct {
  *   and to the cache.  q (optional): bf16 [tokens][n_q_heads][head_dim], heads
  *   contiguous, any token stride, rotated into the contiguous q_out by the same
  *   launch.  k_out may be k and q_out q where those are contiguous; other
- *   overlaps are refused.
+ *   overlaps with what the call reads or writes are refused, and so are pools or
+ *   scales that K and V share.  k, v and q may lie in pages that the call does not
+ *   write.
  *   e4m3 pages: a page's scale is the smallest power of two s >= 2^-100 with
  *   |x| <= 448 s for the finite values written to it.  A page whose first row
  *   is written starts afresh; otherwise its scale never shrinks, and when it
@@ -573,10 +575,11 @@ kvo_status kvo_paged_append(const kvo_paged_cache* cache, const void* k, int64_t
  *   the first counts[b][h] count (counts NULL: all).  A listed block is cut at
  *   the request's length, one past it adds nothing, one listed twice counts
  *   twice.
- *   o: bf16 [batch][n_q_heads][head_dim], apart from q; lse: fp32
- *   [batch][n_q_heads], natural log.  Softmax scale 1/sqrt(head_dim), fp32 accumulation.  A request with
- *   nothing to attend to gets o = 0, lse = -inf.  What lies in a page behind
- *   the last token is never used, NaN included.
+ *   o: bf16 [batch][n_q_heads][head_dim]; lse: fp32 [batch][n_q_heads], natural
+ *   log; both and the workspace apart from each other and from all that the call
+ *   reads.  Softmax scale 1/sqrt(head_dim), fp32 accumulation.  A request with
+ *   nothing to attend to gets o = 0, lse = -inf.  What lies in a page behind the
+ *   last token is never used, NaN included.
  *   o is rounded once to bf16, as the projection that follows takes it: the
  *   weights are rounded to 11 bits (8 with bf16 pages) on the tensor cores, so
  *   fp32 would carry no more.  With e4m3 pages the weights are rounded next to
@@ -609,12 +612,13 @@ kvo_status kvo_paged_attn_workspace(const kvo_paged_cache* cache, int n_q_heads,
  *   .. cu_k[b + 1] - 1; either may be empty.  causal: query token i sees the
  *   keys t <= i + (keys - queries), i.e. the last token sees them all (a chunk
  *   of a prompt behind cached keys has more keys than queries); 0: every key.
- *   o: bf16 [total_q][n_q_heads][head_dim], contiguous, apart from q, k and v;
- *   lse (optional): fp32 [total_q][n_q_heads], natural log.  Softmax scale 1/sqrt(head_dim), fp32
- *   accumulation, weights rounded to bf16, o rounded once to bf16.  A row that
- *   sees no key gets o = 0, lse = -inf; rows outside every request keep their
- *   bytes.  One request's values never reach another's rows; within a request a
- *   NaN or an infinity in v may reach rows before it in the same 128-key tile.
+ *   o: bf16 [total_q][n_q_heads][head_dim], contiguous; lse (optional): fp32
+ *   [total_q][n_q_heads], natural log; apart from each other and from all that the
+ *   call reads.  Softmax scale 1/sqrt(head_dim), fp32 accumulation, weights rounded
+ *   to bf16, o rounded once to bf16.  A row that sees no key gets o = 0, lse =
+ *   -inf; rows outside every request keep their bytes.  One request's values never
+ *   reach another's rows; within a request a NaN or an infinity in v may reach rows
+ *   before it in the same 128-key tile.
  *   Status bits: KVO_DEV_BAD_COUNT (offsets descending or outside 0..total: that
  *   request is not written, nor one whose queries begin before the end of an
  *   earlier one's; all others are, unless the call has more than 32 requests:

@@ -9,6 +9,8 @@
 #include <cuda_fp16.h>
 #include <stdint.h>
 
+#include <initializer_list>
+
 #include "kvo_internal.cuh"
 
 namespace kvo {
@@ -85,6 +87,21 @@ inline bool ranges_meet(const void* a, int64_t na, const void* b, int64_t nb) {
     const uintptr_t x = (uintptr_t)a, y = (uintptr_t)b;
     return na > 0 && nb > 0 && x < y + (uintptr_t)nb && y < x + (uintptr_t)na;
 }
+// Host: whether a byte range shares a byte with any of some others (null pointers: none).
+struct Bytes {
+    const void* at;
+    int64_t n;
+};
+inline bool meets_any(const Bytes& x, std::initializer_list<Bytes> others) {
+    for (const Bytes& y : others)
+        if (x.at && y.at && ranges_meet(x.at, x.n, y.at, y.n)) return true;
+    return false;
+}
+// Host: bytes of a cache's pages of K (and of V), and of their scales.
+inline int64_t page_bytes(const kvo_paged_cache* c) {
+    return (int64_t)c->n_pages * c->n_kv_heads * c->page_size * c->head_dim * (c->format == KVO_PAGES_E4M3 ? 1 : 2);
+}
+inline int64_t scale_bytes(const kvo_paged_cache* c) { return c->format == KVO_PAGES_E4M3 ? 4ll * c->n_pages * c->n_kv_heads : 0; }
 // Host: bytes from the first to the last of `n` bf16 rows of `len` values, `stride` apart.
 inline int64_t rows_bytes(int64_t n, int64_t stride, int64_t len) { return n > 0 ? 2 * ((n - 1) * stride + len) : 0; }
 

@@ -584,6 +584,14 @@ extern "C" kvo_status kvo_paged_append(const kvo_paged_cache* cache, const void*
         }
     if (k_out && q && ranges_meet(k_out, 2 * tokens * out[0].len, q_out, 2 * tokens * out[1].len))
         return bad("k_out and q_out must not overlap");
+    const int64_t pool = page_bytes(cache), scales = scale_bytes(cache), b = cache->batch;
+    if (ranges_meet(cache->k_pages, pool, cache->v_pages, pool) || ranges_meet(cache->k_scale, scales, cache->v_scale, scales))
+        return bad("K and V need pages and scales of their own");
+    for (const Out& o : out)
+        if (meets_any({o.at, 2 * tokens * o.len},
+                      {{cache->k_pages, pool}, {cache->v_pages, pool}, {cache->k_scale, scales}, {cache->v_scale, scales},
+                       {cache->table, 4 * b * cache->max_pages}, {start, 4 * b}, {cu, 4 * (b + 1)}, {freq, 4ll * rot_dim}}))
+            return bad("k_out and q_out must share memory with nothing else that the call reads or writes");
 
     AppendArgs A{};
     A.pages[0] = (uint8_t*)cache->k_pages;

@@ -1094,6 +1094,13 @@ extern "C" kvo_status kvo_paged_attn(const kvo_paged_cache* cache, const void* q
     if (need && (!workspace || workspace_bytes < need)) return bad("the workspace is too small (kvo_paged_attn_workspace)");
     const int64_t bytes = 2ll * cache->batch * n_q_heads * D;
     if (ranges_meet(o, bytes, q, bytes)) return bad("o must not overlap q");
+    const int64_t pool = page_bytes(cache), scales = scale_bytes(cache), b = cache->batch;
+    const Bytes to_o{o, bytes}, to_lse{lse, 4 * b * n_q_heads}, to_ws{workspace, (int64_t)need};
+    bool meet = meets_any(to_o, {to_lse, to_ws}) || meets_any(to_lse, {to_ws});
+    for (const Bytes& x : {to_o, to_lse, to_ws})
+        meet |= meets_any(x, {{q, bytes}, {cache->k_pages, pool}, {cache->v_pages, pool}, {cache->k_scale, scales}, {cache->v_scale, scales},
+                              {cache->table, 4 * b * cache->max_pages}, {lens, 4 * b}, {blocks, 4ll * G * n_blocks}, {counts, 4ll * G}});
+    if (meet) return bad("o, lse and the workspace must be apart from each other and from all that the call reads");
     const bool fp8 = cache->format == KVO_PAGES_E4M3;
     const int rb = fp8 ? D : 2 * D;
     CUtensorMap mk, mv;

@@ -669,6 +669,14 @@ extern "C" kvo_status kvo_prompt_attn(const void* q, int64_t q_token_stride, con
         ranges_meet(o, o_bytes, k, rows_bytes(total_k, k_token_stride, (int64_t)n_kv_heads * head_dim)) ||
         ranges_meet(o, o_bytes, v, rows_bytes(total_k, v_token_stride, (int64_t)n_kv_heads * head_dim)))
         return bad("o must not overlap q, k or v");
+    const Bytes to_o{o, o_bytes}, to_lse{lse, 4 * total_q * n_q_heads};
+    const int64_t cu_bytes = 4 * ((int64_t)batch + 1);
+    if (meets_any(to_o, {to_lse, {cu_q, cu_bytes}, {cu_k, cu_bytes}}) ||
+        meets_any(to_lse, {{q, rows_bytes(total_q, q_token_stride, (int64_t)n_q_heads * head_dim)},
+                           {k, rows_bytes(total_k, k_token_stride, (int64_t)n_kv_heads * head_dim)},
+                           {v, rows_bytes(total_k, v_token_stride, (int64_t)n_kv_heads * head_dim)},
+                           {cu_q, cu_bytes}, {cu_k, cu_bytes}}))
+        return bad("o and lse must be apart from each other and from all that the call reads");
     PromptArgs A{};
     A.cu_q = cu_q;
     A.cu_k = cu_k;

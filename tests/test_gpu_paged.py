@@ -565,3 +565,25 @@ def test_rope_into_views():
         expect.as_strided(b.shape, at[1], at[0]).copy_(want)
         kvo.rope(a, pos, freq, out=b)
         assert torch.equal(whole, expect)
+
+
+def test_outputs_over_what_a_call_reads_are_refused():
+    """Views that share memory, from Python: nothing is launched, the buffers keep their bytes."""
+    g = gen(4)
+    kp, vp, _, _ = pools(g, 8, 2, 16, 64, False)
+    kp[0] = 1.0
+    k, v, q = normal(g, 2, 2, 64), normal(g, 2, 2, 64), normal(g, 2, 8, 64)
+    table, lens = i32([[0, 1], [2, 3]]), i32([20, 9])
+    before = kp.clone()
+    for call, what in ((lambda: kvo.paged_append(k, v, kp, kp, table, lens), "of their own"),
+                       (lambda: kvo.paged_append(k, v, kp, vp, table, lens, k_out=kp.view(-1)[:256].view(2, 2, 64)), "nothing else"),
+                       (lambda: kvo.paged_attn(q, kp, vp, table, lens, o=kp.view(-1)[:1024].view(2, 8, 64)), "apart"),
+                       (lambda: kvo.paged_attn(q, kp, vp, table, lens, lse=q.view(-1).view(torch.float32)[:16].view(2, 8)), "apart"),
+                       (lambda: kvo.prompt_attn(q, k, v, i32([0, 2]), lse=k.view(-1).view(torch.float32)[:16].view(2, 8)), "apart")):
+        with pytest.raises(kvo.KvoError, match=what):
+            call()
+    assert torch.equal(kp, before)
+    # K and V read from one pool are no output
+    o, lse = kvo.paged_attn(q, kp, kp, table, lens)
+    check_attention(q, (o, lse), [[kp[i32([2 * b, 2 * b + 1]).long()].double().cpu().transpose(0, 1).flatten(1, 2)[:, :n]] * 2
+                                  for b, n in enumerate([20, 9])], 2, ref.BF16)

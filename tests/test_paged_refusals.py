@@ -222,3 +222,41 @@ def test_wait_switch_refuses_bad_limits(limit, skip):
     (64 * P, 128, 256, "share memory"), (64 * P, -120, 1024, "share memory"), (64 * P, 1024, -120, "share memory")])
 def test_rope_refuses_overlaps(lib, out, ot, oh, frag):
     refused(lib, lib.kvo_rope(16 * P, 2816, 128, out, ot, oh, P, P, 4, 8, 128, 128, 0, 1.0, None), frag)
+
+
+APART = dict(k=64 * P, v=96 * P, ks=128 * P, vs=129 * P, table=130 * P)      # pages of 16 P bytes, scales of 64, a table of 32
+
+
+@pytest.mark.parametrize("kw,frag", [
+    (dict(v=64 * P), "of their own"), (dict(v=80 * P - 16), "of their own"), (dict(k=96 * P + 1024), "of their own"),
+    (dict(vs=128 * P), "of their own"), (dict(vs=128 * P + 60), "of their own"),
+    (dict(k_out=64 * P + 512), "nothing else"), (dict(k_out=112 * P - 16), "nothing else"), (dict(q_out=96 * P), "nothing else"),
+    (dict(q_out=128 * P), "nothing else"), (dict(k_out=129 * P + 48), "nothing else"), (dict(k_out=130 * P + 16), "nothing else"),
+    (dict(q_out=131 * P), "nothing else"), (dict(k_out=132 * P), "nothing else"), (dict(k_out=133 * P), "nothing else")])
+def test_append_refuses_shared_pools_and_outputs_over_the_cache(lib, kw, frag):
+    """start, cu and freq at 131 P, 132 P and 133 P."""
+    c = cache(**{**APART, **{k: v for k, v in kw.items() if k in APART}})
+    a = {**dict(q_out=4 * P, k_out=6 * P), **kw}
+    refused(lib, lib.kvo_paged_append(c, P, 256, 2 * P, 256, 2, 132 * P, 131 * P, 133 * P, 128, 0, 1.0, 3 * P, 1024, 8, a["q_out"],
+                                      a["k_out"], None, None), frag)
+
+
+@pytest.mark.parametrize("kw", [dict(o=x * P) for x in (64, 128, 129, 130, 147, 148, 149, 400, 1000)]
+                         + [dict(lse=x * P) for x in (1, 64, 96, 128, 130, 147, 148, 149, 1000, 300)] + [dict(lse=301 * P - 4)]
+                         + [dict(o=112 * P - 16), dict(o=300 * P, lse=300 * P), dict(ws=96 * P), dict(ws=140 * P), dict(ws=P)])
+def test_attention_refuses_outputs_over_what_it_reads(lib, kw):
+    """q at P, pages, scales and table as above (the table long), lens, counts and blocks at 147 P to 149 P, the workspace
+    from 400 P on, o at 300 P and lse at 302 P."""
+    c = cache(**{**APART, "max_pages": 8192})
+    n = ctypes.c_size_t(0)
+    assert lib.kvo_paged_attn_workspace(c, 8, 2000, 0, ctypes.byref(n)) == kvo.KVO_OK and 1000 * P < n.value < 2000 * P
+    a = {**dict(o=300 * P, lse=302 * P, ws=400 * P), **kw}
+    refused(lib, lib.kvo_paged_attn(c, P, 8, 147 * P, 0, 149 * P, 148 * P, 2000, a["o"], a["lse"], a["ws"], n.value, None, None),
+            "o, lse and the workspace must be apart")
+
+
+@pytest.mark.parametrize("o,lse", [(P, None), (None, P + 8), (None, 16 * P), (None, 32 * P), (None, 48 * P + 4), (None, 64 * P + 20476)])
+def test_prompt_attention_refuses_outputs_over_what_it_reads(lib, o, lse):
+    """10 tokens; q, k, v at 16 P, 32 P and 48 P, offsets at P, o at 64 P."""
+    refused(lib, lib.kvo_prompt_attn(16 * P, 1024, 32 * P, 256, 48 * P, 256, P, P, 2, 10, 10, 8, 2, 128, 1, o or 64 * P, lse or 80 * P,
+                                     None, None), "o and lse must be apart")
