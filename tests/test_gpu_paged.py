@@ -587,3 +587,27 @@ def test_outputs_over_what_a_call_reads_are_refused():
     o, lse = kvo.paged_attn(q, kp, kp, table, lens)
     check_attention(q, (o, lse), [[kp[i32([2 * b, 2 * b + 1]).long()].double().cpu().transpose(0, 1).flatten(1, 2)[:, :n]] * 2
                                   for b, n in enumerate([20, 9])], 2, ref.BF16)
+
+
+@pytest.mark.parametrize("e4m3", [True, False])
+@pytest.mark.parametrize("cap,lens", [(8000, [3000, 0, 700]), (60, [900, 70, 1])])     # ranges, clusters
+def test_paged_attention_into_given_buffers(e4m3, cap, lens):
+    """The caller's o, lse and workspace, whatever they and the memory behind them hold; a workspace too small is refused."""
+    g = gen(cap)
+    (kp, vp), (ks, vs), table, rows = cache_of(g, lens, 2, 16, 128, e4m3)
+    wide = torch.zeros(len(lens), cap, dtype=torch.int32, device="cuda")
+    wide[:, :table.shape[1]] = table
+    q = normal(g, len(lens), 8, 128)
+    kw = dict(k_scale=ks, v_scale=vs)
+    want = kvo.paged_attn(q, kp, vp, wide, i32(lens), **kw)
+    check_attention(q, want, rows, 2, ref.F16 if e4m3 else ref.BF16)
+    space = torch.full((32 << 20,), 0xFF, dtype=torch.uint8, device="cuda")
+    for fill in (0xFF, 0x7F, 0):
+        space.fill_(fill)
+        o, lse = torch.full_like(q, math.nan), torch.full((len(lens) + 1, 8), 3.0, device="cuda")
+        got = kvo.paged_attn(q, kp, vp, wide, i32(lens), o=o, lse=lse[:-1], workspace=space, **kw)
+        assert got[0].data_ptr() == o.data_ptr() and got[1].data_ptr() == lse.data_ptr()
+        assert torch.equal(o, want[0]) and torch.equal(lse[:-1], want[1]) and bool((lse[-1] == 3.0).all())
+    if cap == 8000:
+        with pytest.raises(kvo.KvoError, match="too small"):
+            kvo.paged_attn(q, kp, vp, wide, i32(lens), workspace=space[:1024], **kw)
