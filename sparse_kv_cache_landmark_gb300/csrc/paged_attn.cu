@@ -431,6 +431,14 @@ __device__ __forceinline__ void pa_query(const PagedAttnArgs& A, int g, uint32_t
     }
 }
 
+// After a wait that ran out: the status bit, and what came too late gets as long again.  Of `stages` stages bit i of
+// `phase` is the parity that stage i's next fill would have.
+static __device__ __noinline__ void pa_late(uint32_t bar, int stages, uint32_t phase, long long limit, int32_t* status) {
+    if ((threadIdx.x & 31) == 0 && status) atomicOr(status, KVO_DEV_TIMEOUT);
+    for (int i = 0; i < stages; ++i) mbar_wait_bounded(bar + 8 * i, ((phase >> i) & 1) ^ 1, limit);
+    __syncwarp();
+}
+
 // One warp attends to `count` tiles in a row, from tile t0 of group g0 on and, unless ONE, through the groups after it.
 // The copies run STAGES tiles ahead, across groups.  finish(T, g, its tiles, first, count) takes each group's state.
 // Returns whether every wait was met; every copy issued has landed in any case.
@@ -583,7 +591,7 @@ __device__ __forceinline__ bool pa_run(const PagedAttnArgs& A, const CUtensorMap
         dead = __any_sync(0xffffffffu, dead);
         if (issued < count && !dead) issue();
     }
-    if (dead && lane == 0 && A.status) atomicOr(A.status, KVO_DEV_TIMEOUT);
+    if (dead) pa_late(bar, S::STAGES, phase, A.wait_ns, A.status);
     finish(T, cg, cn, first, done);
     return !dead;
 }
