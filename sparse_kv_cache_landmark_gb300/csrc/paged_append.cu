@@ -46,7 +46,6 @@ struct AppendArgs {
     int32_t* status;
     int64_t tokens, q_tok;
     int batch, hkv, hq, page, n_pages, max_pages;
-    int units;                    // upper bound of the pages touched
     int runs, run;                // a CTA of pages takes `run` KV heads, `runs` CTAs a page
     int q_per, q_blocks;          // query heads per thread; CTAs for a run of so many
     int page_ctas;                // CTAs of pages; those after them rotate q
@@ -631,7 +630,6 @@ extern "C" kvo_status kvo_paged_append(const kvo_paged_cache* cache, const void*
     } else {
         const int64_t units = tokens / cache->page_size + 2 * (int64_t)cache->batch;
         if (units * hkv > INT32_MAX / 2) return bad("too many tokens");
-        A.units = (int)units;
         // The offsets and the angles of a page's rows cost about as much as one head's rest: where there are pages
         // enough to fill the device, a CTA takes up to 8 heads with them (16391 tokens x 8 heads, e4m3, with q: 80.5 us
         // at 1 head, 73.2 at 2, 70.4 at 4, 68.5 at 8, before rows were fetched ahead), and likewise where many requests touch

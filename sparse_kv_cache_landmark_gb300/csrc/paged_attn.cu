@@ -95,7 +95,7 @@ struct PagedAttnArgs {
     float4* part_ml;              // [2 warps][r]: maximum, sum, sum of the rounded weights
     int2* info;                   // [G]: first slot and last warp of a group cut by range borders; x < 0: not cut
     int32_t* status;
-    int batch, hkv, r, page, shift, n_pages, max_pages, n_blocks, G;
+    int hkv, r, page, shift, n_pages, max_pages, n_blocks, G;
     int warps;                    // of the range kernel
     float scale_log2;
     long long wait_ns, skip;      // skip: the tile that every warp announces without copying it (tests; -1: none)
@@ -1133,7 +1133,6 @@ extern "C" kvo_status kvo_paged_attn(const kvo_paged_cache* cache, const void* q
     A.part_ml = (float4*)(ws + round256((size_t)G * sizeof(int2)));
     A.part_o = (float*)((uint8_t*)A.part_ml + round256((size_t)2 * plan.ctas * PA_WARPS * r * sizeof(float4)));
     A.status = status;
-    A.batch = cache->batch;
     A.hkv = cache->n_kv_heads;
     A.r = r;
     A.page = cache->page_size;
