@@ -582,12 +582,13 @@ kvo_status kvo_paged_append(const kvo_paged_cache* cache, const void* k, int64_t
  *   last token is never used, NaN included.
  *   o is rounded once to bf16, as the projection that follows takes it: the
  *   weights are rounded to 11 bits (8 with bf16 pages) on the tensor cores, so
- *   fp32 would carry no more.  With e4m3 pages the weights are rounded next to
- *   the group's largest v_scale: a page keeps the 11 bits as long as its v_scale
- *   is no more than 2^20 times smaller.  Two calls give the same bits.
+ *   fp32 would carry no more.  With e4m3 pages those are 11 bits of weights down
+ *   to 2^-20 of the running maximum's, and smaller ones are rounded to multiples
+ *   of 2^-30 of it; a page's weights count times its v_scale over the largest of
+ *   the group's there.  Two calls give the same bits.
  *   workspace: kvo_paged_attn_workspace bytes (0 for small calls: NULL will do),
- *   256-byte aligned, contents undefined before and after; one call at a time may use it (two captured
- *   graphs that may overlap need one each).
+ *   256-byte aligned, contents undefined before and after; one call at a time may
+ *   use it (two captured graphs that may overlap need one each).
  *   Status bits: KVO_DEV_BAD_BLOCK_ID (a page or block id out of range: adds
  *   nothing), KVO_DEV_BAD_COUNT (a length or count out of range: clamped),
  *   KVO_DEV_TIMEOUT (a bounded wait of 2 s gave up: outputs are invalid).

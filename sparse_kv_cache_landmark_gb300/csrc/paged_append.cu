@@ -12,8 +12,8 @@
 // to it when it grew, and writes codes.  q is rotated by further CTAs of the same
 // launch, behind those of the pages (a second kernel that starts beside the last
 // pages took 70.3 us for 64.1 with pages of 16 rows, 65.4 for 66.0 with 64, 6.1 for
-// 5.1 at 500 tokens, and 4 us more of the host).  16391 tokens, 32 and 8 heads of 128
-// with k_out, e4m3 pages of 64: 66.0 us, 6.1 TB/s (0.90 of a measured copy).
+// 4.8 at 500 tokens in pages of 16, and 4 us more of the host).  16391 tokens, 32 and 8
+// heads of 128 with k_out, e4m3 pages of 64: 65.5 us, 6.15 TB/s (0.90 of a measured copy).
 //
 // One token per request: a warp owns one (token, head), of K and V or of q; each
 // lane turns D / 64 pairs, so the angles take one or two sincos in a row.  Bound by a
@@ -529,9 +529,10 @@ cudaError_t append_pages_launch(const AppendArgs& A, int64_t ctas, int threads, 
 }
 
 // 16-value units of a page over 64 to 512 threads, 1 or 2 to a thread.  Rows of e4m3 pages are fetched a head ahead
-// where a CTA has several heads (16391 tokens x 8 heads with q, pages of 16 / 32 / 64: 75.5 -> 69.3, 77.8 -> 70.8, 69.5 ->
-// 65.5 us; with one head 2000 tokens took 13.4 for 12.4); bf16 pages, which wait for no scale, gain nothing by it (70.3
-// -> 71.4, 70.3 -> 72.9, 70.4 -> 69.0).  Pages of 128 rows in 256 threads of 4 units would take 206 registers.
+// where a CTA has several heads (16391 tokens x 8 heads, q in a kernel of its own then, pages of 16 / 32 / 64: 75.5 -> 69.3,
+// 77.8 -> 70.8, 69.5 -> 65.5 us; with one head 2000 tokens took 13.4 for 12.4); bf16 pages, which wait for no scale, gain
+// nothing by it (70.3 -> 71.4, 70.3 -> 72.9, 70.4 -> 69.0).  Pages of 128 rows in 256 threads of 4 units would take 206
+// registers.
 int append_threads(int page, int d) {
     const int units = page * (d / 16);
     return units > 512 ? 512 : std::min(APP_THREADS, units);

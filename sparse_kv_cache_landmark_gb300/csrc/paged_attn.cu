@@ -24,13 +24,15 @@
 // Tensor cores: mma.sync m16n8k16 on transposed products, S^T = K Q^T and O^T =
 // V^T P^T: tokens and value columns are the 16 matrix rows, query heads the 8
 // columns, so r <= 8 heads fill one product where heads as rows would leave half
-// of it empty.  P^T comes out of S^T by
-// an 8 x 8 transpose in the warp.  e4m3 codes are widened exactly to f16; q is
-// scaled by a power of two per row so that it is exact in f16 as well down to
-// 2^-32 of its row's largest value.  The weights exp2(s - m) are rounded to f16
-// (11 bits) next to e4m3 values, whose sum is taken before the rounding, and to
-// bf16 (8 bits) next to bf16 values, which have a wider exponent than f16; there o
-// is divided by the sum of the rounded weights and lse takes the unrounded one.
+// of it empty.  P^T comes out of S^T by an 8 x 8 transpose in the warp. 
+// e4m3 codes are widened exactly to f16; q is scaled by a power of two per row, its
+// largest value to 2^8..2^9: what is down to 2^-25 of that is exact in f16 as well
+// (8 bits above its smallest step, 2^-24), smaller values lose low bits, and below
+// 2^-33 they are zero.  The weights exp2(s - m), held times 2^6, are rounded to f16
+// next to e4m3 values, whose sum is taken before the rounding (11 bits down to 2^-20
+// of the running maximum, steps of 2^-30 of it below), and to bf16 (8 bits) next to
+// bf16 values, which have a wider exponent than f16; there o is divided by the sum
+// of the rounded weights and lse takes the unrounded one.
 // The maximum is only raised when a score passes it by more than 2^8, so most
 // tiles have no cross-lane step but one vote.
 //

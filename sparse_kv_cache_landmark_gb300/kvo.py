@@ -5,7 +5,8 @@ turns torch tensors into pointers, allocates outputs with torch, and raises
 ``KvoError`` on any non-OK status.  There is no fallback: without the built
 library or a CUDA device every call fails.  The serving calls (rope, paged_append,
 paged_attn, prompt_attn), which a decode loop makes once per layer and token, go
-through a native binding (csrc/binding.cpp) instead of ctypes.
+through a native binding (csrc/binding.cpp) instead of ctypes.  They are for
+inference: nothing is recorded for a backward pass.
 """
 from __future__ import annotations
 
