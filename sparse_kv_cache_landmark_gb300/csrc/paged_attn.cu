@@ -24,7 +24,7 @@
 // Tensor cores: mma.sync m16n8k16 on transposed products, S^T = K Q^T and O^T =
 // V^T P^T: tokens and value columns are the 16 matrix rows, query heads the 8
 // columns, so r <= 8 heads fill one product where heads as rows would leave half
-// of it empty.  P^T comes out of S^T by an 8 x 8 transpose in the warp. 
+// of it empty.  P^T comes out of S^T by an 8 x 8 transpose in the warp.
 // e4m3 codes are widened exactly to f16; q is scaled by a power of two per row, its
 // largest value to 2^8..2^9: what is down to 2^-25 of that is exact in f16 as well
 // (8 bits above its smallest step, 2^-24), smaller values lose low bits, and below
