@@ -92,6 +92,7 @@ typedef enum {
 #define KVO_DEV_BAD_COUNT    0x4   /* a count outside [0, k] */
 #define KVO_DEV_UNSORTED     0x8   /* an index list that is not strictly ascending */
 #define KVO_DEV_TIMEOUT      0x10  /* a bounded device wait gave up */
+#define KVO_DEV_NO_PAGES     0x20  /* kvo_paged_reserve, kvo_paged_fork: fewer free pages than asked for */
 
 typedef void* kvo_stream_t;        /* cudaStream_t */
 typedef struct kvo_ctx kvo_ctx;    /* opaque, owned by the library */
@@ -630,6 +631,98 @@ kvo_status kvo_prompt_attn(const void* q, int64_t q_token_stride, const void* k,
                            const void* v, int64_t v_token_stride, const int32_t* cu_q, const int32_t* cu_k, int batch,
                            int64_t total_q, int64_t total_k, int n_q_heads, int n_kv_heads, int head_dim, int causal,
                            void* o, float* lse, int32_t* status, kvo_stream_t stream);
+
+/* Who holds which page of a paged cache: one book for all layers, whose pools
+ * have the same page ids.  Every buffer is the caller's, in device memory, and is
+ * updated in place. */
+typedef struct {
+    int32_t* table;        /* [batch][max_pages]: the page ids of each request, as kvo_paged_cache reads them */
+    int32_t* held;         /* [batch]: how many entries of its row a request has; those behind are not looked at */
+    int32_t* refs;         /* [n_pages]: how often the page is named; 0: free.  16-byte aligned */
+    int32_t batch, max_pages, n_pages;      /* batch <= 8192 */
+    int32_t page_size;     /* tokens of a page */
+} kvo_page_book;
+
+/*
+ * The pages' bookkeeping.  A caller that keeps a page for itself (a prefix that no
+ * request holds just now) adds 1 to its refs.  Free pages are handed out lowest
+ * first, to the requests in their order, so that a call's results depend on its
+ * inputs alone.  Calls on one book run one after another (one stream, or events);
+ * kernels that read its table may not overlap with a call that writes it.  Where
+ * refs does not say how often pages are named the results are undefined, but
+ * nothing outside the buffers is touched.
+ *
+ * kvo_paged_reserve -- room for tokens.
+ *   want: device int32 [batch]: the tokens each request is to have room for.  A
+ *   request that holds fewer than ceil(want / page_size) pages is given the missing
+ *   ones at the end of its row (refs 1, held raised).  Where the free pages do not
+ *   do for a request and those before it, it and the requests behind it that need
+ *   pages get none.
+ *   Status bits: KVO_DEV_NO_PAGES (some request got none for that reason),
+ *   KVO_DEV_BAD_COUNT (want < 0 or beyond max_pages, or held out of range: such a
+ *   request gets none).  Errors: KVO_ERR_INVALID, KVO_ERR_CUDA.
+ */
+kvo_status kvo_paged_reserve(const kvo_page_book* book, const int32_t* want, int32_t* status, kvo_stream_t stream);
+
+/*
+ * kvo_paged_fork -- forks, reorders, cuts and frees requests, all at once.
+ *   parent, keep: device int32 [batch].  Request b becomes the first keep[b] tokens
+ *   of what request parent[b] was before the call: its row is the first
+ *   ceil(keep / page_size) entries of that row, its held their number, and the
+ *   entries of its old row behind them become -1.  parent[b] = b with the request's
+ *   length keeps it (pages reserved ahead are given back), with less cuts it;
+ *   parent[b] = -1 frees it.  Pages that nothing names any more are free (refs 0).
+ *   Whole pages are shared.  A last page that is filled in part (keep not a multiple
+ *   of page_size) will be written to, so it belongs to one request alone: where
+ *   every use of it (its refs after the call) is such a last page, the lowest of
+ *   those requests keeps it, and all others get a free page instead, to be filled by
+ *   kvo_paged_copy for each layer: src and dst (device int32 [batch]) list these
+ *   moves in the order of the requests, -1 behind them, *count (device) their
+ *   number.  Pages freed by the call may be handed out by it; no page of src is.
+ *   workspace: kvo_paged_fork_workspace bytes, 256-byte aligned, contents undefined
+ *   before and after; one call at a time may use it.
+ *   Status bits: KVO_DEV_NO_PAGES (no free page for some copy: the request holds its
+ *   whole pages only), KVO_DEV_BAD_COUNT (parent outside -1..batch - 1, keep < 0 or
+ *   beyond what the parent holds: the request stays as it is; held out of range is
+ *   clamped), KVO_DEV_BAD_BLOCK_ID (a page id out of range in a row: not counted).
+ *   batch 0 sets *count to 0.  Errors: KVO_ERR_INVALID, KVO_ERR_CUDA.
+ */
+kvo_status kvo_paged_fork(const kvo_page_book* book, const int32_t* parent, const int32_t* keep, int32_t* src, int32_t* dst,
+                          int32_t* count, void* workspace, size_t workspace_bytes, int32_t* status, kvo_stream_t stream);
+kvo_status kvo_paged_fork_workspace(const kvo_page_book* book, size_t* bytes_out);
+
+/*
+ * kvo_paged_compact -- moves the used pages to the front of the pool.
+ *   With L pages in use, the i-th used page at L or behind goes to the i-th free one
+ *   before L, both ascending: src and dst (device int32 [n_pages / 2]) list these
+ *   moves, -1 behind them, *count (device) their number, for kvo_paged_copy.  The
+ *   rows' first held entries and refs follow; held stays.  table_out, refs_out (NULL:
+ *   in place) take the new table (all of it) and refs, so that kernels in flight may
+ *   go on reading the old ones until the pages are copied.  The caller that keeps
+ *   pages for itself follows src and dst.
+ *   workspace: kvo_paged_compact_workspace bytes, as above.
+ *   Status bits: KVO_DEV_BAD_BLOCK_ID (a page id out of range in a row: left alone),
+ *   KVO_DEV_BAD_COUNT (held out of range: clamped).  Errors: KVO_ERR_INVALID,
+ *   KVO_ERR_CUDA.
+ */
+kvo_status kvo_paged_compact(const kvo_page_book* book, int32_t* table_out, int32_t* refs_out, int32_t* src, int32_t* dst,
+                             int32_t* count, void* workspace, size_t workspace_bytes, int32_t* status, kvo_stream_t stream);
+kvo_status kvo_paged_compact_workspace(const kvo_page_book* book, size_t* bytes_out);
+
+/*
+ * kvo_paged_copy -- copies pages, K, V and scales, of all layers in one launch.
+ *   pools: as kvo_paged_cache, but each of the buffers holds `layers` layers one
+ *   after another ([layers][n_pages][n_kv_heads][page_size][head_dim]); table, batch
+ *   and max_pages are not looked at.  src, dst: device int32 [moves]; count (device,
+ *   optional): how many of them are made.  Page src[i] goes to dst[i] in every
+ *   layer.  A page that is dst twice, or dst of one move and src of another, holds
+ *   undefined values afterwards; src[i] == dst[i] does nothing.
+ *   Status bits: KVO_DEV_BAD_BLOCK_ID (an id out of range: that move is not made),
+ *   KVO_DEV_BAD_COUNT (count out of range: clamped).  Errors: KVO_ERR_INVALID,
+ *   KVO_ERR_CUDA.
+ */
+kvo_status kvo_paged_copy(const kvo_paged_cache* pools, int layers, const int32_t* src, const int32_t* dst, int moves,
+                          const int32_t* count, int32_t* status, kvo_stream_t stream);
 
 /*
  * kvo_set_gather_shape -- launch shape of the host -> HBM gather kernel:

@@ -384,6 +384,140 @@ PyObject* py_prompt_attn(PyObject*, PyObject* const* a, Py_ssize_t n) {
     });
 }
 
+// The checked descriptor of a book: table [batch][max_pages], held [batch], refs [n_pages].
+kvo_page_book book_of(PyObject* table, PyObject* held, PyObject* refs, int64_t page_size, const at::Device& dev) {
+    const at::Tensor& t = need(table, "table", dev, at::kInt);
+    const at::Tensor& r = need(refs, "refs", dev, at::kInt);
+    if (t.dim() != 2 || r.dim() != 1)
+        refuse("table must be [batch][max_pages], refs [n_pages], got " + shape_text(t.sizes()) + " and " + shape_text(r.sizes()));
+    kvo_page_book b{};
+    b.table = (int32_t*)t.data_ptr();
+    b.held = (int32_t*)need(held, "held", dev, at::kInt, {{t.size(0)}}).data_ptr();
+    b.refs = (int32_t*)r.data_ptr();
+    b.batch = int32_size(t.size(0), "batch");
+    b.max_pages = int32_size(t.size(1), "max_pages");
+    b.n_pages = int32_size(r.size(0), "n_pages");
+    b.page_size = int32_size(page_size, "page_size");
+    return b;
+}
+// The caller's int32 [n] buffer, or one of the call's own.
+at::Tensor ids(PyObject* o, const char* name, const at::Device& dev, int64_t n) {
+    return o == Py_None ? empty({n}, at::kInt, dev) : need(o, name, dev, at::kInt, {{n}});
+}
+at::Tensor scratch(PyObject* o, const at::Device& dev, size_t bytes) {
+    return o == Py_None ? empty({(int64_t)bytes}, at::kByte, dev) : need(o, "workspace", dev, at::kByte);
+}
+PyObject* three(const at::Tensor& a, const at::Tensor& b, const at::Tensor& c) {
+    PyObject* x = THPVariable_Wrap(a);
+    PyObject* y = THPVariable_Wrap(b);
+    PyObject* z = THPVariable_Wrap(c);
+    PyObject* r = x && y && z ? PyTuple_Pack(3, x, y, z) : nullptr;
+    Py_XDECREF(x);
+    Py_XDECREF(y);
+    Py_XDECREF(z);
+    return r;
+}
+void sized(kvo_status st) {
+    if (st != KVO_OK) throw Refused{st, kvo_last_error(nullptr)};
+}
+
+// paged_reserve(table, held, refs, want, page_size, status, stream)
+PyObject* py_paged_reserve(PyObject*, PyObject* const* a, Py_ssize_t n) {
+    return guarded(n, 7, [&]() -> PyObject* {
+        const at::Device dev = tensor(a[0], "table").device();
+        const kvo_page_book b = book_of(a[0], a[1], a[2], integer(a[4]), dev);
+        const int32_t* want = (const int32_t*)need(a[3], "want", dev, at::kInt, {{b.batch}}).data_ptr();
+        const Stream stream(a[6], dev);
+        int32_t* status = status_of(a[5], dev);
+        launch(dev, [&] { return kvo_paged_reserve(&b, want, status, stream.handle); });
+        Py_RETURN_NONE;
+    });
+}
+
+// paged_fork(table, held, refs, parent, keep, page_size, src, dst, count, workspace, status, stream)
+PyObject* py_paged_fork(PyObject*, PyObject* const* a, Py_ssize_t n) {
+    return guarded(n, 12, [&]() -> PyObject* {
+        const at::Device dev = tensor(a[0], "table").device();
+        const kvo_page_book b = book_of(a[0], a[1], a[2], integer(a[5]), dev);
+        const int32_t* parent = (const int32_t*)need(a[3], "parent", dev, at::kInt, {{b.batch}}).data_ptr();
+        const int32_t* keep = (const int32_t*)need(a[4], "keep", dev, at::kInt, {{b.batch}}).data_ptr();
+        const Stream stream(a[11], dev);
+        const at::Tensor src = ids(a[6], "src", dev, b.batch), dst = ids(a[7], "dst", dev, b.batch), count = ids(a[8], "count", dev, 1);
+        int32_t* status = status_of(a[10], dev);
+        size_t bytes = 0;
+        sized(kvo_paged_fork_workspace(&b, &bytes));
+        const at::Tensor ws = scratch(a[9], dev, bytes);
+        launch(dev, [&] {
+            return kvo_paged_fork(&b, parent, keep, (int32_t*)src.data_ptr(), (int32_t*)dst.data_ptr(), (int32_t*)count.data_ptr(),
+                                  ws.data_ptr(), ws.numel(), status, stream.handle);
+        });
+        return three(src, dst, count);
+    });
+}
+
+// paged_compact(table, held, refs, table_out, refs_out, src, dst, count, workspace, status, stream)
+PyObject* py_paged_compact(PyObject*, PyObject* const* a, Py_ssize_t n) {
+    return guarded(n, 11, [&]() -> PyObject* {
+        const at::Device dev = tensor(a[0], "table").device();
+        const kvo_page_book b = book_of(a[0], a[1], a[2], 1, dev);
+        const std::vector<int64_t> shape{b.batch, b.max_pages}, rshape{b.n_pages};
+        int32_t* table_out = a[3] == Py_None ? nullptr : (int32_t*)need(a[3], "table_out", dev, at::kInt, at::IntArrayRef(shape)).data_ptr();
+        int32_t* refs_out = a[4] == Py_None ? nullptr : (int32_t*)need(a[4], "refs_out", dev, at::kInt, at::IntArrayRef(rshape)).data_ptr();
+        const Stream stream(a[10], dev);
+        const at::Tensor src = ids(a[5], "src", dev, b.n_pages / 2), dst = ids(a[6], "dst", dev, b.n_pages / 2), count = ids(a[7], "count", dev, 1);
+        int32_t* status = status_of(a[9], dev);
+        size_t bytes = 0;
+        sized(kvo_paged_compact_workspace(&b, &bytes));
+        const at::Tensor ws = scratch(a[8], dev, bytes);
+        launch(dev, [&] {
+            return kvo_paged_compact(&b, table_out, refs_out, (int32_t*)src.data_ptr(), (int32_t*)dst.data_ptr(), (int32_t*)count.data_ptr(),
+                                     ws.data_ptr(), ws.numel(), status, stream.handle);
+        });
+        return three(src, dst, count);
+    });
+}
+
+// paged_copy(k_pages, v_pages, src, dst, count, k_scale, v_scale, status, stream)
+PyObject* py_paged_copy(PyObject*, PyObject* const* a, Py_ssize_t n) {
+    return guarded(n, 9, [&]() -> PyObject* {
+        const at::Tensor& k = tensor(a[0], "k_pages");
+        const at::Device dev = k.device();
+        const int64_t dims = k.dim();
+        if (dims != 4 && dims != 5) refuse("pages must be [n_pages][n_kv_heads][page_size][head_dim], layers of them before if any, got " + shape_text(k.sizes()));
+        const at::ScalarType dt = k.scalar_type();
+        if (dt != at::kBFloat16 && dt != at::kFloat8_e4m3fn) refuse(std::string("pages must be bfloat16 or float8_e4m3fn, got ") + dtype_text(dt));
+        kvo_paged_cache c{};
+        c.k_pages = need(a[0], "k_pages", dev, dt).data_ptr();
+        c.v_pages = need(a[1], "v_pages", dev, dt, k.sizes()).data_ptr();
+        const int64_t layers = dims == 5 ? k.size(0) : 1;
+        if (dt == at::kFloat8_e4m3fn) {
+            const std::vector<int64_t> s = k.sizes().slice(0, dims - 2).vec();
+            c.k_scale = (float*)need(a[5], "k_scale", dev, at::kFloat, at::IntArrayRef(s)).data_ptr();
+            c.v_scale = (float*)need(a[6], "v_scale", dev, at::kFloat, at::IntArrayRef(s)).data_ptr();
+            c.format = KVO_PAGES_E4M3;
+        }
+        c.n_pages = int32_size(k.size(dims - 4), "n_pages");
+        c.n_kv_heads = int32_size(k.size(dims - 3), "n_kv_heads");
+        c.page_size = int32_size(k.size(dims - 2), "page_size");
+        c.head_dim = int32_size(k.size(dims - 1), "head_dim");
+        const at::Tensor& src = need(a[2], "src", dev, at::kInt);
+        const at::Tensor& dst = need(a[3], "dst", dev, at::kInt, src.sizes());
+        const int32_t* count = nullptr;
+        if (a[4] != Py_None) {
+            const at::Tensor& t = need(a[4], "count", dev, at::kInt);
+            if (t.numel() != 1) refuse("count must hold one value");
+            count = (const int32_t*)t.data_ptr();
+        }
+        const Stream stream(a[8], dev);
+        int32_t* status = status_of(a[7], dev);
+        launch(dev, [&] {
+            return kvo_paged_copy(&c, int32_size(layers, "layers"), (const int32_t*)src.data_ptr(), (const int32_t*)dst.data_ptr(),
+                                  int32_size(src.numel(), "moves"), count, status, stream.handle);
+        });
+        Py_RETURN_NONE;
+    });
+}
+
 // raise_with(cls): the exception class, called as cls(status, message)
 PyObject* py_raise_with(PyObject*, PyObject* cls) {
     Py_XINCREF(cls);
@@ -396,6 +530,10 @@ PyMethodDef methods[] = {{"rope", (PyCFunction)(void*)py_rope, METH_FASTCALL, nu
                          {"paged_append", (PyCFunction)(void*)py_paged_append, METH_FASTCALL, nullptr},
                          {"paged_attn", (PyCFunction)(void*)py_paged_attn, METH_FASTCALL, nullptr},
                          {"prompt_attn", (PyCFunction)(void*)py_prompt_attn, METH_FASTCALL, nullptr},
+                         {"paged_reserve", (PyCFunction)(void*)py_paged_reserve, METH_FASTCALL, nullptr},
+                         {"paged_fork", (PyCFunction)(void*)py_paged_fork, METH_FASTCALL, nullptr},
+                         {"paged_compact", (PyCFunction)(void*)py_paged_compact, METH_FASTCALL, nullptr},
+                         {"paged_copy", (PyCFunction)(void*)py_paged_copy, METH_FASTCALL, nullptr},
                          {"raise_with", py_raise_with, METH_O, nullptr},
                          {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_kvo_binding", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};

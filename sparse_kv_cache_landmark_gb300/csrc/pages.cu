@@ -1,0 +1,648 @@
+// The pages of a paged cache through their life: kvo_paged_reserve, kvo_paged_fork, kvo_paged_compact keep the book of
+// who holds which page, kvo_paged_copy moves what pages hold.
+//
+// The book is the table (page ids of each request), `held` (how many of them a request has) and refs[page], how often a
+// page is named; 0 is free.  Free pages are always handed out lowest first, in the order of the requests, so results do
+// not depend on timing: refs change by integer atomics, whose order does not matter, and ranks come from prefix sums.
+//
+// What bounds the book's calls is latency: a look at refs (1 MB for 262144 pages, 0.2 us of HBM) and two dependent passes
+// over it with a sum over all pages between.  One cluster of 8 CTAs takes them in one launch, exchanging the CTAs' sums
+// through distributed shared memory; rows of the table, which may be long, are moved by other CTAs.
+#include <algorithm>
+
+#include "kvo_internal.cuh"
+#include "launch.cuh"
+#include "paged.cuh"
+#include "tma_ptx.cuh"
+
+namespace kvo {
+
+constexpr int PG_THREADS = 1024;
+constexpr int PG_CLUSTER = 8;
+constexpr int PG_BATCH = 8192;                // requests of a call
+constexpr int PG_ROW_THREADS = 256;
+
+struct Book {
+    int32_t* table;
+    int32_t* held;
+    int32_t* refs;
+    int32_t* status;
+    int batch, max_pages, n_pages, page;
+};
+
+__device__ __forceinline__ void pg_report(const Book& B, int bits) {
+    if (B.status) atomicOr(B.status, bits);
+}
+
+// Exclusive sum over the CTA's threads; `all` gets the sum of all.  Two barriers; sums: 32 words.
+__device__ __forceinline__ int block_sum(int v, int* sums, int& all) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    int s = v;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int x = __shfl_up_sync(0xffffffffu, s, o);
+        if (lane >= o) s += x;
+    }
+    __syncthreads();                          // the last call's words have been read
+    if (lane == 31) sums[warp] = s;
+    __syncthreads();
+    const int t = lane < (int)blockDim.x / 32 ? sums[lane] : 0;
+    int c = t;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int x = __shfl_up_sync(0xffffffffu, c, o);
+        if (lane >= o) c += x;
+    }
+    all = __shfl_sync(0xffffffffu, c, 31);
+    return s - v + __shfl_sync(0xffffffffu, c - t, warp);
+}
+
+// A thread's share of the pages: a run of whole 16-byte words of refs, in the order of CTAs and threads.
+struct Share {
+    int first, end;
+};
+__device__ __forceinline__ Share pg_share(const Book& B) {
+    const int64_t threads = (int64_t)cluster_size() * PG_THREADS, words = ((int64_t)B.n_pages + 3) / 4;
+    const int64_t each = 4 * ((words + threads - 1) / threads), at = ((int64_t)cluster_rank() * PG_THREADS + threadIdx.x) * each;
+    return {(int)min(at, (int64_t)B.n_pages), (int)min(at + each, (int64_t)B.n_pages)};
+}
+// f(page, refs) for each page of the share.
+template <typename F>
+__device__ __forceinline__ void pg_each(const Book& B, const Share& s, F&& f) {
+    int p = s.first;
+    for (; p + 4 <= s.end; p += 4) {
+        const int4 v = *reinterpret_cast<const int4*>(B.refs + p);
+        f(p, v.x);
+        f(p + 1, v.y);
+        f(p + 2, v.z);
+        f(p + 3, v.w);
+    }
+    for (; p < s.end; ++p) f(p, B.refs[p]);
+}
+__device__ __forceinline__ int pg_count_free(const Book& B, const Share& s) {
+    int n = 0;
+    pg_each(B, s, [&](int, int v) { n += v == 0; });
+    return n;
+}
+// Free pages before this thread's share, of `free` in all; `mine` of them in this CTA before the thread, `cta` in the CTA.
+// One cluster barrier: what any thread of the cluster wrote before it is seen by all after it.
+__device__ __forceinline__ int pg_rank(int mine, int cta, int* exchange, int& free) {
+    if (threadIdx.x == 0) *exchange = cta;
+    cluster_barrier();
+    const int lane = threadIdx.x & 31, me = cluster_rank();
+    int v = lane < (int)cluster_size() ? (int)ld_cluster_u32(exchange, lane) : 0, before = lane < me ? v : 0;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        v += __shfl_xor_sync(0xffffffffu, v, o);
+        before += __shfl_xor_sync(0xffffffffu, before, o);
+    }
+    free = v;
+    return before + mine;
+}
+
+// ------------------------------------------------------------------ reserve
+__global__ void __launch_bounds__(PG_THREADS, 1) pages_reserve_kernel(const Book B, const int32_t* want) {
+    extern __shared__ int32_t smem[];
+    int32_t* end = smem;                      // [batch]: pages asked for by the requests up to this one
+    int32_t* had = smem + B.batch;            // [batch]: pages held before
+    __shared__ int sums[32], exchange, given;
+    grid_wait();
+    const int tid = threadIdx.x;
+    if (tid == 0) given = 0;
+    const int per = (B.batch + PG_THREADS - 1) / PG_THREADS, b0 = min(tid * per, B.batch), b1 = min(b0 + per, B.batch);
+    int need = 0;
+    for (int b = b0; b < b1; ++b) {
+        const int w = want[b], h = B.held[b];
+        const int pages = (int)(((int64_t)w + B.page - 1) / B.page);
+        const bool bad = w < 0 || pages > B.max_pages || h < 0 || h > B.max_pages;
+        if (bad && cluster_rank() == 0) pg_report(B, KVO_DEV_BAD_COUNT);
+        if (!bad) need += max(pages - h, 0);
+        end[b] = need;
+        had[b] = h;
+    }
+    const Share share = pg_share(B);
+    const int free_here = pg_count_free(B, share);
+    int all, cta, free;
+    const int asked_before = block_sum(need, sums, all);
+    const int rank_here = block_sum(free_here, sums, cta);
+    for (int b = b0; b < b1; ++b) end[b] += asked_before;
+    int rank = pg_rank(rank_here, cta, &exchange, free);         // (also a barrier of this CTA, for `end`)
+    int last = 0;
+    for (int b = b0; b < b1; ++b)
+        if (end[b] <= free) last = end[b];
+    if (last) atomicMax(&given, last);
+    __syncthreads();
+    const int n = given;
+    if (cluster_rank() == 0)
+        for (int b = b0; b < b1; ++b) {
+            const int mine = end[b] - (b ? end[b - 1] : 0);
+            if (mine && end[b] <= n) B.held[b] = had[b] + mine;
+            if (mine && end[b] > n) pg_report(B, KVO_DEV_NO_PAGES);
+        }
+    if (rank < n && free_here) {
+        int b = 0;                            // the first request that asked for more than `rank` pages with those before it
+        for (int len = B.batch; len > 1;) {
+            const int half = len / 2;
+            if (end[b + half - 1] <= rank) b += half;
+            len -= half;
+        }
+        pg_each(B, share, [&](int p, int v) {
+            if (v != 0 || rank >= n) return;
+            while (end[b] <= rank) ++b;
+            const int64_t at = (int64_t)b * B.max_pages + had[b] + rank - (b ? end[b - 1] : 0);
+            B.table[at] = p;
+            B.refs[p] = 1;
+            ++rank;
+        });
+    }
+    cluster_barrier();                        // nobody leaves while its sum is read
+}
+
+// ------------------------------------------------------------------ fork
+struct ForkArgs {
+    Book book;
+    const int32_t* parent;
+    const int32_t* keep;
+    int32_t* src;
+    int32_t* dst;
+    int32_t* count;
+    int32_t* rows;                            // [batch][max_pages]: the new rows of requests that change parents
+    int4* meta;                               // [batch]: pages before, pages after, the part-filled last one or -1, parent
+    int32_t* list;                            // [batch]: the requests that get a copy, then their number
+    int slots;                                // of the hash table, a power of two >= 2 batch
+};
+
+// First launch, a CTA per request: the new rows, read from the table as it was, and every page's new number of uses.
+__global__ void __launch_bounds__(PG_ROW_THREADS) pages_fork_rows_kernel(const ForkArgs A) {
+    const Book& B = A.book;
+    grid_wait();
+    const int b = blockIdx.x;
+    int before = B.held[b], p = A.parent[b];
+    const int keep = A.keep[b];
+    bool bad = before < 0 || before > B.max_pages;
+    before = min(max(before, 0), B.max_pages);
+    int after = before, part = 0;
+    if (p < -1 || p >= B.batch) bad = true;
+    else if (p < 0) after = 0;
+    else {
+        const int pages = (int)(((int64_t)max(keep, 0) + B.page - 1) / B.page), most = p == b ? before : B.held[p];
+        if (keep < 0 || pages > most || most > B.max_pages) bad = true;
+        else { after = pages; part = keep % B.page; }
+    }
+    if (bad) { p = b; after = before; part = 0; }             // stays as it is
+    if (bad && threadIdx.x == 0) pg_report(B, KVO_DEV_BAD_COUNT);
+    const int32_t* old = B.table + (int64_t)b * B.max_pages;
+    const int32_t* from = B.table + (int64_t)max(p, 0) * B.max_pages;
+    int32_t* to = A.rows + (int64_t)b * B.max_pages;
+    bool wrong = false;
+    auto use = [&](int page, int n) {
+        if (page < 0 || page >= B.n_pages) wrong = true;
+        else atomicAdd(B.refs + page, n);
+    };
+    for (int j = (p == b ? after : 0) + threadIdx.x; j < max(after, before); j += PG_ROW_THREADS) {
+        const int o = j < before ? old[j] : -1, e = j < after ? from[j] : -1;
+        if (j < after) to[j] = e;
+        if (j < after && j < before && e == o) continue;
+        if (j < after) use(e, 1);
+        if (j < before) use(o, -1);
+    }
+    if (threadIdx.x == 0) {
+        int last = -1;
+        if (part && after) {
+            last = from[after - 1];
+            if (last < 0 || last >= B.n_pages) { wrong = true; last = -1; }
+        }
+        A.meta[b] = make_int4(before, after, last, p);
+    }
+    if (wrong) pg_report(B, KVO_DEV_BAD_BLOCK_ID);
+}
+
+// Second launch.  The first cluster settles the part-filled pages: a request that will write into one must be alone with
+// it.  The other CTAs write the rows, but for the entry of such a page.
+__global__ void __launch_bounds__(PG_THREADS, 1) pages_fork_kernel(const ForkArgs A) {
+    const Book& B = A.book;
+    extern __shared__ int32_t smem[];
+    __shared__ int sums[32], exchange;
+    grid_wait();
+    const int tid = threadIdx.x;
+    if (blockIdx.x >= cluster_size()) {
+        constexpr int AT_ONCE = PG_THREADS / PG_ROW_THREADS;
+        const int ctas = gridDim.x - cluster_size(), t = tid % PG_ROW_THREADS;
+        for (int64_t b = (int64_t)(blockIdx.x - cluster_size()) * AT_ONCE + tid / PG_ROW_THREADS; b < B.batch; b += (int64_t)ctas * AT_ONCE) {
+            const int4 m = A.meta[b];
+            const int before = m.x, after = m.y;
+            const bool same = m.w == b;
+            int32_t* to = B.table + b * B.max_pages;
+            const int32_t* from = A.rows + b * B.max_pages;
+            for (int j = (same ? after : 0) + t; j < max(after, before); j += PG_ROW_THREADS)
+                if (j >= after) to[j] = -1;
+                else if (m.z < 0 || j != after - 1) to[j] = from[j];
+        }
+        return;
+    }
+    const Share share = pg_share(B);
+    const int free_here = pg_count_free(B, share);
+    int cta, free;
+    const int rank_here = block_sum(free_here, sums, cta);
+    int mine = 0, first_rank = 0;             // copies of this thread's requests (first CTA only), and those before them
+    const int per = (B.batch + PG_THREADS - 1) / PG_THREADS, b0 = min(tid * per, B.batch), b1 = min(b0 + per, B.batch);
+    int total = 0;
+    if (cluster_rank() == 0) {
+        int32_t *key = smem, *first = smem + A.slots, *holders = smem + 2 * A.slots;
+        for (int i = tid; i < A.slots; i += PG_THREADS) { key[i] = -1; first[i] = INT32_MAX; holders[i] = 0; }
+        __syncthreads();
+        auto find = [&](int page) {           // its slot; there are twice as many slots as pages
+            uint32_t i = (uint32_t)page * 2654435761u >> 7 & (A.slots - 1);
+            while (true) {
+                const int k = atomicCAS(key + i, -1, page);
+                if (k == -1 || k == page) return i;
+                i = (i + 1) & (A.slots - 1);
+            }
+        };
+        for (int b = b0; b < b1; ++b) {
+            const int page = A.meta[b].z;
+            if (page < 0) continue;
+            const uint32_t i = find(page);
+            atomicMin(first + i, b);
+            atomicAdd(holders + i, 1);
+        }
+        __syncthreads();
+        auto copies = [&](int b, int page) {
+            if (page < 0) return false;
+            const uint32_t i = find(page);
+            return !(first[i] == b && B.refs[page] == holders[i]);
+        };
+        for (int b = b0; b < b1; ++b) mine += copies(b, A.meta[b].z);
+        first_rank = block_sum(mine, sums, total);
+        int at = first_rank;
+        for (int b = b0; b < b1; ++b)
+            if (copies(b, A.meta[b].z)) A.list[at++] = b;
+        if (tid == 0) A.list[B.batch] = total;
+    }
+    int rank = pg_rank(rank_here, cta, &exchange, free);
+    const int n = min(__ldcg(A.list + B.batch), free);
+    if (cluster_rank() == 0) {
+        int at = first_rank;
+        for (int b = b0; b < b1; ++b) {
+            const int4 m = A.meta[b];
+            const bool copied = mine && at < total && A.list[at] == b;
+            const bool lost = copied && at >= n;
+            if (copied) {
+                ++at;
+                atomicSub(B.refs + m.z, 1);   // others hold it, or hold on to it: it does not become free
+            }
+            if (lost) pg_report(B, KVO_DEV_NO_PAGES);
+            if (m.z >= 0 && (!copied || lost)) B.table[(int64_t)b * B.max_pages + m.y - 1] = lost ? -1 : m.z;
+            B.held[b] = m.y - lost;
+        }
+        for (int i = n + tid; i < B.batch; i += PG_THREADS) A.src[i] = A.dst[i] = -1;
+        if (tid == 0) *A.count = n;
+    }
+    if (rank < n && free_here)
+        pg_each(B, share, [&](int p, int v) {
+            if (v != 0 || rank >= n) return;
+            const int b = __ldcg(A.list + rank);
+            const int4 m = A.meta[b];
+            B.table[(int64_t)b * B.max_pages + m.y - 1] = p;
+            B.refs[p] = 1;
+            A.src[rank] = m.z;
+            A.dst[rank] = p;
+            ++rank;
+        });
+    cluster_barrier();                        // nobody leaves while its sum is read
+}
+
+// ------------------------------------------------------------------ compact
+struct CompactArgs {
+    Book book;
+    int32_t* table_out;
+    int32_t* refs_out;
+    int32_t* src;
+    int32_t* dst;
+    int32_t* count;
+    int32_t* head;                            // [0]: the pages in use, L; [1]: the moves
+    int32_t* to;                              // [n_pages]: where page p >= L goes
+};
+
+// First launch, one cluster: L pages are in use; the i-th of those at L and behind goes to the i-th free one before L.
+__global__ void __launch_bounds__(PG_THREADS, 1) pages_compact_kernel(const CompactArgs A) {
+    const Book& B = A.book;
+    __shared__ int sums[32], exchange;
+    grid_wait();
+    const Share share = pg_share(B);
+    const int free_here = pg_count_free(B, share);
+    int cta, free;
+    const int rank_here = block_sum(free_here, sums, cta);
+    const int first = pg_rank(rank_here, cta, &exchange, free);
+    const int live = B.n_pages - free;
+    int rank = first;
+    pg_each(B, share, [&](int p, int v) {
+        if (p == live) A.head[1] = rank;      // the free pages before L are as many as the used ones from L on
+        if (v == 0) {
+            if (p < live) A.dst[rank] = p;
+            ++rank;
+        }
+        if (A.refs_out != B.refs) A.refs_out[p] = v;
+    });
+    if (cluster_rank() == 0 && threadIdx.x == 0) {
+        A.head[0] = live;
+        if (live == B.n_pages) A.head[1] = 0;
+    }
+    cluster_barrier();
+    const int moves = __ldcg(A.head + 1);
+    rank = first;
+    pg_each(B, share, [&](int p, int v) {
+        if (p == live) rank = moves;          // (free pages before L may have been filled meanwhile)
+        if (p >= live) {
+            int to = p;
+            if (v != 0) {
+                const int i = p - rank - (live - moves);
+                to = __ldcg(A.dst + i);
+                A.src[i] = p;
+                A.refs_out[to] = v;
+                A.refs_out[p] = 0;
+            }
+            A.to[p] = to;
+        }
+        rank += v == 0;
+    });
+    for (int i = moves + cluster_rank() * PG_THREADS + threadIdx.x; i < B.n_pages / 2; i += cluster_size() * PG_THREADS)
+        A.src[i] = A.dst[i] = -1;
+    if (cluster_rank() == 0 && threadIdx.x == 0) *A.count = moves;
+}
+
+// Second launch, a CTA per request: the rows' entries follow their pages.
+__global__ void __launch_bounds__(PG_ROW_THREADS) pages_compact_rows_kernel(const CompactArgs A) {
+    const Book& B = A.book;
+    grid_wait();
+    const int b = blockIdx.x, live = A.head[0];
+    int held = B.held[b];
+    if ((held < 0 || held > B.max_pages) && threadIdx.x == 0) pg_report(B, KVO_DEV_BAD_COUNT);
+    held = min(max(held, 0), B.max_pages);
+    const int32_t* from = B.table + (int64_t)b * B.max_pages;
+    int32_t* to = A.table_out + (int64_t)b * B.max_pages;
+    const int end = A.table_out == B.table ? held : B.max_pages;
+    bool wrong = false;
+    for (int j = threadIdx.x; j < end; j += PG_ROW_THREADS) {
+        int e = from[j];
+        if (j < held) {
+            if (e < 0 || e >= B.n_pages) wrong = true;
+            else if (e >= live) e = A.to[e];
+        }
+        to[j] = e;
+    }
+    if (wrong) pg_report(B, KVO_DEV_BAD_BLOCK_ID);
+}
+
+// ------------------------------------------------------------------ copy
+struct CopyArgs {
+    uint8_t* pages[2];
+    float* scale[2];
+    const int32_t* src;
+    const int32_t* dst;
+    const int32_t* count;                     // or NULL: all `moves`
+    int32_t* status;
+    int64_t layer_bytes;                      // of one layer's K (or V)
+    int page_bytes, n_pages, hkv, layers, moves, pieces;
+};
+constexpr int PC_THREADS = 256, PC_LOADS = 8, PC_PIECE = PC_THREADS * PC_LOADS * 16;
+
+// Bound by HBM: every byte is read once and written once.  A piece is 32 KB of a page (or a page, where that is smaller).
+__global__ void __launch_bounds__(PC_THREADS) pages_copy_kernel(const CopyArgs A) {
+    grid_wait();
+    int n = A.moves;
+    if (A.count) {
+        const int c = *A.count;
+        if ((c < 0 || c > n) && blockIdx.x == 0 && threadIdx.x == 0 && A.status) atomicOr(A.status, KVO_DEV_BAD_COUNT);
+        n = min(max(c, 0), n);
+    }
+    const int64_t units = (int64_t)n * A.pieces * 2 * A.layers;
+    for (int64_t u = blockIdx.x; u < units; u += gridDim.x) {
+        const int piece = (int)(u % A.pieces), kv = (int)(u / A.pieces & 1);
+        const int64_t m = u / A.pieces >> 1;
+        const int layer = (int)(m / n), i = (int)(m - (int64_t)layer * n);
+        const int s = A.src[i], d = A.dst[i];
+        if (s < 0 || s >= A.n_pages || d < 0 || d >= A.n_pages) {
+            if (threadIdx.x == 0 && A.status) atomicOr(A.status, KVO_DEV_BAD_BLOCK_ID);
+            continue;
+        }
+        if (s == d) continue;
+        uint8_t* base = A.pages[kv] + layer * A.layer_bytes;
+        const int off = piece * PC_PIECE, bytes = min(PC_PIECE, A.page_bytes - off);
+        const uint4* from = reinterpret_cast<const uint4*>(base + (int64_t)s * A.page_bytes + off);
+        uint4* to = reinterpret_cast<uint4*>(base + (int64_t)d * A.page_bytes + off);
+        uint4 v[PC_LOADS];
+#pragma unroll
+        for (int e = 0; e < PC_LOADS; ++e)
+            if ((e * PC_THREADS + (int)threadIdx.x) * 16 < bytes) v[e] = __ldcs(from + e * PC_THREADS + threadIdx.x);
+#pragma unroll
+        for (int e = 0; e < PC_LOADS; ++e)
+            if ((e * PC_THREADS + (int)threadIdx.x) * 16 < bytes) to[e * PC_THREADS + threadIdx.x] = v[e];
+        if (A.scale[kv] && piece == 0) {
+            float* sc = A.scale[kv] + (int64_t)layer * A.n_pages * A.hkv;
+            for (int h = threadIdx.x; h < A.hkv; h += PC_THREADS) sc[(int64_t)d * A.hkv + h] = sc[(int64_t)s * A.hkv + h];
+        }
+    }
+}
+
+// ------------------------------------------------------------------ host
+const char* book_error(const kvo_page_book* b) {
+    if (!b) return "null book";
+    if (b->batch < 0 || b->batch > PG_BATCH) return "batch must be in 0..8192";
+    if (b->n_pages < 1 || b->max_pages < 1) return "need n_pages >= 1 and max_pages >= 1";
+    if (b->page_size < 1 || (int64_t)b->max_pages * b->page_size > INT32_MAX) return "need page_size >= 1 and max_pages * page_size below 2^31";
+    if ((int64_t)b->batch * b->max_pages > INT32_MAX) return "batch * max_pages must fit in 31 bits";
+    if (!b->refs || (b->batch > 0 && (!b->table || !b->held))) return "null table, held or refs";
+    if ((uintptr_t)b->refs % 16) return "refs must be 16-byte aligned";
+    return nullptr;
+}
+Book device_book(const kvo_page_book* b, int32_t* status) {
+    return {b->table, b->held, b->refs, status, b->batch, b->max_pages, b->n_pages, b->page_size};
+}
+Bytes table_of(const kvo_page_book* b) { return {b->table, 4ll * b->batch * b->max_pages}; }
+Bytes held_of(const kvo_page_book* b) { return {b->held, 4ll * b->batch}; }
+Bytes refs_of(const kvo_page_book* b) { return {b->refs, 4ll * b->n_pages}; }
+// Whether a range of `some` shares a byte with another of them, or with one of `others`.
+bool any_meet(std::initializer_list<Bytes> some, std::initializer_list<Bytes> others) {
+    for (const Bytes* x = some.begin(); x != some.end(); ++x) {
+        if (meets_any(*x, others)) return true;
+        for (const Bytes* y = x + 1; y != some.end(); ++y)
+            if (meets_any(*x, {*y})) return true;
+    }
+    return false;
+}
+size_t up256(size_t x) { return (x + 255) / 256 * 256; }
+// CTAs of the cluster that looks at refs: one where it can hold a page of each in a word, without barriers of clusters.
+int pages_cluster(int n_pages) { return n_pages <= 4 * PG_THREADS ? 1 : PG_CLUSTER; }
+
+size_t fork_workspace(const kvo_page_book* b) {
+    return up256((size_t)b->batch * sizeof(int4)) + up256(((size_t)b->batch + 1) * 4) + up256((size_t)b->batch * b->max_pages * 4);
+}
+size_t compact_workspace(const kvo_page_book* b) { return 256 + up256((size_t)b->n_pages * 4); }
+
+cudaError_t allow_smem(const void* kernel, std::atomic<uint64_t>& done, int bytes) {
+    if (!first_on_device(done)) return cudaSuccess;
+    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (e == cudaSuccess) mark_on_device(done);
+    return e;
+}
+
+}  // namespace kvo
+
+namespace {
+
+kvo_status refuse(const char* m) {
+    kvo::set_last_error(m);
+    return KVO_ERR_INVALID;
+}
+kvo_status launched(cudaError_t e) {
+    if (e == cudaSuccess) return KVO_OK;
+    kvo::set_last_error(cudaGetErrorString(e));
+    return KVO_ERR_CUDA;
+}
+
+}  // namespace
+
+extern "C" kvo_status kvo_paged_reserve(const kvo_page_book* book, const int32_t* want, int32_t* status, kvo_stream_t stream) {
+    using namespace kvo;
+    if (const char* m = book_error(book)) return refuse(m);
+    if (book->batch == 0) return KVO_OK;
+    if (!want) return refuse("null pointer argument");
+    if (any_meet({table_of(book), held_of(book), refs_of(book)}, {{want, 4ll * book->batch}}))
+        return refuse("table, held and refs must be apart from each other and from want");
+    static std::atomic<uint64_t> done{0};
+    cudaError_t e = allow_smem((const void*)pages_reserve_kernel, done, PG_BATCH * 8);
+    if (e == cudaSuccess) {
+        const int cluster = pages_cluster(book->n_pages);
+        e = launch_dependent(pages_reserve_kernel, dim3(cluster), PG_THREADS, (size_t)book->batch * 8, (cudaStream_t)stream, cluster,
+                             device_book(book, status), want);
+    }
+    return launched(e);
+}
+
+extern "C" kvo_status kvo_paged_fork_workspace(const kvo_page_book* book, size_t* bytes_out) {
+    if (!bytes_out) return refuse("null output pointer");
+    *bytes_out = 0;
+    if (const char* m = kvo::book_error(book)) return refuse(m);
+    *bytes_out = kvo::fork_workspace(book);
+    return KVO_OK;
+}
+
+extern "C" kvo_status kvo_paged_fork(const kvo_page_book* book, const int32_t* parent, const int32_t* keep, int32_t* src,
+                                     int32_t* dst, int32_t* count, void* workspace, size_t workspace_bytes, int32_t* status,
+                                     kvo_stream_t stream) {
+    using namespace kvo;
+    if (const char* m = book_error(book)) return refuse(m);
+    if (!count) return refuse("null pointer argument");
+    cudaStream_t s = (cudaStream_t)stream;
+    if (book->batch == 0) return launched(cudaMemsetAsync(count, 0, 4, s));
+    if (!parent || !keep || !src || !dst) return refuse("null pointer argument");
+    const size_t need = fork_workspace(book);
+    if (!workspace || workspace_bytes < need) return refuse("the workspace is too small (kvo_paged_fork_workspace)");
+    if ((uintptr_t)workspace % 256) return refuse("the workspace must be 256-byte aligned");
+    const int64_t b4 = 4ll * book->batch;
+    if (any_meet({table_of(book), held_of(book), refs_of(book), {src, b4}, {dst, b4}, {count, 4}, {workspace, (int64_t)need}},
+                 {{parent, b4}, {keep, b4}}))
+        return refuse("what the call writes must be apart from each other and from parent and keep");
+    ForkArgs A{};
+    A.book = device_book(book, status);
+    A.parent = parent;
+    A.keep = keep;
+    A.src = src;
+    A.dst = dst;
+    A.count = count;
+    uint8_t* ws = (uint8_t*)workspace;
+    A.meta = (int4*)ws;
+    A.list = (int32_t*)(ws + up256((size_t)book->batch * sizeof(int4)));
+    A.rows = (int32_t*)((uint8_t*)A.list + up256(((size_t)book->batch + 1) * 4));
+    A.slots = 32;
+    while (A.slots < 2 * book->batch) A.slots *= 2;
+    static std::atomic<uint64_t> done{0};
+    cudaError_t e = allow_smem((const void*)pages_fork_kernel, done, 2 * PG_BATCH * 12);
+    if (e != cudaSuccess) return launched(e);
+    e = launch_dependent(pages_fork_rows_kernel, dim3(book->batch), PG_ROW_THREADS, 0, s, 0, A);
+    if (e != cudaSuccess) return launched(e);
+    const int cluster = pages_cluster(book->n_pages), rows = (book->batch + 3) / 4;
+    const int ctas = cluster + (std::min(rows, 128) + cluster - 1) / cluster * cluster;
+    return launched(launch_dependent(pages_fork_kernel, dim3(ctas), PG_THREADS, (size_t)A.slots * 12, s, cluster, A));
+}
+
+extern "C" kvo_status kvo_paged_compact_workspace(const kvo_page_book* book, size_t* bytes_out) {
+    if (!bytes_out) return refuse("null output pointer");
+    *bytes_out = 0;
+    if (const char* m = kvo::book_error(book)) return refuse(m);
+    *bytes_out = kvo::compact_workspace(book);
+    return KVO_OK;
+}
+
+extern "C" kvo_status kvo_paged_compact(const kvo_page_book* book, int32_t* table_out, int32_t* refs_out, int32_t* src,
+                                        int32_t* dst, int32_t* count, void* workspace, size_t workspace_bytes,
+                                        int32_t* status, kvo_stream_t stream) {
+    using namespace kvo;
+    if (const char* m = book_error(book)) return refuse(m);
+    if (!table_out) table_out = book->table;
+    if (!refs_out) refs_out = book->refs;
+    if (!count || (book->n_pages > 1 && (!src || !dst))) return refuse("null pointer argument");
+    const size_t need = compact_workspace(book);
+    if (!workspace || workspace_bytes < need) return refuse("the workspace is too small (kvo_paged_compact_workspace)");
+    if ((uintptr_t)workspace % 256) return refuse("the workspace must be 256-byte aligned");
+    const int64_t half = 4ll * (book->n_pages / 2);
+    const Bytes table = table_of(book), refs = refs_of(book);
+    if (any_meet({{src, half}, {dst, half}, {count, 4}, {workspace, (int64_t)need}, {table_out, table.n}, {refs_out, refs.n}}, {held_of(book)}) ||
+        any_meet({{src, half}, {dst, half}, {count, 4}, {workspace, (int64_t)need}}, {table, refs}) ||
+        (table_out != book->table && meets_any({table_out, table.n}, {table, refs})) ||
+        (refs_out != book->refs && meets_any({refs_out, refs.n}, {table, refs})))
+        return refuse("what the call writes must be apart from each other and from what it reads (table_out and refs_out may be table and refs)");
+    CompactArgs A{};
+    A.book = device_book(book, status);
+    A.table_out = table_out;
+    A.refs_out = refs_out;
+    A.src = src;
+    A.dst = dst;
+    A.count = count;
+    A.head = (int32_t*)workspace;
+    A.to = A.head + 64;
+    cudaStream_t s = (cudaStream_t)stream;
+    const int cluster = pages_cluster(book->n_pages);
+    cudaError_t e = launch_dependent(pages_compact_kernel, dim3(cluster), PG_THREADS, 0, s, cluster, A);
+    if (e == cudaSuccess && book->batch)
+        e = launch_dependent(pages_compact_rows_kernel, dim3(book->batch), PG_ROW_THREADS, 0, s, 0, A);
+    return launched(e);
+}
+
+extern "C" kvo_status kvo_paged_copy(const kvo_paged_cache* pools, int layers, const int32_t* src, const int32_t* dst, int moves,
+                                     const int32_t* count, int32_t* status, kvo_stream_t stream) {
+    using namespace kvo;
+    if (!pools) return refuse("null cache");
+    kvo_paged_cache c = *pools;               // a call without requests: table and batch are not looked at
+    c.batch = 0;
+    c.max_pages = 1;
+    if (const char* m = paged_cache_error(&c)) return refuse(m);
+    if (layers < 0 || moves < 0) return refuse("layers and moves must be >= 0");
+    const int64_t layer = page_bytes(&c), scales = scale_bytes(&c);
+    if (layer / c.n_pages > (1 << 30)) return refuse("a page must be at most 2^30 bytes");
+    if (layers > 65536 || layer > INT64_MAX / 4 / std::max(layers, 1)) return refuse("layers must be <= 65536");
+    if (layers == 0 || moves == 0) return KVO_OK;
+    if (!src || !dst) return refuse("null pointer argument");
+    const Bytes k{c.k_pages, layer * layers}, v{c.v_pages, layer * layers}, ks{c.k_scale, scales * layers}, vs{c.v_scale, scales * layers};
+    if (any_meet({k, v, ks, vs}, {{src, 4ll * moves}, {dst, 4ll * moves}, {count, 4}}))
+        return refuse("pools and scales must be apart from each other and from src, dst and count");
+    CopyArgs A{};
+    A.pages[0] = (uint8_t*)c.k_pages;
+    A.pages[1] = (uint8_t*)c.v_pages;
+    A.scale[0] = scales ? c.k_scale : nullptr;
+    A.scale[1] = scales ? c.v_scale : nullptr;
+    A.src = src;
+    A.dst = dst;
+    A.count = count;
+    A.status = status;
+    A.layer_bytes = layer;
+    A.n_pages = c.n_pages;
+    A.page_bytes = (int)(layer / c.n_pages);
+    A.hkv = c.n_kv_heads;
+    A.layers = layers;
+    A.moves = moves;
+    A.pieces = (A.page_bytes + PC_PIECE - 1) / PC_PIECE;
+    const int64_t units = (int64_t)moves * A.pieces * 2 * layers;
+    return launched(launch_dependent(pages_copy_kernel, dim3((unsigned)std::min<int64_t>(units, 152 * 6)), PC_THREADS, 0, (cudaStream_t)stream, 0, A));
+}

@@ -4,7 +4,7 @@ Every step of the decode path runs in the library's CUDA kernels; this module
 turns torch tensors into pointers, allocates outputs with torch, and raises
 ``KvoError`` on any non-OK status.  There is no fallback: without the built
 library or a CUDA device every call fails.  The serving calls (rope, paged_append,
-paged_attn, prompt_attn), which a decode loop makes once per layer and token, go
+paged_attn, prompt_attn, the pages' bookkeeping), which a decode loop makes once per layer and token, go
 through a native binding (csrc/binding.cpp) instead of ctypes.  They are for
 inference: nothing is recorded for a backward pass.
 """
@@ -22,7 +22,7 @@ _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libkvo.so")
 
 KVO_OK, KVO_ERR_INVALID, KVO_ERR_CUDA, KVO_ERR_OOM, KVO_ERR_TIMEOUT, KVO_ERR_STATE, KVO_ERR_DEVICE = range(7)
-DEV_BAD_BLOCK_ID, DEV_BAD_SLOT, DEV_BAD_COUNT, DEV_UNSORTED, DEV_TIMEOUT = 1, 2, 4, 8, 16
+DEV_BAD_BLOCK_ID, DEV_BAD_SLOT, DEV_BAD_COUNT, DEV_UNSORTED, DEV_TIMEOUT, DEV_NO_PAGES = 1, 2, 4, 8, 16, 32
 
 EXPORTS = ["kv_offload_init", "kv_offload_destroy", "select_topk", "index_diff", "gather_coalesced",
            "sparse_decode_attn", "merge_lse", "kvo_decode_step", "kvo_reset_prediction", "kvo_get_stream",
@@ -33,7 +33,8 @@ EXPORTS = ["kv_offload_init", "kv_offload_destroy", "select_topk", "index_diff",
            "kvo_set_prefetch_budget", "kvo_set_lowrank_keys", "kvo_plan_attention", "kvo_plan_select", "kvo_set_wait_test",
            "kvo_set_call_wait_test",
            "kvo_set_spec_policy", "kvo_spec_stats", "kvo_rope", "kvo_paged_append", "kvo_paged_attn",
-           "kvo_paged_attn_workspace", "kvo_prompt_attn"]
+           "kvo_paged_attn_workspace", "kvo_prompt_attn", "kvo_paged_reserve", "kvo_paged_fork",
+           "kvo_paged_fork_workspace", "kvo_paged_compact", "kvo_paged_compact_workspace", "kvo_paged_copy"]
 PROFILE_KINDS = ["select", "diff", "coalesce", "gather_prefetch", "gather_urgent", "attention", "recon"]
 
 
@@ -56,6 +57,12 @@ class _PagedCache(ctypes.Structure):
                 ("v_scale", ctypes.c_void_p), ("table", ctypes.c_void_p), ("batch", ctypes.c_int32),
                 ("n_kv_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32), ("page_size", ctypes.c_int32),
                 ("n_pages", ctypes.c_int32), ("max_pages", ctypes.c_int32), ("format", ctypes.c_int32)]
+
+
+class _PageBook(ctypes.Structure):
+    _fields_ = [("table", ctypes.c_void_p), ("held", ctypes.c_void_p), ("refs", ctypes.c_void_p),
+                ("batch", ctypes.c_int32), ("max_pages", ctypes.c_int32), ("n_pages", ctypes.c_int32),
+                ("page_size", ctypes.c_int32)]
 
 
 _LIB: Optional[ctypes.CDLL] = None
@@ -111,6 +118,13 @@ def lib() -> ctypes.CDLL:
         L.kvo_paged_attn.argtypes = [PC, VP, I, VP, I64, VP, VP, I, VP, VP, VP, ctypes.c_size_t, VP, VP]
         L.kvo_paged_attn_workspace.argtypes = [PC, I, I, I64, ctypes.POINTER(ctypes.c_size_t)]
         L.kvo_prompt_attn.argtypes = [VP, I64, VP, I64, VP, I64, VP, VP, I, I64, I64, I, I, I, I, VP, VP, VP, VP]
+        PB, SZ, SP = ctypes.POINTER(_PageBook), ctypes.c_size_t, ctypes.POINTER(ctypes.c_size_t)
+        L.kvo_paged_reserve.argtypes = [PB, VP, VP, VP]
+        L.kvo_paged_fork.argtypes = [PB, VP, VP, VP, VP, VP, VP, SZ, VP, VP]
+        L.kvo_paged_fork_workspace.argtypes = [PB, SP]
+        L.kvo_paged_compact.argtypes = [PB, VP, VP, VP, VP, VP, VP, SZ, VP, VP]
+        L.kvo_paged_compact_workspace.argtypes = [PB, SP]
+        L.kvo_paged_copy.argtypes = [PC, I, VP, VP, I, VP, VP, VP]
         L.kvo_last_error.argtypes = [P]
         L.kvo_last_error.restype = ctypes.c_char_p
         for name in EXPORTS:
@@ -348,6 +362,46 @@ def prompt_attn(q, k, v, cu_q, cu_k=None, causal: bool = True, o=None, lse=None,
     int32 [batch + 1] offsets (cu_k None: cu_q).
     """
     return (_BINDING or _native()).prompt_attn(q, k, v, cu_q, cu_k, causal, o, lse, status, stream)
+
+
+def paged_reserve(table, held, refs, want, page_size: int, status=None, stream=None):
+    """Give requests free pages for ``want`` tokens, in place (C: kvo_paged_reserve).
+
+    The book of a paged cache, CUDA int32: table [batch][max_pages], held [batch] (pages of each row), refs
+    [n_pages] (how often a page is named; 0: free).  want: int32 [batch].  Where the free pages run out the requests
+    from that one on keep what they hold, and ``status`` gets DEV_NO_PAGES.
+    """
+    (_BINDING or _native()).paged_reserve(table, held, refs, want, page_size, status, stream)
+
+
+def paged_fork(table, held, refs, parent, keep, page_size: int, src=None, dst=None, count=None, workspace=None,
+               status=None, stream=None):
+    """Fork, reorder, cut and free requests, in place (C: kvo_paged_fork) -> (src, dst, count), moves for ``paged_copy``.
+
+    Request b becomes the first keep[b] tokens of what request parent[b] was (-1: nothing).  Whole pages are shared; a
+    last page filled in part belongs to one request, the others get copies of it: int32 src, dst [batch], count [1].
+    """
+    return (_BINDING or _native()).paged_fork(table, held, refs, parent, keep, page_size, src, dst, count, workspace,
+                                              status, stream)
+
+
+def paged_compact(table, held, refs, table_out=None, refs_out=None, src=None, dst=None, count=None, workspace=None,
+                  status=None, stream=None):
+    """Move the used pages to the front of the pool (C: kvo_paged_compact) -> (src, dst, count), moves for ``paged_copy``.
+
+    table and refs are updated in place, or into ``table_out`` and ``refs_out``; src, dst: int32 [n_pages // 2].
+    """
+    return (_BINDING or _native()).paged_compact(table, held, refs, table_out, refs_out, src, dst, count, workspace,
+                                                 status, stream)
+
+
+def paged_copy(k_pages, v_pages, src, dst, count=None, *, k_scale=None, v_scale=None, status=None, stream=None):
+    """Copy pages src[i] to dst[i], K, V and scales (C: kvo_paged_copy).
+
+    Pools as in ``paged_append``, or [layers][n_pages][Hkv][page_size][d] with scales [layers][n_pages][Hkv]; src, dst:
+    CUDA int32, of which the first ``count`` (int32 [1]; None: all) are taken.
+    """
+    (_BINDING or _native()).paged_copy(k_pages, v_pages, src, dst, count, k_scale, v_scale, status, stream)
 
 
 def set_call_wait_test(limit_ns: int = 2_000_000_000, skip: int = -1):
