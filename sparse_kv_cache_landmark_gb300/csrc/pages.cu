@@ -21,6 +21,7 @@ constexpr int PG_THREADS = 1024;
 constexpr int PG_CLUSTER = 8;
 constexpr int PG_BATCH = 8192;                // requests of a call
 constexpr int PG_ROW_THREADS = 256;
+constexpr int64_t PG_ONE = 1 << 17;           // entries of a table that one cluster moves by itself
 
 struct Book {
     int32_t* table;
@@ -34,19 +35,10 @@ __device__ __forceinline__ void pg_report(const Book& B, int bits) {
     if (B.status) atomicOr(B.status, bits);
 }
 
-// Exclusive sum over the CTA's threads; `all` gets the sum of all.  Two barriers; sums: 32 words.
-__device__ __forceinline__ int block_sum(int v, int* sums, int& all) {
+// The sum of `sums` over the warps before this one, and of all.
+__device__ __forceinline__ int warps_before(const int* sums, int& all) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    int s = v;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const int x = __shfl_up_sync(0xffffffffu, s, o);
-        if (lane >= o) s += x;
-    }
-    __syncthreads();                          // the last call's words have been read
-    if (lane == 31) sums[warp] = s;
-    __syncthreads();
-    const int t = lane < (int)blockDim.x / 32 ? sums[lane] : 0;
+    const int t = sums[lane];                 // 32 warps
     int c = t;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -54,37 +46,64 @@ __device__ __forceinline__ int block_sum(int v, int* sums, int& all) {
         if (lane >= o) c += x;
     }
     all = __shfl_sync(0xffffffffu, c, 31);
-    return s - v + __shfl_sync(0xffffffffu, c - t, warp);
+    return __shfl_sync(0xffffffffu, c - t, warp);
+}
+// Exclusive sum over the CTA's threads; `all` gets the sum of all.  sums: 32 words that nothing else uses.
+__device__ __forceinline__ int block_sum(int v, int* sums, int& all) {
+    const int lane = threadIdx.x & 31;
+    int s = v;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int x = __shfl_up_sync(0xffffffffu, s, o);
+        if (lane >= o) s += x;
+    }
+    if (lane == 31) sums[threadIdx.x >> 5] = s;
+    __syncthreads();
+    return s - v + warps_before(sums, all);
 }
 
-// A thread's share of the pages: a run of whole 16-byte words of refs, in the order of CTAs and threads.
+// A warp's share of the pages: a run of whole groups of 32, in the order of CTAs and warps.
 struct Share {
     int first, end;
 };
 __device__ __forceinline__ Share pg_share(const Book& B) {
-    const int64_t threads = (int64_t)cluster_size() * PG_THREADS, words = ((int64_t)B.n_pages + 3) / 4;
-    const int64_t each = 4 * ((words + threads - 1) / threads), at = ((int64_t)cluster_rank() * PG_THREADS + threadIdx.x) * each;
+    const int64_t warps = (int64_t)cluster_size() * (PG_THREADS / 32), groups = ((int64_t)B.n_pages + 31) / 32;
+    const int64_t each = 32 * ((groups + warps - 1) / warps), at = ((int64_t)cluster_rank() * (PG_THREADS / 32) + (threadIdx.x >> 5)) * each;
     return {(int)min(at, (int64_t)B.n_pages), (int)min(at + each, (int64_t)B.n_pages)};
 }
-// f(page, refs) for each page of the share.
+// Whole warp: f(page, refs, whether there is such a page) for the share, a page to a lane, until it returns false (to all).
 template <typename F>
 __device__ __forceinline__ void pg_each(const Book& B, const Share& s, F&& f) {
-    int p = s.first;
-    for (; p + 4 <= s.end; p += 4) {
-        const int4 v = *reinterpret_cast<const int4*>(B.refs + p);
-        f(p, v.x);
-        f(p + 1, v.y);
-        f(p + 2, v.z);
-        f(p + 3, v.w);
+    constexpr int AT_ONCE = 16;
+    const int lane = threadIdx.x & 31;
+    for (int p0 = s.first; p0 < s.end; p0 += 32 * AT_ONCE) {
+        int v[AT_ONCE];
+#pragma unroll
+        for (int i = 0; i < AT_ONCE; ++i) {
+            const int p = p0 + 32 * i + lane;
+            v[i] = p < s.end ? B.refs[p] : -1;
+        }
+#pragma unroll
+        for (int i = 0; i < AT_ONCE; ++i) {
+            const int p = p0 + 32 * i + lane;
+            if (p - lane >= s.end) return;
+            if (!f(p, v[i], p < s.end)) return;
+        }
     }
-    for (; p < s.end; ++p) f(p, B.refs[p]);
 }
+// The warp's free pages.
 __device__ __forceinline__ int pg_count_free(const Book& B, const Share& s) {
     int n = 0;
-    pg_each(B, s, [&](int, int v) { n += v == 0; });
-    return n;
+    pg_each(B, s, [&](int, int v, bool) { n += v == 0; return true; });
+    return (int)__reduce_add_sync(0xffffffffu, (unsigned)n);
 }
-// Free pages before this thread's share, of `free` in all; `mine` of them in this CTA before the thread, `cta` in the CTA.
+// Of a group of 32 pages: how many are free before this lane's, and in all.
+__device__ __forceinline__ int pg_free_before(int v, int& all) {
+    const unsigned free = __ballot_sync(0xffffffffu, v == 0);
+    all = __popc(free);
+    return __popc(free & ((1u << (threadIdx.x & 31)) - 1));
+}
+// Free pages before this warp's share, of `free` in all; `mine` of them in this CTA before the warp, `cta` in the CTA.
 // One cluster barrier: what any thread of the cluster wrote before it is seen by all after it.
 __device__ __forceinline__ int pg_rank(int mine, int cta, int* exchange, int& free) {
     if (threadIdx.x == 0) *exchange = cta;
@@ -105,7 +124,7 @@ __global__ void __launch_bounds__(PG_THREADS, 1) pages_reserve_kernel(const Book
     extern __shared__ int32_t smem[];
     int32_t* end = smem;                      // [batch]: pages asked for by the requests up to this one
     int32_t* had = smem + B.batch;            // [batch]: pages held before
-    __shared__ int sums[32], exchange, given;
+    __shared__ int sums[32], free_sums[32], exchange, given;
     grid_wait();
     const int tid = threadIdx.x;
     if (tid == 0) given = 0;
@@ -122,9 +141,10 @@ __global__ void __launch_bounds__(PG_THREADS, 1) pages_reserve_kernel(const Book
     }
     const Share share = pg_share(B);
     const int free_here = pg_count_free(B, share);
+    if (tid % 32 == 0) free_sums[tid / 32] = free_here;
     int all, cta, free;
-    const int asked_before = block_sum(need, sums, all);
-    const int rank_here = block_sum(free_here, sums, cta);
+    const int asked_before = block_sum(need, sums, all);      // its barrier is that of free_sums as well
+    const int rank_here = warps_before(free_sums, cta);
     for (int b = b0; b < b1; ++b) end[b] += asked_before;
     int rank = pg_rank(rank_here, cta, &exchange, free);         // (also a barrier of this CTA, for `end`)
     int last = 0;
@@ -140,19 +160,25 @@ __global__ void __launch_bounds__(PG_THREADS, 1) pages_reserve_kernel(const Book
             if (mine && end[b] > n) pg_report(B, KVO_DEV_NO_PAGES);
         }
     if (rank < n && free_here) {
-        int b = 0;                            // the first request that asked for more than `rank` pages with those before it
-        for (int len = B.batch; len > 1;) {
-            const int half = len / 2;
-            if (end[b + half - 1] <= rank) b += half;
-            len -= half;
-        }
-        pg_each(B, share, [&](int p, int v) {
-            if (v != 0 || rank >= n) return;
-            while (end[b] <= rank) ++b;
-            const int64_t at = (int64_t)b * B.max_pages + had[b] + rank - (b ? end[b - 1] : 0);
-            B.table[at] = p;
-            B.refs[p] = 1;
-            ++rank;
+        int b = -1;
+        pg_each(B, share, [&](int p, int v, bool) {
+            int here;
+            const int r = rank + pg_free_before(v, here);
+            if (v == 0 && r < n) {
+                if (b < 0) {                  // the first request that asked for more than r pages with those before it
+                    b = 0;
+                    for (int len = B.batch; len > 1;) {
+                        const int half = len / 2;
+                        if (end[b + half - 1] <= r) b += half;
+                        len -= half;
+                    }
+                }
+                while (end[b] <= r) ++b;
+                B.table[(int64_t)b * B.max_pages + had[b] + r - (b ? end[b - 1] : 0)] = p;
+                B.refs[p] = 1;
+            }
+            rank += here;
+            return rank < n;
         });
     }
     cluster_barrier();                        // nobody leaves while its sum is read
@@ -172,11 +198,11 @@ struct ForkArgs {
     int slots;                                // of the hash table, a power of two >= 2 batch
 };
 
-// First launch, a CTA per request: the new rows, read from the table as it was, and every page's new number of uses.
-__global__ void __launch_bounds__(PG_ROW_THREADS) pages_fork_rows_kernel(const ForkArgs A) {
+// The new row of request b, read from the table as it was, and every page's new number of uses; by PG_ROW_THREADS threads,
+// of which this is the t-th.
+__device__ __forceinline__ void fork_gather(const ForkArgs& A, int b, int t) {
+    constexpr int AT_ONCE = 4;
     const Book& B = A.book;
-    grid_wait();
-    const int b = blockIdx.x;
     int before = B.held[b], p = A.parent[b];
     const int keep = A.keep[b];
     bool bad = before < 0 || before > B.max_pages;
@@ -190,7 +216,7 @@ __global__ void __launch_bounds__(PG_ROW_THREADS) pages_fork_rows_kernel(const F
         else { after = pages; part = keep % B.page; }
     }
     if (bad) { p = b; after = before; part = 0; }             // stays as it is
-    if (bad && threadIdx.x == 0) pg_report(B, KVO_DEV_BAD_COUNT);
+    if (bad && t == 0) pg_report(B, KVO_DEV_BAD_COUNT);
     const int32_t* old = B.table + (int64_t)b * B.max_pages;
     const int32_t* from = B.table + (int64_t)max(p, 0) * B.max_pages;
     int32_t* to = A.rows + (int64_t)b * B.max_pages;
@@ -199,14 +225,25 @@ __global__ void __launch_bounds__(PG_ROW_THREADS) pages_fork_rows_kernel(const F
         if (page < 0 || page >= B.n_pages) wrong = true;
         else atomicAdd(B.refs + page, n);
     };
-    for (int j = (p == b ? after : 0) + threadIdx.x; j < max(after, before); j += PG_ROW_THREADS) {
-        const int o = j < before ? old[j] : -1, e = j < after ? from[j] : -1;
-        if (j < after) to[j] = e;
-        if (j < after && j < before && e == o) continue;
-        if (j < after) use(e, 1);
-        if (j < before) use(o, -1);
+    const int end = max(after, before);
+    for (int j0 = (p == b ? after : 0) + t; j0 < end; j0 += PG_ROW_THREADS * AT_ONCE) {
+        int o[AT_ONCE], e[AT_ONCE];
+#pragma unroll
+        for (int i = 0; i < AT_ONCE; ++i) {
+            const int j = j0 + i * PG_ROW_THREADS;
+            o[i] = j < before ? old[j] : -1;
+            e[i] = j < after ? from[j] : -1;
+        }
+#pragma unroll
+        for (int i = 0; i < AT_ONCE; ++i) {
+            const int j = j0 + i * PG_ROW_THREADS;
+            if (j < after) to[j] = e[i];
+            if (j < after && j < before && e[i] == o[i]) continue;
+            if (j < after) use(e[i], 1);
+            if (j < before) use(o[i], -1);
+        }
     }
-    if (threadIdx.x == 0) {
+    if (t == 0) {
         int last = -1;
         if (part && after) {
             last = from[after - 1];
@@ -216,41 +253,68 @@ __global__ void __launch_bounds__(PG_ROW_THREADS) pages_fork_rows_kernel(const F
     }
     if (wrong) pg_report(B, KVO_DEV_BAD_BLOCK_ID);
 }
+// Writes the new row of request b, but for the entry of a part-filled last page.
+__device__ __forceinline__ void fork_write(const ForkArgs& A, int b, int t) {
+    constexpr int AT_ONCE = 4;
+    const Book& B = A.book;
+    const int4 m = A.meta[b];
+    const int before = m.x, after = m.y, end = max(after, before);
+    int32_t* to = B.table + (int64_t)b * B.max_pages;
+    const int32_t* from = A.rows + (int64_t)b * B.max_pages;
+    for (int j0 = (m.w == b ? after : 0) + t; j0 < end; j0 += PG_ROW_THREADS * AT_ONCE) {
+        int e[AT_ONCE];
+#pragma unroll
+        for (int i = 0; i < AT_ONCE; ++i) {
+            const int j = j0 + i * PG_ROW_THREADS;
+            e[i] = j < after ? from[j] : -1;
+        }
+#pragma unroll
+        for (int i = 0; i < AT_ONCE; ++i) {
+            const int j = j0 + i * PG_ROW_THREADS;
+            if (j < end && (m.z < 0 || j != after - 1)) to[j] = e[i];
+        }
+    }
+}
 
-// Second launch.  The first cluster settles the part-filled pages: a request that will write into one must be alone with
-// it.  The other CTAs write the rows, but for the entry of such a page.
+// The first of two launches, a CTA per request.
+__global__ void __launch_bounds__(PG_ROW_THREADS) pages_fork_rows_kernel(const ForkArgs A) {
+    grid_wait();
+    grid_launch_next();
+    fork_gather(A, blockIdx.x, threadIdx.x);
+}
+
+// The second.  The first cluster settles the part-filled pages: a request that will write into one must be alone with it.
+// The other CTAs write the rows.  ONE: one launch of one cluster does it all, for tables that are small enough.
+template <bool ONE>
 __global__ void __launch_bounds__(PG_THREADS, 1) pages_fork_kernel(const ForkArgs A) {
+    constexpr int AT_ONCE = PG_THREADS / PG_ROW_THREADS;
     const Book& B = A.book;
     extern __shared__ int32_t smem[];
-    __shared__ int sums[32], exchange;
-    grid_wait();
+    __shared__ int sums[32], free_sums[32], exchange;
     const int tid = threadIdx.x;
-    if (blockIdx.x >= cluster_size()) {
-        constexpr int AT_ONCE = PG_THREADS / PG_ROW_THREADS;
-        const int ctas = gridDim.x - cluster_size(), t = tid % PG_ROW_THREADS;
-        for (int64_t b = (int64_t)(blockIdx.x - cluster_size()) * AT_ONCE + tid / PG_ROW_THREADS; b < B.batch; b += (int64_t)ctas * AT_ONCE) {
-            const int4 m = A.meta[b];
-            const int before = m.x, after = m.y;
-            const bool same = m.w == b;
-            int32_t* to = B.table + b * B.max_pages;
-            const int32_t* from = A.rows + b * B.max_pages;
-            for (int j = (same ? after : 0) + t; j < max(after, before); j += PG_ROW_THREADS)
-                if (j >= after) to[j] = -1;
-                else if (m.z < 0 || j != after - 1) to[j] = from[j];
-        }
+    int32_t *key = smem, *first = smem + A.slots, *holders = smem + 2 * A.slots;
+    if (cluster_rank() == 0)
+        for (int i = tid; i < A.slots; i += PG_THREADS) { key[i] = -1; first[i] = INT32_MAX; holders[i] = 0; }
+    grid_wait();
+    const int ctas = ONE ? (int)gridDim.x : (int)(gridDim.x - cluster_size()), cta_row = (ONE ? (int)blockIdx.x : (int)(blockIdx.x - cluster_size())) * AT_ONCE + tid / PG_ROW_THREADS;
+    if (ONE) {
+        for (int b = cta_row; b < B.batch; b += ctas * AT_ONCE) fork_gather(A, b, tid % PG_ROW_THREADS);
+        cluster_barrier();
+        for (int b = cta_row; b < B.batch; b += ctas * AT_ONCE) fork_write(A, b, tid % PG_ROW_THREADS);
+    } else if (cta_row >= 0) {
+        for (int b = cta_row; b < B.batch; b += ctas * AT_ONCE) fork_write(A, b, tid % PG_ROW_THREADS);
         return;
     }
     const Share share = pg_share(B);
     const int free_here = pg_count_free(B, share);
+    if (tid % 32 == 0) free_sums[tid / 32] = free_here;
+    __syncthreads();
     int cta, free;
-    const int rank_here = block_sum(free_here, sums, cta);
+    const int rank_here = warps_before(free_sums, cta);
     int mine = 0, first_rank = 0;             // copies of this thread's requests (first CTA only), and those before them
     const int per = (B.batch + PG_THREADS - 1) / PG_THREADS, b0 = min(tid * per, B.batch), b1 = min(b0 + per, B.batch);
     int total = 0;
     if (cluster_rank() == 0) {
-        int32_t *key = smem, *first = smem + A.slots, *holders = smem + 2 * A.slots;
-        for (int i = tid; i < A.slots; i += PG_THREADS) { key[i] = -1; first[i] = INT32_MAX; holders[i] = 0; }
-        __syncthreads();
         auto find = [&](int page) {           // its slot; there are twice as many slots as pages
             uint32_t i = (uint32_t)page * 2654435761u >> 7 & (A.slots - 1);
             while (true) {
@@ -299,15 +363,19 @@ __global__ void __launch_bounds__(PG_THREADS, 1) pages_fork_kernel(const ForkArg
         if (tid == 0) *A.count = n;
     }
     if (rank < n && free_here)
-        pg_each(B, share, [&](int p, int v) {
-            if (v != 0 || rank >= n) return;
-            const int b = __ldcg(A.list + rank);
-            const int4 m = A.meta[b];
-            B.table[(int64_t)b * B.max_pages + m.y - 1] = p;
-            B.refs[p] = 1;
-            A.src[rank] = m.z;
-            A.dst[rank] = p;
-            ++rank;
+        pg_each(B, share, [&](int p, int v, bool) {
+            int here;
+            const int r = rank + pg_free_before(v, here);
+            if (v == 0 && r < n) {
+                const int b = __ldcg(A.list + r);
+                const int4 m = A.meta[b];
+                B.table[(int64_t)b * B.max_pages + m.y - 1] = p;
+                B.refs[p] = 1;
+                A.src[r] = m.z;
+                A.dst[r] = p;
+            }
+            rank += here;
+            return rank < n;
         });
     cluster_barrier();                        // nobody leaves while its sum is read
 }
@@ -329,53 +397,78 @@ __global__ void __launch_bounds__(PG_THREADS, 1) pages_compact_kernel(const Comp
     const Book& B = A.book;
     __shared__ int sums[32], exchange;
     grid_wait();
+    grid_launch_next();
     const Share share = pg_share(B);
     const int free_here = pg_count_free(B, share);
+    if (threadIdx.x % 32 == 0) sums[threadIdx.x / 32] = free_here;
+    __syncthreads();
     int cta, free;
-    const int rank_here = block_sum(free_here, sums, cta);
+    const int rank_here = warps_before(sums, cta);
     const int first = pg_rank(rank_here, cta, &exchange, free);
     const int live = B.n_pages - free;
     int rank = first;
-    pg_each(B, share, [&](int p, int v) {
-        if (p == live) A.head[1] = rank;      // the free pages before L are as many as the used ones from L on
-        if (v == 0) {
-            if (p < live) A.dst[rank] = p;
-            ++rank;
-        }
-        if (A.refs_out != B.refs) A.refs_out[p] = v;
-    });
+    if (share.first <= live)
+        pg_each(B, share, [&](int p, int v, bool real) {
+            int here;
+            const int r = rank + pg_free_before(v, here);
+            if (real && p == live) A.head[1] = r;             // the free pages before L are as many as the used ones from L on
+            if (v == 0 && p < live) A.dst[r] = p;
+            rank += here;
+            return p - (int)(threadIdx.x & 31) + 32 <= live;
+        });
     if (cluster_rank() == 0 && threadIdx.x == 0) {
         A.head[0] = live;
         if (live == B.n_pages) A.head[1] = 0;
     }
     cluster_barrier();
     const int moves = __ldcg(A.head + 1);
-    rank = first;
-    pg_each(B, share, [&](int p, int v) {
-        if (p == live) rank = moves;          // (free pages before L may have been filled meanwhile)
-        if (p >= live) {
-            int to = p;
-            if (v != 0) {
-                const int i = p - rank - (live - moves);
-                to = __ldcg(A.dst + i);
-                A.src[i] = p;
-                A.refs_out[to] = v;
-                A.refs_out[p] = 0;
-            }
-            A.to[p] = to;
+    // Free pages before L may have been filled meanwhile: counted are those from L on.
+    rank = share.first > live ? first : moves;
+    constexpr int AT_ONCE = 8;                // groups whose places are fetched together: a store may not pass a load
+    const int lane = threadIdx.x & 31;
+    for (int p0 = max(share.first, live / 32 * 32) + lane; p0 - lane < share.end; p0 += 32 * AT_ONCE) {
+        int v[AT_ONCE], at[AT_ONCE], to[AT_ONCE];
+#pragma unroll
+        for (int i = 0; i < AT_ONCE; ++i) {
+            const int p = p0 + 32 * i;
+            v[i] = p >= live && p < share.end ? B.refs[p] : INT32_MIN;
         }
-        rank += v == 0;
-    });
-    for (int i = moves + cluster_rank() * PG_THREADS + threadIdx.x; i < B.n_pages / 2; i += cluster_size() * PG_THREADS)
-        A.src[i] = A.dst[i] = -1;
+#pragma unroll
+        for (int i = 0; i < AT_ONCE; ++i) {
+            int here;
+            at[i] = p0 + 32 * i - (rank + pg_free_before(v[i], here)) - (live - moves);
+            rank += here;
+        }
+#pragma unroll
+        for (int i = 0; i < AT_ONCE; ++i) to[i] = v[i] != INT32_MIN && v[i] != 0 ? __ldcg(A.dst + at[i]) : p0 + 32 * i;
+#pragma unroll
+        for (int i = 0; i < AT_ONCE; ++i) {
+            const int p = p0 + 32 * i;
+            if (v[i] != INT32_MIN && v[i] != 0) {
+                A.src[at[i]] = p;
+                A.refs_out[to[i]] = v[i];
+                if (A.refs_out == B.refs) A.refs_out[p] = 0;
+            }
+            if (v[i] != INT32_MIN) A.to[p] = to[i];
+        }
+    }
     if (cluster_rank() == 0 && threadIdx.x == 0) *A.count = moves;
 }
 
-// Second launch, a CTA per request: the rows' entries follow their pages.
+// Second launch.  A CTA per request: the rows' entries follow their pages.  All CTAs: what the first leaves of the lists,
+// and of refs that go elsewhere.
 __global__ void __launch_bounds__(PG_ROW_THREADS) pages_compact_rows_kernel(const CompactArgs A) {
+    constexpr int AT_ONCE = 4;
     const Book& B = A.book;
     grid_wait();
-    const int b = blockIdx.x, live = A.head[0];
+    const int b = blockIdx.x, live = A.head[0], moves = A.head[1], stripe = gridDim.x * PG_ROW_THREADS;
+    for (int i = moves + b * PG_ROW_THREADS + threadIdx.x; i < B.n_pages / 2; i += stripe) A.src[i] = A.dst[i] = -1;
+    if (A.refs_out != B.refs)
+        for (int p = b * PG_ROW_THREADS + threadIdx.x; p < B.n_pages; p += stripe) {
+            const int v = B.refs[p];
+            if (p >= live || v != 0) A.refs_out[p] = p >= live ? 0 : v;
+        }
+    if (b >= B.batch) return;
     int held = B.held[b];
     if ((held < 0 || held > B.max_pages) && threadIdx.x == 0) pg_report(B, KVO_DEV_BAD_COUNT);
     held = min(max(held, 0), B.max_pages);
@@ -383,13 +476,19 @@ __global__ void __launch_bounds__(PG_ROW_THREADS) pages_compact_rows_kernel(cons
     int32_t* to = A.table_out + (int64_t)b * B.max_pages;
     const int end = A.table_out == B.table ? held : B.max_pages;
     bool wrong = false;
-    for (int j = threadIdx.x; j < end; j += PG_ROW_THREADS) {
-        int e = from[j];
-        if (j < held) {
-            if (e < 0 || e >= B.n_pages) wrong = true;
-            else if (e >= live) e = A.to[e];
+    for (int j = threadIdx.x; j < end; j += PG_ROW_THREADS * AT_ONCE) {
+        int e[AT_ONCE], t[AT_ONCE];
+#pragma unroll
+        for (int i = 0; i < AT_ONCE; ++i) e[i] = j + i * PG_ROW_THREADS < end ? from[j + i * PG_ROW_THREADS] : 0;
+#pragma unroll
+        for (int i = 0; i < AT_ONCE; ++i) {
+            const bool named = j + i * PG_ROW_THREADS < held, in = e[i] >= 0 && e[i] < B.n_pages;
+            wrong |= named && !in;
+            t[i] = named && in && e[i] >= live ? A.to[e[i]] : e[i];
         }
-        to[j] = e;
+#pragma unroll
+        for (int i = 0; i < AT_ONCE; ++i)
+            if (j + i * PG_ROW_THREADS < end) to[j + i * PG_ROW_THREADS] = t[i];
     }
     if (wrong) pg_report(B, KVO_DEV_BAD_BLOCK_ID);
 }
@@ -557,14 +656,20 @@ extern "C" kvo_status kvo_paged_fork(const kvo_page_book* book, const int32_t* p
     A.rows = (int32_t*)((uint8_t*)A.list + up256(((size_t)book->batch + 1) * 4));
     A.slots = 32;
     while (A.slots < 2 * book->batch) A.slots *= 2;
-    static std::atomic<uint64_t> done{0};
-    cudaError_t e = allow_smem((const void*)pages_fork_kernel, done, 2 * PG_BATCH * 12);
+    static std::atomic<uint64_t> done_one{0}, done_two{0};
+    const int cluster = pages_cluster(book->n_pages), rows = (book->batch + 3) / 4;
+    if ((int64_t)book->batch * book->max_pages <= PG_ONE) {
+        const cudaError_t e = allow_smem((const void*)pages_fork_kernel<true>, done_one, 2 * PG_BATCH * 12);
+        if (e != cudaSuccess) return launched(e);
+        const int ctas = std::max(cluster, rows > 1 ? PG_CLUSTER : 1);
+        return launched(launch_dependent(pages_fork_kernel<true>, dim3(ctas), PG_THREADS, (size_t)A.slots * 12, s, ctas, A));
+    }
+    cudaError_t e = allow_smem((const void*)pages_fork_kernel<false>, done_two, 2 * PG_BATCH * 12);
     if (e != cudaSuccess) return launched(e);
     e = launch_dependent(pages_fork_rows_kernel, dim3(book->batch), PG_ROW_THREADS, 0, s, 0, A);
     if (e != cudaSuccess) return launched(e);
-    const int cluster = pages_cluster(book->n_pages), rows = (book->batch + 3) / 4;
     const int ctas = cluster + (std::min(rows, 128) + cluster - 1) / cluster * cluster;
-    return launched(launch_dependent(pages_fork_kernel, dim3(ctas), PG_THREADS, (size_t)A.slots * 12, s, cluster, A));
+    return launched(launch_dependent(pages_fork_kernel<false>, dim3(ctas), PG_THREADS, (size_t)A.slots * 12, s, cluster, A));
 }
 
 extern "C" kvo_status kvo_paged_compact_workspace(const kvo_page_book* book, size_t* bytes_out) {
@@ -605,8 +710,9 @@ extern "C" kvo_status kvo_paged_compact(const kvo_page_book* book, int32_t* tabl
     cudaStream_t s = (cudaStream_t)stream;
     const int cluster = pages_cluster(book->n_pages);
     cudaError_t e = launch_dependent(pages_compact_kernel, dim3(cluster), PG_THREADS, 0, s, cluster, A);
-    if (e == cudaSuccess && book->batch)
-        e = launch_dependent(pages_compact_rows_kernel, dim3(book->batch), PG_ROW_THREADS, 0, s, 0, A);
+    const int stripes = (int)std::min<int64_t>(304, (book->n_pages + 4ll * PG_ROW_THREADS - 1) / (4 * PG_ROW_THREADS));
+    if (e == cudaSuccess)
+        e = launch_dependent(pages_compact_rows_kernel, dim3(std::max(book->batch, stripes)), PG_ROW_THREADS, 0, s, 0, A);
     return launched(e);
 }
 
