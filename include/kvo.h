@@ -605,6 +605,46 @@ kvo_status kvo_paged_attn_workspace(const kvo_paged_cache* cache, int n_q_heads,
                                     size_t* bytes_out);
 
 /*
+ * kvo_paged_chunk_attn -- GQA attention of several new tokens of each request over
+ * a paged cache that holds them already (kvo_paged_append first): pieces of prompts
+ * behind cached tokens, drafted tokens to be checked, single tokens, all in one call.
+ *   q: bf16 [total_q][n_q_heads][head_dim], heads contiguous, any token stride
+ *   (elements, a multiple of 8 that covers the heads), 16-byte aligned; n_q_heads /
+ *   n_kv_heads <= 16.  cu: device int32 [batch + 1], ascending: request b's new
+ *   tokens are rows cu[b] .. cu[b + 1] - 1 (none may be there).  lens: device int32
+ *   [batch]: the tokens of each request, the new ones among them: the i-th of n new
+ *   tokens is token lens[b] - n + i and sees the tokens up to itself.
+ *   max_new, max_len: the caller's upper bounds of the new tokens of a request and
+ *   of lens (0: none known); they only choose how the work is split, larger
+ *   requests are still served in full.
+ *   o: bf16 [total_q][n_q_heads][head_dim], contiguous; lse (optional): fp32
+ *   [total_q][n_q_heads], natural log; both and the workspace apart from each other
+ *   and from all that the call reads.  Softmax scale 1/sqrt(head_dim), fp32
+ *   accumulation, weights (next to e4m3 pages times v_scale) rounded to bf16, o
+ *   rounded once to bf16.  With e4m3 pages q is taken as the sum of two e4m3 values
+ *   times a power of two: exact where a value is at least 2^-9 of its row's largest,
+ *   to 2^-17 of that one else.  A row that sees no token gets o = 0, lse = -inf; rows
+ *   outside every request keep their bytes.  What lies in a page behind the last
+ *   token is never used, NaN included; among the new tokens of a request a NaN or an
+ *   infinity in v may reach tokens before it in the same 128 keys.  Two calls give
+ *   the same bits.
+ *   workspace: kvo_paged_chunk_attn_workspace bytes, 256-byte aligned, contents
+ *   undefined before and after; one call at a time may use it (two captured graphs
+ *   that may overlap need one each).
+ *   Status bits: KVO_DEV_BAD_BLOCK_ID (a page id out of range: its tokens add
+ *   nothing), KVO_DEV_BAD_COUNT (offsets descending or outside 0..total_q, or a
+ *   request that begins before the end of an earlier served one: it is not written;
+ *   a length out of range: clamped), KVO_DEV_TIMEOUT (a bounded wait of 2 s gave up:
+ *   outputs are invalid).  Errors: KVO_ERR_INVALID, KVO_ERR_CUDA.
+ */
+kvo_status kvo_paged_chunk_attn(const kvo_paged_cache* cache, const void* q, int64_t q_token_stride, int64_t total_q,
+                                int n_q_heads, const int32_t* cu, const int32_t* lens, int64_t max_new, int64_t max_len,
+                                void* o, float* lse, void* workspace, size_t workspace_bytes, int32_t* status,
+                                kvo_stream_t stream);
+kvo_status kvo_paged_chunk_attn_workspace(const kvo_paged_cache* cache, int n_q_heads, int64_t total_q, int64_t max_new,
+                                          int64_t max_len, size_t* bytes_out);
+
+/*
  * kvo_prompt_attn -- GQA attention over packed prompts.
  *   q: bf16 [total_q][n_q_heads][head_dim], k, v: bf16 [total_k][n_kv_heads]
  *   [head_dim]; heads contiguous, any token stride (elements, a multiple of 8

@@ -518,6 +518,33 @@ PyObject* py_paged_copy(PyObject*, PyObject* const* a, Py_ssize_t n) {
     });
 }
 
+// paged_chunk_attn(q, k_pages, v_pages, table, lens, cu, k_scale, v_scale, max_new, max_len, o, lse, workspace, status, stream)
+PyObject* py_paged_chunk_attn(PyObject*, PyObject* const* a, Py_ssize_t n) {
+    return guarded(n, 15, [&]() -> PyObject* {
+        const at::Device dev = tensor(a[1], "k_pages").device();
+        const kvo_paged_cache c = paged(a[1], a[2], a[6], a[7], a[3], dev);
+        const Rows q = rows(a[0], "q", dev);
+        const int64_t T = q.t.size(0), hq = q.t.size(1), b = c.batch;
+        const std::vector<int64_t> shape{T, hq, c.head_dim}, lshape{T, hq};
+        if (q.t.sizes() != at::IntArrayRef(shape)) refuse("q must have shape " + shape_text(shape) + ", got " + shape_text(q.t.sizes()));
+        const int32_t* lens = (const int32_t*)need(a[4], "lens", dev, at::kInt, {{b}}).data_ptr();
+        const int32_t* cu = (const int32_t*)need(a[5], "cu", dev, at::kInt, {{b + 1}}).data_ptr();
+        const int64_t max_new = integer(a[8]), max_len = integer(a[9]);
+        const Stream stream(a[14], dev);
+        at::Tensor o = a[10] == Py_None ? empty(shape, at::kBFloat16, dev) : need(a[10], "o", dev, at::kBFloat16, at::IntArrayRef(shape));
+        at::Tensor lse = a[11] == Py_None ? empty(lshape, at::kFloat, dev) : need(a[11], "lse", dev, at::kFloat, at::IntArrayRef(lshape));
+        int32_t* status = status_of(a[13], dev);
+        size_t bytes = 0;
+        sized(kvo_paged_chunk_attn_workspace(&c, int32_size(hq, "n_q_heads"), T, max_new, max_len, &bytes));
+        const at::Tensor ws = scratch(a[12], dev, bytes);
+        launch(dev, [&] {
+            return kvo_paged_chunk_attn(&c, q.t.data_ptr(), q.tok, T, (int)hq, cu, lens, max_new, max_len, o.data_ptr(), (float*)lse.data_ptr(),
+                                        ws.data_ptr(), ws.numel(), status, stream.handle);
+        });
+        return pair(o, lse);
+    });
+}
+
 // raise_with(cls): the exception class, called as cls(status, message)
 PyObject* py_raise_with(PyObject*, PyObject* cls) {
     Py_XINCREF(cls);
@@ -530,6 +557,7 @@ PyMethodDef methods[] = {{"rope", (PyCFunction)(void*)py_rope, METH_FASTCALL, nu
                          {"paged_append", (PyCFunction)(void*)py_paged_append, METH_FASTCALL, nullptr},
                          {"paged_attn", (PyCFunction)(void*)py_paged_attn, METH_FASTCALL, nullptr},
                          {"prompt_attn", (PyCFunction)(void*)py_prompt_attn, METH_FASTCALL, nullptr},
+                         {"paged_chunk_attn", (PyCFunction)(void*)py_paged_chunk_attn, METH_FASTCALL, nullptr},
                          {"paged_reserve", (PyCFunction)(void*)py_paged_reserve, METH_FASTCALL, nullptr},
                          {"paged_fork", (PyCFunction)(void*)py_paged_fork, METH_FASTCALL, nullptr},
                          {"paged_compact", (PyCFunction)(void*)py_paged_compact, METH_FASTCALL, nullptr},

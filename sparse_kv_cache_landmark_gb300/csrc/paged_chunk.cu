@@ -1,0 +1,1184 @@
+// kvo_paged_chunk_attn: attention of several new tokens of each request over a paged cache (bf16, or e4m3 with a scale per
+// page and KV head) that holds them already.
+//
+//   o_i = sum_t softmax_t(q_i . k_t / sqrt(d)) v_t,  t <= len - n + i  for the i-th of n new tokens of len.
+//
+// Work.  An item is a block of 256 query rows of one KV head: two tiles of 128 rows, each floor(128 / r) tokens x the r
+// query heads of the group (one tile where the tokens fit it), over the keys that they see, 128 to a tile.  The items of
+// all requests, laid end to end by an estimate of their cost, are cut into equal ranges, one per CTA and SM; the lengths
+// are device data, so each CTA finds its range by a prefix sum over the requests.  An item that a border cuts leaves its
+// parts (m, l, o in fp32) in the workspace and a second kernel joins them in the order of the keys: results do not depend
+// on timing.
+//
+// One CTA to an SM, its warps
+//   9        walks the items: their descriptors, K and V tiles through rings (TMA, a box per page), the pages' scales,
+//   8, 10    one thread each issues the tcgen05.mma of tile 0 and 1: S_t = Q_t K^T and O_t += P_t V,
+//   0-3, 4-7 the softmax of tile 0 and 1, one thread per row: S from tensor memory, online maximum and sum in fp32, P (bf16)
+//            back over S,
+//   12-15    (e4m3) q to its 8-bit form, V to bf16.
+// An item's first scores are issued behind the last value product of the one before, and its first loads before that.
+//
+// e4m3.  K goes to the tensor cores as it is: a row of q, times a power of two that brings its largest value to 2^7..2^8, is
+// the sum of two e4m3 values, exactly for what is at least 2^-9 of that largest and to 2^-17 of it for all below (a bf16
+// value has 8 bits, an e4m3 value 4), and two 8-bit products take the time of one of bf16.  V is widened to bf16, exactly,
+// on its way through shared memory.  A page's k_scale multiplies its scores, its v_scale its weights before they are
+// rounded to bf16; bf16 has fp32's exponents, so scales of any size do.
+#include <stdio.h>
+
+#include <algorithm>
+
+#include "f32x2.cuh"
+#include "kvo_internal.cuh"
+#include "launch.cuh"
+#include "paged.cuh"
+#include "tcgen05.cuh"
+#include "tensor_map.cuh"
+
+namespace kvo {
+
+constexpr int CH_ROWS = 128;               // query rows of a tile
+constexpr int CH_KEYS = 128;               // keys of a tile
+constexpr int CH_BLOCK = CH_ROWS * 128;    // bytes of 128 rows of 128
+constexpr float CH_RAISE = 8.f;            // log2: how far a score may pass the running maximum
+constexpr int CH_CTAS = 152;               // ranges at most: one CTA to an SM
+constexpr int CH_EVENTS = 16;              // barriers that a tile's products complete in turn
+constexpr int CH_ITEMS = 4;                // descriptors
+constexpr int CH_NAN = -128;
+constexpr int CH_SCALES = 8;               // tiles of keys whose scales are held
+
+template <int D, bool FP8>
+struct ChShape;
+template <int D>
+struct ChShape<D, false> {
+    static constexpr int THREADS = 384;
+    static constexpr int REGS_SOFTMAX = 208, REGS_OTHER = 88;
+    static constexpr int Q = CH_ROWS * D * 2;                   // bytes of a tile of q
+    static constexpr int TILE = CH_KEYS * D * 2;                // of K or V
+    static constexpr int STAGES = D == 128 ? 4 : 10;            // K and V in turn
+    static constexpr int WIDE_BYTES = 0;
+    static constexpr int TILES = 2 * Q + STAGES * TILE;
+};
+template <int D>
+struct ChShape<D, true> {
+    static constexpr int THREADS = 512;
+    static constexpr int REGS_SOFTMAX = 184, REGS_OTHER = 72;
+    static constexpr int Q = 2 * CH_ROWS * D;                   // the two pieces
+    static constexpr int TILE = CH_KEYS * D;                    // of K or V as they are
+    static constexpr int WIDE_BYTES = CH_KEYS * D * 2;          // of V in bf16
+    static constexpr int STAGES = 6;                            // K and V in turn
+    static constexpr int WIDES = 2;
+    static constexpr int TILES = 2 * Q + STAGES * TILE + WIDES * WIDE_BYTES;
+};
+
+struct ChunkArgs {
+    const uint16_t* q;
+    int64_t q_stride;
+    const float* k_scale;
+    const float* v_scale;
+    const int32_t* table;
+    const int32_t* lens;
+    const int32_t* cu;
+    uint16_t* o;
+    float* lse;                    // or NULL
+    int32_t* status;
+    struct ChunkCut* cut;          // [CTAs]
+    float* part_o;                 // [CTAs][2][tiles][D / 4][128] of 4 values
+    float2* part_ml;               // [CTAs][2][tiles][128]
+    int64_t total;
+    int batch, hq, hkv, r, tq, page, shift, n_pages, max_pages, tiles;
+    int w1, w2, base;              // cost of a key for one tile of rows and for two, and of an item in itself
+    int64_t least;                 // cost of a range, unless there are more than CTAs
+    float scale_log2;
+    int skip;                      // the load that every CTA announces without copying it (tests; -1: none)
+    long long wait_ns;
+};
+
+// What a CTA tells the join: the item that begins in its range and ends in a later one.
+struct ChunkCut {
+    int64_t row;                   // the request's first row of q
+    int32_t last;                  // the range in which it ends; -1: no such item
+    int32_t more;                  // whether this CTA's range begins with a part of an item that began before
+    int32_t tok0, n, g, pad;       // first token of the block, the request's tokens, KV head
+};
+
+struct ChunkItem {
+    int64_t row;
+    int32_t n[2];                  // tiles of keys of each tile of rows; n[0] = -1: the end
+    int32_t first;                 // tile of keys
+    int32_t b, g, tok0, nq, len;
+    int32_t part;                  // -1: the whole item; else its place in the workspace
+};
+
+struct ChShared {
+    uint64_t q_full[2], kv_full[10], raw_free[3], wide_full[2], event[2][CH_EVENTS], p_full[2][2], turn[2], drain[2], v_tail, item_full[CH_ITEMS],
+        item_free[CH_ITEMS], sc_full[CH_SCALES];
+    ChunkItem item[CH_ITEMS];
+    float k_scale[CH_SCALES][8], v_scale[CH_SCALES][8];
+    uint32_t bad[CH_SCALES];       // groups of 16 keys in pages that do not exist
+    int8_t q_exp[2][2][CH_ROWS];   // q's pieces are its values times 2^this; CH_NAN: not finite
+    uint32_t tmem;
+    int abort;
+    int issued, tail_open, tail_phase;
+    // the plan
+    int64_t sum[16], at[2];
+    int32_t top[16], found[2], high[2];
+};
+
+__device__ __forceinline__ bool ch_wait_long(int* abort, int32_t* status, uint32_t bar, uint32_t parity, long long limit) {
+    const uint64_t t0 = global_ns();
+    while (!mbar_try_wait(bar, parity)) {
+        if (*(volatile int*)abort) return false;
+        if ((long long)(global_ns() - t0) > limit) {
+            *(volatile int*)abort = 1;
+            if (status) atomicOr(status, KVO_DEV_TIMEOUT);
+            return false;
+        }
+    }
+    return true;
+}
+__device__ __forceinline__ bool ch_wait(ChShared& sh, const ChunkArgs& A, uint64_t& bar, uint32_t parity) {
+    const uint32_t b = smem_u32(&bar);
+    if (mbar_try_wait(b, parity & 1)) return true;
+    return ch_wait_long(&sh.abort, A.status, b, parity & 1, A.wait_ns);
+}
+// The e-th completion of tile t's products: its scores of each tile of keys, then its last value product, item after item.
+__device__ __forceinline__ bool ch_event(ChShared& sh, const ChunkArgs& A, int t, uint32_t e) {
+    return ch_wait(sh, A, sh.event[t][e % CH_EVENTS], e / CH_EVENTS);
+}
+
+// ------------------------------------------------------------------ the plan
+struct ChRequest {
+    int a, n, len;                 // first row, new tokens, tokens in all
+    bool served;
+};
+// Cost of the first i blocks of a request, all but its last, and of one of them; for all KV heads.
+__device__ __forceinline__ int64_t ch_before(const ChunkArgs& A, const ChRequest& r, int64_t i) {
+    const int64_t past = max(r.len - r.n, 0);
+    return A.hkv * (i * (A.base + A.w2 * past) + (int64_t)A.w2 * A.tq * i * (i + 1));
+}
+__device__ __forceinline__ int ch_blocks(const ChunkArgs& A, const ChRequest& r) { return (r.n + 2 * A.tq - 1) / (2 * A.tq); }
+// Cost of one item of block i.
+__device__ __forceinline__ int64_t ch_cost(const ChunkArgs& A, const ChRequest& r, int i) {
+    const int64_t past = max(r.len - r.n, 0), end = min((int64_t)(i + 1) * 2 * A.tq, (int64_t)r.n);
+    return A.base + (end - (int64_t)i * 2 * A.tq > A.tq ? A.w2 : A.w1) * (past + end);
+}
+__device__ __forceinline__ int64_t ch_total(const ChunkArgs& A, const ChRequest& r) {
+    if (!r.served || r.n == 0) return 0;
+    const int nb = ch_blocks(A, r);
+    return ch_before(A, r, nb - 1) + A.hkv * ch_cost(A, r, nb - 1);
+}
+// Tiles of keys that tile t of rows of block i sees.
+__device__ __forceinline__ int ch_tiles(const ChunkArgs& A, const ChRequest& r, int i, int t) {
+    const int first = (i * 2 + t) * A.tq, have = min(r.n - first, A.tq);
+    if (have <= 0) return 0;
+    const int64_t see = (int64_t)first + have + r.len - r.n;
+    return (int)((max(see, (int64_t)0) + CH_KEYS - 1) / CH_KEYS);
+}
+
+struct ChWalk {                    // a place in the list of items
+    ChRequest r;
+    int b, i, g;
+    int64_t start, cost;           // of the item
+};
+// The item of request b (which begins at `at`) that holds position x.
+__device__ __forceinline__ ChWalk ch_locate(const ChunkArgs& A, int b, const ChRequest& r, int64_t at, int64_t x) {
+    int lo = 0, n = ch_blocks(A, r);
+    while (n > 1) {
+        const int half = n / 2;
+        if (at + ch_before(A, r, lo + half) <= x) { lo += half; n -= half; }
+        else n = half;
+    }
+    ChWalk w;
+    w.r = r;
+    w.b = b;
+    w.i = lo;
+    w.cost = ch_cost(A, r, lo);
+    at += ch_before(A, r, lo);
+    w.g = (int)((x - at) / w.cost);
+    w.start = at + w.g * w.cost;
+    return w;
+}
+// Which of an item's n tiles of keys lie in [lo, hi).
+__device__ __forceinline__ void ch_part(const ChWalk& w, int64_t lo, int64_t hi, int n, int& first, int& last) {
+    first = w.start >= lo ? 0 : (int)((lo - w.start) * n / w.cost);
+    last = w.start + w.cost <= hi ? n : (int)((hi - w.start) * n / w.cost);
+}
+__device__ __forceinline__ ChRequest ch_request(const ChunkArgs& A, int b) {
+    const int a = A.cu[b], e = A.cu[b + 1], len = A.lens[b];
+    return {a, e - a, (int)min((int64_t)max(len, 0), (int64_t)A.max_pages * A.page), offsets_ascend(a, e, A.total)};
+}
+__device__ __forceinline__ int64_t ch_bound(int64_t total, int ranges, int c) { return total / ranges * c + total % ranges * c / ranges; }
+
+struct ChPlan {
+    int64_t all;                   // the cost of everything
+    int64_t lo, hi;                // this CTA's range
+    int ranges;
+};
+// All threads.  Finds this CTA's range and the requests that hold its first and last position; false where it has none.
+template <int THREADS>
+__device__ __forceinline__ bool ch_plan(ChShared& sh, const ChunkArgs& A, ChPlan& plan) {
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    constexpr int WARPS = THREADS / 32;
+    int64_t total = 0;
+    int top = 0;                   // the end of the served requests so far
+    ChRequest mine;
+    int64_t before = 0, cost = 0;
+    int top_before = 0;
+    // Adds the next THREADS requests: this thread's cost and what lies before it.
+    auto add = [&](int base, bool report) {
+        const int b = base + tid;
+        mine = {0, 0, 0, false};
+        if (b < A.batch) {
+            mine = ch_request(A, b);
+            const int len = A.lens[b];
+            if (report && A.status && (!mine.served || len < 0 || len > (int64_t)A.max_pages * A.page)) atomicOr(A.status, KVO_DEV_BAD_COUNT);
+        }
+        int m = mine.served ? mine.a + mine.n : 0;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int x = __shfl_up_sync(0xffffffffu, m, o);
+            if (lane >= o) m = max(m, x);
+        }
+        int m_before = __shfl_up_sync(0xffffffffu, m, 1);
+        if (lane == 0) m_before = 0;
+        __syncthreads();
+        if (lane == 31) sh.top[warp] = m;
+        __syncthreads();
+        top_before = top;
+        for (int w = 0; w < WARPS; ++w) {
+            if (w < warp) top_before = max(top_before, sh.top[w]);
+            top = max(top, sh.top[w]);
+        }
+        top_before = max(top_before, m_before);
+        mine.served = mine.served && mine.a >= top_before;
+        cost = ch_total(A, mine);
+        int64_t s = cost;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int64_t x = __shfl_up_sync(0xffffffffu, s, o);
+            if (lane >= o) s += x;
+        }
+        if (lane == 31) sh.sum[warp] = s;
+        __syncthreads();
+        before = total + s - cost;
+        for (int w = 0; w < WARPS; ++w) {
+            if (w < warp) before += sh.sum[w];
+            total += sh.sum[w];
+        }
+    };
+    for (int base = 0; base < A.batch; base += THREADS) add(base, blockIdx.x == 0);
+    plan.all = total;
+    plan.ranges = (int)min((int64_t)gridDim.x, max(total / A.least, (int64_t)1));
+    const int c = blockIdx.x;
+    if (c >= plan.ranges || total == 0) return false;
+    plan.lo = ch_bound(total, plan.ranges, c);
+    plan.hi = ch_bound(total, plan.ranges, c + 1);
+    if (plan.lo >= plan.hi) return false;
+    auto look = [&](int base) {
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+            const int64_t x = k ? plan.hi - 1 : plan.lo;
+            if (before <= x && x < before + cost) {
+                sh.found[k] = base + tid;
+                sh.at[k] = before;
+                sh.high[k] = top_before;
+            }
+        }
+    };
+    if (A.batch <= THREADS) {
+        look(0);
+    } else {
+        total = 0;
+        top = 0;
+        for (int base = 0; base < A.batch; base += THREADS) {
+            add(base, false);
+            look(base);
+        }
+    }
+    return true;                   // (what was found is there after a barrier)
+}
+// What the join has to know of this CTA's range, which begins with item `head`.
+__device__ __forceinline__ ChunkCut ch_cut(const ChShared& sh, const ChunkArgs& A, const ChPlan& P, const ChWalk& head) {
+    ChunkCut cut;
+    const ChWalk tail = ch_locate(A, sh.found[1], ch_request(A, sh.found[1]), sh.at[1], P.hi - 1);
+    int first, last, n = max(ch_tiles(A, head.r, head.i, 0), ch_tiles(A, head.r, head.i, 1));
+    ch_part(head, P.lo, P.hi, n, first, last);
+    cut.more = first > 0 && last > first;
+    n = max(ch_tiles(A, tail.r, tail.i, 0), ch_tiles(A, tail.r, tail.i, 1));
+    ch_part(tail, P.lo, P.hi, n, first, last);
+    cut.last = -1;
+    if (first == 0 && last > 0 && last < n) {
+        const int64_t end = tail.start + tail.cost - 1;       // and the range that holds it
+        int k = (int)min(end / max(P.all / P.ranges, (int64_t)1), (int64_t)P.ranges - 1);
+        while (k + 1 < P.ranges && ch_bound(P.all, P.ranges, k + 1) <= end) ++k;
+        while (k > 0 && ch_bound(P.all, P.ranges, k) > end) --k;
+        cut.last = k;
+    }
+    cut.row = tail.r.a;
+    cut.tok0 = tail.i * 2 * A.tq;
+    cut.n = tail.r.n;
+    cut.g = tail.g;
+    cut.pad = 0;
+    return cut;
+}
+
+// ------------------------------------------------------------------ softmax
+// The softmax of one tile of an item: a thread owns a row; it sees its request's keys [0, limit).  False: a wait gave up.
+template <int D, bool FP8>
+__device__ __forceinline__ bool ch_softmax(ChShared& sh, const ChunkArgs& A, const ChunkItem& I, int t, uint32_t& events, uint32_t& keys,
+                                           int turn) {
+    const uint32_t lanes = (uint32_t)(threadIdx.x & 96) << 16;          // this warp's quarter of the lanes
+    const uint32_t S = sh.tmem + 128 * t + lanes, O = sh.tmem + 256 + D * t + lanes;
+    const int row = threadIdx.x & 127, tl = row / A.r, head = row - tl * A.r;
+    const int tok = I.tok0 + t * A.tq + tl;
+    const bool real = tl < A.tq && tok < I.nq;
+    const int n_tiles = I.n[t];
+    int limit = real ? (int)min(max((int64_t)tok + 1 + (I.len - I.nq), (int64_t)0), (int64_t)I.len) - I.first * CH_KEYS : 0;
+    float m = -INFINITY, l = 0.f;                                       // log2 units; l in units of 2^m
+    for (int j = 0; j < n_tiles; ++j) {
+        bool ok = ch_event(sh, A, t, events++);
+        const uint32_t slot = (keys + j) % CH_SCALES;
+        ok = ok && ch_wait(sh, A, sh.sc_full[slot], (keys + j) / CH_SCALES);
+        if (!__all_sync(0xffffffffu, ok)) return false;
+        tc_fence_after();
+        uint32_t s[CH_KEYS];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) tmem_ld32(S + 32 * i, s + 32 * i);
+        const uint32_t bad = sh.bad[slot];
+        tmem_wait_ld();
+        const int rem = limit - j * CH_KEYS;
+        if (rem < CH_KEYS) {
+#pragma unroll
+            for (int i = 0; i < CH_KEYS; ++i)
+                if (i >= rem) s[i] = 0xFF800000u;                       // -inf
+        }
+        if (bad) {
+#pragma unroll
+            for (int i = 0; i < CH_KEYS; ++i)
+                if (bad >> (i / 16) & 1) s[i] = 0xFF800000u;
+        }
+        float top;
+        float c[FP8 ? 8 : 1];
+        if constexpr (FP8) {
+            const int e = sh.q_exp[turn][t][row];
+            const float q_scale = e == CH_NAN ? __uint_as_float(0x7FC00000u) : __uint_as_float((uint32_t)(127 - e) << 23) * A.scale_log2;
+            float run[8];
+#pragma unroll
+            for (int g = 0; g < 8; ++g) {
+                c[g] = sh.k_scale[slot][g] * q_scale;
+                c[g] = c[g] < 1.2e-38f ? 1.2e-38f : c[g];               // a masked score times zero would be NaN
+                float x = max3(__uint_as_float(s[16 * g]), __uint_as_float(s[16 * g + 1]), __uint_as_float(s[16 * g + 2]));
+                float y = __uint_as_float(s[16 * g + 3]);
+#pragma unroll
+                for (int i = 4; i < 16; i += 4) {
+                    x = max3(x, __uint_as_float(s[16 * g + i]), __uint_as_float(s[16 * g + i + 1]));
+                    y = max3(y, __uint_as_float(s[16 * g + i + 2]), __uint_as_float(s[16 * g + i + 3]));
+                }
+                run[g] = fmaxf(x, y) * c[g];
+            }
+            top = fmaxf(max3(run[0], run[1], run[2]), max3(run[3], run[4], max3(run[5], run[6], run[7])));
+        } else {
+            c[0] = A.scale_log2;
+            float mx[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) mx[e] = __uint_as_float(s[e]);
+#pragma unroll
+            for (int i = 4; i + 8 <= CH_KEYS; i += 8)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) mx[e] = max3(mx[e], __uint_as_float(s[i + e]), __uint_as_float(s[i + 4 + e]));
+#pragma unroll
+            for (int e = 0; e < 4; ++e) mx[e] = fmaxf(mx[e], __uint_as_float(s[CH_KEYS - 4 + e]));
+            top = fmaxf(max3(mx[0], mx[1], mx[2]), mx[3]) * A.scale_log2;
+        }
+        if (__any_sync(0xffffffffu, top > m + CH_RAISE)) {
+            const float to = fmaxf(m, top);
+            const float f = m == -INFINITY ? 0.f : ex2(m - to);
+            m = to;
+            l *= f;
+            if (j > 0) {           // S(j) complete: so is O += P(j - 1) V, which was issued before it
+#pragma unroll 1
+                for (int x = 0; x < D; x += 32) {
+                    uint32_t o[32];
+                    tmem_ld32(O + x, o);
+                    tmem_wait_ld();
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
+                    tmem_st32(O + x, o);
+                }
+            }
+        }
+        const float b = m == -INFINITY ? 0.f : -m;
+        const uint64_t b2 = pack2(b, b);
+        uint64_t sum[2] = {0ull, 0ull};
+#pragma unroll
+        for (int h = 0; h < 4; ++h) {
+            uint32_t p[16];
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+                const float cc = c[FP8 ? 2 * h + i / 8 : 0];
+                float x, y;
+                unpack2(fma2(pack2(__uint_as_float(s[32 * h + 2 * i]), __uint_as_float(s[32 * h + 2 * i + 1])), pack2(cc, cc), b2), x, y);
+                x = ex2(x);
+                y = ex2(y);
+                uint64_t w = pack2(x, y);
+                sum[i & 1] = add2(sum[i & 1], w);
+                if constexpr (FP8) {
+                    const float vs = sh.v_scale[slot][2 * h + i / 8];
+                    unpack2(mul2(w, pack2(vs, vs)), x, y);
+                }
+                const __nv_bfloat162 v = __floats2bfloat162_rn(x, y);
+                p[i] = *reinterpret_cast<const uint32_t*>(&v);
+            }
+            tmem_st16(S + 16 * h, p);
+            if (h & 1) {           // half of the weights are there: the value product may begin on them
+                tmem_wait_st();
+                tc_fence_before();
+                mbar_arrive(smem_u32(&sh.p_full[t][h >> 1]));
+            }
+        }
+        float s0, s1;
+        unpack2(add2(sum[0], sum[1]), s0, s1);
+        l += s0 + s1;
+    }
+    keys += max(I.n[0], I.n[1]);
+    if (n_tiles > 0) {
+        const bool ok = ch_event(sh, A, t, events++);
+        if (!__all_sync(0xffffffffu, ok)) return false;
+        tc_fence_after();
+    }
+    if (I.part >= 0) {             // a part of the item, for the join
+        const int64_t at = (int64_t)I.part * A.tiles + t;
+        float4* to = reinterpret_cast<float4*>(A.part_o) + at * (D / 4) * CH_ROWS + row;
+        if (n_tiles > 0) {
+#pragma unroll 1
+            for (int x = 0; x < D; x += 32) {
+                uint32_t o[32];
+                tmem_ld32(O + x, o);
+                tmem_wait_ld();
+#pragma unroll
+                for (int i = 0; i < 32; i += 4)
+                    if (real)
+                        to[(x + i) / 4 * CH_ROWS] = make_float4(__uint_as_float(o[i]), __uint_as_float(o[i + 1]), __uint_as_float(o[i + 2]),
+                                                               __uint_as_float(o[i + 3]));
+            }
+        }
+        if (real) A.part_ml[at * CH_ROWS + row] = make_float2(m, l);
+        return true;
+    }
+    const float inv = l != 0.f ? 1.f / l : 0.f;
+    const int64_t out = (I.row + tok) * A.hq + I.g * A.r + head;
+    uint4* to = reinterpret_cast<uint4*>(A.o + out * D);
+#pragma unroll 1
+    for (int x = 0; x < D; x += 32) {
+        uint32_t o[32];
+        if (n_tiles > 0) {
+            tmem_ld32(O + x, o);
+            tmem_wait_ld();
+        }
+#pragma unroll
+        for (int i = 0; i < 32; i += 8) {
+            uint32_t w[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                // a row that saw nothing is zero, whatever its lane of tensor memory holds
+                const float a = l != 0.f ? __uint_as_float(o[i + 2 * e]) * inv : 0.f;
+                const float d = l != 0.f ? __uint_as_float(o[i + 2 * e + 1]) * inv : 0.f;
+                const __nv_bfloat162 v = __floats2bfloat162_rn(a, d);
+                w[e] = *reinterpret_cast<const uint32_t*>(&v);
+            }
+            if (real) to[(x + i) / 8] = make_uint4(w[0], w[1], w[2], w[3]);
+        }
+    }
+    if (real && A.lse) A.lse[out] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
+    return true;
+}
+
+// ------------------------------------------------------------------ q and V of 8-bit pages
+// Row `row` of tile t of an item's q as the sum of two e4m3 pieces; times 2^*exponent.
+template <int D>
+__device__ __forceinline__ void ch_split_q(const ChunkArgs& A, const ChunkItem& I, int t, int row, uint8_t* to, int8_t* exponent) {
+    const int tl = row / A.r, head = row - tl * A.r, tok = I.tok0 + t * A.tq + tl;
+    const bool real = tl < A.tq && tok < I.nq;
+    const uint4* q = reinterpret_cast<const uint4*>(A.q + (I.row + tok) * A.q_stride + (int64_t)(I.g * A.r + head) * D);
+    uint32_t top2 = 0;
+    if (real)
+#pragma unroll 8
+        for (int i = 0; i < D / 8; ++i) {
+            const uint4 v = __ldg(q + i);
+            top2 = __vmaxu2(top2, __vmaxu2(__vmaxu2(v.x & 0x7FFF7FFFu, v.y & 0x7FFF7FFFu), __vmaxu2(v.z & 0x7FFF7FFFu, v.w & 0x7FFF7FFFu)));
+        }
+    const uint32_t top = max(top2 & 0xFFFFu, top2 >> 16);     // the largest magnitude's bits
+    const bool finite = top < 0x7F80u;
+    const int e = min(7 - ((int)(top >> 7) - 127), 120);      // 2^7 <= largest * 2^e < 2^8
+    const float up = finite ? __uint_as_float((uint32_t)(e + 127) << 23) : 0.f;
+    *exponent = (int8_t)(finite ? e : CH_NAN);
+#pragma unroll 2
+    for (int c = 0; c < D / 16; ++c) {
+        uint32_t a[4], b[4];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            uint4 v = make_uint4(0, 0, 0, 0);
+            if (real && finite) v = __ldg(q + 2 * c + h);
+            const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+            uint16_t hi[4], lo[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const float x = __uint_as_float(w[i] << 16) * up, y = __uint_as_float(w[i] & 0xFFFF0000u) * up;
+                hi[i] = f32x2_to_e4m3x2(x, y);
+                const uint32_t f = e4m3x2_to_f16x2(hi[i]);
+                const float2 got = __half22float2(*reinterpret_cast<const __half2*>(&f));
+                lo[i] = f32x2_to_e4m3x2(x - got.x, y - got.y);
+            }
+            a[2 * h] = hi[0] | (uint32_t)hi[1] << 16;
+            a[2 * h + 1] = hi[2] | (uint32_t)hi[3] << 16;
+            b[2 * h] = lo[0] | (uint32_t)lo[1] << 16;
+            b[2 * h + 1] = lo[2] | (uint32_t)lo[3] << 16;
+        }
+        const int at = row * D + (D == 128 ? c ^ (row & 7) : c ^ (row >> 1 & 3)) * 16;
+        *reinterpret_cast<uint4*>(to + at) = make_uint4(a[0], a[1], a[2], a[3]);
+        *reinterpret_cast<uint4*>(to + CH_ROWS * D + at) = make_uint4(b[0], b[1], b[2], b[3]);
+    }
+}
+// A tile of V from its codes to bf16, by 128 threads; rows from `have` on become zero, as a weight of zero does not silence
+// the NaN that may lie there.
+template <int D>
+__device__ __forceinline__ void ch_widen_v(const uint8_t* from, uint8_t* to, int have) {
+    constexpr int CH = D / 16;
+#pragma unroll 4
+    for (int k = 0; k < CH; ++k) {
+        const int idx = k * 128 + (threadIdx.x & 127), row = idx / CH, c = idx % CH;
+        uint4 v = *reinterpret_cast<const uint4*>(from + row * D + (D == 128 ? c ^ (row & 7) : c ^ (row >> 1 & 3)) * 16);
+        if (row >= have) v = make_uint4(0, 0, 0, 0);
+        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+        uint32_t o[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const uint32_t f = e4m3x2_to_f16x2((uint16_t)(w[i / 2] >> (i & 1) * 16));
+            const float2 x = __half22float2(*reinterpret_cast<const __half2*>(&f));
+            const __nv_bfloat162 b = __floats2bfloat162_rn(x.x, x.y);
+            o[i] = *reinterpret_cast<const uint32_t*>(&b);
+        }
+        uint8_t* at = to + (c / 4) * CH_BLOCK + row * 128;
+        const int first = (c % 4) * 2;
+        *reinterpret_cast<uint4*>(at + ((first ^ (row & 7)) * 16)) = make_uint4(o[0], o[1], o[2], o[3]);
+        *reinterpret_cast<uint4*>(at + (((first + 1) ^ (row & 7)) * 16)) = make_uint4(o[4], o[5], o[6], o[7]);
+    }
+}
+
+// ------------------------------------------------------------------ the kernel
+template <int D, bool FP8>
+__global__ void __launch_bounds__(ChShape<D, FP8>::THREADS, 1)
+paged_chunk_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_k,
+                   const __grid_constant__ CUtensorMap map_v, const __grid_constant__ ChunkArgs A) {
+    using P = ChShape<D, FP8>;
+    extern __shared__ __align__(1024) uint8_t smem[];           // the tiles, then ChShared
+    ChShared& sh = *reinterpret_cast<ChShared*>(smem + P::TILES);
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const uint32_t base = smem_u32(smem), ring = base + 2 * P::Q;
+    constexpr uint32_t WIDE0 = 2 * P::Q + P::STAGES * P::TILE;
+    if (tid == 0) {
+        if (!FP8) tensor_map_prefetch(&map_q);
+        tensor_map_prefetch(&map_k);
+        tensor_map_prefetch(&map_v);
+        for (int i = 0; i < P::STAGES; ++i) mbar_init(smem_u32(&sh.kv_full[i]), 1);
+        for (int i = 0; i < 3; ++i) mbar_init(smem_u32(&sh.raw_free[i]), 4);
+        for (int i = 0; i < 2; ++i) mbar_init(smem_u32(&sh.wide_full[i]), 4);
+        for (int t = 0; t < 2; ++t) {
+            mbar_init(smem_u32(&sh.q_full[t]), FP8 ? 4 : 1);
+            for (int i = 0; i < CH_EVENTS; ++i) mbar_init(smem_u32(&sh.event[t][i]), 1);
+            mbar_init(smem_u32(&sh.p_full[t][0]), 128);
+            mbar_init(smem_u32(&sh.p_full[t][1]), 128);
+            mbar_init(smem_u32(&sh.turn[t]), 1);
+            mbar_init(smem_u32(&sh.drain[t]), 1);
+        }
+        mbar_init(smem_u32(&sh.v_tail), 1);
+        for (int i = 0; i < CH_ITEMS; ++i) {
+            mbar_init(smem_u32(&sh.item_full[i]), 1);
+            mbar_init(smem_u32(&sh.item_free[i]), FP8 ? 14 : 10);
+        }
+        for (int i = 0; i < CH_SCALES; ++i) mbar_init(smem_u32(&sh.sc_full[i]), 1);
+        sh.abort = sh.issued = sh.tail_open = sh.tail_phase = 0;
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    grid_wait();
+    ChPlan plan;
+    const bool aligned = (base & 1023) == 0;   // as declared; the swizzled tiles would be elsewhere
+    if (!aligned && tid == 0 && A.status) atomicOr(A.status, KVO_DEV_TIMEOUT);
+    if (!aligned || !ch_plan<P::THREADS>(sh, A, plan)) {
+        if (tid == 0) {
+            ChunkCut cut{};
+            cut.last = -1;
+            A.cut[blockIdx.x] = cut;
+        }
+        return;
+    }
+    if (warp == 8) tmem_alloc(smem_u32(&sh.tmem), 512);
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+
+    // The next item, once the walking warp has written it.
+    auto next_item = [&](uint32_t k, ChunkItem& I) {
+        if (!ch_wait(sh, A, sh.item_full[k % CH_ITEMS], k / CH_ITEMS)) return false;
+        I = sh.item[k % CH_ITEMS];
+        return true;
+    };
+    auto free_item = [&](uint32_t k) { mbar_arrive(smem_u32(&sh.item_free[k % CH_ITEMS])); };
+
+    if (warp >= 8) {
+        regs_dec<P::REGS_OTHER>();
+        if (warp == 9) {
+            // ------------------------------------------------ items, loads
+            ChWalk walk = ch_locate(A, sh.found[0], ch_request(A, sh.found[0]), sh.at[0], plan.lo);
+            int high = sh.high[0];
+            const int64_t lo = plan.lo, hi = plan.hi;
+            if (lane == 0) A.cut[blockIdx.x] = ch_cut(sh, A, plan, walk);    // before anything that may give up: the join follows it
+            __syncwarp();
+            bool ok = true, tail_open = false;
+            uint32_t k = 0, tail_phase = 0, tiles = 0;
+            int issued = 0;
+            uint32_t events[2] = {0, 0}, q_issued[2] = {0, 0};
+            uint32_t q_free[2] = {~0u, ~0u};            // the event after which a tile's q may be overwritten
+            uint32_t e0 = ~0u, e1 = ~0u;                // of stage `lane`: the events that free it
+            const int rows = A.n_pages * A.hkv * A.page, chunks = A.page / 16;
+            constexpr int ROW = D * (FP8 ? 1 : 2), BOXES = ROW > 128 ? ROW / 128 : 1, BOX = ROW > 128 ? 128 : ROW;
+            const int boxes = CH_KEYS / A.page * BOXES;
+            auto event_wait = [&](int t, uint32_t e) { return e == ~0u || ch_event(sh, A, t, e); };
+            while (ok) {
+                int n_all[2], first, last;
+                n_all[0] = ch_tiles(A, walk.r, walk.i, 0);
+                n_all[1] = ch_tiles(A, walk.r, walk.i, 1);
+                const int n_item = max(n_all[0], n_all[1]);
+                ch_part(walk, lo, hi, n_item, first, last);
+                if (n_item ? last > first : walk.start >= lo) {
+                    ChunkItem I;
+                    I.row = walk.r.a;
+                    I.first = first;
+                    I.n[0] = min(max(n_all[0] - first, 0), last - first);
+                    I.n[1] = min(max(n_all[1] - first, 0), last - first);
+                    I.b = walk.b;
+                    I.g = walk.g;
+                    I.tok0 = walk.i * 2 * A.tq;
+                    I.nq = walk.r.n;
+                    I.len = walk.r.len;
+                    I.part = first == 0 && last == n_item ? -1 : 2 * (int)blockIdx.x + (first == 0);
+                    if (k >= CH_ITEMS) ok = ch_wait(sh, A, sh.item_free[k % CH_ITEMS], k / CH_ITEMS - 1);
+                    if (!__all_sync(0xffffffffu, ok)) break;
+                    if (lane == 0) {
+                        sh.item[k % CH_ITEMS] = I;
+                        mbar_arrive(smem_u32(&sh.item_full[k % CH_ITEMS]));
+                    }
+                    ++k;
+                    const int n = max(I.n[0], I.n[1]);
+                    const int32_t* table = A.table + (int64_t)I.b * A.max_pages;
+                    // Lane: the (lane % 8)-th 16 keys of tile lane / 8 of four.
+                    auto page_of = [&](int j) {
+                        const int64_t key = (int64_t)(I.first + j + (lane >> 3)) * CH_KEYS + 16 * (lane & 7);
+                        return key < I.len ? __ldg(table + (key >> A.shift)) : -1;
+                    };
+                    int page = 0, page_next = page_of(0);
+                    bool bad = false;
+                    float ks = 0.f, vs = 0.f;
+                    for (int j = 0; ok && j < n; ++j) {
+                        if ((j & 3) == 0) {
+                            page = page_next;
+                            if (j + 4 < n) page_next = page_of(j + 4);
+                            const bool in = (int64_t)(I.first + j + (lane >> 3)) * CH_KEYS + 16 * (lane & 7) < I.len;
+                            bad = in && (page < 0 || page >= A.n_pages);
+                            if (bad && j + (lane >> 3) < n && A.status) atomicOr(A.status, KVO_DEV_BAD_BLOCK_ID);
+                            if (bad || !in) page = -1;
+                            if constexpr (FP8) {
+                                ks = page < 0 ? 1.f : __ldg(A.k_scale + (int64_t)page * A.hkv + I.g);
+                                vs = page < 0 ? 0.f : __ldg(A.v_scale + (int64_t)page * A.hkv + I.g);
+                            }
+                        }
+                        const uint32_t bads = __ballot_sync(0xffffffffu, bad) >> (j & 3) * 8 & 0xFF;
+                        const int sc = tiles % CH_SCALES;
+                        // Box `lane`: its page's first row in the pool, or what lies behind the last (zeros).
+                        const int from = __shfl_sync(0xffffffffu, page, (j & 3) * 8 + lane / BOXES * chunks & 31);
+                        const int y = from < 0 ? rows : (from * A.hkv + I.g) * A.page;
+                        const int key0 = (I.first + j) * CH_KEYS;
+                        for (int v = 0; v < 2; ++v) {
+                            const int st = issued % P::STAGES;
+                            if (issued >= P::STAGES) {
+                                if (FP8 && v) {
+                                    ok = ch_wait(sh, A, sh.raw_free[st / 2], issued / P::STAGES - 1);
+                                } else {
+                                    ok = event_wait(0, __shfl_sync(0xffffffffu, e0, st));
+                                    ok = event_wait(1, __shfl_sync(0xffffffffu, e1, st)) && ok;
+                                }
+                                if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
+                            }
+                            if (v == 0) {
+                                // Before the keys are asked for: their scores are there only after this.
+                                if constexpr (FP8)
+                                    if (lane >> 3 == (j & 3)) {
+                                        sh.k_scale[sc][lane & 7] = ks;
+                                        sh.v_scale[sc][lane & 7] = vs;
+                                    }
+                                if (lane == 0) sh.bad[sc] = bads;
+                                __syncwarp();
+                                if (lane == 0) mbar_arrive(smem_u32(&sh.sc_full[sc]));
+                            }
+                            // The last tile of a request runs into what lies behind it in its page.  Its keys are masked as
+                            // scores, but a weight of zero does not silence a NaN or an infinity in V: those rows are cleared.
+                            const bool tail = !FP8 && v && key0 + CH_KEYS > I.len;
+                            const uint32_t bar = smem_u32(tail ? &sh.v_tail : &sh.kv_full[st]), dst = ring + st * P::TILE;
+                            if (lane == 0) mbar_expect_tx(bar, P::TILE);
+                            __syncwarp();
+                            if (lane < boxes && issued != A.skip)
+                                tma_load_2d(dst + (lane % BOXES) * CH_BLOCK + lane / BOXES * A.page * BOX, v ? &map_v : &map_k,
+                                            (lane % BOXES) * (FP8 ? 128 : 64), y, bar);
+                            if (tail) {
+                                tail_open = true;
+                                ok = ch_wait(sh, A, sh.v_tail, tail_phase);
+                                if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
+                                tail_open = false;
+                                ++tail_phase;
+                                for (int x = 0; x < BOXES; ++x)
+                                    for (uint32_t a = (I.len - key0) * 128 + lane * 16; a < CH_BLOCK; a += 512)
+                                        asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(dst + x * CH_BLOCK + a), "r"(0) : "memory");
+                                fence_async_smem();
+                                __syncwarp();
+                                if (lane == 0) mbar_arrive(smem_u32(&sh.kv_full[st]));
+                            }
+                            if (lane == st) {
+                                e0 = j < I.n[0] ? events[0] + j + v : ~0u;
+                                e1 = j < I.n[1] ? events[1] + j + v : ~0u;
+                            }
+                            ++issued;
+                            if (!FP8 && j == 0 && v == 0)
+                                for (int t = 0; t < 2; ++t) {
+                                    if (I.n[t] == 0) continue;
+                                    ok = event_wait(t, q_free[t]);
+                                    if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
+                                    if (lane == 0) {
+                                        mbar_expect_tx(smem_u32(&sh.q_full[t]), (uint32_t)((D / 64) * 128 * A.r * A.tq));
+                                        for (int x = 0; x < D / 64; ++x)
+                                            tma_load_3d(base + t * P::Q + x * CH_BLOCK, &map_q, 64 * x, I.g * A.r, (int)I.row + I.tok0 + t * A.tq,
+                                                        smem_u32(&sh.q_full[t]));
+                                    }
+                                    ++q_issued[t];
+                                }
+                            if (!ok) break;
+                        }
+                        ++tiles;
+                    }
+                    for (int t = 0; t < 2; ++t)
+                        if (I.n[t]) {
+                            q_free[t] = events[t] + I.n[t] - 1;
+                            events[t] += I.n[t] + 1;
+                        }
+                }
+                walk.start += walk.cost;
+                if (!ok || walk.start >= hi) break;
+                if (++walk.g == A.hkv) {
+                    walk.g = 0;
+                    if (++walk.i == ch_blocks(A, walk.r)) {
+                        walk.i = 0;
+                        do {                   // the range does not end here: there is another served request with new tokens
+                            if (walk.r.served) high = max(high, walk.r.a + walk.r.n);
+                            if (++walk.b >= A.batch) { ok = false; break; }
+                            walk.r = ch_request(A, walk.b);
+                            walk.r.served = walk.r.served && walk.r.a >= high;
+                        } while (!walk.r.served || walk.r.n == 0);
+                        if (!ok) { ok = true; break; }
+                    }
+                    walk.cost = ch_cost(A, walk.r, walk.i);
+                }
+            }
+            if (ok && k >= CH_ITEMS) ok = ch_wait(sh, A, sh.item_free[k % CH_ITEMS], k / CH_ITEMS - 1);
+            ok = __all_sync(0xffffffffu, ok);
+            if (lane == 0) {
+                if (ok) {
+                    sh.item[k % CH_ITEMS].n[0] = -1;
+                    mbar_arrive(smem_u32(&sh.item_full[k % CH_ITEMS]));
+                }
+                sh.issued = issued;
+                sh.tail_open = tail_open;
+                sh.tail_phase = tail_phase;
+            }
+            // Where somebody gave up not all loads may have landed: the warp that issued them stays until they have, and
+            // with it the CTA and its shared memory.  (`abort` is final only once all have left their waits: below.)
+            __syncwarp();
+            if (lane == 0) { sh.found[0] = q_issued[0]; sh.found[1] = q_issued[1]; }
+        } else if ((warp == 8 || warp == 10) && lane == 0) {
+            // ------------------------------------------------ matrix products of one tile
+            // The tensor cores queue a few instructions only; with a thread of its own for each tile, one tile's waits and
+            // commits pass while the other's products run.  They take turns, so that the tiles stay half a period apart.
+            constexpr uint32_t ID_S = FP8 ? mma_desc_e4m3(CH_ROWS, CH_KEYS) : mma_desc(CH_ROWS, CH_KEYS, false), ID_O = mma_desc(CH_ROWS, D, true);
+            const int t = (warp - 8) >> 1;
+            const uint32_t S = sh.tmem + 128 * t, O = sh.tmem + 256 + D * t;
+            constexpr bool HALF = FP8 && D == 64;              // rows of 64 bytes
+            const uint64_t q = HALF ? smem_desc64(base + t * P::Q) : smem_desc(base + t * P::Q, 16);
+            const uint64_t k0 = HALF ? smem_desc64(ring) : smem_desc(ring, 16);
+            const uint64_t v0 = smem_desc(FP8 ? base + WIDE0 : ring, CH_BLOCK);
+            uint32_t item = 0, events = 0, events_other = 0, weights = 0, qs = 0, turns = 0, tiles = 0;
+            bool ok = true, behind = false;
+            while (true) {
+                ChunkItem I;
+                if (!next_item(item, I)) break;
+                free_item(item++);
+                if (I.n[0] < 0) break;
+                const int n_mine = I.n[t], n_other = I.n[t ^ 1], n = max(n_mine, n_other);
+                auto stage = [&](int load, uint32_t& phase) {
+                    phase = load / P::STAGES;
+                    return load % P::STAGES;
+                };
+                auto keys_there = [&](int j) {
+                    uint32_t phase;
+                    const int st = stage(2 * (tiles + j), phase);
+                    return ch_wait(sh, A, sh.kv_full[st], phase);
+                };
+                auto values_there = [&](int j) {
+                    uint32_t phase;
+                    if (FP8) return ch_wait(sh, A, sh.wide_full[(tiles + j) % 2], (tiles + j) / 2);
+                    const int st = stage(2 * (tiles + j) + 1, phase);
+                    return ch_wait(sh, A, sh.kv_full[st], phase);
+                };
+                auto scores = [&](int j, bool pass) {
+                    const uint64_t kd = k0 + (uint64_t)((2 * (tiles + j)) % P::STAGES) * (P::TILE >> 4);
+                    constexpr int STEPS = FP8 ? 2 * (D / 32) : D / 16;
+#pragma unroll
+                    for (int e = 0; e < STEPS; ++e) {
+                        if (e == STEPS / 2 && pass) mbar_arrive(smem_u32(&sh.turn[t ^ 1]));     // queued work covers the hand-over
+                        if (FP8) {
+                            constexpr int PER = D / 32;
+                            mma_ss_e4m3(S, q + (e / PER) * (CH_ROWS * D >> 4) + (e % PER) * 2, kd + (e % PER) * 2, ID_S, e > 0);
+                        } else {
+                            const int off = (e >> 2) * (CH_BLOCK >> 4) + (e & 3) * 2;
+                            mma_ss(S, q + off, kd + off, ID_S, e > 0);
+                        }
+                    }
+                    tc_commit(smem_u32(&sh.event[t][(events + j) % CH_EVENTS]));
+                };
+                if (n_mine > 0) {
+                    // Tiles that only the other one used: their loads have landed once its products are complete (a barrier's
+                    // parity tells phases apart only where none is passed over).
+                    if (behind && !(ok = ch_event(sh, A, t ^ 1, events_other - 1))) break;
+                    behind = false;
+                    ok = ch_wait(sh, A, sh.q_full[t], qs++) && keys_there(0);
+                    if (!ok) break;
+                    tc_fence_after();
+                    scores(0, false);
+                    for (int j = 0; j < n_mine; ++j) {
+                        if (!(ok = values_there(j))) break;
+                        if (j + 1 < n_mine && !(ok = keys_there(j + 1))) break;
+                        const uint64_t v = v0 + (uint64_t)(FP8 ? (tiles + j) % 2 * (P::WIDE_BYTES >> 4) : (2 * (tiles + j) + 1) % P::STAGES * (P::TILE >> 4));
+#pragma unroll
+                        for (int h = 0; h < 2; ++h) {        // in two halves of the keys, each as its weights come
+                            if (!ok || !(ok = ch_wait(sh, A, sh.p_full[t][h], weights))) break;
+                            if (h == 0) {
+                                const int x = t ? j : j - 1;             // the other tile's round before this one
+                                if (x >= 0 && x < n_other && !(ok = ch_wait(sh, A, sh.turn[t], turns + x))) break;
+                            }
+                            tc_fence_after();
+#pragma unroll
+                            for (int e = 4 * h; e < 4 * h + 4; ++e)
+                                mma_ts(O, S + 8 * e, v + e * (2048 >> 4), ID_O, j > 0 || e > 0);
+                        }
+                        if (!ok) break;
+                        ++weights;
+                        // One commit for the scores stands for the value product before them as well.
+                        if (j + 1 < n_mine) {
+                            scores(j + 1, n_other > 0);
+                        } else {
+                            tc_commit(smem_u32(&sh.event[t][(events + n_mine) % CH_EVENTS]));
+                            if (n_other > 0) mbar_arrive(smem_u32(&sh.turn[t ^ 1]));
+                        }
+                    }
+                    if (!ok) break;
+                    events += n_mine + 1;
+                    if (n_other > 0) turns += n_other;
+                }
+                if (n_other > n_mine) behind = true;
+                if (n_other > 0) events_other += n_other + 1;
+                tiles += n;
+            }
+            // nothing of this CTA may be in flight when it leaves
+            tc_commit(smem_u32(&sh.drain[t]));
+            if (!mbar_wait_bounded(smem_u32(&sh.drain[t]), 0, A.wait_ns)) {
+                *(volatile int*)&sh.abort = 1;
+                if (A.status) atomicOr(A.status, KVO_DEV_TIMEOUT);
+            }
+        } else if (FP8 && warp >= 12) {
+            // ------------------------------------------------ q and V of 8-bit pages
+            if constexpr (FP8) {
+                uint32_t item = 0, tiles = 0, events[2] = {0, 0}, q_free[2] = {~0u, ~0u}, wide_free[2][2] = {{~0u, ~0u}, {~0u, ~0u}};
+                const int row = tid & 127;
+                bool ok = true;
+                while (ok) {
+                    ChunkItem I;
+                    ok = next_item(item, I);
+                    if (!__all_sync(0xffffffffu, ok)) break;
+                    if (lane == 0) free_item(item);
+                    if (I.n[0] < 0) break;
+                    for (int t = 0; t < 2 && ok; ++t) {
+                        if (I.n[t] == 0) continue;
+                        if (q_free[t] != ~0u) ok = ch_event(sh, A, t, q_free[t]);
+                        if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
+                        ch_split_q<D>(A, I, t, row, smem + t * P::Q, &sh.q_exp[item & 1][t][row]);
+                        fence_async_smem();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(smem_u32(&sh.q_full[t]));
+                    }
+                    ++item;
+                    const int n = max(I.n[0], I.n[1]);
+                    for (int j = 0; j < n && ok; ++j) {
+                        const uint32_t load = 2 * tiles + 1, st = load % P::STAGES;
+                        const int w = tiles % 2;
+                        ok = ch_wait(sh, A, sh.kv_full[st], load / P::STAGES);
+                        for (int t = 0; t < 2; ++t) {
+                            const uint32_t e = w ? wide_free[1][t] : wide_free[0][t];
+                            if (ok && e != ~0u) ok = ch_event(sh, A, t, e);
+                        }
+                        if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
+                        ch_widen_v<D>(smem + 2 * P::Q + st * P::TILE, smem + WIDE0 + w * P::WIDE_BYTES, I.len - (I.first + j) * CH_KEYS);
+                        fence_async_smem();
+                        __syncwarp();
+                        if (lane == 0) {
+                            mbar_arrive(smem_u32(&sh.raw_free[st / 2]));
+                            mbar_arrive(smem_u32(&sh.wide_full[w]));
+                        }
+#pragma unroll
+                        for (int t = 0; t < 2; ++t) {
+                            const uint32_t e = j < I.n[t] ? events[t] + j + 1 : ~0u;
+                            if (w) wide_free[1][t] = e;
+                            else wide_free[0][t] = e;
+                        }
+                        ++tiles;
+                    }
+#pragma unroll
+                    for (int t = 0; t < 2; ++t)
+                        if (I.n[t]) {
+                            q_free[t] = events[t] + I.n[t] - 1;
+                            events[t] += I.n[t] + 1;
+                        }
+                }
+            }
+        }
+        __syncwarp();
+    } else {
+        regs_inc<P::REGS_SOFTMAX>();
+        const int t = warp >> 2;
+        uint32_t item = 0, events = 0, keys = 0;
+        while (true) {
+            ChunkItem I;
+            const bool ok = next_item(item, I);
+            if (!__all_sync(0xffffffffu, ok)) break;
+            if (lane == 0) free_item(item);
+            if (I.n[0] < 0) break;
+            if (!ch_softmax<D, FP8>(sh, A, I, t, events, keys, item & 1)) break;
+            ++item;
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (warp == 8) tmem_free(sh.tmem, 512);
+    // Every warp has left its waits, so `abort` is final.  Where it is set somebody stopped before all loads had landed: the
+    // thread that issued them stays until they have.
+    if (tid == 9 * 32 && sh.abort) {
+        const int issued = sh.issued;
+        if (!FP8)
+            for (int t = 0; t < 2; ++t)
+                if (sh.found[t]) mbar_wait_bounded(smem_u32(&sh.q_full[t]), (sh.found[t] - 1) & 1, A.wait_ns);
+        for (int i = max(0, issued - P::STAGES); i < issued; ++i)
+            mbar_wait_bounded(smem_u32(&sh.kv_full[i % P::STAGES]), (i / P::STAGES) & 1, A.wait_ns);
+        if (sh.tail_open) mbar_wait_bounded(smem_u32(&sh.v_tail), sh.tail_phase & 1, A.wait_ns);
+    }
+}
+
+// ------------------------------------------------------------------ the join
+// Rows of an item that range borders cut: CTA (c, t, x) joins 32 columns x of tile t of the item that begins in range c.
+template <int D>
+__global__ void __launch_bounds__(CH_ROWS) paged_chunk_join_kernel(const __grid_constant__ ChunkArgs A) {
+    __shared__ int slots[CH_CTAS + 1], count;
+    grid_wait();
+    const int c = blockIdx.x, t = blockIdx.y, row = threadIdx.x;
+    const ChunkCut cut = A.cut[c];
+    if (cut.last < 0) return;
+    const int tl = row / A.r, head = row - tl * A.r, tok = cut.tok0 + t * A.tq + tl;
+    const bool real = tl < A.tq && tok < cut.n;
+    if (cut.tok0 + t * A.tq >= cut.n) return;
+    if (row < 32) {
+        int n = 1;
+        if (row == 0) slots[0] = 2 * c + 1;
+        for (int k0 = c + 1; k0 <= cut.last; k0 += 32) {
+            const bool more = k0 + row <= cut.last && A.cut[k0 + row].more;
+            const unsigned all = __ballot_sync(0xffffffffu, more);
+            if (more) slots[n + __popc(all & ((1u << row) - 1))] = 2 * (k0 + row);
+            n += __popc(all);
+        }
+        if (row == 0) count = n;
+    }
+    __syncthreads();
+    if (!real) return;
+    const int n = count;
+    float m = -INFINITY, l = 0.f;
+#pragma unroll 8
+    for (int i = 0; i < n; ++i) {
+        const float2 ml = A.part_ml[((int64_t)slots[i] * A.tiles + t) * CH_ROWS + row];
+        if (ml.y != 0.f) m = fmaxf(m, ml.x);
+    }
+    float4 acc[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) acc[e] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 2
+    for (int i = 0; i < n; ++i) {
+        const int64_t at = (int64_t)slots[i] * A.tiles + t;
+        const float2 ml = A.part_ml[at * CH_ROWS + row];
+        if (ml.y == 0.f) continue;             // it saw nothing: its memory may hold anything
+        const float4* from = reinterpret_cast<const float4*>(A.part_o) + (at * (D / 4) + blockIdx.z * 8) * CH_ROWS + row;
+        const float f = ex2(ml.x - m);
+        l += f * ml.y;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            const float4 o = from[e * CH_ROWS];
+            acc[e].x += f * o.x;
+            acc[e].y += f * o.y;
+            acc[e].z += f * o.z;
+            acc[e].w += f * o.w;
+        }
+    }
+    const float inv = l != 0.f ? 1.f / l : 0.f;
+    const int64_t out = (cut.row + tok) * A.hq + cut.g * A.r + head;
+    uint4* to = reinterpret_cast<uint4*>(A.o + out * D + blockIdx.z * 32);
+#pragma unroll
+    for (int e = 0; e < 8; e += 2) {
+        const __nv_bfloat162 a = __floats2bfloat162_rn(acc[e].x * inv, acc[e].y * inv), b = __floats2bfloat162_rn(acc[e].z * inv, acc[e].w * inv);
+        const __nv_bfloat162 g = __floats2bfloat162_rn(acc[e + 1].x * inv, acc[e + 1].y * inv), d = __floats2bfloat162_rn(acc[e + 1].z * inv, acc[e + 1].w * inv);
+        to[e / 2] = make_uint4(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b), *reinterpret_cast<const uint32_t*>(&g),
+                               *reinterpret_cast<const uint32_t*>(&d));
+    }
+    if (blockIdx.z == 0 && A.lse) A.lse[out] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
+}
+
+// ------------------------------------------------------------------ host
+struct ChunkSpace {
+    size_t cut, ml, o;
+};
+ChunkSpace chunk_space(int tiles, int d) {
+    auto up = [](size_t x) { return (x + 255) / 256 * 256; };
+    const size_t rows = (size_t)CH_CTAS * 2 * tiles * CH_ROWS;
+    return {up(CH_CTAS * sizeof(ChunkCut)), up(rows * sizeof(float2)), rows * d * sizeof(float)};
+}
+int chunk_tiles(int64_t total_q, int r) { return total_q <= CH_ROWS / r ? 1 : 2; }
+
+const char* chunk_error(const kvo_paged_cache* c, int n_q_heads, int64_t total_q, int64_t max_new, int64_t max_len) {
+    if (const char* m = paged_cache_error(c)) return m;
+    if (n_q_heads < c->n_kv_heads || n_q_heads % c->n_kv_heads) return "n_q_heads must be a multiple of n_kv_heads";
+    if (n_q_heads / c->n_kv_heads > 16) return "n_q_heads / n_kv_heads must be <= 16";
+    if (total_q < 0 || total_q > INT32_MAX) return "total_q must be in 0..2^31 - 1";
+    if (max_new < 0 || max_len < 0) return "max_new and max_len must be >= 0";
+    return nullptr;
+}
+
+template <int D, bool FP8>
+cudaError_t paged_chunk_launch(const CUtensorMap& mq, const CUtensorMap& mk, const CUtensorMap& mv, const ChunkArgs& A, cudaStream_t s) {
+    using P = ChShape<D, FP8>;
+    constexpr int SMEM = P::TILES + (int)sizeof(ChShared);
+    static_assert(SMEM <= 227 * 1024 && SMEM > 114 * 1024, "one CTA to an SM");
+    static std::atomic<uint64_t> done{0};
+    if (first_on_device(done)) {
+        const cudaError_t e = cudaFuncSetAttribute(paged_chunk_kernel<D, FP8>, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM);
+        if (e != cudaSuccess) return e;
+        mark_on_device(done);
+    }
+    const cudaError_t e = launch_dependent(paged_chunk_kernel<D, FP8>, dim3(CH_CTAS), P::THREADS, SMEM, s, 0, mq, mk, mv, A);
+    if (e != cudaSuccess) return e;
+    return launch_dependent(paged_chunk_join_kernel<D>, dim3(CH_CTAS, A.tiles, D / 32), CH_ROWS, 0, s, 0, A);
+}
+
+}  // namespace kvo
+
+extern "C" kvo_status kvo_paged_chunk_attn_workspace(const kvo_paged_cache* cache, int n_q_heads, int64_t total_q, int64_t max_new,
+                                                     int64_t max_len, size_t* bytes_out) {
+    using namespace kvo;
+    auto bad = [](const char* m) { set_last_error(m); return KVO_ERR_INVALID; };
+    if (!bytes_out) return bad("null output pointer");
+    *bytes_out = 0;
+    if (const char* m = chunk_error(cache, n_q_heads, total_q, max_new, max_len)) return bad(m);
+    const ChunkSpace sp = chunk_space(chunk_tiles(total_q, n_q_heads / cache->n_kv_heads), cache->head_dim);
+    *bytes_out = sp.cut + sp.ml + sp.o;
+    return KVO_OK;
+}
+
+extern "C" kvo_status kvo_paged_chunk_attn(const kvo_paged_cache* cache, const void* q, int64_t q_token_stride, int64_t total_q,
+                                           int n_q_heads, const int32_t* cu, const int32_t* lens, int64_t max_new, int64_t max_len,
+                                           void* o, float* lse, void* workspace, size_t workspace_bytes, int32_t* status,
+                                           kvo_stream_t stream) {
+    using namespace kvo;
+    auto bad = [](const char* m) { set_last_error(m); return KVO_ERR_INVALID; };
+    if (const char* m = chunk_error(cache, n_q_heads, total_q, max_new, max_len)) return bad(m);
+    if (cache->batch == 0 || total_q == 0) return KVO_OK;
+    if (!q || !o || !cu || !lens) return bad("null pointer argument");
+    if ((uintptr_t)q % 16 || (uintptr_t)o % 16 || (uintptr_t)workspace % 256)
+        return bad("q and o must be 16-byte aligned, the workspace 256-byte aligned");
+    const int r = n_q_heads / cache->n_kv_heads, D = cache->head_dim;
+    const int64_t width = (int64_t)n_q_heads * D, b = cache->batch;
+    if (q_token_stride % 8) return bad("strides must be multiples of 8 elements");
+    if (q_token_stride < width) return bad("token strides must cover the heads");
+    if (q_token_stride > (1ll << 38)) return bad("token strides must be below 2^38 elements");
+    const int tiles = chunk_tiles(total_q, r);
+    const ChunkSpace sp = chunk_space(tiles, D);
+    const size_t need = sp.cut + sp.ml + sp.o;
+    if (!workspace || workspace_bytes < need) return bad("the workspace is too small (kvo_paged_chunk_attn_workspace)");
+    const int64_t pool = page_bytes(cache), scales = scale_bytes(cache);
+    const Bytes to_o{o, 2 * total_q * width}, to_lse{lse, 4 * total_q * n_q_heads}, to_ws{workspace, (int64_t)need};
+    bool meet = meets_any(to_o, {to_lse, to_ws}) || meets_any(to_lse, {to_ws});
+    for (const Bytes& x : {to_o, to_lse, to_ws})
+        meet |= meets_any(x, {{q, rows_bytes(total_q, q_token_stride, width)}, {cache->k_pages, pool}, {cache->v_pages, pool},
+                              {cache->k_scale, scales}, {cache->v_scale, scales}, {cache->table, 4 * b * cache->max_pages}, {lens, 4 * b},
+                              {cu, 4 * (b + 1)}});
+    if (meet) return bad("o, lse and the workspace must be apart from each other and from all that the call reads");
+    const bool fp8 = cache->format == KVO_PAGES_E4M3;
+    ChunkArgs A{};
+    A.q = (const uint16_t*)q;
+    A.q_stride = q_token_stride;
+    A.k_scale = fp8 ? cache->k_scale : nullptr;
+    A.v_scale = fp8 ? cache->v_scale : nullptr;
+    A.table = cache->table;
+    A.lens = lens;
+    A.cu = cu;
+    A.o = (uint16_t*)o;
+    A.lse = lse;
+    A.status = status;
+    A.cut = (ChunkCut*)workspace;
+    A.part_ml = (float2*)((uint8_t*)workspace + sp.cut);
+    A.part_o = (float*)((uint8_t*)workspace + sp.cut + sp.ml);
+    A.total = total_q;
+    A.batch = cache->batch;
+    A.hq = n_q_heads;
+    A.hkv = cache->n_kv_heads;
+    A.r = r;
+    A.tq = CH_ROWS / r;
+    A.page = cache->page_size;
+    A.shift = cache->page_size == 16 ? 4 : cache->page_size == 32 ? 5 : cache->page_size == 64 ? 6 : 7;
+    A.n_pages = cache->n_pages;
+    A.max_pages = cache->max_pages;
+    A.tiles = tiles;
+    A.w1 = fp8 ? 4 : 6;
+    A.w2 = 7;
+    A.base = 2 * CH_KEYS * A.w2;
+    A.least = 2 * CH_KEYS * A.w1 + A.base;
+    A.scale_log2 = (float)(1.4426950408889634 / sqrt((double)D));
+    A.skip = call_wait.skip;
+    A.wait_ns = call_wait.limit_ns;
+    CUtensorMap mq, mk, mv;
+    const uint64_t sq[3] = {(uint64_t)D, (uint64_t)n_q_heads, (uint64_t)total_q}, tq[2] = {(uint64_t)D * 2, (uint64_t)q_token_stride * 2};
+    const uint32_t bq[3] = {64, (uint32_t)r, (uint32_t)A.tq};
+    const uint64_t rows = (uint64_t)cache->n_pages * cache->n_kv_heads * cache->page_size;
+    const int elem = fp8 ? 1 : 2, box = std::min(D * elem, 128);
+    if (!tensor_map(&mq, q, 2, 3, sq, tq, bq) || !tensor_map_rows(&mk, cache->k_pages, elem, D, rows, box, cache->page_size) ||
+        !tensor_map_rows(&mv, cache->v_pages, elem, D, rows, box, cache->page_size)) {
+        set_last_error("cuTensorMapEncodeTiled failed for q or the pages");
+        return KVO_ERR_CUDA;
+    }
+    cudaStream_t s = (cudaStream_t)stream;
+    cudaError_t e;
+    if (D == 128) e = fp8 ? paged_chunk_launch<128, true>(mq, mk, mv, A, s) : paged_chunk_launch<128, false>(mq, mk, mv, A, s);
+    else e = fp8 ? paged_chunk_launch<64, true>(mq, mk, mv, A, s) : paged_chunk_launch<64, false>(mq, mk, mv, A, s);
+    if (e != cudaSuccess) { set_last_error(cudaGetErrorString(e)); return KVO_ERR_CUDA; }
+    return KVO_OK;
+}

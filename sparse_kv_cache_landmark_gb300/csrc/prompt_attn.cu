@@ -43,6 +43,7 @@
 
 #include <algorithm>
 
+#include "f32x2.cuh"
 #include "kvo_internal.cuh"
 #include "launch.cuh"
 #include "paged.cuh"
@@ -77,35 +78,6 @@ struct PromptArgs {
     int skip;                      // the load (K(0), V(0), K(1), ..) that every CTA announces without copying it (tests; -1: none)
     long long wait_ns;
 };
-
-__device__ __forceinline__ float pr_ex2(float x) {
-    float y;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-}
-
-// Two fp32 lanes in one instruction.
-__device__ __forceinline__ uint64_t pack2(float lo, float hi) {
-    uint64_t r;
-    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
-    return r;
-}
-__device__ __forceinline__ void unpack2(uint64_t v, float& lo, float& hi) { asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v)); }
-__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
-    uint64_t r;
-    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
-    return r;
-}
-__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
-    uint64_t r;
-    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-    return r;
-}
-__device__ __forceinline__ float max3(float a, float b, float c) {
-    float r;
-    asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
-    return r;
-}
 
 struct PrShared {
     uint64_t q_full[2], kv_full[12], s_full[2][6], p_full[2][2], o_done[2], turn[2], drain[2], v_tail;
@@ -180,7 +152,7 @@ __device__ __forceinline__ void pr_softmax(PrShared& sh, const PromptArgs& A, in
         const float top = fmaxf(max3(mx[0], mx[1], mx[2]), mx[3]) * A.scale_log2;
         if (__any_sync(0xffffffffu, top > m + PR_RAISE)) {
             const float to = fmaxf(m, top);
-            const float f = m == -INFINITY ? 0.f : pr_ex2(m - to);
+            const float f = m == -INFINITY ? 0.f : ex2(m - to);
             m = to;
             l *= f;
             if (j > 0) {           // S(j) complete: so is O += P(j - 1) V, which was issued before it
@@ -205,8 +177,8 @@ __device__ __forceinline__ void pr_softmax(PrShared& sh, const PromptArgs& A, in
             for (int i = 0; i < 16; ++i) {
                 float x, y;
                 unpack2(fma2(pack2(__uint_as_float(s[32 * h + 2 * i]), __uint_as_float(s[32 * h + 2 * i + 1])), scale2, b2), x, y);
-                x = pr_ex2(x);
-                y = pr_ex2(y);
+                x = ex2(x);
+                y = ex2(y);
                 sum[i & 1] = add2(sum[i & 1], pack2(x, y));
                 const __nv_bfloat162 v = __floats2bfloat162_rn(x, y);
                 p[i] = *reinterpret_cast<const uint32_t*>(&v);
@@ -306,7 +278,7 @@ __device__ __forceinline__ void pr_join(const PromptArgs& A, uint8_t* smem, int 
     float to = ml.x;
 #pragma unroll
     for (int k = 1; k < PARTS; k <<= 1) to = fmaxf(to, __shfl_xor_sync(0xffffffffu, to, k));
-    const float f = ml.y == 0.f ? 0.f : pr_ex2(ml.x - to);     // a part that saw nothing has weight 0
+    const float f = ml.y == 0.f ? 0.f : ex2(ml.x - to);     // a part that saw nothing has weight 0
     float sum = f * ml.y;
 #pragma unroll
     for (int k = 1; k < PARTS; k <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, k);

@@ -4,7 +4,7 @@ Every step of the decode path runs in the library's CUDA kernels; this module
 turns torch tensors into pointers, allocates outputs with torch, and raises
 ``KvoError`` on any non-OK status.  There is no fallback: without the built
 library or a CUDA device every call fails.  The serving calls (rope, paged_append,
-paged_attn, prompt_attn, the pages' bookkeeping), which a decode loop makes once per layer and token, go
+paged_attn, paged_chunk_attn, prompt_attn, the pages' bookkeeping), which a decode loop makes once per layer and token, go
 through a native binding (csrc/binding.cpp) instead of ctypes.  They are for
 inference: nothing is recorded for a backward pass.
 """
@@ -33,7 +33,7 @@ EXPORTS = ["kv_offload_init", "kv_offload_destroy", "select_topk", "index_diff",
            "kvo_set_prefetch_budget", "kvo_set_lowrank_keys", "kvo_plan_attention", "kvo_plan_select", "kvo_set_wait_test",
            "kvo_set_call_wait_test",
            "kvo_set_spec_policy", "kvo_spec_stats", "kvo_rope", "kvo_paged_append", "kvo_paged_attn",
-           "kvo_paged_attn_workspace", "kvo_prompt_attn", "kvo_paged_reserve", "kvo_paged_fork",
+           "kvo_paged_attn_workspace", "kvo_paged_chunk_attn", "kvo_paged_chunk_attn_workspace", "kvo_prompt_attn", "kvo_paged_reserve", "kvo_paged_fork",
            "kvo_paged_fork_workspace", "kvo_paged_compact", "kvo_paged_compact_workspace", "kvo_paged_copy"]
 PROFILE_KINDS = ["select", "diff", "coalesce", "gather_prefetch", "gather_urgent", "attention", "recon"]
 
@@ -119,6 +119,8 @@ def lib() -> ctypes.CDLL:
         L.kvo_paged_attn_workspace.argtypes = [PC, I, I, I64, ctypes.POINTER(ctypes.c_size_t)]
         L.kvo_prompt_attn.argtypes = [VP, I64, VP, I64, VP, I64, VP, VP, I, I64, I64, I, I, I, I, VP, VP, VP, VP]
         PB, SZ, SP = ctypes.POINTER(_PageBook), ctypes.c_size_t, ctypes.POINTER(ctypes.c_size_t)
+        L.kvo_paged_chunk_attn.argtypes = [PC, VP, I64, I64, I, VP, VP, I64, I64, VP, VP, VP, SZ, VP, VP]
+        L.kvo_paged_chunk_attn_workspace.argtypes = [PC, I, I64, I64, I64, SP]
         L.kvo_paged_reserve.argtypes = [PB, VP, VP, VP]
         L.kvo_paged_fork.argtypes = [PB, VP, VP, VP, VP, VP, VP, SZ, VP, VP]
         L.kvo_paged_fork_workspace.argtypes = [PB, SP]
@@ -353,6 +355,19 @@ def paged_attn(q, k_pages, v_pages, table, lens, *, k_scale=None, v_scale=None, 
     """
     return (_BINDING or _native()).paged_attn(q, k_pages, v_pages, table, lens, k_scale, v_scale, blocks, counts, max_len,
                                               o, lse, workspace, status, stream)
+
+
+def paged_chunk_attn(q, k_pages, v_pages, table, lens, cu, *, k_scale=None, v_scale=None, max_new: int = 0,
+                     max_len: int = 0, o=None, lse=None, workspace=None, status=None, stream=None):
+    """Attention of new tokens over a paged cache that holds them (C: kvo_paged_chunk_attn) -> (o, lse).
+
+    q: CUDA bf16 [total_q][Hq][d], any token stride; cu: int32 [batch + 1] offsets of each request's new tokens; lens:
+    int32 [batch], the tokens of each request, new ones included; pools, scales and table as in ``paged_append``.
+    max_new, max_len: upper bounds of the new tokens of a request and of lens, where known.  o: bf16 [total_q][Hq][d],
+    lse: fp32 [total_q][Hq].
+    """
+    return (_BINDING or _native()).paged_chunk_attn(q, k_pages, v_pages, table, lens, cu, k_scale, v_scale, max_new,
+                                                    max_len, o, lse, workspace, status, stream)
 
 
 def prompt_attn(q, k, v, cu_q, cu_k=None, causal: bool = True, o=None, lse=None, status=None, stream=None):
