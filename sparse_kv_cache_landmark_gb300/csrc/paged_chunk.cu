@@ -20,9 +20,9 @@
 //
 // e4m3.  K goes to the tensor cores as it is: a row of q, times a power of two that brings its largest value to 2^7..2^8, is
 // the sum of two e4m3 values, exactly for what is at least 2^-9 of that largest and to 2^-17 of it for all below (a bf16
-// value has 8 bits, an e4m3 value 4), and two 8-bit products take the time of one of bf16.  V is widened to bf16, exactly,
-// on its way through shared memory.  A page's k_scale multiplies its scores, its v_scale its weights before they are
-// rounded to bf16; bf16 has fp32's exponents, so scales of any size do.
+// value has 8 bits, an e4m3 value 4), and two 8-bit products take the time of one of bf16.  V is widened to bf16 on its way
+// through shared memory, times its page's v_scale (exactly for powers of two; bf16 has fp32's exponents, so scales of any
+// size do); a page's k_scale multiplies its scores.
 #include <stdio.h>
 
 #include <algorithm>
@@ -54,20 +54,19 @@ struct ChShape<D, false> {
     static constexpr int REGS_SOFTMAX = 208, REGS_OTHER = 88;
     static constexpr int Q = CH_ROWS * D * 2;                   // bytes of a tile of q
     static constexpr int TILE = CH_KEYS * D * 2;                // of K or V
-    static constexpr int STAGES = D == 128 ? 4 : 10;            // K and V in turn
+    static constexpr int KS = D == 128 ? 2 : 4, VS = KS;        // stages of K and of V: even numbers (see `dual`)
     static constexpr int WIDE_BYTES = 0;
-    static constexpr int TILES = 2 * Q + STAGES * TILE;
+    static constexpr int TILES = 2 * Q + (KS + VS) * TILE;
 };
 template <int D>
 struct ChShape<D, true> {
     static constexpr int THREADS = 512;
-    static constexpr int REGS_SOFTMAX = 184, REGS_OTHER = 72;
+    static constexpr int REGS_SOFTMAX = 168, REGS_OTHER = 88;
     static constexpr int Q = 2 * CH_ROWS * D;                   // the two pieces
     static constexpr int TILE = CH_KEYS * D;                    // of K or V as they are
     static constexpr int WIDE_BYTES = CH_KEYS * D * 2;          // of V in bf16
-    static constexpr int STAGES = 6;                            // K and V in turn
-    static constexpr int WIDES = 2;
-    static constexpr int TILES = 2 * Q + STAGES * TILE + WIDES * WIDE_BYTES;
+    static constexpr int KS = 4, VS = 2;
+    static constexpr int TILES = 2 * Q + (KS + VS) * TILE + 2 * WIDE_BYTES;
 };
 
 struct ChunkArgs {
@@ -104,24 +103,35 @@ struct ChunkCut {
 struct ChunkItem {
     int64_t row;
     int32_t n[2];                  // tiles of keys of each tile of rows; n[0] = -1: the end
+    int32_t tiles;                 // of keys in all
+    int32_t dual;                  // one tile of rows only: both take it, with the even and the odd tiles of keys
     int32_t first;                 // tile of keys
     int32_t b, g, tok0, nq, len;
     int32_t part;                  // -1: the whole item; else its place in the workspace
+    // The completions of a tile of rows' products are counted: its scores with the i-th of its tiles of keys (value 0) and
+    // the value product after them (1).  One commit for the next scores stands for a value product as well, where the
+    // other tile's products run meanwhile; a dual item's stages of V would wait for it too long.
+    __device__ __forceinline__ uint32_t event(int i, int value) const { return dual ? 2 * i + value : i + value; }
+    __device__ __forceinline__ uint32_t events(int t) const { return n[t] == 0 ? 0 : event(n[t] - 1, 1) + 1; }
 };
 
 struct ChShared {
-    uint64_t q_full[2], kv_full[10], raw_free[3], wide_full[2], event[2][CH_EVENTS], p_full[2][2], turn[2], drain[2], v_tail, item_full[CH_ITEMS],
-        item_free[CH_ITEMS], sc_full[CH_SCALES];
+    uint64_t q_full[2], k_full[4], v_full[4], raw_free[2], wide_full[2], event[2][CH_EVENTS], p_full[2], turn[2], drain[2], v_tail, item_full[CH_ITEMS],
+        item_free[CH_ITEMS], sc_full[CH_SCALES], ml_there, weights_there, o_read;
     ChunkItem item[CH_ITEMS];
     float k_scale[CH_SCALES][8], v_scale[CH_SCALES][8];
     uint32_t bad[CH_SCALES];       // groups of 16 keys in pages that do not exist
     int8_t q_exp[2][2][CH_ROWS];   // q's pieces are its values times 2^this; CH_NAN: not finite
     uint32_t tmem;
     int abort;
-    int issued, tail_open, tail_phase;
-    // the plan
-    int64_t sum[16], at[2];
-    int32_t top[16], found[2], high[2];
+    int issued, tail_open, tail_phase, q_issued[2];
+    union {
+        struct {                   // the plan
+            int64_t sum[16], at[2];
+            int32_t top[16], found[2], high[2];
+        };
+        float2 share[CH_ROWS];     // the two halves of a dual item: maximum and sum one way, weights the other
+    };
 };
 
 __device__ __forceinline__ bool ch_wait_long(int* abort, int32_t* status, uint32_t bar, uint32_t parity, long long limit) {
@@ -325,178 +335,252 @@ __device__ __forceinline__ ChunkCut ch_cut(const ChShared& sh, const ChunkArgs& 
 // ------------------------------------------------------------------ softmax
 // The softmax of one tile of an item: a thread owns a row; it sees its request's keys [0, limit).  False: a wait gave up.
 template <int D, bool FP8>
-__device__ __forceinline__ bool ch_softmax(ChShared& sh, const ChunkArgs& A, const ChunkItem& I, int t, uint32_t& events, uint32_t& keys,
-                                           int turn) {
+__device__ __forceinline__ bool ch_softmax(ChShared& sh, const ChunkArgs& A, const ChunkItem& I, int t, uint32_t events, uint32_t keys, int turn,
+                                           uint32_t& shares) {
     const uint32_t lanes = (uint32_t)(threadIdx.x & 96) << 16;          // this warp's quarter of the lanes
     const uint32_t S = sh.tmem + 128 * t + lanes, O = sh.tmem + 256 + D * t + lanes;
     const int row = threadIdx.x & 127, tl = row / A.r, head = row - tl * A.r;
-    const int tok = I.tok0 + t * A.tq + tl;
+    const int tok = I.tok0 + (I.dual ? 0 : t * A.tq) + tl;
     const bool real = tl < A.tq && tok < I.nq;
+    const bool any = __any_sync(0xffffffffu, real);
     const int n_tiles = I.n[t];
-    int limit = real ? (int)min(max((int64_t)tok + 1 + (I.len - I.nq), (int64_t)0), (int64_t)I.len) - I.first * CH_KEYS : 0;
+    // a row that is none may see anything
+    const int limit = real ? (int)min(max((int64_t)tok + 1 + (I.len - I.nq), (int64_t)0), (int64_t)I.len) - I.first * CH_KEYS : INT32_MAX;
     float m = -INFINITY, l = 0.f;                                       // log2 units; l in units of 2^m
-    for (int j = 0; j < n_tiles; ++j) {
-        bool ok = ch_event(sh, A, t, events++);
+    float q_scale = A.scale_log2;
+    for (int i = 0; i < n_tiles; ++i) {
+        const int j = I.dual ? 2 * i + t : i;
+        bool ok = ch_event(sh, A, t, events + I.event(i, 0));
         const uint32_t slot = (keys + j) % CH_SCALES;
         ok = ok && ch_wait(sh, A, sh.sc_full[slot], (keys + j) / CH_SCALES);
         if (!__all_sync(0xffffffffu, ok)) return false;
+        if (!any) {                // no rows in this warp: nothing reads what its lanes of P and O hold
+            mbar_arrive(smem_u32(&sh.p_full[t]));
+            continue;
+        }
         tc_fence_after();
-        uint32_t s[CH_KEYS];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) tmem_ld32(S + 32 * i, s + 32 * i);
-        const uint32_t bad = sh.bad[slot];
-        tmem_wait_ld();
-        const int rem = limit - j * CH_KEYS;
-        if (rem < CH_KEYS) {
-#pragma unroll
-            for (int i = 0; i < CH_KEYS; ++i)
-                if (i >= rem) s[i] = 0xFF800000u;                       // -inf
-        }
-        if (bad) {
-#pragma unroll
-            for (int i = 0; i < CH_KEYS; ++i)
-                if (bad >> (i / 16) & 1) s[i] = 0xFF800000u;
-        }
-        float top;
-        float c[FP8 ? 8 : 1];
-        if constexpr (FP8) {
+        if (FP8 && i == 0) {
             const int e = sh.q_exp[turn][t][row];
-            const float q_scale = e == CH_NAN ? __uint_as_float(0x7FC00000u) : __uint_as_float((uint32_t)(127 - e) << 23) * A.scale_log2;
-            float run[8];
-#pragma unroll
-            for (int g = 0; g < 8; ++g) {
-                c[g] = sh.k_scale[slot][g] * q_scale;
-                c[g] = c[g] < 1.2e-38f ? 1.2e-38f : c[g];               // a masked score times zero would be NaN
-                float x = max3(__uint_as_float(s[16 * g]), __uint_as_float(s[16 * g + 1]), __uint_as_float(s[16 * g + 2]));
-                float y = __uint_as_float(s[16 * g + 3]);
-#pragma unroll
-                for (int i = 4; i < 16; i += 4) {
-                    x = max3(x, __uint_as_float(s[16 * g + i]), __uint_as_float(s[16 * g + i + 1]));
-                    y = max3(y, __uint_as_float(s[16 * g + i + 2]), __uint_as_float(s[16 * g + i + 3]));
-                }
-                run[g] = fmaxf(x, y) * c[g];
-            }
-            top = fmaxf(max3(run[0], run[1], run[2]), max3(run[3], run[4], max3(run[5], run[6], run[7])));
-        } else {
-            c[0] = A.scale_log2;
-            float mx[4];
-#pragma unroll
-            for (int e = 0; e < 4; ++e) mx[e] = __uint_as_float(s[e]);
-#pragma unroll
-            for (int i = 4; i + 8 <= CH_KEYS; i += 8)
-#pragma unroll
-                for (int e = 0; e < 4; ++e) mx[e] = max3(mx[e], __uint_as_float(s[i + e]), __uint_as_float(s[i + 4 + e]));
-#pragma unroll
-            for (int e = 0; e < 4; ++e) mx[e] = fmaxf(mx[e], __uint_as_float(s[CH_KEYS - 4 + e]));
-            top = fmaxf(max3(mx[0], mx[1], mx[2]), mx[3]) * A.scale_log2;
+            q_scale = e == CH_NAN ? __uint_as_float(0x7FC00000u) : __uint_as_float((uint32_t)(127 - e) << 23) * A.scale_log2;
         }
-        if (__any_sync(0xffffffffu, top > m + CH_RAISE)) {
-            const float to = fmaxf(m, top);
-            const float f = m == -INFINITY ? 0.f : ex2(m - to);
-            m = to;
-            l *= f;
-            if (j > 0) {           // S(j) complete: so is O += P(j - 1) V, which was issued before it
-#pragma unroll 1
-                for (int x = 0; x < D; x += 32) {
-                    uint32_t o[32];
-                    tmem_ld32(O + x, o);
-                    tmem_wait_ld();
+        const uint32_t bad = sh.bad[slot];
+        const int rem = limit - j * CH_KEYS;
+        auto scale_of = [&](int g) {           // of the g-th 16 scores
+            const float x = FP8 ? sh.k_scale[slot][g] * q_scale : q_scale;
+            return FP8 && x < 1.2e-38f ? 1.2e-38f : x;                  // a masked score times zero would be NaN
+        };
+        auto top_of = [](const uint32_t* x) {
+            float u = fmaxf(__uint_as_float(x[0]), __uint_as_float(x[1])), v = fmaxf(__uint_as_float(x[2]), __uint_as_float(x[3]));
 #pragma unroll
-                    for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
-                    tmem_st32(O + x, o);
-                }
+            for (int e = 4; e < 16; e += 4) {
+                u = max3(u, __uint_as_float(x[e]), __uint_as_float(x[e + 1]));
+                v = max3(v, __uint_as_float(x[e + 2]), __uint_as_float(x[e + 3]));
             }
-        }
-        const float b = m == -INFINITY ? 0.f : -m;
-        const uint64_t b2 = pack2(b, b);
+            return fmaxf(u, v);
+        };
+        // 16 scores to weights, two to a word.
+        auto weights = [&](const uint32_t* x, uint32_t* p, float scale, float b, uint64_t (&sum)[2]) {
+            const uint64_t scale2 = pack2(scale, scale), b2 = pack2(b, b);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                float u, v;
+                unpack2(fma2(pack2(__uint_as_float(x[2 * e]), __uint_as_float(x[2 * e + 1])), scale2, b2), u, v);
+                u = ex2(u);
+                v = ex2(v);
+                sum[e & 1] = add2(sum[e & 1], pack2(u, v));
+                const __nv_bfloat162 y = __floats2bfloat162_rn(u, v);
+                p[e] = *reinterpret_cast<const uint32_t*>(&y);
+            }
+        };
         uint64_t sum[2] = {0ull, 0ull};
+        // Most tiles: every key seen, no score far above the maximum so far.  One pass, and the weights go over the scores
+        // only once that is known.
+        bool done = false;
+        if (i > 0 && !bad && !__any_sync(0xffffffffu, rem < CH_KEYS)) {
+            uint32_t p[CH_KEYS / 2], x[2][32];
+            const float b = m == -INFINITY ? 0.f : -m;
+            float top = -INFINITY;
+            tmem_ld32(S, x[0]);
+            tmem_wait_ld();
 #pragma unroll
-        for (int h = 0; h < 4; ++h) {
-            uint32_t p[16];
+            for (int c = 0; c < 4; ++c) {
+                if (c < 3) tmem_ld32(S + 32 * c + 32, x[(c & 1) ^ 1]);
 #pragma unroll
-            for (int i = 0; i < 16; ++i) {
-                const float cc = c[FP8 ? 2 * h + i / 8 : 0];
-                float x, y;
-                unpack2(fma2(pack2(__uint_as_float(s[32 * h + 2 * i]), __uint_as_float(s[32 * h + 2 * i + 1])), pack2(cc, cc), b2), x, y);
-                x = ex2(x);
-                y = ex2(y);
-                uint64_t w = pack2(x, y);
-                sum[i & 1] = add2(sum[i & 1], w);
-                if constexpr (FP8) {
-                    const float vs = sh.v_scale[slot][2 * h + i / 8];
-                    unpack2(mul2(w, pack2(vs, vs)), x, y);
+                for (int g = 0; g < 2; ++g) {
+                    const float scale = scale_of(2 * c + g);
+                    weights(x[c & 1] + 16 * g, p + 16 * c + 8 * g, scale, b, sum);
+                    top = fmaxf(top, top_of(x[c & 1] + 16 * g) * scale);
                 }
-                const __nv_bfloat162 v = __floats2bfloat162_rn(x, y);
-                p[i] = *reinterpret_cast<const uint32_t*>(&v);
+                if (c < 3) tmem_wait_ld();
             }
-            tmem_st16(S + 16 * h, p);
-            if (h & 1) {           // half of the weights are there: the value product may begin on them
-                tmem_wait_st();
-                tc_fence_before();
-                mbar_arrive(smem_u32(&sh.p_full[t][h >> 1]));
+            done = !__any_sync(0xffffffffu, top > m + CH_RAISE);
+            if (done) {
+                tmem_st32(S, p);
+                tmem_st32(S + 32, p + 32);
+            } else {
+                sum[0] = sum[1] = 0ull;
             }
         }
+        if (!done) {               // first the maximum, then the weights, over scores that have been read
+            uint32_t x[32], p[16];
+            auto fetch = [&](int c) {
+                tmem_ld32(S + 32 * c, x);
+                tmem_wait_ld();
+                if (rem < 32 * c + 32) {
+#pragma unroll
+                    for (int e = 0; e < 32; ++e)
+                        if (32 * c + e >= rem) x[e] = 0xFF800000u;      // -inf
+                }
+                if (bad >> 2 * c & 3) {
+#pragma unroll
+                    for (int e = 0; e < 32; ++e)
+                        if (bad >> (2 * c + e / 16) & 1) x[e] = 0xFF800000u;
+                }
+            };
+            float top = -INFINITY;
+#pragma unroll 1
+            for (int c = 0; c < 4; ++c) {
+                fetch(c);
+#pragma unroll
+                for (int g = 0; g < 2; ++g) top = fmaxf(top, top_of(x + 16 * g) * scale_of(2 * c + g));
+            }
+            if (__any_sync(0xffffffffu, top > m + CH_RAISE)) {
+                const float to = fmaxf(m, top);
+                const float f = m == -INFINITY ? 0.f : ex2(m - to);
+                m = to;
+                l *= f;
+                if (i > 0) {       // these scores are complete: so is the value product that was issued before them
+#pragma unroll 1
+                    for (int c = 0; c < D; c += 32) {
+                        tmem_ld32(O + c, x);
+                        tmem_wait_ld();
+#pragma unroll
+                        for (int e = 0; e < 32; ++e) x[e] = __float_as_uint(__uint_as_float(x[e]) * f);
+                        tmem_st32(O + c, x);
+                    }
+                }
+            }
+            const float b = m == -INFINITY ? 0.f : -m;
+#pragma unroll 1
+            for (int c = 0; c < 4; ++c) {
+                fetch(c);
+#pragma unroll
+                for (int g = 0; g < 2; ++g) weights(x + 16 * g, p + 8 * g, scale_of(2 * c + g), b, sum);
+                tmem_st16(S + 16 * c, p);
+            }
+        }
+        tmem_wait_st();
+        tc_fence_before();
+        mbar_arrive(smem_u32(&sh.p_full[t]));
         float s0, s1;
         unpack2(add2(sum[0], sum[1]), s0, s1);
         l += s0 + s1;
     }
-    keys += max(I.n[0], I.n[1]);
     if (n_tiles > 0) {
-        const bool ok = ch_event(sh, A, t, events++);
+        const bool ok = ch_event(sh, A, t, events + I.event(n_tiles - 1, 1));
         if (!__all_sync(0xffffffffu, ok)) return false;
         tc_fence_after();
     }
-    if (I.part >= 0) {             // a part of the item, for the join
-        const int64_t at = (int64_t)I.part * A.tiles + t;
-        float4* to = reinterpret_cast<float4*>(A.part_o) + at * (D / 4) * CH_ROWS + row;
-        if (n_tiles > 0) {
+    // A dual item's halves: this thread writes half of the row's values, from both.
+    const bool both = I.dual && I.n[1] > 0;
+    float w0 = t == 0 ? 1.f : 0.f, w1 = 1.f - w0;              // weights of the tiles' sums
+    if (both) {
+        bool ok = true;
+        if (t == 1) {
+            sh.share[row] = make_float2(m, l);
+            mbar_arrive(smem_u32(&sh.ml_there));
+            ok = ch_wait(sh, A, sh.weights_there, shares);
+            if (!__all_sync(0xffffffffu, ok)) return false;
+            const float2 x = sh.share[row];
+            w0 = x.x;
+            w1 = x.y;
+        } else {
+            ok = ch_wait(sh, A, sh.ml_there, shares);
+            if (!__all_sync(0xffffffffu, ok)) return false;
+            const float2 x = sh.share[row];
+            const float to = fmaxf(l != 0.f ? m : -INFINITY, x.y != 0.f ? x.x : -INFINITY);
+            w0 = l != 0.f ? ex2(m - to) : 0.f;                 // one that saw nothing has weight 0
+            w1 = x.y != 0.f ? ex2(x.x - to) : 0.f;
+            l = (l != 0.f ? w0 * l : 0.f) + (x.y != 0.f ? w1 * x.y : 0.f);
+            m = to;
+            if (I.part < 0) {
+                const float inv = l != 0.f ? 1.f / l : 0.f;
+                w0 *= inv;
+                w1 *= inv;
+            }
+            sh.share[row] = make_float2(w0, w1);
+            mbar_arrive(smem_u32(&sh.weights_there));
+        }
+        ++shares;
+    } else if (I.part < 0) {
+        const float inv = l != 0.f ? 1.f / l : 0.f;
+        w0 *= inv;
+        w1 *= inv;
+    }
+    if (I.dual && !both && t == 1) return true;
+    const int tile = I.dual ? 0 : t, col0 = both ? t * (D / 2) : 0, cols = both ? D / 2 : D;
+    const bool some = both || n_tiles > 0;
+    const int64_t at = I.part >= 0 ? (int64_t)I.part * A.tiles + tile : 0, out = (I.row + tok) * A.hq + I.g * A.r + head;
+    const uint32_t O0 = sh.tmem + 256 + lanes, O1 = O0 + D;
+    if (any)
 #pragma unroll 1
-            for (int x = 0; x < D; x += 32) {
-                uint32_t o[32];
-                tmem_ld32(O + x, o);
+        for (int x = col0; x < col0 + cols; x += 32) {
+            uint32_t o[32];
+            if (some) {
+                tmem_ld32((both || t == 0 ? O0 : O1) + x, o);
                 tmem_wait_ld();
+                // a row that saw nothing is zero, whatever its lane of tensor memory holds
+                const float f = both || t == 0 ? w0 : w1;
+#pragma unroll
+                for (int i = 0; i < 32; ++i) o[i] = f != 0.f ? __float_as_uint(__uint_as_float(o[i]) * f) : 0u;
+                if (both) {
+                    uint32_t o1[32];
+                    tmem_ld32(O1 + x, o1);
+                    tmem_wait_ld();
+#pragma unroll
+                    for (int i = 0; i < 32; ++i)
+                        if (w1 != 0.f) o[i] = __float_as_uint(fmaf(w1, __uint_as_float(o1[i]), __uint_as_float(o[i])));
+                }
+            } else {
+#pragma unroll
+                for (int i = 0; i < 32; ++i) o[i] = 0u;
+            }
+            if (I.part >= 0) {     // a part of the item, for the join
+                float4* to = reinterpret_cast<float4*>(A.part_o) + (at * (D / 4) + x / 4) * CH_ROWS + row;
 #pragma unroll
                 for (int i = 0; i < 32; i += 4)
                     if (real)
-                        to[(x + i) / 4 * CH_ROWS] = make_float4(__uint_as_float(o[i]), __uint_as_float(o[i + 1]), __uint_as_float(o[i + 2]),
-                                                               __uint_as_float(o[i + 3]));
+                        to[i / 4 * CH_ROWS] = make_float4(__uint_as_float(o[i]), __uint_as_float(o[i + 1]), __uint_as_float(o[i + 2]), __uint_as_float(o[i + 3]));
+            } else {
+                uint4* to = reinterpret_cast<uint4*>(A.o + out * D + x);
+#pragma unroll
+                for (int i = 0; i < 32; i += 8) {
+                    uint32_t y[4];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const __nv_bfloat162 v = __floats2bfloat162_rn(__uint_as_float(o[i + 2 * e]), __uint_as_float(o[i + 2 * e + 1]));
+                        y[e] = *reinterpret_cast<const uint32_t*>(&v);
+                    }
+                    if (real) to[i / 8] = make_uint4(y[0], y[1], y[2], y[3]);
+                }
             }
         }
-        if (real) A.part_ml[at * CH_ROWS + row] = make_float2(m, l);
-        return true;
+    if (both) {                    // the next item's value products may go over these sums
+        tc_fence_before();
+        mbar_arrive(smem_u32(&sh.o_read));
     }
-    const float inv = l != 0.f ? 1.f / l : 0.f;
-    const int64_t out = (I.row + tok) * A.hq + I.g * A.r + head;
-    uint4* to = reinterpret_cast<uint4*>(A.o + out * D);
-#pragma unroll 1
-    for (int x = 0; x < D; x += 32) {
-        uint32_t o[32];
-        if (n_tiles > 0) {
-            tmem_ld32(O + x, o);
-            tmem_wait_ld();
-        }
-#pragma unroll
-        for (int i = 0; i < 32; i += 8) {
-            uint32_t w[4];
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                // a row that saw nothing is zero, whatever its lane of tensor memory holds
-                const float a = l != 0.f ? __uint_as_float(o[i + 2 * e]) * inv : 0.f;
-                const float d = l != 0.f ? __uint_as_float(o[i + 2 * e + 1]) * inv : 0.f;
-                const __nv_bfloat162 v = __floats2bfloat162_rn(a, d);
-                w[e] = *reinterpret_cast<const uint32_t*>(&v);
-            }
-            if (real) to[(x + i) / 8] = make_uint4(w[0], w[1], w[2], w[3]);
-        }
+    if (real && (!both || t == 0)) {
+        if (I.part >= 0) A.part_ml[at * CH_ROWS + row] = make_float2(m, l);
+        else if (A.lse) A.lse[out] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
     }
-    if (real && A.lse) A.lse[out] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
     return true;
 }
 
 // ------------------------------------------------------------------ q and V of 8-bit pages
-// Row `row` of tile t of an item's q as the sum of two e4m3 pieces; times 2^*exponent.
+// Row `row` of tile t of an item's q as the sum of two e4m3 pieces; times 2^*exponent.  `too`, if not NULL,
+// gets the same.
 template <int D>
-__device__ __forceinline__ void ch_split_q(const ChunkArgs& A, const ChunkItem& I, int t, int row, uint8_t* to, int8_t* exponent) {
+__device__ __forceinline__ void ch_split_q(const ChunkArgs& A, const ChunkItem& I, int t, int row, uint8_t* to, uint8_t* too, int8_t* exponent) {
     const int tl = row / A.r, head = row - tl * A.r, tok = I.tok0 + t * A.tq + tl;
     const bool real = tl < A.tq && tok < I.nq;
     const uint4* q = reinterpret_cast<const uint4*>(A.q + (I.row + tok) * A.q_stride + (int64_t)(I.g * A.r + head) * D);
@@ -537,25 +621,33 @@ __device__ __forceinline__ void ch_split_q(const ChunkArgs& A, const ChunkItem& 
         const int at = row * D + (D == 128 ? c ^ (row & 7) : c ^ (row >> 1 & 3)) * 16;
         *reinterpret_cast<uint4*>(to + at) = make_uint4(a[0], a[1], a[2], a[3]);
         *reinterpret_cast<uint4*>(to + CH_ROWS * D + at) = make_uint4(b[0], b[1], b[2], b[3]);
+        if (too) {
+            *reinterpret_cast<uint4*>(too + at) = make_uint4(a[0], a[1], a[2], a[3]);
+            *reinterpret_cast<uint4*>(too + CH_ROWS * D + at) = make_uint4(b[0], b[1], b[2], b[3]);
+        }
     }
 }
-// A tile of V from its codes to bf16, by 128 threads; rows from `have` on become zero, as a weight of zero does not silence
-// the NaN that may lie there.
+// A tile of V from its codes, times their pages' scales, to bf16, by 128 threads; rows from `have` on become zero, as a weight
+// of zero does not silence the NaN that may lie there.
 template <int D>
-__device__ __forceinline__ void ch_widen_v(const uint8_t* from, uint8_t* to, int have) {
+__device__ __forceinline__ void ch_widen_v(const uint8_t* from, uint8_t* to, const float* scales, int have) {
     constexpr int CH = D / 16;
 #pragma unroll 4
     for (int k = 0; k < CH; ++k) {
         const int idx = k * 128 + (threadIdx.x & 127), row = idx / CH, c = idx % CH;
         uint4 v = *reinterpret_cast<const uint4*>(from + row * D + (D == 128 ? c ^ (row & 7) : c ^ (row >> 1 & 3)) * 16);
         if (row >= have) v = make_uint4(0, 0, 0, 0);
+        const float scale = scales[row / 16];
+        const uint64_t scale2 = pack2(scale, scale);
         const uint32_t w[4] = {v.x, v.y, v.z, v.w};
         uint32_t o[8];
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
             const uint32_t f = e4m3x2_to_f16x2((uint16_t)(w[i / 2] >> (i & 1) * 16));
             const float2 x = __half22float2(*reinterpret_cast<const __half2*>(&f));
-            const __nv_bfloat162 b = __floats2bfloat162_rn(x.x, x.y);
+            float y, z;
+            unpack2(mul2(pack2(x.x, x.y), scale2), y, z);
+            const __nv_bfloat162 b = __floats2bfloat162_rn(y, z);
             o[i] = *reinterpret_cast<const uint32_t*>(&b);
         }
         uint8_t* at = to + (c / 4) * CH_BLOCK + row * 128;
@@ -574,20 +666,23 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
     extern __shared__ __align__(1024) uint8_t smem[];           // the tiles, then ChShared
     ChShared& sh = *reinterpret_cast<ChShared*>(smem + P::TILES);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const uint32_t base = smem_u32(smem), ring = base + 2 * P::Q;
-    constexpr uint32_t WIDE0 = 2 * P::Q + P::STAGES * P::TILE;
+    const uint32_t base = smem_u32(smem);
+    constexpr uint32_t K0 = 2 * P::Q, V0 = K0 + P::KS * P::TILE, WIDE0 = V0 + P::VS * P::TILE;
     if (tid == 0) {
         if (!FP8) tensor_map_prefetch(&map_q);
         tensor_map_prefetch(&map_k);
         tensor_map_prefetch(&map_v);
-        for (int i = 0; i < P::STAGES; ++i) mbar_init(smem_u32(&sh.kv_full[i]), 1);
-        for (int i = 0; i < 3; ++i) mbar_init(smem_u32(&sh.raw_free[i]), 4);
+        for (int i = 0; i < P::KS; ++i) mbar_init(smem_u32(&sh.k_full[i]), 1);
+        for (int i = 0; i < P::VS; ++i) mbar_init(smem_u32(&sh.v_full[i]), 1);
+        for (int i = 0; i < 2; ++i) mbar_init(smem_u32(&sh.raw_free[i]), 4);
         for (int i = 0; i < 2; ++i) mbar_init(smem_u32(&sh.wide_full[i]), 4);
+        mbar_init(smem_u32(&sh.ml_there), 128);
+        mbar_init(smem_u32(&sh.weights_there), 128);
+        mbar_init(smem_u32(&sh.o_read), 256);
         for (int t = 0; t < 2; ++t) {
             mbar_init(smem_u32(&sh.q_full[t]), FP8 ? 4 : 1);
             for (int i = 0; i < CH_EVENTS; ++i) mbar_init(smem_u32(&sh.event[t][i]), 1);
-            mbar_init(smem_u32(&sh.p_full[t][0]), 128);
-            mbar_init(smem_u32(&sh.p_full[t][1]), 128);
+            mbar_init(smem_u32(&sh.p_full[t]), 128);
             mbar_init(smem_u32(&sh.turn[t]), 1);
             mbar_init(smem_u32(&sh.drain[t]), 1);
         }
@@ -597,7 +692,7 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
             mbar_init(smem_u32(&sh.item_free[i]), FP8 ? 14 : 10);
         }
         for (int i = 0; i < CH_SCALES; ++i) mbar_init(smem_u32(&sh.sc_full[i]), 1);
-        sh.abort = sh.issued = sh.tail_open = sh.tail_phase = 0;
+        sh.abort = sh.issued = sh.tail_open = sh.tail_phase = sh.q_issued[0] = sh.q_issued[1] = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
     grid_wait();
@@ -636,10 +731,10 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
             __syncwarp();
             bool ok = true, tail_open = false;
             uint32_t k = 0, tail_phase = 0, tiles = 0;
-            int issued = 0;
+            int issued = 0;                             // loads: K and V of each tile in turn
             uint32_t events[2] = {0, 0}, q_issued[2] = {0, 0};
             uint32_t q_free[2] = {~0u, ~0u};            // the event after which a tile's q may be overwritten
-            uint32_t e0 = ~0u, e1 = ~0u;                // of stage `lane`: the events that free it
+            uint32_t e0 = ~0u, e1 = ~0u;                // of stage `lane` of K, or `lane - 16` of V: the events that free it
             const int rows = A.n_pages * A.hkv * A.page, chunks = A.page / 16;
             constexpr int ROW = D * (FP8 ? 1 : 2), BOXES = ROW > 128 ? ROW / 128 : 1, BOX = ROW > 128 ? 128 : ROW;
             const int boxes = CH_KEYS / A.page * BOXES;
@@ -654,8 +749,10 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
                     ChunkItem I;
                     I.row = walk.r.a;
                     I.first = first;
-                    I.n[0] = min(max(n_all[0] - first, 0), last - first);
-                    I.n[1] = min(max(n_all[1] - first, 0), last - first);
+                    I.dual = walk.r.n - walk.i * 2 * A.tq <= A.tq;
+                    I.tiles = last - first;
+                    I.n[0] = I.dual ? (I.tiles + 1) / 2 : min(max(n_all[0] - first, 0), I.tiles);
+                    I.n[1] = I.dual ? I.tiles / 2 : min(max(n_all[1] - first, 0), I.tiles);
                     I.b = walk.b;
                     I.g = walk.g;
                     I.tok0 = walk.i * 2 * A.tq;
@@ -669,7 +766,7 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
                         mbar_arrive(smem_u32(&sh.item_full[k % CH_ITEMS]));
                     }
                     ++k;
-                    const int n = max(I.n[0], I.n[1]);
+                    const int n = I.tiles;
                     const int32_t* table = A.table + (int64_t)I.b * A.max_pages;
                     // Lane: the (lane % 8)-th 16 keys of tile lane / 8 of four.
                     auto page_of = [&](int j) {
@@ -699,13 +796,13 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
                         const int y = from < 0 ? rows : (from * A.hkv + I.g) * A.page;
                         const int key0 = (I.first + j) * CH_KEYS;
                         for (int v = 0; v < 2; ++v) {
-                            const int st = issued % P::STAGES;
-                            if (issued >= P::STAGES) {
+                            const int st = tiles % (v ? P::VS : P::KS), stages = v ? P::VS : P::KS, holder = st + 16 * v;
+                            if (tiles >= stages) {
                                 if (FP8 && v) {
-                                    ok = ch_wait(sh, A, sh.raw_free[st / 2], issued / P::STAGES - 1);
+                                    ok = ch_wait(sh, A, sh.raw_free[st], tiles / stages - 1);
                                 } else {
-                                    ok = event_wait(0, __shfl_sync(0xffffffffu, e0, st));
-                                    ok = event_wait(1, __shfl_sync(0xffffffffu, e1, st)) && ok;
+                                    ok = event_wait(0, __shfl_sync(0xffffffffu, e0, holder));
+                                    ok = event_wait(1, __shfl_sync(0xffffffffu, e1, holder)) && ok;
                                 }
                                 if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
                             }
@@ -723,7 +820,8 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
                             // The last tile of a request runs into what lies behind it in its page.  Its keys are masked as
                             // scores, but a weight of zero does not silence a NaN or an infinity in V: those rows are cleared.
                             const bool tail = !FP8 && v && key0 + CH_KEYS > I.len;
-                            const uint32_t bar = smem_u32(tail ? &sh.v_tail : &sh.kv_full[st]), dst = ring + st * P::TILE;
+                            const uint32_t full = smem_u32(v ? &sh.v_full[st] : &sh.k_full[st]), bar = tail ? smem_u32(&sh.v_tail) : full;
+                            const uint32_t dst = base + (v ? V0 : K0) + st * P::TILE;
                             if (lane == 0) mbar_expect_tx(bar, P::TILE);
                             __syncwarp();
                             if (lane < boxes && issued != A.skip)
@@ -740,11 +838,12 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
                                         asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(dst + x * CH_BLOCK + a), "r"(0) : "memory");
                                 fence_async_smem();
                                 __syncwarp();
-                                if (lane == 0) mbar_arrive(smem_u32(&sh.kv_full[st]));
+                                if (lane == 0) mbar_arrive(full);
                             }
-                            if (lane == st) {
-                                e0 = j < I.n[0] ? events[0] + j + v : ~0u;
-                                e1 = j < I.n[1] ? events[1] + j + v : ~0u;
+                            if (lane == holder) {
+                                const int i = I.dual ? j >> 1 : j;
+                                e0 = (I.dual ? !(j & 1) : j < I.n[0]) ? events[0] + I.event(i, v) : ~0u;
+                                e1 = (I.dual ? j & 1 : j < I.n[1]) ? events[1] + I.event(i, v) : ~0u;
                             }
                             ++issued;
                             if (!FP8 && j == 0 && v == 0)
@@ -755,7 +854,7 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
                                     if (lane == 0) {
                                         mbar_expect_tx(smem_u32(&sh.q_full[t]), (uint32_t)((D / 64) * 128 * A.r * A.tq));
                                         for (int x = 0; x < D / 64; ++x)
-                                            tma_load_3d(base + t * P::Q + x * CH_BLOCK, &map_q, 64 * x, I.g * A.r, (int)I.row + I.tok0 + t * A.tq,
+                                            tma_load_3d(base + t * P::Q + x * CH_BLOCK, &map_q, 64 * x, I.g * A.r, (int)I.row + I.tok0 + (I.dual ? 0 : t * A.tq),
                                                         smem_u32(&sh.q_full[t]));
                                     }
                                     ++q_issued[t];
@@ -766,8 +865,8 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
                     }
                     for (int t = 0; t < 2; ++t)
                         if (I.n[t]) {
-                            q_free[t] = events[t] + I.n[t] - 1;
-                            events[t] += I.n[t] + 1;
+                            q_free[t] = events[t] + I.event(I.n[t] - 1, 0);
+                            events[t] += I.events(t);
                         }
                 }
                 walk.start += walk.cost;
@@ -801,7 +900,7 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
             // Where somebody gave up not all loads may have landed: the warp that issued them stays until they have, and
             // with it the CTA and its shared memory.  (`abort` is final only once all have left their waits: below.)
             __syncwarp();
-            if (lane == 0) { sh.found[0] = q_issued[0]; sh.found[1] = q_issued[1]; }
+            if (lane == 0) { sh.q_issued[0] = q_issued[0]; sh.q_issued[1] = q_issued[1]; }
         } else if ((warp == 8 || warp == 10) && lane == 0) {
             // ------------------------------------------------ matrix products of one tile
             // The tensor cores queue a few instructions only; with a thread of its own for each tile, one tile's waits and
@@ -811,33 +910,25 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
             const uint32_t S = sh.tmem + 128 * t, O = sh.tmem + 256 + D * t;
             constexpr bool HALF = FP8 && D == 64;              // rows of 64 bytes
             const uint64_t q = HALF ? smem_desc64(base + t * P::Q) : smem_desc(base + t * P::Q, 16);
-            const uint64_t k0 = HALF ? smem_desc64(ring) : smem_desc(ring, 16);
-            const uint64_t v0 = smem_desc(FP8 ? base + WIDE0 : ring, CH_BLOCK);
-            uint32_t item = 0, events = 0, events_other = 0, weights = 0, qs = 0, turns = 0, tiles = 0;
-            bool ok = true, behind = false;
+            const uint64_t k0 = HALF ? smem_desc64(base + K0) : smem_desc(base + K0, 16);
+            const uint64_t v0 = smem_desc(base + (FP8 ? WIDE0 : V0), CH_BLOCK);
+            uint32_t item = 0, events = 0, events_other = 0, weights = 0, qs = 0, turns = 0, tiles = 0, shares = 0;
+            bool ok = true, behind = false, shared = false;
             while (true) {
                 ChunkItem I;
                 if (!next_item(item, I)) break;
                 free_item(item++);
                 if (I.n[0] < 0) break;
-                const int n_mine = I.n[t], n_other = I.n[t ^ 1], n = max(n_mine, n_other);
-                auto stage = [&](int load, uint32_t& phase) {
-                    phase = load / P::STAGES;
-                    return load % P::STAGES;
+                const int n_mine = I.n[t], n_other = I.n[t ^ 1];
+                const bool turn = !I.dual && n_other > 0;
+                // The i-th tile of keys of this tile of rows, counted over all items.
+                auto at = [&](int i) { return tiles + (I.dual ? 2 * i + t : i); };
+                auto keys_there = [&](int i) { return ch_wait(sh, A, sh.k_full[at(i) % P::KS], at(i) / P::KS); };
+                auto values_there = [&](int i) {
+                    return FP8 ? ch_wait(sh, A, sh.wide_full[at(i) % 2], at(i) / 2) : ch_wait(sh, A, sh.v_full[at(i) % P::VS], at(i) / P::VS);
                 };
-                auto keys_there = [&](int j) {
-                    uint32_t phase;
-                    const int st = stage(2 * (tiles + j), phase);
-                    return ch_wait(sh, A, sh.kv_full[st], phase);
-                };
-                auto values_there = [&](int j) {
-                    uint32_t phase;
-                    if (FP8) return ch_wait(sh, A, sh.wide_full[(tiles + j) % 2], (tiles + j) / 2);
-                    const int st = stage(2 * (tiles + j) + 1, phase);
-                    return ch_wait(sh, A, sh.kv_full[st], phase);
-                };
-                auto scores = [&](int j, bool pass) {
-                    const uint64_t kd = k0 + (uint64_t)((2 * (tiles + j)) % P::STAGES) * (P::TILE >> 4);
+                auto scores = [&](int i, bool pass) {
+                    const uint64_t kd = k0 + (uint64_t)(at(i) % P::KS) * (P::TILE >> 4);
                     constexpr int STEPS = FP8 ? 2 * (D / 32) : D / 16;
 #pragma unroll
                     for (int e = 0; e < STEPS; ++e) {
@@ -850,7 +941,7 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
                             mma_ss(S, q + off, kd + off, ID_S, e > 0);
                         }
                     }
-                    tc_commit(smem_u32(&sh.event[t][(events + j) % CH_EVENTS]));
+                    tc_commit(smem_u32(&sh.event[t][(events + I.event(i, 0)) % CH_EVENTS]));
                 };
                 if (n_mine > 0) {
                     // Tiles that only the other one used: their loads have landed once its products are complete (a barrier's
@@ -861,39 +952,35 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
                     if (!ok) break;
                     tc_fence_after();
                     scores(0, false);
-                    for (int j = 0; j < n_mine; ++j) {
-                        if (!(ok = values_there(j))) break;
-                        if (j + 1 < n_mine && !(ok = keys_there(j + 1))) break;
-                        const uint64_t v = v0 + (uint64_t)(FP8 ? (tiles + j) % 2 * (P::WIDE_BYTES >> 4) : (2 * (tiles + j) + 1) % P::STAGES * (P::TILE >> 4));
+                    for (int i = 0; i < n_mine; ++i) {
+                        if (!(ok = values_there(i))) break;
+                        if (i + 1 < n_mine && !(ok = keys_there(i + 1))) break;
+                        const uint64_t v = v0 + (uint64_t)(FP8 ? at(i) % 2 * (P::WIDE_BYTES >> 4) : at(i) % P::VS * (P::TILE >> 4));
+                        if (!(ok = ch_wait(sh, A, sh.p_full[t], weights))) break;
+                        // Both halves of the last dual item have been read.
+                        if (shared && !(ok = ch_wait(sh, A, sh.o_read, shares - 1))) break;
+                        shared = false;
+                        // The other tile's round before this one; that may be the last of an item before.  No phase is
+                        // passed over.
+                        const int x = t ? i : i - 1;
+                        if (turn && x < n_other && turns + x != ~0u && !(ok = ch_wait(sh, A, sh.turn[t], turns + x))) break;
+                        tc_fence_after();
 #pragma unroll
-                        for (int h = 0; h < 2; ++h) {        // in two halves of the keys, each as its weights come
-                            if (!ok || !(ok = ch_wait(sh, A, sh.p_full[t][h], weights))) break;
-                            if (h == 0) {
-                                const int x = t ? j : j - 1;             // the other tile's round before this one
-                                if (x >= 0 && x < n_other && !(ok = ch_wait(sh, A, sh.turn[t], turns + x))) break;
-                            }
-                            tc_fence_after();
-#pragma unroll
-                            for (int e = 4 * h; e < 4 * h + 4; ++e)
-                                mma_ts(O, S + 8 * e, v + e * (2048 >> 4), ID_O, j > 0 || e > 0);
-                        }
-                        if (!ok) break;
+                        for (int e = 0; e < 8; ++e) mma_ts(O, S + 8 * e, v + e * (2048 >> 4), ID_O, i > 0 || e > 0);
                         ++weights;
-                        // One commit for the scores stands for the value product before them as well.
-                        if (j + 1 < n_mine) {
-                            scores(j + 1, n_other > 0);
-                        } else {
-                            tc_commit(smem_u32(&sh.event[t][(events + n_mine) % CH_EVENTS]));
-                            if (n_other > 0) mbar_arrive(smem_u32(&sh.turn[t ^ 1]));
-                        }
+                        const bool more = i + 1 < n_mine;
+                        if (!more || I.dual) tc_commit(smem_u32(&sh.event[t][(events + I.event(i, 1)) % CH_EVENTS]));
+                        if (more) scores(i + 1, turn);
+                        else if (turn) mbar_arrive(smem_u32(&sh.turn[t ^ 1]));
                     }
                     if (!ok) break;
-                    events += n_mine + 1;
-                    if (n_other > 0) turns += n_other;
+                    events += I.events(t);
+                    if (turn) turns += n_other;
                 }
-                if (n_other > n_mine) behind = true;
-                if (n_other > 0) events_other += n_other + 1;
-                tiles += n;
+                if (I.dual ? n_other > 0 : n_other > n_mine) behind = true;
+                events_other += I.events(t ^ 1);
+                if (I.dual && I.n[1] > 0) { shared = true; ++shares; }
+                tiles += I.tiles;
             }
             // nothing of this CTA may be in flight when it leaves
             tc_commit(smem_u32(&sh.drain[t]));
@@ -904,7 +991,7 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
         } else if (FP8 && warp >= 12) {
             // ------------------------------------------------ q and V of 8-bit pages
             if constexpr (FP8) {
-                uint32_t item = 0, tiles = 0, events[2] = {0, 0}, q_free[2] = {~0u, ~0u}, wide_free[2][2] = {{~0u, ~0u}, {~0u, ~0u}};
+                uint32_t item = 0, tiles = 0, turn[2] = {0, 0}, events[2] = {0, 0}, q_free[2] = {~0u, ~0u}, wide_free[2][2] = {{~0u, ~0u}, {~0u, ~0u}};
                 const int row = tid & 127;
                 bool ok = true;
                 while (ok) {
@@ -914,35 +1001,41 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
                     if (lane == 0) free_item(item);
                     if (I.n[0] < 0) break;
                     for (int t = 0; t < 2 && ok; ++t) {
-                        if (I.n[t] == 0) continue;
+                        const bool copy = I.dual && I.n[1] > 0;             // both take the same rows
+                        if (I.n[t] == 0 || (copy && t == 1)) continue;
                         if (q_free[t] != ~0u) ok = ch_event(sh, A, t, q_free[t]);
+                        if (copy && ok && q_free[1] != ~0u) ok = ch_event(sh, A, 1, q_free[1]);
                         if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
-                        ch_split_q<D>(A, I, t, row, smem + t * P::Q, &sh.q_exp[item & 1][t][row]);
+                        int8_t* const exponent = &sh.q_exp[turn[t]++ & 1][t][row];
+                        ch_split_q<D>(A, I, t, row, smem + t * P::Q, copy ? smem + P::Q : nullptr, exponent);
+                        if (copy) sh.q_exp[turn[1]++ & 1][1][row] = *exponent;
                         fence_async_smem();
                         __syncwarp();
-                        if (lane == 0) mbar_arrive(smem_u32(&sh.q_full[t]));
+                        if (lane == 0) {
+                            mbar_arrive(smem_u32(&sh.q_full[t]));
+                            if (copy) mbar_arrive(smem_u32(&sh.q_full[1]));
+                        }
                     }
                     ++item;
-                    const int n = max(I.n[0], I.n[1]);
-                    for (int j = 0; j < n && ok; ++j) {
-                        const uint32_t load = 2 * tiles + 1, st = load % P::STAGES;
-                        const int w = tiles % 2;
-                        ok = ch_wait(sh, A, sh.kv_full[st], load / P::STAGES);
+                    for (int j = 0; j < I.tiles && ok; ++j) {
+                        const int st = tiles % P::VS, w = tiles % 2, sc = tiles % CH_SCALES;
+                        ok = ch_wait(sh, A, sh.v_full[st], tiles / P::VS) && ch_wait(sh, A, sh.sc_full[sc], tiles / CH_SCALES);
                         for (int t = 0; t < 2; ++t) {
                             const uint32_t e = w ? wide_free[1][t] : wide_free[0][t];
                             if (ok && e != ~0u) ok = ch_event(sh, A, t, e);
                         }
                         if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
-                        ch_widen_v<D>(smem + 2 * P::Q + st * P::TILE, smem + WIDE0 + w * P::WIDE_BYTES, I.len - (I.first + j) * CH_KEYS);
+                        ch_widen_v<D>(smem + V0 + st * P::TILE, smem + WIDE0 + w * P::WIDE_BYTES, sh.v_scale[sc], I.len - (I.first + j) * CH_KEYS);
                         fence_async_smem();
                         __syncwarp();
                         if (lane == 0) {
-                            mbar_arrive(smem_u32(&sh.raw_free[st / 2]));
+                            mbar_arrive(smem_u32(&sh.raw_free[st]));
                             mbar_arrive(smem_u32(&sh.wide_full[w]));
                         }
+                        const int i = I.dual ? j >> 1 : j;
 #pragma unroll
                         for (int t = 0; t < 2; ++t) {
-                            const uint32_t e = j < I.n[t] ? events[t] + j + 1 : ~0u;
+                            const uint32_t e = (I.dual ? (j & 1) == t : j < I.n[t]) ? events[t] + I.event(i, 1) : ~0u;
                             if (w) wide_free[1][t] = e;
                             else wide_free[0][t] = e;
                         }
@@ -951,8 +1044,8 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
 #pragma unroll
                     for (int t = 0; t < 2; ++t)
                         if (I.n[t]) {
-                            q_free[t] = events[t] + I.n[t] - 1;
-                            events[t] += I.n[t] + 1;
+                            q_free[t] = events[t] + I.event(I.n[t] - 1, 0);
+                            events[t] += I.events(t);
                         }
                 }
             }
@@ -961,14 +1054,17 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
     } else {
         regs_inc<P::REGS_SOFTMAX>();
         const int t = warp >> 2;
-        uint32_t item = 0, events = 0, keys = 0;
+        uint32_t item = 0, events = 0, keys = 0, shares = 0, turn = 0;     // turn: of the items that this tile has a part in
         while (true) {
             ChunkItem I;
             const bool ok = next_item(item, I);
             if (!__all_sync(0xffffffffu, ok)) break;
             if (lane == 0) free_item(item);
             if (I.n[0] < 0) break;
-            if (!ch_softmax<D, FP8>(sh, A, I, t, events, keys, item & 1)) break;
+            if (!ch_softmax<D, FP8>(sh, A, I, t, events, keys, turn & 1, shares)) break;
+            events += I.events(t);
+            turn += I.n[t] > 0;
+            keys += I.tiles;
             ++item;
         }
     }
@@ -982,9 +1078,11 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
         const int issued = sh.issued;
         if (!FP8)
             for (int t = 0; t < 2; ++t)
-                if (sh.found[t]) mbar_wait_bounded(smem_u32(&sh.q_full[t]), (sh.found[t] - 1) & 1, A.wait_ns);
-        for (int i = max(0, issued - P::STAGES); i < issued; ++i)
-            mbar_wait_bounded(smem_u32(&sh.kv_full[i % P::STAGES]), (i / P::STAGES) & 1, A.wait_ns);
+                if (sh.q_issued[t]) mbar_wait_bounded(smem_u32(&sh.q_full[t]), (sh.q_issued[t] - 1) & 1, A.wait_ns);
+        for (int i = max(0, (issued + 1) / 2 - P::KS); i < (issued + 1) / 2; ++i)
+            mbar_wait_bounded(smem_u32(&sh.k_full[i % P::KS]), (i / P::KS) & 1, A.wait_ns);
+        for (int i = max(0, issued / 2 - P::VS); i < issued / 2; ++i)
+            mbar_wait_bounded(smem_u32(&sh.v_full[i % P::VS]), (i / P::VS) & 1, A.wait_ns);
         if (sh.tail_open) mbar_wait_bounded(smem_u32(&sh.v_tail), sh.tail_phase & 1, A.wait_ns);
     }
 }

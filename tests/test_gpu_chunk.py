@@ -80,7 +80,8 @@ class Case:
                     k, v = self.rows[0][b][:see, g], self.rows[1][b][:see, g]
                     if hide:
                         k, v = k[keep], v[keep]
-                    want, wl, tol, tl = ref.attention(q, k, v, ref.BF16)
+                    # weights are rounded to bf16, and so are e4m3 values times scales that are no powers of two
+                    want, wl, tol, tl = ref.attention(q, k, v, 2 * ref.BF16 if self.e4m3 else ref.BF16)
                     if self.e4m3 and len(keep):
                         # q as two e4m3 values: each within 2^-17 of the row's largest
                         ds = float(2.0 ** -17 * q.abs().max() * k.abs().sum(1).max() / math.sqrt(self.d))
