@@ -614,14 +614,16 @@ kvo_status kvo_paged_attn_workspace(const kvo_paged_cache* cache, int n_q_heads,
  *   tokens are rows cu[b] .. cu[b + 1] - 1 (none may be there).  lens: device int32
  *   [batch]: the tokens of each request, the new ones among them: the i-th of n new
  *   tokens is token lens[b] - n + i and sees the tokens up to itself.
- *   max_new, max_len: the caller's upper bounds of the new tokens of a request and
- *   of lens (0: none known); they only choose how the work is split, larger
- *   requests are still served in full.
+ *   max_new: the caller's upper bound of the new tokens of a request (0: none known);
+ *   a request with more may be left out.  Up to 16 rows (max_new * n_q_heads /
+ *   n_kv_heads) take the way of kvo_paged_attn.  max_len: the caller's upper bound of
+ *   lens (0: none known); it only sizes the launch and the workspace, longer requests
+ *   are still attended to in full.
  *   o: bf16 [total_q][n_q_heads][head_dim], contiguous; lse (optional): fp32
  *   [total_q][n_q_heads], natural log; both and the workspace apart from each other
  *   and from all that the call reads.  Softmax scale 1/sqrt(head_dim), fp32
- *   accumulation, weights rounded to bf16, o rounded once to bf16.  With e4m3 pages
- *   values times v_scale are rounded to bf16 (exact for powers of two, which
+ *   accumulation, weights rounded to bf16 (or as kvo_paged_attn does, on its way), o
+ *   rounded once to bf16.  With e4m3 pages values times v_scale are rounded to bf16 (exact for powers of two, which
  *   kvo_paged_append takes), and q is taken as the sum of two e4m3 values times a
  *   power of two: exact where a value is at least 2^-9 of its row's largest, to 2^-17
  *   of that one else.  A row that sees no token gets o = 0, lse = -inf; rows
@@ -634,8 +636,9 @@ kvo_status kvo_paged_attn_workspace(const kvo_paged_cache* cache, int n_q_heads,
  *   that may overlap need one each).
  *   Status bits: KVO_DEV_BAD_BLOCK_ID (a page id out of range: its tokens add
  *   nothing), KVO_DEV_BAD_COUNT (offsets descending or outside 0..total_q, or a
- *   request that begins before the end of an earlier served one: it is not written;
- *   a length out of range: clamped), KVO_DEV_TIMEOUT (a bounded wait of 2 s gave up:
+ *   request that begins before the end of an earlier one with good offsets, or has
+ *   more new tokens than max_new allows for: it is not written; a length out of
+ *   range: clamped), KVO_DEV_TIMEOUT (a bounded wait of 2 s gave up:
  *   outputs are invalid).  Errors: KVO_ERR_INVALID, KVO_ERR_CUDA.
  */
 kvo_status kvo_paged_chunk_attn(const kvo_paged_cache* cache, const void* q, int64_t q_token_stride, int64_t total_q,

@@ -31,6 +31,7 @@
 #include "kvo_internal.cuh"
 #include "launch.cuh"
 #include "paged.cuh"
+#include "paged_few.cuh"
 #include "tcgen05.cuh"
 #include "tensor_map.cuh"
 
@@ -1161,6 +1162,8 @@ ChunkSpace chunk_space(int tiles, int d) {
     const size_t rows = (size_t)CH_CTAS * 2 * tiles * CH_ROWS;
     return {up(CH_CTAS * sizeof(ChunkCut)), up(rows * sizeof(float2)), rows * d * sizeof(float)};
 }
+// Few rows to a request: bound by the bytes of K and V, and products of 128 rows would be mostly empty.
+bool chunk_few(int r, int64_t max_new) { return max_new > 0 && max_new * r <= FEW_ROWS; }
 int chunk_tiles(int64_t total_q, int r) { return total_q <= CH_ROWS / r ? 1 : 2; }
 
 const char* chunk_error(const kvo_paged_cache* c, int n_q_heads, int64_t total_q, int64_t max_new, int64_t max_len) {
@@ -1197,8 +1200,9 @@ extern "C" kvo_status kvo_paged_chunk_attn_workspace(const kvo_paged_cache* cach
     if (!bytes_out) return bad("null output pointer");
     *bytes_out = 0;
     if (const char* m = chunk_error(cache, n_q_heads, total_q, max_new, max_len)) return bad(m);
-    const ChunkSpace sp = chunk_space(chunk_tiles(total_q, n_q_heads / cache->n_kv_heads), cache->head_dim);
-    *bytes_out = sp.cut + sp.ml + sp.o;
+    const int r = n_q_heads / cache->n_kv_heads;
+    const ChunkSpace sp = chunk_space(chunk_tiles(total_q, r), cache->head_dim);
+    *bytes_out = chunk_few(r, max_new) ? paged_few_workspace(cache, r, max_new, max_len) : sp.cut + sp.ml + sp.o;
     return KVO_OK;
 }
 
@@ -1220,8 +1224,9 @@ extern "C" kvo_status kvo_paged_chunk_attn(const kvo_paged_cache* cache, const v
     if (q_token_stride > (1ll << 38)) return bad("token strides must be below 2^38 elements");
     const int tiles = chunk_tiles(total_q, r);
     const ChunkSpace sp = chunk_space(tiles, D);
-    const size_t need = sp.cut + sp.ml + sp.o;
-    if (!workspace || workspace_bytes < need) return bad("the workspace is too small (kvo_paged_chunk_attn_workspace)");
+    const bool few = chunk_few(r, max_new);
+    const size_t need = few ? paged_few_workspace(cache, r, max_new, max_len) : sp.cut + sp.ml + sp.o;
+    if (need && (!workspace || workspace_bytes < need)) return bad("the workspace is too small (kvo_paged_chunk_attn_workspace)");
     const int64_t pool = page_bytes(cache), scales = scale_bytes(cache);
     const Bytes to_o{o, 2 * total_q * width}, to_lse{lse, 4 * total_q * n_q_heads}, to_ws{workspace, (int64_t)need};
     bool meet = meets_any(to_o, {to_lse, to_ws}) || meets_any(to_lse, {to_ws});
@@ -1231,6 +1236,19 @@ extern "C" kvo_status kvo_paged_chunk_attn(const kvo_paged_cache* cache, const v
                               {cu, 4 * (b + 1)}});
     if (meet) return bad("o, lse and the workspace must be apart from each other and from all that the call reads");
     const bool fp8 = cache->format == KVO_PAGES_E4M3;
+    const uint64_t rows = (uint64_t)cache->n_pages * cache->n_kv_heads * cache->page_size;
+    const int elem = fp8 ? 1 : 2, box = std::min(D * elem, 128), box_rows = few ? 16 : cache->page_size;
+    cudaStream_t s = (cudaStream_t)stream;
+    CUtensorMap mq, mk, mv;
+    if (!tensor_map_rows(&mk, cache->k_pages, elem, D, rows, box, box_rows) || !tensor_map_rows(&mv, cache->v_pages, elem, D, rows, box, box_rows)) {
+        set_last_error("cuTensorMapEncodeTiled failed for the pages");
+        return KVO_ERR_CUDA;
+    }
+    if (few) {
+        const cudaError_t e = launch_paged_few(cache, mk, mv, q, q_token_stride, total_q, r, cu, lens, max_new, max_len, o, lse, workspace, status, s);
+        if (e != cudaSuccess) { set_last_error(cudaGetErrorString(e)); return KVO_ERR_CUDA; }
+        return KVO_OK;
+    }
     ChunkArgs A{};
     A.q = (const uint16_t*)q;
     A.q_stride = q_token_stride;
@@ -1263,17 +1281,12 @@ extern "C" kvo_status kvo_paged_chunk_attn(const kvo_paged_cache* cache, const v
     A.scale_log2 = (float)(1.4426950408889634 / sqrt((double)D));
     A.skip = call_wait.skip;
     A.wait_ns = call_wait.limit_ns;
-    CUtensorMap mq, mk, mv;
     const uint64_t sq[3] = {(uint64_t)D, (uint64_t)n_q_heads, (uint64_t)total_q}, tq[2] = {(uint64_t)D * 2, (uint64_t)q_token_stride * 2};
     const uint32_t bq[3] = {64, (uint32_t)r, (uint32_t)A.tq};
-    const uint64_t rows = (uint64_t)cache->n_pages * cache->n_kv_heads * cache->page_size;
-    const int elem = fp8 ? 1 : 2, box = std::min(D * elem, 128);
-    if (!tensor_map(&mq, q, 2, 3, sq, tq, bq) || !tensor_map_rows(&mk, cache->k_pages, elem, D, rows, box, cache->page_size) ||
-        !tensor_map_rows(&mv, cache->v_pages, elem, D, rows, box, cache->page_size)) {
-        set_last_error("cuTensorMapEncodeTiled failed for q or the pages");
+    if (!tensor_map(&mq, q, 2, 3, sq, tq, bq)) {
+        set_last_error("cuTensorMapEncodeTiled failed for q");
         return KVO_ERR_CUDA;
     }
-    cudaStream_t s = (cudaStream_t)stream;
     cudaError_t e;
     if (D == 128) e = fp8 ? paged_chunk_launch<128, true>(mq, mk, mv, A, s) : paged_chunk_launch<128, false>(mq, mk, mv, A, s);
     else e = fp8 ? paged_chunk_launch<64, true>(mq, mk, mv, A, s) : paged_chunk_launch<64, false>(mq, mk, mv, A, s);

@@ -107,9 +107,65 @@ def test_chunks_match_reference(e4m3, d, hkv, r, page, new, lens):
     status = i32([0])
     o, lse = c.call(status=status)
     assert int(status.item()) == 0
-    c.check(o, lse, rows=None if sum(new) * hkv * r < 400 else [0, 1, 2, 4, 31, 32, 63, 64, 85, 127, 128, 199, -1], heads=None if hkv * r <= 8 else [0, r - 1, hkv * r - 1])
-    again = c.call(max_new=max(new), max_len=max(lens))
-    assert torch.equal(again[0], o) and torch.equal(again[1], lse)
+    which = dict(rows=None if sum(new) * hkv * r < 400 else [0, 1, 2, 4, 31, 32, 63, 64, 85, 127, 128, 199, -1],
+                 heads=None if hkv * r <= 8 else [0, r - 1, hkv * r - 1])
+    c.check(o, lse, **which)
+    again = c.call(max_new=max(new), max_len=max(lens))        # up to 16 rows: other kernels
+    if max(new) * r > 16:
+        assert torch.equal(again[0], o) and torch.equal(again[1], lse)
+    else:
+        c.check(*again, **which)
+        third = c.call(max_new=max(new), max_len=max(lens))
+        assert torch.equal(again[0], third[0]) and torch.equal(again[1], third[1])
+
+
+@pytest.mark.parametrize("e4m3", [False, True])
+@pytest.mark.parametrize("cap", [0, 100000])                  # clusters, ranges and their join
+@pytest.mark.parametrize("d,hkv,r,page,new,lens", [
+    (128, 2, 4, 16, [4, 0, 1, 3, 2], [2000, 5, 1, 700, 128]), (64, 1, 1, 32, [16, 5, 16], [16, 400, 1030]), (128, 8, 2, 64, [1, 4], [3001, 2500]),
+    (64, 4, 16, 128, [1, 1, 0, 1], [900, 3, 7, 128]), (128, 1, 3, 32, [5, 2, 5], [5, 3, 611]), (64, 2, 8, 16, [2, 1], [1000, 66]),
+    (128, 1, 8, 128, [1], [5000]), (128, 4, 5, 16, [3] * 40, [40 * i + 3 for i in range(40)]), (64, 1, 4, 16, [4] * 300, [7 * i % 90 + 4 for i in range(300)])])
+def test_few_new_tokens(e4m3, cap, d, hkv, r, page, new, lens):
+    """Up to 16 rows to a request, each with its own last key."""
+    c = Case(sum(lens), d, hkv, r, page, e4m3, new, lens, q_scale=2.0, spare=3)
+    status = i32([0])
+    o, lse = (torch.full(s, 3.0, dtype=t, device="cuda") for s, t in ((c.q.shape, torch.bfloat16), (c.q.shape[:2], torch.float32)))
+    c.call(o=o, lse=lse, status=status, max_new=max(new), max_len=max(cap, max(lens)))
+    assert int(status.item()) == 0
+    some = None if len(new) < 10 else range(0, len(new), len(new) // 12)
+    c.check(o, lse, heads=None if hkv * r <= 8 else [0, r - 1, hkv * r - 1], requests=some)
+    assert (o[c.cu[-1]:] == 3.0).all() and (lse[c.cu[-1]:] == 3.0).all()
+    assert (o[:c.cu[-1]] != 3.0).any(-1).all()
+    again = c.call(max_new=max(new), max_len=max(cap, max(lens)))
+    assert torch.equal(again[0][:c.cu[-1]], o[:c.cu[-1]]) and torch.equal(again[1][:c.cu[-1]], lse[:c.cu[-1]])
+
+
+@pytest.mark.parametrize("e4m3", [False, True])
+@pytest.mark.parametrize("cap", [0, 200000])
+def test_few_new_tokens_out_of_range(e4m3, cap):
+    """Rows that see nothing, more new tokens than announced, pages that do not exist, NaN in a neighbour's pages."""
+    c = Case(41, 64, 2, 4, 16, e4m3, [4, 3, 4, 2], [2, 0, 300, 80])
+    status = i32([0])
+    kw = dict(max_new=4, max_len=max(cap, 300))
+    o, lse = c.call(status=status, **kw)
+    assert int(status.item()) == 0
+    c.check(o, lse)
+    for p in c.table[2, :19].tolist():
+        c.kp.view(torch.uint8)[p], c.vp.view(torch.uint8)[p] = 255, 255
+    o2, lse2 = c.call(**kw)
+    assert o2[7:11].isnan().all() and torch.equal(o2[:7], o[:7]) and torch.equal(o2[11:], o[11:])
+    c = Case(43, 64, 2, 4, 16, e4m3, [4, 3, 4, 2], [100, 50, 300, 80])
+    c.table[2, 3], c.table[0, 6], c.table[3, 0] = -1, c.n_pages, 2 ** 31 - 1
+    o, lse = c.call(status=status, **kw)
+    assert int(status.item()) == kvo.DEV_BAD_BLOCK_ID
+    c.check(o, lse, hide={(2, 3), (0, 6), (3, 0)})
+    c = Case(47, 64, 2, 4, 16, e4m3, [4, 30, 4, 2], [100, 50, 300, 80])
+    status.zero_()
+    o = torch.full(c.q.shape, 3.0, dtype=torch.bfloat16, device="cuda")
+    c.call(o=o, status=status, **kw)
+    assert int(status.item()) == kvo.DEV_BAD_COUNT and (o[4:34] == 3.0).all()
+    o, lse = c.call(o=o, **kw)
+    c.check(o, lse, requests=[0, 2, 3])
 
 
 @pytest.mark.parametrize("e4m3", [False, True])
@@ -196,13 +252,14 @@ def test_out_of_range_pages_add_nothing(e4m3):
 
 
 @pytest.mark.parametrize("e4m3", [False, True])
-def test_bad_offsets_and_lengths(e4m3):
+@pytest.mark.parametrize("bounds", [{}, dict(max_new=6), dict(max_new=6, max_len=300000)])
+def test_bad_offsets_and_lengths(e4m3, bounds):
     """A request that is not served leaves its rows alone, all others are served."""
     for batch in (5, 40):
         new, lens = [6] * batch, [60] * batch
         c = Case(batch, 64, 1, 2, 16, e4m3, new, lens)
-        want = c.call()
-        for spoil, lost in (({2: 13}, {2: range(12, 13)}), ({2: -1}, {}), ({3: 1000}, {})):
+        want = c.call(**bounds)
+        for spoil in ({2: 13}, {2: -1}, {3: 1000}, {2: 9, 3: 7}):
             cu = list(c.cu)
             for i, x in spoil.items():
                 cu[i] = x
@@ -212,9 +269,11 @@ def test_bad_offsets_and_lengths(e4m3):
                     if cu[b] >= end:
                         rows[b] = (cu[b], cu[b + 1])
                     end = max(end, cu[b + 1])
+            if bounds:             # one with more new tokens than announced is left out
+                rows = {b: x for b, x in rows.items() if x[1] - x[0] <= 8}
             o = torch.full(c.q.shape, 3.0, dtype=torch.bfloat16, device="cuda")
             status = i32([0])
-            kvo.paged_chunk_attn(c.q, c.kp, c.vp, c.table, i32(lens), i32(cu), k_scale=c.scales[0], v_scale=c.scales[1], o=o, status=status)
+            kvo.paged_chunk_attn(c.q, c.kp, c.vp, c.table, i32(lens), i32(cu), k_scale=c.scales[0], v_scale=c.scales[1], o=o, status=status, **bounds)
             assert int(status.item()) & kvo.DEV_BAD_COUNT or len(rows) == batch
             served = torch.zeros(total, dtype=torch.bool)
             for b, (a, e) in rows.items():
@@ -224,7 +283,7 @@ def test_bad_offsets_and_lengths(e4m3):
             assert (o[~served.cuda()] == 3.0).all() and (o[served.cuda()] != 3.0).any()
         status = i32([0])
         o, _ = kvo.paged_chunk_attn(c.q, c.kp, c.vp, c.table, i32([-4] + [60] * (batch - 2) + [10 ** 6]), i32(c.cu), k_scale=c.scales[0],
-                                    v_scale=c.scales[1], status=status)
+                                    v_scale=c.scales[1], status=status, **bounds)
         assert int(status.item()) & kvo.DEV_BAD_COUNT
         assert (o[:6] == 0).all() and torch.equal(o[6:-6], want[0][6:-6])
 
@@ -284,6 +343,31 @@ def test_no_tokens():
     o = torch.full_like(q, 2.0)
     kvo.paged_chunk_attn(q, c.kp, c.vp, empty, i32([]), i32([0]), o=o)
     assert (o == 2.0).all()
+
+
+@pytest.mark.parametrize("cap", [200, 100000])
+def test_few_new_tokens_in_a_graph(cap):
+    """Captured once and replayed on other offsets and lengths, whatever the workspace held before."""
+    c = Case(53, 128, 2, 4, 16, True, [4, 1, 2, 4], [150, 9, 40, 200])
+    lens, cu, q = i32(c.lens), i32(c.cu), c.q.clone()
+    o, lse = torch.empty_like(c.q), torch.empty(c.q.shape[:2], device="cuda")
+    ws = torch.full((64 << 20,), 255, dtype=torch.uint8, device="cuda")
+    call = lambda: kvo.paged_chunk_attn(q, c.kp, c.vp, c.table, lens, cu, k_scale=c.scales[0], v_scale=c.scales[1], max_new=4, max_len=cap, o=o,
+                                        lse=lse, workspace=ws)
+    call()
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=side):
+        call()
+    for new, have in (([4, 1, 2, 4], [150, 9, 40, 200]), ([1, 1, 4, 0], [100, 5, 30, 2]), ([0, 0, 0, 4], [0, 0, 0, 131])):
+        c.new, c.lens, c.cu = new, have, cuts(new)
+        cu.copy_(i32(c.cu))
+        lens.copy_(i32(have))
+        ws.fill_(127)
+        graph.replay()
+        torch.cuda.synchronize()
+        c.check(o, lse, heads=[0, 3, 7])
 
 
 @pytest.mark.parametrize("e4m3", [False, True])
