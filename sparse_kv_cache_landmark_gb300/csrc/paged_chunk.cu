@@ -89,6 +89,7 @@ struct ChunkArgs {
     int w1, w2, base;              // cost of a key for one tile of rows and for two, and of an item in itself
     int64_t least;                 // cost of a range, unless there are more than CTAs
     float scale_log2;
+    int wide;                      // o is 32-byte aligned
     int skip;                      // the load that every CTA announces without copying it (tests; -1: none)
     long long wait_ns;
 };
@@ -103,7 +104,7 @@ struct ChunkCut {
 
 struct ChunkItem {
     int64_t row;
-    int32_t n[2];                  // tiles of keys of each tile of rows; n[0] = -1: the end
+    int32_t n0, n1;                // tiles of keys of each tile of rows; n0 = -1: the end
     int32_t tiles;                 // of keys in all
     int32_t dual;                  // one tile of rows only: both take it, with the even and the odd tiles of keys
     int32_t first;                 // tile of keys
@@ -113,11 +114,12 @@ struct ChunkItem {
     // the value product after them (1).  One commit for the next scores stands for a value product as well, where the
     // other tile's products run meanwhile; a dual item's stages of V would wait for it too long.
     __device__ __forceinline__ uint32_t event(int i, int value) const { return dual ? 2 * i + value : i + value; }
-    __device__ __forceinline__ uint32_t events(int t) const { return n[t] == 0 ? 0 : event(n[t] - 1, 1) + 1; }
+    __device__ __forceinline__ int n(int t) const { return t ? n1 : n0; }       // (an array would live in local memory)
+    __device__ __forceinline__ uint32_t events(int t) const { return n(t) == 0 ? 0 : event(n(t) - 1, 1) + 1; }
 };
 
 struct ChShared {
-    uint64_t q_full[2], k_full[4], v_full[4], raw_free[2], wide_full[2], event[2][CH_EVENTS], p_full[2], turn[2], drain[2], v_tail, item_full[CH_ITEMS],
+    uint64_t q_full[2], k_full[4], v_full[4], raw_free[2], wide_full[2], event[2][CH_EVENTS], p_full[2][2], turn[2], drain[2], v_tail, item_full[CH_ITEMS],
         item_free[CH_ITEMS], sc_full[CH_SCALES], ml_there, weights_there, o_read;
     ChunkItem item[CH_ITEMS];
     float k_scale[CH_SCALES][8], v_scale[CH_SCALES][8];
@@ -334,6 +336,12 @@ __device__ __forceinline__ ChunkCut ch_cut(const ChShared& sh, const ChunkArgs& 
 }
 
 // ------------------------------------------------------------------ softmax
+// 32 bytes, a whole sector, from one thread: a warp's threads hold a row each.
+__device__ __forceinline__ void st_global_32(void* p, const uint32_t (&v)[8]) {
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]),
+                 "r"(v[5]), "r"(v[6]), "r"(v[7])
+                 : "memory");
+}
 // The softmax of one tile of an item: a thread owns a row; it sees its request's keys [0, limit).  False: a wait gave up.
 template <int D, bool FP8>
 __device__ __forceinline__ bool ch_softmax(ChShared& sh, const ChunkArgs& A, const ChunkItem& I, int t, uint32_t events, uint32_t keys, int turn,
@@ -344,7 +352,7 @@ __device__ __forceinline__ bool ch_softmax(ChShared& sh, const ChunkArgs& A, con
     const int tok = I.tok0 + (I.dual ? 0 : t * A.tq) + tl;
     const bool real = tl < A.tq && tok < I.nq;
     const bool any = __any_sync(0xffffffffu, real);
-    const int n_tiles = I.n[t];
+    const int n_tiles = I.n(t);
     // a row that is none may see anything
     const int limit = real ? (int)min(max((int64_t)tok + 1 + (I.len - I.nq), (int64_t)0), (int64_t)I.len) - I.first * CH_KEYS : INT32_MAX;
     float m = -INFINITY, l = 0.f;                                       // log2 units; l in units of 2^m
@@ -356,7 +364,8 @@ __device__ __forceinline__ bool ch_softmax(ChShared& sh, const ChunkArgs& A, con
         ok = ok && ch_wait(sh, A, sh.sc_full[slot], (keys + j) / CH_SCALES);
         if (!__all_sync(0xffffffffu, ok)) return false;
         if (!any) {                // no rows in this warp: nothing reads what its lanes of P and O hold
-            mbar_arrive(smem_u32(&sh.p_full[t]));
+            mbar_arrive(smem_u32(&sh.p_full[t][0]));
+            mbar_arrive(smem_u32(&sh.p_full[t][1]));
             continue;
         }
         tc_fence_after();
@@ -394,32 +403,58 @@ __device__ __forceinline__ bool ch_softmax(ChShared& sh, const ChunkArgs& A, con
             }
         };
         uint64_t sum[2] = {0ull, 0ull};
-        // Most tiles: every key seen, no score far above the maximum so far.  One pass, and the weights go over the scores
-        // only once that is known.
+        auto release = [&](int h) {            // half of the weights are there: the value product may begin on them
+            tmem_wait_st();
+            tc_fence_before();
+            mbar_arrive(smem_u32(&sh.p_full[t][h]));
+        };
+        auto hide = [&](uint32_t (&x)[32], int c) {
+            if (rem < 32 * c + 32) {
+#pragma unroll
+                for (int e = 0; e < 32; ++e)
+                    if (32 * c + e >= rem) x[e] = 0xFF800000u;          // -inf
+            }
+        };
+        // Most tiles: no score far above the maximum so far, which the first tile takes from its first 64 keys.  The weights
+        // go over the scores only once that is known.
         bool done = false;
-        if (i > 0 && !bad && !__any_sync(0xffffffffu, rem < CH_KEYS)) {
-            uint32_t p[CH_KEYS / 2], x[2][32];
+        if (!bad) {
+            const bool edge = __any_sync(0xffffffffu, rem < CH_KEYS);
+            uint32_t p[32], x[2][32];
+            tmem_ld32(S, x[0]);
+            tmem_ld32(S + 32, x[1]);
+            tmem_wait_ld();
+            if (edge) { hide(x[0], 0); hide(x[1], 1); }
+            if (i == 0)
+#pragma unroll
+                for (int g = 0; g < 4; ++g) m = fmaxf(m, top_of(x[g / 2] + 16 * (g & 1)) * scale_of(g));
             const float b = m == -INFINITY ? 0.f : -m;
             float top = -INFINITY;
-            tmem_ld32(S, x[0]);
-            tmem_wait_ld();
 #pragma unroll
-            for (int c = 0; c < 4; ++c) {
-                if (c < 3) tmem_ld32(S + 32 * c + 32, x[(c & 1) ^ 1]);
+            for (int c = 0; c < 2; ++c) {
 #pragma unroll
                 for (int g = 0; g < 2; ++g) {
                     const float scale = scale_of(2 * c + g);
-                    weights(x[c & 1] + 16 * g, p + 16 * c + 8 * g, scale, b, sum);
-                    top = fmaxf(top, top_of(x[c & 1] + 16 * g) * scale);
+                    weights(x[c] + 16 * g, p + 16 * c + 8 * g, scale, b, sum);
+                    top = fmaxf(top, top_of(x[c] + 16 * g) * scale);
                 }
-                if (c < 3) tmem_wait_ld();
+                tmem_ld32(S + 64 + 32 * c, x[c]);
             }
-            done = !__any_sync(0xffffffffu, top > m + CH_RAISE);
+            tmem_wait_ld();
+            if (edge) { hide(x[0], 2); hide(x[1], 3); }
+#pragma unroll
+            for (int g = 0; g < 4; ++g) top = fmaxf(top, top_of(x[g / 2] + 16 * (g & 1)) * scale_of(4 + g));
+            done = !__any_sync(0xffffffffu, real && top > m + CH_RAISE);
             if (done) {
                 tmem_st32(S, p);
-                tmem_st32(S + 32, p + 32);
+                release(0);
+#pragma unroll
+                for (int g = 0; g < 4; ++g) weights(x[g / 2] + 16 * (g & 1), p + 8 * g, scale_of(4 + g), b, sum);
+                tmem_st32(S + 32, p);
+                release(1);
             } else {
                 sum[0] = sum[1] = 0ull;
+                if (i == 0) m = -INFINITY;
             }
         }
         if (!done) {               // first the maximum, then the weights, over scores that have been read
@@ -427,11 +462,7 @@ __device__ __forceinline__ bool ch_softmax(ChShared& sh, const ChunkArgs& A, con
             auto fetch = [&](int c) {
                 tmem_ld32(S + 32 * c, x);
                 tmem_wait_ld();
-                if (rem < 32 * c + 32) {
-#pragma unroll
-                    for (int e = 0; e < 32; ++e)
-                        if (32 * c + e >= rem) x[e] = 0xFF800000u;      // -inf
-                }
+                hide(x, c);
                 if (bad >> 2 * c & 3) {
 #pragma unroll
                     for (int e = 0; e < 32; ++e)
@@ -445,7 +476,7 @@ __device__ __forceinline__ bool ch_softmax(ChShared& sh, const ChunkArgs& A, con
 #pragma unroll
                 for (int g = 0; g < 2; ++g) top = fmaxf(top, top_of(x + 16 * g) * scale_of(2 * c + g));
             }
-            if (__any_sync(0xffffffffu, top > m + CH_RAISE)) {
+            if (__any_sync(0xffffffffu, real && top > m + CH_RAISE)) {
                 const float to = fmaxf(m, top);
                 const float f = m == -INFINITY ? 0.f : ex2(m - to);
                 m = to;
@@ -468,11 +499,9 @@ __device__ __forceinline__ bool ch_softmax(ChShared& sh, const ChunkArgs& A, con
 #pragma unroll
                 for (int g = 0; g < 2; ++g) weights(x + 16 * g, p + 8 * g, scale_of(2 * c + g), b, sum);
                 tmem_st16(S + 16 * c, p);
+                if (c & 1) release(c >> 1);
             }
         }
-        tmem_wait_st();
-        tc_fence_before();
-        mbar_arrive(smem_u32(&sh.p_full[t]));
         float s0, s1;
         unpack2(add2(sum[0], sum[1]), s0, s1);
         l += s0 + s1;
@@ -483,7 +512,7 @@ __device__ __forceinline__ bool ch_softmax(ChShared& sh, const ChunkArgs& A, con
         tc_fence_after();
     }
     // A dual item's halves: this thread writes half of the row's values, from both.
-    const bool both = I.dual && I.n[1] > 0;
+    const bool both = I.dual && I.n1 > 0;
     float w0 = t == 0 ? 1.f : 0.f, w1 = 1.f - w0;              // weights of the tiles' sums
     if (both) {
         bool ok = true;
@@ -553,16 +582,22 @@ __device__ __forceinline__ bool ch_softmax(ChShared& sh, const ChunkArgs& A, con
                     if (real)
                         to[i / 4 * CH_ROWS] = make_float4(__uint_as_float(o[i]), __uint_as_float(o[i + 1]), __uint_as_float(o[i + 2]), __uint_as_float(o[i + 3]));
             } else {
-                uint4* to = reinterpret_cast<uint4*>(A.o + out * D + x);
+                uint16_t* to = A.o + out * D + x;
 #pragma unroll
-                for (int i = 0; i < 32; i += 8) {
-                    uint32_t y[4];
+                for (int i = 0; i < 32; i += 16) {
+                    uint32_t y[8];
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) {
+                    for (int e = 0; e < 8; ++e) {
                         const __nv_bfloat162 v = __floats2bfloat162_rn(__uint_as_float(o[i + 2 * e]), __uint_as_float(o[i + 2 * e + 1]));
                         y[e] = *reinterpret_cast<const uint32_t*>(&v);
                     }
-                    if (real) to[i / 8] = make_uint4(y[0], y[1], y[2], y[3]);
+                    if (!real) continue;
+                    if (A.wide) {
+                        st_global_32(to + i, y);
+                    } else {
+                        *reinterpret_cast<uint4*>(to + i) = make_uint4(y[0], y[1], y[2], y[3]);
+                        *reinterpret_cast<uint4*>(to + i + 8) = make_uint4(y[4], y[5], y[6], y[7]);
+                    }
                 }
             }
         }
@@ -683,7 +718,8 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
         for (int t = 0; t < 2; ++t) {
             mbar_init(smem_u32(&sh.q_full[t]), FP8 ? 4 : 1);
             for (int i = 0; i < CH_EVENTS; ++i) mbar_init(smem_u32(&sh.event[t][i]), 1);
-            mbar_init(smem_u32(&sh.p_full[t]), 128);
+            mbar_init(smem_u32(&sh.p_full[t][0]), 128);
+            mbar_init(smem_u32(&sh.p_full[t][1]), 128);
             mbar_init(smem_u32(&sh.turn[t]), 1);
             mbar_init(smem_u32(&sh.drain[t]), 1);
         }
@@ -741,10 +777,8 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
             const int boxes = CH_KEYS / A.page * BOXES;
             auto event_wait = [&](int t, uint32_t e) { return e == ~0u || ch_event(sh, A, t, e); };
             while (ok) {
-                int n_all[2], first, last;
-                n_all[0] = ch_tiles(A, walk.r, walk.i, 0);
-                n_all[1] = ch_tiles(A, walk.r, walk.i, 1);
-                const int n_item = max(n_all[0], n_all[1]);
+                int first, last;
+                const int all0 = ch_tiles(A, walk.r, walk.i, 0), all1 = ch_tiles(A, walk.r, walk.i, 1), n_item = max(all0, all1);
                 ch_part(walk, lo, hi, n_item, first, last);
                 if (n_item ? last > first : walk.start >= lo) {
                     ChunkItem I;
@@ -752,8 +786,8 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
                     I.first = first;
                     I.dual = walk.r.n - walk.i * 2 * A.tq <= A.tq;
                     I.tiles = last - first;
-                    I.n[0] = I.dual ? (I.tiles + 1) / 2 : min(max(n_all[0] - first, 0), I.tiles);
-                    I.n[1] = I.dual ? I.tiles / 2 : min(max(n_all[1] - first, 0), I.tiles);
+                    I.n0 = I.dual ? (I.tiles + 1) / 2 : min(max(all0 - first, 0), I.tiles);
+                    I.n1 = I.dual ? I.tiles / 2 : min(max(all1 - first, 0), I.tiles);
                     I.b = walk.b;
                     I.g = walk.g;
                     I.tok0 = walk.i * 2 * A.tq;
@@ -843,30 +877,32 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
                             }
                             if (lane == holder) {
                                 const int i = I.dual ? j >> 1 : j;
-                                e0 = (I.dual ? !(j & 1) : j < I.n[0]) ? events[0] + I.event(i, v) : ~0u;
-                                e1 = (I.dual ? j & 1 : j < I.n[1]) ? events[1] + I.event(i, v) : ~0u;
+                                e0 = (I.dual ? !(j & 1) : j < I.n0) ? events[0] + I.event(i, v) : ~0u;
+                                e1 = (I.dual ? j & 1 : j < I.n1) ? events[1] + I.event(i, v) : ~0u;
                             }
                             ++issued;
                             if (!FP8 && j == 0 && v == 0)
+#pragma unroll
                                 for (int t = 0; t < 2; ++t) {
-                                    if (I.n[t] == 0) continue;
+                                    if (I.n(t) == 0 || !ok) continue;
                                     ok = event_wait(t, q_free[t]);
-                                    if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
-                                    if (lane == 0) {
+                                    ok = __all_sync(0xffffffffu, ok);
+                                    if (lane == 0 && ok) {
                                         mbar_expect_tx(smem_u32(&sh.q_full[t]), (uint32_t)((D / 64) * 128 * A.r * A.tq));
                                         for (int x = 0; x < D / 64; ++x)
                                             tma_load_3d(base + t * P::Q + x * CH_BLOCK, &map_q, 64 * x, I.g * A.r, (int)I.row + I.tok0 + (I.dual ? 0 : t * A.tq),
                                                         smem_u32(&sh.q_full[t]));
                                     }
-                                    ++q_issued[t];
+                                    q_issued[t] += ok;
                                 }
                             if (!ok) break;
                         }
                         ++tiles;
                     }
+#pragma unroll
                     for (int t = 0; t < 2; ++t)
-                        if (I.n[t]) {
-                            q_free[t] = events[t] + I.event(I.n[t] - 1, 0);
+                        if (I.n(t)) {
+                            q_free[t] = events[t] + I.event(I.n(t) - 1, 0);
                             events[t] += I.events(t);
                         }
                 }
@@ -891,7 +927,7 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
             ok = __all_sync(0xffffffffu, ok);
             if (lane == 0) {
                 if (ok) {
-                    sh.item[k % CH_ITEMS].n[0] = -1;
+                    sh.item[k % CH_ITEMS].n0 = -1;
                     mbar_arrive(smem_u32(&sh.item_full[k % CH_ITEMS]));
                 }
                 sh.issued = issued;
@@ -919,8 +955,8 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
                 ChunkItem I;
                 if (!next_item(item, I)) break;
                 free_item(item++);
-                if (I.n[0] < 0) break;
-                const int n_mine = I.n[t], n_other = I.n[t ^ 1];
+                if (I.n0 < 0) break;
+                const int n_mine = I.n(t), n_other = I.n(t ^ 1);
                 const bool turn = !I.dual && n_other > 0;
                 // The i-th tile of keys of this tile of rows, counted over all items.
                 auto at = [&](int i) { return tiles + (I.dual ? 2 * i + t : i); };
@@ -957,7 +993,7 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
                         if (!(ok = values_there(i))) break;
                         if (i + 1 < n_mine && !(ok = keys_there(i + 1))) break;
                         const uint64_t v = v0 + (uint64_t)(FP8 ? at(i) % 2 * (P::WIDE_BYTES >> 4) : at(i) % P::VS * (P::TILE >> 4));
-                        if (!(ok = ch_wait(sh, A, sh.p_full[t], weights))) break;
+                        if (!(ok = ch_wait(sh, A, sh.p_full[t][0], weights))) break;
                         // Both halves of the last dual item have been read.
                         if (shared && !(ok = ch_wait(sh, A, sh.o_read, shares - 1))) break;
                         shared = false;
@@ -967,7 +1003,11 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
                         if (turn && x < n_other && turns + x != ~0u && !(ok = ch_wait(sh, A, sh.turn[t], turns + x))) break;
                         tc_fence_after();
 #pragma unroll
-                        for (int e = 0; e < 8; ++e) mma_ts(O, S + 8 * e, v + e * (2048 >> 4), ID_O, i > 0 || e > 0);
+                        for (int e = 0; e < 4; ++e) mma_ts(O, S + 8 * e, v + e * (2048 >> 4), ID_O, i > 0 || e > 0);
+                        if (!(ok = ch_wait(sh, A, sh.p_full[t][1], weights))) break;
+                        tc_fence_after();
+#pragma unroll
+                        for (int e = 4; e < 8; ++e) mma_ts(O, S + 8 * e, v + e * (2048 >> 4), ID_O, true);
                         ++weights;
                         const bool more = i + 1 < n_mine;
                         if (!more || I.dual) tc_commit(smem_u32(&sh.event[t][(events + I.event(i, 1)) % CH_EVENTS]));
@@ -980,7 +1020,7 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
                 }
                 if (I.dual ? n_other > 0 : n_other > n_mine) behind = true;
                 events_other += I.events(t ^ 1);
-                if (I.dual && I.n[1] > 0) { shared = true; ++shares; }
+                if (I.dual && I.n1 > 0) { shared = true; ++shares; }
                 tiles += I.tiles;
             }
             // nothing of this CTA may be in flight when it leaves
@@ -1000,13 +1040,15 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
                     ok = next_item(item, I);
                     if (!__all_sync(0xffffffffu, ok)) break;
                     if (lane == 0) free_item(item);
-                    if (I.n[0] < 0) break;
-                    for (int t = 0; t < 2 && ok; ++t) {
-                        const bool copy = I.dual && I.n[1] > 0;             // both take the same rows
-                        if (I.n[t] == 0 || (copy && t == 1)) continue;
+                    if (I.n0 < 0) break;
+                    const bool copy = I.dual && I.n1 > 0;                 // both take the same rows
+#pragma unroll
+                    for (int t = 0; t < 2; ++t) {
+                        if (I.n(t) == 0 || (copy && t == 1) || !ok) continue;
                         if (q_free[t] != ~0u) ok = ch_event(sh, A, t, q_free[t]);
                         if (copy && ok && q_free[1] != ~0u) ok = ch_event(sh, A, 1, q_free[1]);
-                        if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
+                        ok = __all_sync(0xffffffffu, ok);
+                        if (!ok) continue;
                         int8_t* const exponent = &sh.q_exp[turn[t]++ & 1][t][row];
                         ch_split_q<D>(A, I, t, row, smem + t * P::Q, copy ? smem + P::Q : nullptr, exponent);
                         if (copy) sh.q_exp[turn[1]++ & 1][1][row] = *exponent;
@@ -1021,6 +1063,7 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
                     for (int j = 0; j < I.tiles && ok; ++j) {
                         const int st = tiles % P::VS, w = tiles % 2, sc = tiles % CH_SCALES;
                         ok = ch_wait(sh, A, sh.v_full[st], tiles / P::VS) && ch_wait(sh, A, sh.sc_full[sc], tiles / CH_SCALES);
+#pragma unroll
                         for (int t = 0; t < 2; ++t) {
                             const uint32_t e = w ? wide_free[1][t] : wide_free[0][t];
                             if (ok && e != ~0u) ok = ch_event(sh, A, t, e);
@@ -1036,7 +1079,7 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
                         const int i = I.dual ? j >> 1 : j;
 #pragma unroll
                         for (int t = 0; t < 2; ++t) {
-                            const uint32_t e = (I.dual ? (j & 1) == t : j < I.n[t]) ? events[t] + I.event(i, 1) : ~0u;
+                            const uint32_t e = (I.dual ? (j & 1) == t : j < I.n(t)) ? events[t] + I.event(i, 1) : ~0u;
                             if (w) wide_free[1][t] = e;
                             else wide_free[0][t] = e;
                         }
@@ -1044,8 +1087,8 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
                     }
 #pragma unroll
                     for (int t = 0; t < 2; ++t)
-                        if (I.n[t]) {
-                            q_free[t] = events[t] + I.event(I.n[t] - 1, 0);
+                        if (I.n(t)) {
+                            q_free[t] = events[t] + I.event(I.n(t) - 1, 0);
                             events[t] += I.events(t);
                         }
                 }
@@ -1061,10 +1104,10 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
             const bool ok = next_item(item, I);
             if (!__all_sync(0xffffffffu, ok)) break;
             if (lane == 0) free_item(item);
-            if (I.n[0] < 0) break;
+            if (I.n0 < 0) break;
             if (!ch_softmax<D, FP8>(sh, A, I, t, events, keys, turn & 1, shares)) break;
             events += I.events(t);
-            turn += I.n[t] > 0;
+            turn += I.n(t) > 0;
             keys += I.tiles;
             ++item;
         }
@@ -1279,6 +1322,7 @@ extern "C" kvo_status kvo_paged_chunk_attn(const kvo_paged_cache* cache, const v
     A.base = 2 * CH_KEYS * A.w2;
     A.least = 2 * CH_KEYS * A.w1 + A.base;
     A.scale_log2 = (float)(1.4426950408889634 / sqrt((double)D));
+    A.wide = (uintptr_t)o % 32 == 0;
     A.skip = call_wait.skip;
     A.wait_ns = call_wait.limit_ns;
     const uint64_t sq[3] = {(uint64_t)D, (uint64_t)n_q_heads, (uint64_t)total_q}, tq[2] = {(uint64_t)D * 2, (uint64_t)q_token_stride * 2};
