@@ -622,10 +622,11 @@ kvo_status kvo_paged_attn_workspace(const kvo_paged_cache* cache, int n_q_heads,
  *   o: bf16 [total_q][n_q_heads][head_dim], contiguous; lse (optional): fp32
  *   [total_q][n_q_heads], natural log; both and the workspace apart from each other
  *   and from all that the call reads.  Softmax scale 1/sqrt(head_dim), fp32
- *   accumulation, weights rounded to bf16 (or as kvo_paged_attn does, on its way), o
- *   rounded once to bf16.  With e4m3 pages values times v_scale are rounded to bf16 (exact for powers of two, which
- *   kvo_paged_append takes), and q is taken as the sum of two e4m3 values times a
- *   power of two: exact where a value is at least 2^-9 of its row's largest, to 2^-17
+ *   accumulation, weights rounded to bf16, o rounded once to bf16.  With e4m3 pages
+ *   the weights times v_scale are rounded to f16 instead (11 bits down to 2^-20 of the
+ *   running maximum of those, steps of 2^-30 of it below), and, but for few rows, q is
+ *   taken as the sum of two e4m3 values times a power of two: exact where a value is
+ *   at least 2^-9 of its row's largest, to 2^-17
  *   of that one else.  A row that sees no token gets o = 0, lse = -inf; rows
  *   outside every request keep their bytes.  What lies in a page behind the last
  *   token is never used, NaN included; among the new tokens of a request a NaN or an

@@ -13,16 +13,17 @@
 // One CTA to an SM, its warps
 //   9        walks the items: their descriptors, K and V tiles through rings (TMA, a box per page), the pages' scales,
 //   8, 10    one thread each issues the tcgen05.mma of tile 0 and 1: S_t = Q_t K^T and O_t += P_t V,
-//   0-3, 4-7 the softmax of tile 0 and 1, one thread per row: S from tensor memory, online maximum and sum in fp32, P (bf16)
-//            back over S,
-//   12-15    (e4m3) q to its 8-bit form, V to bf16.
+//   0-3, 4-7 the softmax of tile 0 and 1, one thread per row: S from tensor memory, online maximum and sum in fp32, P (bf16, or
+//            f16 next to e4m3) back over S,
+//   12-15    (e4m3) q to its 8-bit form, V to f16.
 // An item's first scores are issued behind the last value product of the one before, and its first loads before that.
 //
 // e4m3.  K goes to the tensor cores as it is: a row of q, times a power of two that brings its largest value to 2^7..2^8, is
 // the sum of two e4m3 values, exactly for what is at least 2^-9 of that largest and to 2^-17 of it for all below (a bf16
-// value has 8 bits, an e4m3 value 4), and two 8-bit products take the time of one of bf16.  V is widened to bf16 on its way
-// through shared memory, times its page's v_scale (exactly for powers of two; bf16 has fp32's exponents, so scales of any
-// size do); a page's k_scale multiplies its scores.
+// value has 8 bits, an e4m3 value 4), and two 8-bit products take the time of one of bf16.  V is widened to f16, exactly, on its
+// way through shared memory.  A page's k_scale multiplies its scores; its v_scale goes into the exponents of its weights,
+// exp2(s + log2 v_scale - m) with m the maximum of those, so that f16 holds what contributes most whatever the scales are,
+// and the sum of the weights takes each page's share times 1 / v_scale, in fp32.
 #include <stdio.h>
 
 #include <algorithm>
@@ -62,10 +63,10 @@ struct ChShape<D, false> {
 template <int D>
 struct ChShape<D, true> {
     static constexpr int THREADS = 512;
-    static constexpr int REGS_SOFTMAX = 168, REGS_OTHER = 88;
+    static constexpr int REGS_SOFTMAX = 184, REGS_OTHER = 72;
     static constexpr int Q = 2 * CH_ROWS * D;                   // the two pieces
     static constexpr int TILE = CH_KEYS * D;                    // of K or V as they are
-    static constexpr int WIDE_BYTES = CH_KEYS * D * 2;          // of V in bf16
+    static constexpr int WIDE_BYTES = CH_KEYS * D * 2;          // of V in f16
     static constexpr int KS = 4, VS = 2;
     static constexpr int TILES = 2 * Q + (KS + VS) * TILE + 2 * WIDE_BYTES;
 };
@@ -89,6 +90,7 @@ struct ChunkArgs {
     int w1, w2, base;              // cost of a key for one tile of rows and for two, and of an item in itself
     int64_t least;                 // cost of a range, unless there are more than CTAs
     float scale_log2;
+    float bias;                    // log2: weights are held times 2^this
     int wide;                      // o is 32-byte aligned
     int skip;                      // the load that every CTA announces without copying it (tests; -1: none)
     long long wait_ns;
@@ -122,7 +124,7 @@ struct ChShared {
     uint64_t q_full[2], k_full[4], v_full[4], raw_free[2], wide_full[2], event[2][CH_EVENTS], p_full[2][2], turn[2], drain[2], v_tail, item_full[CH_ITEMS],
         item_free[CH_ITEMS], sc_full[CH_SCALES], ml_there, weights_there, o_read;
     ChunkItem item[CH_ITEMS];
-    float k_scale[CH_SCALES][8], v_scale[CH_SCALES][8];
+    float k_scale[CH_SCALES][8], v_log[CH_SCALES][8];          // of each 16 keys of a tile: k_scale, log2 of v_scale
     uint32_t bad[CH_SCALES];       // groups of 16 keys in pages that do not exist
     int8_t q_exp[2][2][CH_ROWS];   // q's pieces are its values times 2^this; CH_NAN: not finite
     uint32_t tmem;
@@ -355,29 +357,37 @@ __device__ __forceinline__ bool ch_softmax(ChShared& sh, const ChunkArgs& A, con
     const int n_tiles = I.n(t);
     // a row that is none may see anything
     const int limit = real ? (int)min(max((int64_t)tok + 1 + (I.len - I.nq), (int64_t)0), (int64_t)I.len) - I.first * CH_KEYS : INT32_MAX;
-    float m = -INFINITY, l = 0.f;                                       // log2 units; l in units of 2^m
+    // log2 units.  Next to e4m3 pages m is the maximum of the scores times their v_scale, and weights are held times 2^6:
+    // they are rounded to f16, whose smallest step is 2^-24.  l is in units of 2^m (times 2^6).
+    constexpr float CH_BIAS = FP8 ? 6.f : 0.f;
+    float m = -INFINITY, l = 0.f;
     float q_scale = A.scale_log2;
-    for (int i = 0; i < n_tiles; ++i) {
-        const int j = I.dual ? 2 * i + t : i;
-        bool ok = ch_event(sh, A, t, events + I.event(i, 0));
+    const int step = I.dual ? 2 : 1;                                    // of the item's tiles of keys, from tile j on
+    int j = I.dual ? t : 0;
+    for (int i = 0; i < n_tiles; ++i, j += step) {
+        bool ok = ch_event(sh, A, t, events + (step == 2 ? 2 * i : i));
         const uint32_t slot = (keys + j) % CH_SCALES;
-        ok = ok && ch_wait(sh, A, sh.sc_full[slot], (keys + j) / CH_SCALES);
-        if (!__all_sync(0xffffffffu, ok)) return false;
         if (!any) {                // no rows in this warp: nothing reads what its lanes of P and O hold
-            mbar_arrive(smem_u32(&sh.p_full[t][0]));
-            mbar_arrive(smem_u32(&sh.p_full[t][1]));
+            if (!__all_sync(0xffffffffu, ok)) return false;
+            for (int h = 0; h < 2; ++h) mbar_arrive(smem_u32(&sh.p_full[t][h]));
             continue;
         }
         tc_fence_after();
+        uint32_t x[CH_KEYS];
+#pragma unroll
+        for (int c = 0; c < 4; ++c) tmem_ld32(S + 32 * c, x + 32 * c);
+        // (the scores are on their way; the next lines are those of the keys' pages)
+        ok = ok && ch_wait(sh, A, sh.sc_full[slot], (keys + j) / CH_SCALES);
+        if (!__all_sync(0xffffffffu, ok)) { tmem_wait_ld(); return false; }
         if (FP8 && i == 0) {
             const int e = sh.q_exp[turn][t][row];
-            q_scale = e == CH_NAN ? __uint_as_float(0x7FC00000u) : __uint_as_float((uint32_t)(127 - e) << 23) * A.scale_log2;
+            q_scale = e == CH_NAN ? 0.f : __uint_as_float((uint32_t)(127 - e) << 23) * A.scale_log2;
         }
         const uint32_t bad = sh.bad[slot];
-        const int rem = limit - j * CH_KEYS;
+        const int rem = min(limit - j * CH_KEYS, CH_KEYS);
+        const bool edge = bad || __any_sync(0xffffffffu, rem < CH_KEYS);
         auto scale_of = [&](int g) {           // of the g-th 16 scores
-            const float x = FP8 ? sh.k_scale[slot][g] * q_scale : q_scale;
-            return FP8 && x < 1.2e-38f ? 1.2e-38f : x;                  // a masked score times zero would be NaN
+            return FP8 ? fmaxf(sh.k_scale[slot][g] * q_scale, 1.2e-38f) : q_scale;      // (a masked score times zero would be NaN)
         };
         auto top_of = [](const uint32_t* x) {
             float u = fmaxf(__uint_as_float(x[0]), __uint_as_float(x[1])), v = fmaxf(__uint_as_float(x[2]), __uint_as_float(x[3]));
@@ -398,114 +408,95 @@ __device__ __forceinline__ bool ch_softmax(ChShared& sh, const ChunkArgs& A, con
                 u = ex2(u);
                 v = ex2(v);
                 sum[e & 1] = add2(sum[e & 1], pack2(u, v));
-                const __nv_bfloat162 y = __floats2bfloat162_rn(u, v);
-                p[e] = *reinterpret_cast<const uint32_t*>(&y);
+                if (FP8) {
+                    const __half2 y = __floats2half2_rn(u, v);
+                    p[e] = *reinterpret_cast<const uint32_t*>(&y);
+                } else {
+                    const __nv_bfloat162 y = __floats2bfloat162_rn(u, v);
+                    p[e] = *reinterpret_cast<const uint32_t*>(&y);
+                }
             }
         };
-        uint64_t sum[2] = {0ull, 0ull};
-        auto release = [&](int h) {            // half of the weights are there: the value product may begin on them
-            tmem_wait_st();
-            tc_fence_before();
-            mbar_arrive(smem_u32(&sh.p_full[t][h]));
-        };
-        auto hide = [&](uint32_t (&x)[32], int c) {
-            if (rem < 32 * c + 32) {
+        tmem_wait_ld();
+        // Keys that a row does not see, at an item's end: hidden in tensor memory, by little code.
+        if (edge) {
+#pragma unroll 1
+            for (int c = 0; c < 4; ++c) {
+                uint32_t y[32];
+                tmem_ld32(S + 32 * c, y);
+                tmem_wait_ld();
+                const uint32_t seen = rem >= 32 * c + 32 ? ~0u : rem <= 32 * c ? 0u : (1u << (rem - 32 * c)) - 1;
+                const uint32_t keep = seen & ~((bad >> 2 * c & 1 ? 0xFFFFu : 0u) | (bad >> 2 * c & 2 ? 0xFFFF0000u : 0u));
 #pragma unroll
                 for (int e = 0; e < 32; ++e)
-                    if (32 * c + e >= rem) x[e] = 0xFF800000u;          // -inf
+                    if (!(keep >> e & 1)) y[e] = 0xFF800000u;           // -inf
+                tmem_st32(S + 32 * c, y);
             }
-        };
-        // Most tiles: no score far above the maximum so far, which the first tile takes from its first 64 keys.  The weights
-        // go over the scores only once that is known.
-        bool done = false;
-        if (!bad) {
-            const bool edge = __any_sync(0xffffffffu, rem < CH_KEYS);
-            uint32_t p[32], x[2][32];
-            tmem_ld32(S, x[0]);
-            tmem_ld32(S + 32, x[1]);
+            tmem_wait_st();
+#pragma unroll
+            for (int c = 0; c < 4; ++c) tmem_ld32(S + 32 * c, x + 32 * c);
             tmem_wait_ld();
-            if (edge) { hide(x[0], 0); hide(x[1], 1); }
-            if (i == 0)
+        }
+        float top = -INFINITY;
+        if (FP8) {
 #pragma unroll
-                for (int g = 0; g < 4; ++g) m = fmaxf(m, top_of(x[g / 2] + 16 * (g & 1)) * scale_of(g));
-            const float b = m == -INFINITY ? 0.f : -m;
-            float top = -INFINITY;
+            for (int g = 0; g < 8; ++g) top = fmaxf(top, fmaf(top_of(x + 16 * g), scale_of(g), sh.v_log[slot][g]));
+        } else {
 #pragma unroll
-            for (int c = 0; c < 2; ++c) {
+            for (int g = 0; g < 8; g += 2) top = max3(top, top_of(x + 16 * g), top_of(x + 16 * g + 16));
+            top *= q_scale;
+        }
+        if (__any_sync(0xffffffffu, real && top > m + CH_RAISE)) {
+            const float to = fmaxf(m, top);
+            const float f = m == -INFINITY ? 0.f : ex2(m - to);
+            m = to;
+            l *= f;
+            if (i > 0) {           // these scores are complete: so is the value product that was issued before them
+#pragma unroll 1
+                for (int c = 0; c < D; c += 32) {
+                    uint32_t o[32];
+                    tmem_ld32(O + c, o);
+                    tmem_wait_ld();
 #pragma unroll
-                for (int g = 0; g < 2; ++g) {
-                    const float scale = scale_of(2 * c + g);
-                    weights(x[c] + 16 * g, p + 16 * c + 8 * g, scale, b, sum);
-                    top = fmaxf(top, top_of(x[c] + 16 * g) * scale);
+                    for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+                    tmem_st32(O + c, o);
                 }
-                tmem_ld32(S + 64 + 32 * c, x[c]);
-            }
-            tmem_wait_ld();
-            if (edge) { hide(x[0], 2); hide(x[1], 3); }
-#pragma unroll
-            for (int g = 0; g < 4; ++g) top = fmaxf(top, top_of(x[g / 2] + 16 * (g & 1)) * scale_of(4 + g));
-            done = !__any_sync(0xffffffffu, real && top > m + CH_RAISE);
-            if (done) {
-                tmem_st32(S, p);
-                release(0);
-#pragma unroll
-                for (int g = 0; g < 4; ++g) weights(x[g / 2] + 16 * (g & 1), p + 8 * g, scale_of(4 + g), b, sum);
-                tmem_st32(S + 32, p);
-                release(1);
-            } else {
-                sum[0] = sum[1] = 0ull;
-                if (i == 0) m = -INFINITY;
             }
         }
-        if (!done) {               // first the maximum, then the weights, over scores that have been read
-            uint32_t x[32], p[16];
-            auto fetch = [&](int c) {
-                tmem_ld32(S + 32 * c, x);
-                tmem_wait_ld();
-                hide(x, c);
-                if (bad >> 2 * c & 3) {
+        const float b = m == -INFINITY ? 0.f : CH_BIAS - m;
+        uint64_t sum[2] = {0ull, 0ull};
+        float total = 0.f;
 #pragma unroll
-                    for (int e = 0; e < 32; ++e)
-                        if (bad >> (2 * c + e / 16) & 1) x[e] = 0xFF800000u;
-                }
-            };
-            float top = -INFINITY;
-#pragma unroll 1
-            for (int c = 0; c < 4; ++c) {
-                fetch(c);
+        for (int c = 0; c < 4; ++c) {
+            uint32_t p[16];
 #pragma unroll
-                for (int g = 0; g < 2; ++g) top = fmaxf(top, top_of(x + 16 * g) * scale_of(2 * c + g));
-            }
-            if (__any_sync(0xffffffffu, real && top > m + CH_RAISE)) {
-                const float to = fmaxf(m, top);
-                const float f = m == -INFINITY ? 0.f : ex2(m - to);
-                m = to;
-                l *= f;
-                if (i > 0) {       // these scores are complete: so is the value product that was issued before them
-#pragma unroll 1
-                    for (int c = 0; c < D; c += 32) {
-                        tmem_ld32(O + c, x);
-                        tmem_wait_ld();
-#pragma unroll
-                        for (int e = 0; e < 32; ++e) x[e] = __float_as_uint(__uint_as_float(x[e]) * f);
-                        tmem_st32(O + c, x);
-                    }
+            for (int g = 0; g < 2; ++g) {
+                if (FP8) {
+                    sum[0] = sum[1] = 0ull;
+                    const float v_log = sh.v_log[slot][2 * c + g];
+                    weights(x + 32 * c + 16 * g, p + 8 * g, scale_of(2 * c + g), b + v_log, sum);
+                    float s0, s1;
+                    unpack2(add2(sum[0], sum[1]), s0, s1);
+                    total = fmaf(s0 + s1, ex2(-v_log), total);
+                } else {
+                    weights(x + 32 * c + 16 * g, p + 8 * g, q_scale, b, sum);
                 }
             }
-            const float b = m == -INFINITY ? 0.f : -m;
-#pragma unroll 1
-            for (int c = 0; c < 4; ++c) {
-                fetch(c);
-#pragma unroll
-                for (int g = 0; g < 2; ++g) weights(x + 16 * g, p + 8 * g, scale_of(2 * c + g), b, sum);
-                tmem_st16(S + 16 * c, p);
-                if (c & 1) release(c >> 1);
+            tmem_st16(S + 16 * c, p);
+            if (c & 1) {           // the value product may begin on half of the keys
+                tmem_wait_st();
+                tc_fence_before();
+                mbar_arrive(smem_u32(&sh.p_full[t][c >> 1]));
             }
         }
-        float s0, s1;
-        unpack2(add2(sum[0], sum[1]), s0, s1);
-        l += s0 + s1;
+        if (!FP8) {
+            float s0, s1;
+            unpack2(add2(sum[0], sum[1]), s0, s1);
+            total = s0 + s1;
+        }
+        l += total;
     }
+    if (FP8 && any && n_tiles > 0 && sh.q_exp[turn][t][row] == CH_NAN) l = __uint_as_float(0x7FC00000u);
     if (n_tiles > 0) {
         const bool ok = ch_event(sh, A, t, events + I.event(n_tiles - 1, 1));
         if (!__all_sync(0xffffffffu, ok)) return false;
@@ -607,7 +598,7 @@ __device__ __forceinline__ bool ch_softmax(ChShared& sh, const ChunkArgs& A, con
     }
     if (real && (!both || t == 0)) {
         if (I.part >= 0) A.part_ml[at * CH_ROWS + row] = make_float2(m, l);
-        else if (A.lse) A.lse[out] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
+        else if (A.lse) A.lse[out] = l == 0.f ? -INFINITY : (m + log2f(l) - CH_BIAS) * 0.6931471805599453f;
     }
     return true;
 }
@@ -663,33 +654,31 @@ __device__ __forceinline__ void ch_split_q(const ChunkArgs& A, const ChunkItem& 
         }
     }
 }
-// A tile of V from its codes, times their pages' scales, to bf16, by 128 threads; rows from `have` on become zero, as a weight
-// of zero does not silence the NaN that may lie there.
+// A tile of V from its codes to f16, by 128 threads; rows from `have` on become zero, as a weight of zero does not silence the
+// NaN that may lie there.
 template <int D>
-__device__ __forceinline__ void ch_widen_v(const uint8_t* from, uint8_t* to, const float* scales, int have) {
+__device__ __forceinline__ void ch_widen_v(const uint8_t* from, uint8_t* to, int have) {
     constexpr int CH = D / 16;
-#pragma unroll 4
+    const int t = threadIdx.x & 127, row0 = t / CH, c = t % CH;
+    // Rows of a thread are 128 / CH apart, a multiple of 8: their swizzles are alike.
+    const uint8_t* a = from + row0 * D + (D == 128 ? c ^ (row0 & 7) : c ^ (row0 >> 1 & 3)) * 16;
+    uint8_t* b = to + (c / 4) * CH_BLOCK + row0 * 128;
+    const int x0 = ((c % 4 * 2) ^ (row0 & 7)) * 16, x1 = ((c % 4 * 2 + 1) ^ (row0 & 7)) * 16;
+    uint4 v[CH];
+#pragma unroll
+    for (int k = 0; k < CH; ++k) v[k] = *reinterpret_cast<const uint4*>(a + k * (128 / CH) * D);
+#pragma unroll
     for (int k = 0; k < CH; ++k) {
-        const int idx = k * 128 + (threadIdx.x & 127), row = idx / CH, c = idx % CH;
-        uint4 v = *reinterpret_cast<const uint4*>(from + row * D + (D == 128 ? c ^ (row & 7) : c ^ (row >> 1 & 3)) * 16);
-        if (row >= have) v = make_uint4(0, 0, 0, 0);
-        const float scale = scales[row / 16];
-        const uint64_t scale2 = pack2(scale, scale);
-        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+        const uint32_t w[4] = {v[k].x, v[k].y, v[k].z, v[k].w};
         uint32_t o[8];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const uint32_t f = e4m3x2_to_f16x2((uint16_t)(w[i / 2] >> (i & 1) * 16));
-            const float2 x = __half22float2(*reinterpret_cast<const __half2*>(&f));
-            float y, z;
-            unpack2(mul2(pack2(x.x, x.y), scale2), y, z);
-            const __nv_bfloat162 b = __floats2bfloat162_rn(y, z);
-            o[i] = *reinterpret_cast<const uint32_t*>(&b);
-        }
-        uint8_t* at = to + (c / 4) * CH_BLOCK + row * 128;
-        const int first = (c % 4) * 2;
-        *reinterpret_cast<uint4*>(at + ((first ^ (row & 7)) * 16)) = make_uint4(o[0], o[1], o[2], o[3]);
-        *reinterpret_cast<uint4*>(at + (((first + 1) ^ (row & 7)) * 16)) = make_uint4(o[4], o[5], o[6], o[7]);
+        for (int i = 0; i < 8; ++i) o[i] = e4m3x2_to_f16x2((uint16_t)(w[i / 2] >> (i & 1) * 16));
+        if (row0 + k * (128 / CH) >= have)
+#pragma unroll
+            for (int i = 0; i < 8; ++i) o[i] = 0u;
+        uint8_t* to_row = b + k * (128 / CH) * 128;
+        *reinterpret_cast<uint4*>(to_row + x0) = make_uint4(o[0], o[1], o[2], o[3]);
+        *reinterpret_cast<uint4*>(to_row + x1) = make_uint4(o[4], o[5], o[6], o[7]);
     }
 }
 
@@ -718,8 +707,7 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
         for (int t = 0; t < 2; ++t) {
             mbar_init(smem_u32(&sh.q_full[t]), FP8 ? 4 : 1);
             for (int i = 0; i < CH_EVENTS; ++i) mbar_init(smem_u32(&sh.event[t][i]), 1);
-            mbar_init(smem_u32(&sh.p_full[t][0]), 128);
-            mbar_init(smem_u32(&sh.p_full[t][1]), 128);
+            for (int i = 0; i < 2; ++i) mbar_init(smem_u32(&sh.p_full[t][i]), 128);
             mbar_init(smem_u32(&sh.turn[t]), 1);
             mbar_init(smem_u32(&sh.drain[t]), 1);
         }
@@ -821,7 +809,7 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
                             if (bad || !in) page = -1;
                             if constexpr (FP8) {
                                 ks = page < 0 ? 1.f : __ldg(A.k_scale + (int64_t)page * A.hkv + I.g);
-                                vs = page < 0 ? 0.f : __ldg(A.v_scale + (int64_t)page * A.hkv + I.g);
+                                vs = page < 0 ? 1.f : __ldg(A.v_scale + (int64_t)page * A.hkv + I.g);
                             }
                         }
                         const uint32_t bads = __ballot_sync(0xffffffffu, bad) >> (j & 3) * 8 & 0xFF;
@@ -846,7 +834,7 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
                                 if constexpr (FP8)
                                     if (lane >> 3 == (j & 3)) {
                                         sh.k_scale[sc][lane & 7] = ks;
-                                        sh.v_scale[sc][lane & 7] = vs;
+                                        sh.v_log[sc][lane & 7] = log2f(vs);
                                     }
                                 if (lane == 0) sh.bad[sc] = bads;
                                 __syncwarp();
@@ -942,7 +930,8 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
             // ------------------------------------------------ matrix products of one tile
             // The tensor cores queue a few instructions only; with a thread of its own for each tile, one tile's waits and
             // commits pass while the other's products run.  They take turns, so that the tiles stay half a period apart.
-            constexpr uint32_t ID_S = FP8 ? mma_desc_e4m3(CH_ROWS, CH_KEYS) : mma_desc(CH_ROWS, CH_KEYS, false), ID_O = mma_desc(CH_ROWS, D, true);
+            constexpr uint32_t ID_S = FP8 ? mma_desc_e4m3(CH_ROWS, CH_KEYS) : mma_desc(CH_ROWS, CH_KEYS, false);
+            constexpr uint32_t ID_O = FP8 ? mma_desc_f16(CH_ROWS, D, true) : mma_desc(CH_ROWS, D, true);
             const int t = (warp - 8) >> 1;
             const uint32_t S = sh.tmem + 128 * t, O = sh.tmem + 256 + D * t;
             constexpr bool HALF = FP8 && D == 64;              // rows of 64 bytes
@@ -1003,11 +992,15 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
                         if (turn && x < n_other && turns + x != ~0u && !(ok = ch_wait(sh, A, sh.turn[t], turns + x))) break;
                         tc_fence_after();
 #pragma unroll
-                        for (int e = 0; e < 4; ++e) mma_ts(O, S + 8 * e, v + e * (2048 >> 4), ID_O, i > 0 || e > 0);
-                        if (!(ok = ch_wait(sh, A, sh.p_full[t][1], weights))) break;
-                        tc_fence_after();
+                        for (int h = 0; h < 2; ++h) {
+                            if (h > 0) {
+                                if (!(ok = ch_wait(sh, A, sh.p_full[t][1], weights))) break;
+                                tc_fence_after();
+                            }
 #pragma unroll
-                        for (int e = 4; e < 8; ++e) mma_ts(O, S + 8 * e, v + e * (2048 >> 4), ID_O, true);
+                            for (int e = 4 * h; e < 4 * h + 4; ++e) mma_ts(O, S + 8 * e, v + e * (2048 >> 4), ID_O, i > 0 || e > 0);
+                        }
+                        if (!ok) break;
                         ++weights;
                         const bool more = i + 1 < n_mine;
                         if (!more || I.dual) tc_commit(smem_u32(&sh.event[t][(events + I.event(i, 1)) % CH_EVENTS]));
@@ -1061,15 +1054,15 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
                     }
                     ++item;
                     for (int j = 0; j < I.tiles && ok; ++j) {
-                        const int st = tiles % P::VS, w = tiles % 2, sc = tiles % CH_SCALES;
-                        ok = ch_wait(sh, A, sh.v_full[st], tiles / P::VS) && ch_wait(sh, A, sh.sc_full[sc], tiles / CH_SCALES);
+                        const int st = tiles % P::VS, w = tiles % 2;
+                        ok = ch_wait(sh, A, sh.v_full[st], tiles / P::VS);
 #pragma unroll
                         for (int t = 0; t < 2; ++t) {
                             const uint32_t e = w ? wide_free[1][t] : wide_free[0][t];
                             if (ok && e != ~0u) ok = ch_event(sh, A, t, e);
                         }
                         if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
-                        ch_widen_v<D>(smem + V0 + st * P::TILE, smem + WIDE0 + w * P::WIDE_BYTES, sh.v_scale[sc], I.len - (I.first + j) * CH_KEYS);
+                        ch_widen_v<D>(smem + V0 + st * P::TILE, smem + WIDE0 + w * P::WIDE_BYTES, I.len - (I.first + j) * CH_KEYS);
                         fence_async_smem();
                         __syncwarp();
                         if (lane == 0) {
@@ -1100,15 +1093,17 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
         const int t = warp >> 2;
         uint32_t item = 0, events = 0, keys = 0, shares = 0, turn = 0;     // turn: of the items that this tile has a part in
         while (true) {
-            ChunkItem I;
-            const bool ok = next_item(item, I);
+            // The item stays where it is: 128 scores leave few registers.
+            const bool ok = ch_wait(sh, A, sh.item_full[item % CH_ITEMS], item / CH_ITEMS);
             if (!__all_sync(0xffffffffu, ok)) break;
-            if (lane == 0) free_item(item);
+            const ChunkItem& I = sh.item[item % CH_ITEMS];
             if (I.n0 < 0) break;
             if (!ch_softmax<D, FP8>(sh, A, I, t, events, keys, turn & 1, shares)) break;
             events += I.events(t);
             turn += I.n(t) > 0;
             keys += I.tiles;
+            __syncwarp();
+            if (lane == 0) free_item(item);
             ++item;
         }
     }
@@ -1193,7 +1188,7 @@ __global__ void __launch_bounds__(CH_ROWS) paged_chunk_join_kernel(const __grid_
         to[e / 2] = make_uint4(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b), *reinterpret_cast<const uint32_t*>(&g),
                                *reinterpret_cast<const uint32_t*>(&d));
     }
-    if (blockIdx.z == 0 && A.lse) A.lse[out] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
+    if (blockIdx.z == 0 && A.lse) A.lse[out] = l == 0.f ? -INFINITY : (m + log2f(l) - A.bias) * 0.6931471805599453f;
 }
 
 // ------------------------------------------------------------------ host
@@ -1322,6 +1317,7 @@ extern "C" kvo_status kvo_paged_chunk_attn(const kvo_paged_cache* cache, const v
     A.base = 2 * CH_KEYS * A.w2;
     A.least = 2 * CH_KEYS * A.w1 + A.base;
     A.scale_log2 = (float)(1.4426950408889634 / sqrt((double)D));
+    A.bias = fp8 ? 6.f : 0.f;
     A.wide = (uintptr_t)o % 32 == 0;
     A.skip = call_wait.skip;
     A.wait_ns = call_wait.limit_ns;

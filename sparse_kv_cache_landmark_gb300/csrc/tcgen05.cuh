@@ -38,6 +38,10 @@ __host__ __device__ constexpr uint32_t mma_desc(int m, int n, bool b_mn_major) {
 __device__ __forceinline__ uint64_t smem_desc64(uint32_t addr) {
     return (uint64_t)((addr >> 4) & 0x3FFF) | (uint64_t)1 << 16 | (uint64_t)(512 >> 4) << 32 | (uint64_t)1 << 46 | (uint64_t)4 << 61;
 }
+// f16 x f16 -> fp32, otherwise as above.
+__host__ __device__ constexpr uint32_t mma_desc_f16(int m, int n, bool b_mn_major) {
+    return 1u << 4 | (b_mn_major ? 1u << 16 : 0u) | (uint32_t)(n >> 3) << 17 | (uint32_t)(m >> 4) << 24;
+}
 // e4m3 x e4m3 -> fp32, M x N, both K-major.
 __host__ __device__ constexpr uint32_t mma_desc_e4m3(int m, int n) { return 1u << 4 | (uint32_t)(n >> 3) << 17 | (uint32_t)(m >> 4) << 24; }
 // D (tensor memory) = A B (+ D if `add`), K = 16: A and B in shared memory.
