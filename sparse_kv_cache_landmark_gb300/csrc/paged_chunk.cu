@@ -63,7 +63,7 @@ struct ChShape<D, false> {
 template <int D>
 struct ChShape<D, true> {
     static constexpr int THREADS = 512;
-    static constexpr int REGS_SOFTMAX = 184, REGS_OTHER = 72;
+    static constexpr int REGS_SOFTMAX = 152, REGS_OTHER = 104;
     static constexpr int Q = 2 * CH_ROWS * D;                   // the two pieces
     static constexpr int TILE = CH_KEYS * D;                    // of K or V as they are
     static constexpr int WIDE_BYTES = CH_KEYS * D * 2;          // of V in f16
@@ -372,13 +372,9 @@ __device__ __forceinline__ bool ch_softmax(ChShared& sh, const ChunkArgs& A, con
             for (int h = 0; h < 2; ++h) mbar_arrive(smem_u32(&sh.p_full[t][h]));
             continue;
         }
-        tc_fence_after();
-        uint32_t x[CH_KEYS];
-#pragma unroll
-        for (int c = 0; c < 4; ++c) tmem_ld32(S + 32 * c, x + 32 * c);
-        // (the scores are on their way; the next lines are those of the keys' pages)
         ok = ok && ch_wait(sh, A, sh.sc_full[slot], (keys + j) / CH_SCALES);
-        if (!__all_sync(0xffffffffu, ok)) { tmem_wait_ld(); return false; }
+        if (!__all_sync(0xffffffffu, ok)) return false;
+        tc_fence_after();
         if (FP8 && i == 0) {
             const int e = sh.q_exp[turn][t][row];
             q_scale = e == CH_NAN ? 0.f : __uint_as_float((uint32_t)(127 - e) << 23) * A.scale_log2;
@@ -417,8 +413,7 @@ __device__ __forceinline__ bool ch_softmax(ChShared& sh, const ChunkArgs& A, con
                 }
             }
         };
-        tmem_wait_ld();
-        // Keys that a row does not see, at an item's end: hidden in tensor memory, by little code.
+        // Keys that a row does not see, at an item's end: hidden in tensor memory.
         if (edge) {
 #pragma unroll 1
             for (int c = 0; c < 4; ++c) {
@@ -433,19 +428,25 @@ __device__ __forceinline__ bool ch_softmax(ChShared& sh, const ChunkArgs& A, con
                 tmem_st32(S + 32 * c, y);
             }
             tmem_wait_st();
-#pragma unroll
-            for (int c = 0; c < 4; ++c) tmem_ld32(S + 32 * c, x + 32 * c);
-            tmem_wait_ld();
         }
+        // Half of the keys at a time, in loops that stay loops: what two warps of a scheduler, the products' and the widening
+        // one run all the time has to fit its instruction cache.
+        uint32_t x[64];
         float top = -INFINITY;
-        if (FP8) {
+#pragma unroll 1
+        for (int h = 1; h >= 0; --h) {
+            tmem_ld32(S + 64 * h, x);
+            tmem_ld32(S + 64 * h + 32, x + 32);
+            tmem_wait_ld();
+            if (FP8) {
 #pragma unroll
-            for (int g = 0; g < 8; ++g) top = fmaxf(top, fmaf(top_of(x + 16 * g), scale_of(g), sh.v_log[slot][g]));
-        } else {
+                for (int g = 0; g < 4; ++g) top = fmaxf(top, fmaf(top_of(x + 16 * g), scale_of(4 * h + g), sh.v_log[slot][4 * h + g]));
+            } else {
 #pragma unroll
-            for (int g = 0; g < 8; g += 2) top = max3(top, top_of(x + 16 * g), top_of(x + 16 * g + 16));
-            top *= q_scale;
+                for (int g = 0; g < 4; g += 2) top = max3(top, top_of(x + 16 * g), top_of(x + 16 * g + 16));
+            }
         }
+        if (!FP8) top *= q_scale;
         if (__any_sync(0xffffffffu, real && top > m + CH_RAISE)) {
             const float to = fmaxf(m, top);
             const float f = m == -INFINITY ? 0.f : ex2(m - to);
@@ -466,28 +467,31 @@ __device__ __forceinline__ bool ch_softmax(ChShared& sh, const ChunkArgs& A, con
         const float b = m == -INFINITY ? 0.f : CH_BIAS - m;
         uint64_t sum[2] = {0ull, 0ull};
         float total = 0.f;
+#pragma unroll 1
+        for (int h = 0; h < 2; ++h) {          // (the first half is still there)
+            uint32_t p[32];
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
-            uint32_t p[16];
-#pragma unroll
-            for (int g = 0; g < 2; ++g) {
+            for (int g = 0; g < 4; ++g) {
                 if (FP8) {
                     sum[0] = sum[1] = 0ull;
-                    const float v_log = sh.v_log[slot][2 * c + g];
-                    weights(x + 32 * c + 16 * g, p + 8 * g, scale_of(2 * c + g), b + v_log, sum);
+                    const float v_log = sh.v_log[slot][4 * h + g];
+                    weights(x + 16 * g, p + 8 * g, scale_of(4 * h + g), b + v_log, sum);
                     float s0, s1;
                     unpack2(add2(sum[0], sum[1]), s0, s1);
                     total = fmaf(s0 + s1, ex2(-v_log), total);
                 } else {
-                    weights(x + 32 * c + 16 * g, p + 8 * g, q_scale, b, sum);
+                    weights(x + 16 * g, p + 8 * g, q_scale, b, sum);
                 }
             }
-            tmem_st16(S + 16 * c, p);
-            if (c & 1) {           // the value product may begin on half of the keys
-                tmem_wait_st();
-                tc_fence_before();
-                mbar_arrive(smem_u32(&sh.p_full[t][c >> 1]));
+            if (h == 0) {
+                tmem_ld32(S + 64, x);
+                tmem_ld32(S + 96, x + 32);
             }
+            tmem_st32(S + 32 * h, p);
+            tmem_wait_st();
+            tc_fence_before();
+            mbar_arrive(smem_u32(&sh.p_full[t][h]));           // the value product may begin on half of the keys
+            tmem_wait_ld();
         }
         if (!FP8) {
             float s0, s1;
@@ -953,22 +957,6 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
                 auto values_there = [&](int i) {
                     return FP8 ? ch_wait(sh, A, sh.wide_full[at(i) % 2], at(i) / 2) : ch_wait(sh, A, sh.v_full[at(i) % P::VS], at(i) / P::VS);
                 };
-                auto scores = [&](int i, bool pass) {
-                    const uint64_t kd = k0 + (uint64_t)(at(i) % P::KS) * (P::TILE >> 4);
-                    constexpr int STEPS = FP8 ? 2 * (D / 32) : D / 16;
-#pragma unroll
-                    for (int e = 0; e < STEPS; ++e) {
-                        if (e == STEPS / 2 && pass) mbar_arrive(smem_u32(&sh.turn[t ^ 1]));     // queued work covers the hand-over
-                        if (FP8) {
-                            constexpr int PER = D / 32;
-                            mma_ss_e4m3(S, q + (e / PER) * (CH_ROWS * D >> 4) + (e % PER) * 2, kd + (e % PER) * 2, ID_S, e > 0);
-                        } else {
-                            const int off = (e >> 2) * (CH_BLOCK >> 4) + (e & 3) * 2;
-                            mma_ss(S, q + off, kd + off, ID_S, e > 0);
-                        }
-                    }
-                    tc_commit(smem_u32(&sh.event[t][(events + I.event(i, 0)) % CH_EVENTS]));
-                };
                 if (n_mine > 0) {
                     // Tiles that only the other one used: their loads have landed once its products are complete (a barrier's
                     // parity tells phases apart only where none is passed over).
@@ -976,36 +964,50 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
                     behind = false;
                     ok = ch_wait(sh, A, sh.q_full[t], qs++) && keys_there(0);
                     if (!ok) break;
-                    tc_fence_after();
-                    scores(0, false);
-                    for (int i = 0; i < n_mine; ++i) {
-                        if (!(ok = values_there(i))) break;
-                        if (i + 1 < n_mine && !(ok = keys_there(i + 1))) break;
-                        const uint64_t v = v0 + (uint64_t)(FP8 ? at(i) % 2 * (P::WIDE_BYTES >> 4) : at(i) % P::VS * (P::TILE >> 4));
-                        if (!(ok = ch_wait(sh, A, sh.p_full[t][0], weights))) break;
-                        // Both halves of the last dual item have been read.
-                        if (shared && !(ok = ch_wait(sh, A, sh.o_read, shares - 1))) break;
-                        shared = false;
-                        // The other tile's round before this one; that may be the last of an item before.  No phase is
-                        // passed over.
-                        const int x = t ? i : i - 1;
-                        if (turn && x < n_other && turns + x != ~0u && !(ok = ch_wait(sh, A, sh.turn[t], turns + x))) break;
-                        tc_fence_after();
+                    for (int i = 0; i <= n_mine; ++i) {        // the value product of the tile before, then this one's scores
+                        if (i > 0) {
+                            if (!(ok = values_there(i - 1))) break;
+                            if (i < n_mine && !(ok = keys_there(i))) break;
+                            const uint64_t v = v0 + (uint64_t)(FP8 ? at(i - 1) % 2 * (P::WIDE_BYTES >> 4) : at(i - 1) % P::VS * (P::TILE >> 4));
+                            if (!(ok = ch_wait(sh, A, sh.p_full[t][0], weights))) break;
+                            // Both halves of the last dual item have been read.
+                            if (shared && !(ok = ch_wait(sh, A, sh.o_read, shares - 1))) break;
+                            shared = false;
+                            // The other tile's round before this one; that may be the last of an item before.  No phase is
+                            // passed over.
+                            const int x = t ? i - 1 : i - 2;
+                            if (turn && x < n_other && turns + x != ~0u && !(ok = ch_wait(sh, A, sh.turn[t], turns + x))) break;
 #pragma unroll
-                        for (int h = 0; h < 2; ++h) {
-                            if (h > 0) {
-                                if (!(ok = ch_wait(sh, A, sh.p_full[t][1], weights))) break;
+                            for (int h = 0; h < 2; ++h) {
+                                if (h > 0 && !(ok = ch_wait(sh, A, sh.p_full[t][1], weights))) break;
                                 tc_fence_after();
-                            }
 #pragma unroll
-                            for (int e = 4 * h; e < 4 * h + 4; ++e) mma_ts(O, S + 8 * e, v + e * (2048 >> 4), ID_O, i > 0 || e > 0);
+                                for (int e = 4 * h; e < 4 * h + 4; ++e) mma_ts(O, S + 8 * e, v + e * (2048 >> 4), ID_O, i > 1 || e > 0);
+                            }
+                            if (!ok) break;
+                            ++weights;
+                            // One commit for the next scores stands for the value product before them as well.
+                            if (i == n_mine || I.dual) tc_commit(smem_u32(&sh.event[t][(events + I.event(i - 1, 1)) % CH_EVENTS]));
                         }
-                        if (!ok) break;
-                        ++weights;
-                        const bool more = i + 1 < n_mine;
-                        if (!more || I.dual) tc_commit(smem_u32(&sh.event[t][(events + I.event(i, 1)) % CH_EVENTS]));
-                        if (more) scores(i + 1, turn);
-                        else if (turn) mbar_arrive(smem_u32(&sh.turn[t ^ 1]));
+                        if (i == n_mine) {
+                            if (turn) mbar_arrive(smem_u32(&sh.turn[t ^ 1]));
+                            break;
+                        }
+                        tc_fence_after();
+                        const uint64_t kd = k0 + (uint64_t)(at(i) % P::KS) * (P::TILE >> 4);
+                        constexpr int STEPS = FP8 ? 2 * (D / 32) : D / 16;
+#pragma unroll
+                        for (int e = 0; e < STEPS; ++e) {
+                            if (e == STEPS / 2 && turn && i > 0) mbar_arrive(smem_u32(&sh.turn[t ^ 1]));      // queued work covers the hand-over
+                            if (FP8) {
+                                constexpr int PER = D / 32;
+                                mma_ss_e4m3(S, q + (e / PER) * (CH_ROWS * D >> 4) + (e % PER) * 2, kd + (e % PER) * 2, ID_S, e > 0);
+                            } else {
+                                const int off = (e >> 2) * (CH_BLOCK >> 4) + (e & 3) * 2;
+                                mma_ss(S, q + off, kd + off, ID_S, e > 0);
+                            }
+                        }
+                        tc_commit(smem_u32(&sh.event[t][(events + I.event(i, 0)) % CH_EVENTS]));
                     }
                     if (!ok) break;
                     events += I.events(t);
