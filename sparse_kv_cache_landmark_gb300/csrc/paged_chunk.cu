@@ -67,7 +67,7 @@ struct ChShape<D, true> {
     static constexpr int Q = 2 * CH_ROWS * D;                   // the two pieces
     static constexpr int TILE = CH_KEYS * D;                    // of K or V as they are
     static constexpr int WIDE_BYTES = CH_KEYS * D * 2;          // of V in f16
-    static constexpr int KS = 4, VS = 2;
+    static constexpr int KS = D == 128 ? 2 : 4, VS = 2;
     static constexpr int TILES = 2 * Q + (KS + VS) * TILE + 2 * WIDE_BYTES;
 };
 
@@ -124,7 +124,8 @@ struct ChShared {
     uint64_t q_full[2], k_full[4], v_full[4], raw_free[2], wide_full[2], event[2][CH_EVENTS], p_full[2][2], turn[2], drain[2], v_tail, item_full[CH_ITEMS],
         item_free[CH_ITEMS], sc_full[CH_SCALES], ml_there, weights_there, o_read;
     ChunkItem item[CH_ITEMS];
-    float k_scale[CH_SCALES][8], v_log[CH_SCALES][8];          // of each 16 keys of a tile: k_scale, log2 of v_scale
+    alignas(16) float k_scale[CH_SCALES][8];
+    alignas(16) float v_log[CH_SCALES][8];          // of each 16 keys of a tile: k_scale, log2 of v_scale
     uint32_t bad[CH_SCALES];       // groups of 16 keys in pages that do not exist
     int8_t q_exp[2][2][CH_ROWS];   // q's pieces are its values times 2^this; CH_NAN: not finite
     uint32_t tmem;
@@ -344,6 +345,23 @@ __device__ __forceinline__ void st_global_32(void* p, const uint32_t (&v)[8]) {
                  "r"(v[5]), "r"(v[6]), "r"(v[7])
                  : "memory");
 }
+// One arrival for the warp, after what all its threads did.  (32 of them are made one by one.)
+__device__ __forceinline__ void warp_arrive(uint64_t& bar) {
+    __syncwarp();
+    if ((threadIdx.x & 31) == 0) mbar_arrive(smem_u32(&bar));
+}
+// A barrier of 128 threads, and whether any of them asked for `x`.  One warp waits for an mbarrier and the others here:
+// every warp that waits at an mbarrier is woken by others' arrivals, and takes issue slots.
+__device__ __forceinline__ bool group_any(int id, bool x) {
+    uint32_t any;
+    asm volatile(
+        "{\n .reg .pred p, q;\n setp.ne.u32 p, %1, 0;\n barrier.cta.red.or.pred.aligned q, %2, 128, p;\n selp.u32 %0, 1, 0, q;\n}\n"
+        : "=r"(any)
+        : "r"((uint32_t)x), "r"(id)
+        : "memory");
+    return any != 0;
+}
+
 // The softmax of one tile of an item: a thread owns a row; it sees its request's keys [0, limit).  False: a wait gave up.
 template <int D, bool FP8>
 __device__ __forceinline__ bool ch_softmax(ChShared& sh, const ChunkArgs& A, const ChunkItem& I, int t, uint32_t events, uint32_t keys, int turn,
@@ -365,15 +383,15 @@ __device__ __forceinline__ bool ch_softmax(ChShared& sh, const ChunkArgs& A, con
     const int step = I.dual ? 2 : 1;                                    // of the item's tiles of keys, from tile j on
     int j = I.dual ? t : 0;
     for (int i = 0; i < n_tiles; ++i, j += step) {
-        bool ok = ch_event(sh, A, t, events + (step == 2 ? 2 * i : i));
         const uint32_t slot = (keys + j) % CH_SCALES;
+        bool ok = true;
+        if ((threadIdx.x & 96) == 0)           // the group's first warp
+            ok = ch_event(sh, A, t, events + (step == 2 ? 2 * i : i)) && ch_wait(sh, A, sh.sc_full[slot], (keys + j) / CH_SCALES);
+        if (group_any(1 + t, !ok)) return false;
         if (!any) {                // no rows in this warp: nothing reads what its lanes of P and O hold
-            if (!__all_sync(0xffffffffu, ok)) return false;
-            for (int h = 0; h < 2; ++h) mbar_arrive(smem_u32(&sh.p_full[t][h]));
+            for (int h = 0; h < 2; ++h) warp_arrive(sh.p_full[t][h]);
             continue;
         }
-        ok = ok && ch_wait(sh, A, sh.sc_full[slot], (keys + j) / CH_SCALES);
-        if (!__all_sync(0xffffffffu, ok)) return false;
         tc_fence_after();
         if (FP8 && i == 0) {
             const int e = sh.q_exp[turn][t][row];
@@ -382,8 +400,8 @@ __device__ __forceinline__ bool ch_softmax(ChShared& sh, const ChunkArgs& A, con
         const uint32_t bad = sh.bad[slot];
         const int rem = min(limit - j * CH_KEYS, CH_KEYS);
         const bool edge = bad || __any_sync(0xffffffffu, rem < CH_KEYS);
-        auto scale_of = [&](int g) {           // of the g-th 16 scores
-            return FP8 ? fmaxf(sh.k_scale[slot][g] * q_scale, 1.2e-38f) : q_scale;      // (a masked score times zero would be NaN)
+        auto scale_of = [&](float k_scale) {   // (a masked score times zero would be NaN)
+            return FP8 ? fmaxf(k_scale * q_scale, 1.2e-38f) : q_scale;
         };
         auto top_of = [](const uint32_t* x) {
             float u = fmaxf(__uint_as_float(x[0]), __uint_as_float(x[1])), v = fmaxf(__uint_as_float(x[2]), __uint_as_float(x[3]));
@@ -439,8 +457,10 @@ __device__ __forceinline__ bool ch_softmax(ChShared& sh, const ChunkArgs& A, con
             tmem_ld32(S + 64 * h + 32, x + 32);
             tmem_wait_ld();
             if (FP8) {
+                const float4 k = *reinterpret_cast<const float4*>(&sh.k_scale[slot][4 * h]), v = *reinterpret_cast<const float4*>(&sh.v_log[slot][4 * h]);
+                const float ks[4] = {k.x, k.y, k.z, k.w}, vs[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-                for (int g = 0; g < 4; ++g) top = fmaxf(top, fmaf(top_of(x + 16 * g), scale_of(4 * h + g), sh.v_log[slot][4 * h + g]));
+                for (int g = 0; g < 4; ++g) top = fmaxf(top, fmaf(top_of(x + 16 * g), scale_of(ks[g]), vs[g]));
             } else {
 #pragma unroll
                 for (int g = 0; g < 4; g += 2) top = max3(top, top_of(x + 16 * g), top_of(x + 16 * g + 16));
@@ -470,15 +490,16 @@ __device__ __forceinline__ bool ch_softmax(ChShared& sh, const ChunkArgs& A, con
 #pragma unroll 1
         for (int h = 0; h < 2; ++h) {          // (the first half is still there)
             uint32_t p[32];
+            const float4 k = *reinterpret_cast<const float4*>(&sh.k_scale[slot][4 * h]), v = *reinterpret_cast<const float4*>(&sh.v_log[slot][4 * h]);
+            const float ks[4] = {k.x, k.y, k.z, k.w}, vs[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
             for (int g = 0; g < 4; ++g) {
                 if (FP8) {
                     sum[0] = sum[1] = 0ull;
-                    const float v_log = sh.v_log[slot][4 * h + g];
-                    weights(x + 16 * g, p + 8 * g, scale_of(4 * h + g), b + v_log, sum);
+                    weights(x + 16 * g, p + 8 * g, scale_of(ks[g]), b + vs[g], sum);
                     float s0, s1;
                     unpack2(add2(sum[0], sum[1]), s0, s1);
-                    total = fmaf(s0 + s1, ex2(-v_log), total);
+                    total = fmaf(s0 + s1, ex2(-vs[g]), total);
                 } else {
                     weights(x + 16 * g, p + 8 * g, q_scale, b, sum);
                 }
@@ -490,7 +511,7 @@ __device__ __forceinline__ bool ch_softmax(ChShared& sh, const ChunkArgs& A, con
             tmem_st32(S + 32 * h, p);
             tmem_wait_st();
             tc_fence_before();
-            mbar_arrive(smem_u32(&sh.p_full[t][h]));           // the value product may begin on half of the keys
+            warp_arrive(sh.p_full[t][h]);      // the value product may begin on half of the keys
             tmem_wait_ld();
         }
         if (!FP8) {
@@ -502,8 +523,9 @@ __device__ __forceinline__ bool ch_softmax(ChShared& sh, const ChunkArgs& A, con
     }
     if (FP8 && any && n_tiles > 0 && sh.q_exp[turn][t][row] == CH_NAN) l = __uint_as_float(0x7FC00000u);
     if (n_tiles > 0) {
-        const bool ok = ch_event(sh, A, t, events + I.event(n_tiles - 1, 1));
-        if (!__all_sync(0xffffffffu, ok)) return false;
+        bool ok = true;
+        if ((threadIdx.x & 96) == 0) ok = ch_event(sh, A, t, events + I.event(n_tiles - 1, 1));
+        if (group_any(1 + t, !ok)) return false;
         tc_fence_after();
     }
     // A dual item's halves: this thread writes half of the row's values, from both.
@@ -513,15 +535,15 @@ __device__ __forceinline__ bool ch_softmax(ChShared& sh, const ChunkArgs& A, con
         bool ok = true;
         if (t == 1) {
             sh.share[row] = make_float2(m, l);
-            mbar_arrive(smem_u32(&sh.ml_there));
-            ok = ch_wait(sh, A, sh.weights_there, shares);
-            if (!__all_sync(0xffffffffu, ok)) return false;
+            warp_arrive(sh.ml_there);
+            if ((threadIdx.x & 96) == 0) ok = ch_wait(sh, A, sh.weights_there, shares);
+            if (group_any(2, !ok)) return false;
             const float2 x = sh.share[row];
             w0 = x.x;
             w1 = x.y;
         } else {
-            ok = ch_wait(sh, A, sh.ml_there, shares);
-            if (!__all_sync(0xffffffffu, ok)) return false;
+            if ((threadIdx.x & 96) == 0) ok = ch_wait(sh, A, sh.ml_there, shares);
+            if (group_any(1, !ok)) return false;
             const float2 x = sh.share[row];
             const float to = fmaxf(l != 0.f ? m : -INFINITY, x.y != 0.f ? x.x : -INFINITY);
             w0 = l != 0.f ? ex2(m - to) : 0.f;                 // one that saw nothing has weight 0
@@ -534,7 +556,7 @@ __device__ __forceinline__ bool ch_softmax(ChShared& sh, const ChunkArgs& A, con
                 w1 *= inv;
             }
             sh.share[row] = make_float2(w0, w1);
-            mbar_arrive(smem_u32(&sh.weights_there));
+            warp_arrive(sh.weights_there);
         }
         ++shares;
     } else if (I.part < 0) {
@@ -598,7 +620,7 @@ __device__ __forceinline__ bool ch_softmax(ChShared& sh, const ChunkArgs& A, con
         }
     if (both) {                    // the next item's value products may go over these sums
         tc_fence_before();
-        mbar_arrive(smem_u32(&sh.o_read));
+        warp_arrive(sh.o_read);
     }
     if (real && (!both || t == 0)) {
         if (I.part >= 0) A.part_ml[at * CH_ROWS + row] = make_float2(m, l);
@@ -680,9 +702,12 @@ __device__ __forceinline__ void ch_widen_v(const uint8_t* from, uint8_t* to, int
         if (row0 + k * (128 / CH) >= have)
 #pragma unroll
             for (int i = 0; i < 8; ++i) o[i] = 0u;
+        // Eight lanes hold a row; half of them begin with the second chunk, so that the eight meet all banks.
         uint8_t* to_row = b + k * (128 / CH) * 128;
-        *reinterpret_cast<uint4*>(to_row + x0) = make_uint4(o[0], o[1], o[2], o[3]);
-        *reinterpret_cast<uint4*>(to_row + x1) = make_uint4(o[4], o[5], o[6], o[7]);
+        const bool second = c / 4 & 1;
+        const uint4 lo = make_uint4(o[0], o[1], o[2], o[3]), hi = make_uint4(o[4], o[5], o[6], o[7]);
+        *reinterpret_cast<uint4*>(to_row + (second ? x1 : x0)) = second ? hi : lo;
+        *reinterpret_cast<uint4*>(to_row + (second ? x0 : x1)) = second ? lo : hi;
     }
 }
 
@@ -705,13 +730,13 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
         for (int i = 0; i < P::VS; ++i) mbar_init(smem_u32(&sh.v_full[i]), 1);
         for (int i = 0; i < 2; ++i) mbar_init(smem_u32(&sh.raw_free[i]), 4);
         for (int i = 0; i < 2; ++i) mbar_init(smem_u32(&sh.wide_full[i]), 4);
-        mbar_init(smem_u32(&sh.ml_there), 128);
-        mbar_init(smem_u32(&sh.weights_there), 128);
-        mbar_init(smem_u32(&sh.o_read), 256);
+        mbar_init(smem_u32(&sh.ml_there), 4);
+        mbar_init(smem_u32(&sh.weights_there), 4);
+        mbar_init(smem_u32(&sh.o_read), 8);
         for (int t = 0; t < 2; ++t) {
             mbar_init(smem_u32(&sh.q_full[t]), FP8 ? 4 : 1);
             for (int i = 0; i < CH_EVENTS; ++i) mbar_init(smem_u32(&sh.event[t][i]), 1);
-            for (int i = 0; i < 2; ++i) mbar_init(smem_u32(&sh.p_full[t][i]), 128);
+            for (int i = 0; i < 2; ++i) mbar_init(smem_u32(&sh.p_full[t][i]), 4);
             mbar_init(smem_u32(&sh.turn[t]), 1);
             mbar_init(smem_u32(&sh.drain[t]), 1);
         }
@@ -1032,17 +1057,22 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
                 bool ok = true;
                 while (ok) {
                     ChunkItem I;
-                    ok = next_item(item, I);
-                    if (!__all_sync(0xffffffffu, ok)) break;
+                    if (warp == 12) ok = ch_wait(sh, A, sh.item_full[item % CH_ITEMS], item / CH_ITEMS);
+                    ok = !group_any(3, !ok);
+                    if (!ok) break;
+                    I = sh.item[item % CH_ITEMS];
+                    __syncwarp();
                     if (lane == 0) free_item(item);
                     if (I.n0 < 0) break;
                     const bool copy = I.dual && I.n1 > 0;                 // both take the same rows
 #pragma unroll
                     for (int t = 0; t < 2; ++t) {
                         if (I.n(t) == 0 || (copy && t == 1) || !ok) continue;
-                        if (q_free[t] != ~0u) ok = ch_event(sh, A, t, q_free[t]);
-                        if (copy && ok && q_free[1] != ~0u) ok = ch_event(sh, A, 1, q_free[1]);
-                        ok = __all_sync(0xffffffffu, ok);
+                        if (warp == 12) {
+                            if (q_free[t] != ~0u) ok = ch_event(sh, A, t, q_free[t]);
+                            if (copy && ok && q_free[1] != ~0u) ok = ch_event(sh, A, 1, q_free[1]);
+                        }
+                        ok = !group_any(3, !ok);
                         if (!ok) continue;
                         int8_t* const exponent = &sh.q_exp[turn[t]++ & 1][t][row];
                         ch_split_q<D>(A, I, t, row, smem + t * P::Q, copy ? smem + P::Q : nullptr, exponent);
@@ -1057,13 +1087,16 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
                     ++item;
                     for (int j = 0; j < I.tiles && ok; ++j) {
                         const int st = tiles % P::VS, w = tiles % 2;
-                        ok = ch_wait(sh, A, sh.v_full[st], tiles / P::VS);
+                        if (warp == 12) {
+                            ok = ch_wait(sh, A, sh.v_full[st], tiles / P::VS);
 #pragma unroll
-                        for (int t = 0; t < 2; ++t) {
-                            const uint32_t e = w ? wide_free[1][t] : wide_free[0][t];
-                            if (ok && e != ~0u) ok = ch_event(sh, A, t, e);
+                            for (int t = 0; t < 2; ++t) {
+                                const uint32_t e = w ? wide_free[1][t] : wide_free[0][t];
+                                if (ok && e != ~0u) ok = ch_event(sh, A, t, e);
+                            }
                         }
-                        if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
+                        ok = !group_any(3, !ok);
+                        if (!ok) break;
                         ch_widen_v<D>(smem + V0 + st * P::TILE, smem + WIDE0 + w * P::WIDE_BYTES, I.len - (I.first + j) * CH_KEYS);
                         fence_async_smem();
                         __syncwarp();
@@ -1096,8 +1129,9 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
         uint32_t item = 0, events = 0, keys = 0, shares = 0, turn = 0;     // turn: of the items that this tile has a part in
         while (true) {
             // The item stays where it is: 128 scores leave few registers.
-            const bool ok = ch_wait(sh, A, sh.item_full[item % CH_ITEMS], item / CH_ITEMS);
-            if (!__all_sync(0xffffffffu, ok)) break;
+            bool ok = true;
+            if ((warp & 3) == 0) ok = ch_wait(sh, A, sh.item_full[item % CH_ITEMS], item / CH_ITEMS);
+            if (group_any(1 + t, !ok)) break;
             const ChunkItem& I = sh.item[item % CH_ITEMS];
             if (I.n0 < 0) break;
             if (!ch_softmax<D, FP8>(sh, A, I, t, events, keys, turn & 1, shares)) break;
