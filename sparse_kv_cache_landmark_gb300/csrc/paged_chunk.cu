@@ -63,7 +63,7 @@ struct ChShape<D, false> {
 template <int D>
 struct ChShape<D, true> {
     static constexpr int THREADS = 512;
-    static constexpr int REGS_SOFTMAX = 152, REGS_OTHER = 104;
+    static constexpr int REGS_SOFTMAX = 160, REGS_OTHER = 96;
     static constexpr int Q = 2 * CH_ROWS * D;                   // the two pieces
     static constexpr int TILE = CH_KEYS * D;                    // of K or V as they are
     static constexpr int WIDE_BYTES = CH_KEYS * D * 2;          // of V in f16
@@ -139,6 +139,13 @@ struct ChShared {
         float2 share[CH_ROWS];     // the two halves of a dual item: maximum and sum one way, weights the other
     };
 };
+
+// Whole warp: true for one of its threads, the same each time; the compiler knows that it is one.
+__device__ __forceinline__ bool elect_one() {
+    uint32_t p;
+    asm volatile("{\n .reg .pred q;\n elect.sync _|q, 0xffffffff;\n selp.u32 %0, 1, 0, q;\n}\n" : "=r"(p));
+    return p != 0;
+}
 
 __device__ __forceinline__ bool ch_wait_long(int* abort, int32_t* status, uint32_t bar, uint32_t parity, long long limit) {
     const uint64_t t0 = global_ns();
@@ -719,7 +726,7 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
     using P = ChShape<D, FP8>;
     extern __shared__ __align__(1024) uint8_t smem[];           // the tiles, then ChShared
     ChShared& sh = *reinterpret_cast<ChShared*>(smem + P::TILES);
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
     const uint32_t base = smem_u32(smem);
     constexpr uint32_t K0 = 2 * P::Q, V0 = K0 + P::KS * P::TILE, WIDE0 = V0 + P::VS * P::TILE;
     if (tid == 0) {
@@ -955,7 +962,7 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
             // with it the CTA and its shared memory.  (`abort` is final only once all have left their waits: below.)
             __syncwarp();
             if (lane == 0) { sh.q_issued[0] = q_issued[0]; sh.q_issued[1] = q_issued[1]; }
-        } else if ((warp == 8 || warp == 10) && lane == 0) {
+        } else if ((warp == 8 || warp == 10) && elect_one()) {
             // ------------------------------------------------ matrix products of one tile
             // The tensor cores queue a few instructions only; with a thread of its own for each tile, one tile's waits and
             // commits pass while the other's products run.  They take turns, so that the tiles stay half a period apart.
