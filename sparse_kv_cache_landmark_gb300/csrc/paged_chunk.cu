@@ -57,18 +57,19 @@ struct ChShape<D, false> {
     static constexpr int Q = CH_ROWS * D * 2;                   // bytes of a tile of q
     static constexpr int TILE = CH_KEYS * D * 2;                // of K or V
     static constexpr int KS = D == 128 ? 2 : 4, VS = KS;        // stages of K and of V: even numbers (see `dual`)
-    static constexpr int WIDE_BYTES = 0;
+    static constexpr int WIDE_BYTES = 0, WIDES = 1;
     static constexpr int TILES = 2 * Q + (KS + VS) * TILE;
 };
 template <int D>
 struct ChShape<D, true> {
     static constexpr int THREADS = 512;
-    static constexpr int REGS_SOFTMAX = 160, REGS_OTHER = 96;
+    static constexpr int REGS_SOFTMAX = 168, REGS_OTHER = 88;
     static constexpr int Q = 2 * CH_ROWS * D;                   // the two pieces
     static constexpr int TILE = CH_KEYS * D;                    // of K or V as they are
     static constexpr int WIDE_BYTES = CH_KEYS * D * 2;          // of V in f16
     static constexpr int KS = D == 128 ? 2 : 4, VS = 2;
-    static constexpr int TILES = 2 * Q + (KS + VS) * TILE + 2 * WIDE_BYTES;
+    static constexpr int WIDES = 3;                             // (any number: tiles are widened in their order)
+    static constexpr int TILES = 2 * Q + (KS + VS) * TILE + WIDES * WIDE_BYTES;
 };
 
 struct ChunkArgs {
@@ -121,7 +122,7 @@ struct ChunkItem {
 };
 
 struct ChShared {
-    uint64_t q_full[2], k_full[4], v_full[4], raw_free[2], wide_full[2], event[2][CH_EVENTS], p_full[2][2], turn[2], drain[2], v_tail, item_full[CH_ITEMS],
+    uint64_t q_full[2], k_full[4], v_full[4], raw_free[2], wide_full[3], event[2][CH_EVENTS], p_full[2][2], turn[2], drain[2], v_tail, item_full[CH_ITEMS],
         item_free[CH_ITEMS], sc_full[CH_SCALES], ml_there, weights_there, o_read;
     ChunkItem item[CH_ITEMS];
     alignas(16) float k_scale[CH_SCALES][8];
@@ -736,7 +737,7 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
         for (int i = 0; i < P::KS; ++i) mbar_init(smem_u32(&sh.k_full[i]), 1);
         for (int i = 0; i < P::VS; ++i) mbar_init(smem_u32(&sh.v_full[i]), 1);
         for (int i = 0; i < 2; ++i) mbar_init(smem_u32(&sh.raw_free[i]), 4);
-        for (int i = 0; i < 2; ++i) mbar_init(smem_u32(&sh.wide_full[i]), 4);
+        for (int i = 0; i < P::WIDES; ++i) mbar_init(smem_u32(&sh.wide_full[i]), 4);
         mbar_init(smem_u32(&sh.ml_there), 4);
         mbar_init(smem_u32(&sh.weights_there), 4);
         mbar_init(smem_u32(&sh.o_read), 8);
@@ -987,7 +988,7 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
                 auto at = [&](int i) { return tiles + (I.dual ? 2 * i + t : i); };
                 auto keys_there = [&](int i) { return ch_wait(sh, A, sh.k_full[at(i) % P::KS], at(i) / P::KS); };
                 auto values_there = [&](int i) {
-                    return FP8 ? ch_wait(sh, A, sh.wide_full[at(i) % 2], at(i) / 2) : ch_wait(sh, A, sh.v_full[at(i) % P::VS], at(i) / P::VS);
+                    return FP8 ? ch_wait(sh, A, sh.wide_full[at(i) % P::WIDES], at(i) / P::WIDES) : ch_wait(sh, A, sh.v_full[at(i) % P::VS], at(i) / P::VS);
                 };
                 if (n_mine > 0) {
                     // Tiles that only the other one used: their loads have landed once its products are complete (a barrier's
@@ -1000,7 +1001,7 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
                         if (i > 0) {
                             if (!(ok = values_there(i - 1))) break;
                             if (i < n_mine && !(ok = keys_there(i))) break;
-                            const uint64_t v = v0 + (uint64_t)(FP8 ? at(i - 1) % 2 * (P::WIDE_BYTES >> 4) : at(i - 1) % P::VS * (P::TILE >> 4));
+                            const uint64_t v = v0 + (uint64_t)(FP8 ? at(i - 1) % P::WIDES * (P::WIDE_BYTES >> 4) : at(i - 1) % P::VS * (P::TILE >> 4));
                             if (!(ok = ch_wait(sh, A, sh.p_full[t][0], weights))) break;
                             // Both halves of the last dual item have been read.
                             if (shared && !(ok = ch_wait(sh, A, sh.o_read, shares - 1))) break;
@@ -1059,7 +1060,7 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
         } else if (FP8 && warp >= 12) {
             // ------------------------------------------------ q and V of 8-bit pages
             if constexpr (FP8) {
-                uint32_t item = 0, tiles = 0, turn[2] = {0, 0}, events[2] = {0, 0}, q_free[2] = {~0u, ~0u}, wide_free[2][2] = {{~0u, ~0u}, {~0u, ~0u}};
+                uint32_t item = 0, tiles = 0, turn[2] = {0, 0}, events[2] = {0, 0}, q_free[2] = {~0u, ~0u}, e0 = ~0u, e1 = ~0u;         // of buffer `lane`: the events that free it
                 const int row = tid & 127;
                 bool ok = true;
                 while (ok) {
@@ -1093,14 +1094,12 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
                     }
                     ++item;
                     for (int j = 0; j < I.tiles && ok; ++j) {
-                        const int st = tiles % P::VS, w = tiles % 2;
+                        const int st = tiles % P::VS, w = tiles % P::WIDES;
+                        const uint32_t free0 = __shfl_sync(0xffffffffu, e0, w), free1 = __shfl_sync(0xffffffffu, e1, w);
                         if (warp == 12) {
                             ok = ch_wait(sh, A, sh.v_full[st], tiles / P::VS);
-#pragma unroll
-                            for (int t = 0; t < 2; ++t) {
-                                const uint32_t e = w ? wide_free[1][t] : wide_free[0][t];
-                                if (ok && e != ~0u) ok = ch_event(sh, A, t, e);
-                            }
+                            if (ok && free0 != ~0u) ok = ch_event(sh, A, 0, free0);
+                            if (ok && free1 != ~0u) ok = ch_event(sh, A, 1, free1);
                         }
                         ok = !group_any(3, !ok);
                         if (!ok) break;
@@ -1112,11 +1111,9 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
                             mbar_arrive(smem_u32(&sh.wide_full[w]));
                         }
                         const int i = I.dual ? j >> 1 : j;
-#pragma unroll
-                        for (int t = 0; t < 2; ++t) {
-                            const uint32_t e = (I.dual ? (j & 1) == t : j < I.n(t)) ? events[t] + I.event(i, 1) : ~0u;
-                            if (w) wide_free[1][t] = e;
-                            else wide_free[0][t] = e;
+                        if (lane == w) {
+                            e0 = (I.dual ? !(j & 1) : j < I.n0) ? events[0] + I.event(i, 1) : ~0u;
+                            e1 = (I.dual ? j & 1 : j < I.n1) ? events[1] + I.event(i, 1) : ~0u;
                         }
                         ++tiles;
                     }
