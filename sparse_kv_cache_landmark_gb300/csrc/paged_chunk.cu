@@ -15,7 +15,7 @@
 //   8, 10    one thread each issues the tcgen05.mma of tile 0 and 1: S_t = Q_t K^T and O_t += P_t V,
 //   0-3, 4-7 the softmax of tile 0 and 1, one thread per row: S from tensor memory, online maximum and sum in fp32, P (bf16, or
 //            f16 next to e4m3) back over S,
-//   12-15    (e4m3) q to its 8-bit form, V to f16.
+//   12-15    (e4m3) V to f16.
 // An item's first scores are issued behind the last value product of the one before, and its first loads before that.
 //
 // e4m3.  K goes to the tensor cores as it is: a row of q, times a power of two that brings its largest value to 2^7..2^8, is
@@ -38,6 +38,8 @@
 
 namespace kvo {
 
+size_t round256(size_t x);
+
 constexpr int CH_ROWS = 128;               // query rows of a tile
 constexpr int CH_KEYS = 128;               // keys of a tile
 constexpr int CH_BLOCK = CH_ROWS * 128;    // bytes of 128 rows of 128
@@ -45,7 +47,7 @@ constexpr float CH_RAISE = 8.f;            // log2: how far a score may pass the
 constexpr int CH_CTAS = 152;               // ranges at most: one CTA to an SM
 constexpr int CH_EVENTS = 16;              // barriers that a tile's products complete in turn
 constexpr int CH_ITEMS = 4;                // descriptors
-constexpr int CH_NAN = -128;
+constexpr int CH_NAN = -128;               // the exponent of a row of q that is not finite
 constexpr int CH_SCALES = 8;               // tiles of keys whose scales are held
 
 template <int D, bool FP8>
@@ -75,6 +77,7 @@ struct ChShape<D, true> {
 struct ChunkArgs {
     const uint16_t* q;
     int64_t q_stride;
+    const int8_t* q_exp;           // e4m3 pages: q's pieces are its values times 2^this
     const float* k_scale;
     const float* v_scale;
     const int32_t* table;
@@ -128,7 +131,6 @@ struct ChShared {
     alignas(16) float k_scale[CH_SCALES][8];
     alignas(16) float v_log[CH_SCALES][8];          // of each 16 keys of a tile: k_scale, log2 of v_scale
     uint32_t bad[CH_SCALES];       // groups of 16 keys in pages that do not exist
-    int8_t q_exp[2][2][CH_ROWS];   // q's pieces are its values times 2^this; CH_NAN: not finite
     uint32_t tmem;
     int abort;
     int issued, tail_open, tail_phase, q_issued[2];
@@ -372,8 +374,7 @@ __device__ __forceinline__ bool group_any(int id, bool x) {
 
 // The softmax of one tile of an item: a thread owns a row; it sees its request's keys [0, limit).  False: a wait gave up.
 template <int D, bool FP8>
-__device__ __forceinline__ bool ch_softmax(ChShared& sh, const ChunkArgs& A, const ChunkItem& I, int t, uint32_t events, uint32_t keys, int turn,
-                                           uint32_t& shares) {
+__device__ __forceinline__ bool ch_softmax(ChShared& sh, const ChunkArgs& A, const ChunkItem& I, int t, uint32_t events, uint32_t keys, uint32_t& shares) {
     const uint32_t lanes = (uint32_t)(threadIdx.x & 96) << 16;          // this warp's quarter of the lanes
     const uint32_t S = sh.tmem + 128 * t + lanes, O = sh.tmem + 256 + D * t + lanes;
     const int row = threadIdx.x & 127, tl = row / A.r, head = row - tl * A.r;
@@ -388,6 +389,8 @@ __device__ __forceinline__ bool ch_softmax(ChShared& sh, const ChunkArgs& A, con
     constexpr float CH_BIAS = FP8 ? 6.f : 0.f;
     float m = -INFINITY, l = 0.f;
     float q_scale = A.scale_log2;
+    int q_exp = 0;
+    if (FP8 && real) q_exp = A.q_exp[(I.row + tok) * A.hq + I.g * A.r + head];
     const int step = I.dual ? 2 : 1;                                    // of the item's tiles of keys, from tile j on
     int j = I.dual ? t : 0;
     for (int i = 0; i < n_tiles; ++i, j += step) {
@@ -401,10 +404,7 @@ __device__ __forceinline__ bool ch_softmax(ChShared& sh, const ChunkArgs& A, con
             continue;
         }
         tc_fence_after();
-        if (FP8 && i == 0) {
-            const int e = sh.q_exp[turn][t][row];
-            q_scale = e == CH_NAN ? 0.f : __uint_as_float((uint32_t)(127 - e) << 23) * A.scale_log2;
-        }
+        if (FP8 && i == 0) q_scale = q_exp == CH_NAN ? 0.f : __uint_as_float((uint32_t)(127 - q_exp) << 23) * A.scale_log2;
         const uint32_t bad = sh.bad[slot];
         const int rem = min(limit - j * CH_KEYS, CH_KEYS);
         const bool edge = bad || __any_sync(0xffffffffu, rem < CH_KEYS);
@@ -529,7 +529,7 @@ __device__ __forceinline__ bool ch_softmax(ChShared& sh, const ChunkArgs& A, con
         }
         l += total;
     }
-    if (FP8 && any && n_tiles > 0 && sh.q_exp[turn][t][row] == CH_NAN) l = __uint_as_float(0x7FC00000u);
+    if (q_exp == CH_NAN && n_tiles > 0) l = __uint_as_float(0x7FC00000u);
     if (n_tiles > 0) {
         bool ok = true;
         if ((threadIdx.x & 96) == 0) ok = ch_event(sh, A, t, events + I.event(n_tiles - 1, 1));
@@ -638,56 +638,52 @@ __device__ __forceinline__ bool ch_softmax(ChShared& sh, const ChunkArgs& A, con
 }
 
 // ------------------------------------------------------------------ q and V of 8-bit pages
-// Row `row` of tile t of an item's q as the sum of two e4m3 pieces; times 2^*exponent.  `too`, if not NULL,
-// gets the same.
+// The launch before the others, next to e4m3 pages: the rows of q as sums of two e4m3 pieces, q8 [2][rows][D], times
+// 2^q_exp[row]; D / 16 threads to a row.
+constexpr int CS_THREADS = 256;
 template <int D>
-__device__ __forceinline__ void ch_split_q(const ChunkArgs& A, const ChunkItem& I, int t, int row, uint8_t* to, uint8_t* too, int8_t* exponent) {
-    const int tl = row / A.r, head = row - tl * A.r, tok = I.tok0 + t * A.tq + tl;
-    const bool real = tl < A.tq && tok < I.nq;
-    const uint4* q = reinterpret_cast<const uint4*>(A.q + (I.row + tok) * A.q_stride + (int64_t)(I.g * A.r + head) * D);
+__global__ void __launch_bounds__(CS_THREADS) paged_chunk_split_kernel(const uint16_t* q, int64_t q_stride, int hq, int64_t rows, uint8_t* q8, int8_t* q_exp) {
+    constexpr int LANES = D / 16;
+    grid_wait();
+    grid_launch_next();
+    const int64_t i = (int64_t)blockIdx.x * CS_THREADS + threadIdx.x, row = i / LANES;
+    const int c = (int)(i % LANES);
+    const bool in = row < rows;
+    uint4 v[2] = {make_uint4(0, 0, 0, 0), make_uint4(0, 0, 0, 0)};
+    if (in) {
+        const int64_t tok = row / hq;
+        const uint4* from = reinterpret_cast<const uint4*>(q + tok * q_stride + (row - tok * hq) * D) + 2 * c;
+        v[0] = __ldg(from);
+        v[1] = __ldg(from + 1);
+    }
+    const uint32_t w[8] = {v[0].x, v[0].y, v[0].z, v[0].w, v[1].x, v[1].y, v[1].z, v[1].w};
     uint32_t top2 = 0;
-    if (real)
-#pragma unroll 8
-        for (int i = 0; i < D / 8; ++i) {
-            const uint4 v = __ldg(q + i);
-            top2 = __vmaxu2(top2, __vmaxu2(__vmaxu2(v.x & 0x7FFF7FFFu, v.y & 0x7FFF7FFFu), __vmaxu2(v.z & 0x7FFF7FFFu, v.w & 0x7FFF7FFFu)));
-        }
+#pragma unroll
+    for (int k = 0; k < 8; ++k) top2 = __vmaxu2(top2, w[k] & 0x7FFF7FFFu);
+#pragma unroll
+    for (int o = 1; o < LANES; o <<= 1) top2 = __vmaxu2(top2, __shfl_xor_sync(0xffffffffu, top2, o));
     const uint32_t top = max(top2 & 0xFFFFu, top2 >> 16);     // the largest magnitude's bits
     const bool finite = top < 0x7F80u;
     const int e = min(7 - ((int)(top >> 7) - 127), 120);      // 2^7 <= largest * 2^e < 2^8
     const float up = finite ? __uint_as_float((uint32_t)(e + 127) << 23) : 0.f;
-    *exponent = (int8_t)(finite ? e : CH_NAN);
-#pragma unroll 2
-    for (int c = 0; c < D / 16; ++c) {
-        uint32_t a[4], b[4];
+    uint32_t a[4], b[4];
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            uint4 v = make_uint4(0, 0, 0, 0);
-            if (real && finite) v = __ldg(q + 2 * c + h);
-            const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-            uint16_t hi[4], lo[4];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const float x = __uint_as_float(w[i] << 16) * up, y = __uint_as_float(w[i] & 0xFFFF0000u) * up;
-                hi[i] = f32x2_to_e4m3x2(x, y);
-                const uint32_t f = e4m3x2_to_f16x2(hi[i]);
-                const float2 got = __half22float2(*reinterpret_cast<const __half2*>(&f));
-                lo[i] = f32x2_to_e4m3x2(x - got.x, y - got.y);
-            }
-            a[2 * h] = hi[0] | (uint32_t)hi[1] << 16;
-            a[2 * h + 1] = hi[2] | (uint32_t)hi[3] << 16;
-            b[2 * h] = lo[0] | (uint32_t)lo[1] << 16;
-            b[2 * h + 1] = lo[2] | (uint32_t)lo[3] << 16;
-        }
-        const int at = row * D + (D == 128 ? c ^ (row & 7) : c ^ (row >> 1 & 3)) * 16;
-        *reinterpret_cast<uint4*>(to + at) = make_uint4(a[0], a[1], a[2], a[3]);
-        *reinterpret_cast<uint4*>(to + CH_ROWS * D + at) = make_uint4(b[0], b[1], b[2], b[3]);
-        if (too) {
-            *reinterpret_cast<uint4*>(too + at) = make_uint4(a[0], a[1], a[2], a[3]);
-            *reinterpret_cast<uint4*>(too + CH_ROWS * D + at) = make_uint4(b[0], b[1], b[2], b[3]);
-        }
+    for (int k = 0; k < 8; ++k) {
+        const uint32_t x2 = finite ? w[k] : 0u;
+        const float x = __uint_as_float(x2 << 16) * up, y = __uint_as_float(x2 & 0xFFFF0000u) * up;
+        const uint16_t hi = f32x2_to_e4m3x2(x, y);
+        const uint32_t f = e4m3x2_to_f16x2(hi);
+        const float2 got = __half22float2(*reinterpret_cast<const __half2*>(&f));
+        const uint16_t lo = f32x2_to_e4m3x2(x - got.x, y - got.y);
+        if (k & 1) { a[k / 2] |= (uint32_t)hi << 16; b[k / 2] |= (uint32_t)lo << 16; }
+        else { a[k / 2] = hi; b[k / 2] = lo; }
     }
+    if (!in) return;
+    *reinterpret_cast<uint4*>(q8 + row * D + 16 * c) = make_uint4(a[0], a[1], a[2], a[3]);
+    *reinterpret_cast<uint4*>(q8 + (rows + row) * D + 16 * c) = make_uint4(b[0], b[1], b[2], b[3]);
+    if (c == 0) q_exp[row] = (int8_t)(finite ? e : CH_NAN);
 }
+
 // A tile of V from its codes to f16, by 128 threads; rows from `have` on become zero, as a weight of zero does not silence the
 // NaN that may lie there.
 template <int D>
@@ -731,7 +727,7 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
     const uint32_t base = smem_u32(smem);
     constexpr uint32_t K0 = 2 * P::Q, V0 = K0 + P::KS * P::TILE, WIDE0 = V0 + P::VS * P::TILE;
     if (tid == 0) {
-        if (!FP8) tensor_map_prefetch(&map_q);
+        tensor_map_prefetch(&map_q);
         tensor_map_prefetch(&map_k);
         tensor_map_prefetch(&map_v);
         for (int i = 0; i < P::KS; ++i) mbar_init(smem_u32(&sh.k_full[i]), 1);
@@ -742,7 +738,7 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
         mbar_init(smem_u32(&sh.weights_there), 4);
         mbar_init(smem_u32(&sh.o_read), 8);
         for (int t = 0; t < 2; ++t) {
-            mbar_init(smem_u32(&sh.q_full[t]), FP8 ? 4 : 1);
+            mbar_init(smem_u32(&sh.q_full[t]), 1);
             for (int i = 0; i < CH_EVENTS; ++i) mbar_init(smem_u32(&sh.event[t][i]), 1);
             for (int i = 0; i < 2; ++i) mbar_init(smem_u32(&sh.p_full[t][i]), 4);
             mbar_init(smem_u32(&sh.turn[t]), 1);
@@ -906,17 +902,18 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
                                 e1 = (I.dual ? j & 1 : j < I.n1) ? events[1] + I.event(i, v) : ~0u;
                             }
                             ++issued;
-                            if (!FP8 && j == 0 && v == 0)
+                            if (j == 0 && v == 0)
 #pragma unroll
                                 for (int t = 0; t < 2; ++t) {
                                     if (I.n(t) == 0 || !ok) continue;
                                     ok = event_wait(t, q_free[t]);
                                     ok = __all_sync(0xffffffffu, ok);
                                     if (lane == 0 && ok) {
-                                        mbar_expect_tx(smem_u32(&sh.q_full[t]), (uint32_t)((D / 64) * 128 * A.r * A.tq));
-                                        for (int x = 0; x < D / 64; ++x)
-                                            tma_load_3d(base + t * P::Q + x * CH_BLOCK, &map_q, 64 * x, I.g * A.r, (int)I.row + I.tok0 + (I.dual ? 0 : t * A.tq),
-                                                        smem_u32(&sh.q_full[t]));
+                                        mbar_expect_tx(smem_u32(&sh.q_full[t]), (uint32_t)(2 * D * A.r * A.tq));
+                                        const int tok = (int)I.row + I.tok0 + (I.dual ? 0 : t * A.tq);
+                                        for (int x = 0; x < (FP8 ? 2 : D / 64); ++x)         // the pieces, or 64 values of d
+                                            tma_load_3d(base + t * P::Q + x * (FP8 ? CH_ROWS * D : CH_BLOCK), &map_q, FP8 ? 0 : 64 * x, I.g * A.r,
+                                                        tok + (FP8 ? x * (int)A.total : 0), smem_u32(&sh.q_full[t]));
                                     }
                                     q_issued[t] += ok;
                                 }
@@ -1058,10 +1055,9 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
                 if (A.status) atomicOr(A.status, KVO_DEV_TIMEOUT);
             }
         } else if (FP8 && warp >= 12) {
-            // ------------------------------------------------ q and V of 8-bit pages
+            // ------------------------------------------------ V of 8-bit pages
             if constexpr (FP8) {
-                uint32_t item = 0, tiles = 0, turn[2] = {0, 0}, events[2] = {0, 0}, q_free[2] = {~0u, ~0u}, e0 = ~0u, e1 = ~0u;         // of buffer `lane`: the events that free it
-                const int row = tid & 127;
+                uint32_t item = 0, tiles = 0, events0 = 0, events1 = 0, e0 = ~0u, e1 = ~0u;         // of buffer `lane`: the events that free it
                 bool ok = true;
                 while (ok) {
                     ChunkItem I;
@@ -1072,26 +1068,6 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
                     __syncwarp();
                     if (lane == 0) free_item(item);
                     if (I.n0 < 0) break;
-                    const bool copy = I.dual && I.n1 > 0;                 // both take the same rows
-#pragma unroll
-                    for (int t = 0; t < 2; ++t) {
-                        if (I.n(t) == 0 || (copy && t == 1) || !ok) continue;
-                        if (warp == 12) {
-                            if (q_free[t] != ~0u) ok = ch_event(sh, A, t, q_free[t]);
-                            if (copy && ok && q_free[1] != ~0u) ok = ch_event(sh, A, 1, q_free[1]);
-                        }
-                        ok = !group_any(3, !ok);
-                        if (!ok) continue;
-                        int8_t* const exponent = &sh.q_exp[turn[t]++ & 1][t][row];
-                        ch_split_q<D>(A, I, t, row, smem + t * P::Q, copy ? smem + P::Q : nullptr, exponent);
-                        if (copy) sh.q_exp[turn[1]++ & 1][1][row] = *exponent;
-                        fence_async_smem();
-                        __syncwarp();
-                        if (lane == 0) {
-                            mbar_arrive(smem_u32(&sh.q_full[t]));
-                            if (copy) mbar_arrive(smem_u32(&sh.q_full[1]));
-                        }
-                    }
                     ++item;
                     for (int j = 0; j < I.tiles && ok; ++j) {
                         const int st = tiles % P::VS, w = tiles % P::WIDES;
@@ -1112,17 +1088,13 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
                         }
                         const int i = I.dual ? j >> 1 : j;
                         if (lane == w) {
-                            e0 = (I.dual ? !(j & 1) : j < I.n0) ? events[0] + I.event(i, 1) : ~0u;
-                            e1 = (I.dual ? j & 1 : j < I.n1) ? events[1] + I.event(i, 1) : ~0u;
+                            e0 = (I.dual ? !(j & 1) : j < I.n0) ? events0 + I.event(i, 1) : ~0u;
+                            e1 = (I.dual ? j & 1 : j < I.n1) ? events1 + I.event(i, 1) : ~0u;
                         }
                         ++tiles;
                     }
-#pragma unroll
-                    for (int t = 0; t < 2; ++t)
-                        if (I.n(t)) {
-                            q_free[t] = events[t] + I.event(I.n(t) - 1, 0);
-                            events[t] += I.events(t);
-                        }
+                    events0 += I.events(0);
+                    events1 += I.events(1);
                 }
             }
         }
@@ -1130,7 +1102,7 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
     } else {
         regs_inc<P::REGS_SOFTMAX>();
         const int t = warp >> 2;
-        uint32_t item = 0, events = 0, keys = 0, shares = 0, turn = 0;     // turn: of the items that this tile has a part in
+        uint32_t item = 0, events = 0, keys = 0, shares = 0;
         while (true) {
             // The item stays where it is: 128 scores leave few registers.
             bool ok = true;
@@ -1138,9 +1110,8 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
             if (group_any(1 + t, !ok)) break;
             const ChunkItem& I = sh.item[item % CH_ITEMS];
             if (I.n0 < 0) break;
-            if (!ch_softmax<D, FP8>(sh, A, I, t, events, keys, turn & 1, shares)) break;
+            if (!ch_softmax<D, FP8>(sh, A, I, t, events, keys, shares)) break;
             events += I.events(t);
-            turn += I.n(t) > 0;
             keys += I.tiles;
             __syncwarp();
             if (lane == 0) free_item(item);
@@ -1155,9 +1126,8 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
     // thread that issued them stays until they have.
     if (tid == 9 * 32 && sh.abort) {
         const int issued = sh.issued;
-        if (!FP8)
-            for (int t = 0; t < 2; ++t)
-                if (sh.q_issued[t]) mbar_wait_bounded(smem_u32(&sh.q_full[t]), (sh.q_issued[t] - 1) & 1, A.wait_ns);
+        for (int t = 0; t < 2; ++t)
+            if (sh.q_issued[t]) mbar_wait_bounded(smem_u32(&sh.q_full[t]), (sh.q_issued[t] - 1) & 1, A.wait_ns);
         for (int i = max(0, (issued + 1) / 2 - P::KS); i < (issued + 1) / 2; ++i)
             mbar_wait_bounded(smem_u32(&sh.k_full[i % P::KS]), (i / P::KS) & 1, A.wait_ns);
         for (int i = max(0, issued / 2 - P::VS); i < issued / 2; ++i)
@@ -1233,12 +1203,13 @@ __global__ void __launch_bounds__(CH_ROWS) paged_chunk_join_kernel(const __grid_
 
 // ------------------------------------------------------------------ host
 struct ChunkSpace {
-    size_t cut, ml, o;
+    size_t cut, ml, o, q_exp, q8;
+    size_t all() const { return cut + ml + o + q_exp + q8; }
 };
-ChunkSpace chunk_space(int tiles, int d) {
-    auto up = [](size_t x) { return (x + 255) / 256 * 256; };
+ChunkSpace chunk_space(int tiles, int d, bool fp8, int64_t q_rows) {
     const size_t rows = (size_t)CH_CTAS * 2 * tiles * CH_ROWS;
-    return {up(CH_CTAS * sizeof(ChunkCut)), up(rows * sizeof(float2)), rows * d * sizeof(float)};
+    return {round256(CH_CTAS * sizeof(ChunkCut)), round256(rows * sizeof(float2)), rows * d * sizeof(float), fp8 ? round256((size_t)q_rows) : 0,
+            fp8 ? 2 * (size_t)q_rows * d : 0};
 }
 // Few rows to a request: bound by the bytes of K and V, and products of 128 rows would be mostly empty.
 bool chunk_few(int r, int64_t max_new) { return max_new > 0 && max_new * r <= FEW_ROWS; }
@@ -1248,7 +1219,7 @@ const char* chunk_error(const kvo_paged_cache* c, int n_q_heads, int64_t total_q
     if (const char* m = paged_cache_error(c)) return m;
     if (n_q_heads < c->n_kv_heads || n_q_heads % c->n_kv_heads) return "n_q_heads must be a multiple of n_kv_heads";
     if (n_q_heads / c->n_kv_heads > 16) return "n_q_heads / n_kv_heads must be <= 16";
-    if (total_q < 0 || total_q > INT32_MAX) return "total_q must be in 0..2^31 - 1";
+    if (total_q < 0 || total_q > (1 << 30) || total_q * n_q_heads > (1ll << 34)) return "total_q must be in 0..2^30, with at most 2^34 rows of q";
     if (max_new < 0 || max_len < 0) return "max_new and max_len must be >= 0";
     return nullptr;
 }
@@ -1279,8 +1250,8 @@ extern "C" kvo_status kvo_paged_chunk_attn_workspace(const kvo_paged_cache* cach
     *bytes_out = 0;
     if (const char* m = chunk_error(cache, n_q_heads, total_q, max_new, max_len)) return bad(m);
     const int r = n_q_heads / cache->n_kv_heads;
-    const ChunkSpace sp = chunk_space(chunk_tiles(total_q, r), cache->head_dim);
-    *bytes_out = chunk_few(r, max_new) ? paged_few_workspace(cache, r, max_new, max_len) : sp.cut + sp.ml + sp.o;
+    *bytes_out = chunk_few(r, max_new) ? paged_few_workspace(cache, r, max_new, max_len)
+                                       : chunk_space(chunk_tiles(total_q, r), cache->head_dim, cache->format == KVO_PAGES_E4M3, total_q * n_q_heads).all();
     return KVO_OK;
 }
 
@@ -1301,9 +1272,9 @@ extern "C" kvo_status kvo_paged_chunk_attn(const kvo_paged_cache* cache, const v
     if (q_token_stride < width) return bad("token strides must cover the heads");
     if (q_token_stride > (1ll << 38)) return bad("token strides must be below 2^38 elements");
     const int tiles = chunk_tiles(total_q, r);
-    const ChunkSpace sp = chunk_space(tiles, D);
-    const bool few = chunk_few(r, max_new);
-    const size_t need = few ? paged_few_workspace(cache, r, max_new, max_len) : sp.cut + sp.ml + sp.o;
+    const bool few = chunk_few(r, max_new), fp8 = cache->format == KVO_PAGES_E4M3;
+    const ChunkSpace sp = chunk_space(tiles, D, fp8, total_q * n_q_heads);
+    const size_t need = few ? paged_few_workspace(cache, r, max_new, max_len) : sp.all();
     if (need && (!workspace || workspace_bytes < need)) return bad("the workspace is too small (kvo_paged_chunk_attn_workspace)");
     const int64_t pool = page_bytes(cache), scales = scale_bytes(cache);
     const Bytes to_o{o, 2 * total_q * width}, to_lse{lse, 4 * total_q * n_q_heads}, to_ws{workspace, (int64_t)need};
@@ -1313,7 +1284,6 @@ extern "C" kvo_status kvo_paged_chunk_attn(const kvo_paged_cache* cache, const v
                               {cache->k_scale, scales}, {cache->v_scale, scales}, {cache->table, 4 * b * cache->max_pages}, {lens, 4 * b},
                               {cu, 4 * (b + 1)}});
     if (meet) return bad("o, lse and the workspace must be apart from each other and from all that the call reads");
-    const bool fp8 = cache->format == KVO_PAGES_E4M3;
     const uint64_t rows = (uint64_t)cache->n_pages * cache->n_kv_heads * cache->page_size;
     const int elem = fp8 ? 1 : 2, box = std::min(D * elem, 128), box_rows = few ? 16 : cache->page_size;
     cudaStream_t s = (cudaStream_t)stream;
@@ -1341,6 +1311,9 @@ extern "C" kvo_status kvo_paged_chunk_attn(const kvo_paged_cache* cache, const v
     A.cut = (ChunkCut*)workspace;
     A.part_ml = (float2*)((uint8_t*)workspace + sp.cut);
     A.part_o = (float*)((uint8_t*)workspace + sp.cut + sp.ml);
+    int8_t* const q_exp = (int8_t*)A.part_o + sp.o;
+    uint8_t* const q8 = (uint8_t*)q_exp + sp.q_exp;
+    A.q_exp = q_exp;
     A.total = total_q;
     A.batch = cache->batch;
     A.hq = n_q_heads;
@@ -1361,11 +1334,18 @@ extern "C" kvo_status kvo_paged_chunk_attn(const kvo_paged_cache* cache, const v
     A.wide = (uintptr_t)o % 32 == 0;
     A.skip = call_wait.skip;
     A.wait_ns = call_wait.limit_ns;
-    const uint64_t sq[3] = {(uint64_t)D, (uint64_t)n_q_heads, (uint64_t)total_q}, tq[2] = {(uint64_t)D * 2, (uint64_t)q_token_stride * 2};
-    const uint32_t bq[3] = {64, (uint32_t)r, (uint32_t)A.tq};
-    if (!tensor_map(&mq, q, 2, 3, sq, tq, bq)) {
+    const uint64_t sq[3] = {(uint64_t)D, (uint64_t)n_q_heads, (uint64_t)total_q * (fp8 ? 2 : 1)};
+    const uint64_t tq[2] = {(uint64_t)D * elem, fp8 ? (uint64_t)width : (uint64_t)q_token_stride * 2};
+    const uint32_t bq[3] = {fp8 ? (uint32_t)D : 64u, (uint32_t)r, (uint32_t)A.tq};
+    if (!tensor_map(&mq, fp8 ? (const void*)q8 : q, elem, 3, sq, tq, bq)) {
         set_last_error("cuTensorMapEncodeTiled failed for q");
         return KVO_ERR_CUDA;
+    }
+    if (fp8) {
+        const int64_t q_rows = total_q * n_q_heads, ctas = (q_rows * (D / 16) + CS_THREADS - 1) / CS_THREADS;
+        const cudaError_t e = launch_dependent(D == 128 ? paged_chunk_split_kernel<128> : paged_chunk_split_kernel<64>, dim3((unsigned)ctas), CS_THREADS, 0, s, 0,
+                                               (const uint16_t*)q, q_token_stride, n_q_heads, q_rows, q8, q_exp);
+        if (e != cudaSuccess) { set_last_error(cudaGetErrorString(e)); return KVO_ERR_CUDA; }
     }
     cudaError_t e;
     if (D == 128) e = fp8 ? paged_chunk_launch<128, true>(mq, mk, mv, A, s) : paged_chunk_launch<128, false>(mq, mk, mv, A, s);
