@@ -11,7 +11,8 @@
 // on timing.
 //
 // One CTA to an SM, its warps
-//   9        walks the items: their descriptors, K and V tiles through rings (TMA, a box per page), the pages' scales,
+//   9        walks the items: their descriptors, tiles of K, and of e4m3 V, through rings (TMA, a box per page), the pages' scales,
+//   11       (bf16) tiles of V,
 //   8, 10    one thread each issues the tcgen05.mma of tile 0 and 1: S_t = Q_t K^T and O_t += P_t V,
 //   0-3, 4-7 the softmax of tile 0 and 1, one thread per row: S from tensor memory, online maximum and sum in fp32, P (bf16, or
 //            f16 next to e4m3) back over S,
@@ -24,6 +25,18 @@
 // way through shared memory.  A page's k_scale multiplies its scores; its v_scale goes into the exponents of its weights,
 // exp2(s + log2 v_scale - m) with m the maximum of those, so that f16 holds what contributes most whatever the scales are,
 // and the sum of the weights takes each page's share times 1 / v_scale, in fp32.
+//
+// What bounds it.  Long chunks: the tensor cores, which wait for the softmax (two tiles in turn, a row to a thread) at the
+// hand-overs.  32 query heads over 8 of d 128: 8192 tokens alone in bf16 395 us, 1.39 PFLOP/s of 1.91 measured for a matrix
+// product, in e4m3 459; 2048 behind 30000 in bf16 686 us (1.51 PFLOP/s), in e4m3 810: there the conversions of V and of P and
+// more code than the instruction caches hold.  Few rows on many keys: the loads of K and V, 16 requests of 4 tokens behind 32k
+// in bf16 6.6 TB/s.  A batch of both, 36 single tokens and 4 chunks: 166 us, 0.92 PFLOP/s.
+//
+// Why so.  One thread for both tiles' products kept one tile waiting for the other's barriers: 8192 tokens 440 -> 402 us with
+// two.  Two buffers of f16 V: 2048 e4m3 tokens behind 30000 965 us, three 787.  q split into its pieces by every CTA that
+// needs them: 8192 tokens 744 us, by a launch before 457.  The softmax unrolled over 128 keys: 1016 us, in loops 740.  One
+// warp that loads both K and V keeps K waiting behind V's buffers: in bf16 the mixed batch 251 us, with two 166; in e4m3 the
+// buffers of raw V are free early, and a second warp's code costs more: 2048 behind 30000 945 us, with one 810.
 #include <stdio.h>
 
 #include <algorithm>
@@ -47,6 +60,7 @@ constexpr float CH_RAISE = 8.f;            // log2: how far a score may pass the
 constexpr int CH_CTAS = 152;               // ranges at most: one CTA to an SM
 constexpr int CH_EVENTS = 16;              // barriers that a tile's products complete in turn
 constexpr int CH_ITEMS = 4;                // descriptors
+constexpr int CH_NONE = INT32_MIN;         // no page
 constexpr int CH_NAN = -128;               // the exponent of a row of q that is not finite
 constexpr int CH_SCALES = 8;               // tiles of keys whose scales are held
 
@@ -133,7 +147,7 @@ struct ChShared {
     uint32_t bad[CH_SCALES];       // groups of 16 keys in pages that do not exist
     uint32_t tmem;
     int abort;
-    int issued, tail_open, tail_phase, q_issued[2];
+    int k_issued, v_issued, tail_open, tail_phase, q_issued[2];
     union {
         struct {                   // the plan
             int64_t sum[16], at[2];
@@ -747,10 +761,10 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
         mbar_init(smem_u32(&sh.v_tail), 1);
         for (int i = 0; i < CH_ITEMS; ++i) {
             mbar_init(smem_u32(&sh.item_full[i]), 1);
-            mbar_init(smem_u32(&sh.item_free[i]), FP8 ? 14 : 10);
+            mbar_init(smem_u32(&sh.item_free[i]), FP8 ? 14 : 11);
         }
         for (int i = 0; i < CH_SCALES; ++i) mbar_init(smem_u32(&sh.sc_full[i]), 1);
-        sh.abort = sh.issued = sh.tail_open = sh.tail_phase = sh.q_issued[0] = sh.q_issued[1] = 0;
+        sh.abort = sh.k_issued = sh.v_issued = sh.tail_open = sh.tail_phase = sh.q_issued[0] = sh.q_issued[1] = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
     grid_wait();
@@ -776,6 +790,21 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
         I = sh.item[k % CH_ITEMS];
         return true;
     };
+    // Of the item's tiles j .. j + 3, the page of the (lane % 8)-th 16 keys of tile j + lane / 8; CH_NONE behind the last key.
+    auto page_of = [&](const ChunkItem& I, int j) {
+        const int64_t key = (int64_t)(I.first + j + (lane >> 3)) * CH_KEYS + 16 * (lane & 7);
+        return key < I.len ? __ldg(A.table + (int64_t)I.b * A.max_pages + (key >> A.shift)) : CH_NONE;
+    };
+    // Whole warp: asks for a tile of K or V, a box to a lane: its page's rows in the pool, or, where there is no such page,
+    // what lies behind the last (zeros).
+    auto load_tile = [&](const CUtensorMap* map, const ChunkItem& I, int page, int j, uint32_t at, uint32_t bar, int number) {
+        constexpr int ROW = D * (FP8 ? 1 : 2), BOXES = ROW > 128 ? ROW / 128 : 1, BOX = ROW > 128 ? 128 : ROW;
+        const int from = __shfl_sync(0xffffffffu, page, (j & 3) * 8 + lane / BOXES * (A.page / 16) & 31);
+        const int y = from < 0 ? A.n_pages * A.hkv * A.page : (from * A.hkv + I.g) * A.page;
+        if (lane < CH_KEYS / A.page * BOXES && number != A.skip)
+            tma_load_2d(base + at + (lane % BOXES) * CH_BLOCK + lane / BOXES * A.page * BOX, map, (lane % BOXES) * (FP8 ? 128 : 64), y, bar);
+    };
+    auto event_wait = [&](int t, uint32_t e) { return e == ~0u || ch_event(sh, A, t, e); };
     auto free_item = [&](uint32_t k) { mbar_arrive(smem_u32(&sh.item_free[k % CH_ITEMS])); };
 
     if (warp >= 8) {
@@ -787,16 +816,11 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
             const int64_t lo = plan.lo, hi = plan.hi;
             if (lane == 0) A.cut[blockIdx.x] = ch_cut(sh, A, plan, walk);    // before anything that may give up: the join follows it
             __syncwarp();
-            bool ok = true, tail_open = false;
-            uint32_t k = 0, tail_phase = 0, tiles = 0;
-            int issued = 0;                             // loads: K and V of each tile in turn
+            bool ok = true;
+            uint32_t k = 0, tiles = 0, v_issued = 0;
             uint32_t events[2] = {0, 0}, q_issued[2] = {0, 0};
             uint32_t q_free[2] = {~0u, ~0u};            // the event after which a tile's q may be overwritten
-            uint32_t e0 = ~0u, e1 = ~0u;                // of stage `lane` of K, or `lane - 16` of V: the events that free it
-            const int rows = A.n_pages * A.hkv * A.page, chunks = A.page / 16;
-            constexpr int ROW = D * (FP8 ? 1 : 2), BOXES = ROW > 128 ? ROW / 128 : 1, BOX = ROW > 128 ? 128 : ROW;
-            const int boxes = CH_KEYS / A.page * BOXES;
-            auto event_wait = [&](int t, uint32_t e) { return e == ~0u || ch_event(sh, A, t, e); };
+            uint32_t e0 = ~0u, e1 = ~0u;                // of stage `lane`: the events that free it
             while (ok) {
                 int first, last;
                 const int all0 = ch_tiles(A, walk.r, walk.i, 0), all1 = ch_tiles(A, walk.r, walk.i, 1), n_item = max(all0, all1);
@@ -822,23 +846,16 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
                         mbar_arrive(smem_u32(&sh.item_full[k % CH_ITEMS]));
                     }
                     ++k;
-                    const int n = I.tiles;
-                    const int32_t* table = A.table + (int64_t)I.b * A.max_pages;
-                    // Lane: the (lane % 8)-th 16 keys of tile lane / 8 of four.
-                    auto page_of = [&](int j) {
-                        const int64_t key = (int64_t)(I.first + j + (lane >> 3)) * CH_KEYS + 16 * (lane & 7);
-                        return key < I.len ? __ldg(table + (key >> A.shift)) : -1;
-                    };
-                    int page = 0, page_next = page_of(0);
+                    int page = 0, page_next = page_of(I, 0);
                     bool bad = false;
                     float ks = 0.f, vs = 0.f;
-                    for (int j = 0; ok && j < n; ++j) {
+                    for (int j = 0; ok && j < I.tiles; ++j, ++tiles) {
                         if ((j & 3) == 0) {
                             page = page_next;
-                            if (j + 4 < n) page_next = page_of(j + 4);
-                            const bool in = (int64_t)(I.first + j + (lane >> 3)) * CH_KEYS + 16 * (lane & 7) < I.len;
+                            if (j + 4 < I.tiles) page_next = page_of(I, j + 4);
+                            const bool in = page != CH_NONE;
                             bad = in && (page < 0 || page >= A.n_pages);
-                            if (bad && j + (lane >> 3) < n && A.status) atomicOr(A.status, KVO_DEV_BAD_BLOCK_ID);
+                            if (bad && j + (lane >> 3) < I.tiles && A.status) atomicOr(A.status, KVO_DEV_BAD_BLOCK_ID);
                             if (bad || !in) page = -1;
                             if constexpr (FP8) {
                                 ks = page < 0 ? 1.f : __ldg(A.k_scale + (int64_t)page * A.hkv + I.g);
@@ -846,80 +863,54 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
                             }
                         }
                         const uint32_t bads = __ballot_sync(0xffffffffu, bad) >> (j & 3) * 8 & 0xFF;
-                        const int sc = tiles % CH_SCALES;
-                        // Box `lane`: its page's first row in the pool, or what lies behind the last (zeros).
-                        const int from = __shfl_sync(0xffffffffu, page, (j & 3) * 8 + lane / BOXES * chunks & 31);
-                        const int y = from < 0 ? rows : (from * A.hkv + I.g) * A.page;
-                        const int key0 = (I.first + j) * CH_KEYS;
-                        for (int v = 0; v < 2; ++v) {
-                            const int st = tiles % (v ? P::VS : P::KS), stages = v ? P::VS : P::KS, holder = st + 16 * v;
-                            if (tiles >= stages) {
-                                if (FP8 && v) {
-                                    ok = ch_wait(sh, A, sh.raw_free[st], tiles / stages - 1);
-                                } else {
-                                    ok = event_wait(0, __shfl_sync(0xffffffffu, e0, holder));
-                                    ok = event_wait(1, __shfl_sync(0xffffffffu, e1, holder)) && ok;
-                                }
-                                if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
-                            }
-                            if (v == 0) {
-                                // Before the keys are asked for: their scores are there only after this.
-                                if constexpr (FP8)
-                                    if (lane >> 3 == (j & 3)) {
-                                        sh.k_scale[sc][lane & 7] = ks;
-                                        sh.v_log[sc][lane & 7] = log2f(vs);
-                                    }
-                                if (lane == 0) sh.bad[sc] = bads;
-                                __syncwarp();
-                                if (lane == 0) mbar_arrive(smem_u32(&sh.sc_full[sc]));
-                            }
-                            // The last tile of a request runs into what lies behind it in its page.  Its keys are masked as
-                            // scores, but a weight of zero does not silence a NaN or an infinity in V: those rows are cleared.
-                            const bool tail = !FP8 && v && key0 + CH_KEYS > I.len;
-                            const uint32_t full = smem_u32(v ? &sh.v_full[st] : &sh.k_full[st]), bar = tail ? smem_u32(&sh.v_tail) : full;
-                            const uint32_t dst = base + (v ? V0 : K0) + st * P::TILE;
-                            if (lane == 0) mbar_expect_tx(bar, P::TILE);
-                            __syncwarp();
-                            if (lane < boxes && issued != A.skip)
-                                tma_load_2d(dst + (lane % BOXES) * CH_BLOCK + lane / BOXES * A.page * BOX, v ? &map_v : &map_k,
-                                            (lane % BOXES) * (FP8 ? 128 : 64), y, bar);
-                            if (tail) {
-                                tail_open = true;
-                                ok = ch_wait(sh, A, sh.v_tail, tail_phase);
-                                if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
-                                tail_open = false;
-                                ++tail_phase;
-                                for (int x = 0; x < BOXES; ++x)
-                                    for (uint32_t a = (I.len - key0) * 128 + lane * 16; a < CH_BLOCK; a += 512)
-                                        asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(dst + x * CH_BLOCK + a), "r"(0) : "memory");
-                                fence_async_smem();
-                                __syncwarp();
-                                if (lane == 0) mbar_arrive(full);
-                            }
-                            if (lane == holder) {
-                                const int i = I.dual ? j >> 1 : j;
-                                e0 = (I.dual ? !(j & 1) : j < I.n0) ? events[0] + I.event(i, v) : ~0u;
-                                e1 = (I.dual ? j & 1 : j < I.n1) ? events[1] + I.event(i, v) : ~0u;
-                            }
-                            ++issued;
-                            if (j == 0 && v == 0)
-#pragma unroll
-                                for (int t = 0; t < 2; ++t) {
-                                    if (I.n(t) == 0 || !ok) continue;
-                                    ok = event_wait(t, q_free[t]);
-                                    ok = __all_sync(0xffffffffu, ok);
-                                    if (lane == 0 && ok) {
-                                        mbar_expect_tx(smem_u32(&sh.q_full[t]), (uint32_t)(2 * D * A.r * A.tq));
-                                        const int tok = (int)I.row + I.tok0 + (I.dual ? 0 : t * A.tq);
-                                        for (int x = 0; x < (FP8 ? 2 : D / 64); ++x)         // the pieces, or 64 values of d
-                                            tma_load_3d(base + t * P::Q + x * (FP8 ? CH_ROWS * D : CH_BLOCK), &map_q, FP8 ? 0 : 64 * x, I.g * A.r,
-                                                        tok + (FP8 ? x * (int)A.total : 0), smem_u32(&sh.q_full[t]));
-                                    }
-                                    q_issued[t] += ok;
-                                }
-                            if (!ok) break;
+                        const int st = tiles % P::KS, sc = tiles % CH_SCALES;
+                        if (tiles >= P::KS) {
+                            ok = event_wait(0, __shfl_sync(0xffffffffu, e0, st));
+                            ok = event_wait(1, __shfl_sync(0xffffffffu, e1, st)) && ok;
+                            if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
                         }
-                        ++tiles;
+                        // Before the keys are asked for: their scores are there only after this.
+                        if constexpr (FP8)
+                            if (lane >> 3 == (j & 3)) {
+                                sh.k_scale[sc][lane & 7] = ks;
+                                sh.v_log[sc][lane & 7] = log2f(vs);
+                            }
+                        if (lane == 0) {
+                            sh.bad[sc] = bads;
+                            mbar_expect_tx(smem_u32(&sh.k_full[st]), P::TILE);
+                        }
+                        warp_arrive(sh.sc_full[sc]);
+                        load_tile(&map_k, I, page, j, K0 + st * P::TILE, smem_u32(&sh.k_full[st]), 2 * tiles);
+                        if (lane == st) {
+                            const int i = I.dual ? j >> 1 : j;
+                            e0 = (I.dual ? !(j & 1) : j < I.n0) ? events[0] + I.event(i, 0) : ~0u;
+                            e1 = (I.dual ? j & 1 : j < I.n1) ? events[1] + I.event(i, 0) : ~0u;
+                        }
+                        if (j == 0)
+#pragma unroll
+                            for (int t = 0; t < 2; ++t) {
+                                if (I.n(t) == 0 || !ok) continue;
+                                ok = event_wait(t, q_free[t]);
+                                ok = __all_sync(0xffffffffu, ok);
+                                if (lane == 0 && ok) {
+                                    mbar_expect_tx(smem_u32(&sh.q_full[t]), (uint32_t)(2 * D * A.r * A.tq));
+                                    const int tok = (int)I.row + I.tok0 + (I.dual ? 0 : t * A.tq);
+                                    for (int x = 0; x < (FP8 ? 2 : D / 64); ++x)         // the pieces, or 64 values of d
+                                        tma_load_3d(base + t * P::Q + x * (FP8 ? CH_ROWS * D : CH_BLOCK), &map_q, FP8 ? 0 : 64 * x, I.g * A.r,
+                                                    tok + (FP8 ? x * (int)A.total : 0), smem_u32(&sh.q_full[t]));
+                                }
+                                q_issued[t] += ok;
+                            }
+                        if constexpr (FP8) {
+                            const int sv = tiles % P::VS;
+                            if (ok && tiles >= P::VS) ok = ch_wait(sh, A, sh.raw_free[sv], tiles / P::VS - 1);
+                            ok = __all_sync(0xffffffffu, ok);
+                            if (!ok) { ++tiles; break; }
+                            if (lane == 0) mbar_expect_tx(smem_u32(&sh.v_full[sv]), P::TILE);
+                            __syncwarp();
+                            load_tile(&map_v, I, page, j, V0 + sv * P::TILE, smem_u32(&sh.v_full[sv]), 2 * tiles + 1);
+                            v_issued = tiles + 1;
+                        }
                     }
 #pragma unroll
                     for (int t = 0; t < 2; ++t)
@@ -952,14 +943,74 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
                     sh.item[k % CH_ITEMS].n0 = -1;
                     mbar_arrive(smem_u32(&sh.item_full[k % CH_ITEMS]));
                 }
-                sh.issued = issued;
-                sh.tail_open = tail_open;
-                sh.tail_phase = tail_phase;
+                sh.k_issued = tiles;
+                if (FP8) sh.v_issued = v_issued;
             }
             // Where somebody gave up not all loads may have landed: the warp that issued them stays until they have, and
             // with it the CTA and its shared memory.  (`abort` is final only once all have left their waits: below.)
             __syncwarp();
             if (lane == 0) { sh.q_issued[0] = q_issued[0]; sh.q_issued[1] = q_issued[1]; }
+        } else if (!FP8 && warp == 11) {
+            // ------------------------------------------------ V, which waits for other things than K does
+            bool ok = true, tail_open = false;
+            uint32_t item = 0, tiles = 0, tail_phase = 0, events0 = 0, events1 = 0;
+            uint32_t e0 = ~0u, e1 = ~0u;                // of stage `lane`: the events that free it
+            while (ok) {
+                ChunkItem I;
+                ok = next_item(item, I);
+                ok = __all_sync(0xffffffffu, ok);
+                if (!ok || I.n0 < 0) break;
+                if (lane == 0) free_item(item);
+                ++item;
+                int page = 0, page_next = page_of(I, 0);
+                for (int j = 0; j < I.tiles; ++j) {
+                    if ((j & 3) == 0) {
+                        page = page_next;
+                        if (j + 4 < I.tiles) page_next = page_of(I, j + 4);
+                        if (page < 0 || page >= A.n_pages) page = -1;
+                    }
+                    const int st = tiles % P::VS, key0 = (I.first + j) * CH_KEYS;
+                    if (tiles >= P::VS) {
+                        ok = event_wait(0, __shfl_sync(0xffffffffu, e0, st));
+                        ok = event_wait(1, __shfl_sync(0xffffffffu, e1, st)) && ok;
+                        ok = __all_sync(0xffffffffu, ok);
+                        if (!ok) break;
+                    }
+                    // The last tile of a request runs into what lies behind it in its page.  Its keys are masked as scores, but a
+                    // weight of zero does not silence a NaN or an infinity in V: those rows are cleared.
+                    const bool tail = key0 + CH_KEYS > I.len;
+                    const uint32_t bar = smem_u32(tail ? &sh.v_tail : &sh.v_full[st]);
+                    if (lane == 0) mbar_expect_tx(bar, P::TILE);
+                    __syncwarp();
+                    load_tile(&map_v, I, page, j, V0 + st * P::TILE, bar, 2 * tiles + 1);
+                    if (tail) {
+                        tail_open = true;
+                        ok = ch_wait(sh, A, sh.v_tail, tail_phase);
+                        ok = __all_sync(0xffffffffu, ok);
+                        if (!ok) break;
+                        tail_open = false;
+                        ++tail_phase;
+                        for (int x = 0; x < D / 64; ++x)
+                            for (uint32_t a = (I.len - key0) * 128 + lane * 16; a < CH_BLOCK; a += 512)
+                                *reinterpret_cast<uint4*>(smem + V0 + st * P::TILE + x * CH_BLOCK + a) = make_uint4(0, 0, 0, 0);
+                        fence_async_smem();
+                        warp_arrive(sh.v_full[st]);
+                    }
+                    if (lane == st) {
+                        const int i = I.dual ? j >> 1 : j;
+                        e0 = (I.dual ? !(j & 1) : j < I.n0) ? events0 + I.event(i, 1) : ~0u;
+                        e1 = (I.dual ? j & 1 : j < I.n1) ? events1 + I.event(i, 1) : ~0u;
+                    }
+                    ++tiles;
+                }
+                events0 += I.events(0);
+                events1 += I.events(1);
+            }
+            if (lane == 0) {
+                sh.v_issued = tiles;
+                sh.tail_open = tail_open;
+                sh.tail_phase = tail_phase;
+            }
         } else if ((warp == 8 || warp == 10) && elect_one()) {
             // ------------------------------------------------ matrix products of one tile
             // The tensor cores queue a few instructions only; with a thread of its own for each tile, one tile's waits and
@@ -1125,12 +1176,11 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
     // Every warp has left its waits, so `abort` is final.  Where it is set somebody stopped before all loads had landed: the
     // thread that issued them stays until they have.
     if (tid == 9 * 32 && sh.abort) {
-        const int issued = sh.issued;
         for (int t = 0; t < 2; ++t)
             if (sh.q_issued[t]) mbar_wait_bounded(smem_u32(&sh.q_full[t]), (sh.q_issued[t] - 1) & 1, A.wait_ns);
-        for (int i = max(0, (issued + 1) / 2 - P::KS); i < (issued + 1) / 2; ++i)
+        for (int i = max(0, sh.k_issued - P::KS); i < sh.k_issued; ++i)
             mbar_wait_bounded(smem_u32(&sh.k_full[i % P::KS]), (i / P::KS) & 1, A.wait_ns);
-        for (int i = max(0, issued / 2 - P::VS); i < issued / 2; ++i)
+        for (int i = max(0, sh.v_issued - P::VS); i < sh.v_issued; ++i)
             mbar_wait_bounded(smem_u32(&sh.v_full[i % P::VS]), (i / P::VS) & 1, A.wait_ns);
         if (sh.tail_open) mbar_wait_bounded(smem_u32(&sh.v_tail), sh.tail_phase & 1, A.wait_ns);
     }
@@ -1325,7 +1375,9 @@ extern "C" kvo_status kvo_paged_chunk_attn(const kvo_paged_cache* cache, const v
     A.n_pages = cache->n_pages;
     A.max_pages = cache->max_pages;
     A.tiles = tiles;
-    A.w1 = fp8 ? 4 : 6;
+    // Measured times of 128 keys: one tile of rows is 5/7 of two in bf16 (the mixed batch 173 us with 6/7, 165 with 5/7, 171 with
+    // 4/7), and 4/7 in e4m3 (238 us, 248 with 5/7); an item in itself costs what 256 keys do.
+    A.w1 = fp8 ? 4 : 5;
     A.w2 = 7;
     A.base = 2 * CH_KEYS * A.w2;
     A.least = 2 * CH_KEYS * A.w1 + A.base;
