@@ -80,7 +80,8 @@ class Case:
                     k, v = self.rows[0][b][:see, g], self.rows[1][b][:see, g]
                     if hide:
                         k, v = k[keep], v[keep]
-                    # weights are rounded to bf16, and so are e4m3 values times scales that are no powers of two
+                    # weights are rounded to bf16, next to e4m3 pages to f16 with the page's v_scale in them (its logarithm in
+                    # fp32, and steps of 2^-24 for small ones): twice bf16's half step covers both
                     want, wl, tol, tl = ref.attention(q, k, v, 2 * ref.BF16 if self.e4m3 else ref.BF16)
                     if self.e4m3 and len(keep):
                         # q as two e4m3 values: each within 2^-17 of the row's largest
@@ -219,7 +220,7 @@ def test_rows_that_see_nothing(e4m3, d, new, lens):
 
 
 def test_wild_v_scales():
-    """Pages of V whose scales differ by 2^70: bf16 weights have the exponents for them."""
+    """Pages of V whose scales differ by 2^70: they are in the exponents of the weights, next to the scores."""
     c = Case(11, 128, 2, 4, 16, True, [40, 3], [400, 300], q_scale=8.0, wild=True)
     c.check(*c.call(), rows=[0, 1, 2, 20, 39])
 
