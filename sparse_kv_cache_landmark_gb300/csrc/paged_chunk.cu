@@ -29,8 +29,8 @@
 // What bounds it.  Long chunks: the tensor cores, which wait for the softmax (two tiles in turn, a row to a thread) at the
 // hand-overs.  32 query heads over 8 of d 128: 8192 tokens alone in bf16 395 us, 1.39 PFLOP/s of 1.91 measured for a matrix
 // product, in e4m3 459; 2048 behind 30000 in bf16 686 us (1.51 PFLOP/s), in e4m3 810: there the conversions of V and of P and
-// more code than the instruction caches hold.  Few rows on many keys: the loads of K and V, 16 requests of 4 tokens behind 32k
-// in bf16 6.6 TB/s.  A batch of both, 36 single tokens and 4 chunks: 166 us, 0.92 PFLOP/s.
+// more code than the instruction caches hold.  Few rows on many keys: the loads of K and V, 16 requests of 64 tokens behind 32k
+// in bf16 394 us, 5.5 TB/s.  A batch of both, 36 single tokens and 4 chunks: 166 us, 0.92 PFLOP/s.
 //
 // Why so.  One thread for both tiles' products kept one tile waiting for the other's barriers: 8192 tokens 440 -> 402 us with
 // two.  Two buffers of f16 V: 2048 e4m3 tokens behind 30000 965 us, three 787.  q split into its pieces by every CTA that
@@ -311,8 +311,9 @@ __device__ __forceinline__ bool ch_plan(ChShared& sh, const ChunkArgs& A, ChPlan
     plan.ranges = (int)min((int64_t)gridDim.x, max(total / A.least, (int64_t)1));
     const int c = blockIdx.x;
     if (c >= plan.ranges || total == 0) return false;
-    plan.lo = ch_bound(total, plan.ranges, c);
-    plan.hi = ch_bound(total, plan.ranges, c + 1);
+    const int64_t border = ch_bound(total, plan.ranges, c + (lane & 1));
+    plan.lo = __shfl_sync(0xffffffffu, border, 0);
+    plan.hi = __shfl_sync(0xffffffffu, border, 1);
     if (plan.lo >= plan.hi) return false;
     auto look = [&](int base) {
 #pragma unroll
@@ -814,8 +815,10 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
             ChWalk walk = ch_locate(A, sh.found[0], ch_request(A, sh.found[0]), sh.at[0], plan.lo);
             int high = sh.high[0];
             const int64_t lo = plan.lo, hi = plan.hi;
-            if (lane == 0) A.cut[blockIdx.x] = ch_cut(sh, A, plan, walk);    // before anything that may give up: the join follows it
-            __syncwarp();
+            if (FP8) {
+                if (lane == 0) A.cut[blockIdx.x] = ch_cut(sh, A, plan, walk);        // before anything that may give up: the join follows it
+                __syncwarp();
+            }
             bool ok = true;
             uint32_t k = 0, tiles = 0, v_issued = 0;
             uint32_t events[2] = {0, 0}, q_issued[2] = {0, 0};
@@ -951,6 +954,9 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
             __syncwarp();
             if (lane == 0) { sh.q_issued[0] = q_issued[0]; sh.q_issued[1] = q_issued[1]; }
         } else if (!FP8 && warp == 11) {
+            if (lane == 0)                     // before anything that may give up: the join follows it
+                A.cut[blockIdx.x] = ch_cut(sh, A, plan, ch_locate(A, sh.found[0], ch_request(A, sh.found[0]), sh.at[0], plan.lo));
+            __syncwarp();
             // ------------------------------------------------ V, which waits for other things than K does
             bool ok = true, tail_open = false;
             uint32_t item = 0, tiles = 0, tail_phase = 0, events0 = 0, events1 = 0;
@@ -1376,8 +1382,8 @@ extern "C" kvo_status kvo_paged_chunk_attn(const kvo_paged_cache* cache, const v
     A.max_pages = cache->max_pages;
     A.tiles = tiles;
     // Measured times of 128 keys: one tile of rows is 5/7 of two in bf16 (the mixed batch 173 us with 6/7, 165 with 5/7, 171 with
-    // 4/7), and 4/7 in e4m3 (238 us, 248 with 5/7); an item in itself costs what 256 keys do.
-    A.w1 = fp8 ? 4 : 5;
+    // 4/7), and 4/7 in e4m3 (238 us, 248 with 5/7) and of d 64 (173 us, 179 with 5/7); an item in itself costs what 128 keys do.
+    A.w1 = fp8 || D == 64 ? 4 : 5;
     A.w2 = 7;
     A.base = 2 * CH_KEYS * A.w2;
     A.least = 2 * CH_KEYS * A.w1 + A.base;
