@@ -472,7 +472,9 @@ kvo_status sparse_decode_attn_static(const void* q, const void* k_buf, const voi
 /*
  * Around the decode step: rotary positions, a paged cache held on the GPU
  * (bf16, or 8 bits with a scale for each page and KV head) with the attention
- * that reads it, and the attention over whole prompts.  Like sparse_decode_attn_static these calls need no context;
+ * that reads it, for one new token of each request or several, the attention over
+ * whole prompts, and the bookkeeping of the cache's pages: who holds which, forks
+ * that share them, compaction, copies.  Like sparse_decode_attn_static these calls need no context;
  * every pointer is memory of the current device unless stated, nothing is
  * allocated, kept or synchronized, and all of them can be captured into a CUDA
  * graph.  `stream` NULL is the legacy default stream.  Arguments are checked on
@@ -934,10 +936,11 @@ kvo_status kvo_profile_trace(kvo_ctx* ctx, double* start_ms, double* end_ms, int
 kvo_status kvo_set_wait_test(kvo_ctx* ctx, int64_t limit_ns, int skip_tile);
 
 /*
- * kvo_set_call_wait_test -- the same for the context-free kvo_paged_attn and
- * kvo_prompt_attn, in the calls that this thread makes (and captures) from now
- * on.  skip >= 0 makes every warp of the former announce its tile number skip
- * without copying it, and every CTA of the latter its load number skip (K and V
+ * kvo_set_call_wait_test -- the same for the context-free kvo_paged_attn,
+ * kvo_paged_chunk_attn and kvo_prompt_attn, in the calls that this thread makes
+ * (and captures) from now on.  skip >= 0 makes every warp of the first (and of the
+ * second with up to 16 rows to a request) announce its tile number skip
+ * without copying it, and every CTA of the others its load number skip (K and V
  * of the first tile of keys are 0 and 1, of the next 2 and 3).  Errors:
  * KVO_ERR_INVALID for limit_ns outside 1 ms .. 10 s or skip < -1.  Not for
  * production use.
