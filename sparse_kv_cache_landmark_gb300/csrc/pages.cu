@@ -62,40 +62,48 @@ __device__ __forceinline__ int block_sum(int v, int* sums, int& all) {
     return s - v + warps_before(sums, all);
 }
 
-// A warp's share of the pages: a run of whole groups of 32, in the order of CTAs and warps.
-struct Share {
-    int first, end;
+// The pages are dealt to the cluster's warps in rounds, at most 32 of them: a run of k groups of 32 pages to each warp, in the
+// order of CTAs and warps, then the next round.  The lowest free pages, which are given out first, lie in every warp's hands.
+struct Deal {
+    int warps, mine, k, rounds;               // `mine`: this warp among them
 };
-__device__ __forceinline__ Share pg_share(const Book& B) {
-    const int64_t warps = (int64_t)cluster_size() * (PG_THREADS / 32), groups = ((int64_t)B.n_pages + 31) / 32;
-    const int64_t each = 32 * ((groups + warps - 1) / warps), at = ((int64_t)cluster_rank() * (PG_THREADS / 32) + (threadIdx.x >> 5)) * each;
-    return {(int)min(at, (int64_t)B.n_pages), (int)min(at + each, (int64_t)B.n_pages)};
+// The first `idle` CTAs of a cluster of several take none.
+__device__ __forceinline__ Deal pg_deal(const Book& B, int idle = 0) {
+    const int ctas = (int)cluster_size(), skip = ctas > 1 ? idle : 0, groups = B.n_pages / 32 + (B.n_pages % 32 > 0);
+    Deal d;
+    d.warps = (ctas - skip) * (PG_THREADS / 32);
+    d.mine = ((int)cluster_rank() - skip) * (PG_THREADS / 32) + (int)(threadIdx.x >> 5);
+    d.k = (groups - 1) / (32 * d.warps) + 1;
+    d.rounds = d.mine < 0 ? 0 : (groups - 1) / (d.warps * d.k) + 1;
+    return d;
 }
-// Whole warp: f(page, refs, whether there is such a page) for the share, a page to a lane, until it returns false (to all).
-template <typename F>
-__device__ __forceinline__ void pg_each(const Book& B, const Share& s, F&& f) {
+// The warp's groups number rounds * k.  The first page of its j-th; behind all pages where there is none.
+__device__ __forceinline__ uint32_t pg_first(const Deal& d, int j) {
+    const int round = j / d.k;
+    return round < d.rounds ? ((uint32_t)(round * d.warps + d.mine) * d.k + (j - round * d.k)) * 32 : 1u << 31;
+}
+// Whole warp, its groups j0 .. j0 + 31: lane i gets the i-th one's free pages, a bit each.  Loops that stay loops: these
+// kernels run for some microseconds, and every line of code that they pass has to be fetched.
+__device__ __forceinline__ unsigned pg_masks(const Book& B, uint32_t first) {
     constexpr int AT_ONCE = 16;
     const int lane = threadIdx.x & 31;
-    for (int p0 = s.first; p0 < s.end; p0 += 32 * AT_ONCE) {
+    unsigned mask = 0;
+#pragma unroll 1
+    for (int h = 0; h < 32; h += AT_ONCE) {
         int v[AT_ONCE];
+        if (__shfl_sync(0xffffffffu, first, h) >= (uint32_t)B.n_pages) break;
 #pragma unroll
         for (int i = 0; i < AT_ONCE; ++i) {
-            const int p = p0 + 32 * i + lane;
-            v[i] = p < s.end ? B.refs[p] : -1;
+            const uint32_t p = __shfl_sync(0xffffffffu, first, h + i) + lane;
+            v[i] = p < (uint32_t)B.n_pages ? B.refs[p] : -1;
         }
 #pragma unroll
         for (int i = 0; i < AT_ONCE; ++i) {
-            const int p = p0 + 32 * i + lane;
-            if (p - lane >= s.end) return;
-            if (!f(p, v[i], p < s.end)) return;
+            const unsigned m = __ballot_sync(0xffffffffu, v[i] == 0);
+            if (lane == h + i) mask = m;
         }
     }
-}
-// The warp's free pages.
-__device__ __forceinline__ int pg_count_free(const Book& B, const Share& s) {
-    int n = 0;
-    pg_each(B, s, [&](int, int v, bool) { n += v == 0; return true; });
-    return (int)__reduce_add_sync(0xffffffffu, (unsigned)n);
+    return mask;
 }
 // Of a group of 32 pages: how many are free before this lane's, and in all.
 __device__ __forceinline__ int pg_free_before(int v, int& all) {
@@ -103,20 +111,81 @@ __device__ __forceinline__ int pg_free_before(int v, int& all) {
     all = __popc(free);
     return __popc(free & ((1u << (threadIdx.x & 31)) - 1));
 }
-// Free pages before this warp's share, of `free` in all; `mine` of them in this CTA before the warp, `cta` in the CTA.
-// One cluster barrier: what any thread of the cluster wrote before it is seen by all after it.
-__device__ __forceinline__ int pg_rank(int mine, int cta, int* exchange, int& free) {
-    if (threadIdx.x == 0) *exchange = cta;
-    cluster_barrier();
-    const int lane = threadIdx.x & 31, me = cluster_rank();
-    int v = lane < (int)cluster_size() ? (int)ld_cluster_u32(exchange, lane) : 0, before = lane < me ? v : 0;
+struct Ranks {
+    int count[32][33];                        // [round][warp]
+    int total[32];                            // of the rounds, in this CTA
+};
+// The warp's free pages, counted by rounds; returns the masks of its first 32 groups.
+__device__ __forceinline__ unsigned pg_count_free(const Book& B, const Deal& d, Ranks& R) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, n = d.rounds * d.k;
+    unsigned mask0 = 0;
+    R.count[lane][warp] = 0;
+    __syncwarp();
+#pragma unroll 1
+    for (int j0 = 0; j0 < n; j0 += 32) {
+        const unsigned mask = pg_masks(B, pg_first(d, j0 + lane));
+        if (j0 == 0) mask0 = mask;
+        if (mask) atomicAdd(&R.count[(j0 + lane) / d.k][warp], __popc(mask));
+    }
+    return mask0;
+}
+// Whole warp: f(page, rank) for its free pages, a page to a lane, rank by rank from round to round, up to rank n.  rank: of
+// round `lane`, from pg_rank; mask0: from pg_count_free.
+template <typename F>
+__device__ __forceinline__ void pg_give(const Book& B, const Deal& d, unsigned mask0, int rank, int n, F&& f) {
+    const int lane = threadIdx.x & 31, groups = d.rounds * d.k;
+    int at = 0, in = 0, round = 0;
+#pragma unroll 1
+    for (int j0 = 0; j0 < groups; j0 += 32) {
+        const uint32_t first = pg_first(d, j0 + lane);
+        const unsigned mask = j0 == 0 ? mask0 : pg_masks(B, first);
+#pragma unroll 1
+        for (int i = 0; i < 32 && j0 + i < groups; ++i) {
+            if (in == 0) {
+                at = __shfl_sync(0xffffffffu, rank, round++);
+                if (at >= n) return;          // ranks ascend from round to round
+            }
+            const unsigned m = __shfl_sync(0xffffffffu, mask, i);
+            const uint32_t p = __shfl_sync(0xffffffffu, first, i) + lane;
+            const int r = at + __popc(m & ((1u << lane) - 1));
+            if ((m >> lane & 1) && r < n) f((int)p, r);
+            at += __popc(m);
+            if (++in == d.k) in = 0;
+        }
+    }
+}
+// Free pages before this warp's run of round `lane`, of `free` in all, from the counts.  Barriers of this CTA and of the
+// cluster: what any thread of the cluster wrote before is seen by all after it.
+__device__ __forceinline__ int pg_rank(Ranks& R, int& free) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, me = (int)cluster_rank(), ctas = (int)cluster_size();
+    __syncthreads();
+    const int mine = R.count[warp][lane];     // this warp sums round `warp` up
+    int c = mine;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-        v += __shfl_xor_sync(0xffffffffu, v, o);
-        before += __shfl_xor_sync(0xffffffffu, before, o);
+        const int x = __shfl_up_sync(0xffffffffu, c, o);
+        if (lane >= o) c += x;
     }
-    free = v;
-    return before + mine;
+    R.count[warp][lane] = c - mine;
+    if (lane == 31) R.total[warp] = c;
+    cluster_barrier();
+    int all = 0, before = 0;
+    uint32_t t[PG_CLUSTER];
+#pragma unroll
+    for (int q = 0; q < PG_CLUSTER; ++q) t[q] = q < ctas ? ld_cluster_u32(&R.total[lane], q) : 0;
+#pragma unroll
+    for (int q = 0; q < PG_CLUSTER; ++q) {
+        all += (int)t[q];
+        if (q < me) before += (int)t[q];
+    }
+    c = all;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int x = __shfl_up_sync(0xffffffffu, c, o);
+        if (lane >= o) c += x;
+    }
+    free = __shfl_sync(0xffffffffu, c, 31);
+    return c - all + before + R.count[lane][warp];
 }
 
 // ------------------------------------------------------------------ reserve
@@ -124,63 +193,55 @@ __global__ void __launch_bounds__(PG_THREADS, 1) pages_reserve_kernel(const Book
     extern __shared__ int32_t smem[];
     int32_t* end = smem;                      // [batch]: pages asked for by the requests up to this one
     int32_t* had = smem + B.batch;            // [batch]: pages held before
-    __shared__ int sums[32], free_sums[32], exchange, given;
+    __shared__ int sums[32], given;
+    __shared__ Ranks ranks;
     grid_wait();
     const int tid = threadIdx.x;
     if (tid == 0) given = 0;
     const int per = (B.batch + PG_THREADS - 1) / PG_THREADS, b0 = min(tid * per, B.batch), b1 = min(b0 + per, B.batch);
     int need = 0;
+#pragma unroll 1
     for (int b = b0; b < b1; ++b) {
         const int w = want[b], h = B.held[b];
-        const int pages = (int)(((int64_t)w + B.page - 1) / B.page);
+        const int pages = (int)(((unsigned)max(w, 0) + B.page - 1) / B.page);
         const bool bad = w < 0 || pages > B.max_pages || h < 0 || h > B.max_pages;
         if (bad && cluster_rank() == 0) pg_report(B, KVO_DEV_BAD_COUNT);
         if (!bad) need += max(pages - h, 0);
         end[b] = need;
         had[b] = h;
     }
-    const Share share = pg_share(B);
-    const int free_here = pg_count_free(B, share);
-    if (tid % 32 == 0) free_sums[tid / 32] = free_here;
-    int all, cta, free;
-    const int asked_before = block_sum(need, sums, all);      // its barrier is that of free_sums as well
-    const int rank_here = warps_before(free_sums, cta);
+    const Deal deal = pg_deal(B);
+    const unsigned mask0 = pg_count_free(B, deal, ranks);
+    int all, free;
+    const int asked_before = block_sum(need, sums, all);
+#pragma unroll 1
     for (int b = b0; b < b1; ++b) end[b] += asked_before;
-    int rank = pg_rank(rank_here, cta, &exchange, free);         // (also a barrier of this CTA, for `end`)
+    const int rank = pg_rank(ranks, free);         // (also a barrier of this CTA, for `end`)
     int last = 0;
+#pragma unroll 1
     for (int b = b0; b < b1; ++b)
         if (end[b] <= free) last = end[b];
     if (last) atomicMax(&given, last);
     __syncthreads();
     const int n = given;
     if (cluster_rank() == 0)
+#pragma unroll 1
         for (int b = b0; b < b1; ++b) {
             const int mine = end[b] - (b ? end[b - 1] : 0);
             if (mine && end[b] <= n) B.held[b] = had[b] + mine;
             if (mine && end[b] > n) pg_report(B, KVO_DEV_NO_PAGES);
         }
-    if (rank < n && free_here) {
-        int b = -1;
-        pg_each(B, share, [&](int p, int v, bool) {
-            int here;
-            const int r = rank + pg_free_before(v, here);
-            if (v == 0 && r < n) {
-                if (b < 0) {                  // the first request that asked for more than r pages with those before it
-                    b = 0;
-                    for (int len = B.batch; len > 1;) {
-                        const int half = len / 2;
-                        if (end[b + half - 1] <= r) b += half;
-                        len -= half;
-                    }
-                }
-                while (end[b] <= r) ++b;
-                B.table[(int64_t)b * B.max_pages + had[b] + r - (b ? end[b - 1] : 0)] = p;
-                B.refs[p] = 1;
-            }
-            rank += here;
-            return rank < n;
-        });
-    }
+    pg_give(B, deal, mask0, rank, n, [&](int p, int r) {
+        int b = 0;                            // the first request that asked for more than r pages with those before it
+        for (int len = B.batch; len > 1;) {
+            const int half = len / 2;
+            if (end[b + half - 1] <= r) b += half;
+            len -= half;
+        }
+        while (end[b] <= r) ++b;
+        B.table[(int64_t)b * B.max_pages + had[b] + r - (b ? end[b - 1] : 0)] = p;
+        B.refs[p] = 1;
+    });
     cluster_barrier();                        // nobody leaves while its sum is read
 }
 
@@ -211,7 +272,7 @@ __device__ __forceinline__ void fork_gather(const ForkArgs& A, int b, int t) {
     if (p < -1 || p >= B.batch) bad = true;
     else if (p < 0) after = 0;
     else {
-        const int pages = (int)(((int64_t)max(keep, 0) + B.page - 1) / B.page), most = p == b ? before : B.held[p];
+        const int pages = (int)(((unsigned)max(keep, 0) + B.page - 1) / B.page), most = p == b ? before : B.held[p];
         if (keep < 0 || pages > most || most > B.max_pages) bad = true;
         else { after = pages; part = keep % B.page; }
     }
@@ -290,7 +351,8 @@ __global__ void __launch_bounds__(PG_THREADS, 1) pages_fork_kernel(const ForkArg
     constexpr int AT_ONCE = PG_THREADS / PG_ROW_THREADS;
     const Book& B = A.book;
     extern __shared__ int32_t smem[];
-    __shared__ int sums[32], free_sums[32], exchange;
+    __shared__ int sums[32];
+    __shared__ Ranks ranks;
     const int tid = threadIdx.x;
     int32_t *key = smem, *first = smem + A.slots, *holders = smem + 2 * A.slots;
     if (cluster_rank() == 0)
@@ -305,13 +367,11 @@ __global__ void __launch_bounds__(PG_THREADS, 1) pages_fork_kernel(const ForkArg
         for (int b = cta_row; b < B.batch; b += ctas * AT_ONCE) fork_write(A, b, tid % PG_ROW_THREADS);
         return;
     }
-    const Share share = pg_share(B);
-    const int free_here = pg_count_free(B, share);
-    if (tid % 32 == 0) free_sums[tid / 32] = free_here;
-    __syncthreads();
-    int cta, free;
-    const int rank_here = warps_before(free_sums, cta);
-    int mine = 0, first_rank = 0;             // copies of this thread's requests (first CTA only), and those before them
+    const Deal deal = pg_deal(B, 1);          // the first CTA has the part-filled pages to do
+    const unsigned mask0 = pg_count_free(B, deal, ranks);
+    int free, first_rank = 0;                 // (first CTA) copies of the requests before this thread's
+    unsigned mine = 0;                        // which of its up to 8 get one
+    static_assert(PG_BATCH / PG_THREADS <= 32, "a bit to a request");
     const int per = (B.batch + PG_THREADS - 1) / PG_THREADS, b0 = min(tid * per, B.batch), b1 = min(b0 + per, B.batch);
     int total = 0;
     if (cluster_rank() == 0) {
@@ -323,6 +383,7 @@ __global__ void __launch_bounds__(PG_THREADS, 1) pages_fork_kernel(const ForkArg
                 i = (i + 1) & (A.slots - 1);
             }
         };
+#pragma unroll 1
         for (int b = b0; b < b1; ++b) {
             const int page = A.meta[b].z;
             if (page < 0) continue;
@@ -331,25 +392,29 @@ __global__ void __launch_bounds__(PG_THREADS, 1) pages_fork_kernel(const ForkArg
             atomicAdd(holders + i, 1);
         }
         __syncthreads();
-        auto copies = [&](int b, int page) {
-            if (page < 0) return false;
+#pragma unroll 1
+        for (int b = b0; b < b1; ++b) {
+            const int page = A.meta[b].z;
+            if (page < 0) continue;
+            const int uses = B.refs[page];
             const uint32_t i = find(page);
-            return !(first[i] == b && B.refs[page] == holders[i]);
-        };
-        for (int b = b0; b < b1; ++b) mine += copies(b, A.meta[b].z);
-        first_rank = block_sum(mine, sums, total);
+            if (first[i] != b || uses != holders[i]) mine |= 1u << (b - b0);
+        }
+        first_rank = block_sum(__popc(mine), sums, total);
         int at = first_rank;
+#pragma unroll 1
         for (int b = b0; b < b1; ++b)
-            if (copies(b, A.meta[b].z)) A.list[at++] = b;
+            if (mine >> (b - b0) & 1) A.list[at++] = b;
         if (tid == 0) A.list[B.batch] = total;
     }
-    int rank = pg_rank(rank_here, cta, &exchange, free);
+    const int rank = pg_rank(ranks, free);
     const int n = min(__ldcg(A.list + B.batch), free);
     if (cluster_rank() == 0) {
         int at = first_rank;
+#pragma unroll 1
         for (int b = b0; b < b1; ++b) {
             const int4 m = A.meta[b];
-            const bool copied = mine && at < total && A.list[at] == b;
+            const bool copied = mine >> (b - b0) & 1;
             const bool lost = copied && at >= n;
             if (copied) {
                 ++at;
@@ -362,21 +427,14 @@ __global__ void __launch_bounds__(PG_THREADS, 1) pages_fork_kernel(const ForkArg
         for (int i = n + tid; i < B.batch; i += PG_THREADS) A.src[i] = A.dst[i] = -1;
         if (tid == 0) *A.count = n;
     }
-    if (rank < n && free_here)
-        pg_each(B, share, [&](int p, int v, bool) {
-            int here;
-            const int r = rank + pg_free_before(v, here);
-            if (v == 0 && r < n) {
-                const int b = __ldcg(A.list + r);
-                const int4 m = A.meta[b];
-                B.table[(int64_t)b * B.max_pages + m.y - 1] = p;
-                B.refs[p] = 1;
-                A.src[r] = m.z;
-                A.dst[r] = p;
-            }
-            rank += here;
-            return rank < n;
-        });
+    pg_give(B, deal, mask0, rank, n, [&](int p, int r) {
+        const int b = __ldcg(A.list + r);
+        const int4 m = A.meta[b];
+        B.table[(int64_t)b * B.max_pages + m.y - 1] = p;
+        B.refs[p] = 1;
+        A.src[r] = m.z;
+        A.dst[r] = p;
+    });
     cluster_barrier();                        // nobody leaves while its sum is read
 }
 
@@ -395,64 +453,68 @@ struct CompactArgs {
 // First launch, one cluster: L pages are in use; the i-th of those at L and behind goes to the i-th free one before L.
 __global__ void __launch_bounds__(PG_THREADS, 1) pages_compact_kernel(const CompactArgs A) {
     const Book& B = A.book;
-    __shared__ int sums[32], exchange;
+    __shared__ Ranks ranks;
+    __shared__ int below;                     // free pages before L among this CTA's
+    if (threadIdx.x == 0) below = 0;
     grid_wait();
     grid_launch_next();
-    const Share share = pg_share(B);
-    const int free_here = pg_count_free(B, share);
-    if (threadIdx.x % 32 == 0) sums[threadIdx.x / 32] = free_here;
-    __syncthreads();
-    int cta, free;
-    const int rank_here = warps_before(sums, cta);
-    const int first = pg_rank(rank_here, cta, &exchange, free);
+    const Deal deal = pg_deal(B);
+    const int lane = threadIdx.x & 31, groups = deal.rounds * deal.k;
+    const unsigned mask0 = pg_count_free(B, deal, ranks);
+    int free, mine = 0;
+    const int rank = pg_rank(ranks, free);
     const int live = B.n_pages - free;
-    int rank = first;
-    if (share.first <= live)
-        pg_each(B, share, [&](int p, int v, bool real) {
-            int here;
-            const int r = rank + pg_free_before(v, here);
-            if (real && p == live) A.head[1] = r;             // the free pages before L are as many as the used ones from L on
-            if (v == 0 && p < live) A.dst[r] = p;
-            rank += here;
-            return p - (int)(threadIdx.x & 31) + 32 <= live;
-        });
+    pg_give(B, deal, mask0, rank, free, [&](int p, int r) {
+        if (p < live) { A.dst[r] = p; ++mine; }
+    });
+    mine = (int)__reduce_add_sync(0xffffffffu, (unsigned)mine);
+    if (lane == 0 && mine) atomicAdd(&below, mine);
+    cluster_barrier();
+    int moves = lane < (int)cluster_size() ? (int)ld_cluster_u32(&below, lane) : 0;
+    moves = (int)__reduce_add_sync(0xffffffffu, (unsigned)moves);
     if (cluster_rank() == 0 && threadIdx.x == 0) {
         A.head[0] = live;
-        if (live == B.n_pages) A.head[1] = 0;
+        A.head[1] = moves;
     }
-    cluster_barrier();
-    const int moves = __ldcg(A.head + 1);
-    // Free pages before L may have been filled meanwhile: counted are those from L on.
-    rank = share.first > live ? first : moves;
     constexpr int AT_ONCE = 8;                // groups whose places are fetched together: a store may not pass a load
-    const int lane = threadIdx.x & 31;
-    for (int p0 = max(share.first, live / 32 * 32) + lane; p0 - lane < share.end; p0 += 32 * AT_ONCE) {
-        int v[AT_ONCE], at[AT_ONCE], to[AT_ONCE];
+    int before = moves;
+#pragma unroll 1
+    for (int j0 = 0; j0 < groups; j0 += AT_ONCE) {
+        const int j = j0 + (lane & (AT_ONCE - 1)), round = j / deal.k;
+        const uint32_t first = pg_first(deal, j);
+        // Free pages before L may have been filled meanwhile: counted are those from L on.
+        const int at_round = __shfl_sync(0xffffffffu, rank, round & 31), start = first >= (uint32_t)live ? at_round : moves;
+        const unsigned begins = __ballot_sync(0xffffffffu, j == round * deal.k);
+        if (__shfl_sync(0xffffffffu, first, AT_ONCE - 1) + 32 <= (uint32_t)live) continue;      // (all before L: `before` is `moves`)
+        int p[AT_ONCE], v[AT_ONCE], at[AT_ONCE], to[AT_ONCE];
 #pragma unroll
         for (int i = 0; i < AT_ONCE; ++i) {
-            const int p = p0 + 32 * i;
-            v[i] = p >= live && p < share.end ? B.refs[p] : INT32_MIN;
+            const uint32_t x = __shfl_sync(0xffffffffu, first, i) + lane;
+            p[i] = (int)x;
+            v[i] = x >= (uint32_t)live && x < (uint32_t)B.n_pages ? B.refs[x] : INT32_MIN;
         }
 #pragma unroll
         for (int i = 0; i < AT_ONCE; ++i) {
+            const int s = __shfl_sync(0xffffffffu, start, i);
+            if (begins >> i & 1) before = s;
             int here;
-            at[i] = p0 + 32 * i - (rank + pg_free_before(v[i], here)) - (live - moves);
-            rank += here;
+            at[i] = p[i] - (before + pg_free_before(v[i], here)) - (live - moves);
+            before += here;
         }
 #pragma unroll
-        for (int i = 0; i < AT_ONCE; ++i) to[i] = v[i] != INT32_MIN && v[i] != 0 ? __ldcg(A.dst + at[i]) : p0 + 32 * i;
+        for (int i = 0; i < AT_ONCE; ++i) to[i] = v[i] != INT32_MIN && v[i] != 0 ? __ldcg(A.dst + at[i]) : p[i];
 #pragma unroll
         for (int i = 0; i < AT_ONCE; ++i) {
-            const int p = p0 + 32 * i;
             if (v[i] != INT32_MIN && v[i] != 0) {
-                A.src[at[i]] = p;
+                A.src[at[i]] = p[i];
                 A.refs_out[to[i]] = v[i];
-                if (A.refs_out == B.refs) A.refs_out[p] = 0;
+                if (A.refs_out == B.refs) A.refs_out[p[i]] = 0;
             }
-            if (v[i] != INT32_MIN) A.to[p] = to[i];
+            if (v[i] != INT32_MIN) A.to[p[i]] = to[i];
         }
     }
     if (cluster_rank() == 0 && threadIdx.x == 0) *A.count = moves;
+    cluster_barrier();                        // nobody leaves while its sum is read
 }
 
 // Second launch.  A CTA per request: the rows' entries follow their pages.  All CTAs: what the first leaves of the lists,
