@@ -134,6 +134,18 @@ __device__ __forceinline__ unsigned pg_count_free(const Book& B, const Deal& d, 
 template <typename F>
 __device__ __forceinline__ void pg_give(const Book& B, const Deal& d, unsigned mask0, int rank, int n, F&& f) {
     const int lane = threadIdx.x & 31, groups = d.rounds * d.k;
+    if (d.k == 1) {                           // a round is a group: half as much to do for each
+        uint32_t p = (uint32_t)d.mine * 32 + lane;
+#pragma unroll 2
+        for (int i = 0; i < groups; ++i, p += (uint32_t)d.warps * 32) {
+            const unsigned m = __shfl_sync(0xffffffffu, mask0, i);
+            const int at = __shfl_sync(0xffffffffu, rank, i);
+            if (at >= n) return;              // ranks ascend from round to round
+            const int r = at + __popc(m & ((1u << lane) - 1));
+            if ((m >> lane & 1) && r < n) f((int)p, r);
+        }
+        return;
+    }
     int at = 0, in = 0, round = 0;
 #pragma unroll 1
     for (int j0 = 0; j0 < groups; j0 += 32) {
@@ -143,7 +155,7 @@ __device__ __forceinline__ void pg_give(const Book& B, const Deal& d, unsigned m
         for (int i = 0; i < 32 && j0 + i < groups; ++i) {
             if (in == 0) {
                 at = __shfl_sync(0xffffffffu, rank, round++);
-                if (at >= n) return;          // ranks ascend from round to round
+                if (at >= n) return;
             }
             const unsigned m = __shfl_sync(0xffffffffu, mask, i);
             const uint32_t p = __shfl_sync(0xffffffffu, first, i) + lane;
