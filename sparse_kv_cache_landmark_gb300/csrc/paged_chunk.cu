@@ -27,10 +27,10 @@
 // and the sum of the weights takes each page's share times 1 / v_scale, in fp32.
 //
 // What bounds it.  Long chunks: the tensor cores, which wait for the softmax (two tiles in turn, a row to a thread) at the
-// hand-overs.  32 query heads over 8 of d 128: 8192 tokens alone in bf16 395 us, 1.39 PFLOP/s of 1.91 measured for a matrix
-// product, in e4m3 459; 2048 behind 30000 in bf16 686 us (1.51 PFLOP/s), in e4m3 810: there the conversions of V and of P and
+// hand-overs.  32 query heads over 8 of d 128: 8192 tokens alone in bf16 393 us, 1.40 PFLOP/s of 1.91 measured for a matrix
+// product, in e4m3 466; 2048 behind 30000 in bf16 674 us (1.54 PFLOP/s), in e4m3 820: there the conversions of V and of P and
 // more code than the instruction caches hold.  Few rows on many keys: the loads of K and V, 16 requests of 64 tokens behind 32k
-// in bf16 394 us, 5.5 TB/s.  A batch of both, 36 single tokens and 4 chunks: 166 us, 0.92 PFLOP/s.
+// in bf16 386 us, 5.6 TB/s.  A batch of both, 36 single tokens and 4 chunks: 164 us, 0.93 PFLOP/s.
 //
 // Why so.  One thread for both tiles' products kept one tile waiting for the other's barriers: 8192 tokens 440 -> 402 us with
 // two.  Two buffers of f16 V: 2048 e4m3 tokens behind 30000 965 us, three 787.  q split into its pieces by every CTA that

@@ -8,6 +8,12 @@
 // What bounds the book's calls is latency: a look at refs (1 MB for 262144 pages, 0.2 us of HBM) and two dependent passes
 // over it with a sum over all pages between.  One cluster of 8 CTAs takes them in one launch, exchanging the CTAs' sums
 // through distributed shared memory; rows of the table, which may be long, are moved by other CTAs.
+//
+// Measured (replayed graph): 256 requests of 2000 to 16384 tokens forked in a pool of 196608 pages of 16 9.3 us (1.2 for the rows'
+// uses, 3 for the look at refs, 2 for the ranks, 2 for pages and lists), 32 beams 8.3 in one launch; room for 64 prompts in a pool of
+// 262144 7.4 us; such a pool compacted 20 us (3 for the look, 2 for the ranks, 3 and 6 for the two lists, 4 for the rows), one of 2048
+// pages 8.7.  Clusters of 16 CTAs: 11.4 us for the 256, 11.2 for the prompts, 19.3 for the compaction.  A run of pages to each
+// warp instead of rounds (below): 14.4, 14 and 22, as few warps hold what is given out.
 #include <algorithm>
 
 #include "kvo_internal.cuh"
@@ -580,7 +586,8 @@ struct CopyArgs {
 };
 constexpr int PC_THREADS = 256, PC_LOADS = 8, PC_PIECE = PC_THREADS * PC_LOADS * 16;
 
-// Bound by HBM: every byte is read once and written once.  A piece is 32 KB of a page (or a page, where that is smaller).
+// Bound by HBM: every byte is read once and written once.  A piece is 32 KB of a page (or a page, where that is smaller), eight
+// 16-byte loads to a thread.  501 pages of 4 layers, 263 MB read and as many written, 87 us: 6.1 TB/s, 0.89 of a measured copy.
 __global__ void __launch_bounds__(PC_THREADS) pages_copy_kernel(const CopyArgs A) {
     grid_wait();
     int n = A.moves;

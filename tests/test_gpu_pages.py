@@ -97,7 +97,7 @@ def check_moves(got, moves, size):
 @pytest.mark.parametrize("batch,n_pages,page,most,seed", [
     (1, 1, 16, 1, 0), (1, 5, 16, 3, 1), (3, 17, 16, 9, 2), (7, 63, 32, 8, 3), (33, 1000, 64, 40, 4), (130, 4096, 128, 33, 5),
     (64, 4097, 16, 90, 6), (64, 8191, 16, 90, 7), (300, 40003, 16, 120, 8), (1030, 9000, 16, 7, 9), (256, 300000, 16, 1000, 10),
-    (4000, 20000, 32, 4, 11), (8192, 33000, 16, 3, 12)])
+    (4000, 20000, 32, 4, 11), (8192, 33000, 16, 3, 12), (256, 700001, 16, 1200, 13)])
 def test_a_long_run_matches_plain_python(batch, n_pages, page, most, seed):
     """Forks, cuts, reorders, frees, reservations and compactions in turn, the pool often short of pages."""
     rng = random.Random(seed)
