@@ -404,6 +404,29 @@ kvo_page_book book_of(PyObject* table, PyObject* held, PyObject* refs, int64_t p
 at::Tensor ids(PyObject* o, const char* name, const at::Device& dev, int64_t n) {
     return o == Py_None ? empty({n}, at::kInt, dev) : need(o, name, dev, at::kInt, {{n}});
 }
+// src, dst [n] and count [1] of the calls that list moves: one allocation for all that are not given, at 1 us each.
+struct Moves {
+    at::Tensor src, dst, count;
+
+    Moves(PyObject* s, PyObject* d, PyObject* c, const at::Device& dev, int64_t n) {
+        if (s != Py_None || d != Py_None || c != Py_None) {
+            src = ids(s, "src", dev, n);
+            dst = ids(d, "dst", dev, n);
+            count = ids(c, "count", dev, 1);
+            return;
+        }
+        const at::Tensor all = empty({2 * n + 1}, at::kInt, dev);
+        auto part = [&](int64_t at, int64_t size) {
+            at::Tensor t = at::detail::make_tensor<c10::TensorImpl>(c10::Storage(all.storage()), all.key_set(), all.dtype());
+            t.unsafeGetTensorImpl()->set_storage_offset(at);
+            t.unsafeGetTensorImpl()->set_sizes_contiguous({size});
+            return t;
+        };
+        src = part(0, n);
+        dst = part(n, n);
+        count = part(2 * n, 1);
+    }
+};
 at::Tensor scratch(PyObject* o, const at::Device& dev, size_t bytes) {
     return o == Py_None ? empty({(int64_t)bytes}, at::kByte, dev) : need(o, "workspace", dev, at::kByte);
 }
@@ -442,16 +465,16 @@ PyObject* py_paged_fork(PyObject*, PyObject* const* a, Py_ssize_t n) {
         const int32_t* parent = (const int32_t*)need(a[3], "parent", dev, at::kInt, {{b.batch}}).data_ptr();
         const int32_t* keep = (const int32_t*)need(a[4], "keep", dev, at::kInt, {{b.batch}}).data_ptr();
         const Stream stream(a[11], dev);
-        const at::Tensor src = ids(a[6], "src", dev, b.batch), dst = ids(a[7], "dst", dev, b.batch), count = ids(a[8], "count", dev, 1);
+        const Moves m(a[6], a[7], a[8], dev, b.batch);
         int32_t* status = status_of(a[10], dev);
         size_t bytes = 0;
         sized(kvo_paged_fork_workspace(&b, &bytes));
         const at::Tensor ws = scratch(a[9], dev, bytes);
         launch(dev, [&] {
-            return kvo_paged_fork(&b, parent, keep, (int32_t*)src.data_ptr(), (int32_t*)dst.data_ptr(), (int32_t*)count.data_ptr(),
+            return kvo_paged_fork(&b, parent, keep, (int32_t*)m.src.data_ptr(), (int32_t*)m.dst.data_ptr(), (int32_t*)m.count.data_ptr(),
                                   ws.data_ptr(), ws.numel(), status, stream.handle);
         });
-        return three(src, dst, count);
+        return three(m.src, m.dst, m.count);
     });
 }
 
@@ -464,16 +487,16 @@ PyObject* py_paged_compact(PyObject*, PyObject* const* a, Py_ssize_t n) {
         int32_t* table_out = a[3] == Py_None ? nullptr : (int32_t*)need(a[3], "table_out", dev, at::kInt, at::IntArrayRef(shape)).data_ptr();
         int32_t* refs_out = a[4] == Py_None ? nullptr : (int32_t*)need(a[4], "refs_out", dev, at::kInt, at::IntArrayRef(rshape)).data_ptr();
         const Stream stream(a[10], dev);
-        const at::Tensor src = ids(a[5], "src", dev, b.n_pages / 2), dst = ids(a[6], "dst", dev, b.n_pages / 2), count = ids(a[7], "count", dev, 1);
+        const Moves m(a[5], a[6], a[7], dev, b.n_pages / 2);
         int32_t* status = status_of(a[9], dev);
         size_t bytes = 0;
         sized(kvo_paged_compact_workspace(&b, &bytes));
         const at::Tensor ws = scratch(a[8], dev, bytes);
         launch(dev, [&] {
-            return kvo_paged_compact(&b, table_out, refs_out, (int32_t*)src.data_ptr(), (int32_t*)dst.data_ptr(), (int32_t*)count.data_ptr(),
+            return kvo_paged_compact(&b, table_out, refs_out, (int32_t*)m.src.data_ptr(), (int32_t*)m.dst.data_ptr(), (int32_t*)m.count.data_ptr(),
                                      ws.data_ptr(), ws.numel(), status, stream.handle);
         });
-        return three(src, dst, count);
+        return three(m.src, m.dst, m.count);
     });
 }
 
