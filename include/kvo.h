@@ -588,7 +588,9 @@ kvo_status kvo_paged_append(const kvo_paged_cache* cache, const void* k, int64_t
  *   fp32 would carry no more.  With e4m3 pages those are 11 bits of weights down
  *   to 2^-20 of the running maximum's, and smaller ones are rounded to multiples
  *   of 2^-30 of it; a page's weights count times its v_scale over the largest of
- *   the group's there.  Two calls give the same bits.
+ *   the group's there, and v_scale is to lie between 2^-100 and 2^100 over the tokens
+ *   (sums of weights and codes are held in fp32 times v_scale).  Two calls give the
+ *   same bits.
  *   workspace: kvo_paged_attn_workspace bytes (0 for small calls: NULL will do),
  *   256-byte aligned, contents undefined before and after; one call at a time may
  *   use it (two captured graphs that may overlap need one each).
@@ -629,7 +631,8 @@ kvo_status kvo_paged_attn_workspace(const kvo_paged_cache* cache, int n_q_heads,
  *   running maximum of those, steps of 2^-30 of it below), and, but for few rows, q is
  *   taken as the sum of two e4m3 values times a power of two: exact where a value is
  *   at least 2^-9 of its row's largest, to 2^-17
- *   of that one else.  A row that sees no token gets o = 0, lse = -inf; rows
+ *   of that one else.  v_scale may have any finite size, 0 among them, and pages any
+ *   scales next to each other (up to 16 rows: as kvo_paged_attn).  A row that sees no token gets o = 0, lse = -inf; rows
  *   outside every request keep their bytes.  What lies in a page behind the last
  *   token is never used, NaN included; among the new tokens of a request a NaN or an
  *   infinity in v may reach tokens before it in the same 128 keys.  Two calls give

@@ -23,8 +23,10 @@
 // the sum of two e4m3 values, exactly for what is at least 2^-9 of that largest and to 2^-17 of it for all below (a bf16
 // value has 8 bits, an e4m3 value 4), and two 8-bit products take the time of one of bf16.  V is widened to f16, exactly, on its
 // way through shared memory.  A page's k_scale multiplies its scores; its v_scale goes into the exponents of its weights,
-// exp2(s + log2 v_scale - m) with m the maximum of those, so that f16 holds what contributes most whatever the scales are,
-// and the sum of the weights takes each page's share times 1 / v_scale, in fp32.
+// exp2(s + log2 v_scale - m) with m the maximum of those, so that f16 holds what contributes most whatever the scales are.
+// The sum l of the exponentials without v_scale takes each page's share times 2^c / v_scale, in fp32: l counts in units of
+// 2^(m - c), with 2^c about the first page's scale, or what keeps l in fp32's range where scales differ by more than 2^32; c
+// is a whole number, so that o = (sum of weights and codes) / l * 2^c takes no further rounding.
 //
 // What bounds it.  Long chunks: the tensor cores, which wait for the softmax (two tiles in turn, a row to a thread) at the
 // hand-overs.  32 query heads over 8 of d 128: 8192 tokens alone in bf16 393 us, 1.40 PFLOP/s of 1.91 measured for a matrix
@@ -63,6 +65,11 @@ constexpr int CH_ITEMS = 4;                // descriptors
 constexpr int CH_NONE = INT32_MIN;         // no page
 constexpr int CH_NAN = -128;               // the exponent of a row of q that is not finite
 constexpr int CH_SCALES = 8;               // tiles of keys whose scales are held
+constexpr uint32_t CH_FAR = 1u << 8;       // beside a tile's bad groups: some v_scale of the item so far is far from its first,
+constexpr float CH_SPREAD = 32.f;          // log2: that is, further than this
+constexpr float CH_NEAR = 40.f;            // log2: where l takes 2^-c at an item's end
+constexpr float CH_NO_SCALE = -160.f;      // log2 of a v_scale of 0: 2^-160 times any code is 0 in fp32
+constexpr float CH_TOP_C = 256.f;          // above any c that a page asks for
 
 template <int D, bool FP8>
 struct ChShape;
@@ -102,7 +109,7 @@ struct ChunkArgs {
     int32_t* status;
     struct ChunkCut* cut;          // [CTAs]
     float* part_o;                 // [CTAs][2][tiles][D / 4][128] of 4 values
-    float2* part_ml;               // [CTAs][2][tiles][128]
+    void* part_ml;                 // [CTAs][2][tiles][128]: m, l (float2) or, next to e4m3 pages, m, l, c (float4)
     int64_t total;
     int batch, hq, hkv, r, tq, page, shift, n_pages, max_pages, tiles;
     int w1, w2, base;              // cost of a key for one tile of rows and for two, and of an item in itself
@@ -144,7 +151,8 @@ struct ChShared {
     ChunkItem item[CH_ITEMS];
     alignas(16) float k_scale[CH_SCALES][8];
     alignas(16) float v_log[CH_SCALES][8];          // of each 16 keys of a tile: k_scale, log2 of v_scale
-    uint32_t bad[CH_SCALES];       // groups of 16 keys in pages that do not exist
+    alignas(16) float v_share[CH_SCALES][8];        // 2^v_first over v_scale; 0 from CH_FAR on
+    uint2 bad[CH_SCALES];          // groups of 16 keys in pages that do not exist, and CH_FAR; log2 of the item's first v_scale, rounded
     uint32_t tmem;
     int abort;
     int k_issued, v_issued, tail_open, tail_phase, q_issued[2];
@@ -153,7 +161,10 @@ struct ChShared {
             int64_t sum[16], at[2];
             int32_t top[16], found[2], high[2];
         };
-        float2 share[CH_ROWS];     // the two halves of a dual item: maximum and sum one way, weights the other
+        struct {                   // the two halves of a dual item: maximum, sum and c one way, weights and c the other
+            float2 share[CH_ROWS];
+            int16_t share_c[CH_ROWS];
+        };
     };
 };
 
@@ -387,6 +398,14 @@ __device__ __forceinline__ bool group_any(int id, bool x) {
     return any != 0;
 }
 
+// What the sum l of a row's exponentials counts in, 2^(m - c).
+struct ChUnit {
+    float m, c;
+    __device__ __forceinline__ bool above(const ChUnit& o) const { return m - o.m > c - o.c; }
+    __device__ __forceinline__ float in(const ChUnit& o) const { return ex2((m - o.m) - (c - o.c)); }      // 1 of this in units of `o`
+    __device__ __forceinline__ ChUnit with(float to) const { return {to, floorf(to - m + c)}; }            // the next above with this m
+};
+
 // The softmax of one tile of an item: a thread owns a row; it sees its request's keys [0, limit).  False: a wait gave up.
 template <int D, bool FP8>
 __device__ __forceinline__ bool ch_softmax(ChShared& sh, const ChunkArgs& A, const ChunkItem& I, int t, uint32_t events, uint32_t keys, uint32_t& shares) {
@@ -400,9 +419,9 @@ __device__ __forceinline__ bool ch_softmax(ChShared& sh, const ChunkArgs& A, con
     // a row that is none may see anything
     const int limit = real ? (int)min(max((int64_t)tok + 1 + (I.len - I.nq), (int64_t)0), (int64_t)I.len) - I.first * CH_KEYS : INT32_MAX;
     // log2 units.  Next to e4m3 pages m is the maximum of the scores times their v_scale, and weights are held times 2^6:
-    // they are rounded to f16, whose smallest step is 2^-24.  l is in units of 2^m (times 2^6).
+    // they are rounded to f16, whose smallest step is 2^-24.  l is in units of 2^(m - c) (times 2^6); c is 0 next to bf16.
     constexpr float CH_BIAS = FP8 ? 6.f : 0.f;
-    float m = -INFINITY, l = 0.f;
+    float m = -INFINITY, l = 0.f, c = 0.f;
     float q_scale = A.scale_log2;
     int q_exp = 0;
     if (FP8 && real) q_exp = A.q_exp[(I.row + tok) * A.hq + I.g * A.r + head];
@@ -419,8 +438,11 @@ __device__ __forceinline__ bool ch_softmax(ChShared& sh, const ChunkArgs& A, con
             continue;
         }
         tc_fence_after();
+        const uint2 bads = sh.bad[slot];
+        if (FP8 && i == 0) c = __uint_as_float(bads.y);
         if (FP8 && i == 0) q_scale = q_exp == CH_NAN ? 0.f : __uint_as_float((uint32_t)(127 - q_exp) << 23) * A.scale_log2;
-        const uint32_t bad = sh.bad[slot];
+        const uint32_t bad = bads.x & 0xFF;
+        const bool far_scales = FP8 && bads.x >= CH_FAR;
         const int rem = min(limit - j * CH_KEYS, CH_KEYS);
         const bool edge = bad || __any_sync(0xffffffffu, rem < CH_KEYS);
         auto scale_of = [&](float k_scale) {   // (a masked score times zero would be NaN)
@@ -490,21 +512,52 @@ __device__ __forceinline__ bool ch_softmax(ChShared& sh, const ChunkArgs& A, con
             }
         }
         if (!FP8) top *= q_scale;
-        if (__any_sync(0xffffffffu, real && top > m + CH_RAISE)) {
+        if (far_scales || __any_sync(0xffffffffu, real && top > m + CH_RAISE)) {
             const float to = fmaxf(m, top);
             const float f = m == -INFINITY ? 0.f : ex2(m - to);
-            m = to;
+            const float l_before = l, was = m;
             l *= f;
+            m = to;
             if (i > 0) {           // these scores are complete: so is the value product that was issued before them
 #pragma unroll 1
-                for (int c = 0; c < D; c += 32) {
+                for (int x = 0; x < D; x += 32) {
                     uint32_t o[32];
-                    tmem_ld32(O + c, o);
+                    tmem_ld32(O + x, o);
                     tmem_wait_ld();
 #pragma unroll
                     for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
-                    tmem_st32(O + c, o);
+                    tmem_st32(O + x, o);
                 }
+            }
+            // Scales far apart: a weight times 2^c / v_scale may pass fp32's range, or the weight be 0 where its share of l is not.
+            // There shares are exponentials of their own (8 keys at a time: little code), and c follows down to the page that
+            // leads among them.
+            if (far_scales) {
+                // What leads m may be a larger scale alone, and what came before still be most of l: l stays, but that one that
+                // has become small is counted in a smaller unit, so that c is no lower than it has to be.
+                const float rise = l_before == 0.f ? 0.f : to - was, whole = floorf(rise);
+                const int up = l_before != 0.f && l_before < 0x1p-32f ? 127 - (int)(__float_as_uint(l_before) >> 23) : 0;
+                l = l_before * ex2(whole - rise) * __uint_as_float((uint32_t)(up + 127) << 23);
+                c = l_before == 0.f ? CH_TOP_C : c + whole + (float)up;
+                const float b = m == -INFINITY ? 0.f : CH_BIAS - m;
+#pragma unroll 1
+                for (int g = 0; g < 16; ++g) {
+                    tmem_ld8(S + 8 * g, x);
+                    tmem_wait_ld();
+                    const float v = sh.v_log[slot][g / 2], scale = scale_of(sh.k_scale[slot][g / 2]);
+                    float y[8], first = -INFINITY;
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) first = fmaxf(first, y[e] = fmaf(__uint_as_float(x[e]), scale, b + v));
+                    const bool seen = first != -INFINITY;
+                    const float low = seen ? fminf(c, floorf(v + CH_BIAS - first)) : c, by = seen ? low - v : -INFINITY;
+                    l *= ex2(low - c);
+                    c = low;                                            // no share is above 2^6
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) l += ex2(y[e] + by);
+                }
+                tmem_ld32(S, x);
+                tmem_ld32(S + 32, x + 32);
+                tmem_wait_ld();
             }
         }
         const float b = m == -INFINITY ? 0.f : CH_BIAS - m;
@@ -514,7 +567,8 @@ __device__ __forceinline__ bool ch_softmax(ChShared& sh, const ChunkArgs& A, con
         for (int h = 0; h < 2; ++h) {          // (the first half is still there)
             uint32_t p[32];
             const float4 k = *reinterpret_cast<const float4*>(&sh.k_scale[slot][4 * h]), v = *reinterpret_cast<const float4*>(&sh.v_log[slot][4 * h]);
-            const float ks[4] = {k.x, k.y, k.z, k.w}, vs[4] = {v.x, v.y, v.z, v.w};
+            const float4 share = *reinterpret_cast<const float4*>(&sh.v_share[slot][4 * h]);
+            const float ks[4] = {k.x, k.y, k.z, k.w}, vs[4] = {v.x, v.y, v.z, v.w}, shares[4] = {share.x, share.y, share.z, share.w};
 #pragma unroll
             for (int g = 0; g < 4; ++g) {
                 if (FP8) {
@@ -522,7 +576,7 @@ __device__ __forceinline__ bool ch_softmax(ChShared& sh, const ChunkArgs& A, con
                     weights(x + 16 * g, p + 8 * g, scale_of(ks[g]), b + vs[g], sum);
                     float s0, s1;
                     unpack2(add2(sum[0], sum[1]), s0, s1);
-                    total = fmaf(s0 + s1, ex2(-vs[g]), total);
+                    total = fmaf(s0 + s1, shares[g], total);
                 } else {
                     weights(x + 16 * g, p + 8 * g, q_scale, b, sum);
                 }
@@ -544,6 +598,10 @@ __device__ __forceinline__ bool ch_softmax(ChShared& sh, const ChunkArgs& A, con
         }
         l += total;
     }
+    if (FP8) {                     // for all but extreme scales c is 0 from here on
+        l *= fabsf(c) <= CH_NEAR ? ex2(-c) : 1.f;
+        c = fabsf(c) <= CH_NEAR || l == 0.f ? 0.f : c;
+    }
     if (q_exp == CH_NAN && n_tiles > 0) l = __uint_as_float(0x7FC00000u);
     if (n_tiles > 0) {
         bool ok = true;
@@ -554,16 +612,27 @@ __device__ __forceinline__ bool ch_softmax(ChShared& sh, const ChunkArgs& A, con
     // A dual item's halves: this thread writes half of the row's values, from both.
     const bool both = I.dual && I.n1 > 0;
     float w0 = t == 0 ? 1.f : 0.f, w1 = 1.f - w0;              // weights of the tiles' sums
+    float lse = 0.f;               // log2
+    // 2^c / l, but for a power of two that would take it out of fp32's range, which is left in c.
+    auto inverse = [&]() {
+        if (!FP8 || c == 0.f) return l != 0.f ? 1.f / l : 0.f;
+        const int e = min((int)(__float_as_uint(l) >> 23 & 255) - 127, 126);
+        const float all = c - (float)e, here = fminf(fmaxf(all, -64.f), 64.f);
+        c = all - here;
+        return 1.f / (l * __uint_as_float((uint32_t)(127 - e) << 23)) * ex2(here);
+    };
     if (both) {
         bool ok = true;
         if (t == 1) {
             sh.share[row] = make_float2(m, l);
+            if (FP8) sh.share_c[row] = (int16_t)c;
             warp_arrive(sh.ml_there);
             if ((threadIdx.x & 96) == 0) ok = ch_wait(sh, A, sh.weights_there, shares);
             if (group_any(2, !ok)) return false;
             const float2 x = sh.share[row];
             w0 = x.x;
             w1 = x.y;
+            if (FP8) c = sh.share_c[row];
         } else {
             if ((threadIdx.x & 96) == 0) ok = ch_wait(sh, A, sh.ml_there, shares);
             if (group_any(1, !ok)) return false;
@@ -571,19 +640,31 @@ __device__ __forceinline__ bool ch_softmax(ChShared& sh, const ChunkArgs& A, con
             const float to = fmaxf(l != 0.f ? m : -INFINITY, x.y != 0.f ? x.x : -INFINITY);
             w0 = l != 0.f ? ex2(m - to) : 0.f;                 // one that saw nothing has weight 0
             w1 = x.y != 0.f ? ex2(x.x - to) : 0.f;
-            l = (l != 0.f ? w0 * l : 0.f) + (x.y != 0.f ? w1 * x.y : 0.f);
+            const float c1 = FP8 ? (float)sh.share_c[row] : 0.f;
+            if (FP8 && __any_sync(0xffffffffu, c != 0.f || c1 != 0.f)) {
+                const ChUnit u{m, c}, u1{x.x, c1};
+                const bool above = l == 0.f || (x.y != 0.f && u1.above(u));
+                const ChUnit sum = ChUnit{above ? u1.m : u.m, above ? u1.c : u.c}.with(to);
+                l = (l != 0.f ? u.in(sum) * l : 0.f) + (x.y != 0.f ? u1.in(sum) * x.y : 0.f);
+                c = l != 0.f ? sum.c : 0.f;
+            } else {
+                l = (l != 0.f ? w0 * l : 0.f) + (x.y != 0.f ? w1 * x.y : 0.f);
+            }
             m = to;
             if (I.part < 0) {
-                const float inv = l != 0.f ? 1.f / l : 0.f;
+                lse = l == 0.f ? -INFINITY : m - c + log2f(l) - CH_BIAS;
+                const float inv = inverse();
                 w0 *= inv;
                 w1 *= inv;
+                if (FP8) sh.share_c[row] = (int16_t)c;
             }
             sh.share[row] = make_float2(w0, w1);
             warp_arrive(sh.weights_there);
         }
         ++shares;
     } else if (I.part < 0) {
-        const float inv = l != 0.f ? 1.f / l : 0.f;
+        lse = l == 0.f ? -INFINITY : m - c + log2f(l) - CH_BIAS;
+        const float inv = inverse();
         w0 *= inv;
         w1 *= inv;
     }
@@ -592,6 +673,8 @@ __device__ __forceinline__ bool ch_softmax(ChShared& sh, const ChunkArgs& A, con
     const bool some = both || n_tiles > 0;
     const int64_t at = I.part >= 0 ? (int64_t)I.part * A.tiles + tile : 0, out = (I.row + tok) * A.hq + I.g * A.r + head;
     const uint32_t O0 = sh.tmem + 256 + lanes, O1 = O0 + D;
+    const float rest = FP8 && I.part < 0 ? ex2(c) : 1.f;
+    const uint64_t rest2 = pack2(rest, rest);
     if (any)
 #pragma unroll 1
         for (int x = col0; x < col0 + cols; x += 32) {
@@ -611,6 +694,14 @@ __device__ __forceinline__ bool ch_softmax(ChShared& sh, const ChunkArgs& A, con
                     for (int i = 0; i < 32; ++i)
                         if (w1 != 0.f) o[i] = __float_as_uint(fmaf(w1, __uint_as_float(o1[i]), __uint_as_float(o[i])));
                 }
+                if (FP8)
+#pragma unroll
+                    for (int i = 0; i < 32; i += 2) {
+                        float y, z;
+                        unpack2(mul2(pack2(__uint_as_float(o[i]), __uint_as_float(o[i + 1])), rest2), y, z);
+                        o[i] = __float_as_uint(y);
+                        o[i + 1] = __float_as_uint(z);
+                    }
             } else {
 #pragma unroll
                 for (int i = 0; i < 32; ++i) o[i] = 0u;
@@ -646,8 +737,12 @@ __device__ __forceinline__ bool ch_softmax(ChShared& sh, const ChunkArgs& A, con
         warp_arrive(sh.o_read);
     }
     if (real && (!both || t == 0)) {
-        if (I.part >= 0) A.part_ml[at * CH_ROWS + row] = make_float2(m, l);
-        else if (A.lse) A.lse[out] = l == 0.f ? -INFINITY : (m + log2f(l) - CH_BIAS) * 0.6931471805599453f;
+        if (I.part >= 0) {
+            if constexpr (FP8) reinterpret_cast<float4*>(A.part_ml)[at * CH_ROWS + row] = make_float4(m, l, c, 0.f);
+            else reinterpret_cast<float2*>(A.part_ml)[at * CH_ROWS + row] = make_float2(m, l);
+        } else if (A.lse) {
+            A.lse[out] = lse * 0.6931471805599453f;
+        }
     }
     return true;
 }
@@ -851,7 +946,8 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
                     ++k;
                     int page = 0, page_next = page_of(I, 0);
                     bool bad = false;
-                    float ks = 0.f, vs = 0.f;
+                    float ks = 0.f, vs = 0.f, v_log = 0.f, v_share = 0.f, v_first = 0.f;
+                    uint32_t far = 0;
                     for (int j = 0; ok && j < I.tiles; ++j, ++tiles) {
                         if ((j & 3) == 0) {
                             page = page_next;
@@ -872,17 +968,8 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
                             ok = event_wait(1, __shfl_sync(0xffffffffu, e1, st)) && ok;
                             if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
                         }
-                        // Before the keys are asked for: their scores are there only after this.
-                        if constexpr (FP8)
-                            if (lane >> 3 == (j & 3)) {
-                                sh.k_scale[sc][lane & 7] = ks;
-                                sh.v_log[sc][lane & 7] = log2f(vs);
-                            }
-                        if (lane == 0) {
-                            sh.bad[sc] = bads;
-                            mbar_expect_tx(smem_u32(&sh.k_full[st]), P::TILE);
-                        }
-                        warp_arrive(sh.sc_full[sc]);
+                        if (lane == 0) mbar_expect_tx(smem_u32(&sh.k_full[st]), P::TILE);
+                        __syncwarp();
                         load_tile(&map_k, I, page, j, K0 + st * P::TILE, smem_u32(&sh.k_full[st]), 2 * tiles);
                         if (lane == st) {
                             const int i = I.dual ? j >> 1 : j;
@@ -904,6 +991,24 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
                                 }
                                 q_issued[t] += ok;
                             }
+                        // What the softmax has to know of the tile, while its keys are on their way.
+                        if constexpr (FP8) {
+                            if ((j & 3) == 0) {
+                                const uint32_t there = __ballot_sync(0xffffffffu, page >= 0);
+                                v_log = vs == 0.f ? CH_NO_SCALE : log2f(vs);
+                                if (j == 0) v_first = there ? rintf(__shfl_sync(0xffffffffu, v_log, __ffs((int)there) - 1)) : 0.f;
+                                if (page < 0) v_log = v_first;          // (nothing is seen there)
+                                far |= __any_sync(0xffffffffu, !(fabsf(v_log - v_first) <= CH_SPREAD)) ? CH_FAR : 0u;
+                                v_share = far ? 0.f : exp2f(v_first - v_log);
+                            }
+                            if (lane >> 3 == (j & 3)) {
+                                sh.k_scale[sc][lane & 7] = ks;
+                                sh.v_log[sc][lane & 7] = v_log;
+                                sh.v_share[sc][lane & 7] = v_share;
+                            }
+                        }
+                        if (lane == 0) sh.bad[sc] = make_uint2(bads | far, __float_as_uint(v_first));
+                        warp_arrive(sh.sc_full[sc]);
                         if constexpr (FP8) {
                             const int sv = tiles % P::VS;
                             if (ok && tiles >= P::VS) ok = ch_wait(sh, A, sh.raw_free[sv], tiles / P::VS - 1);
@@ -1194,7 +1299,7 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
 
 // ------------------------------------------------------------------ the join
 // Rows of an item that range borders cut: CTA (c, t, x) joins 32 columns x of tile t of the item that begins in range c.
-template <int D>
+template <int D, bool FP8>
 __global__ void __launch_bounds__(CH_ROWS) paged_chunk_join_kernel(const __grid_constant__ ChunkArgs A) {
     __shared__ int slots[CH_CTAS + 1], count;
     grid_wait();
@@ -1219,10 +1324,19 @@ __global__ void __launch_bounds__(CH_ROWS) paged_chunk_join_kernel(const __grid_
     if (!real) return;
     const int n = count;
     float m = -INFINITY, l = 0.f;
-#pragma unroll 8
+    auto part = [&](int i) {       // m, l, c
+        const int64_t at = ((int64_t)slots[i] * A.tiles + t) * CH_ROWS + row;
+        if (FP8) return reinterpret_cast<const float4*>(A.part_ml)[at];
+        const float2 ml = reinterpret_cast<const float2*>(A.part_ml)[at];
+        return make_float4(ml.x, ml.y, 0.f, 0.f);
+    };
+    float cl = 0.f;                // l counts in units of 2^(m - cl)
+    bool units = false;
+#pragma unroll (FP8 ? 4 : 8)
     for (int i = 0; i < n; ++i) {
-        const float2 ml = A.part_ml[((int64_t)slots[i] * A.tiles + t) * CH_ROWS + row];
+        const float4 ml = part(i);
         if (ml.y != 0.f) m = fmaxf(m, ml.x);
+        units |= ml.z != 0.f;
     }
     float4 acc[8];
 #pragma unroll
@@ -1230,7 +1344,7 @@ __global__ void __launch_bounds__(CH_ROWS) paged_chunk_join_kernel(const __grid_
 #pragma unroll 2
     for (int i = 0; i < n; ++i) {
         const int64_t at = (int64_t)slots[i] * A.tiles + t;
-        const float2 ml = A.part_ml[at * CH_ROWS + row];
+        const float4 ml = part(i);
         if (ml.y == 0.f) continue;             // it saw nothing: its memory may hold anything
         const float4* from = reinterpret_cast<const float4*>(A.part_o) + (at * (D / 4) + blockIdx.z * 8) * CH_ROWS + row;
         const float f = ex2(ml.x - m);
@@ -1244,7 +1358,34 @@ __global__ void __launch_bounds__(CH_ROWS) paged_chunk_join_kernel(const __grid_
             acc[e].w += f * o.w;
         }
     }
-    const float inv = l != 0.f ? 1.f / l : 0.f;
+    if (FP8 && units) {            // parts whose l counts in units of their own
+        ChUnit unit{-INFINITY, 0.f};
+#pragma unroll 1
+        for (int i = 0; i < n; ++i) {
+            const float4 ml = part(i);
+            if (ml.y != 0.f && (unit.m == -INFINITY || ChUnit{ml.x, ml.z}.above(unit))) unit = {ml.x, ml.z};
+        }
+        unit = unit.with(m);
+        l = 0.f;
+#pragma unroll 1
+        for (int i = 0; i < n; ++i) {
+            const float4 ml = part(i);
+            if (ml.y != 0.f) l += ChUnit{ml.x, ml.z}.in(unit) * ml.y;
+        }
+        cl = l != 0.f ? unit.c : 0.f;
+    }
+    float inv = l != 0.f ? 1.f / l : 0.f;
+    if (FP8 && units) {            // (neither 2^c nor 2^c / l need be in fp32's range)
+        const float half = truncf(0.5f * cl), a = ex2(half), b = ex2(cl - half);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            acc[e].x = acc[e].x * inv * a * b;
+            acc[e].y = acc[e].y * inv * a * b;
+            acc[e].z = acc[e].z * inv * a * b;
+            acc[e].w = acc[e].w * inv * a * b;
+        }
+        inv = 1.f;
+    }
     const int64_t out = (cut.row + tok) * A.hq + cut.g * A.r + head;
     uint4* to = reinterpret_cast<uint4*>(A.o + out * D + blockIdx.z * 32);
 #pragma unroll
@@ -1254,7 +1395,7 @@ __global__ void __launch_bounds__(CH_ROWS) paged_chunk_join_kernel(const __grid_
         to[e / 2] = make_uint4(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b), *reinterpret_cast<const uint32_t*>(&g),
                                *reinterpret_cast<const uint32_t*>(&d));
     }
-    if (blockIdx.z == 0 && A.lse) A.lse[out] = l == 0.f ? -INFINITY : (m + log2f(l) - A.bias) * 0.6931471805599453f;
+    if (blockIdx.z == 0 && A.lse) A.lse[out] = l == 0.f ? -INFINITY : (m - cl + log2f(l) - A.bias) * 0.6931471805599453f;
 }
 
 // ------------------------------------------------------------------ host
@@ -1264,7 +1405,7 @@ struct ChunkSpace {
 };
 ChunkSpace chunk_space(int tiles, int d, bool fp8, int64_t q_rows) {
     const size_t rows = (size_t)CH_CTAS * 2 * tiles * CH_ROWS;
-    return {round256(CH_CTAS * sizeof(ChunkCut)), round256(rows * sizeof(float2)), rows * d * sizeof(float), fp8 ? round256((size_t)q_rows) : 0,
+    return {round256(CH_CTAS * sizeof(ChunkCut)), round256(rows * (fp8 ? sizeof(float4) : sizeof(float2))), rows * d * sizeof(float), fp8 ? round256((size_t)q_rows) : 0,
             fp8 ? 2 * (size_t)q_rows * d : 0};
 }
 // Few rows to a request: bound by the bytes of K and V, and products of 128 rows would be mostly empty.
@@ -1293,7 +1434,7 @@ cudaError_t paged_chunk_launch(const CUtensorMap& mq, const CUtensorMap& mk, con
     }
     const cudaError_t e = launch_dependent(paged_chunk_kernel<D, FP8>, dim3(CH_CTAS), P::THREADS, SMEM, s, 0, mq, mk, mv, A);
     if (e != cudaSuccess) return e;
-    return launch_dependent(paged_chunk_join_kernel<D>, dim3(CH_CTAS, A.tiles, D / 32), CH_ROWS, 0, s, 0, A);
+    return launch_dependent(paged_chunk_join_kernel<D, FP8>, dim3(CH_CTAS, A.tiles, D / 32), CH_ROWS, 0, s, 0, A);
 }
 
 }  // namespace kvo
@@ -1365,7 +1506,7 @@ extern "C" kvo_status kvo_paged_chunk_attn(const kvo_paged_cache* cache, const v
     A.lse = lse;
     A.status = status;
     A.cut = (ChunkCut*)workspace;
-    A.part_ml = (float2*)((uint8_t*)workspace + sp.cut);
+    A.part_ml = (uint8_t*)workspace + sp.cut;
     A.part_o = (float*)((uint8_t*)workspace + sp.cut + sp.ml);
     int8_t* const q_exp = (int8_t*)A.part_o + sp.o;
     uint8_t* const q8 = (uint8_t*)q_exp + sp.q_exp;
