@@ -632,7 +632,8 @@ kvo_status kvo_paged_attn_workspace(const kvo_paged_cache* cache, int n_q_heads,
  *   taken as the sum of two e4m3 values times a power of two: exact where a value is
  *   at least 2^-9 of its row's largest, to 2^-17
  *   of that one else.  v_scale may have any finite size, 0 among them, and pages any
- *   scales next to each other (up to 16 rows: as kvo_paged_attn).  A row that sees no token gets o = 0, lse = -inf; rows
+ *   scales next to each other (up to 16 rows: as kvo_paged_attn).  Scores may be as large
+ *   as fp32 holds (times log2(e)).  A row that sees no token gets o = 0, lse = -inf; rows
  *   outside every request keep their bytes.  What lies in a page behind the last
  *   token is never used, NaN included; among the new tokens of a request a NaN or an
  *   infinity in v may reach tokens before it in the same 128 keys.  Two calls give

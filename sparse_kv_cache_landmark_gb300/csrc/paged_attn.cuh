@@ -133,6 +133,13 @@ __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
     const __half2 v = __floats2half2_rn(lo, hi);
     return *reinterpret_cast<const uint32_t*>(&v);
 }
+// The same for weights, no larger than f16's largest value: where fp32's steps are 8 or more (scores from 2^26 on) the roundings of
+// the rise that is let pass and of the bias may make one 2^16.
+__device__ __forceinline__ uint32_t pack_weights_f16(float lo, float hi) {
+    uint32_t r;
+    asm("cvt.rn.satfinite.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
 __device__ __forceinline__ uint32_t pack_bf(float lo, float hi) {
     const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
     return *reinterpret_cast<const uint32_t*>(&v);
@@ -276,7 +283,7 @@ __device__ __forceinline__ void pa_tile(PaState<D, FP8, NH>& T, const uint32_t (
             }
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
-                const uint32_t v = FP8 ? pack_f16(p[2 * i] * fold[u], p[2 * i + 1] * fold[u]) : pack_bf(p[2 * i], p[2 * i + 1]);
+                const uint32_t v = FP8 ? pack_weights_f16(p[2 * i] * fold[u], p[2 * i + 1] * fold[u]) : pack_bf(p[2 * i], p[2 * i + 1]);
                 if (!FP8) {
                     // o is divided by the sum of the weights as the product takes them: a bf16 rounding (2^-8)
                     // shared by numerator and denominator cancels where few tokens carry the weight

@@ -59,6 +59,7 @@ constexpr int CH_ROWS = 128;               // query rows of a tile
 constexpr int CH_KEYS = 128;               // keys of a tile
 constexpr int CH_BLOCK = CH_ROWS * 128;    // bytes of 128 rows of 128
 constexpr float CH_RAISE = 8.f;            // log2: how far a score may pass the running maximum
+constexpr float CH_BIG = 0x1p20f;          // from here on scores are taken less the maximum before anything is added to them
 constexpr int CH_CTAS = 152;               // ranges at most: one CTA to an SM
 constexpr int CH_EVENTS = 16;              // barriers that a tile's products complete in turn
 constexpr int CH_ITEMS = 4;                // descriptors
@@ -406,6 +407,62 @@ struct ChUnit {
     __device__ __forceinline__ ChUnit with(float to) const { return {to, floorf(to - m + c)}; }            // the next above with this m
 };
 
+__device__ __forceinline__ bool ch_big(float m) { return fabsf(m) >= CH_BIG && fabsf(m) < INFINITY; }
+// A key's factor from product to score.  (A masked score times zero would be NaN.)
+template <bool FP8>
+__device__ __forceinline__ float ch_scale(float q_scale, float k_scale) { return FP8 ? fmaxf(k_scale * q_scale, 1.2e-38f) : q_scale; }
+// What few tiles of scores need, before their weights.  l and c before the tile, and by how much m has risen; returns l with the
+// tile's share, and c, where scales are far apart.  For d 128 a function of its own, as the others' code has to fit
+// the instruction caches (8192 tokens in e4m3 478 us, 499 with it inside); for d 64 it is faster inside (417 us against 470).
+template <bool FP8>
+__device__ __forceinline__ float2 ch_rare_tile(const ChShared& sh, uint32_t S, uint32_t slot, float q_scale, bool far_scales, float m, float l, float rise, float c) {
+    constexpr float CH_BIAS = FP8 ? 6.f : 0.f;
+    // Large scores: m is the maximum of rounded ones, and m's rounding alone would take exp2(x scale - m) out of its range.
+    // They become what, times the scale, is each one's distance from m.
+    const bool big = ch_big(m);
+    const float b = m == -INFINITY ? 0.f : CH_BIAS - (big ? 0.f : m);
+    // Scales far apart: a weight times 2^c / v_scale may pass fp32's range, or the weight be 0 where its share of l is not.
+    // There shares are exponentials of their own, and c follows down to the page that leads among them.  What leads m may be a
+    // larger scale alone, and what came before still be most of l: l does not shrink as m rises, but c does rise; and an l that
+    // has become small is counted in a smaller unit, so that c is no lower than it has to be.
+    if (far_scales) {
+        const float whole = floorf(rise);
+        const int up = l != 0.f && l < 0x1p-32f ? 127 - (int)(__float_as_uint(l) >> 23) : 0;
+        c = l == 0.f ? CH_TOP_C : c + whole + (float)up;
+        l = l * ex2(whole - rise) * __uint_as_float((uint32_t)(up + 127) << 23);
+    }
+#pragma unroll 1
+    for (int g = 0; g < 16; ++g) {
+        uint32_t x[8];
+        tmem_ld8(S + 8 * g, x);
+        tmem_wait_ld();
+        const float v = FP8 ? sh.v_log[slot][g / 2] : 0.f, scale = ch_scale<FP8>(q_scale, sh.k_scale[slot][g / 2]);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            const float y = __uint_as_float(x[e]), z = FP8 ? fmaf(y, scale, v) : __fmul_rn(y, scale);
+            x[e] = __float_as_uint(big ? __fdividef(__fsub_rn(z, m) - v, scale) : y);
+        }
+        tmem_st8(S + 8 * g, x);
+        if (FP8 && far_scales) {
+            float y[8], first = -INFINITY;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) first = fmaxf(first, y[e] = fmaf(__uint_as_float(x[e]), scale, b + v));
+            const bool seen = first != -INFINITY;
+            const float low = seen ? fminf(c, floorf(v + CH_BIAS - first)) : c, by = seen ? low - v : -INFINITY;
+            l *= ex2(low - c);
+            c = low;               // no share is above 2^6
+#pragma unroll
+            for (int e = 0; e < 8; ++e) l += ex2(y[e] + by);
+        }
+    }
+    tmem_wait_st();
+    return make_float2(l, c);
+}
+template <bool FP8>
+__device__ __noinline__ float2 ch_rare_call(const ChShared& sh, uint32_t S, uint32_t slot, float q_scale, bool far_scales, float m, float l, float rise, float c) {
+    return ch_rare_tile<FP8>(sh, S, slot, q_scale, far_scales, m, l, rise, c);
+}
+
 // The softmax of one tile of an item: a thread owns a row; it sees its request's keys [0, limit).  False: a wait gave up.
 template <int D, bool FP8>
 __device__ __forceinline__ bool ch_softmax(ChShared& sh, const ChunkArgs& A, const ChunkItem& I, int t, uint32_t events, uint32_t keys, uint32_t& shares) {
@@ -422,6 +479,7 @@ __device__ __forceinline__ bool ch_softmax(ChShared& sh, const ChunkArgs& A, con
     // they are rounded to f16, whose smallest step is 2^-24.  l is in units of 2^(m - c) (times 2^6); c is 0 next to bf16.
     constexpr float CH_BIAS = FP8 ? 6.f : 0.f;
     float m = -INFINITY, l = 0.f, c = 0.f;
+    float pass = -INFINITY, b = 0.f;                                    // a score beyond this raises m; what is added to a score
     float q_scale = A.scale_log2;
     int q_exp = 0;
     if (FP8 && real) q_exp = A.q_exp[(I.row + tok) * A.hq + I.g * A.r + head];
@@ -445,9 +503,7 @@ __device__ __forceinline__ bool ch_softmax(ChShared& sh, const ChunkArgs& A, con
         const bool far_scales = FP8 && bads.x >= CH_FAR;
         const int rem = min(limit - j * CH_KEYS, CH_KEYS);
         const bool edge = bad || __any_sync(0xffffffffu, rem < CH_KEYS);
-        auto scale_of = [&](float k_scale) {   // (a masked score times zero would be NaN)
-            return FP8 ? fmaxf(k_scale * q_scale, 1.2e-38f) : q_scale;
-        };
+        auto scale_of = [&](float k_scale) { return ch_scale<FP8>(q_scale, k_scale); };
         auto top_of = [](const uint32_t* x) {
             float u = fmaxf(__uint_as_float(x[0]), __uint_as_float(x[1])), v = fmaxf(__uint_as_float(x[2]), __uint_as_float(x[3]));
 #pragma unroll
@@ -512,12 +568,14 @@ __device__ __forceinline__ bool ch_softmax(ChShared& sh, const ChunkArgs& A, con
             }
         }
         if (!FP8) top *= q_scale;
-        if (far_scales || __any_sync(0xffffffffu, real && top > m + CH_RAISE)) {
+        if (far_scales || __any_sync(0xffffffffu, real && top > pass)) {
             const float to = fmaxf(m, top);
             const float f = m == -INFINITY ? 0.f : ex2(m - to);
             const float l_before = l, was = m;
             l *= f;
             m = to;
+            pass = fabsf(m) < CH_BIG ? m + CH_RAISE : -INFINITY;
+            b = fabsf(m) < CH_BIG ? CH_BIAS - m : m == -INFINITY ? 0.f : CH_BIAS;
             if (i > 0) {           // these scores are complete: so is the value product that was issued before them
 #pragma unroll 1
                 for (int x = 0; x < D; x += 32) {
@@ -529,38 +587,19 @@ __device__ __forceinline__ bool ch_softmax(ChShared& sh, const ChunkArgs& A, con
                     tmem_st32(O + x, o);
                 }
             }
-            // Scales far apart: a weight times 2^c / v_scale may pass fp32's range, or the weight be 0 where its share of l is not.
-            // There shares are exponentials of their own (8 keys at a time: little code), and c follows down to the page that
-            // leads among them.
-            if (far_scales) {
-                // What leads m may be a larger scale alone, and what came before still be most of l: l stays, but that one that
-                // has become small is counted in a smaller unit, so that c is no lower than it has to be.
-                const float rise = l_before == 0.f ? 0.f : to - was, whole = floorf(rise);
-                const int up = l_before != 0.f && l_before < 0x1p-32f ? 127 - (int)(__float_as_uint(l_before) >> 23) : 0;
-                l = l_before * ex2(whole - rise) * __uint_as_float((uint32_t)(up + 127) << 23);
-                c = l_before == 0.f ? CH_TOP_C : c + whole + (float)up;
-                const float b = m == -INFINITY ? 0.f : CH_BIAS - m;
-#pragma unroll 1
-                for (int g = 0; g < 16; ++g) {
-                    tmem_ld8(S + 8 * g, x);
-                    tmem_wait_ld();
-                    const float v = sh.v_log[slot][g / 2], scale = scale_of(sh.k_scale[slot][g / 2]);
-                    float y[8], first = -INFINITY;
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) first = fmaxf(first, y[e] = fmaf(__uint_as_float(x[e]), scale, b + v));
-                    const bool seen = first != -INFINITY;
-                    const float low = seen ? fminf(c, floorf(v + CH_BIAS - first)) : c, by = seen ? low - v : -INFINITY;
-                    l *= ex2(low - c);
-                    c = low;                                            // no share is above 2^6
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) l += ex2(y[e] + by);
+            if (far_scales || __any_sync(0xffffffffu, real && ch_big(m))) {
+                const float rise = l_before == 0.f ? 0.f : to - was;
+                const float2 lc = D == 64 ? ch_rare_tile<FP8>(sh, S, slot, q_scale, far_scales, m, l_before, rise, c)
+                                          : ch_rare_call<FP8>(sh, S, slot, q_scale, far_scales, m, l_before, rise, c);
+                if (far_scales) {
+                    l = lc.x;
+                    c = lc.y;
                 }
                 tmem_ld32(S, x);
                 tmem_ld32(S + 32, x + 32);
                 tmem_wait_ld();
             }
         }
-        const float b = m == -INFINITY ? 0.f : CH_BIAS - m;
         uint64_t sum[2] = {0ull, 0ull};
         float total = 0.f;
 #pragma unroll 1

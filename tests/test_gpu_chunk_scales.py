@@ -40,7 +40,8 @@ def check(c, o, lse, rows, heads, unit=1.0):
                 want, wl, tol, tl = ref.attention(q, k, v, 2 * ref.BF16)
                 s = k @ q / math.sqrt(c.d)
                 w = torch.softmax(s, 0)
-                scale = c.scales[1][c.table[b, :need].long(), g].double().cpu().repeat_interleave(c.page)[:see]
+                scale = c.scales[1][c.table[b, :need].long(), g].double().cpu() if c.e4m3 else torch.ones(need, dtype=torch.float64)
+                scale = scale.repeat_interleave(c.page)[:see]
                 log = torch.log2(scale.clamp(min=2.0 ** -160))
                 # q as two e4m3 values, each within 2^-17 of the row's largest; the scores' logarithms with v_scale's in them,
                 # in fp32: the product, the maximum, their difference and the sum's unit, half a step of the largest each
