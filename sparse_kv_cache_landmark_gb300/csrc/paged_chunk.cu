@@ -1448,7 +1448,7 @@ ChunkSpace chunk_space(int tiles, int d, bool fp8, int64_t q_rows) {
             fp8 ? 2 * (size_t)q_rows * d : 0};
 }
 // Few rows to a request: bound by the bytes of K and V, and products of 128 rows would be mostly empty.
-bool chunk_few(int r, int64_t max_new) { return max_new > 0 && max_new * r <= FEW_ROWS; }
+bool chunk_few(int r, int64_t max_new) { return max_new > 0 && max_new <= FEW_ROWS / r; }       // (a product may overflow)
 int chunk_tiles(int64_t total_q, int r) { return total_q <= CH_ROWS / r ? 1 : 2; }
 
 const char* chunk_error(const kvo_paged_cache* c, int n_q_heads, int64_t total_q, int64_t max_new, int64_t max_len) {
