@@ -1,4 +1,4 @@
-"""Attention of new tokens over a paged cache under bounds of any size."""
+"""Attention of new tokens over a paged cache under bounds of any size, and next to requests whose offsets are bad."""
 import pytest
 import torch
 
@@ -21,3 +21,33 @@ def test_a_bound_beyond_all_is_none(e4m3, r):
         assert torch.equal(o, want[0]) and torch.equal(lse, want[1])
     assert int(status.item()) == 0
     c.check(*want, rows=[0, 3, 17, -1], heads=[0, 2 * r - 1])
+
+
+@pytest.mark.parametrize("e4m3", [False, True])
+@pytest.mark.parametrize("bounds", [{}, dict(max_new=6), dict(max_new=6, max_len=300000)])
+@pytest.mark.parametrize("batch", [5, 40])
+@pytest.mark.parametrize("spoil", [{2: 13}, {2: 9, 3: 7}, {1: 8, 2: 10}, {1: 0}, {2: 11, 4: 19}])
+def test_neighbours_of_a_bad_offset(spoil, batch, bounds, e4m3):
+    """One offset stands between two requests: the one that is still served gets all of its rows, with its new number of tokens."""
+    c = Case(batch, 64, 1, 2, 16, e4m3, [6] * batch, [60] * batch)
+    cu = list(c.cu)
+    for i, x in spoil.items():
+        cu[i] = x
+    total, end, rows = c.cu[-1], 0, {}
+    for b in range(batch):
+        if 0 <= cu[b] <= cu[b + 1] <= total:
+            if cu[b] >= end and not (bounds and cu[b + 1] - cu[b] > 8):      # (more new tokens than 16 rows: left out)
+                rows[b] = (cu[b], cu[b + 1])
+            end = max(end, cu[b + 1])
+    assert any(rows[b] != (c.cu[b], c.cu[b + 1]) for b in rows)
+    o, lse = (torch.full(s, 3.0, dtype=t, device="cuda") for s, t in ((c.q.shape, torch.bfloat16), (c.q.shape[:2], torch.float32)))
+    status = i32([0])
+    kvo.paged_chunk_attn(c.q, c.kp, c.vp, c.table, i32(c.lens), i32(cu), k_scale=c.scales[0], v_scale=c.scales[1], o=o, lse=lse, status=status, **bounds)
+    assert int(status.item()) == (0 if len(rows) == batch else kvo.DEV_BAD_COUNT)
+    served = torch.zeros(total, dtype=torch.bool, device="cuda")
+    for a, e in rows.values():
+        served[a:e] = True
+    assert (o[~served] == 3.0).all() and (lse[~served] == 3.0).all()
+    assert (o[served] != 3.0).any(-1).all()
+    c.new, c.cu = [rows[b][1] - rows[b][0] if b in rows else 0 for b in range(batch)], [rows[b][0] if b in rows else 0 for b in range(batch)]
+    c.check(o, lse, requests=sorted(rows)[:6] + sorted(rows)[-2:])
