@@ -734,8 +734,8 @@ kvo_status kvo_paged_reserve(const kvo_page_book* book, const int32_t* want, int
  *   before and after; one call at a time may use it.
  *   Status bits: KVO_DEV_NO_PAGES (no free page for some copy: the request holds its
  *   whole pages only), KVO_DEV_BAD_COUNT (parent outside -1..batch - 1, keep < 0 or
- *   beyond what the parent holds: the request stays as it is; held out of range is
- *   clamped), KVO_DEV_BAD_BLOCK_ID (a page id out of range in a row: not counted).
+ *   beyond what the parent holds: the request stays as it is; held out of range, a
+ *   parent's too: clamped), KVO_DEV_BAD_BLOCK_ID (a page id out of range in a row: not counted).
  *   batch 0 sets *count to 0.  Errors: KVO_ERR_INVALID, KVO_ERR_CUDA.
  */
 kvo_status kvo_paged_fork(const kvo_page_book* book, const int32_t* parent, const int32_t* keep, int32_t* src, int32_t* dst,

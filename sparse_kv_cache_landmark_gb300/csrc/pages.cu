@@ -282,20 +282,19 @@ struct ForkArgs {
 __device__ __forceinline__ void fork_gather(const ForkArgs& A, int b, int t) {
     constexpr int AT_ONCE = 4;
     const Book& B = A.book;
-    int before = B.held[b], p = A.parent[b];
-    const int keep = A.keep[b];
-    bool bad = before < 0 || before > B.max_pages;
-    before = min(max(before, 0), B.max_pages);
-    int after = before, part = 0;
+    auto clamped = [&](int held) { return min(max(held, 0), B.max_pages); };
+    const int held = B.held[b], before = clamped(held), keep = A.keep[b];
+    int p = A.parent[b], after = before, part = 0;
+    bool bad = false;
     if (p < -1 || p >= B.batch) bad = true;
     else if (p < 0) after = 0;
     else {
-        const int pages = (int)(((unsigned)max(keep, 0) + B.page - 1) / B.page), most = p == b ? before : B.held[p];
-        if (keep < 0 || pages > most || most > B.max_pages) bad = true;
+        const int pages = (int)(((unsigned)max(keep, 0) + B.page - 1) / B.page), most = p == b ? before : clamped(B.held[p]);
+        if (keep < 0 || pages > most) bad = true;
         else { after = pages; part = keep % B.page; }
     }
     if (bad) { p = b; after = before; part = 0; }             // stays as it is
-    if (bad && t == 0) pg_report(B, KVO_DEV_BAD_COUNT);
+    if ((bad || held != before) && t == 0) pg_report(B, KVO_DEV_BAD_COUNT);
     const int32_t* old = B.table + (int64_t)b * B.max_pages;
     const int32_t* from = B.table + (int64_t)max(p, 0) * B.max_pages;
     int32_t* to = A.rows + (int64_t)b * B.max_pages;
