@@ -690,7 +690,7 @@ typedef struct {
     int32_t* table;        /* [batch][max_pages]: the page ids of each request, as kvo_paged_cache reads them */
     int32_t* held;         /* [batch]: how many entries of its row a request has; those behind are not looked at */
     int32_t* refs;         /* [n_pages]: how often the page is named; 0: free.  16-byte aligned */
-    int32_t batch, max_pages, n_pages;      /* batch <= 8192 */
+    int32_t batch, max_pages, n_pages;      /* batch <= 8192; max_pages, n_pages <= 2^30 */
     int32_t page_size;     /* tokens of a page */
 } kvo_page_book;
 

@@ -632,6 +632,7 @@ const char* book_error(const kvo_page_book* b) {
     if (b->batch < 0 || b->batch > PG_BATCH) return "batch must be in 0..8192";
     if (b->n_pages < 1 || b->max_pages < 1) return "need n_pages >= 1 and max_pages >= 1";
     if (b->page_size < 1 || (int64_t)b->max_pages * b->page_size > INT32_MAX) return "need page_size >= 1 and max_pages * page_size below 2^31";
+    if (b->n_pages > 1 << 30 || b->max_pages > 1 << 30) return "n_pages and max_pages must be at most 2^30";      // (kernels step past them)
     if ((int64_t)b->batch * b->max_pages > INT32_MAX) return "batch * max_pages must fit in 31 bits";
     if (!b->refs || (b->batch > 0 && (!b->table || !b->held))) return "null table, held or refs";
     if ((uintptr_t)b->refs % 16) return "refs must be 16-byte aligned";
@@ -653,7 +654,7 @@ bool any_meet(std::initializer_list<Bytes> some, std::initializer_list<Bytes> ot
     return false;
 }
 size_t up256(size_t x) { return (x + 255) / 256 * 256; }
-// CTAs of the cluster that looks at refs: one where it can hold a page of each in a word, without barriers of clusters.
+// CTAs of the cluster that looks at refs: one for pools of up to 4 groups of 32 pages to a warp, without barriers of clusters.
 int pages_cluster(int n_pages) { return n_pages <= 4 * PG_THREADS ? 1 : PG_CLUSTER; }
 
 size_t fork_workspace(const kvo_page_book* b) {
