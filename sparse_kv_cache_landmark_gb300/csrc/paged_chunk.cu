@@ -648,7 +648,8 @@ __device__ __forceinline__ bool ch_softmax(ChShared& sh, const ChunkArgs& A, con
         if (group_any(1 + t, !ok)) return false;
         tc_fence_after();
     }
-    // A dual item's halves: this thread writes half of the row's values, from both.
+    // A dual item's halves: this thread writes half of the row's values, from both.  (The fences about the exchange order the other
+    // half's products, which its threads have waited for, before this one's loads of them.)
     const bool both = I.dual && I.n1 > 0;
     float w0 = t == 0 ? 1.f : 0.f, w1 = 1.f - w0;              // weights of the tiles' sums
     float lse = 0.f;               // log2
@@ -665,9 +666,11 @@ __device__ __forceinline__ bool ch_softmax(ChShared& sh, const ChunkArgs& A, con
         if (t == 1) {
             sh.share[row] = make_float2(m, l);
             if (FP8) sh.share_c[row] = (int16_t)c;
+            tc_fence_before();
             warp_arrive(sh.ml_there);
             if ((threadIdx.x & 96) == 0) ok = ch_wait(sh, A, sh.weights_there, shares);
             if (group_any(2, !ok)) return false;
+            tc_fence_after();
             const float2 x = sh.share[row];
             w0 = x.x;
             w1 = x.y;
@@ -675,6 +678,7 @@ __device__ __forceinline__ bool ch_softmax(ChShared& sh, const ChunkArgs& A, con
         } else {
             if ((threadIdx.x & 96) == 0) ok = ch_wait(sh, A, sh.ml_there, shares);
             if (group_any(1, !ok)) return false;
+            tc_fence_after();
             const float2 x = sh.share[row];
             const float to = fmaxf(l != 0.f ? m : -INFINITY, x.y != 0.f ? x.x : -INFINITY);
             w0 = l != 0.f ? ex2(m - to) : 0.f;                 // one that saw nothing has weight 0
@@ -698,6 +702,7 @@ __device__ __forceinline__ bool ch_softmax(ChShared& sh, const ChunkArgs& A, con
                 if (FP8) sh.share_c[row] = (int16_t)c;
             }
             sh.share[row] = make_float2(w0, w1);
+            tc_fence_before();
             warp_arrive(sh.weights_there);
         }
         ++shares;
