@@ -575,7 +575,7 @@ __device__ __forceinline__ bool ch_softmax(ChShared& sh, const ChunkArgs& A, con
             l *= f;
             m = to;
             pass = fabsf(m) < CH_BIG ? m + CH_RAISE : -INFINITY;
-            b = fabsf(m) < CH_BIG ? CH_BIAS - m : m == -INFINITY ? 0.f : CH_BIAS;
+            b = fabsf(m) < CH_BIG ? CH_BIAS - m : m == -INFINITY ? 0.f : m == INFINITY ? __uint_as_float(0x7FC00000u) : CH_BIAS;
             if (i > 0) {           // these scores are complete: so is the value product that was issued before them
 #pragma unroll 1
                 for (int x = 0; x < D; x += 32) {

@@ -147,3 +147,50 @@ def test_scores_one_step_apart_for_few_rows(a, less, e4m3, decode):
         o, lse = kvo.paged_chunk_attn(q, kp, vp, table, lens, i32(list(range(b + 1))), k_scale=one, v_scale=one, max_new=1)
     assert o.isfinite().all() and (o.double().cpu().abs() <= v.double().abs().max() * (1 + 2.0 ** -7)).all()
     assert ((lse - 2.0 ** a - 14 * 2.0 ** (a - less)).abs() <= 2.0 ** (a - 21) + 9).all()
+
+
+@pytest.mark.parametrize("few", [False, True])
+@pytest.mark.parametrize("e4m3", [False, True])
+@pytest.mark.parametrize("bad", [math.inf, math.nan, "overflow"])
+def test_scores_that_are_not_finite(bad, e4m3, few):
+    """Rows that see such a score are NaN, o and lse; rows before that key are as they were."""
+    if e4m3 and bad == math.inf:
+        pytest.skip("e4m3 has no infinity")
+    new, lens = ([4, 2], [300, 40]) if few else ([40, 6], [300, 40])
+    kw = dict(max_new=4 if few else 0)
+    for at in (lens[0] - 2, 0, 130):               # the last token but one, the first, and one in the middle
+        c = Case(5, 64, 1, 4, 16, e4m3, new, lens)
+        c.q[..., 3] = c.q[..., 3].abs() + 1.0
+        want = c.call(**kw)
+        page, row = int(c.table[0, at // 16]), at % 16
+        if bad == "overflow":                      # 2^30 times the other scores, and those near fp32's largest number
+            if e4m3:                               # (a scale is its whole page's: the other keys there become 0)
+                c.kp[page] = 0.0
+                c.scales[0][page] = 2.0 ** 26
+            c.kp[page, 0, row, 3] = 448.0 if e4m3 else 3e38
+            c.q[..., 3] *= 2.0 ** 100
+            want = None
+        else:
+            c.kp.view(torch.uint8 if e4m3 else torch.bfloat16)[page, 0, row, 3] = 0x7F if e4m3 else bad
+        o, lse = c.call(**kw)
+        first = max(at - (lens[0] - new[0]), 0)
+        if want is not None:
+            assert torch.equal(o[:first], want[0][:first]) and torch.equal(lse[:first], want[1][:first])
+            assert torch.equal(o[new[0]:], want[0][new[0]:]) and torch.equal(lse[new[0]:], want[1][new[0]:])
+        else:
+            assert o[:first].isfinite().all() and o[new[0]:].isfinite().all()
+        assert o[first:new[0]].isnan().all() and not lse[first:new[0]].isfinite().any()
+
+
+@pytest.mark.parametrize("d", [64, 128])
+def test_an_infinite_score_in_a_row_of_its_own(d):
+    """The first score that a row's maximum takes up, and the last: many requests, most in one range of the plan."""
+    n = 700
+    kp, vp = (torch.randn(40, 1, 16, d, generator=torch.Generator().manual_seed(s)).bfloat16().cuda() for s in (1, 2))
+    kp[2, 0, 6, 3] = math.inf                      # token 38 of every request
+    q = torch.randn(n * 40, 4, d, generator=torch.Generator().manual_seed(3)).bfloat16().cuda()
+    q[..., 3] = q[..., 3].abs() + 0.5
+    o, lse = kvo.paged_chunk_attn(q, kp, vp, i32([[0, 1, 2]] * n), i32([40] * n), i32([40 * b for b in range(n + 1)]))
+    o, lse = o.view(n, 40, 4, d), lse.view(n, 40, 4)
+    assert o[:, 38:].isnan().all() and not lse[:, 38:].isfinite().any()
+    assert o[:, :38].isfinite().all() and lse[:, :38].isfinite().all()
