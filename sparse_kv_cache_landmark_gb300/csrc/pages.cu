@@ -383,6 +383,8 @@ __global__ void __launch_bounds__(PG_THREADS, 1) pages_fork_kernel(const ForkArg
     } else if (cta_row >= 0) {
         for (int b = cta_row; b < B.batch; b += ctas * AT_ONCE) fork_write(A, b, tid % PG_ROW_THREADS);
         return;
+    } else {
+        __syncthreads();                      // the table of part-filled pages is laid out (above, the cluster's barrier says so)
     }
     const Deal deal = pg_deal(B, 1);          // the first CTA has the part-filled pages to do
     const unsigned mask0 = pg_count_free(B, deal, ranks);
