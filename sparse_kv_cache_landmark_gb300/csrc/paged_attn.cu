@@ -1,47 +1,4 @@
-// kvo_paged_attn: decode attention of one query token per request over a paged
-// cache (bf16, or e4m3 with a scale per page and KV head).
-//
-//   o_h = sum_t softmax_t(q_h . k_t / sqrt(d)) v_t over the tokens of the
-//   request (or of the listed blocks of its KV head), lse_h the natural log of
-//   the softmax's denominator.
-//
-// Bound by HBM: each KV head's bytes are read once for all r query heads of its
-// group.  Work: the tiles (8 KB of K and V: 32 tokens of 128 e4m3 values) of every
-// (request, KV head), laid out group after group, are cut into contiguous ranges
-// of equal cost, one per warp, so ragged batches end together; the lengths are
-// device data, so each CTA finds its warps' ranges by a prefix sum.  A warp keeps its
-// next tiles in flight in its own ring of shared-memory stages, across the borders
-// of groups, and waits for no other warp.  TMA fills the stages (128-byte-swizzled
-// boxes of 16 rows, so that key and value fragments are read without bank
-// conflicts); a page's scales follow by cp.async into the same barrier.  128 KB in
-// flight on an SM is enough: with 192 KB 16 x 64K-128K took 450 us instead of 433.
-// One pass: running maximum and sum in fp32 registers.
-//
-// Measured (e4m3, 32 query and 8 KV heads of 128): 16 x 32768 tokens 166 us (6.5 TB/s,
-// 0.95 of a measured copy), 16 x 65536-131072 433 us (6.8 TB/s, 1.0), 64 x 256-4096
-// 55 us (0.72: about 7 us until the first tile, 5 us for the join), 1 x 131072 56 us.
-//
-// Tensor cores: mma.sync m16n8k16 on transposed products, S^T = K Q^T and O^T =
-// V^T P^T: tokens and value columns are the 16 matrix rows, query heads the 8
-// columns, so r <= 8 heads fill one product where heads as rows would leave half
-// of it empty.  P^T comes out of S^T by an 8 x 8 transpose in the warp.
-// e4m3 codes are widened exactly to f16; q is scaled by a power of two per row, its
-// largest value to 2^8..2^9: what is down to 2^-25 of that is exact in f16 as well
-// (8 bits above its smallest step, 2^-24), smaller values lose low bits, and below
-// 2^-33 they are zero.  The weights exp2(s - m), held times 2^6, are rounded to f16
-// next to e4m3 values, whose sum is taken before the rounding (11 bits down to 2^-20
-// of the running maximum, steps of 2^-30 of it below), and to bf16 (8 bits) next to
-// bf16 values, which have a wider exponent than f16; there o is divided by the sum
-// of the rounded weights and lse takes the unrounded one.
-// The maximum is only raised when a score passes it by more than 2^8, so most
-// tiles have no cross-lane step but one vote.
-//
-// A group cut by range borders leaves partial (m, l, o) in the workspace, in
-// fp32, joined by a second kernel.  Small calls, where latency counts, take one
-// cluster per group instead, whose CTAs join through distributed shared memory
-// in the same launch: each CTA leaves its part of a row in the memory of the CTA
-// that joins it (one barrier; reading the others' parts takes two, and 1 us more).
-// Both join in a fixed order: results do not depend on timing.
+// kvo_paged_attn: decode attention of one query token per request over a paged cache; the kernels are in paged_attn.cuh.
 #include "paged_attn.cuh"
 
 namespace kvo {

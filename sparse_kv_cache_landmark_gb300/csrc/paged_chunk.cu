@@ -39,8 +39,6 @@
 // needs them: 8192 tokens 744 us, by a launch before 457.  The softmax unrolled over 128 keys: 1016 us, in loops 740.  One
 // warp that loads both K and V keeps K waiting behind V's buffers: in bf16 the mixed batch 251 us, with two 166; in e4m3 the
 // buffers of raw V are free early, and a second warp's code costs more: 2048 behind 30000 945 us, with one 810.
-#include <stdio.h>
-
 #include <algorithm>
 
 #include "f32x2.cuh"
@@ -59,6 +57,8 @@ constexpr int CH_ROWS = 128;               // query rows of a tile
 constexpr int CH_KEYS = 128;               // keys of a tile
 constexpr int CH_BLOCK = CH_ROWS * 128;    // bytes of 128 rows of 128
 constexpr float CH_RAISE = 8.f;            // log2: how far a score may pass the running maximum
+template <bool FP8>
+constexpr float CH_BIAS_OF = FP8 ? 6.f : 0.f;          // log2: weights are held times 2^this; in f16, whose smallest step is 2^-24
 constexpr float CH_BIG = 0x1p20f;          // from here on scores are taken less the maximum before anything is added to them
 constexpr int CH_CTAS = 152;               // ranges at most: one CTA to an SM
 constexpr int CH_EVENTS = 16;              // barriers that a tile's products complete in turn
@@ -97,8 +97,6 @@ struct ChShape<D, true> {
 };
 
 struct ChunkArgs {
-    const uint16_t* q;
-    int64_t q_stride;
     const int8_t* q_exp;           // e4m3 pages: q's pieces are its values times 2^this
     const float* k_scale;
     const float* v_scale;
@@ -116,7 +114,6 @@ struct ChunkArgs {
     int w1, w2, base;              // cost of a key for one tile of rows and for two, and of an item in itself
     int64_t least;                 // cost of a range, unless there are more than CTAs
     float scale_log2;
-    float bias;                    // log2: weights are held times 2^this
     int wide;                      // o is 32-byte aligned
     int skip;                      // the load that every CTA announces without copying it (tests; -1: none)
     long long wait_ns;
@@ -127,7 +124,7 @@ struct ChunkCut {
     int64_t row;                   // the request's first row of q
     int32_t last;                  // the range in which it ends; -1: no such item
     int32_t more;                  // whether this CTA's range begins with a part of an item that began before
-    int32_t tok0, n, g, pad;       // first token of the block, the request's tokens, KV head
+    int32_t tok0, n, g;            // first token of the block, the request's tokens, KV head
 };
 
 struct ChunkItem {
@@ -371,7 +368,6 @@ __device__ __forceinline__ ChunkCut ch_cut(const ChShared& sh, const ChunkArgs& 
     cut.tok0 = tail.i * 2 * A.tq;
     cut.n = tail.r.n;
     cut.g = tail.g;
-    cut.pad = 0;
     return cut;
 }
 
@@ -416,7 +412,7 @@ __device__ __forceinline__ float ch_scale(float q_scale, float k_scale) { return
 // the instruction caches (8192 tokens in e4m3 478 us, 499 with it inside); for d 64 it is faster inside (417 us against 470).
 template <bool FP8>
 __device__ __forceinline__ float2 ch_rare_tile(const ChShared& sh, uint32_t S, uint32_t slot, float q_scale, bool far_scales, float m, float l, float rise, float c) {
-    constexpr float CH_BIAS = FP8 ? 6.f : 0.f;
+    constexpr float CH_BIAS = CH_BIAS_OF<FP8>;
     // Large scores: m is the maximum of rounded ones, and m's rounding alone would take exp2(x scale - m) out of its range.
     // They become what, times the scale, is each one's distance from m.
     const bool big = ch_big(m);
@@ -475,9 +471,9 @@ __device__ __forceinline__ bool ch_softmax(ChShared& sh, const ChunkArgs& A, con
     const int n_tiles = I.n(t);
     // a row that is none may see anything
     const int limit = real ? (int)min(max((int64_t)tok + 1 + (I.len - I.nq), (int64_t)0), (int64_t)I.len) - I.first * CH_KEYS : INT32_MAX;
-    // log2 units.  Next to e4m3 pages m is the maximum of the scores times their v_scale, and weights are held times 2^6:
-    // they are rounded to f16, whose smallest step is 2^-24.  l is in units of 2^(m - c) (times 2^6); c is 0 next to bf16.
-    constexpr float CH_BIAS = FP8 ? 6.f : 0.f;
+    // log2 units.  Next to e4m3 pages m is the maximum of the scores times their v_scale.  l is in units of 2^(m - c) (and of 2^-6, as the weights);
+    // c is 0 next to bf16.
+    constexpr float CH_BIAS = CH_BIAS_OF<FP8>;
     float m = -INFINITY, l = 0.f, c = 0.f;
     float pass = -INFINITY, b = 0.f;                                    // a score beyond this raises m; what is added to a score
     float q_scale = A.scale_log2;
@@ -1439,7 +1435,7 @@ __global__ void __launch_bounds__(CH_ROWS) paged_chunk_join_kernel(const __grid_
         to[e / 2] = make_uint4(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b), *reinterpret_cast<const uint32_t*>(&g),
                                *reinterpret_cast<const uint32_t*>(&d));
     }
-    if (blockIdx.z == 0 && A.lse) A.lse[out] = l == 0.f ? -INFINITY : (m - cl + log2f(l) - A.bias) * 0.6931471805599453f;
+    if (blockIdx.z == 0 && A.lse) A.lse[out] = l == 0.f ? -INFINITY : (m - cl + log2f(l) - CH_BIAS_OF<FP8>) * 0.6931471805599453f;
 }
 
 // ------------------------------------------------------------------ host
@@ -1539,8 +1535,6 @@ extern "C" kvo_status kvo_paged_chunk_attn(const kvo_paged_cache* cache, const v
         return KVO_OK;
     }
     ChunkArgs A{};
-    A.q = (const uint16_t*)q;
-    A.q_stride = q_token_stride;
     A.k_scale = fp8 ? cache->k_scale : nullptr;
     A.v_scale = fp8 ? cache->v_scale : nullptr;
     A.table = cache->table;
@@ -1573,7 +1567,6 @@ extern "C" kvo_status kvo_paged_chunk_attn(const kvo_paged_cache* cache, const v
     A.base = 2 * CH_KEYS * A.w2;
     A.least = 2 * CH_KEYS * A.w1 + A.base;
     A.scale_log2 = (float)(1.4426950408889634 / sqrt((double)D));
-    A.bias = fp8 ? 6.f : 0.f;
     A.wide = (uintptr_t)o % 32 == 0;
     A.skip = call_wait.skip;
     A.wait_ns = call_wait.limit_ns;
