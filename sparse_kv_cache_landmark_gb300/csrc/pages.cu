@@ -27,7 +27,11 @@ constexpr int PG_THREADS = 1024;
 constexpr int PG_CLUSTER = 8;
 constexpr int PG_BATCH = 8192;                // requests of a call
 constexpr int PG_ROW_THREADS = 256;
-constexpr int64_t PG_ONE = 1 << 17;           // entries of a table that one cluster moves by itself
+// A fork is one launch, of one cluster, up to so many requests (rows that its threads take at once) and entries of the table.
+// Measured in us, one launch and two: 16 requests 7.4 and 7.6, 32 of 512 entries 8.3 and 7.7 (and a launch less on the host), 64
+// 9.5 and 7.6, 256 18.8 and 8.1, 1024 of 64 entries 57 and 9.5; 32 of 8192 18.5 and 15.4.
+constexpr int PG_ONE_BATCH = 32;
+constexpr int64_t PG_ONE = 1 << 15;
 
 struct Book {
     int32_t* table;
@@ -362,7 +366,7 @@ __global__ void __launch_bounds__(PG_ROW_THREADS) pages_fork_rows_kernel(const F
 }
 
 // The second.  The first cluster settles the part-filled pages: a request that will write into one must be alone with it.
-// The other CTAs write the rows.  ONE: one launch of one cluster does it all, for tables that are small enough.
+// The other CTAs write the rows.  ONE: one launch of one cluster does it all (PG_ONE).
 template <bool ONE>
 __global__ void __launch_bounds__(PG_THREADS, 1) pages_fork_kernel(const ForkArgs A) {
     constexpr int AT_ONCE = PG_THREADS / PG_ROW_THREADS;
@@ -743,7 +747,7 @@ extern "C" kvo_status kvo_paged_fork(const kvo_page_book* book, const int32_t* p
     while (A.slots < 2 * book->batch) A.slots *= 2;
     static std::atomic<uint64_t> done_one{0}, done_two{0};
     const int cluster = pages_cluster(book->n_pages), rows = (book->batch + 3) / 4;
-    if ((int64_t)book->batch * book->max_pages <= PG_ONE) {
+    if (book->batch <= PG_ONE_BATCH && (int64_t)book->batch * book->max_pages <= PG_ONE) {
         const cudaError_t e = allow_smem((const void*)pages_fork_kernel<true>, done_one, 2 * PG_BATCH * 12);
         if (e != cudaSuccess) return launched(e);
         const int ctas = std::max(cluster, rows > 1 ? PG_CLUSTER : 1);
