@@ -29,16 +29,18 @@
 // is a whole number, so that o = (sum of weights and codes) / l * 2^c takes no further rounding.
 //
 // What bounds it.  Long chunks: the tensor cores, which wait for the softmax (two tiles in turn, a row to a thread) at the
-// hand-overs.  32 query heads over 8 of d 128: 8192 tokens alone in bf16 393 us, 1.40 PFLOP/s of 1.91 measured for a matrix
-// product, in e4m3 466; 2048 behind 30000 in bf16 674 us (1.54 PFLOP/s), in e4m3 820: there the conversions of V and of P and
+// hand-overs.  32 query heads over 8 of d 128: 8192 tokens alone in bf16 390 us, 1.41 PFLOP/s of 1.91 measured for a matrix
+// product, in e4m3 478; 2048 behind 30000 in bf16 665 us (1.57 PFLOP/s), in e4m3 820: there the conversions of V and of P and
 // more code than the instruction caches hold.  Few rows on many keys: the loads of K and V, 16 requests of 64 tokens behind 32k
-// in bf16 386 us, 5.6 TB/s.  A batch of both, 36 single tokens and 4 chunks: 164 us, 0.93 PFLOP/s.
+// in bf16 385 us, 5.6 TB/s.  A batch of both, 36 single tokens and 4 chunks: 161 us replayed, 170 called, 0.90 PFLOP/s.  Of d 64
+// the products take half and the softmax what it takes: 8192 tokens 343 us in bf16, 417 in e4m3.
 //
 // Why so.  One thread for both tiles' products kept one tile waiting for the other's barriers: 8192 tokens 440 -> 402 us with
 // two.  Two buffers of f16 V: 2048 e4m3 tokens behind 30000 965 us, three 787.  q split into its pieces by every CTA that
 // needs them: 8192 tokens 744 us, by a launch before 457.  The softmax unrolled over 128 keys: 1016 us, in loops 740.  One
 // warp that loads both K and V keeps K waiting behind V's buffers: in bf16 the mixed batch 251 us, with two 166; in e4m3 the
-// buffers of raw V are free early, and a second warp's code costs more: 2048 behind 30000 945 us, with one 810.
+// buffers of raw V are free early, and a second warp's code costs more: 2048 behind 30000 945 us, with one 810.  K asked for
+// before its tile's scales are read: 16 pieces of 8 tokens behind 32k in e4m3 265 -> 250 us.
 #include <algorithm>
 
 #include "f32x2.cuh"
@@ -1560,8 +1562,9 @@ extern "C" kvo_status kvo_paged_chunk_attn(const kvo_paged_cache* cache, const v
     A.n_pages = cache->n_pages;
     A.max_pages = cache->max_pages;
     A.tiles = tiles;
-    // Measured times of 128 keys: one tile of rows is 5/7 of two in bf16 (the mixed batch 173 us with 6/7, 165 with 5/7, 171 with
-    // 4/7), and 4/7 in e4m3 (238 us, 248 with 5/7) and of d 64 (173 us, 179 with 5/7); an item in itself costs what 128 keys do.
+    // Measured times of 128 keys: one tile of rows is 5/7 of two in bf16 and 4/7 in e4m3 and of d 64; an item in itself costs what
+    // 128 keys do.  With 4/7, 5/7 and 6/7, us: 56 single tokens and 8 pieces of 250 behind 512-8192 in bf16 271, 267, 279, in e4m3
+    // 269, 292, 318, of d 64 189, 209, 228 and 234, 257, 278; 20 and 4 of 1000 in bf16 615, 613, 615, in e4m3 679, 696, 712.
     A.w1 = fp8 || D == 64 ? 4 : 5;
     A.w2 = 7;
     A.base = 2 * CH_KEYS * A.w2;

@@ -2,7 +2,9 @@
 // of the decode attention with a number of visible keys for each row.  Up to 8 rows cost what one does; 16 are two tiles of the
 // products' 8 columns, with twice the exponentials, and bound by issue slots where 8 are by HBM.  Measured (32 query and 8 KV
 // heads of 128, 4 tokens each): 48 requests of 8K to 32K tokens in e4m3 350 us, 5.6 TB/s (one token each 297), 16 of 32K in
-// bf16 323 us, 6.6 TB/s, one of 500 7.9 us.  As tiles of 128 rows on tcgen05 the 48 took 604 us, the one of 4096 21.
+// bf16 323 us, 6.6 TB/s, one of 500 7.9 us.  Both ways at 16 rows, here and as tiles of 128 rows on tcgen05: 48 behind 16K in
+// e4m3 293 and 365 us (12 rows 291, 366; 8 rows 249, 365), in bf16 485 and 468; one behind 4096 in e4m3 13 and 27, in bf16 12 and
+// 24, behind 32K 33 and 45, 49 and 48.  20 rows, which only the tiles hold: 367, 471, one behind 32K 45 and 54.
 #include "paged_few.cuh"
 
 #include "paged_attn.cuh"

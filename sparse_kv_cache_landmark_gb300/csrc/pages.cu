@@ -10,7 +10,7 @@
 // through distributed shared memory; rows of the table, which may be long, are moved by other CTAs.
 //
 // Measured (replayed graph): 256 requests of 2000 to 16384 tokens forked in a pool of 196608 pages of 16 9.3 us (1.2 for the rows'
-// uses, 3 for the look at refs, 2 for the ranks, 2 for pages and lists), 32 beams 8.3 in one launch; room for 64 prompts in a pool of
+// uses, 3 for the look at refs, 2 for the ranks, 2 for pages and lists), 32 beams 8.0 in one launch; room for 64 prompts in a pool of
 // 262144 7.4 us; such a pool compacted 20 us (3 for the look, 2 for the ranks, 3 and 6 for the two lists, 4 for the rows), one of 2048
 // pages 8.7.  Clusters of 16 CTAs: 11.4 us for the 256, 11.2 for the prompts, 19.3 for the compaction.  A run of pages to each
 // warp instead of rounds (below): 14.4, 14 and 22, as few warps hold what is given out.
