@@ -65,7 +65,6 @@ constexpr float CH_BIG = 0x1p20f;          // from here on scores are taken less
 constexpr int CH_CTAS = 152;               // ranges at most: one CTA to an SM
 constexpr int CH_EVENTS = 16;              // barriers that a tile's products complete in turn
 constexpr int CH_ITEMS = 4;                // descriptors
-constexpr int CH_NONE = INT32_MIN;         // no page
 constexpr int CH_NAN = -128;               // the exponent of a row of q that is not finite
 constexpr int CH_SCALES = 8;               // tiles of keys whose scales are held
 constexpr uint32_t CH_FAR = 1u << 8;       // beside a tile's bad groups: some v_scale of the item so far is far from its first,
@@ -928,10 +927,12 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
         I = sh.item[k % CH_ITEMS];
         return true;
     };
-    // Of the item's tiles j .. j + 3, the page of the (lane % 8)-th 16 keys of tile j + lane / 8; CH_NONE behind the last key.
+    // Of the item's tiles j .. j + 3, the (lane % 8)-th 16 keys of tile j + lane / 8: the first of them, and their page, an entry
+    // of the table that may be anything and is not looked at here (it is on its way); -1 behind the last key.
+    auto key_of = [&](const ChunkItem& I, int j) { return (int64_t)(I.first + j + (lane >> 3)) * CH_KEYS + 16 * (lane & 7); };
     auto page_of = [&](const ChunkItem& I, int j) {
-        const int64_t key = (int64_t)(I.first + j + (lane >> 3)) * CH_KEYS + 16 * (lane & 7);
-        return key < I.len ? __ldg(A.table + (int64_t)I.b * A.max_pages + (key >> A.shift)) : CH_NONE;
+        const int64_t key = key_of(I, j);
+        return key < I.len ? __ldg(A.table + (int64_t)I.b * A.max_pages + (key >> A.shift)) : -1;
     };
     // Whole warp: asks for a tile of K or V, a box to a lane: its page's rows in the pool, or, where there is no such page,
     // what lies behind the last (zeros).
@@ -994,7 +995,7 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
                         if ((j & 3) == 0) {
                             page = page_next;
                             if (j + 4 < I.tiles) page_next = page_of(I, j + 4);
-                            const bool in = page != CH_NONE;
+                            const bool in = key_of(I, j) < I.len;
                             bad = in && (page < 0 || page >= A.n_pages);
                             if (bad && j + (lane >> 3) < I.tiles && A.status) atomicOr(A.status, KVO_DEV_BAD_BLOCK_ID);
                             if (bad || !in) page = -1;

@@ -51,3 +51,19 @@ def test_neighbours_of_a_bad_offset(spoil, batch, bounds, e4m3):
     assert (o[served] != 3.0).any(-1).all()
     c.new, c.cu = [rows[b][1] - rows[b][0] if b in rows else 0 for b in range(batch)], [rows[b][0] if b in rows else 0 for b in range(batch)]
     c.check(o, lse, requests=sorted(rows)[:6] + sorted(rows)[-2:])
+
+
+@pytest.mark.parametrize("few", [False, True])
+@pytest.mark.parametrize("e4m3", [False, True])
+@pytest.mark.parametrize("bad", [-1, -2, -2 ** 31, -2 ** 31 + 1, "n_pages", 2 ** 31 - 1, 2 ** 30])
+def test_page_ids_of_any_value(bad, e4m3, few):
+    """Whatever an entry holds that names no page, its tokens add nothing."""
+    new, lens = ([4, 3, 1], [300, 30, 9]) if few else ([70, 3, 1], [300, 30, 9])
+    c = Case(61, 64, 2, 4, 16, e4m3, new, lens)
+    bad = c.n_pages if bad == "n_pages" else bad
+    c.table[0, 3], c.table[0, 17], c.table[1, 0], c.table[2, 0] = bad, bad, bad, bad
+    status = i32([0])
+    o, lse = c.call(status=status, max_new=4 if few else 0)
+    assert int(status.item()) == kvo.DEV_BAD_BLOCK_ID
+    c.check(o, lse, rows=[0, 1, 2, 33, -1], heads=[0, 7], hide={(0, 3), (0, 17), (1, 0), (2, 0)})
+    assert (o[sum(new) - 1] == 0).all() and (lse[sum(new) - 1] == -float("inf")).all()
